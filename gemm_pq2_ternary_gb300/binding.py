@@ -31,6 +31,23 @@ PQ2_OP_SWIGLU_DOWN = 4
 
 PQ2_WEIGHTS_STATIC = 1
 
+# element types
+PQ2_F32 = 0
+PQ2_F16 = 1
+PQ2_BF16 = 2
+_TYPE = {torch.float32: PQ2_F32, torch.float16: PQ2_F16, torch.bfloat16: PQ2_BF16}
+
+# flags of the norms
+PQ2_NORM_UNIT_OFFSET = 2
+PQ2_NORM_NO_POST = 4
+PQ2_GATE_SIGMOID = 8
+PQ2_GATE_SILU = 16
+
+PQ2_NORM_MAX_H = 49152
+PQ2_LORA_MAX_R = 256
+PQ2_LORA_MAX_L = 16384
+PQ2_LORA_MAX_M = 1048576
+
 # kernel variants for pq2_debug_force_kernel
 PQ2_VARIANT_DEFAULT = 0
 PQ2_VARIANT_GEMV_DIRECT = 1
@@ -50,6 +67,17 @@ SIZE_MAX = ctypes.c_size_t(-1).value
 # Exported names and argument types (every one declared in include/pq2.h).
 _P, _I64, _SZ, _I, _U64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint64
 _U32 = ctypes.c_uint32
+_F = ctypes.c_float
+
+
+class NormResidualArgs(ctypes.Structure):
+    """pq2_norm_residual_args of include/pq2.h."""
+    _fields_ = ([(n, _P) for n in ("y", "r", "r_out", "w_post", "gate", "w_next", "x")] +
+                [(n, _I64) for n in ("ld_y", "ld_r", "ld_r_out", "ld_gate", "ld_x")] +
+                [(n, ctypes.c_int32) for n in ("y_type", "r_type", "w_type", "gate_type", "x_type")] +
+                [("eps", _F), ("alpha", _F), ("flags", _U32)])
+
+
 SIGNATURES = {
     "pq2_status_string": ([_I], ctypes.c_char_p),
     "pq2_version": ([], ctypes.c_char_p),
@@ -64,6 +92,14 @@ SIGNATURES = {
     "pq2_quantize_swiglu": ([_P, _I64, _I64, _P, _P, _P, _P], _I),
     "pq2_gemm_bf16_splitk": ([_P, _P, _P, _I64, _I64, _I64, _U32, _P], _I),
     "pq2_mlp_down_swiglu": ([_P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P], _I),
+    "pq2_rmsnorm": ([_P, _I, _I64, _P, _I, _P, _I, _I64, _I64, _I64, _F, _U32, _P], _I),
+    "pq2_norm_residual": ([ctypes.POINTER(NormResidualArgs), _I64, _I64, _P], _I),
+    "pq2_lora_workspace_bytes": ([_I64] * 5, _SZ),
+    "pq2_lora_add": ([_P, _I64, _P, _P, _I, _P, _P, _P, _P, _I64, _P, _I64, _I] + [_I64] * 5 +
+                     [_P, _SZ, _P], _I),
+    "pq2_verify_workspace_bytes": ([_I64] * 3, _SZ),
+    "pq2_verify_drafts": ([_P, _I64, _P, _P, _P, _I64, _P, _P, _I64, _P, _P, _P] + [_I64] * 3 +
+                          [_P, _SZ, _P], _I),
     "pq2_workspace_bytes": ([_I, _I64, _I64, _I64], _SZ),
     "pq2_group_dots": ([_I, _P, _P, _P, _I64, _I64, _I64, _P, _P, _SZ, _P], _I),
     "pq2_last_device_error": ([_P], _I),
@@ -255,6 +291,146 @@ def pq2_mlp_down_swiglu(gu, codes, ws, y, workspace, stream=None):
     wp, wb = _ws(workspace)
     _check(_lib.pq2_mlp_down_swiglu(_ptr(gu), _ptr(codes), _ptr(ws), _ptr(y), M, N, I2 // 2,
                                     wp, wb, _stream(stream)), "pq2_mlp_down_swiglu")
+
+
+def _row(t, shape, name):
+    """(pointer, element type, row stride) of a 2-D CUDA tensor whose rows are
+    contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    ld, unit = t.stride()
+    if unit != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    ty = _TYPE.get(t.dtype)
+    if ty is None:
+        raise ValueError(f"{name}: expected float32, float16 or bfloat16, got {t.dtype}")
+    # a single row's stride says nothing
+    return t.data_ptr(), ty, (shape[1] if shape[0] <= 1 or ld < shape[1] and ld != 0 else ld)
+
+
+def _weight(w, H, name):
+    if w is None:
+        return None, None
+    if tuple(w.shape) != (H,) or w.dtype not in _TYPE:
+        raise ValueError(f"{name}: expected a float tensor of shape ({H},)")
+    return _ptr(w), _TYPE[w.dtype]
+
+
+def pq2_rmsnorm(r, w, x, eps=1e-6, flags=0, stream=None):
+    """x = r / sqrt(mean(r^2) + eps) * w per row; r and x [M, H] (rows
+    contiguous, any row stride), w [H] or None."""
+    shape = r.shape
+    rp, rt, rl = _row(r, shape, "r")
+    xp, xt, xl = _row(x, shape, "x")
+    wp, wt = _weight(w, shape[1], "w")
+    _check(_lib.pq2_rmsnorm(rp, rt, rl, wp, wt or 0, xp, xt, xl, shape[0], shape[1], eps, flags,
+                            _stream(stream)), "pq2_rmsnorm")
+
+
+def pq2_norm_residual(y, r, r_out, w_post=None, gate=None, w_next=None, x=None, eps=1e-6, alpha=1.0,
+                      flags=0, stream=None):
+    """r_out = r + alpha * act(gate) * norm(y) * w_post and, if x is given,
+    x = norm(r_out) * w_next, in one pass.  y, r, r_out, x [M, H]; gate [M, H]
+    or [H]; rows contiguous, any row stride.  r_out may be r."""
+    shape = r.shape
+    yp, yt, yl = _row(y, shape, "y")
+    rp, rt, rl = _row(r, shape, "r")
+    op, ot, ol = _row(r_out, shape, "r_out")
+    if ot != rt:
+        raise ValueError("r_out: expected r's type")
+    pp, pt = _weight(w_post, shape[1], "w_post")
+    np_, nt = _weight(w_next, shape[1], "w_next")
+    if pt is not None and nt is not None and pt != nt:
+        raise ValueError("w_post and w_next: expected one type")
+    gp, gt, gl = None, 0, 0
+    if gate is not None:
+        if gate.dim() == 1:
+            gp, gt = _weight(gate, shape[1], "gate")
+        else:
+            gp, gt, gl = _row(gate, shape, "gate")
+    xp, xt, xl = (None, 0, 0) if x is None else _row(x, shape, "x")
+    args = NormResidualArgs(yp, rp, op, pp, gp, np_, xp, yl, rl, ol, gl, xl, yt, rt,
+                            pt if pt is not None else nt or 0, gt, xt, eps, alpha, flags)
+    _check(_lib.pq2_norm_residual(ctypes.byref(args), shape[0], shape[1], _stream(stream)),
+           "pq2_norm_residual")
+
+
+def pq2_lora_workspace_bytes(M, N, K, L, R) -> int:
+    return int(_lib.pq2_lora_workspace_bytes(M, N, K, L, R))
+
+
+def alloc_lora_workspace(M, N, K, L, R, device="cuda"):
+    n = pq2_lora_workspace_bytes(M, N, K, L, R)
+    if n == SIZE_MAX:
+        raise PQ2Error(PQ2_ERR_UNSUPPORTED_SHAPE, "pq2_lora_workspace_bytes")
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def pq2_lora_add(x, A, B, ids, y_in, y_out, workspace, ranks=None, scales=None, stream=None):
+    """y_out[m] = y_in[m] + scales[l] * B[l] (A[l] x[m]) with l = ids[m]
+    (l < 0: y_in[m]).  x [M, K], A [L, R, K], B [L, N, R] fp16 or bf16; ids
+    int32 [M]; ranks int32 [L], scales fp32 [L] or None; y fp32 or bf16 [M, N]."""
+    M, K = x.shape
+    L, N, R = B.shape
+    if A.shape != (L, R, K) or ids.shape != (M,):
+        raise ValueError(f"shapes: x {tuple(x.shape)}, A {tuple(A.shape)}, B {tuple(B.shape)}, "
+                         f"ids {tuple(ids.shape)}")
+    xp, xt, xl = _row(x, x.shape, "x")
+    if A.dtype != x.dtype or B.dtype != x.dtype:
+        raise ValueError("A and B: expected x's type")
+    _dtype(ids, torch.int32, "ids")
+    if ranks is not None:
+        _dtype(ranks, torch.int32, "ranks")
+    if scales is not None:
+        _dtype(scales, torch.float32, "scales")
+    for t in (ranks, scales):
+        if t is not None and t.shape != (L,):
+            raise ValueError("ranks and scales: one value per adapter")
+    ip, it, il = _row(y_in, (M, N), "y_in")
+    op, ot, ol = _row(y_out, (M, N), "y_out")
+    if it != ot:
+        raise ValueError("y_out: expected y_in's type")
+    wp, wb = _ws(workspace)
+    _check(_lib.pq2_lora_add(xp, xl, _ptr(A), _ptr(B), xt, _ptr(ids), _ptr(ranks), _ptr(scales), ip,
+                             il, op, ol, it, M, N, K, L, R, wp, wb, _stream(stream)), "pq2_lora_add")
+
+
+def pq2_verify_workspace_bytes(B, rows, V) -> int:
+    return int(_lib.pq2_verify_workspace_bytes(B, rows, V))
+
+
+def alloc_verify_workspace(B, rows, V, device="cuda"):
+    n = pq2_verify_workspace_bytes(B, rows, V)
+    if n == SIZE_MAX:
+        raise PQ2Error(PQ2_ERR_UNSUPPORTED_SHAPE, "pq2_verify_workspace_bytes")
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def pq2_verify_drafts(logits, row_start, drafts, q, u, e, temperature, accepted, tokens, workspace,
+                      stream=None):
+    """Kept drafts of each sequence and the token after them: logits, q (or
+    None) fp32 [rows, V]; row_start int32 [B + 1]; drafts, tokens int32
+    [rows]; u fp32 [rows]; e fp32 [B, V]; temperature fp32, accepted int32 [B]."""
+    rows, V = logits.shape
+    nb = temperature.shape[0]
+    lp, lt, ll = _row(logits, logits.shape, "logits")
+    ep, et, el = _row(e, (nb, V), "e")
+    qp, qt, ql = (None, PQ2_F32, 0) if q is None else _row(q, logits.shape, "q")
+    if lt or et or qt:
+        raise ValueError("logits, q and e: expected torch.float32")
+    for t, n, dt, name in ((row_start, nb + 1, torch.int32, "row_start"),
+                           (drafts, rows, torch.int32, "drafts"), (u, rows, torch.float32, "u"),
+                           (temperature, nb, torch.float32, "temperature"),
+                           (accepted, nb, torch.int32, "accepted"),
+                           (tokens, rows, torch.int32, "tokens")):
+        if t.dtype != dt or t.shape != (n,):
+            raise ValueError(f"{name}: expected {dt} of shape ({n},), got {t.dtype} {tuple(t.shape)}")
+    wp, wb = _ws(workspace)
+    _check(_lib.pq2_verify_drafts(lp, ll, _ptr(row_start), _ptr(drafts), qp, ql, _ptr(u), ep, el,
+                                  _ptr(temperature), _ptr(accepted), _ptr(tokens), nb, rows, V, wp,
+                                  wb, _stream(stream)), "pq2_verify_drafts")
 
 
 def pq2_group_dots(op, qp, T, codes, dots, workspace=None, stream=None):

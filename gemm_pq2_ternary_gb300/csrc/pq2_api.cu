@@ -1,5 +1,6 @@
 // The C ABI (include/pq2.h): host-side argument checks, per-device set-up,
 // routing to the kernels, and the device error word.
+#include <algorithm>
 #include <atomic>
 #include <cstring>
 #include <mutex>
@@ -492,6 +493,170 @@ pq2_status pq2_gemm_bf16_splitk(const uint16_t* x, const uint16_t* w, uint16_t* 
                                                 static_cast<cudaStream_t>(stream), c.ctl));
 }
 
+static size_t type_bytes(int type) { return type == PQ2_F32 ? 4 : 2; }
+static bool type_ok(int type) { return type == PQ2_F32 || type == PQ2_F16 || type == PQ2_BF16; }
+static bool aligned_to(const void* p, size_t unit) {
+    return reinterpret_cast<uintptr_t>(p) % unit == 0;
+}
+
+// The checks and the launch shared by the two norms (a.y null: the norm
+// before a block alone).
+static pq2_status norm(const pq2_norm_residual_args& a, int64_t M, int64_t H, void* stream) {
+    const uint32_t flags = PQ2_WEIGHTS_STATIC | PQ2_NORM_UNIT_OFFSET | PQ2_NORM_NO_POST |
+                           PQ2_GATE_SIGMOID | PQ2_GATE_SILU;
+    const uint32_t both = PQ2_GATE_SIGMOID | PQ2_GATE_SILU;
+    if (M < 0 || H < 1 || (a.flags & ~flags) || (a.flags & both) == both) return PQ2_ERR_INVALID_ARG;
+    if (!(a.eps >= 0.0f)) return PQ2_ERR_INVALID_ARG;
+    if (H > PQ2_NORM_MAX_H || M > (int64_t(1) << 31) - 1) return PQ2_ERR_UNSUPPORTED_SHAPE;
+    if (!type_ok(a.r_type) || (a.x && !type_ok(a.x_type)) || (a.y && !type_ok(a.y_type)) ||
+        (a.gate && !type_ok(a.gate_type)) || ((a.w_post || a.w_next) && !type_ok(a.w_type)))
+        return PQ2_ERR_INVALID_ARG;
+    if ((a.y && a.ld_y < H) || a.ld_r < H || (a.r_out && a.ld_r_out < H) || (a.x && a.ld_x < H) ||
+        (a.gate && a.ld_gate != 0 && a.ld_gate < H))
+        return PQ2_ERR_INVALID_ARG;
+    if (M == 0) return PQ2_OK;
+    if (!a.r) return PQ2_ERR_INVALID_ARG;
+    if (!aligned_to(a.r, type_bytes(a.r_type)) || !aligned_to(a.r_out, type_bytes(a.r_type)) ||
+        !aligned_to(a.y, type_bytes(a.y_type)) || !aligned_to(a.gate, type_bytes(a.gate_type)) ||
+        !aligned_to(a.w_post, type_bytes(a.w_type)) || !aligned_to(a.w_next, type_bytes(a.w_type)) ||
+        !aligned_to(a.x, type_bytes(a.x_type)))
+        return PQ2_ERR_MISALIGNED;
+    Ctx c;
+    const pq2_status s = get_ctx(&c);
+    if (s != PQ2_OK) return s;
+    pq2h::NormParams p = {};
+    p.y = a.y, p.r = a.r, p.r_out = a.r_out, p.w_post = a.w_post, p.gate = a.gate;
+    p.w_next = a.w_next, p.x = a.x;
+    p.ld_y = a.ld_y, p.ld_r = a.ld_r, p.ld_ro = a.ld_r_out, p.ld_gate = a.ld_gate, p.ld_x = a.ld_x;
+    p.M = M;
+    p.H = static_cast<int>(H);
+    p.ro_elems = (M - 1) * a.ld_r_out + H;
+    p.x_elems = (M - 1) * a.ld_x + H;
+    p.y_type = a.y_type, p.r_type = a.r_type, p.w_type = a.w_type, p.gate_type = a.gate_type;
+    p.x_type = a.x_type;
+    p.eps = a.eps, p.alpha = a.alpha;
+    p.w_offset = (a.flags & PQ2_NORM_UNIT_OFFSET) ? 1.0f : 0.0f;
+    p.flags = a.flags;
+    p.weights_static = (a.flags & PQ2_WEIGHTS_STATIC) ? 1 : 0;
+    p.ctl = c.ctl;
+    return cuda_status(pq2h::launch_norm(p, static_cast<cudaStream_t>(stream), c.dev));
+}
+
+pq2_status pq2_rmsnorm(const void* r, int r_type, int64_t ld_r, const void* w, int w_type, void* x,
+                       int x_type, int64_t ld_x, int64_t M, int64_t H, float eps, uint32_t flags,
+                       void* stream) {
+    if (flags & ~(PQ2_WEIGHTS_STATIC | PQ2_NORM_UNIT_OFFSET)) return PQ2_ERR_INVALID_ARG;
+    if (M > 0 && !x) return PQ2_ERR_INVALID_ARG;
+    pq2_norm_residual_args a = {};
+    a.r = r, a.w_next = w, a.x = x;
+    a.ld_r = ld_r, a.ld_x = ld_x;
+    a.r_type = r_type, a.w_type = w_type, a.x_type = x_type;
+    a.eps = eps, a.flags = flags;
+    return norm(a, M, H, stream);
+}
+
+pq2_status pq2_norm_residual(const pq2_norm_residual_args* args, int64_t M, int64_t H,
+                             void* stream) {
+    if (!args) return PQ2_ERR_INVALID_ARG;
+    if (M > 0 && (!args->y || !args->r || !args->r_out)) return PQ2_ERR_INVALID_ARG;
+    return norm(*args, M, H, stream);
+}
+
+static pq2_status check_lora(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+    if (M < 0 || N < 0 || K < 1 || L < 1 || R < 1) return PQ2_ERR_INVALID_ARG;
+    if (K % 8 != 0 || K > PQ2_MAX_K || R % 8 != 0 || R > PQ2_LORA_MAX_R || L > PQ2_LORA_MAX_L ||
+        M > PQ2_LORA_MAX_M || N > (int64_t(1) << 30))
+        return PQ2_ERR_UNSUPPORTED_SHAPE;
+    return PQ2_OK;
+}
+
+size_t pq2_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+    if (check_lora(M, N, K, L, R) != PQ2_OK) return SIZE_MAX;
+    return M == 0 ? 0 : pq2h::lora_workspace_bytes(M, N, K, L, R);
+}
+
+pq2_status pq2_lora_add(const void* x, int64_t ld_x, const void* A, const void* B, int type,
+                        const int32_t* ids, const int32_t* ranks, const float* scales,
+                        const void* y_in, int64_t ld_in, void* y_out, int64_t ld_out, int y_type,
+                        int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    pq2_status s = check_lora(M, N, K, L, R);
+    if (s != PQ2_OK) return s;
+    if ((type != PQ2_F16 && type != PQ2_BF16) || (y_type != PQ2_F32 && y_type != PQ2_BF16))
+        return PQ2_ERR_INVALID_ARG;
+    if (ld_x < K || ld_in < N || ld_out < N) return PQ2_ERR_INVALID_ARG;
+    if (ld_x % 8 != 0) return PQ2_ERR_UNSUPPORTED_SHAPE;
+    if (M == 0 || N == 0) return PQ2_OK;
+    if (!x || !A || !B || !ids || !y_in || !y_out) return PQ2_ERR_INVALID_ARG;
+    if (y_in == y_out && ld_in != ld_out) return PQ2_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(A) || !aligned16(B) || !aligned16(workspace) ||
+        !aligned_to(ids, 4) || !aligned_to(ranks, 4) || !aligned_to(scales, 4) ||
+        !aligned_to(y_in, type_bytes(y_type)) || !aligned_to(y_out, type_bytes(y_type)))
+        return PQ2_ERR_MISALIGNED;
+    if (!workspace || workspace_bytes < pq2h::lora_workspace_bytes(M, N, K, L, R))
+        return PQ2_ERR_WORKSPACE;
+    Ctx c;
+    s = get_ctx(&c);
+    if (s != PQ2_OK) return s;
+    pq2h::LoraParams p = {};
+    p.x = static_cast<const uint16_t*>(x);
+    p.A = static_cast<const uint16_t*>(A);
+    p.B = static_cast<const uint16_t*>(B);
+    p.ids = ids, p.ranks = ranks, p.scales = scales;
+    p.y_in = y_in, p.y_out = y_out;
+    p.ld_x = ld_x, p.ld_in = ld_in, p.ld_out = ld_out;
+    p.M = static_cast<int>(M), p.N = static_cast<int>(N), p.K = static_cast<int>(K);
+    p.L = static_cast<int>(L), p.R = static_cast<int>(R);
+    p.bf16 = type == PQ2_BF16;
+    p.y_type = y_type;
+    p.ctl = c.ctl;
+    return cuda_status(pq2h::launch_lora(p, workspace, static_cast<cudaStream_t>(stream), c.dev));
+}
+
+static pq2_status check_verify(int64_t B, int64_t rows, int64_t V) {
+    if (B < 0 || rows < 0 || V < 1) return PQ2_ERR_INVALID_ARG;
+    // pieces of rows, and of sequences, are counted in 31 bits
+    const int64_t pieces = V / 4096 + 2;
+    if (V > (int64_t(1) << 30) || rows > (int64_t(1) << 24) || B > (int64_t(1) << 24) ||
+        std::max(B, rows) * pieces > (int64_t(1) << 31) - 1)
+        return PQ2_ERR_UNSUPPORTED_SHAPE;
+    return PQ2_OK;
+}
+
+size_t pq2_verify_workspace_bytes(int64_t B, int64_t rows, int64_t V) {
+    if (check_verify(B, rows, V) != PQ2_OK) return SIZE_MAX;
+    return pq2h::verify_workspace_bytes(B, rows, V);
+}
+
+pq2_status pq2_verify_drafts(const float* logits, int64_t ld_logits, const int32_t* row_start,
+                             const int32_t* drafts, const float* q, int64_t ld_q, const float* u,
+                             const float* e, int64_t ld_e, const float* temperature,
+                             int32_t* accepted, int32_t* tokens, int64_t B, int64_t rows, int64_t V,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+    pq2_status s = check_verify(B, rows, V);
+    if (s != PQ2_OK) return s;
+    if (ld_logits < V || (q && ld_q < V) || ld_e < V) return PQ2_ERR_INVALID_ARG;
+    if (B == 0) return PQ2_OK;
+    if (!row_start || !e || !temperature || !accepted) return PQ2_ERR_INVALID_ARG;
+    if (rows > 0 && (!logits || !drafts || !u || !tokens)) return PQ2_ERR_INVALID_ARG;
+    if (!aligned_to(logits, 4) || !aligned_to(q, 4) || !aligned_to(u, 4) || !aligned_to(e, 4) ||
+        !aligned_to(row_start, 4) || !aligned_to(drafts, 4) || !aligned_to(temperature, 4) ||
+        !aligned_to(accepted, 4) || !aligned_to(tokens, 4) || !aligned16(workspace))
+        return PQ2_ERR_MISALIGNED;
+    if (!workspace || workspace_bytes < pq2h::verify_workspace_bytes(B, rows, V))
+        return PQ2_ERR_WORKSPACE;
+    Ctx c;
+    s = get_ctx(&c);
+    if (s != PQ2_OK) return s;
+    pq2h::VerifyParams p = {};
+    p.logits = logits, p.row_start = row_start, p.drafts = drafts, p.q = q, p.u = u, p.e = e;
+    p.temperature = temperature, p.accepted = accepted, p.tokens = tokens;
+    p.ld_logits = ld_logits, p.ld_q = ld_q, p.ld_e = ld_e;
+    p.B = B, p.rows = rows, p.V = static_cast<int>(V);
+    p.ctl = c.ctl;
+    return cuda_status(pq2h::launch_verify(p, workspace, static_cast<cudaStream_t>(stream)));
+}
+
 pq2_status pq2_group_dots(int op, const int8_t* qp, const int32_t* T, const uint8_t* codes,
                           int64_t M, int64_t N, int64_t K, int32_t* dots, void* workspace,
                           size_t workspace_bytes, void* stream) {
@@ -536,7 +701,7 @@ pq2_status pq2_last_device_error(void* stream) {
         return PQ2_ERR_CUDA;
     if (word & pq2::DEVERR_TIMEOUT) return PQ2_ERR_TIMEOUT;
     if (word & pq2::DEVERR_BOUNDS) return PQ2_ERR_BOUNDS;
-    if (word & pq2::DEVERR_BAD_TERNARY) return PQ2_ERR_INVALID_ARG;
+    if (word & (pq2::DEVERR_BAD_TERNARY | pq2::DEVERR_BAD_INDEX)) return PQ2_ERR_INVALID_ARG;
     return PQ2_OK;
 }
 

@@ -22,6 +22,7 @@ enum : unsigned {
     DEVERR_TIMEOUT = 1u,      // a bounded wait ran out
     DEVERR_BAD_TERNARY = 2u,  // pack met a value outside {-1,0,1}
     DEVERR_BOUNDS = 4u,       // bounds-checked build: a store outside its buffer (skipped)
+    DEVERR_BAD_INDEX = 8u,    // an index array held a value outside its range
 };
 
 // Passed by value to every kernel.

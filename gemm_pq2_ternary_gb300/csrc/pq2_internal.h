@@ -156,4 +156,72 @@ cudaError_t launch_prefill(const int8_t* qp, const float* S, const int32_t* T, c
                            int64_t K, void* workspace, cudaStream_t st, const pq2::DevCtl& ctl,
                            const DeviceInfo& dev);
 
+// Norms around a block (pq2_norm.cu).  y == nullptr: the norm before a block
+// alone (x = rms(r) * w_next).  Row strides in elements; ld_gate 0 = one
+// vector for all rows.  ro_elems, x_elems: extent of r_out and x in elements,
+// for the bounds-checked build.
+struct NormParams {
+    const void* y;
+    const void* r;
+    void* r_out;
+    const void* w_post;
+    const void* gate;
+    const void* w_next;
+    void* x;
+    int64_t ld_y, ld_r, ld_ro, ld_gate, ld_x;
+    int64_t M;
+    long long ro_elems, x_elems;
+    int H;
+    int y_type, r_type, w_type, gate_type, x_type;
+    float eps, alpha, w_offset;
+    uint32_t flags;
+    int weights_static;
+    pq2::DevCtl ctl;
+};
+cudaError_t launch_norm(const NormParams& p, cudaStream_t st, const DeviceInfo& dev);
+
+// Verification of drafted tokens (pq2_verify.cu).
+struct VerifyParams {
+    const float* logits;       // [rows, V], row stride ld_logits
+    const int32_t* row_start;  // [B + 1]
+    const int32_t* drafts;     // [rows]
+    const float* q;            // [rows, V] or null, row stride ld_q
+    const float* u;            // [rows]
+    const float* e;            // [B, V], row stride ld_e
+    const float* temperature;  // [B]
+    int32_t* accepted;         // [B]
+    int32_t* tokens;           // [rows]
+    int64_t ld_logits, ld_q, ld_e;
+    int64_t B, rows;
+    int V;
+    int chunks;                // pieces of a row (verify_chunks)
+    float2* stats;             // [rows][chunks] maximum, sum of exponentials
+    int32_t* best;             // [rows][chunks] index of the maximum
+    unsigned long long* keys;  // [B][2] best score and index, residual and target
+    unsigned* done;            // [B] pieces finished
+    pq2::DevCtl ctl;
+};
+size_t verify_workspace_bytes(int64_t B, int64_t rows, int64_t V);
+cudaError_t launch_verify(VerifyParams p, void* workspace, cudaStream_t st);
+
+// Low-rank adapters (pq2_lora.cu).
+struct LoraParams {
+    const uint16_t* x;      // [M, K], row stride ld_x
+    const uint16_t* A;      // [L, R, K]
+    const uint16_t* B;      // [L, N, R]
+    const int32_t* ids;     // [M]
+    const int32_t* ranks;   // [L] or null
+    const float* scales;    // [L] or null
+    const void* y_in;       // [M, N], row stride ld_in
+    void* y_out;            // [M, N], row stride ld_out
+    int64_t ld_x, ld_in, ld_out;
+    int M, N, K, L, R;
+    int bf16;               // type of x, A, B: 0 fp16, 1 bf16
+    int y_type;             // PQ2_F32 or PQ2_BF16
+    pq2::DevCtl ctl;
+};
+size_t lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
+cudaError_t launch_lora(const LoraParams& p, void* workspace, cudaStream_t st,
+                        const DeviceInfo& dev);
+
 }  // namespace pq2h

@@ -1,0 +1,903 @@
+// Low-rank adapters of many requests beside a shared projection:
+//
+//   v[m]  = A[id(m)] x[m]                       (rank values, fp32)
+//   y'[m] = y[m] + scale[id(m)] * B[id(m)] v[m]
+//
+// A is [L][R][K], B [L][N][R], fp16 or bf16 like x; y is the projection's
+// output.  Two kernels, "shrink" (x -> v) and "expand" (v -> y').
+//
+// Both products run on the warp-level tensor instructions
+// (mma.m16n8k16, fp32 accumulators) with the weights as the 16-row operand
+// and the tokens as the 8 columns: a decode step has one or a few tokens per
+// adapter, and 8 columns waste the least.  The sum index may be visited in
+// any order, so a lane feeds the instructions from 16-byte loads of 8
+// consecutive values (columns 8t .. 8t + 7 of a block of 32, t = lane % 4):
+// the first instruction takes their first four, the second the others, the
+// same for both operands.  Weights go from global memory straight to
+// registers, with no shared-memory stage: each is used once per tile of
+// tokens.
+//
+// Precision.  v stays fp32 and would lose 13 bits (16 for bf16) as an operand
+// of the expand product, so it enters as a sum of 16-bit terms: hi + lo for
+// fp16 (22 bits below the largest |v| of the token; each token is scaled by a
+// power of two, undone in fp32, so no term overflows), hi + mid + lo for
+// bf16 (24 bits).  Tensor accumulation may round towards zero: chains are cut
+// every 16 instructions and added up in fp32.
+//
+// Two forms:
+//   few tokens (M <= 32): every warp groups the tokens by adapter itself
+//     (one match over its lanes), and expand adds up the K-split partials of
+//     shrink in a fixed order.  Two launches.
+//   more tokens: a plan kernel sorts the tokens by adapter into tiles of at
+//     most 64 (stable counting sort in shared memory); shrink's last CTA of a
+//     tile adds up the K-split partials and writes v's 16-bit terms; expand
+//     streams y through registers against them.  Three launches.
+// Results do not depend on which tokens share a tile: deterministic.
+//
+// Bounds: bytes.  Decode: A and B of the adapters in use; prompts: y in and
+// out (8 N bytes per token against 2 K + 2 R (K + N) / tokens).
+#include <algorithm>
+
+#include <cuda_bf16.h>
+
+#include "pq2_common.cuh"
+#include "pq2_internal.h"
+
+namespace pq2 {
+namespace {
+
+constexpr int kFewTokens = 32;
+constexpr int kTile = 64;        // tokens per tile of the planned form
+constexpr int kShrinkWarps = 8;
+constexpr int kExpandWarps = 4;
+constexpr int kMaxSplits = 32;
+constexpr int kFlush = 8;        // k32 blocks (16 MMAs) per accumulator chain
+
+// d += a . b (16 x 8 x 16), fp32 accumulators.
+template <bool BF>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (BF)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The two instructions of a block of 32: rows g and g + 8 from r0 and r1.
+template <bool BF>
+__device__ __forceinline__ void mma_block(float (&d)[4], const uint4& r0, const uint4& r1,
+                                          const uint4& c) {
+    mma16816<BF>(d, r0.x, r1.x, r0.y, r1.y, c.x, c.y);
+    mma16816<BF>(d, r0.z, r1.z, r0.w, r1.w, c.z, c.w);
+}
+
+__device__ __forceinline__ uint4 zero4() { return make_uint4(0, 0, 0, 0); }
+
+__device__ __forceinline__ uint4 load16(const uint16_t* p) {
+    return *reinterpret_cast<const uint4*>(p);
+}
+// Past L1, for what a kernel reads before its dependency wait (or once).
+__device__ __forceinline__ uint4 load16_cg(const uint16_t* p) {
+    return __ldcg(reinterpret_cast<const uint4*>(p));
+}
+
+// Keeps the first n of 8 values (n <= 0: none): a row's padding may hold
+// anything, NaN included.
+__device__ __forceinline__ uint4 keep_first(uint4 v, int n) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (2 * i >= n) w[i] = 0;
+        else if (2 * i + 1 >= n) w[i] &= 0xffffu;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ int rank_of(const pq2h::LoraParams& p, int l) {
+    return p.ranks ? max(0, min(__ldcg(p.ranks + l), p.R)) : p.R;
+}
+
+// Adapter of token m: -1 if none.
+__device__ __forceinline__ int adapter_of(const pq2h::LoraParams& p, int m, bool report) {
+    const int id = __ldcg(p.ids + m);
+    if (id >= p.L) {
+        if (report) atomicOr(p.ctl.err, DEVERR_BAD_INDEX);
+        return -1;
+    }
+    return id < 0 ? -1 : id;
+}
+
+// The i-th distinct adapter among M <= 32 tokens, as every warp finds it:
+// its tokens as a lane mask.  kNone: tokens without an adapter form a group
+// too.  mask = 0: there is no such group.
+struct Group {
+    int adapter;
+    unsigned mask;
+};
+template <bool kNone>
+__device__ __forceinline__ Group find_group(const pq2h::LoraParams& p, int i, bool report) {
+    const int lane = threadIdx.x & 31;
+    const int id = lane < p.M ? adapter_of(p, lane, report) : -2;
+    const unsigned same = __match_any_sync(0xffffffffu, id);
+    const bool leads = (__ffs(same) - 1) == lane && (kNone ? id >= -1 : id >= 0);
+    unsigned lead = __ballot_sync(0xffffffffu, leads);
+    for (int k = 0; k < i; ++k) lead &= lead - 1;
+    if (lead == 0) return {-1, 0u};
+    const int src = __ffs(lead) - 1;
+    return {__shfl_sync(0xffffffffu, id, src), __shfl_sync(0xffffffffu, same, src)};
+}
+
+// v's token as 16-bit terms.  fp16: the token is scaled by 2^-e first.
+template <bool BF>
+__device__ __forceinline__ void split_terms(float v, uint16_t (&t)[3]) {
+    if constexpr (BF) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const __nv_bfloat16 h = __float2bfloat16_rn(v);
+            t[i] = *reinterpret_cast<const uint16_t*>(&h);
+            v -= __bfloat162float(h);
+        }
+    } else {
+        const __half h = __float2half_rn(v);
+        t[0] = __half_as_ushort(h);
+        t[1] = __half_as_ushort(__float2half_rn(v - __half2float(h)));
+        t[2] = 0;
+    }
+}
+template <bool BF>
+constexpr int terms() {
+    return BF ? 3 : 2;
+}
+
+// 2^e with e the exponent of the token's largest |v| (kept in the range where
+// 2^e and 2^-e are normal numbers); 1 for bf16, whose terms have fp32's range.
+template <bool BF>
+__device__ __forceinline__ float pow2_below(float top) {
+    if constexpr (BF) return 1.0f;
+    const int e = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 0xff), 27), 227);
+    return top > 0.0f ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 1.0f;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+
+// Rows of v's terms in shared memory: a block of 32 ranks is 16 words; an
+// odd number of 16-word blocks per row keeps the 16-byte reads of two
+// neighbouring tokens in different banks.
+__host__ __device__ __forceinline__ int term_pitch(int blocks) { return (blocks | 1) * 32; }
+
+// ----------------------------------------------------------------------------
+// shrink
+// ----------------------------------------------------------------------------
+
+// Warps per rank tile of 16 within a CTA (the others split K).
+__device__ __forceinline__ int k_warps(int rank_tiles) {
+    return rank_tiles == 1 ? 8 : rank_tiles == 2 ? 4 : rank_tiles <= 4 ? 2 : 1;
+}
+
+// One CTA's partial product: the ranks of adapter l x `count` tokens (token
+// list in shared memory) over columns [k0, k1) of K.  out(j, r, v) receives
+// the result for token j of the list and rank r.
+template <bool BF, int NT, typename Out>
+__device__ __forceinline__ void shrink_tile(const pq2h::LoraParams& p, int l, int rank,
+                                            const int* tok, int count, int k0, int k1, float* red,
+                                            Out out) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int rank_tiles = (rank + 15) / 16;
+    const int kw = k_warps(rank_tiles);
+    const int per_round = kShrinkWarps / kw;
+    const int ks = warp % kw;
+    const uint16_t* x[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int j = i * 8 + g;
+        x[i] = j < count ? p.x + static_cast<size_t>(tok[j]) * p.ld_x : nullptr;
+    }
+    // more than one round only with kw == 1, where `red` is not used
+    for (int rt = warp / kw; rt < rank_tiles; rt += per_round) {
+        const int ra = rt * 16 + g, rb = ra + 8;
+        const uint16_t* a0 = p.A + (static_cast<size_t>(l) * p.R + ra) * p.K;
+        const uint16_t* a1 = a0 + static_cast<size_t>(8) * p.K;
+        float sum[NT][4], acc[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sum[i][c] = acc[i][c] = 0.0f;
+        constexpr int U = NT == 1 ? 8 : NT == 4 ? 4 : 2;  // blocks in flight
+        int chain = 0;
+        for (int kb = k0 + ks * 32; kb < k1; kb += kw * 32 * U) {
+            uint4 fa[U], fb[U], fx[U][NT];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = kb + u * kw * 32 + 8 * t;
+                fa[u] = k < k1 && ra < rank ? load16(a0 + k) : zero4();
+                fb[u] = k < k1 && rb < rank ? load16(a1 + k) : zero4();
+#pragma unroll
+                for (int i = 0; i < NT; ++i) fx[u][i] = k < k1 && x[i] ? load16(x[i] + k) : zero4();
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    if (i * 8 < count) mma_block<BF>(acc[i], fa[u], fb[u], fx[u][i]);
+            chain += U;
+            if (chain >= kFlush) {
+                chain = 0;
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        sum[i][c] += acc[i][c];
+                        acc[i][c] = 0.0f;
+                    }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float v = sum[i][c] + acc[i][c];
+                const int r = (c >> 1) * 8 + g, j = i * 8 + 2 * t + (c & 1);
+                if (kw > 1)
+                    red[(warp * 16 + r) * (NT * 8) + j] = v;
+                else if (j < count && rt * 16 + r < rank)
+                    out(j, rt * 16 + r, v);
+            }
+    }
+    if (kw > 1) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < rank_tiles * 16 * count; i += kShrinkWarps * 32) {
+            const int r = i % (rank_tiles * 16), j = i / (rank_tiles * 16);
+            if (r >= rank) continue;
+            const float* src = red + ((r / 16) * kw * 16 + r % 16) * (NT * 8) + j;
+            float v = 0.0f;
+            for (int w = 0; w < kw; ++w) v += src[w * 16 * NT * 8];
+            out(j, r, v);
+        }
+    }
+}
+
+// Few tokens: CTA (split, group).  part [splits][M][R].
+template <bool BF, int NT>
+__global__ void __launch_bounds__(kShrinkWarps * 32) lora_shrink_few(pq2h::LoraParams p,
+                                                                     float* part, int k_split) {
+    __shared__ float red[kShrinkWarps * 16 * NT * 8];
+    __shared__ int tok[kFewTokens];
+    pdl_wait();
+    pdl_launch_dependents();
+    const Group grp = find_group<false>(p, blockIdx.y, blockIdx.x + blockIdx.y + threadIdx.x / 32 == 0);
+    if (grp.mask == 0) return;  // uniform over the CTA
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x < 32 && ((grp.mask >> lane) & 1u))
+        tok[__popc(grp.mask & ((1u << lane) - 1u))] = lane;
+    __syncthreads();
+    const int rank = rank_of(p, grp.adapter);
+    const int k0 = blockIdx.x * k_split, k1 = min(k0 + k_split, p.K);
+    float* dst = part + static_cast<size_t>(blockIdx.x) * p.M * p.R;
+    shrink_tile<BF, NT>(p, grp.adapter, rank, tok, __popc(grp.mask), k0, k1, red,
+                        [&](int j, int r, float v) { dst[tok[j] * p.R + r] = v; });
+}
+
+// ----------------------------------------------------------------------------
+// expand
+// ----------------------------------------------------------------------------
+
+// Four consecutive values of y (n .. n + 3 of a row).
+template <int YT>
+__device__ __forceinline__ float4 y_load(const void* y, size_t i, int left, bool vec) {
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (YT == PQ2_F32) {
+        const float* s = static_cast<const float*>(y) + i;
+        if (vec && left >= 4) return __ldcg(reinterpret_cast<const float4*>(s));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < left) v[j] = __ldcg(s + j);
+    } else {
+        const uint16_t* s = static_cast<const uint16_t*>(y) + i;
+        if (vec && left >= 4) {
+            const uint2 u = __ldcg(reinterpret_cast<const uint2*>(s));
+            return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                               __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < left) v[j] = __uint_as_float(static_cast<uint32_t>(__ldcg(s + j)) << 16);
+    }
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+template <int YT>
+__device__ __forceinline__ void y_store(const pq2h::LoraParams& p, size_t i, int left, bool vec,
+                                        const float4& v) {
+    const long long elems = static_cast<long long>(p.M - 1) * p.ld_out + p.N;
+    const float w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (YT == PQ2_F32) {
+        float* d = static_cast<float*>(p.y_out) + i;
+        if (vec && left >= 4) {
+            if (store_ok(p.ctl, i, 4, elems)) *reinterpret_cast<float4*>(d) = v;
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < left && store_ok(p.ctl, i + j, 1, elems)) d[j] = w[j];
+    } else {
+        uint16_t* d = static_cast<uint16_t*>(p.y_out) + i;
+        if (vec && left >= 4) {
+            if (store_ok(p.ctl, i, 4, elems))
+                *reinterpret_cast<uint2*>(d) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < left && store_ok(p.ctl, i + j, 1, elems))
+                d[j] = static_cast<uint16_t>(bf16x2(w[j], 0.0f) & 0xffffu);
+    }
+}
+
+// The four rows of B of this lane (outputs n .. n + 3) in block `blk` of 32
+// ranks: rows g and g + 8 of two instructions' operands.
+struct BRows {
+    uint4 r[4];
+};
+__device__ __forceinline__ BRows b_load(const pq2h::LoraParams& p, int l, int rank, int n, int blk) {
+    BRows b;
+    const int r0 = blk * 32 + 8 * (threadIdx.x & 3);
+    const int left = rank - r0;
+    const uint16_t* src = p.B + (static_cast<size_t>(l) * p.N + n) * p.R + r0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        b.r[i] = left > 0 && n + i < p.N ? load16_cg(src + static_cast<size_t>(i) * p.R) : zero4();
+        if (left < 8) b.r[i] = keep_first(b.r[i], left);
+    }
+    return b;
+}
+
+// acc += B rows x v terms of one block of 32 ranks, for NT groups of 8
+// tokens (those below `count`).  sv: terms of token 0, block 0.
+template <bool BF, int NT>
+__device__ __forceinline__ void expand_block(float (&acc)[2][NT][4], const BRows& b,
+                                             const uint16_t* sv, int pitch, int term_size, int blk,
+                                             int count) {
+    const int lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        if (i * 8 >= count) break;
+        const uint16_t* src = sv + (i * 8 + g) * pitch + blk * 32 + 8 * t;
+#pragma unroll
+        for (int q = 0; q < terms<BF>(); ++q) {
+            const uint4 c = *reinterpret_cast<const uint4*>(src + q * term_size);
+            mma_block<BF>(acc[0][i], b.r[0], b.r[1], c);
+            mma_block<BF>(acc[1][i], b.r[2], b.r[3], c);
+        }
+    }
+}
+
+// y' = y + f acc for this lane's two tokens of each group of 8 (f: scale and
+// the token's power of two).
+template <int YT, int NT>
+__device__ __forceinline__ void expand_store(const pq2h::LoraParams& p, const float (&acc)[2][NT][4],
+                                             const float4 (&y)[NT][2], const int* tok,
+                                             const float* f, int count, int n, bool vec) {
+    const int t = threadIdx.x & 3;
+    if (n >= p.N) return;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int j = i * 8 + 2 * t + h;
+            if (j >= count) continue;
+            const float s = f[j];
+            float4 o = y[i][h];
+            o.x = fmaf(s, acc[0][i][h], o.x);
+            o.y = fmaf(s, acc[0][i][2 + h], o.y);
+            o.z = fmaf(s, acc[1][i][h], o.z);
+            o.w = fmaf(s, acc[1][i][2 + h], o.w);
+            y_store<YT>(p, static_cast<size_t>(tok[j]) * p.ld_out + n, p.N - n, vec, o);
+        }
+}
+
+template <int YT, int NT>
+__device__ __forceinline__ void y_fetch(const pq2h::LoraParams& p, float4 (&y)[NT][2], const int* tok,
+                                        int count, int n, bool vec) {
+    const int t = threadIdx.x & 3;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int j = i * 8 + 2 * t + h;
+            y[i][h] = j < count && n < p.N
+                          ? y_load<YT>(p.y_in, static_cast<size_t>(tok[j]) * p.ld_in + n, p.N - n, vec)
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+}
+
+// Few tokens: CTA (128 outputs, group).  The operands that do not come from
+// shrink (B, y) are loaded before the dependency wait: shrink lets this
+// kernel start only after its own wait, so everything before it is done.
+template <bool BF, int NT, int YT>
+__global__ void __launch_bounds__(kExpandWarps * 32)
+    lora_expand_few(pq2h::LoraParams p, const float* part, int splits, int vec) {
+    extern __shared__ __align__(16) uint16_t sv[];
+    __shared__ int tok[kFewTokens];
+    __shared__ float f[kFewTokens];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Group grp = find_group<true>(p, blockIdx.y, false);
+    if (grp.mask == 0) {  // uniform over the CTA
+        pdl_wait();
+        return;
+    }
+    if (warp == 0 && ((grp.mask >> lane) & 1u))
+        tok[__popc(grp.mask & ((1u << lane) - 1u))] = lane;
+    __syncthreads();
+    const int count = __popc(grp.mask);
+    const int l = grp.adapter;
+    const int rank = l >= 0 ? rank_of(p, l) : 0;
+    const int blocks = (rank + 31) / 32;
+    const int n = blockIdx.x * (kExpandWarps * 32) + warp * 32 + 4 * (lane >> 2);
+    constexpr int kAhead = 2;  // blocks of B loaded before the wait
+    BRows b[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (i < blocks) b[i] = b_load(p, l, rank, n, i);
+    float4 y[NT][2];
+    y_fetch<YT, NT>(p, y, tok, count, n, vec != 0);
+    const float scale = l >= 0 && p.scales ? __ldcg(p.scales + l) : 1.0f;
+
+    pdl_wait();
+    pdl_launch_dependents();
+    // v: the K-split partials in order; then the 16-bit terms
+    const int pitch = term_pitch((p.R + 31) / 32), term_size = NT * 8 * pitch;
+    for (int j = warp; j < NT * 8 && blocks > 0; j += kExpandWarps) {
+        float v[8], top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 32 + lane;
+            v[i] = 0.0f;
+            if (i >= blocks || j >= count || r >= rank) continue;
+            const float* src = part + static_cast<size_t>(tok[j]) * p.R + r;
+            const size_t step = static_cast<size_t>(p.M) * p.R;
+            for (int s0 = 0; s0 < splits; s0 += 16) {
+                float w[16];
+#pragma unroll
+                for (int s = 0; s < 16; ++s) w[s] = s0 + s < splits ? src[(s0 + s) * step] : 0.0f;
+#pragma unroll
+                for (int s = 0; s < 16; ++s) v[i] += w[s];
+            }
+            top = fmaxf(top, fabsf(v[i]));
+        }
+        const float up = pow2_below<BF>(warp_max(top)), down = 1.0f / up;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i >= blocks) break;
+            uint16_t w[3];
+            split_terms<BF>(v[i] * down, w);
+#pragma unroll
+            for (int q = 0; q < terms<BF>(); ++q)
+                sv[q * term_size + j * pitch + i * 32 + lane] = w[q];
+        }
+        if (lane == 0 && j < count) f[j] = scale * up;
+    }
+    __syncthreads();
+    if (blocks == 0) {
+        if (p.y_in == p.y_out && p.ld_in == p.ld_out) return;
+        if (threadIdx.x < kFewTokens) f[threadIdx.x] = 0.0f;
+        __syncthreads();
+    }
+    float acc[2][NT][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[h][i][c] = 0.0f;
+    for (int blk = 0; blk < blocks; blk += kAhead) {
+        if (blk > 0) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (blk + i < blocks) b[i] = b_load(p, l, rank, n, blk + i);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (blk + i < blocks)
+                expand_block<BF, NT>(acc, b[i], sv, pitch, term_size, blk + i, count);
+    }
+    expand_store<YT, NT>(p, acc, y, tok, f, count, n, vec != 0);
+}
+
+// ----------------------------------------------------------------------------
+// More tokens: plan, shrink, expand over tiles
+// ----------------------------------------------------------------------------
+
+struct Plan {
+    int* perm;           // [M] tokens, sorted by adapter
+    int4* tiles;         // adapter (-1: none), first position, tokens
+    int* num_tiles;
+    unsigned* arrived;   // [max_tiles] K splits finished
+    float* part;         // [splits][M][R], by position
+    uint16_t* terms;     // [terms][M][rp], by position
+    float* f;            // [M] scale and power of two, by position
+    int max_tiles;
+    int rp;              // R rounded up to 32
+};
+
+// One CTA: stable counting sort of the tokens by adapter (tokens without one
+// last), cut into tiles of at most kTile.  Every warp counts and places a
+// contiguous range of tokens in its own histogram, so the order is fixed.
+__global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Plan pl, int warps) {
+    extern __shared__ int hist[];  // [warps][bins], then offsets [bins], tiles [bins]
+    __shared__ int ws[2][32];
+    const int bins = p.L + 1;
+    int* off = hist + warps * bins;
+    int* tfirst = off + bins;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nthreads = blockDim.x;
+    for (int i = threadIdx.x; i < warps * bins; i += nthreads) hist[i] = 0;
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int i = threadIdx.x; i < pl.max_tiles; i += nthreads) pl.arrived[i] = 0u;
+    __syncthreads();
+    const int per = ((p.M + warps - 1) / warps + 31) / 32 * 32;
+    const int m0 = warp * per, m1 = min(m0 + per, p.M);
+    int* mine = hist + warp * bins;
+    for (int base = m0; base < m1; base += 32) {
+        const int m = base + lane;
+        int key = -1;
+        if (m < m1) {
+            key = adapter_of(p, m, true);
+            if (key < 0) key = p.L;
+        }
+        const unsigned same = __match_any_sync(0xffffffffu, key);
+        if (key >= 0 && __ffs(same) - 1 == lane) mine[key] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    // per bin: the warps' counts to offsets; then a scan over the bins, each
+    // thread owning a contiguous span
+    const int span = (bins + nthreads - 1) / nthreads;
+    const int b0 = min(static_cast<int>(threadIdx.x) * span, bins), b1 = min(b0 + span, bins);
+    int n_tok = 0, n_tile = 0;
+    for (int b = b0; b < b1; ++b) {
+        int total = 0;
+        for (int w = 0; w < warps; ++w) {
+            const int c = hist[w * bins + b];
+            hist[w * bins + b] = total;
+            total += c;
+        }
+        off[b] = total;
+        n_tok += total;
+        n_tile += (total + kTile - 1) / kTile;
+    }
+    int s_tok = n_tok, s_tile = n_tile;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, s_tok, o), c = __shfl_up_sync(0xffffffffu, s_tile, o);
+        if (lane >= o) s_tok += a, s_tile += c;
+    }
+    if (lane == 31) ws[0][warp] = s_tok, ws[1][warp] = s_tile;
+    __syncthreads();
+    int at_tok = s_tok - n_tok, at_tile = s_tile - n_tile;
+    for (int w = 0; w < warp; ++w) at_tok += ws[0][w], at_tile += ws[1][w];
+    for (int b = b0; b < b1; ++b) {
+        const int total = off[b];
+        off[b] = at_tok;
+        tfirst[b] = at_tile;
+        for (int k = 0; k < total; k += kTile)
+            pl.tiles[at_tile++] = make_int4(b < p.L ? b : -1, at_tok + k, min(kTile, total - k), 0);
+        at_tok += total;
+    }
+    if (threadIdx.x == nthreads - 1) *pl.num_tiles = at_tile;
+    __syncthreads();
+    for (int base = m0; base < m1; base += 32) {
+        const int m = base + lane;
+        int key = -1;
+        if (m < m1) {
+            key = adapter_of(p, m, false);
+            if (key < 0) key = p.L;
+        }
+        const unsigned same = __match_any_sync(0xffffffffu, key);
+        const int leader = __ffs(same) - 1;
+        int at = 0;
+        if (key >= 0 && leader == lane) {
+            at = mine[key];
+            mine[key] = at + __popc(same);
+        }
+        at = __shfl_sync(0xffffffffu, at, leader);
+        if (key >= 0) pl.perm[off[key] + at + __popc(same & ((1u << lane) - 1u))] = m;
+        __syncwarp();
+    }
+}
+
+// CTA (split, tile).  The last split of a tile to finish adds up the
+// partials in split order and writes v's terms.
+template <bool BF>
+__global__ void __launch_bounds__(kShrinkWarps * 32)
+    lora_shrink_tiles(pq2h::LoraParams p, Plan pl, int k_split) {
+    constexpr int NT = kTile / 8;
+    __shared__ float red[kShrinkWarps * 16 * NT * 8];
+    __shared__ int tok[kTile];
+    __shared__ bool s_last;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (static_cast<int>(blockIdx.y) >= *pl.num_tiles) return;
+    const int4 tile = pl.tiles[blockIdx.y];
+    if (tile.x < 0) return;
+    const int l = tile.x, first = tile.y, count = tile.z;
+    const int rank = rank_of(p, l);
+    if (rank == 0) return;
+    if (threadIdx.x < count) tok[threadIdx.x] = pl.perm[first + threadIdx.x];
+    __syncthreads();
+    const int splits = gridDim.x;
+    const int k0 = blockIdx.x * k_split, k1 = min(k0 + k_split, p.K);
+    float* dst = pl.part + (static_cast<size_t>(blockIdx.x) * p.M + first) * p.R;
+    shrink_tile<BF, NT>(p, l, rank, tok, count, k0, k1, red,
+                        [&](int j, int r, float v) { dst[static_cast<size_t>(j) * p.R + r] = v; });
+    __syncthreads();
+    if (threadIdx.x == 0)
+        s_last = atom_add_acq_rel_gpu(&pl.arrived[blockIdx.y], 1u) + 1u == static_cast<unsigned>(splits);
+    __syncthreads();
+    if (!s_last) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float scale = p.scales ? p.scales[l] : 1.0f;
+    const size_t step = static_cast<size_t>(p.M) * p.R;
+    const size_t term_size = static_cast<size_t>(p.M) * pl.rp;
+    const int blocks = (rank + 31) / 32;
+    // each warp's tokens (warp, warp + 8, ...), 4 at a time, 4 ranks a lane
+    for (int j0 = warp; j0 < count; j0 += kShrinkWarps * 4) {
+        float top[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int pass = 0; pass < 2; ++pass) {
+            float up[4];
+            if (pass == 1) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    up[q] = pow2_below<BF>(warp_max(top[q]));
+                    const int j = j0 + q * kShrinkWarps;
+                    if (lane == 0 && j < count) pl.f[first + j] = scale * up[q];
+                }
+            }
+            for (int i0 = 0; i0 < blocks; i0 += 4) {
+                float v[4][4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[q][i] = 0.0f;
+                for (int s = 0; s < splits; ++s)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int j = j0 + q * kShrinkWarps, r = (i0 + i) * 32 + lane;
+                            if (j < count && r < rank)
+                                v[q][i] += __ldcg(pl.part + s * step +
+                                                  static_cast<size_t>(first + j) * p.R + r);
+                        }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = j0 + q * kShrinkWarps, blk = i0 + i;
+                        if (pass == 0) {
+                            top[q] = fmaxf(top[q], fabsf(v[q][i]));
+                        } else if (j < count && blk < blocks) {
+                            uint16_t w[3];
+                            split_terms<BF>(v[q][i] / up[q], w);
+#pragma unroll
+                            for (int k = 0; k < terms<BF>(); ++k)
+                                pl.terms[k * term_size + static_cast<size_t>(first + j) * pl.rp +
+                                         blk * 32 + lane] = w[k];
+                        }
+                    }
+            }
+        }
+    }
+}
+
+// CTA (rounds x 128 outputs, tile): v's terms in shared memory, then per 32
+// outputs and warp: y loads first, the product meanwhile, one store.
+template <bool BF, int YT>
+__global__ void __launch_bounds__(kExpandWarps * 32, 3)
+    lora_expand_tiles(pq2h::LoraParams p, Plan pl, int rounds, int vec) {
+    constexpr int NT = kTile / 8;
+    extern __shared__ __align__(16) uint16_t sv[];
+    __shared__ int tok[kTile];
+    __shared__ float f[kTile];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // the plan is complete before shrink lets this kernel start
+    const bool here = static_cast<int>(blockIdx.y) < __ldcg(pl.num_tiles);
+    const int4 tile = here ? __ldcg(pl.tiles + blockIdx.y) : make_int4(-1, 0, 0, 0);
+    const int l = tile.x, first = tile.y, count = tile.z;
+    const int rank = l >= 0 ? rank_of(p, l) : 0;
+    const int blocks = (rank + 31) / 32;
+    const bool in_place = p.y_in == p.y_out && p.ld_in == p.ld_out;
+    if (!here || (rank == 0 && in_place)) {  // uniform over the CTA
+        pdl_wait();
+        return;
+    }
+    if (threadIdx.x < count) tok[threadIdx.x] = __ldcg(pl.perm + first + threadIdx.x);
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+    const int pitch = term_pitch(blocks), term_size = kTile * pitch;
+    if (threadIdx.x < kTile)
+        f[threadIdx.x] = rank > 0 && static_cast<int>(threadIdx.x) < count ? pl.f[first + threadIdx.x] : 0.0f;
+    const int per_row = blocks * 4;  // 16-byte pieces
+    for (int i = threadIdx.x; i < terms<BF>() * kTile * per_row; i += kExpandWarps * 32) {
+        const int c = i % per_row, j = (i / per_row) % kTile, q = i / (per_row * kTile);
+        *reinterpret_cast<uint4*>(sv + q * term_size + j * pitch + c * 8) =
+            j < count ? load16(pl.terms + (static_cast<size_t>(q) * p.M + first + j) * pl.rp + c * 8)
+                      : zero4();
+    }
+    __syncthreads();
+    for (int round = 0; round < rounds; ++round) {
+        const int n = (blockIdx.x * rounds + round) * (kExpandWarps * 32) + warp * 32 + 4 * (lane >> 2);
+        float4 y[NT][2];
+        y_fetch<YT, NT>(p, y, tok, count, n, vec != 0);
+        float acc[2][NT][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[h][i][c] = 0.0f;
+        for (int blk = 0; blk < blocks; ++blk) {
+            const BRows b = b_load(p, l, rank, n, blk);
+            expand_block<BF, NT>(acc, b, sv, pitch, term_size, blk, count);
+        }
+        expand_store<YT, NT>(p, acc, y, tok, f, count, n, vec != 0);
+    }
+}
+
+}  // namespace
+}  // namespace pq2
+
+namespace pq2h {
+
+namespace {
+
+using pq2::kFewTokens;
+using pq2::kMaxSplits;
+using pq2::kTile;
+
+// The GPU's SMs: the K splits are sized for it on the host, before a device
+// is known (pq2_lora_workspace_bytes).
+constexpr int64_t kSms = 152;
+
+size_t pad(size_t b) { return (b + 255) & ~size_t(255); }
+
+struct Layout {
+    int splits, k_split, max_tiles, rp;
+    size_t part, terms, f, perm, tiles, num_tiles, arrived, bytes;
+};
+
+// K splits: two CTAs per SM over the groups or tiles that may appear, at
+// least 16 KB of A each.
+Layout layout(int64_t M, int64_t K, int64_t L, int64_t R) {
+    Layout y = {};
+    const bool few = M <= kFewTokens;
+    const int64_t work = few ? std::min(M, L) : (M + kTile - 1) / kTile + std::min(L, M / 2);
+    int64_t s = (2 * kSms + work - 1) / work;
+    s = std::min(s, std::max<int64_t>(1, K * R * 2 / 16384));
+    s = std::min<int64_t>(s, kMaxSplits);
+    y.k_split = static_cast<int>(((K + s - 1) / s + 127) / 128 * 128);
+    y.splits = static_cast<int>((K + y.k_split - 1) / y.k_split);
+    y.rp = static_cast<int>((R + 31) / 32 * 32);
+    size_t o = 0;
+    y.part = o;
+    o += pad(static_cast<size_t>(y.splits) * M * R * 4);
+    if (!few) {
+        y.max_tiles = static_cast<int>((M + kTile - 1) / kTile + std::min(L + 1, M));
+        y.terms = o;
+        o += pad(static_cast<size_t>(3) * M * y.rp * 2);
+        y.f = o;
+        o += pad(static_cast<size_t>(M) * 4);
+        y.perm = o;
+        o += pad(static_cast<size_t>(M) * 4);
+        y.tiles = o;
+        o += pad(static_cast<size_t>(y.max_tiles) * 16);
+        y.num_tiles = o;
+        o += 256;
+        y.arrived = o;
+        o += pad(static_cast<size_t>(y.max_tiles) * 4);
+    }
+    y.bytes = o;
+    return y;
+}
+
+template <bool BF, int NT, int YT>
+cudaError_t run_few(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cudaStream_t st) {
+    float* part = reinterpret_cast<float*>(ws + lay.part);
+    cudaError_t e = launch(pq2::lora_shrink_few<BF, NT>,
+                           dim3(lay.splits, static_cast<unsigned>(std::min(p.M, p.L))),
+                           dim3(pq2::kShrinkWarps * 32), 0, st, true, p, part, lay.k_split);
+    if (e != cudaSuccess) return e;
+    static SmemLimit lim;
+    const size_t smem = static_cast<size_t>(pq2::terms<BF>()) * NT * 8 *
+                        pq2::term_pitch((p.R + 31) / 32) * 2;
+    e = ensure_smem(lim, pq2::lora_expand_few<BF, NT, YT>, smem);
+    if (e != cudaSuccess) return e;
+    const int cols = pq2::kExpandWarps * 32;
+    return launch(pq2::lora_expand_few<BF, NT, YT>,
+                  dim3((p.N + cols - 1) / cols, static_cast<unsigned>(std::min(p.M, p.L + 1))),
+                  dim3(cols), smem, st, true, p, part, lay.splits, vec);
+}
+
+template <bool BF, int YT>
+cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cudaStream_t st) {
+    if (p.M <= 8) return run_few<BF, 1, YT>(p, lay, ws, vec, st);
+    if (p.M <= kFewTokens) return run_few<BF, 4, YT>(p, lay, ws, vec, st);
+    pq2::Plan pl = {};
+    pl.part = reinterpret_cast<float*>(ws + lay.part);
+    pl.terms = reinterpret_cast<uint16_t*>(ws + lay.terms);
+    pl.f = reinterpret_cast<float*>(ws + lay.f);
+    pl.perm = reinterpret_cast<int*>(ws + lay.perm);
+    pl.tiles = reinterpret_cast<int4*>(ws + lay.tiles);
+    pl.num_tiles = reinterpret_cast<int*>(ws + lay.num_tiles);
+    pl.arrived = reinterpret_cast<unsigned*>(ws + lay.arrived);
+    pl.max_tiles = lay.max_tiles;
+    pl.rp = lay.rp;
+    // as many warps as have tokens and fit their histograms in 200 KB
+    const int bins = p.L + 1;
+    int warps = 32;
+    while (warps > 1 && (warps / 2 * 32 >= p.M || static_cast<size_t>(warps + 2) * bins * 4 > 200 * 1024))
+        warps /= 2;
+    const size_t plan_smem = static_cast<size_t>(warps + 2) * bins * 4;
+    static SmemLimit plan_lim;
+    cudaError_t e = ensure_smem(plan_lim, pq2::lora_plan_kernel, plan_smem);
+    if (e != cudaSuccess) return e;
+    e = launch(pq2::lora_plan_kernel, dim3(1), dim3(warps * 32), plan_smem, st, true, p, pl, warps);
+    if (e != cudaSuccess) return e;
+    e = launch(pq2::lora_shrink_tiles<BF>, dim3(lay.splits, lay.max_tiles),
+               dim3(pq2::kShrinkWarps * 32), 0, st, true, p, pl, lay.k_split);
+    if (e != cudaSuccess) return e;
+    static SmemLimit lim;
+    const size_t smem = static_cast<size_t>(pq2::terms<BF>()) * kTile *
+                        pq2::term_pitch((p.R + 31) / 32) * 2;
+    e = ensure_smem(lim, pq2::lora_expand_tiles<BF, YT>, smem);
+    if (e != cudaSuccess) return e;
+    const int rounds = p.M <= 512 ? 1 : 4;
+    const int cols = pq2::kExpandWarps * 32 * rounds;
+    return launch(pq2::lora_expand_tiles<BF, YT>, dim3((p.N + cols - 1) / cols, lay.max_tiles),
+                  dim3(pq2::kExpandWarps * 32), smem, st, true, p, pl, rounds, vec);
+}
+
+}  // namespace
+
+size_t lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+    (void)N;
+    return layout(M, K, L, R).bytes;
+}
+
+cudaError_t launch_lora(const LoraParams& p, void* workspace, cudaStream_t st,
+                        const DeviceInfo& dev) {
+    (void)dev;
+    const Layout lay = layout(p.M, p.K, p.L, p.R);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    // 4-wide accesses to y: every row starts on their boundary
+    const size_t unit = p.y_type == PQ2_F32 ? 16 : 8;
+    const bool vec = p.ld_in % 4 == 0 && p.ld_out % 4 == 0 &&
+                     reinterpret_cast<uintptr_t>(p.y_in) % unit == 0 &&
+                     reinterpret_cast<uintptr_t>(p.y_out) % unit == 0;
+    if (p.bf16)
+        return p.y_type == PQ2_F32 ? run<true, PQ2_F32>(p, lay, ws, vec, st)
+                                   : run<true, PQ2_BF16>(p, lay, ws, vec, st);
+    return p.y_type == PQ2_F32 ? run<false, PQ2_F32>(p, lay, ws, vec, st)
+                               : run<false, PQ2_BF16>(p, lay, ws, vec, st);
+}
+
+}  // namespace pq2h

@@ -1,0 +1,372 @@
+// Verification of drafted tokens: the step after the lm_head when M = drafts
+// + 1 token rows of a sequence went through the model at once.  For each
+// sequence, with p_i = softmax(logits_i / T) and q_i the drafter's
+// probabilities at position i:
+//
+//   draft d_i is taken while u_i q_i(d_i) < p_i(d_i);
+//   the token after the taken ones is argmax_v w(v) / e(v), e(v) ~ Exp(1),
+//   w = max(p_i - q_i, 0) at the first refused draft, w = p_n if none is.
+//
+// argmax_v w(v) / e(v) draws v with probability w(v) / sum w (the smallest of
+// exponential variables e(v) / w(v)), so the drawn tokens follow the target's
+// distribution, and no prefix sum over the vocabulary is needed.
+// T = 0: drafts are taken while they are the argmax, and the argmax follows.
+//
+// Bound by HBM: one pass over all logits rows, and one over a single row of
+// logits (mostly still in L2), q and e per sequence.  Two kernels:
+//   verify_stats_kernel  splits every row into pieces of kPiece values; a
+//       thread holds its values in registers, so maximum and sum of
+//       exponentials take one read and no rescaling within a piece.
+//   verify_pick_kernel   the same pieces of each sequence's chosen row; every
+//       CTA joins the pieces' statistics of the sequence's rows, finds the
+//       first refusal (the same arithmetic in each CTA) and reduces its piece
+//       to one 64-bit key (score bits, then lowest index first).  atomicMax
+//       joins the keys: the maximum does not depend on the order.  The last
+//       CTA of a sequence writes the result.
+#include <algorithm>
+#include <climits>
+
+#include "pq2_common.cuh"
+#include "pq2_internal.h"
+
+namespace pq2 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kVecs = 4;                        // 16-byte vectors per thread
+constexpr int kPiece = kThreads * kVecs * 4;    // values of a row per CTA
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Values e .. e + 3 of a row of V values, with `fill` outside [0, V); `vec`:
+// e is on a 16-byte boundary of the row's memory.
+__device__ __forceinline__ float4 load4(const float* row, int e, int V, bool vec, float fill) {
+    if (vec && e >= 0 && e + 3 < V) return *reinterpret_cast<const float4*>(row + e);
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = (e + j >= 0 && e + j < V) ? row[e + j] : fill;
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// Number of values between the 16-byte boundary below `p` and `p`.
+__device__ __forceinline__ int lead(const float* p) {
+    return static_cast<int>((reinterpret_cast<uintptr_t>(p) >> 2) & 3u);
+}
+
+// 1 / temperature in units of log2(e); 0 selects the greedy rule.
+__device__ __forceinline__ float scale_of(float temperature) {
+    return temperature > 0.0f ? kLog2e / temperature : 0.0f;
+}
+
+// The later of two (maximum, lowest index) pairs.
+__device__ __forceinline__ void best_of(float& m, int& at, float m2, int at2) {
+    if (m2 > m || (m2 == m && at2 < at)) {
+        m = m2;
+        at = at2;
+    }
+}
+
+// (maximum, sum of exponentials relative to it) of two pieces.
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2, float c) {
+    const float top = fmaxf(m, m2);
+    if (top == neg_inf()) return;  // both empty: s = 0
+    s = s * ex2((m - top) * c) + s2 * ex2((m2 - top) * c);
+    m = top;
+}
+
+__global__ void __launch_bounds__(kThreads) verify_stats_kernel(pq2h::VerifyParams p) {
+    __shared__ float sm[kWarps], ss[kWarps];
+    __shared__ int si[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long row = blockIdx.x / p.chunks;
+    const int chunk = static_cast<int>(blockIdx.x - row * p.chunks);
+    pdl_wait();
+    pdl_launch_dependents();
+    const float* l = p.logits + row * p.ld_logits;
+    const int e0 = chunk * kPiece - lead(l);
+    float v[kVecs][4];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        const float4 f = load4(l, e0 + (i * kThreads + tid) * 4, p.V, true, neg_inf());
+        v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
+    }
+    if (blockIdx.x == 0) {
+        for (long long b = tid; b < p.B; b += kThreads) {
+            p.keys[2 * b] = p.keys[2 * b + 1] = 0ull;
+            p.done[b] = 0u;
+        }
+    }
+    // the row's sequence: the number of sequences that end at or before it
+    int seq = 0;
+    for (long long b0 = 0; b0 < p.B; b0 += kThreads) {
+        const long long b = b0 + tid;
+        seq += __syncthreads_count(b < p.B && p.row_start[b + 1] <= row);
+    }
+    const float c = seq < p.B ? scale_of(p.temperature[seq]) : 0.0f;
+
+    float m = neg_inf();
+    int at = INT_MAX;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (v[i][j] > m) {
+                m = v[i][j];
+                at = e0 + (i * kThreads + tid) * 4 + j;
+            }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        best_of(m, at, __shfl_xor_sync(0xffffffffu, m, off), __shfl_xor_sync(0xffffffffu, at, off));
+    if (lane == 0) sm[warp] = m, si[warp] = at;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) best_of(m, at, sm[w], si[w]);
+    float s = 0.0f;
+    if (m > neg_inf()) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s += ex2((v[i][j] - m) * c);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if (lane == 0) ss[warp] = s;
+    __syncthreads();
+    if (tid == 0) {
+        s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) s += ss[w];
+        p.stats[blockIdx.x] = make_float2(m, s);
+        p.best[blockIdx.x] = at;
+    }
+}
+
+// Score and index as one key: larger scores first, then lower indexes; 0 for
+// a value that cannot be drawn.
+__device__ __forceinline__ unsigned long long key_of(float score, int at) {
+    return score > 0.0f ? (static_cast<unsigned long long>(__float_as_uint(score)) << 32) |
+                              (0xffffffffu - static_cast<unsigned>(at))
+                        : 0ull;
+}
+
+__global__ void __launch_bounds__(kThreads) verify_pick_kernel(pq2h::VerifyParams p) {
+    __shared__ int s_stop;
+    __shared__ float s_max, s_inv;
+    __shared__ int s_best, s_refused;
+    __shared__ unsigned long long sk[2][kWarps];
+    __shared__ bool s_last;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long b = blockIdx.x / p.chunks;
+    const int chunk = static_cast<int>(blockIdx.x - b * p.chunks);
+    if (tid == 0) s_stop = INT_MAX;
+    pdl_wait();
+    pdl_launch_dependents();
+    __syncthreads();
+    const int r0 = p.row_start[b], r1 = p.row_start[b + 1];
+    if (r0 < 0 || r1 < r0 || r1 > p.rows) {  // uniform over the CTA
+        if (tid == 0 && chunk == 0) {
+            atomicOr(p.ctl.err, DEVERR_BAD_INDEX);
+            p.accepted[b] = 0;
+        }
+        return;
+    }
+    if (r0 == r1) {
+        if (tid == 0 && chunk == 0) p.accepted[b] = 0;
+        return;
+    }
+    const float c = scale_of(p.temperature[b]);
+    const bool greedy = c == 0.0f;
+    // A warp per row, a round of kWarps rows at a time: join the row's pieces
+    // and decide its draft.  The first row that stops ends the search.
+    for (int base = r0; base < r1; base += kWarps) {
+        const int row = base + warp;
+        float m = neg_inf(), s = 0.0f;
+        int at = INT_MAX;
+        bool stops = false, refused = false;
+        if (row < r1) {
+            const int d = p.drafts[row];
+            const bool last = row == r1 - 1 || d < 0 || d >= p.V;
+            float ld = 0.0f, qd = 1.0f, u = 0.0f;
+            if (!last) {
+                ld = p.logits[row * p.ld_logits + d];
+                if (!greedy) {
+                    u = p.u[row];
+                    if (p.q) qd = p.q[row * p.ld_q + d];
+                }
+            }
+            const long long o = static_cast<long long>(row) * p.chunks;
+            for (int k = lane; k < p.chunks; k += 32) {
+                const float2 f = p.stats[o + k];
+                if (greedy) {
+                    best_of(m, at, f.x, p.best[o + k]);
+                } else {
+                    join(m, s, f.x, f.y, c);
+                }
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+                const float m2 = __shfl_xor_sync(0xffffffffu, m, off);
+                const float s2 = __shfl_xor_sync(0xffffffffu, s, off);
+                const int at2 = __shfl_xor_sync(0xffffffffu, at, off);
+                if (greedy)
+                    best_of(m, at, m2, at2);
+                else
+                    join(m, s, m2, s2, c);
+            }
+            bool take = false;
+            if (!last) {
+                if (greedy)
+                    take = d == at;
+                else if (s > 0.0f)
+                    take = u * qd < ex2((ld - m) * c) / s;
+            }
+            stops = !take;
+            refused = stops && !last;
+            if (stops && lane == 0) atomicMin(&s_stop, row);
+        }
+        __syncthreads();
+        const int stop = s_stop;
+        __syncthreads();  // read by all before the next round's atomicMin
+        if (stop != INT_MAX) {
+            if (row == stop && lane == 0) {
+                s_max = m;
+                s_inv = s > 0.0f ? 1.0f / s : 0.0f;
+                s_best = at;
+                s_refused = refused;
+            }
+            break;
+        }
+    }
+    __syncthreads();
+    const int stop = s_stop;
+    const bool refused = s_refused != 0;
+    if (greedy) {
+        if (chunk != 0) return;
+    } else {
+        const float m = s_max, inv = s_inv;
+        const int d = p.drafts[stop];
+        const float* l = p.logits + stop * p.ld_logits;
+        const float* e = p.e + b * p.ld_e;
+        const float* q = refused && p.q ? p.q + stop * p.ld_q : nullptr;
+        const int off = lead(l);
+        const bool ve = lead(e) == off, vq = q && lead(q) == off;
+        unsigned long long k0 = 0, k1 = 0;
+        const int e0 = chunk * kPiece - off;
+        float4 lv[kVecs], ev[kVecs], qv[kVecs];
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int v0 = e0 + (i * kThreads + tid) * 4;
+            lv[i] = load4(l, v0, p.V, true, neg_inf());
+            ev[i] = load4(e, v0, p.V, ve, 1.0f);
+            qv[i] = q ? load4(q, v0, p.V, vq, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        if (m > neg_inf()) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const int v0 = e0 + (i * kThreads + tid) * 4;
+                const float lj[4] = {lv[i].x, lv[i].y, lv[i].z, lv[i].w};
+                const float ej[4] = {ev[i].x, ev[i].y, ev[i].z, ev[i].w};
+                const float qj[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float pv = ex2((lj[j] - m) * c) * inv;
+                    float w = pv;
+                    if (refused) w = q ? pv - qj[j] : (v0 + j == d ? 0.0f : pv);
+                    const unsigned long long a = key_of(__fdividef(w, ej[j]), v0 + j);
+                    k0 = a > k0 ? a : k0;
+                    if (refused) {
+                        const unsigned long long t = key_of(__fdividef(pv, ej[j]), v0 + j);
+                        k1 = t > k1 ? t : k1;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const unsigned long long a = __shfl_xor_sync(0xffffffffu, k0, o);
+            const unsigned long long t = __shfl_xor_sync(0xffffffffu, k1, o);
+            k0 = a > k0 ? a : k0;
+            k1 = t > k1 ? t : k1;
+        }
+        if (lane == 0) sk[0][warp] = k0, sk[1][warp] = k1;
+        __syncthreads();
+        if (tid == 0) {
+            for (int w = 0; w < kWarps; ++w) {
+                k0 = sk[0][w] > k0 ? sk[0][w] : k0;
+                k1 = sk[1][w] > k1 ? sk[1][w] : k1;
+            }
+            if (k0) atomicMax(&p.keys[2 * b], k0);
+            if (k1) atomicMax(&p.keys[2 * b + 1], k1);
+            s_last = atom_add_acq_rel_gpu(&p.done[b], 1u) + 1u == static_cast<unsigned>(p.chunks);
+        }
+        __syncthreads();
+        if (!s_last) return;
+    }
+    // the sequence's result
+    int token;
+    if (greedy) {
+        token = s_max > neg_inf() ? s_best : -1;
+    } else {
+        unsigned long long k = __ldcg(&p.keys[2 * b]);
+        if (k == 0) k = __ldcg(&p.keys[2 * b + 1]);  // p <= q everywhere: from p itself
+        token = k ? static_cast<int>(0xffffffffu - static_cast<unsigned>(k)) : -1;
+    }
+    if (tid == 0 && store_ok(p.ctl, b, 1, p.B)) p.accepted[b] = stop - r0;
+    for (int row = r0 + tid; row < r1; row += kThreads) {
+        const int t = row < stop ? p.drafts[row] : row == stop ? token : -1;
+        if (store_ok(p.ctl, row, 1, p.rows)) p.tokens[row] = t;
+    }
+}
+
+}  // namespace
+}  // namespace pq2
+
+namespace pq2h {
+
+namespace {
+
+int verify_chunks(int64_t V) {
+    // up to three values before the first 16-byte boundary of a row
+    return static_cast<int>((V + 3 + pq2::kPiece - 1) / pq2::kPiece);
+}
+
+size_t pad(size_t b) { return (b + 255) & ~size_t(255); }
+
+}  // namespace
+
+size_t verify_workspace_bytes(int64_t B, int64_t rows, int64_t V) {
+    const size_t pieces = static_cast<size_t>(rows) * verify_chunks(V);
+    return pad(pieces * 8) + pad(pieces * 4) + pad(static_cast<size_t>(B) * 16) +
+           pad(static_cast<size_t>(B) * 4);
+}
+
+cudaError_t launch_verify(VerifyParams p, void* workspace, cudaStream_t st) {
+    p.chunks = verify_chunks(p.V);
+    const size_t pieces = static_cast<size_t>(p.rows) * p.chunks;
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    p.stats = reinterpret_cast<float2*>(w);
+    w += pad(pieces * 8);
+    p.best = reinterpret_cast<int32_t*>(w);
+    w += pad(pieces * 4);
+    p.keys = reinterpret_cast<unsigned long long*>(w);
+    w += pad(static_cast<size_t>(p.B) * 16);
+    p.done = reinterpret_cast<unsigned*>(w);
+    // without rows every sequence is empty: nothing to prepare for pick
+    if (pieces > 0) {
+        const cudaError_t e = launch(pq2::verify_stats_kernel, dim3(static_cast<unsigned>(pieces)),
+                                     dim3(pq2::kThreads), 0, st, true, p);
+        if (e != cudaSuccess) return e;
+    }
+    return launch(pq2::verify_pick_kernel, dim3(static_cast<unsigned>(p.B * p.chunks)),
+                  dim3(pq2::kThreads), 0, st, true, p);
+}
+
+}  // namespace pq2h

@@ -282,6 +282,149 @@ pq2_status pq2_gemm_bf16_splitk(const uint16_t* x, const uint16_t* w, uint16_t* 
                                 int64_t N, int64_t K, uint32_t flags, void* stream);
 
 /*
+ * The steps around a projection (the pages time the projections alone; these
+ * are what a serving step over several requests runs between them).
+ */
+
+/* Element types of the arrays below. */
+#define PQ2_F32 0
+#define PQ2_F16 1
+#define PQ2_BF16 2
+
+/* Flags of pq2_rmsnorm and pq2_norm_residual (PQ2_WEIGHTS_STATIC, the norm
+ * weights, may be added). */
+#define PQ2_NORM_UNIT_OFFSET 2u /* weights are stored as w - 1                  */
+#define PQ2_NORM_NO_POST 4u     /* the block's output is not normed             */
+#define PQ2_GATE_SIGMOID 8u     /* the gate enters as sigmoid(gate)             */
+#define PQ2_GATE_SILU 16u       /* the gate enters as gate * sigmoid(gate)      */
+
+/* Widest row of the two norms. */
+#define PQ2_NORM_MAX_H 49152
+
+/*
+ * pq2_rmsnorm -- the norm before a block:
+ *   x[m] = r[m] / sqrt(mean(r[m]^2) + eps) * w
+ * in fp32, rounded once (nearest even; values past fp16's range become inf)
+ * to x's type -- fp16 is what pq2_matmul takes, bf16 what
+ * pq2_gemm_bf16_splitk takes.
+ *   r in [M, H] (r_type, row stride ld_r >= H elements), w in [H] (w_type) or
+ *   NULL (1), x out [M, H] (x_type, ld_x >= H).  x may be r where their types
+ *   and strides are the same.
+ * M >= 0 (M == 0 enqueues nothing), 1 <= H <= PQ2_NORM_MAX_H, eps >= 0.
+ * Pointers need their element's alignment only (PQ2_ERR_MISALIGNED
+ * otherwise); rows on 16-byte boundaries with H % 8 == 0 take the vector path.
+ */
+pq2_status pq2_rmsnorm(const void* r, int r_type, int64_t ld_r, const void* w, int w_type, void* x,
+                       int x_type, int64_t ld_x, int64_t M, int64_t H, float eps, uint32_t flags,
+                       void* stream);
+
+/*
+ * pq2_norm_residual -- the end of a block, and the norm before the next one,
+ * in one pass:
+ *   n    = y / sqrt(mean(y^2) + eps) * w_post      (n = y with NO_POST)
+ *   r'   = r + alpha * act(gate) * n               (gate absent: 1)
+ *   x    = r' / sqrt(mean(r'^2) + eps) * w_next    (from r' before rounding)
+ * per row, in fp32; r' and x are rounded once.  A struct, for its many
+ * optional parts; every pointer is a device pointer.
+ *   y       in   [M, H] the block's output (fp32 from pq2_matmul)
+ *   r       in   [M, H] residual stream
+ *   r_out   out  [M, H] of r's type; may be r
+ *   w_post  in   [H] or NULL (1)
+ *   gate    in   [M, H] with row stride ld_gate >= H, or one vector [H] for
+ *                all rows (ld_gate == 0), or NULL
+ *   w_next  in   [H] or NULL (1)
+ *   x       out  [M, H] the next block's input, or NULL (not computed)
+ * Other rules as pq2_rmsnorm.  Nothing but r_out and r may overlap.
+ */
+typedef struct pq2_norm_residual_args {
+    const void* y;
+    const void* r;
+    void* r_out;
+    const void* w_post;
+    const void* gate;
+    const void* w_next;
+    void* x;
+    int64_t ld_y, ld_r, ld_r_out, ld_gate, ld_x; /* row strides, elements */
+    int32_t y_type, r_type, w_type, gate_type, x_type;
+    float eps, alpha;
+    uint32_t flags;
+} pq2_norm_residual_args;
+pq2_status pq2_norm_residual(const pq2_norm_residual_args* args, int64_t M, int64_t H,
+                             void* stream);
+
+/*
+ * pq2_lora_add -- low-rank adapters of many requests beside a shared
+ * projection: for every token m with adapter l = ids[m] >= 0
+ *   y_out[m] = y_in[m] + scales[l] * B[l] (A[l] x[m])
+ * and y_out[m] = y_in[m] for ids[m] < 0.  Products and sums in fp32 or
+ * better; the rank-sized intermediate is never rounded to fewer than 22 bits
+ * of its largest value.
+ *   x       in   [M, K] (type: PQ2_F16 or PQ2_BF16; row stride ld_x >= K)
+ *   A       in   [L, R, K], B in [L, N, R], both of x's type
+ *   ids     in   int32 [M].  A value >= L counts as no adapter and sets the
+ *                device error word (PQ2_ERR_INVALID_ARG from
+ *                pq2_last_device_error).
+ *   ranks   in   int32 [L] or NULL (all R): rows of A (columns of B) in use,
+ *                0 <= rank <= R; the others may hold anything
+ *   scales  in   fp32 [L] or NULL (1)
+ *   y_in, y_out  [M, N] (y_type: PQ2_F32 or PQ2_BF16; row strides ld_in,
+ *                ld_out >= N); the same array, or arrays that do not overlap
+ *   workspace    pq2_lora_workspace_bytes(M, N, K, L, R) bytes
+ * M >= 0 and N >= 0 (either 0 enqueues nothing), 8 <= K <= PQ2_MAX_K with
+ * K % 8 == 0, 8 <= R <= PQ2_LORA_MAX_R with R % 8 == 0,
+ * 1 <= L <= PQ2_LORA_MAX_L, M <= PQ2_LORA_MAX_M.  x, A, B and workspace
+ * 16-byte aligned and ld_x % 8 == 0; y_in and y_out aligned to their element.
+ * NaN or Inf in x, or in the ranks in use: that token's y is undefined.
+ */
+#define PQ2_LORA_MAX_R 256
+#define PQ2_LORA_MAX_L 16384
+#define PQ2_LORA_MAX_M 1048576
+size_t pq2_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
+pq2_status pq2_lora_add(const void* x, int64_t ld_x, const void* A, const void* B, int type,
+                        const int32_t* ids, const int32_t* ranks, const float* scales,
+                        const void* y_in, int64_t ld_in, void* y_out, int64_t ld_out, int y_type,
+                        int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * pq2_verify_drafts -- which drafted tokens the target model keeps, and the
+ * token after them, from given random numbers.  Sequence b's token rows are
+ * row_start[b] .. row_start[b+1]-1: one per draft and one more.  With
+ * p = softmax(logits[row] / temperature[b]) and q the drafter's probabilities
+ * at the row (q NULL: it proposed its draft with certainty), row after row:
+ *   draft d = drafts[row] is kept while u[row] * q(d) < p(d);
+ *   at the first draft that is not: token = argmax_v max(p(v) - q(v), 0) / e[b][v]
+ *   (argmax_v p(v) / e[b][v] where that is 0 everywhere);
+ *   after the last draft: token = argmax_v p(v) / e[b][v].
+ * With e drawn from Exp(1) and u from U[0, 1), kept drafts and token follow
+ * the target's distribution.  temperature[b] <= 0: greedy -- a draft is kept
+ * while it is the row's argmax, and token is the argmax of the row after.
+ * Ties go to the lowest index.  Values of -inf are masked (never drawn); a
+ * row with nothing else keeps no draft and gives token -1.  A draft outside
+ * [0, V) ends the sequence's drafts (padding): its row is the row after.
+ *   logits      in   fp32 [rows, V], row stride ld_logits >= V (no NaN, no +inf)
+ *   row_start   in   int32 [B + 1], 0 <= row_start[b] <= row_start[b+1] <= rows;
+ *                    a sequence that breaks this keeps 0 and sets the device
+ *                    error word.  A sequence without rows keeps 0.
+ *   drafts      in   int32 [rows] (a sequence's last one is not read as a draft)
+ *   q           in   fp32 [rows, V], row stride ld_q >= V, or NULL
+ *   u           in   fp32 [rows]
+ *   e           in   fp32 [B, V], row stride ld_e >= V, > 0
+ *   temperature in   fp32 [B]
+ *   accepted    out  int32 [B]   drafts kept
+ *   tokens      out  int32 [rows] kept drafts, then token, then -1
+ *   workspace   pq2_verify_workspace_bytes(B, rows, V) bytes, 16-byte aligned
+ * B >= 0 (0 enqueues nothing), rows >= 0, 1 <= V <= 2^30.  logits, q, u and e:
+ * 4-byte aligned (PQ2_ERR_MISALIGNED otherwise).
+ */
+size_t pq2_verify_workspace_bytes(int64_t B, int64_t rows, int64_t V);
+pq2_status pq2_verify_drafts(const float* logits, int64_t ld_logits, const int32_t* row_start,
+                             const int32_t* drafts, const float* q, int64_t ld_q, const float* u,
+                             const float* e, int64_t ld_e, const float* temperature,
+                             int32_t* accepted, int32_t* tokens, int64_t B, int64_t rows, int64_t V,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * pq2_workspace_bytes -- scratch bytes `op` needs for this shape (0 if none,
  * SIZE_MAX if the shape is not supported).
  */
@@ -304,7 +447,8 @@ pq2_status pq2_group_dots(int op, const int8_t* qp, const int32_t* T, const uint
  * current device's error word: PQ2_ERR_TIMEOUT if a kernel's bounded wait ran
  * out, PQ2_ERR_BOUNDS (bounds-checked build only) if a kernel skipped a store
  * outside its buffer, PQ2_ERR_INVALID_ARG if pq2_pack_weights met a
- * non-ternary value,
+ * non-ternary value or an index array of pq2_lora_add or pq2_verify_drafts a
+ * value outside its range,
  * PQ2_OK otherwise (PQ2_ERR_CUDA if the synchronisation itself failed).
  */
 pq2_status pq2_last_device_error(void* stream);
