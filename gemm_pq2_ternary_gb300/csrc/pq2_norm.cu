@@ -228,12 +228,280 @@ __global__ void __launch_bounds__(1024) norm_wide_kernel(pq2h::NormParams p) {
     }
 }
 
+// Many rows: a bulk-copy ring.  One CTA per SM walks over rows; a producer
+// warp keeps the next rows' y, r and gate on their way into shared memory
+// (stages rows deep, whatever registers and barriers are doing), and groups of
+// warps take the rows in turn, one row a group.  Both weight vectors (a gate
+// that is one vector is folded into the first) wait in shared memory as fp32.
+constexpr int kRingVpt = 4;            // vectors of 4 values per thread
+constexpr int kRingMaxGroups = 12;     // named barriers 1 .. 12
+constexpr int kRingMaxWarps = 23;      // consumer warps (and one producer): 80 registers
+constexpr int kRingMaxStages = 16;
+
+// This thread's values of a row in shared memory (vectors t, t + threads, ...
+// of 4; zeros past H, which no thread has where kFull).  The type is asked once per row, not per vector.
+template <int kType, bool kFull>
+__device__ __forceinline__ void lds_values(const uint8_t* base, int t, int threads, int H,
+                                           float (&v)[kRingVpt][4]) {
+#pragma unroll
+    for (int k = 0; k < kRingVpt; ++k) {
+        const int e = (t + k * threads) * 4;
+        if constexpr (kType == PQ2_F32) {
+            const float4 f = kFull || e < H ? *reinterpret_cast<const float4*>(base + e * 4)
+                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            v[k][0] = f.x, v[k][1] = f.y, v[k][2] = f.z, v[k][3] = f.w;
+        } else {
+            const uint2 u = kFull || e < H ? *reinterpret_cast<const uint2*>(base + e * 2) : make_uint2(0, 0);
+            const uint32_t w[2] = {u.x, u.y};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if constexpr (kType == PQ2_BF16) {
+                    v[k][2 * j] = __uint_as_float(w[j] << 16);
+                    v[k][2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+                } else {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+                    v[k][2 * j] = f.x;
+                    v[k][2 * j + 1] = f.y;
+                }
+            }
+        }
+    }
+}
+template <bool kFull>
+__device__ __forceinline__ void lds_row(const uint8_t* base, int type, int t, int threads, int H,
+                                        float (&v)[kRingVpt][4]) {
+    if (type == PQ2_F32)
+        lds_values<PQ2_F32, kFull>(base, t, threads, H, v);
+    else if (type == PQ2_BF16)
+        lds_values<PQ2_BF16, kFull>(base, t, threads, H, v);
+    else
+        lds_values<PQ2_F16, kFull>(base, t, threads, H, v);
+}
+
+template <int kType, bool kFull>
+__device__ __forceinline__ void store_values(const DevCtl& ctl, void* out, long long o, long long n,
+                                             int t, int threads, int H,
+                                             const float (&v)[kRingVpt][4]) {
+#pragma unroll
+    for (int k = 0; k < kRingVpt; ++k) {
+        const int e = (t + k * threads) * 4;
+        if ((!kFull && e >= H) || !store_ok(ctl, o + e, 4, n)) continue;
+        if constexpr (kType == PQ2_F32)
+            *reinterpret_cast<float4*>(static_cast<float*>(out) + o + e) =
+                make_float4(v[k][0], v[k][1], v[k][2], v[k][3]);
+        else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + o + e) = make_uint2(
+                f32x2_to_elem16(v[k][0], v[k][1], kType), f32x2_to_elem16(v[k][2], v[k][3], kType));
+    }
+}
+template <bool kFull>
+__device__ __forceinline__ void store_row(const DevCtl& ctl, void* out, int type, long long o,
+                                          long long n, int t, int threads, int H,
+                                          const float (&v)[kRingVpt][4]) {
+    if (type == PQ2_F32)
+        store_values<PQ2_F32, kFull>(ctl, out, o, n, t, threads, H, v);
+    else if (type == PQ2_BF16)
+        store_values<PQ2_BF16, kFull>(ctl, out, o, n, t, threads, H, v);
+    else
+        store_values<PQ2_F16, kFull>(ctl, out, o, n, t, threads, H, v);
+}
+
+// Four chains, so that no addition waits for the one before it.
+__device__ __forceinline__ float sum_squares(const float (&v)[kRingVpt][4]) {
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < kRingVpt; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] = fmaf(v[k][j], v[k][j], s[j]);
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// Sum over a group of `threads` threads (named barrier `bar`); `bad` of any of
+// them reaches all in `any`.
+__device__ __forceinline__ float group_sum(float v, float* slot, int bar, int threads, bool bad,
+                                           bool& any) {
+    v = warp_sum(v);
+    if (threads == 32) {
+        any = bad;  // warp-uniform
+        return v;
+    }
+    const int warp = (threadIdx.x % threads) >> 5, nwarps = threads >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) slot[warp] = v;
+    any = named_bar_any(bar, threads, bad);
+    // the warps' sums, added in the same order by every warp
+    return warp_sum(lane < nwarps ? slot[lane] : 0.0f);
+}
+
+template <bool kAfter, bool kFull>
+__global__ void __launch_bounds__((kRingMaxWarps + 1) * 32, 1)
+    norm_ring_kernel(pq2h::NormParams p, int threads, int groups, int stages, int stage_bytes) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t full[kRingMaxStages], empty[kRingMaxStages];
+    __shared__ float slot[kRingMaxGroups][2][kRingMaxWarps];
+    __shared__ int abort_word;
+    volatile int* abort_flag = &abort_word;
+    uint8_t* ring = smem;
+    float* w_post = reinterpret_cast<float*>(smem + static_cast<size_t>(stages) * stage_bytes);
+    float* w_next = w_post + p.H;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int consumers = threads * groups;
+    const bool producer = tid >= consumers;
+    if (tid == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], threads / 32);
+        }
+        abort_word = 0;
+        fence_mbar_init();
+    }
+    const int y_bytes = kAfter ? p.H * (p.y_type == PQ2_F32 ? 4 : 2) : 0;
+    const int r_bytes = p.H * (p.r_type == PQ2_F32 ? 4 : 2);
+    const bool gate_rows = kAfter && p.gate && p.ld_gate != 0;
+    const bool gate_vec = kAfter && p.gate && p.ld_gate == 0;
+    const int g_bytes = gate_rows ? p.H * (p.gate_type == PQ2_F32 ? 4 : 2) : 0;
+    // rows of this CTA: blockIdx.x + i * gridDim.x, i < count
+    const int count = static_cast<int>((p.M - blockIdx.x + gridDim.x - 1) / gridDim.x);
+    __syncthreads();  // the barriers are there
+    if (producer) {
+        pdl_wait();
+        pdl_launch_dependents();
+        // lanes 0, 1, 2: the copies of y, r and the gate
+        const int bytes = lane == 0 ? y_bytes : lane == 1 ? r_bytes : lane == 2 ? g_bytes : 0;
+        const int at = lane == 0 ? 0 : lane == 1 ? y_bytes : y_bytes + r_bytes;
+        const uint8_t* src = static_cast<const uint8_t*>(lane == 0 ? p.y : lane == 1 ? p.r : p.gate);
+        const long long ld =
+            lane == 0 ? p.ld_y * (y_bytes / p.H)
+                      : lane == 1 ? p.ld_r * (r_bytes / p.H) : p.ld_gate * (g_bytes / p.H);
+        src += blockIdx.x * ld;
+        int i = 0, s = 0;
+        uint32_t turn = 0;  // times the ring has gone round
+        for (; i < count; ++i) {
+            if (turn > 0 && !mbar_wait_warp(&empty[s], (turn - 1) & 1, p.ctl, abort_flag)) break;
+            if (i != p.ctl.debug_skip_stage) {  // else withheld (timeout test)
+                if (lane == 0) mbar_arrive_expect_tx(&full[s], y_bytes + r_bytes + g_bytes);
+                __syncwarp();
+                if (bytes > 0)
+                    bulk_g2s(ring + static_cast<size_t>(s) * stage_bytes + at,
+                             src + static_cast<long long>(i) * gridDim.x * ld, bytes, &full[s]);
+            }
+            if (++s == stages) s = 0, ++turn;
+        }
+        // the last copies land before the CTA ends, whatever the consumers do
+        for (int k = max(0, i - stages); k < i; ++k)
+            if (k != p.ctl.debug_skip_stage)
+                mbar_wait_warp(&full[k % stages], static_cast<uint32_t>(k / stages) & 1, p.ctl);
+        return;
+    }
+    if (!p.weights_static) pdl_wait();
+    // eight weights a thread, every load before the first conversion: one
+    // trip to L2 (value by value this took 9 us)
+    for (int e = tid * 8; e < p.H; e += consumers * 8) {
+        RawVec<8> rp = raw_zero<8>(), rg = rp, rn = rp;
+        if (kAfter && p.w_post) rp = raw_load<8>(p.w_post, p.w_type, e);
+        if (gate_vec) rg = raw_load<8>(p.gate, p.gate_type, e);
+        if (p.w_next) rn = raw_load<8>(p.w_next, p.w_type, e);
+        float v[8], g[8], n[8];
+        raw_to_f32<8>(rp, p.w_type, v);
+        raw_to_f32<8>(rg, p.gate_type, g);
+        raw_to_f32<8>(rn, p.w_type, n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = p.w_post ? v[j] + p.w_offset : 1.0f;
+            if (gate_vec) v[j] *= act_of(g[j], p.flags);
+            w_post[e + j] = v[j];
+            w_next[e + j] = p.w_next ? n[j] + p.w_offset : 1.0f;
+        }
+    }
+    if (p.weights_static) pdl_wait();
+    pdl_launch_dependents();
+    named_bar_sync(kRingMaxGroups + 1, consumers);  // the weights are there
+
+    const int group = tid / threads, t = tid % threads;
+    const int bar = 1 + group;
+    const float inv_h = 1.0f / static_cast<float>(p.H);
+    int s = group % stages;
+    uint32_t turn = group / stages;
+    for (int i = group; i < count; i += groups) {
+        const long long row = blockIdx.x + static_cast<long long>(i) * gridDim.x;
+        const bool ok = mbar_wait_warp(&full[s], turn & 1, p.ctl, abort_flag);
+        if (!ok) *abort_flag = 1;
+        const uint8_t* st = ring + static_cast<size_t>(s) * stage_bytes;
+        float y[kRingVpt][4], r[kRingVpt][4];
+        bool failed = false;
+        float scale = p.alpha;
+        if constexpr (kAfter) {
+            lds_row<kFull>(st, p.y_type, t, threads, p.H, y);
+            if (!(p.flags & PQ2_NORM_NO_POST)) {
+                float s2 = sum_squares(y);
+                s2 = group_sum(s2, slot[group][0], bar, threads, !ok, failed);
+                scale *= rsqrtf(s2 * inv_h + p.eps);
+            }
+            if (gate_rows) {
+                lds_row<kFull>(st + y_bytes + r_bytes, p.gate_type, t, threads, p.H, r);
+                if (p.flags & (PQ2_GATE_SIGMOID | PQ2_GATE_SILU)) {
+#pragma unroll
+                    for (int k = 0; k < kRingVpt; ++k)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) r[k][j] = act_of(r[k][j], p.flags);
+                }
+#pragma unroll
+                for (int k = 0; k < kRingVpt; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[k][j] *= r[k][j];
+            }
+        }
+        lds_row<kFull>(st + y_bytes, p.r_type, t, threads, p.H, r);
+        // every value of the stage is in registers: back to the producer
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(&empty[s]);
+        s += groups;
+        while (s >= stages) s -= stages, ++turn;
+        if (failed || (!ok && threads == 32)) return;  // uniform over the group
+#pragma unroll
+        for (int k = 0; k < kRingVpt; ++k) {
+            if constexpr (kAfter) {
+                const int e = (t + k * threads) * 4;
+                const float4 w = kFull || e < p.H ? *reinterpret_cast<const float4*>(w_post + e)
+                                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                r[k][0] = fmaf(y[k][0] * scale, w.x, r[k][0]);
+                r[k][1] = fmaf(y[k][1] * scale, w.y, r[k][1]);
+                r[k][2] = fmaf(y[k][2] * scale, w.z, r[k][2]);
+                r[k][3] = fmaf(y[k][3] * scale, w.w, r[k][3]);
+            }
+        }
+        if (kAfter && ok)
+            store_row<kFull>(p.ctl, p.r_out, p.r_type, row * p.ld_ro, p.ro_elems, t, threads, p.H, r);
+        if (p.x) {
+            const float ss = group_sum(sum_squares(r), slot[group][1], bar, threads, !ok, failed);
+            if (failed) return;
+            const float sx = rsqrtf(ss * inv_h + p.eps);
+#pragma unroll
+            for (int k = 0; k < kRingVpt; ++k) {
+                const int e = (t + k * threads) * 4;
+                const float4 w = kFull || e < p.H ? *reinterpret_cast<const float4*>(w_next + e)
+                                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                r[k][0] *= sx * w.x, r[k][1] *= sx * w.y, r[k][2] *= sx * w.z, r[k][3] *= sx * w.w;
+            }
+            store_row<kFull>(p.ctl, p.x, p.x_type, row * p.ld_x, p.x_elems, t, threads, p.H, r);
+        }
+        // slot 1 (or 0) may be written again only once all have read it:
+        // the other sum's barrier separates two rows; with one sum a row,
+        // or none, this one does (and agrees on a failed wait)
+        if (threads > 32 && (!kAfter || !p.x || (p.flags & PQ2_NORM_NO_POST)) &&
+            named_bar_any(bar, threads, !ok))
+            return;
+    }
+}
+
 }  // namespace
 }  // namespace pq2
 
 namespace pq2h {
 
 namespace {
+
+constexpr int kRingMaxH = 8192;
+constexpr int kRingMinRows = 4;  // rows per SM
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -255,6 +523,26 @@ cudaError_t route(const NormParams& p, cudaStream_t st, const DeviceInfo& dev) {
                      rows_on16(p.r_out, p.ld_ro) && rows_on16(p.gate, p.ld_gate) &&
                      rows_on16(p.x, p.ld_x) && rows_on16(p.w_post, 0) && rows_on16(p.w_next, 0);
     const int64_t sms = dev.num_sms;
+    if (vec && H > 512 && H <= kRingMaxH && p.M >= kRingMinRows * sms) {
+        // whole warps of 16 values a thread, as many groups as fit 23 warps
+        const int threads = (H / 4 + pq2::kRingVpt * 32 - 1) / (pq2::kRingVpt * 32) * 32;
+        const int groups = std::min(pq2::kRingMaxGroups, pq2::kRingMaxWarps * 32 / threads);
+        auto bytes = [&](int type) { return H * (type == PQ2_F32 ? 4 : 2); };
+        const int stage = bytes(p.r_type) + (kAfter ? bytes(p.y_type) : 0) +
+                          (kAfter && p.gate && p.ld_gate != 0 ? bytes(p.gate_type) : 0);
+        const int room = dev.max_smem_optin - 4096 - 8 * H;
+        const int stages = std::min(pq2::kRingMaxStages, room / stage);
+        if (stages >= 3) {
+            const bool full = H == threads * pq2::kRingVpt * 4;
+            auto kern = full ? pq2::norm_ring_kernel<kAfter, true> : pq2::norm_ring_kernel<kAfter, false>;
+            static SmemLimit lim[2];
+            const size_t smem = static_cast<size_t>(stages) * stage + 8 * static_cast<size_t>(H);
+            const cudaError_t e = ensure_smem(lim[full], kern, smem);
+            if (e != cudaSuccess) return e;
+            return launch(kern, dim3(static_cast<unsigned>(sms)), dim3(threads * groups + 32), smem, st,
+                          true, p, threads, groups, stages, stage);
+        }
+    }
     if (vec && H <= 512) return go<8, 2, kAfter, true>(p, 256, 8, sms * 4, st);
     if (vec && H <= 8192) {
         const int threads = (H / 16 + 31) / 32 * 32;

@@ -71,6 +71,14 @@ CASES = [
     (6, 5120, "f32", "bf16", "f32", None, None, None, True, False, 0, 0),         # no next norm
     (6, 777, "f32", "bf16", "f32", "f32", None, "silu", False, False, 0, 0),
     (300, 2560, "f32", "f32", "f32", None, None, None, False, False, 0, 0),
+    # many rows: the copy ring (a few rows per SM and more)
+    (1300, 5120, "f32", "bf16", "f32", "bf16", "f16", "sigmoid", True, True, 5120, 0),
+    (2048, 520, "f32", "f32", "bf16", "vector", "bf16", "silu", True, True, 0, 0),
+    (700, 8192, "f32", "bf16", "f32", None, "f16", None, True, True, 0, 0),
+    (700, 8192, "f32", "f32", "f32", "f32", "f16", "silu", True, True, 0, 0),  # too wide for it
+    (901, 1024, "bf16", "f16", None, "f16", None, "sigmoid", True, False, 8, 0),
+    (613, 6144, "f32", "f32", "f32", None, "f16", None, False, True, 0, 0),
+    (777, 2048, "f16", "f32", "f32", "f32", None, None, False, False, 0, 0),
 ]
 
 
@@ -124,7 +132,8 @@ def test_norm_residual(case, in_place):
     (1, 5120, "bf16", "f16", "f32", 0, 0), (4096, 64, "f32", "f16", "f32", 0, 0),
     (65, 1001, "f16", "bf16", "bf16", 0, 0), (5, 6144, "f32", "f16", None, 16, 0),
     (3, 9000, "bf16", "f32", "f32", 0, 0), (40, 300, "f16", "f16", "f16", 0, 1),
-    (500, 8, "f32", "bf16", "f32", 0, 0)])
+    (500, 8, "f32", "bf16", "f32", 0, 0), (1999, 5120, "bf16", "f16", "f32", 0, 0),
+    (3000, 600, "f32", "bf16", "f16", 8, 0)])
 def test_rmsnorm(M, H, tr, tx, tw, extra, offset):
     from gemm_pq2_ternary_gb300 import binding as pq2
     gen = torch.Generator(device=DEV).manual_seed(H)
@@ -184,6 +193,29 @@ def test_same_bits_on_another_stream_and_after_a_producer():
         torch.cuda.synchronize()
         outs.append((o, x))
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+def test_the_copy_ring_reports_a_stage_that_never_comes():
+    # each CTA's producer withholds a row; the rows' groups give up after the
+    # limit and the host reads the timeout; the next call is right
+    from gemm_pq2_ternary_gb300 import binding as pq2
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    for M, H in ((1300, 1024), (2000, 5120)):
+        r = torch.randn((M, H), generator=gen, device=DEV)
+        x = torch.empty((M, H), dtype=torch.float16, device=DEV)
+        try:
+            pq2.pq2_debug_set_wait_limit_ns(20_000_000)
+            pq2.pq2_debug_skip_stage(1)
+            pq2.pq2_norm_residual(r, r, torch.empty_like(r), x=x, eps=EPS)
+            assert pq2.pq2_last_device_error() == pq2.PQ2_ERR_TIMEOUT
+        finally:
+            pq2.pq2_debug_skip_stage(-1)
+            pq2.pq2_debug_set_wait_limit_ns(2_000_000_000)
+        pq2.pq2_rmsnorm(r, None, x, EPS)
+        torch.cuda.synchronize()
+        assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+        want = step.rmsnorm(_np(r), None, EPS)
+        assert np.all(np.abs(_np(x) - want) <= 64 * step.U32 * np.abs(want) + _round(want, "f16"))
 
 
 def test_binding_refuses():
