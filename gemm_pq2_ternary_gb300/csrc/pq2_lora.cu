@@ -29,9 +29,10 @@
 //     (one match over its lanes), and expand adds up the K-split partials of
 //     shrink in a fixed order.  Two launches.
 //   more tokens: a plan kernel sorts the tokens by adapter into tiles of at
-//     most 64 (stable counting sort in shared memory); shrink's last CTA of a
-//     tile adds up the K-split partials and writes v's 16-bit terms; expand
-//     streams y through registers against them.  Three launches.
+//     most 64 (stable counting sort in shared memory); shrink computes a tile
+//     in a cluster of CTAs that split K and join their partials through
+//     distributed shared memory; expand streams y and B through a ring in
+//     shared memory against v's 16-bit terms.  Three launches.
 // Results do not depend on which tokens share a tile: deterministic.
 //
 // Bounds: bytes.  Decode: A and B of the adapters in use; prompts: y in and
@@ -215,7 +216,7 @@ __device__ __forceinline__ void shrink_tile(const pq2h::LoraParams& p, int l, in
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) sum[i][c] = acc[i][c] = 0.0f;
-        constexpr int U = NT == 1 ? 8 : NT == 4 ? 4 : 2;  // blocks in flight
+        constexpr int U = NT == 1 ? 8 : 4;  // blocks in flight
         int chain = 0;
         for (int kb = k0 + ks * 32; kb < k1; kb += kw * 32 * U) {
             uint4 fa[U], fb[U], fx[U][NT];
@@ -530,8 +531,6 @@ struct Plan {
     int* perm;           // [M] tokens, sorted by adapter
     int4* tiles;         // adapter (-1: none), first position, tokens
     int* num_tiles;
-    unsigned* arrived;   // [max_tiles] K splits finished
-    float* part;         // [splits][M][R], by position
     uint16_t* terms;     // [terms][M][rp], by position
     float* f;            // [M] scale and power of two, by position
     int max_tiles;
@@ -551,7 +550,6 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
     for (int i = threadIdx.x; i < warps * bins; i += nthreads) hist[i] = 0;
     pdl_wait();
     pdl_launch_dependents();
-    for (int i = threadIdx.x; i < pl.max_tiles; i += nthreads) pl.arrived[i] = 0u;
     __syncthreads();
     const int per = ((p.M + warps - 1) / warps + 31) / 32 * 32;
     const int m0 = warp * per, m1 = min(m0 + per, p.M);
@@ -624,88 +622,228 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
     }
 }
 
-// CTA (split, tile).  The last split of a tile to finish adds up the
-// partials in split order and writes v's terms.
-template <bool BF>
+// 16-byte asynchronous copy to shared memory; `bytes` 0 writes zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Every CTA's earlier stores to shared memory are visible to the cluster.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t saddr, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+constexpr int kStageK = 64;       // columns of K per pipeline stage: rows of 128 bytes
+// Pipeline stages: about 96 KB a CTA, two CTAs per SM (ranks above 128: 160 KB).
+template <int RPW, int WN>
+constexpr int shrink_stages() {
+    return RPW * WN <= 2 ? 8 : RPW * WN == 4 ? 6 : 4;
+}
+
+// A warp's share of one pipeline stage.  x0, a0: this lane's first rows of x
+// and A (shared-memory addresses); at[blk]: its chunk in either block of 32.
+template <bool BF, int RPW, int NI, int WN>
+__device__ __forceinline__ void shrink_stage(float (&acc)[RPW][WN][4], uint32_t x0, uint32_t a0,
+                                             const uint32_t (&at)[2]) {
+#pragma unroll
+    for (int blk = 0; blk < 2; ++blk) {
+        uint4 a[RPW][2], c[NI];
+#pragma unroll
+        for (int r = 0; r < RPW; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) a[r][h] = lds_v4(a0 + (r * 16 + h * 8) * 128 + at[blk]);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) c[i] = lds_v4(x0 + i * 8 * 128 + at[blk]);
+#pragma unroll
+        for (int r = 0; r < RPW; ++r)
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                mma16816<BF>(acc[r][i], a[r][0].x, a[r][1].x, a[r][0].y, a[r][1].y, c[i].x, c[i].y);
+#pragma unroll
+        for (int r = 0; r < RPW; ++r)
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                mma16816<BF>(acc[r][i], a[r][0].z, a[r][1].z, a[r][0].w, a[r][1].w, c[i].z, c[i].w);
+    }
+}
+
+// A cluster of CTAs computes one tile: v[64 tokens][R] over its share of K
+// each.  x and A come through a pipeline of asynchronous copies; a row is 8
+// chunks of 16 bytes, the halves swapped in odd rows, so that the 8 lanes of a
+// 16-byte read (two rows, four chunks) touch all banks once.  A warp owns RPW
+// rank tiles of 16 and WN groups of 8 tokens.  The partials meet in
+// distributed shared memory: each CTA adds up its share of the tokens, CTA by
+// CTA in order, and writes their 16-bit terms.
+template <bool BF, int RPW, int WN>
 __global__ void __launch_bounds__(kShrinkWarps * 32)
-    lora_shrink_tiles(pq2h::LoraParams p, Plan pl, int k_split) {
-    constexpr int NT = kTile / 8;
-    __shared__ float red[kShrinkWarps * 16 * NT * 8];
+    lora_shrink_tiles(pq2h::LoraParams p, Plan pl, int splits, int k_split) {
+    constexpr int kShrinkStages = shrink_stages<RPW, WN>();
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int tok[kTile];
-    __shared__ bool s_last;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
     pdl_wait();
     pdl_launch_dependents();
-    if (static_cast<int>(blockIdx.y) >= *pl.num_tiles) return;
-    const int4 tile = pl.tiles[blockIdx.y];
-    if (tile.x < 0) return;
+    const int index = blockIdx.x / splits;
+    const int4 tile = pl.tiles[index];    // there for every index; a tile if below num_tiles
+    if (index >= *pl.num_tiles) return;   // the whole cluster
     const int l = tile.x, first = tile.y, count = tile.z;
-    const int rank = rank_of(p, l);
+    const int rank = l >= 0 ? rank_of(p, l) : 0;
     if (rank == 0) return;
-    if (threadIdx.x < count) tok[threadIdx.x] = pl.perm[first + threadIdx.x];
+    if (tid < count) tok[tid] = pl.perm[first + tid];
     __syncthreads();
-    const int splits = gridDim.x;
-    const int k0 = blockIdx.x * k_split, k1 = min(k0 + k_split, p.K);
-    float* dst = pl.part + (static_cast<size_t>(blockIdx.x) * p.M + first) * p.R;
-    shrink_tile<BF, NT>(p, l, rank, tok, count, k0, k1, red,
-                        [&](int j, int r, float v) { dst[static_cast<size_t>(j) * p.R + r] = v; });
-    __syncthreads();
-    if (threadIdx.x == 0)
-        s_last = atom_add_acq_rel_gpu(&pl.arrived[blockIdx.y], 1u) + 1u == static_cast<unsigned>(splits);
-    __syncthreads();
-    if (!s_last) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float scale = p.scales ? p.scales[l] : 1.0f;
-    const size_t step = static_cast<size_t>(p.M) * p.R;
-    const size_t term_size = static_cast<size_t>(p.M) * pl.rp;
-    const int blocks = (rank + 31) / 32;
-    // each warp's tokens (warp, warp + 8, ...), 4 at a time, 4 ranks a lane
-    for (int j0 = warp; j0 < count; j0 += kShrinkWarps * 4) {
-        float top[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int pass = 0; pass < 2; ++pass) {
-            float up[4];
-            if (pass == 1) {
+    const int part = splits > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int k0 = part * k_split, k1 = min(k0 + k_split, p.K);
+
+    // copies: thread -> chunk tid % 8 of rows tid / 8 + 32 i
+    // rows of A per stage: whole shares of a warp (16 RPW)
+    const int r16 = (p.R + 16 * RPW - 1) / (16 * RPW) * (16 * RPW);
+    const int stage_bytes = (kTile + r16) * 128;
+    const int chunk = tid & 7, row0 = tid >> 3;
+    const uint32_t base = smem_u32(smem);
+    const uint32_t dst0 = row0 * 128 + ((chunk ^ ((row0 & 1) * 4)) * 16);
+    const uint16_t* xs[2];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    up[q] = pow2_below<BF>(warp_max(top[q]));
-                    const int j = j0 + q * kShrinkWarps;
-                    if (lane == 0 && j < count) pl.f[first + j] = scale * up[q];
-                }
-            }
-            for (int i0 = 0; i0 < blocks; i0 += 4) {
-                float v[4][4];
+    for (int i = 0; i < 2; ++i) {
+        const int j = row0 + 32 * i;
+        xs[i] = j < count ? p.x + static_cast<size_t>(tok[j]) * p.ld_x + chunk * 8 : nullptr;
+    }
+    const uint16_t* as = p.A + (static_cast<size_t>(l) * p.R + row0) * p.K + chunk * 8;
+    const int a_rows = (rank + 16 * RPW - 1) / (16 * RPW) * (16 * RPW);
+    const size_t a_step = static_cast<size_t>(32) * p.K;
+    auto issue = [&](int kb, int slot) {
+        const uint32_t st = base + slot * stage_bytes + dst0;
+        const int k = k0 + kb;
+        const uint32_t in = k + chunk * 8 < k1 ? 16 : 0;  // else zeros (the address is not read)
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+        for (int i = 0; i < 2; ++i)
+            if (xs[i]) cp_async16(st + i * 32 * 128, xs[i] + (in ? k : 0), in);
+        const uint16_t* a = as + (in ? k : 0);
+        for (int r = row0; r < a_rows; r += 32, a += a_step)
+            cp_async16(st + (kTile + r - row0) * 128, r < rank ? a : p.A, r < rank ? in : 0);
+    };
+    // this warp's rank tiles and token groups
+    constexpr int kTokenWarps = kTile / 8 / WN;
+    const int rt0 = warp / kTokenWarps * RPW, n0 = warp % kTokenWarps * WN;
+    const bool works = rt0 * 16 < rank && n0 * 8 < count;
+    const uint32_t at[2] = {static_cast<uint32_t>((t ^ ((g & 1) * 4)) * 16),
+                            static_cast<uint32_t>(((4 + t) ^ ((g & 1) * 4)) * 16)};
+    float sum[RPW][WN][4], acc[RPW][WN][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[q][i] = 0.0f;
-                for (int s = 0; s < splits; ++s)
+    for (int r = 0; r < RPW; ++r)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+        for (int i = 0; i < WN; ++i)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int j = j0 + q * kShrinkWarps, r = (i0 + i) * 32 + lane;
-                            if (j < count && r < rank)
-                                v[q][i] += __ldcg(pl.part + s * step +
-                                                  static_cast<size_t>(first + j) * p.R + r);
-                        }
+            for (int c = 0; c < 4; ++c) sum[r][i][c] = acc[r][i][c] = 0.0f;
+    const int kspan = max(k1 - k0, 0);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+    for (int s = 0; s < kShrinkStages - 1; ++s) {
+        if (s * kStageK < kspan) issue(s * kStageK, s);
+        cp_async_commit();
+    }
+    for (int kb = 0, step = 0; kb < kspan; kb += kStageK, ++step) {
+        cp_async_wait<kShrinkStages - 2>();
+        __syncthreads();
+        const int ahead = kb + (kShrinkStages - 1) * kStageK;
+        if (ahead < kspan) issue(ahead, (step + kShrinkStages - 1) % kShrinkStages);
+        cp_async_commit();
+        if (!works) continue;
+        const uint32_t st = base + (step % kShrinkStages) * stage_bytes;
+        const uint32_t x0 = st + (n0 * 8 + g) * 128, a0 = st + (kTile + rt0 * 16 + g) * 128;
+        // one group of tokens, or all of this warp's (columns past the
+        // tile's last token hold anything and are not stored)
+        if (count - n0 * 8 > 8)
+            shrink_stage<BF, RPW, WN, WN>(acc, x0, a0, at);
+        else
+            shrink_stage<BF, RPW, 1, WN>(acc, x0, a0, at);
+        if ((step + 1) % (kFlush / 2) == 0) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int j = j0 + q * kShrinkWarps, blk = i0 + i;
-                        if (pass == 0) {
-                            top[q] = fmaxf(top[q], fabsf(v[q][i]));
-                        } else if (j < count && blk < blocks) {
-                            uint16_t w[3];
-                            split_terms<BF>(v[q][i] / up[q], w);
+            for (int r = 0; r < RPW; ++r)
 #pragma unroll
-                            for (int k = 0; k < terms<BF>(); ++k)
-                                pl.terms[k * term_size + static_cast<size_t>(first + j) * pl.rp +
-                                         blk * 32 + lane] = w[k];
-                        }
+                for (int i = 0; i < WN; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        sum[r][i][c] += acc[r][i][c];
+                        acc[r][i][c] = 0.0f;
                     }
-            }
         }
     }
+    cp_async_wait<0>();
+    __syncthreads();
+    // partials [token][r16 + 4] in the pipeline's memory
+    float* red = reinterpret_cast<float*>(smem);
+    const int pitch = r16 + 4;
+    if (works) {
+#pragma unroll
+        for (int r = 0; r < RPW; ++r)
+#pragma unroll
+            for (int i = 0; i < WN; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int rr = (rt0 + r) * 16 + (c >> 1) * 8 + g;
+                    const int j = (n0 + i) * 8 + 2 * t + (c & 1);
+                    if (rr < rank && j < count) red[j * pitch + rr] = sum[r][i][c] + acc[r][i][c];
+                }
+    }
+    if (splits > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    const float scale = p.scales ? p.scales[l] : 1.0f;
+    const size_t term_size = static_cast<size_t>(p.M) * pl.rp;
+    const int blocks = (rank + 31) / 32;
+    for (int j = part + splits * warp; j < count; j += splits * kShrinkWarps) {
+        float v[8], top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 32 + lane;
+            v[i] = 0.0f;
+            if (i >= blocks || r >= rank) continue;
+            if (splits > 1) {
+                float w[8];
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    w[s] = s < splits ? ld_cluster_f32(smem_u32(red + j * pitch + r), s) : 0.0f;
+#pragma unroll
+                for (int s = 0; s < 8; ++s) v[i] += w[s];
+            } else {
+                v[i] = red[j * pitch + r];
+            }
+            top = fmaxf(top, fabsf(v[i]));
+        }
+        const float up = pow2_below<BF>(warp_max(top)), down = 1.0f / up;
+        if (lane == 0) pl.f[first + j] = scale * up;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i >= blocks) break;
+            uint16_t w[3];
+            split_terms<BF>(v[i] * down, w);
+#pragma unroll
+            for (int q = 0; q < terms<BF>(); ++q)
+                pl.terms[q * term_size + static_cast<size_t>(first + j) * pl.rp + i * 32 + lane] = w[q];
+        }
+    }
+    if (splits > 1) cluster_sync();  // nobody leaves while its partials are read
 }
 
 // CTA (rounds x 128 outputs, tile): v's terms in shared memory, then per 32
@@ -763,6 +901,257 @@ __global__ void __launch_bounds__(kExpandWarps * 32, 3)
     }
 }
 
+// The same over a ring in shared memory.  One CTA per SM takes a contiguous
+// range of the items (tile, kNB outputs), so that v's terms rarely change;
+// producer warps keep the next items' y and B on their way while the consumer
+// warps multiply, add and store.  y comes by asynchronous copies of kPiece
+// bytes a thread (a warp per token row; bulk copies of 512-byte rows topped
+// out at one per 46 ns and SM, half the rate needed), B by one bulk copy: kNB
+// rows of B are contiguous.  A consumer warp owns 32 outputs and kNI groups
+// of 8 tokens.  Token rows of y are 16 bytes longer in shared memory, so that
+// the 4 tokens of an access lie in different banks.
+constexpr int kRingWarps = 16;      // consumers
+constexpr int kRingLoaders = 4;     // producer warps
+constexpr int kRingMaxStages = 8;
+
+// Asynchronous copy of 4 or 16 bytes to shared memory.
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// One arrival on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
+template <bool BF, int YT, int kNB, int kPiece>
+__global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
+    lora_expand_ring(pq2h::LoraParams p, Plan pl, int stages, int stage_bytes, int term_bytes) {
+    constexpr int kUnit = YT == PQ2_F32 ? 4 : 2;
+    constexpr int kYPitch = kNB * kUnit + 16;
+    constexpr int kNWarps = kNB / 32;                    // warps side by side along n
+    constexpr int kNI = kTile / 8 / (kRingWarps / kNWarps);
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t full[kRingMaxStages], empty[kRingMaxStages];
+    __shared__ int tok[kTile];
+    __shared__ float f[kTile];
+    __shared__ int abort_word;
+    volatile int* abort_flag = &abort_word;
+    uint16_t* sv = reinterpret_cast<uint16_t*>(smem);
+    uint8_t* ring = smem + term_bytes;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&full[s], kRingLoaders * 32 + 1);
+            mbar_init(&empty[s], kRingWarps);
+        }
+        abort_word = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const int nblocks = (p.N + kNB - 1) / kNB;
+    const bool in_place = p.y_in == p.y_out && p.ld_in == p.ld_out;
+    // the plan is complete before shrink lets this kernel start, as are y and
+    // B; v's terms are not
+    const long long total = static_cast<long long>(__ldcg(pl.num_tiles)) * nblocks;
+    const long long it0 = total * blockIdx.x / gridDim.x, it1 = total * (blockIdx.x + 1) / gridDim.x;
+    int index = static_cast<int>(it0 / nblocks), nb = static_cast<int>(it0 - static_cast<long long>(index) * nblocks);
+    int left = static_cast<int>(it1 - it0);
+
+    if (warp >= kRingWarps) {
+        constexpr int kPieces = kNB * kUnit / kPiece;            // of a token row
+        constexpr int kRows = kRingLoaders * 32 / kPieces;       // rows per round of the loaders
+        static_assert(kRows >= 1, "a row is at most one round");
+        const int pt = tid - kRingWarps * 32;
+        const int row0 = pt / kPieces, piece = pt % kPieces;     // row0 is a warp's, or two
+        const uint8_t* yb = static_cast<const uint8_t*>(p.y_in) + piece * kPiece;
+        const long long ld = p.ld_in * kUnit;
+        int cached = -1, l = -1, rank = 0, count = 0;
+        int tk[2] = {0, 0};        // the tile's tokens: lane, lane + 32
+        int issued = 0, s = 0;
+        uint32_t turn = 0;
+        for (; left > 0; --left) {
+            if (index != cached) {
+                const int4 tile = __ldcg(pl.tiles + index);
+                cached = index, l = tile.x, count = tile.z;
+                rank = l >= 0 ? rank_of(p, l) : 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (lane + 32 * h < count) tk[h] = __ldcg(pl.perm + tile.y + lane + 32 * h);
+            }
+            const int n0 = nb * kNB, n = min(kNB, p.N - n0);
+            if (++nb == nblocks) nb = 0, ++index;
+            if (rank == 0 && in_place) continue;   // nothing to read or write
+            if (turn > 0 && !mbar_wait_warp(&empty[s], (turn - 1) & 1, p.ctl, abort_flag)) break;
+            if (issued != p.ctl.debug_skip_stage) {  // else withheld (timeout test)
+                uint8_t* st = ring + static_cast<size_t>(s) * stage_bytes;
+                if (pt == 0) {
+                    const uint32_t brow = rank > 0 ? n * p.R * 2 : 0;
+                    mbar_arrive_expect_tx(&full[s], brow);
+                    if (rank > 0)
+                        bulk_g2s(st + kTile * kYPitch,
+                                 p.B + (static_cast<size_t>(l) * p.N + n0) * p.R, brow, &full[s]);
+                }
+                __syncwarp();
+                const uint8_t* src = yb + static_cast<size_t>(n0) * kUnit;
+                uint32_t dst = smem_u32(st) + row0 * kYPitch + piece * kPiece;
+                const bool in = piece * kPiece < n * kUnit;
+#pragma unroll 8
+                for (int j = row0; j - row0 < count; j += kRows, dst += kRows * kYPitch) {
+                    const int lo = __shfl_sync(0xffffffffu, tk[0], j & 31);
+                    const int hi = __shfl_sync(0xffffffffu, tk[1], j & 31);
+                    const int tj = j & 32 ? hi : lo;
+                    if (in && j < count) cp_async<kPiece>(dst, src + tj * ld);
+                }
+                cp_async_arrive(&full[s]);
+            }
+            ++issued;
+            if (++s == stages) s = 0, ++turn;
+        }
+        // the last copies land before the CTA ends, whatever the consumers do
+        for (int k = max(0, issued - stages); k < issued; ++k)
+            if (k != p.ctl.debug_skip_stage)
+                mbar_wait_warp(&full[k % stages], static_cast<uint32_t>(k / stages) & 1, p.ctl);
+        cp_async_wait<0>();
+        pdl_wait();
+        return;
+    }
+
+    const int g = lane >> 2, t = lane & 3;
+    const int wn = (warp % kNWarps) * 32 + 4 * g;   // this lane's outputs within the item
+    const int j0 = (warp / kNWarps) * kNI * 8;      // this warp's first token
+    int cached = -1, rank = 0, count = 0, blocks = 0, pitch = 0, term_size = 0;
+    const uint32_t b_step = p.R * 2;
+    uint32_t v_base = 0, i_step = 0, q_step = 0;
+    size_t out[kNI][2];
+    float fs[kNI][2];
+    int s = 0;
+    uint32_t turn = 0;
+    bool ok = true;
+    pdl_wait();
+    pdl_launch_dependents();
+    for (; left > 0; --left) {
+        if (index != cached) {
+            // every warp is done with the old tile; a failed wait reaches all
+            if (named_bar_any(1, kRingWarps * 32, !ok)) return;
+            const int4 tile = __ldcg(pl.tiles + index);
+            cached = index, count = tile.z;
+            rank = tile.x >= 0 ? rank_of(p, tile.x) : 0;
+            blocks = (rank + 31) / 32;
+            pitch = term_pitch(blocks), term_size = kTile * pitch;
+            if (tid < count) {
+                tok[tid] = __ldcg(pl.perm + tile.y + tid);
+                f[tid] = rank > 0 ? __ldcg(pl.f + tile.y + tid) : 0.0f;
+            }
+            const int per_row = blocks * 4;  // 16-byte pieces
+            for (int i = tid; i < terms<BF>() * kTile * per_row; i += kRingWarps * 32) {
+                const int c = i % per_row, j = (i / per_row) % kTile, q = i / (per_row * kTile);
+                *reinterpret_cast<uint4*>(sv + q * term_size + j * pitch + c * 8) =
+                    j < count ? load16_cg(pl.terms + (static_cast<size_t>(q) * p.M + tile.y + j) * pl.rp + c * 8)
+                              : zero4();
+            }
+            named_bar_sync(2, kRingWarps * 32);
+#pragma unroll
+            for (int i = 0; i < kNI; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int j = j0 + i * 8 + 2 * t + h;
+                    out[i][h] = j < count ? static_cast<size_t>(tok[j]) * p.ld_out : 0;
+                    fs[i][h] = j < count ? f[j] : 0.0f;
+                }
+            // shared-memory addresses of this lane's terms
+            v_base = smem_u32(sv + (j0 + g) * pitch + 8 * t);
+            i_step = 8 * pitch * 2, q_step = term_size * 2;
+        }
+        const int n = nb * kNB + wn;
+        if (++nb == nblocks) nb = 0, ++index;
+        if (rank == 0 && in_place) continue;
+        if (ok) ok = mbar_wait_warp(&full[s], turn & 1, p.ctl, abort_flag);
+        if (!ok) {
+            *abort_flag = 1;
+            continue;   // to the next tile's barrier
+        }
+        const uint8_t* st = ring + static_cast<size_t>(s) * stage_bytes;
+        const uint8_t* sy = st;
+        const uint16_t* sb = reinterpret_cast<const uint16_t*>(st + kTile * kYPitch);
+        float acc[2][kNI][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < kNI; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[h][i][c] = 0.0f;
+        if (j0 < count) {
+            // every group of tokens, also one past the tile's last (its
+            // columns are not stored): no branch between the instructions
+            uint32_t bp = smem_u32(sb + wn * p.R + 8 * t);
+            uint32_t vp = v_base;
+            for (int blk = 0; blk < blocks; ++blk, bp += 64, vp += 64) {
+                uint4 b[4], c[terms<BF>()][kNI];
+                const bool in = blk * 32 + 8 * t < rank;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) b[i] = in ? lds_v4(bp + i * b_step) : zero4();
+#pragma unroll
+                for (int q = 0; q < terms<BF>(); ++q)
+#pragma unroll
+                    for (int i = 0; i < kNI; ++i) c[q][i] = lds_v4(vp + q * q_step + i * i_step);
+                if (blk * 32 + 32 > rank) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) b[i] = keep_first(b[i], rank - blk * 32 - 8 * t);
+                }
+#pragma unroll
+                for (int q = 0; q < terms<BF>(); ++q) {
+#pragma unroll
+                    for (int i = 0; i < kNI; ++i) {
+                        mma16816<BF>(acc[0][i], b[0].x, b[1].x, b[0].y, b[1].y, c[q][i].x, c[q][i].y);
+                        mma16816<BF>(acc[1][i], b[2].x, b[3].x, b[2].y, b[3].y, c[q][i].x, c[q][i].y);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kNI; ++i) {
+                        mma16816<BF>(acc[0][i], b[0].z, b[1].z, b[0].w, b[1].w, c[q][i].z, c[q][i].w);
+                        mma16816<BF>(acc[1][i], b[2].z, b[3].z, b[2].w, b[3].w, c[q][i].z, c[q][i].w);
+                    }
+                }
+            }
+        }
+        float4 y[kNI][2];
+#pragma unroll
+        for (int i = 0; i < kNI; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t* a = sy + (j0 + i * 8 + 2 * t + h) * kYPitch + wn * kUnit;
+                if constexpr (YT == PQ2_F32) {
+                    y[i][h] = *reinterpret_cast<const float4*>(a);
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2*>(a);
+                    y[i][h] = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                                          __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+                }
+            }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);   // the stage is in registers
+        if (++s == stages) s = 0, ++turn;
+        if (n < p.N) {
+#pragma unroll
+            for (int i = 0; i < kNI; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (j0 + i * 8 + 2 * t + h >= count) continue;
+                    float4 o = y[i][h];
+                    o.x = fmaf(fs[i][h], acc[0][i][h], o.x);
+                    o.y = fmaf(fs[i][h], acc[0][i][2 + h], o.y);
+                    o.z = fmaf(fs[i][h], acc[1][i][h], o.z);
+                    o.w = fmaf(fs[i][h], acc[1][i][2 + h], o.w);
+                    y_store<YT>(p, out[i][h] + n, p.N - n, kPiece == 16, o);
+                }
+        }
+    }
+}
+
 }  // namespace
 }  // namespace pq2
 
@@ -782,25 +1171,36 @@ size_t pad(size_t b) { return (b + 255) & ~size_t(255); }
 
 struct Layout {
     int splits, k_split, max_tiles, rp;
-    size_t part, terms, f, perm, tiles, num_tiles, arrived, bytes;
+    size_t part, terms, f, perm, tiles, num_tiles, bytes;
 };
 
-// K splits: two CTAs per SM over the groups or tiles that may appear, at
-// least 16 KB of A each.
 Layout layout(int64_t M, int64_t K, int64_t L, int64_t R) {
     Layout y = {};
     const bool few = M <= kFewTokens;
-    const int64_t work = few ? std::min(M, L) : (M + kTile - 1) / kTile + std::min(L, M / 2);
-    int64_t s = (2 * kSms + work - 1) / work;
-    s = std::min(s, std::max<int64_t>(1, K * R * 2 / 16384));
-    s = std::min<int64_t>(s, kMaxSplits);
+    int64_t s;
+    if (few) {
+        // K splits: two CTAs per SM over the groups that may appear, at
+        // least 16 KB of A each
+        const int64_t groups = std::min(M, L);
+        s = (2 * kSms + groups - 1) / groups;
+        s = std::min(s, std::max<int64_t>(1, K * R * 2 / 16384));
+        s = std::min<int64_t>(s, kMaxSplits);
+    } else {
+        // a cluster per tile: one and a half CTAs per SM over the tiles that
+        // are likely, at least 256 columns each, no more than 8 (the portable
+        // cluster size)
+        const int64_t tiles = (M + kTile - 1) / kTile + std::min(L, M / 2);
+        s = 1;
+        while (s < 8 && s * tiles * 2 < 3 * kSms && K / (2 * s) >= 256) s *= 2;
+    }
     y.k_split = static_cast<int>(((K + s - 1) / s + 127) / 128 * 128);
-    y.splits = static_cast<int>((K + y.k_split - 1) / y.k_split);
+    y.splits = few ? static_cast<int>((K + y.k_split - 1) / y.k_split) : static_cast<int>(s);
     y.rp = static_cast<int>((R + 31) / 32 * 32);
     size_t o = 0;
-    y.part = o;
-    o += pad(static_cast<size_t>(y.splits) * M * R * 4);
-    if (!few) {
+    if (few) {
+        y.part = o;
+        o += pad(static_cast<size_t>(y.splits) * M * R * 4);
+    } else {
         y.max_tiles = static_cast<int>((M + kTile - 1) / kTile + std::min(L + 1, M));
         y.terms = o;
         o += pad(static_cast<size_t>(3) * M * y.rp * 2);
@@ -812,8 +1212,6 @@ Layout layout(int64_t M, int64_t K, int64_t L, int64_t R) {
         o += pad(static_cast<size_t>(y.max_tiles) * 16);
         y.num_tiles = o;
         o += 256;
-        y.arrived = o;
-        o += pad(static_cast<size_t>(y.max_tiles) * 4);
     }
     y.bytes = o;
     return y;
@@ -837,18 +1235,78 @@ cudaError_t run_few(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec
                   dim3(cols), smem, st, true, p, part, lay.splits, vec);
 }
 
+template <bool BF, int RPW, int WN>
+cudaError_t run_shrink(const LoraParams& p, const pq2::Plan& pl, const Layout& lay, cudaStream_t st) {
+    auto kern = pq2::lora_shrink_tiles<BF, RPW, WN>;
+    static SmemLimit lim;
+    const size_t r16 = static_cast<size_t>((p.R + 16 * RPW - 1) / (16 * RPW) * (16 * RPW));
+    const size_t smem = std::max((kTile + r16) * 128 * pq2::shrink_stages<RPW, WN>(), kTile * (r16 + 4) * 4);
+    const cudaError_t e = ensure_smem(lim, kern, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(lay.splits * lay.max_tiles));
+    cfg.blockDim = dim3(pq2::kShrinkWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(lay.splits);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = lay.splits > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, p, pl, lay.splits, lay.k_split);
+}
+
+// The ring's shared memory: v's terms, then as many stages as fit (0: fewer
+// than two).
+template <bool BF, int YT, int kNB>
+int ring_stages(const LoraParams& p, const DeviceInfo& dev, int* stage_bytes, int* term_bytes) {
+    constexpr int kUnit = YT == PQ2_F32 ? 4 : 2;
+    *term_bytes = pq2::terms<BF>() * kTile * pq2::term_pitch((p.R + 31) / 32) * 2;
+    *stage_bytes = kTile * (kNB * kUnit + 16) + kNB * p.R * 2;
+    const int stages = (dev.max_smem_optin - 2048 - *term_bytes) / *stage_bytes;
+    return stages < 2 ? 0 : std::min(stages, pq2::kRingMaxStages);
+}
+
+template <bool BF, int YT, int kNB, int kPiece>
+cudaError_t run_ring(const LoraParams& p, const pq2::Plan& pl, int stages, int stage_bytes,
+                     int term_bytes, cudaStream_t st, const DeviceInfo& dev) {
+    auto kern = pq2::lora_expand_ring<BF, YT, kNB, kPiece>;
+    static SmemLimit lim;
+    const size_t smem = static_cast<size_t>(term_bytes) + static_cast<size_t>(stages) * stage_bytes;
+    const cudaError_t e = ensure_smem(lim, kern, smem);
+    if (e != cudaSuccess) return e;
+    return launch(kern, dim3(dev.num_sms), dim3((pq2::kRingWarps + pq2::kRingLoaders) * 32), smem, st,
+                  true, p, pl, stages, stage_bytes, term_bytes);
+}
+
+// 128 outputs an item where three stages fit beside v's terms (they take two
+// thirds of the barriers and shuffles of 64), else 64.
+template <bool BF, int YT, int kPiece>
+cudaError_t run_ring(const LoraParams& p, const pq2::Plan& pl, cudaStream_t st, const DeviceInfo& dev) {
+    int sb, tb;
+    int stages = ring_stages<BF, YT, 128>(p, dev, &sb, &tb);
+    if (stages >= 3) return run_ring<BF, YT, 128, kPiece>(p, pl, stages, sb, tb, st, dev);
+    stages = ring_stages<BF, YT, 64>(p, dev, &sb, &tb);
+    return run_ring<BF, YT, 64, kPiece>(p, pl, stages, sb, tb, st, dev);
+}
+
+SmemLimit g_plan_smem;  // one for the kernel: run() has several instantiations
+
 template <bool BF, int YT>
-cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cudaStream_t st) {
+cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cudaStream_t st,
+                const DeviceInfo& dev) {
     if (p.M <= 8) return run_few<BF, 1, YT>(p, lay, ws, vec, st);
     if (p.M <= kFewTokens) return run_few<BF, 4, YT>(p, lay, ws, vec, st);
     pq2::Plan pl = {};
-    pl.part = reinterpret_cast<float*>(ws + lay.part);
     pl.terms = reinterpret_cast<uint16_t*>(ws + lay.terms);
     pl.f = reinterpret_cast<float*>(ws + lay.f);
     pl.perm = reinterpret_cast<int*>(ws + lay.perm);
     pl.tiles = reinterpret_cast<int4*>(ws + lay.tiles);
     pl.num_tiles = reinterpret_cast<int*>(ws + lay.num_tiles);
-    pl.arrived = reinterpret_cast<unsigned*>(ws + lay.arrived);
     pl.max_tiles = lay.max_tiles;
     pl.rp = lay.rp;
     // as many warps as have tokens and fit their histograms in 200 KB
@@ -857,23 +1315,37 @@ cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cu
     while (warps > 1 && (warps / 2 * 32 >= p.M || static_cast<size_t>(warps + 2) * bins * 4 > 200 * 1024))
         warps /= 2;
     const size_t plan_smem = static_cast<size_t>(warps + 2) * bins * 4;
-    static SmemLimit plan_lim;
-    cudaError_t e = ensure_smem(plan_lim, pq2::lora_plan_kernel, plan_smem);
+    cudaError_t e = ensure_smem(g_plan_smem, pq2::lora_plan_kernel, plan_smem);
     if (e != cudaSuccess) return e;
     e = launch(pq2::lora_plan_kernel, dim3(1), dim3(warps * 32), plan_smem, st, true, p, pl, warps);
     if (e != cudaSuccess) return e;
-    e = launch(pq2::lora_shrink_tiles<BF>, dim3(lay.splits, lay.max_tiles),
-               dim3(pq2::kShrinkWarps * 32), 0, st, true, p, pl, lay.k_split);
+    // 8 warps over the rank tiles, the rest over the token groups
+    const int rt = (p.R + 15) / 16;
+    e = rt == 1 ? run_shrink<BF, 1, 1>(p, pl, lay, st)
+        : rt == 2 ? run_shrink<BF, 1, 2>(p, pl, lay, st)
+        : rt <= 4 ? run_shrink<BF, 1, 4>(p, pl, lay, st)
+        : rt <= 8 ? run_shrink<BF, 1, 8>(p, pl, lay, st)
+                  : run_shrink<BF, 2, 8>(p, pl, lay, st);
     if (e != cudaSuccess) return e;
-    static SmemLimit lim;
-    const size_t smem = static_cast<size_t>(pq2::terms<BF>()) * kTile *
-                        pq2::term_pitch((p.R + 31) / 32) * 2;
-    e = ensure_smem(lim, pq2::lora_expand_tiles<BF, YT>, smem);
-    if (e != cudaSuccess) return e;
-    const int rounds = p.M <= 512 ? 1 : 4;
-    const int cols = pq2::kExpandWarps * 32 * rounds;
-    return launch(pq2::lora_expand_tiles<BF, YT>, dim3((p.N + cols - 1) / cols, lay.max_tiles),
-                  dim3(pq2::kExpandWarps * 32), smem, st, true, p, pl, rounds, vec);
+    // the ring, by 16-byte pieces of y where its rows allow, else (fp32) by
+    // values; bf16 rows off their 16 bytes go by plain loads
+    constexpr int kPer16 = YT == PQ2_F32 ? 4 : 8;
+    if (p.N % kPer16 == 0 && p.ld_in % kPer16 == 0 && p.ld_out % 4 == 0 && vec &&
+        reinterpret_cast<uintptr_t>(p.y_in) % 16 == 0)
+        return run_ring<BF, YT, 16>(p, pl, st, dev);
+    if constexpr (YT == PQ2_F32) {
+        return run_ring<BF, YT, 4>(p, pl, st, dev);
+    } else {
+        static SmemLimit lim;
+        const size_t smem = static_cast<size_t>(pq2::terms<BF>()) * kTile *
+                            pq2::term_pitch((p.R + 31) / 32) * 2;
+        e = ensure_smem(lim, pq2::lora_expand_tiles<BF, YT>, smem);
+        if (e != cudaSuccess) return e;
+        const int rounds = p.M <= 512 ? 1 : 4;
+        const int cols = pq2::kExpandWarps * 32 * rounds;
+        return launch(pq2::lora_expand_tiles<BF, YT>, dim3((p.N + cols - 1) / cols, lay.max_tiles),
+                      dim3(pq2::kExpandWarps * 32), smem, st, true, p, pl, rounds, vec);
+    }
 }
 
 }  // namespace
@@ -885,7 +1357,6 @@ size_t lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t 
 
 cudaError_t launch_lora(const LoraParams& p, void* workspace, cudaStream_t st,
                         const DeviceInfo& dev) {
-    (void)dev;
     const Layout lay = layout(p.M, p.K, p.L, p.R);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     // 4-wide accesses to y: every row starts on their boundary
@@ -894,10 +1365,10 @@ cudaError_t launch_lora(const LoraParams& p, void* workspace, cudaStream_t st,
                      reinterpret_cast<uintptr_t>(p.y_in) % unit == 0 &&
                      reinterpret_cast<uintptr_t>(p.y_out) % unit == 0;
     if (p.bf16)
-        return p.y_type == PQ2_F32 ? run<true, PQ2_F32>(p, lay, ws, vec, st)
-                                   : run<true, PQ2_BF16>(p, lay, ws, vec, st);
-    return p.y_type == PQ2_F32 ? run<false, PQ2_F32>(p, lay, ws, vec, st)
-                               : run<false, PQ2_BF16>(p, lay, ws, vec, st);
+        return p.y_type == PQ2_F32 ? run<true, PQ2_F32>(p, lay, ws, vec, st, dev)
+                                   : run<true, PQ2_BF16>(p, lay, ws, vec, st, dev);
+    return p.y_type == PQ2_F32 ? run<false, PQ2_F32>(p, lay, ws, vec, st, dev)
+                               : run<false, PQ2_BF16>(p, lay, ws, vec, st, dev);
 }
 
 }  // namespace pq2h

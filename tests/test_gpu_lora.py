@@ -112,6 +112,15 @@ SHAPES = [
     (700, 256, 515, 8, 2, "bf16", "f32", dict(ids="runs", offset=3)),
     (1500, 512, 384, 40, 700, "f16", "f32", {}),
     (2100, 128, 130, 16, 5, "f16", "f32", dict(ids="runs")),
+    # whole 16-byte rows of y and more than 32 tokens: the copy ring
+    (40, 5120, 5120, 32, 30, "bf16", "f32", {}),
+    (200, 2048, 1000, 256, 4, "bf16", "bf16", {}),
+    (97, 640, 2056, 136, 3, "f16", "bf16", dict(ld_y=2064)),
+    (97, 640, 2052, 136, 3, "f16", "f32", dict(ld_y=2060)),
+    (300, 72, 4, 8, 2, "f16", "f32", {}),
+    (1025, 1000, 1028, 48, 2, "bf16", "f32", dict(ranks=False, ids="runs")),
+    (129, 6144, 700, 64, 1, "f16", "f32", dict(scales=False)),
+    (4000, 256, 264, 128, 64, "f16", "bf16", {}),
 ]
 
 
@@ -124,10 +133,11 @@ def test_lora_add(shape):
     _check(pq2, p, p["out"])
 
 
+@pytest.mark.parametrize("N", [301, 516])
 @pytest.mark.parametrize("M", [1, 20, 64, 400])
-def test_in_place_equals_out_of_place(M):
+def test_in_place_equals_out_of_place(M, N):
     from gemm_pq2_ternary_gb300 import binding as pq2
-    p = _problem(M, 640, 301, 24, 5, "f16", "f32", seed=M)
+    p = _problem(M, 640, N, 24, 5, "f16", "f32", seed=M)
     _call(pq2, p)
     y = p["y"].clone()
     _call(pq2, p, out=y, y=y)
@@ -135,20 +145,22 @@ def test_in_place_equals_out_of_place(M):
     assert torch.equal(y, p["out"])
 
 
+@pytest.mark.parametrize("N", [77, 160])
 @pytest.mark.parametrize("M", [1, 31, 32, 33, 300])
-def test_a_batch_without_adapters_is_a_copy(M):
+def test_a_batch_without_adapters_is_a_copy(M, N):
     from gemm_pq2_ternary_gb300 import binding as pq2
-    p = _problem(M, 256, 77, 8, 2, "f16", "f32", seed=1, ids=[-1] * M)
+    p = _problem(M, 256, N, 8, 2, "f16", "f32", seed=1, ids=[-1] * M)
     p["y"][0, 0] = float("inf")
     _call(pq2, p)
     torch.cuda.synchronize()
     assert torch.equal(p["out"], p["y"])
 
 
+@pytest.mark.parametrize("N", [77, 160])
 @pytest.mark.parametrize("M", [3, 90])
-def test_every_rank_zero_is_a_copy(M):
+def test_every_rank_zero_is_a_copy(M, N):
     from gemm_pq2_ternary_gb300 import binding as pq2
-    p = _problem(M, 256, 77, 8, 2, "bf16", "bf16", seed=1, ids=[0] * M)
+    p = _problem(M, 256, N, 8, 2, "bf16", "bf16", seed=1, ids=[0] * M)
     p["ranks"] = torch.zeros(2, dtype=torch.int32, device=DEV)
     _call(pq2, p)
     torch.cuda.synchronize()
@@ -222,6 +234,21 @@ def test_repeated_calls_give_the_same_bits():
             _call(pq2, p, out=o)
         torch.cuda.synchronize()
         assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def test_the_copy_ring_reports_a_stage_that_never_comes():
+    from gemm_pq2_ternary_gb300 import binding as pq2
+    p = _problem(200, 640, 2048, 32, 3, "f16", "f32", seed=21)
+    try:
+        pq2.pq2_debug_set_wait_limit_ns(20_000_000)
+        pq2.pq2_debug_skip_stage(0)
+        _call(pq2, p)
+        assert pq2.pq2_last_device_error() == pq2.PQ2_ERR_TIMEOUT
+    finally:
+        pq2.pq2_debug_skip_stage(-1)
+        pq2.pq2_debug_set_wait_limit_ns(2_000_000_000)
+    _call(pq2, p)
+    _check(pq2, p, p["out"])
 
 
 def test_offsets_past_32_bits():
