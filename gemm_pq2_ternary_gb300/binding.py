@@ -144,9 +144,12 @@ def _check(status: int, where: str):
 
 
 def _stream(stream):
+    """The cudaStream_t as an int (ctypes passes it as the void* argument).
+    The current stream is asked for as a raw handle: 0.2 us against 2.9 us for
+    torch.cuda.current_stream(), which builds an object around it."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream  # an int: ctypes passes it as the void* argument
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _ptr(t):
@@ -296,26 +299,28 @@ def pq2_mlp_down_swiglu(gu, codes, ws, y, workspace, stream=None):
 def _row(t, shape, name):
     """(pointer, element type, row stride) of a 2-D CUDA tensor whose rows are
     contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    if t.shape != shape:
+    ty = _TYPE.get(t.dtype)
+    if ty is None or not t.is_cuda or t.shape != shape:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: expected a CUDA tensor")
+        if ty is None:
+            raise ValueError(f"{name}: expected float32, float16 or bfloat16, got {t.dtype}")
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     ld, unit = t.stride()
     if unit != 1 and shape[1] > 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    ty = _TYPE.get(t.dtype)
-    if ty is None:
-        raise ValueError(f"{name}: expected float32, float16 or bfloat16, got {t.dtype}")
     # a single row's stride says nothing
-    return t.data_ptr(), ty, (shape[1] if shape[0] <= 1 or ld < shape[1] and ld != 0 else ld)
+    if shape[0] <= 1:
+        ld = shape[1]
+    return t.data_ptr(), ty, ld
 
 
 def _weight(w, H, name):
-    if w is None:
-        return None, None
-    if tuple(w.shape) != (H,) or w.dtype not in _TYPE:
+    """(pointer, element type) of a contiguous CUDA vector [H]."""
+    ty = _TYPE.get(w.dtype)
+    if ty is None or w.shape != (H,):
         raise ValueError(f"{name}: expected a float tensor of shape ({H},)")
-    return _ptr(w), _TYPE[w.dtype]
+    return _ptr(w), ty
 
 
 def pq2_rmsnorm(r, w, x, eps=1e-6, flags=0, stream=None):
@@ -324,8 +329,8 @@ def pq2_rmsnorm(r, w, x, eps=1e-6, flags=0, stream=None):
     shape = r.shape
     rp, rt, rl = _row(r, shape, "r")
     xp, xt, xl = _row(x, shape, "x")
-    wp, wt = _weight(w, shape[1], "w")
-    _check(_lib.pq2_rmsnorm(rp, rt, rl, wp, wt or 0, xp, xt, xl, shape[0], shape[1], eps, flags,
+    wp, wt = (None, 0) if w is None else _weight(w, shape[1], "w")
+    _check(_lib.pq2_rmsnorm(rp, rt, rl, wp, wt, xp, xt, xl, shape[0], shape[1], eps, flags,
                             _stream(stream)), "pq2_rmsnorm")
 
 
@@ -340,19 +345,25 @@ def pq2_norm_residual(y, r, r_out, w_post=None, gate=None, w_next=None, x=None, 
     op, ot, ol = _row(r_out, shape, "r_out")
     if ot != rt:
         raise ValueError("r_out: expected r's type")
-    pp, pt = _weight(w_post, shape[1], "w_post")
-    np_, nt = _weight(w_next, shape[1], "w_next")
-    if pt is not None and nt is not None and pt != nt:
-        raise ValueError("w_post and w_next: expected one type")
-    gp, gt, gl = None, 0, 0
+    H = shape[1]
+    pp = np_ = gp = xp = None
+    wt = gt = gl = xt = xl = 0
+    if w_post is not None:
+        pp, wt = _weight(w_post, H, "w_post")
+    if w_next is not None:
+        np_, nt = _weight(w_next, H, "w_next")
+        if pp is not None and nt != wt:
+            raise ValueError("w_post and w_next: expected one type")
+        wt = nt
     if gate is not None:
         if gate.dim() == 1:
-            gp, gt = _weight(gate, shape[1], "gate")
+            gp, gt = _weight(gate, H, "gate")
         else:
             gp, gt, gl = _row(gate, shape, "gate")
-    xp, xt, xl = (None, 0, 0) if x is None else _row(x, shape, "x")
-    args = NormResidualArgs(yp, rp, op, pp, gp, np_, xp, yl, rl, ol, gl, xl, yt, rt,
-                            pt if pt is not None else nt or 0, gt, xt, eps, alpha, flags)
+    if x is not None:
+        xp, xt, xl = _row(x, shape, "x")
+    args = NormResidualArgs(yp, rp, op, pp, gp, np_, xp, yl, rl, ol, gl, xl, yt, rt, wt, gt, xt, eps,
+                            alpha, flags)
     _check(_lib.pq2_norm_residual(ctypes.byref(args), shape[0], shape[1], _stream(stream)),
            "pq2_norm_residual")
 
@@ -383,11 +394,12 @@ def pq2_lora_add(x, A, B, ids, y_in, y_out, workspace, ranks=None, scales=None, 
     _dtype(ids, torch.int32, "ids")
     if ranks is not None:
         _dtype(ranks, torch.int32, "ranks")
+        if ranks.shape != (L,):
+            raise ValueError("ranks: one value per adapter")
     if scales is not None:
         _dtype(scales, torch.float32, "scales")
-    for t in (ranks, scales):
-        if t is not None and t.shape != (L,):
-            raise ValueError("ranks and scales: one value per adapter")
+        if scales.shape != (L,):
+            raise ValueError("scales: one value per adapter")
     ip, it, il = _row(y_in, (M, N), "y_in")
     op, ot, ol = _row(y_out, (M, N), "y_out")
     if it != ot:

@@ -25,9 +25,9 @@
 // every 16 instructions and added up in fp32.
 //
 // Two forms:
-//   few tokens (M <= 32): every warp groups the tokens by adapter itself
-//     (one match over its lanes), and expand adds up the K-split partials of
-//     shrink in a fixed order.  Two launches.
+//   few tokens (M <= 128): every CTA finds its tile of at most 8 tokens of one
+//     adapter itself, and expand adds up the K-split partials of shrink in a
+//     fixed order.  Two launches.
 //   more tokens: a plan kernel sorts the tokens by adapter into tiles of at
 //     most 64 (stable counting sort in shared memory); shrink computes a tile
 //     in a cluster of CTAs that split K and join their partials through
@@ -38,6 +38,7 @@
 // Bounds: bytes.  Decode: A and B of the adapters in use; prompts: y in and
 // out (8 N bytes per token against 2 K + 2 R (K + N) / tokens).
 #include <algorithm>
+#include <cstddef>
 
 #include <cuda_bf16.h>
 
@@ -47,10 +48,12 @@
 namespace pq2 {
 namespace {
 
-constexpr int kFewTokens = 32;
+constexpr int kFewTokens = 128;
+constexpr int kFewTile = 8;       // tokens per tile of the few-token form
 constexpr int kTile = 64;        // tokens per tile of the planned form
 constexpr int kShrinkWarps = 8;
-constexpr int kExpandWarps = 4;
+constexpr int kExpandWarps = 4;   // 32 outputs each
+constexpr int kExpandMaxWarps = 8;
 constexpr int kMaxSplits = 32;
 constexpr int kFlush = 8;        // k32 blocks (16 MMAs) per accumulator chain
 
@@ -116,24 +119,76 @@ __device__ __forceinline__ int adapter_of(const pq2h::LoraParams& p, int m, bool
     return id < 0 ? -1 : id;
 }
 
-// The i-th distinct adapter among M <= 32 tokens, as every warp finds it:
-// its tokens as a lane mask.  kNone: tokens without an adapter form a group
-// too.  mask = 0: there is no such group.
-struct Group {
+// The few-token form's tiles: the tokens of an adapter in their order, cut by
+// eights; a tile counts where its first token stands.  Every CTA works out its
+// own tile (the ids are one load, the rest is a few hundred instructions)
+// instead of waiting for another kernel to do it.  kNone: tokens without an
+// adapter form tiles too (adapter -1).
+struct alignas(16) FewTile {
+    int ids[kFewTokens];    // read by fours: on its 16 bytes
+    int tok[kFewTile];
     int adapter;
-    unsigned mask;
+    int count;              // 0: there is no such tile
+    int starts[kFewTokens / 32];
+    int sel[2];
 };
+static_assert(offsetof(FewTile, ids) % 16 == 0, "int4 reads");
+// All threads of the CTA (at least 128 of them where M > 32); the answer is
+// in `f` after the last barrier.
 template <bool kNone>
-__device__ __forceinline__ Group find_group(const pq2h::LoraParams& p, int i, bool report) {
-    const int lane = threadIdx.x & 31;
-    const int id = lane < p.M ? adapter_of(p, lane, report) : -2;
-    const unsigned same = __match_any_sync(0xffffffffu, id);
-    const bool leads = (__ffs(same) - 1) == lane && (kNone ? id >= -1 : id >= 0);
-    unsigned lead = __ballot_sync(0xffffffffu, leads);
-    for (int k = 0; k < i; ++k) lead &= lead - 1;
-    if (lead == 0) return {-1, 0u};
-    const int src = __ffs(lead) - 1;
-    return {__shfl_sync(0xffffffffu, id, src), __shfl_sync(0xffffffffu, same, src)};
+__device__ __forceinline__ void find_tile(const pq2h::LoraParams& p, int index, bool report,
+                                          FewTile& f) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (p.M <= 32) {
+        if (warp == 0) {
+            const int id = lane < p.M ? adapter_of(p, lane, report) : -2;
+            const unsigned same = __match_any_sync(0xffffffffu, id);
+            const int rank = __popc(same & ((1u << lane) - 1u));
+            const bool starts = (kNone ? id >= -1 : id >= 0) && rank % kFewTile == 0;
+            unsigned lead = __ballot_sync(0xffffffffu, starts);
+            for (int k = 0; k < index; ++k) lead &= lead - 1;
+            const int src = lead ? __ffs(lead) - 1 : 0;
+            const int sid = __shfl_sync(0xffffffffu, id, src), sr = __shfl_sync(0xffffffffu, rank, src);
+            const bool member = lead && id == sid && rank / kFewTile == sr / kFewTile;
+            const unsigned all = __ballot_sync(0xffffffffu, member);
+            if (member) f.tok[rank % kFewTile] = lane;
+            if (lane == 0) f.adapter = sid, f.count = __popc(all);
+        }
+        __syncthreads();
+        return;
+    }
+    const int id = tid < p.M ? adapter_of(p, tid, report) : -2;
+    if (tid < kFewTokens) f.ids[tid] = id;
+    if (tid == 0) f.sel[0] = -3;
+    __syncthreads();
+    int rank = 0;
+    if (tid < p.M) {
+        const int4* v = reinterpret_cast<const int4*>(f.ids);
+        for (int j = 0; j < tid / 4; ++j) {
+            const int4 q = v[j];
+            rank += (q.x == id) + (q.y == id) + (q.z == id) + (q.w == id);
+        }
+        for (int j = tid / 4 * 4; j < tid; ++j) rank += f.ids[j] == id;
+    }
+    const bool starts = tid < p.M && (kNone ? id >= -1 : id >= 0) && rank % kFewTile == 0;
+    const unsigned lead = __ballot_sync(0xffffffffu, starts);
+    if (lane == 0 && warp < kFewTokens / 32) f.starts[warp] = __popc(lead);
+    __syncthreads();
+    if (starts) {
+        int at = __popc(lead & ((1u << lane) - 1u));
+        for (int w = 0; w < warp; ++w) at += f.starts[w];
+        if (at == index) f.sel[0] = id, f.sel[1] = rank / kFewTile;
+    }
+    __syncthreads();
+    const bool member = tid < p.M && id == f.sel[0] && rank / kFewTile == f.sel[1];
+    if (member) f.tok[rank % kFewTile] = tid;
+    const int count = __syncthreads_count(member);
+    if (tid == 0) f.adapter = f.sel[0], f.count = count;
+    __syncthreads();
+}
+// Tiles there can be among M tokens of L adapters.
+constexpr int64_t few_tiles(int64_t M, int64_t groups) {
+    return groups + M / kFewTile < M ? groups + M / kFewTile : M;
 }
 
 // v's token as 16-bit terms.  fp16: the token is scaled by 2^-e first.
@@ -187,108 +242,71 @@ __device__ __forceinline__ int k_warps(int rank_tiles) {
     return rank_tiles == 1 ? 8 : rank_tiles == 2 ? 4 : rank_tiles <= 4 ? 2 : 1;
 }
 
-// One CTA's partial product: the ranks of adapter l x `count` tokens (token
-// list in shared memory) over columns [k0, k1) of K.  out(j, r, v) receives
-// the result for token j of the list and rank r.
-template <bool BF, int NT, typename Out>
-__device__ __forceinline__ void shrink_tile(const pq2h::LoraParams& p, int l, int rank,
-                                            const int* tok, int count, int k0, int k1, float* red,
-                                            Out out) {
+// Few tokens: CTA (split, tile): the ranks of the tile's adapter times its
+// tokens over one share of K, straight from global memory, eight blocks of 32
+// columns in flight per warp.  part [splits][M][R].
+template <bool BF>
+__global__ void __launch_bounds__(kShrinkWarps * 32)
+    lora_shrink_few(pq2h::LoraParams p, float* part, int k_split) {
+    __shared__ float red[kShrinkWarps * 16 * kFewTile];
+    __shared__ FewTile tile;
+    pdl_wait();
+    pdl_launch_dependents();
+    find_tile<false>(p, blockIdx.y, blockIdx.x + blockIdx.y == 0, tile);
+    const int count = tile.count, l = tile.adapter;
+    if (count == 0) return;  // uniform over the CTA
+    const int rank = rank_of(p, l);
+    const int k0 = blockIdx.x * k_split, k1 = min(k0 + k_split, p.K);
+    float* dst = part + static_cast<size_t>(blockIdx.x) * p.M * p.R;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int rank_tiles = (rank + 15) / 16;
     const int kw = k_warps(rank_tiles);
     const int per_round = kShrinkWarps / kw;
     const int ks = warp % kw;
-    const uint16_t* x[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int j = i * 8 + g;
-        x[i] = j < count ? p.x + static_cast<size_t>(tok[j]) * p.ld_x : nullptr;
-    }
+    const uint16_t* x = g < count ? p.x + static_cast<size_t>(tile.tok[g]) * p.ld_x : nullptr;
     // more than one round only with kw == 1, where `red` is not used
     for (int rt = warp / kw; rt < rank_tiles; rt += per_round) {
         const int ra = rt * 16 + g, rb = ra + 8;
         const uint16_t* a0 = p.A + (static_cast<size_t>(l) * p.R + ra) * p.K;
         const uint16_t* a1 = a0 + static_cast<size_t>(8) * p.K;
-        float sum[NT][4], acc[NT][4];
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) sum[i][c] = acc[i][c] = 0.0f;
-        constexpr int U = NT == 1 ? 8 : 4;  // blocks in flight
-        int chain = 0;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        constexpr int U = kFlush;  // blocks in flight, and in a chain
         for (int kb = k0 + ks * 32; kb < k1; kb += kw * 32 * U) {
-            uint4 fa[U], fb[U], fx[U][NT];
+            uint4 fa[U], fb[U], fx[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int k = kb + u * kw * 32 + 8 * t;
                 fa[u] = k < k1 && ra < rank ? load16(a0 + k) : zero4();
                 fb[u] = k < k1 && rb < rank ? load16(a1 + k) : zero4();
-#pragma unroll
-                for (int i = 0; i < NT; ++i) fx[u][i] = k < k1 && x[i] ? load16(x[i] + k) : zero4();
+                fx[u] = k < k1 && x ? load16(x + k) : zero4();
             }
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u) mma_block<BF>(acc, fa[u], fb[u], fx[u]);
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
-                    if (i * 8 < count) mma_block<BF>(acc[i], fa[u], fb[u], fx[u][i]);
-            chain += U;
-            if (chain >= kFlush) {
-                chain = 0;
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        sum[i][c] += acc[i][c];
-                        acc[i][c] = 0.0f;
-                    }
-            }
+            for (int c = 0; c < 4; ++c) sum[c] += acc[c];
         }
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float v = sum[i][c] + acc[i][c];
-                const int r = (c >> 1) * 8 + g, j = i * 8 + 2 * t + (c & 1);
-                if (kw > 1)
-                    red[(warp * 16 + r) * (NT * 8) + j] = v;
-                else if (j < count && rt * 16 + r < rank)
-                    out(j, rt * 16 + r, v);
-            }
+        for (int c = 0; c < 4; ++c) {
+            const int r = (c >> 1) * 8 + g, j = 2 * t + (c & 1);
+            if (kw > 1)
+                red[(warp * 16 + r) * kFewTile + j] = sum[c];
+            else if (j < count && rt * 16 + r < rank)
+                dst[static_cast<size_t>(tile.tok[j]) * p.R + rt * 16 + r] = sum[c];
+        }
     }
     if (kw > 1) {
         __syncthreads();
         for (int i = threadIdx.x; i < rank_tiles * 16 * count; i += kShrinkWarps * 32) {
             const int r = i % (rank_tiles * 16), j = i / (rank_tiles * 16);
             if (r >= rank) continue;
-            const float* src = red + ((r / 16) * kw * 16 + r % 16) * (NT * 8) + j;
+            const float* src = red + ((r / 16) * kw * 16 + r % 16) * kFewTile + j;
             float v = 0.0f;
-            for (int w = 0; w < kw; ++w) v += src[w * 16 * NT * 8];
-            out(j, r, v);
+            for (int w = 0; w < kw; ++w) v += src[w * 16 * kFewTile];
+            dst[static_cast<size_t>(tile.tok[j]) * p.R + r] = v;
         }
     }
-}
-
-// Few tokens: CTA (split, group).  part [splits][M][R].
-template <bool BF, int NT>
-__global__ void __launch_bounds__(kShrinkWarps * 32) lora_shrink_few(pq2h::LoraParams p,
-                                                                     float* part, int k_split) {
-    __shared__ float red[kShrinkWarps * 16 * NT * 8];
-    __shared__ int tok[kFewTokens];
-    pdl_wait();
-    pdl_launch_dependents();
-    const Group grp = find_group<false>(p, blockIdx.y, blockIdx.x + blockIdx.y + threadIdx.x / 32 == 0);
-    if (grp.mask == 0) return;  // uniform over the CTA
-    const int lane = threadIdx.x & 31;
-    if (threadIdx.x < 32 && ((grp.mask >> lane) & 1u))
-        tok[__popc(grp.mask & ((1u << lane) - 1u))] = lane;
-    __syncthreads();
-    const int rank = rank_of(p, grp.adapter);
-    const int k0 = blockIdx.x * k_split, k1 = min(k0 + k_split, p.K);
-    float* dst = part + static_cast<size_t>(blockIdx.x) * p.M * p.R;
-    shrink_tile<BF, NT>(p, grp.adapter, rank, tok, __popc(grp.mask), k0, k1, red,
-                        [&](int j, int r, float v) { dst[tok[j] * p.R + r] = v; });
 }
 
 // ----------------------------------------------------------------------------
@@ -430,49 +448,46 @@ __device__ __forceinline__ void y_fetch(const pq2h::LoraParams& p, float4 (&y)[N
         }
 }
 
-// Few tokens: CTA (128 outputs, group).  The operands that do not come from
-// shrink (B, y) are loaded before the dependency wait: shrink lets this
+// Few tokens: CTA (32 outputs a warp, tile).  The operands that do not come
+// from shrink (B, y) are loaded before the dependency wait: shrink lets this
 // kernel start only after its own wait, so everything before it is done.
-template <bool BF, int NT, int YT>
-__global__ void __launch_bounds__(kExpandWarps * 32)
+template <bool BF, int YT>
+__global__ void __launch_bounds__(kExpandMaxWarps * 32)
     lora_expand_few(pq2h::LoraParams p, const float* part, int splits, int vec) {
     extern __shared__ __align__(16) uint16_t sv[];
-    __shared__ int tok[kFewTokens];
-    __shared__ float f[kFewTokens];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Group grp = find_group<true>(p, blockIdx.y, false);
-    if (grp.mask == 0) {  // uniform over the CTA
+    __shared__ FewTile tile;
+    __shared__ float f[kFewTile];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+    find_tile<true>(p, blockIdx.y, false, tile);
+    const int count = tile.count, l = tile.adapter;
+    const int* tok = tile.tok;
+    if (count == 0) {  // uniform over the CTA
         pdl_wait();
         return;
     }
-    if (warp == 0 && ((grp.mask >> lane) & 1u))
-        tok[__popc(grp.mask & ((1u << lane) - 1u))] = lane;
-    __syncthreads();
-    const int count = __popc(grp.mask);
-    const int l = grp.adapter;
     const int rank = l >= 0 ? rank_of(p, l) : 0;
     const int blocks = (rank + 31) / 32;
-    const int n = blockIdx.x * (kExpandWarps * 32) + warp * 32 + 4 * (lane >> 2);
+    const int n = (blockIdx.x * nwarps + warp) * 32 + 4 * (lane >> 2);
     constexpr int kAhead = 2;  // blocks of B loaded before the wait
     BRows b[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
         if (i < blocks) b[i] = b_load(p, l, rank, n, i);
-    float4 y[NT][2];
-    y_fetch<YT, NT>(p, y, tok, count, n, vec != 0);
+    float4 y[1][2];
+    y_fetch<YT, 1>(p, y, tok, count, n, vec != 0);
     const float scale = l >= 0 && p.scales ? __ldcg(p.scales + l) : 1.0f;
 
     pdl_wait();
     pdl_launch_dependents();
     // v: the K-split partials in order; then the 16-bit terms
-    const int pitch = term_pitch((p.R + 31) / 32), term_size = NT * 8 * pitch;
-    for (int j = warp; j < NT * 8 && blocks > 0; j += kExpandWarps) {
+    const int pitch = term_pitch((p.R + 31) / 32), term_size = kFewTile * pitch;
+    for (int j = warp; j < count && blocks > 0; j += nwarps) {
         float v[8], top = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = i * 32 + lane;
             v[i] = 0.0f;
-            if (i >= blocks || j >= count || r >= rank) continue;
+            if (i >= blocks || r >= rank) continue;
             const float* src = part + static_cast<size_t>(tok[j]) * p.R + r;
             const size_t step = static_cast<size_t>(p.M) * p.R;
             for (int s0 = 0; s0 < splits; s0 += 16) {
@@ -494,21 +509,18 @@ __global__ void __launch_bounds__(kExpandWarps * 32)
             for (int q = 0; q < terms<BF>(); ++q)
                 sv[q * term_size + j * pitch + i * 32 + lane] = w[q];
         }
-        if (lane == 0 && j < count) f[j] = scale * up;
+        if (lane == 0) f[j] = scale * up;
     }
-    __syncthreads();
     if (blocks == 0) {
         if (p.y_in == p.y_out && p.ld_in == p.ld_out) return;
-        if (threadIdx.x < kFewTokens) f[threadIdx.x] = 0.0f;
-        __syncthreads();
+        if (threadIdx.x < kFewTile) f[threadIdx.x] = 0.0f;
     }
-    float acc[2][NT][4];
+    __syncthreads();
+    float acc[2][1][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[h][i][c] = 0.0f;
+        for (int c = 0; c < 4; ++c) acc[h][0][c] = 0.0f;
     for (int blk = 0; blk < blocks; blk += kAhead) {
         if (blk > 0) {
 #pragma unroll
@@ -517,10 +529,9 @@ __global__ void __launch_bounds__(kExpandWarps * 32)
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-            if (blk + i < blocks)
-                expand_block<BF, NT>(acc, b[i], sv, pitch, term_size, blk + i, count);
+            if (blk + i < blocks) expand_block<BF, 1>(acc, b[i], sv, pitch, term_size, blk + i, count);
     }
-    expand_store<YT, NT>(p, acc, y, tok, f, count, n, vec != 0);
+    expand_store<YT, 1>(p, acc, y, tok, f, count, n, vec != 0);
 }
 
 // ----------------------------------------------------------------------------
@@ -554,16 +565,27 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
     const int per = ((p.M + warps - 1) / warps + 31) / 32 * 32;
     const int m0 = warp * per, m1 = min(m0 + per, p.M);
     int* mine = hist + warp * bins;
-    for (int base = m0; base < m1; base += 32) {
-        const int m = base + lane;
-        int key = -1;
-        if (m < m1) {
-            key = adapter_of(p, m, true);
-            if (key < 0) key = p.L;
+    // the tokens four at a time a lane, loaded together
+    constexpr int kBatch = 4;
+    int keys[kBatch];
+    auto load_keys = [&](int base, bool report) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int m = base + i * 32 + lane;
+            keys[i] = m < m1 ? adapter_of(p, m, report) : -2;
         }
-        const unsigned same = __match_any_sync(0xffffffffu, key);
-        if (key >= 0 && __ffs(same) - 1 == lane) mine[key] += __popc(same);
-        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) keys[i] = keys[i] == -1 ? p.L : keys[i];
+    };
+    for (int base = m0; base < m1; base += 32 * kBatch) {
+        load_keys(base, true);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (base + i * 32 >= m1) break;
+            const unsigned same = __match_any_sync(0xffffffffu, keys[i]);
+            if (keys[i] >= 0 && __ffs(same) - 1 == lane) mine[keys[i]] += __popc(same);
+            __syncwarp();
+        }
     }
     __syncthreads();
     // per bin: the warps' counts to offsets; then a scan over the bins, each
@@ -602,23 +624,24 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
     }
     if (threadIdx.x == nthreads - 1) *pl.num_tiles = at_tile;
     __syncthreads();
-    for (int base = m0; base < m1; base += 32) {
-        const int m = base + lane;
-        int key = -1;
-        if (m < m1) {
-            key = adapter_of(p, m, false);
-            if (key < 0) key = p.L;
+    for (int base = m0; base < m1; base += 32 * kBatch) {
+        if (per > 32 * kBatch) load_keys(base, false);   // else still there
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (base + i * 32 >= m1) break;
+            const int key = keys[i];
+            const unsigned same = __match_any_sync(0xffffffffu, key);
+            const int leader = __ffs(same) - 1;
+            int at = 0;
+            if (key >= 0 && leader == lane) {
+                at = mine[key];
+                mine[key] = at + __popc(same);
+            }
+            at = __shfl_sync(0xffffffffu, at, leader);
+            if (key >= 0)
+                pl.perm[off[key] + at + __popc(same & ((1u << lane) - 1u))] = base + i * 32 + lane;
+            __syncwarp();
         }
-        const unsigned same = __match_any_sync(0xffffffffu, key);
-        const int leader = __ffs(same) - 1;
-        int at = 0;
-        if (key >= 0 && leader == lane) {
-            at = mine[key];
-            mine[key] = at + __popc(same);
-        }
-        at = __shfl_sync(0xffffffffu, at, leader);
-        if (key >= 0) pl.perm[off[key] + at + __popc(same & ((1u << lane) - 1u))] = m;
-        __syncwarp();
     }
 }
 
@@ -627,9 +650,20 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
+// Asynchronous copy of 4 or 16 bytes to shared memory.
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
+// One arrival on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
 template <int kLeft>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
@@ -645,19 +679,28 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t saddr, uint32_t rank) {
+// First phase of the barrier apart: this CTA has started (and orders nothing).
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
     uint32_t a;
-    float v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
+    return a;
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 constexpr int kStageK = 64;       // columns of K per pipeline stage: rows of 128 bytes
-// Pipeline stages: about 96 KB a CTA, two CTAs per SM (ranks above 128: 160 KB).
+// Pipeline stages: with the partials about 100 KB a CTA, two CTAs per SM (ranks
+// above 128: 184 KB).
 template <int RPW, int WN>
 constexpr int shrink_stages() {
-    return RPW * WN <= 2 ? 8 : RPW * WN == 4 ? 6 : 4;
+    return RPW * WN <= 2 ? 8 : RPW * WN == 4 ? 5 : 3;
 }
 
 // A warp's share of one pipeline stage.  x0, a0: this lane's first rows of x
@@ -688,18 +731,24 @@ __device__ __forceinline__ void shrink_stage(float (&acc)[RPW][WN][4], uint32_t 
 }
 
 // A cluster of CTAs computes one tile: v[64 tokens][R] over its share of K
-// each.  x and A come through a pipeline of asynchronous copies; a row is 8
-// chunks of 16 bytes, the halves swapped in odd rows, so that the 8 lanes of a
-// 16-byte read (two rows, four chunks) touch all banks once.  A warp owns RPW
-// rank tiles of 16 and WN groups of 8 tokens.  The partials meet in
-// distributed shared memory: each CTA adds up its share of the tokens, CTA by
-// CTA in order, and writes their 16-bit terms.
+// each.  Loader warps bring x and A through a ring of asynchronous copies; a
+// row is 8 chunks of 16 bytes, the halves swapped in odd rows, so that the 8
+// lanes of a 16-byte read (two rows, four chunks) touch all banks once.  A
+// consumer warp owns RPW rank tiles of 16 and WN groups of 8 tokens, and
+// waits for nothing but its stage.  Every CTA stores its partials of token j
+// into the shared memory of CTA j % splits of the cluster, which adds them up,
+// CTA by CTA in order, and writes the token's 16-bit terms: one cluster
+// barrier, and nobody has to stay for the others.
+constexpr int kShrinkLoaders = 4;
+
 template <bool BF, int RPW, int WN>
-__global__ void __launch_bounds__(kShrinkWarps * 32)
+__global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
     lora_shrink_tiles(pq2h::LoraParams p, Plan pl, int splits, int k_split) {
-    constexpr int kShrinkStages = shrink_stages<RPW, WN>();
+    constexpr int kStages = shrink_stages<RPW, WN>();
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int tok[kTile];
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
+    __shared__ int abort_word;
+    volatile int* abort_flag = &abort_word;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     pdl_wait();
@@ -710,101 +759,156 @@ __global__ void __launch_bounds__(kShrinkWarps * 32)
     const int l = tile.x, first = tile.y, count = tile.z;
     const int rank = l >= 0 ? rank_of(p, l) : 0;
     if (rank == 0) return;
-    if (tid < count) tok[tid] = pl.perm[first + tid];
+    // warps that have ranks and tokens
+    constexpr int kTokenWarps = kTile / 8 / WN;
+    const int busy = ((rank + 16 * RPW - 1) / (16 * RPW)) * ((count + 8 * WN - 1) / (8 * WN));
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], kShrinkLoaders * 32);
+            mbar_init(&empty[s], busy);
+        }
+        abort_word = 0;
+        fence_mbar_init();
+    }
+    if (splits > 1) cluster_arrive_relaxed();
     __syncthreads();
     const int part = splits > 1 ? static_cast<int>(cluster_rank()) : 0;
     const int k0 = part * k_split, k1 = min(k0 + k_split, p.K);
-
-    // copies: thread -> chunk tid % 8 of rows tid / 8 + 32 i
+    const int steps = (max(k1 - k0, 0) + kStageK - 1) / kStageK;
     // rows of A per stage: whole shares of a warp (16 RPW)
     const int r16 = (p.R + 16 * RPW - 1) / (16 * RPW) * (16 * RPW);
     const int stage_bytes = (kTile + r16) * 128;
-    const int chunk = tid & 7, row0 = tid >> 3;
     const uint32_t base = smem_u32(smem);
-    const uint32_t dst0 = row0 * 128 + ((chunk ^ ((row0 & 1) * 4)) * 16);
-    const uint16_t* xs[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int j = row0 + 32 * i;
-        xs[i] = j < count ? p.x + static_cast<size_t>(tok[j]) * p.ld_x + chunk * 8 : nullptr;
-    }
-    const uint16_t* as = p.A + (static_cast<size_t>(l) * p.R + row0) * p.K + chunk * 8;
-    const int a_rows = (rank + 16 * RPW - 1) / (16 * RPW) * (16 * RPW);
-    const size_t a_step = static_cast<size_t>(32) * p.K;
-    auto issue = [&](int kb, int slot) {
-        const uint32_t st = base + slot * stage_bytes + dst0;
-        const int k = k0 + kb;
-        const uint32_t in = k + chunk * 8 < k1 ? 16 : 0;  // else zeros (the address is not read)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (xs[i]) cp_async16(st + i * 32 * 128, xs[i] + (in ? k : 0), in);
-        const uint16_t* a = as + (in ? k : 0);
-        for (int r = row0; r < a_rows; r += 32, a += a_step)
-            cp_async16(st + (kTile + r - row0) * 128, r < rank ? a : p.A, r < rank ? in : 0);
-    };
-    // this warp's rank tiles and token groups
-    constexpr int kTokenWarps = kTile / 8 / WN;
     const int rt0 = warp / kTokenWarps * RPW, n0 = warp % kTokenWarps * WN;
-    const bool works = rt0 * 16 < rank && n0 * 8 < count;
-    const uint32_t at[2] = {static_cast<uint32_t>((t ^ ((g & 1) * 4)) * 16),
-                            static_cast<uint32_t>(((4 + t) ^ ((g & 1) * 4)) * 16)};
-    float sum[RPW][WN][4], acc[RPW][WN][4];
+    const bool works = warp < kShrinkWarps && rt0 * 16 < rank && n0 * 8 < count;
+    float sum[RPW][WN][4];
 #pragma unroll
     for (int r = 0; r < RPW; ++r)
 #pragma unroll
         for (int i = 0; i < WN; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sum[r][i][c] = acc[r][i][c] = 0.0f;
-    const int kspan = max(k1 - k0, 0);
+            for (int c = 0; c < 4; ++c) sum[r][i][c] = 0.0f;
+
+    if (warp >= kShrinkWarps) {
+        // thread -> chunk pt % 8 of rows pt / 8 + 16 i.  Rows past the rank or
+        // the tile are left as they are in shared memory: a row of A only
+        // reaches its own rank's sums, a row of x its own token's, and those
+        // are not stored.  Columns past K enter every sum: zeros.
+        const int pt = tid - kShrinkWarps * 32;
+        const int chunk = pt & 7, row0 = pt >> 3;
+        constexpr int kRows = kShrinkLoaders * 4;   // rows per round
+        constexpr int kXRounds = kTile / kRows, kARounds = kShrinkWarps / kTokenWarps * RPW * 16 / kRows;
+        const uint32_t dst0 = base + row0 * 128 + ((chunk ^ ((row0 & 1) * 4)) * 16);
+        const uint16_t *xs[kXRounds], *as[kARounds];
 #pragma unroll
-    for (int s = 0; s < kShrinkStages - 1; ++s) {
-        if (s * kStageK < kspan) issue(s * kStageK, s);
-        cp_async_commit();
-    }
-    for (int kb = 0, step = 0; kb < kspan; kb += kStageK, ++step) {
-        cp_async_wait<kShrinkStages - 2>();
-        __syncthreads();
-        const int ahead = kb + (kShrinkStages - 1) * kStageK;
-        if (ahead < kspan) issue(ahead, (step + kShrinkStages - 1) % kShrinkStages);
-        cp_async_commit();
-        if (!works) continue;
-        const uint32_t st = base + (step % kShrinkStages) * stage_bytes;
-        const uint32_t x0 = st + (n0 * 8 + g) * 128, a0 = st + (kTile + rt0 * 16 + g) * 128;
-        // one group of tokens, or all of this warp's (columns past the
-        // tile's last token hold anything and are not stored)
-        if (count - n0 * 8 > 8)
-            shrink_stage<BF, RPW, WN, WN>(acc, x0, a0, at);
-        else
-            shrink_stage<BF, RPW, 1, WN>(acc, x0, a0, at);
-        if ((step + 1) % (kFlush / 2) == 0) {
-#pragma unroll
-            for (int r = 0; r < RPW; ++r)
-#pragma unroll
-                for (int i = 0; i < WN; ++i)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        sum[r][i][c] += acc[r][i][c];
-                        acc[r][i][c] = 0.0f;
-                    }
+        for (int i = 0; i < kXRounds; ++i) {
+            const int j = row0 + kRows * i;
+            xs[i] = j < count ? p.x + static_cast<size_t>(pl.perm[first + j]) * p.ld_x + k0 + chunk * 8
+                              : nullptr;
         }
-    }
-    cp_async_wait<0>();
-    __syncthreads();
-    // partials [token][r16 + 4] in the pipeline's memory
-    float* red = reinterpret_cast<float*>(smem);
-    const int pitch = r16 + 4;
-    if (works) {
+#pragma unroll
+        for (int i = 0; i < kARounds; ++i) {
+            const int r = row0 + kRows * i;
+            as[i] = r < rank ? p.A + (static_cast<size_t>(l) * p.R + r) * p.K + k0 + chunk * 8 : nullptr;
+        }
+        int s = 0;
+        uint32_t turn = 0;
+        for (int step = 0; step < steps; ++step) {
+            if (turn > 0 && !mbar_wait_warp(&empty[s], (turn - 1) & 1, p.ctl, abort_flag)) break;
+            if (step != p.ctl.debug_skip_stage) {  // else withheld (timeout test)
+                const uint32_t st = dst0 + s * stage_bytes;
+                const int k = step * kStageK;
+                if (k0 + k + kStageK <= k1) {
+#pragma unroll
+                    for (int i = 0; i < kARounds; ++i)
+                        if (as[i]) cp_async<16>(st + (kTile + i * kRows) * 128, as[i] + k);
+#pragma unroll
+                    for (int i = 0; i < kXRounds; ++i)
+                        if (xs[i]) cp_async<16>(st + i * kRows * 128, xs[i] + k);
+                } else {
+                    const bool in = k0 + k + chunk * 8 < k1;
+#pragma unroll
+                    for (int i = 0; i < kARounds; ++i)
+                        if (as[i]) cp_async16(st + (kTile + i * kRows) * 128, in ? as[i] + k : p.A, in ? 16 : 0);
+#pragma unroll
+                    for (int i = 0; i < kXRounds; ++i)
+                        if (xs[i]) cp_async16(st + i * kRows * 128, in ? xs[i] + k : p.x, in ? 16 : 0);
+                }
+                cp_async_arrive(&full[s]);
+            }
+            if (++s == kStages) s = 0, ++turn;
+        }
+        cp_async_wait<0>();
+    } else if (works) {
+        const uint32_t at[2] = {static_cast<uint32_t>((t ^ ((g & 1) * 4)) * 16),
+                                static_cast<uint32_t>(((4 + t) ^ ((g & 1) * 4)) * 16)};
+        float acc[RPW][WN][4];
 #pragma unroll
         for (int r = 0; r < RPW; ++r)
 #pragma unroll
             for (int i = 0; i < WN; ++i)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int rr = (rt0 + r) * 16 + (c >> 1) * 8 + g;
-                    const int j = (n0 + i) * 8 + 2 * t + (c & 1);
-                    if (rr < rank && j < count) red[j * pitch + rr] = sum[r][i][c] + acc[r][i][c];
-                }
+                for (int c = 0; c < 4; ++c) acc[r][i][c] = 0.0f;
+        int s = 0;
+        uint32_t turn = 0;
+        for (int step = 0; step < steps; ++step) {
+            if (!mbar_wait_warp(&full[s], turn & 1, p.ctl, abort_flag)) {
+                *abort_flag = 1;   // the host reads the error; v is not used
+                break;
+            }
+            const uint32_t st = base + s * stage_bytes;
+            const uint32_t x0 = st + (n0 * 8 + g) * 128, a0 = st + (kTile + rt0 * 16 + g) * 128;
+            // one group of tokens, or all of this warp's (columns past the
+            // tile's last token hold anything and are not stored)
+            if (count - n0 * 8 > 8)
+                shrink_stage<BF, RPW, WN, WN>(acc, x0, a0, at);
+            else
+                shrink_stage<BF, RPW, 1, WN>(acc, x0, a0, at);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);
+            if (++s == kStages) s = 0, ++turn;
+            if ((step + 1) % (kFlush / 2) == 0 || step + 1 == steps) {
+#pragma unroll
+                for (int r = 0; r < RPW; ++r)
+#pragma unroll
+                    for (int i = 0; i < WN; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            sum[r][i][c] += acc[r][i][c];
+                            acc[r][i][c] = 0.0f;
+                        }
+            }
+        }
     }
+    // partials [from CTA][token / splits][r16], in the owner's shared memory
+    float* inbox = reinterpret_cast<float*>(smem + kStages * stage_bytes);
+    const int per_cta = (kTile + splits - 1) / splits;
+    __syncwarp();
+    if (splits > 1) cluster_wait();   // all of the cluster have started
+    if (works) {
+        const uint32_t mine = smem_u32(inbox) + part * per_cta * r16 * 4;
+#pragma unroll
+        for (int i = 0; i < WN; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int j = (n0 + i) * 8 + 2 * t + h;
+                if (j >= count) continue;
+                uint32_t to = mine + (j / splits) * r16 * 4;
+                if (splits > 1) to = map_to_rank(to, j % splits);
+#pragma unroll
+                for (int r = 0; r < RPW; ++r)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int rr = (rt0 + r) * 16 + c * 8 + g;
+                        if (rr >= rank) continue;
+                        if (splits > 1)
+                            st_cluster_f32(to + rr * 4, sum[r][i][c * 2 + h]);
+                        else
+                            sts_f32(to + rr * 4, sum[r][i][c * 2 + h]);
+                    }
+            }
+    }
+    __syncwarp();
     if (splits > 1)
         cluster_sync();
     else
@@ -812,23 +916,15 @@ __global__ void __launch_bounds__(kShrinkWarps * 32)
     const float scale = p.scales ? p.scales[l] : 1.0f;
     const size_t term_size = static_cast<size_t>(p.M) * pl.rp;
     const int blocks = (rank + 31) / 32;
-    for (int j = part + splits * warp; j < count; j += splits * kShrinkWarps) {
+    for (int j = part + splits * warp; j < count; j += splits * (kShrinkWarps + kShrinkLoaders)) {
         float v[8], top = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = i * 32 + lane;
             v[i] = 0.0f;
             if (i >= blocks || r >= rank) continue;
-            if (splits > 1) {
-                float w[8];
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    w[s] = s < splits ? ld_cluster_f32(smem_u32(red + j * pitch + r), s) : 0.0f;
-#pragma unroll
-                for (int s = 0; s < 8; ++s) v[i] += w[s];
-            } else {
-                v[i] = red[j * pitch + r];
-            }
+            const float* src = inbox + (j / splits) * r16 + r;
+            for (int s = 0; s < splits; ++s) v[i] += src[s * per_cta * r16];
             top = fmaxf(top, fabsf(v[i]));
         }
         const float up = pow2_below<BF>(warp_max(top)), down = 1.0f / up;
@@ -843,7 +939,6 @@ __global__ void __launch_bounds__(kShrinkWarps * 32)
                 pl.terms[q * term_size + static_cast<size_t>(first + j) * pl.rp + i * 32 + lane] = w[q];
         }
     }
-    if (splits > 1) cluster_sync();  // nobody leaves while its partials are read
 }
 
 // CTA (rounds x 128 outputs, tile): v's terms in shared memory, then per 32
@@ -914,20 +1009,6 @@ constexpr int kRingWarps = 16;      // consumers
 constexpr int kRingLoaders = 4;     // producer warps
 constexpr int kRingMaxStages = 8;
 
-// Asynchronous copy of 4 or 16 bytes to shared memory.
-template <int kBytes>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-    if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-// One arrival on `bar` once this thread's copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-
 template <bool BF, int YT, int kNB, int kPiece>
 __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
     lora_expand_ring(pq2h::LoraParams p, Plan pl, int stages, int stage_bytes, int term_bytes) {
@@ -970,8 +1051,13 @@ __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
         const int row0 = pt / kPieces, piece = pt % kPieces;     // row0 is a warp's, or two
         const uint8_t* yb = static_cast<const uint8_t*>(p.y_in) + piece * kPiece;
         const long long ld = p.ld_in * kUnit;
+        // each thread's rows by their addresses where they are few, else the
+        // tile's tokens (lane, lane + 32) shared by shuffles
+        constexpr int kRounds = kTile / kRows;
+        constexpr bool kByAddress = kRounds <= 16;
+        const uint8_t* rows[kByAddress ? kRounds : 1];
+        int tk[2] = {0, 0};
         int cached = -1, l = -1, rank = 0, count = 0;
-        int tk[2] = {0, 0};        // the tile's tokens: lane, lane + 32
         int issued = 0, s = 0;
         uint32_t turn = 0;
         for (; left > 0; --left) {
@@ -979,9 +1065,17 @@ __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
                 const int4 tile = __ldcg(pl.tiles + index);
                 cached = index, l = tile.x, count = tile.z;
                 rank = l >= 0 ? rank_of(p, l) : 0;
+                if constexpr (kByAddress) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (lane + 32 * h < count) tk[h] = __ldcg(pl.perm + tile.y + lane + 32 * h);
+                    for (int i = 0; i < kRounds; ++i) {
+                        const int j = row0 + kRows * i;
+                        rows[i] = j < count ? yb + __ldcg(pl.perm + tile.y + j) * ld : nullptr;
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (lane + 32 * h < count) tk[h] = __ldcg(pl.perm + tile.y + lane + 32 * h);
+                }
             }
             const int n0 = nb * kNB, n = min(kNB, p.N - n0);
             if (++nb == nblocks) nb = 0, ++index;
@@ -997,15 +1091,26 @@ __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
                                  p.B + (static_cast<size_t>(l) * p.N + n0) * p.R, brow, &full[s]);
                 }
                 __syncwarp();
-                const uint8_t* src = yb + static_cast<size_t>(n0) * kUnit;
-                uint32_t dst = smem_u32(st) + row0 * kYPitch + piece * kPiece;
-                const bool in = piece * kPiece < n * kUnit;
+                const uint32_t dst = smem_u32(st) + row0 * kYPitch + piece * kPiece;
+                if (kByAddress) {
+                    if (piece * kPiece < n * kUnit) {
+#pragma unroll
+                        for (int i = 0; i < (kByAddress ? kRounds : 0); ++i)
+                            if (rows[i])
+                                cp_async<kPiece>(dst + i * kRows * kYPitch,
+                                                 rows[i] + static_cast<size_t>(n0) * kUnit);
+                    }
+                } else {
+                    const uint8_t* src = yb + static_cast<size_t>(n0) * kUnit;
+                    const bool in = piece * kPiece < n * kUnit;
 #pragma unroll 8
-                for (int j = row0; j - row0 < count; j += kRows, dst += kRows * kYPitch) {
-                    const int lo = __shfl_sync(0xffffffffu, tk[0], j & 31);
-                    const int hi = __shfl_sync(0xffffffffu, tk[1], j & 31);
-                    const int tj = j & 32 ? hi : lo;
-                    if (in && j < count) cp_async<kPiece>(dst, src + tj * ld);
+                    for (int i = 0; i * kRows < count; ++i) {
+                        const int j = row0 + i * kRows;
+                        const int lo = __shfl_sync(0xffffffffu, tk[0], j & 31);
+                        const int hi = __shfl_sync(0xffffffffu, tk[1], j & 31);
+                        if (in && j < count)
+                            cp_async<kPiece>(dst + i * kRows * kYPitch, src + (j & 32 ? hi : lo) * ld);
+                    }
                 }
                 cp_async_arrive(&full[s]);
             }
@@ -1024,7 +1129,8 @@ __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
     const int g = lane >> 2, t = lane & 3;
     const int wn = (warp % kNWarps) * 32 + 4 * g;   // this lane's outputs within the item
     const int j0 = (warp / kNWarps) * kNI * 8;      // this warp's first token
-    int cached = -1, rank = 0, count = 0, blocks = 0, pitch = 0, term_size = 0;
+    int cached = -1, rank = 0, count = 0, blocks = 0;
+    const int pitch = term_pitch(pl.rp / 32), term_size = kTile * pitch;
     const uint32_t b_step = p.R * 2;
     uint32_t v_base = 0, i_step = 0, q_step = 0;
     size_t out[kNI][2];
@@ -1032,27 +1138,35 @@ __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
     int s = 0;
     uint32_t turn = 0;
     bool ok = true;
+    // the tile's record a tile ahead
+    int4 next = __ldcg(pl.tiles + min(index, pl.max_tiles - 1));
     pdl_wait();
     pdl_launch_dependents();
     for (; left > 0; --left) {
         if (index != cached) {
             // every warp is done with the old tile; a failed wait reaches all
             if (named_bar_any(1, kRingWarps * 32, !ok)) return;
-            const int4 tile = __ldcg(pl.tiles + index);
+            const int4 tile = next;
             cached = index, count = tile.z;
-            rank = tile.x >= 0 ? rank_of(p, tile.x) : 0;
-            blocks = (rank + 31) / 32;
-            pitch = term_pitch(blocks), term_size = kTile * pitch;
+            next = __ldcg(pl.tiles + min(index + 1, pl.max_tiles - 1));
+            const int pieces = pl.rp / 8;   // of 16 bytes, at most 32
+            float fv = 0.0f;
+            int tv = 0;
             if (tid < count) {
-                tok[tid] = __ldcg(pl.perm + tile.y + tid);
-                f[tid] = rank > 0 ? __ldcg(pl.f + tile.y + tid) : 0.0f;
+                tv = __ldcg(pl.perm + tile.y + tid);
+                fv = __ldcg(pl.f + tile.y + tid);
             }
-            const int per_row = blocks * 4;  // 16-byte pieces
-            for (int i = tid; i < terms<BF>() * kTile * per_row; i += kRingWarps * 32) {
-                const int c = i % per_row, j = (i / per_row) % kTile, q = i / (per_row * kTile);
-                *reinterpret_cast<uint4*>(sv + q * term_size + j * pitch + c * 8) =
-                    j < count ? load16_cg(pl.terms + (static_cast<size_t>(q) * p.M + tile.y + j) * pl.rp + c * 8)
-                              : zero4();
+            rank = tile.x >= 0 ? rank_of(p, tile.x) : 0;
+            for (int i = warp; i < terms<BF>() * count && tile.x >= 0; i += kRingWarps) {
+                const int q = i % terms<BF>(), j = i / terms<BF>();
+                if (lane < pieces)
+                    *reinterpret_cast<uint4*>(sv + q * term_size + j * pitch + lane * 8) =
+                        load16_cg(pl.terms + (static_cast<size_t>(q) * p.M + tile.y + j) * pl.rp + lane * 8);
+            }
+            blocks = (rank + 31) / 32;
+            if (tid < count) {
+                tok[tid] = tv;
+                f[tid] = rank > 0 ? fv : 0.0f;
             }
             named_bar_sync(2, kRingWarps * 32);
 #pragma unroll
@@ -1179,19 +1293,19 @@ Layout layout(int64_t M, int64_t K, int64_t L, int64_t R) {
     const bool few = M <= kFewTokens;
     int64_t s;
     if (few) {
-        // K splits: two CTAs per SM over the groups that may appear, at
+        // K splits: two CTAs per SM over the tiles that may appear, at
         // least 16 KB of A each
-        const int64_t groups = std::min(M, L);
-        s = (2 * kSms + groups - 1) / groups;
+        const int64_t tiles = pq2::few_tiles(M, std::min(M, L));
+        s = (2 * kSms + tiles - 1) / tiles;
         s = std::min(s, std::max<int64_t>(1, K * R * 2 / 16384));
         s = std::min<int64_t>(s, kMaxSplits);
     } else {
         // a cluster per tile: one and a half CTAs per SM over the tiles that
-        // are likely, at least 256 columns each, no more than 8 (the portable
-        // cluster size)
+        // are likely, at least 256 columns each; more than 8 CTAs (the portable
+        // cluster size) from 512 columns each
         const int64_t tiles = (M + kTile - 1) / kTile + std::min(L, M / 2);
         s = 1;
-        while (s < 8 && s * tiles * 2 < 3 * kSms && K / (2 * s) >= 256) s *= 2;
+        while (s < 16 && s * tiles * 2 < 3 * kSms && K / (2 * s) >= (s < 8 ? 256 : 512)) s *= 2;
     }
     y.k_split = static_cast<int>(((K + s - 1) / s + 127) / 128 * 128);
     y.splits = few ? static_cast<int>((K + y.k_split - 1) / y.k_split) : static_cast<int>(s);
@@ -1217,22 +1331,34 @@ Layout layout(int64_t M, int64_t K, int64_t L, int64_t R) {
     return y;
 }
 
-template <bool BF, int NT, int YT>
+template <bool BF, int YT>
 cudaError_t run_few(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cudaStream_t st) {
     float* part = reinterpret_cast<float*>(ws + lay.part);
-    cudaError_t e = launch(pq2::lora_shrink_few<BF, NT>,
-                           dim3(lay.splits, static_cast<unsigned>(std::min(p.M, p.L))),
+    const int64_t with = pq2::few_tiles(p.M, std::min(p.M, p.L));
+    cudaError_t e = launch(pq2::lora_shrink_few<BF>, dim3(lay.splits, static_cast<unsigned>(with)),
                            dim3(pq2::kShrinkWarps * 32), 0, st, true, p, part, lay.k_split);
     if (e != cudaSuccess) return e;
     static SmemLimit lim;
-    const size_t smem = static_cast<size_t>(pq2::terms<BF>()) * NT * 8 *
+    const size_t smem = static_cast<size_t>(pq2::terms<BF>()) * pq2::kFewTile *
                         pq2::term_pitch((p.R + 31) / 32) * 2;
-    e = ensure_smem(lim, pq2::lora_expand_few<BF, NT, YT>, smem);
+    e = ensure_smem(lim, pq2::lora_expand_few<BF, YT>, smem);
     if (e != cudaSuccess) return e;
-    const int cols = pq2::kExpandWarps * 32;
-    return launch(pq2::lora_expand_few<BF, NT, YT>,
-                  dim3((p.N + cols - 1) / cols, static_cast<unsigned>(std::min(p.M, p.L + 1))),
-                  dim3(cols), smem, st, true, p, part, lay.splits, vec);
+    // 128 outputs a CTA while the GPU has SMs to spare, 256 beyond
+    const int64_t all = pq2::few_tiles(p.M, std::min(p.M, p.L + 1));
+    const int warps = (p.N + 127) / 128 * all <= 2 * kSms ? pq2::kExpandWarps : pq2::kExpandMaxWarps;
+    return launch(pq2::lora_expand_few<BF, YT>,
+                  dim3((p.N + warps * 32 - 1) / (warps * 32), static_cast<unsigned>(all)),
+                  dim3(warps * 32), smem, st, true, p, part, lay.splits, vec);
+}
+
+template <typename Kern>
+cudaError_t ensure_wide_cluster(SmemLimit& done, Kern kern) {
+    int dev = -1;
+    const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kSmemLimitDevices;
+    if (known && done.bytes[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && known) done.bytes[dev].store(1, std::memory_order_release);
+    return e;
 }
 
 template <bool BF, int RPW, int WN>
@@ -1240,12 +1366,19 @@ cudaError_t run_shrink(const LoraParams& p, const pq2::Plan& pl, const Layout& l
     auto kern = pq2::lora_shrink_tiles<BF, RPW, WN>;
     static SmemLimit lim;
     const size_t r16 = static_cast<size_t>((p.R + 16 * RPW - 1) / (16 * RPW) * (16 * RPW));
-    const size_t smem = std::max((kTile + r16) * 128 * pq2::shrink_stages<RPW, WN>(), kTile * (r16 + 4) * 4);
-    const cudaError_t e = ensure_smem(lim, kern, smem);
+    const size_t inbox = static_cast<size_t>(lay.splits) * ((kTile + lay.splits - 1) / lay.splits) * r16 * 4;
+    const size_t smem = (kTile + r16) * 128 * pq2::shrink_stages<RPW, WN>() + inbox;
+    cudaError_t e = ensure_smem(lim, kern, smem);
     if (e != cudaSuccess) return e;
+    if (lay.splits > 8) {
+        // clusters past the portable size are asked for once per kernel
+        static SmemLimit wide;
+        e = ensure_wide_cluster(wide, kern);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(lay.splits * lay.max_tiles));
-    cfg.blockDim = dim3(pq2::kShrinkWarps * 32);
+    cfg.blockDim = dim3((pq2::kShrinkWarps + pq2::kShrinkLoaders) * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -1299,8 +1432,7 @@ SmemLimit g_plan_smem;  // one for the kernel: run() has several instantiations
 template <bool BF, int YT>
 cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cudaStream_t st,
                 const DeviceInfo& dev) {
-    if (p.M <= 8) return run_few<BF, 1, YT>(p, lay, ws, vec, st);
-    if (p.M <= kFewTokens) return run_few<BF, 4, YT>(p, lay, ws, vec, st);
+    if (p.M <= kFewTokens) return run_few<BF, YT>(p, lay, ws, vec, st);
     pq2::Plan pl = {};
     pl.terms = reinterpret_cast<uint16_t*>(ws + lay.terms);
     pl.f = reinterpret_cast<float*>(ws + lay.f);

@@ -112,11 +112,18 @@ SHAPES = [
     (700, 256, 515, 8, 2, "bf16", "f32", dict(ids="runs", offset=3)),
     (1500, 512, 384, 40, 700, "f16", "f32", {}),
     (2100, 128, 130, 16, 5, "f16", "f32", dict(ids="runs")),
-    # whole 16-byte rows of y and more than 32 tokens: the copy ring
+    (128, 640, 301, 16, 3, "f16", "f32", {}),
+    (128, 128, 40, 8, 128, "f16", "f32", {}),
+    (100, 1664, 260, 40, 2, "bf16", "f32", dict(ids="runs")),
+    (129, 640, 300, 16, 3, "f16", "f32", {}),
+    (4097, 64, 36, 8, 3, "f16", "f32", {}),
+    (9000, 64, 36, 8, 1000, "f16", "f32", {}),
+    # whole 16-byte rows of y and more than 128 tokens: the copy ring
     (40, 5120, 5120, 32, 30, "bf16", "f32", {}),
+    (140, 5120, 5120, 32, 30, "bf16", "f32", {}),
     (200, 2048, 1000, 256, 4, "bf16", "bf16", {}),
-    (97, 640, 2056, 136, 3, "f16", "bf16", dict(ld_y=2064)),
-    (97, 640, 2052, 136, 3, "f16", "f32", dict(ld_y=2060)),
+    (197, 640, 2056, 136, 3, "f16", "bf16", dict(ld_y=2064)),
+    (197, 640, 2052, 136, 3, "f16", "f32", dict(ld_y=2060)),
     (300, 72, 4, 8, 2, "f16", "f32", {}),
     (1025, 1000, 1028, 48, 2, "bf16", "f32", dict(ranks=False, ids="runs")),
     (129, 6144, 700, 64, 1, "f16", "f32", dict(scales=False)),
@@ -146,7 +153,7 @@ def test_in_place_equals_out_of_place(M, N):
 
 
 @pytest.mark.parametrize("N", [77, 160])
-@pytest.mark.parametrize("M", [1, 31, 32, 33, 300])
+@pytest.mark.parametrize("M", [1, 31, 32, 33, 128, 129, 300])
 def test_a_batch_without_adapters_is_a_copy(M, N):
     from gemm_pq2_ternary_gb300 import binding as pq2
     p = _problem(M, 256, N, 8, 2, "f16", "f32", seed=1, ids=[-1] * M)
@@ -157,7 +164,7 @@ def test_a_batch_without_adapters_is_a_copy(M, N):
 
 
 @pytest.mark.parametrize("N", [77, 160])
-@pytest.mark.parametrize("M", [3, 90])
+@pytest.mark.parametrize("M", [3, 90, 200])
 def test_every_rank_zero_is_a_copy(M, N):
     from gemm_pq2_ternary_gb300 import binding as pq2
     p = _problem(M, 256, N, 8, 2, "bf16", "bf16", seed=1, ids=[0] * M)
@@ -167,7 +174,7 @@ def test_every_rank_zero_is_a_copy(M, N):
     assert torch.equal(p["out"], p["y"])
 
 
-@pytest.mark.parametrize("M", [5, 100])
+@pytest.mark.parametrize("M", [5, 100, 300])
 def test_an_id_past_the_adapters_is_reported_and_passes_through(M):
     from gemm_pq2_ternary_gb300 import binding as pq2
     p = _problem(M, 256, 64, 8, 2, "f16", "f32", seed=2, ids=[m % 3 for m in range(M)])
@@ -199,7 +206,7 @@ def test_the_same_bits_whatever_the_token_order(M):
 def test_small_and_large_intermediates(ty, scale):
     # v far outside fp16's range of 16-bit terms: the token's power of two
     from gemm_pq2_ternary_gb300 import binding as pq2
-    for M in (2, 70):
+    for M in (2, 70, 140):
         p = _problem(M, 512, 96, 16, 2, ty, "f32", seed=4, ranks=False)
         p["A"] = (p["A"].float() * (scale if ty == "bf16" else min(scale, 2.0 ** 12))).to(T[ty])
         if ty == "f16" and scale > 1:
@@ -211,7 +218,7 @@ def test_small_and_large_intermediates(ty, scale):
 
 def test_on_another_stream_after_a_producer():
     from gemm_pq2_ternary_gb300 import binding as pq2
-    for M in (4, 128):
+    for M in (4, 100, 228):
         p = _problem(M, 640, 256, 16, 3, "f16", "f32", seed=8)
         _call(pq2, p)
         torch.cuda.synchronize()
