@@ -193,6 +193,15 @@ __device__ __forceinline__ bool mbar_suspend_bounded(uint64_t* bar, uint32_t par
     }
 }
 
+// The same, for phases that are mostly complete when asked for: all lanes try
+// at once and agree by a vote, and only if that fails lane 0 polls (its branch
+// and the shuffle after it take about 300 cycles in a short loop).
+__device__ __forceinline__ bool mbar_ready_warp(uint64_t* bar, uint32_t parity, const DevCtl& ctl,
+                                                volatile int* abort_flag = nullptr) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return mbar_wait_warp(bar, parity, ctl, abort_flag);
+}
+
 // Warp-wide suspending wait (lane 0 waits in try_wait, the warp then
 // synchronises).  All 32 lanes must call it; the result is warp-uniform.
 __device__ __forceinline__ bool mbar_suspend_warp(uint64_t* bar, uint32_t parity,

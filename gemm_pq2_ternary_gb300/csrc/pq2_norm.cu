@@ -376,7 +376,7 @@ __global__ void __launch_bounds__((kRingMaxWarps + 1) * 32, 1)
         int i = 0, s = 0;
         uint32_t turn = 0;  // times the ring has gone round
         for (; i < count; ++i) {
-            if (turn > 0 && !mbar_wait_warp(&empty[s], (turn - 1) & 1, p.ctl, abort_flag)) break;
+            if (turn > 0 && !mbar_ready_warp(&empty[s], (turn - 1) & 1, p.ctl, abort_flag)) break;
             if (i != p.ctl.debug_skip_stage) {  // else withheld (timeout test)
                 if (lane == 0) mbar_arrive_expect_tx(&full[s], y_bytes + r_bytes + g_bytes);
                 __syncwarp();
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__((kRingMaxWarps + 1) * 32, 1)
         // the last copies land before the CTA ends, whatever the consumers do
         for (int k = max(0, i - stages); k < i; ++k)
             if (k != p.ctl.debug_skip_stage)
-                mbar_wait_warp(&full[k % stages], static_cast<uint32_t>(k / stages) & 1, p.ctl);
+                mbar_ready_warp(&full[k % stages], static_cast<uint32_t>(k / stages) & 1, p.ctl);
         return;
     }
     if (!p.weights_static) pdl_wait();
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__((kRingMaxWarps + 1) * 32, 1)
     uint32_t turn = group / stages;
     for (int i = group; i < count; i += groups) {
         const long long row = blockIdx.x + static_cast<long long>(i) * gridDim.x;
-        const bool ok = mbar_wait_warp(&full[s], turn & 1, p.ctl, abort_flag);
+        const bool ok = mbar_ready_warp(&full[s], turn & 1, p.ctl, abort_flag);
         if (!ok) *abort_flag = 1;
         const uint8_t* st = ring + static_cast<size_t>(s) * stage_bytes;
         float y[kRingVpt][4], r[kRingVpt][4];
@@ -526,13 +526,17 @@ cudaError_t route(const NormParams& p, cudaStream_t st, const DeviceInfo& dev) {
     if (vec && H > 512 && H <= kRingMaxH && p.M >= kRingMinRows * sms) {
         // whole warps of 16 values a thread, as many groups as fit 23 warps
         const int threads = (H / 4 + pq2::kRingVpt * 32 - 1) / (pq2::kRingVpt * 32) * 32;
-        const int groups = std::min(pq2::kRingMaxGroups, pq2::kRingMaxWarps * 32 / threads);
+        int groups = std::min(pq2::kRingMaxGroups, pq2::kRingMaxWarps * 32 / threads);
         auto bytes = [&](int type) { return H * (type == PQ2_F32 ? 4 : 2); };
         const int stage = bytes(p.r_type) + (kAfter ? bytes(p.y_type) : 0) +
                           (kAfter && p.gate && p.ld_gate != 0 ? bytes(p.gate_type) : 0);
         const int room = dev.max_smem_optin - 4096 - 8 * H;
-        const int stages = std::min(pq2::kRingMaxStages, room / stage);
+        int stages = std::min(pq2::kRingMaxStages, room / stage);
         if (stages >= 3) {
+            // whole turns of the groups: a stage is always the same group's,
+            // which sees each phase of its barrier (a parity says no more)
+            groups = std::min(groups, stages);
+            stages -= stages % groups;
             const bool full = H == threads * pq2::kRingVpt * 4;
             auto kern = full ? pq2::norm_ring_kernel<kAfter, true> : pq2::norm_ring_kernel<kAfter, false>;
             static SmemLimit lim[2];
