@@ -39,6 +39,7 @@
 // out (8 N bytes per token against 2 K + 2 R (K + N) / tokens).
 #include <algorithm>
 #include <cstddef>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -814,7 +815,7 @@ __global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
         int s = 0;
         uint32_t turn = 0;
         for (int step = 0; step < steps; ++step) {
-            if (turn > 0 && !mbar_wait_warp(&empty[s], (turn - 1) & 1, p.ctl, abort_flag)) break;
+            if (turn > 0 && !mbar_ready_warp(&empty[s], (turn - 1) & 1, p.ctl, abort_flag)) break;
             if (step != p.ctl.debug_skip_stage) {  // else withheld (timeout test)
                 const uint32_t st = dst0 + s * stage_bytes;
                 const int k = step * kStageK;
@@ -852,7 +853,7 @@ __global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
         int s = 0;
         uint32_t turn = 0;
         for (int step = 0; step < steps; ++step) {
-            if (!mbar_wait_warp(&full[s], turn & 1, p.ctl, abort_flag)) {
+            if (!mbar_ready_warp(&full[s], turn & 1, p.ctl, abort_flag)) {
                 *abort_flag = 1;   // the host reads the error; v is not used
                 break;
             }
@@ -998,27 +999,103 @@ __global__ void __launch_bounds__(kExpandWarps * 32, 3)
 
 // The same over a ring in shared memory.  One CTA per SM takes a contiguous
 // range of the items (tile, kNB outputs), so that v's terms rarely change;
-// producer warps keep the next items' y and B on their way while the consumer
-// warps multiply, add and store.  y comes by asynchronous copies of kPiece
-// bytes a thread (a warp per token row; bulk copies of 512-byte rows topped
-// out at one per 46 ns and SM, half the rate needed), B by one bulk copy: kNB
-// rows of B are contiguous.  A consumer warp owns 32 outputs and kNI groups
-// of 8 tokens.  Token rows of y are 16 bytes longer in shared memory, so that
-// the 4 tokens of an access lie in different banks.
-constexpr int kRingWarps = 16;      // consumers
+// producer warps keep the next items' y and B on their way while groups of
+// consumer warps take the items in turn.  y comes by asynchronous copies of
+// kPiece bytes a thread (a warp per token row; bulk copies of 512-byte rows
+// topped out at one per 46 ns and SM, half the rate needed), B by one bulk
+// copy: kNB rows of B are contiguous.  A group has a warp per 32 outputs and
+// goes over the tile's tokens by 32: eight accumulators a warp and three
+// items at once, because a dependent mma.sync returns after some 150 cycles
+// here (one item at a time took 3600 cycles for 64 tokens x 128 outputs of
+// rank 64, against 2800 for its bytes).  Token rows of y are 16 bytes longer
+// in shared memory, so that the 4 tokens of an access lie in different banks.
+constexpr int kRingWarps = 12;      // consumers: 128 registers a thread
 constexpr int kRingLoaders = 4;     // producer warps
 constexpr int kRingMaxStages = 8;
 
+// One item's product for a warp: 32 outputs x NI groups of 8 tokens.  bp: this
+// lane's first row of B (shared-memory address, rows b_step apart), vp: its
+// terms (groups i_step, terms q_step apart).  A column past the tile's last
+// token holds anything and is not stored.
+template <bool BF, int NI>
+__device__ __forceinline__ void ring_product(float (&acc)[2][NI][4], uint32_t bp, uint32_t b_step,
+                                             uint32_t vp, uint32_t i_step, uint32_t q_step,
+                                             int blocks, int rank) {
+    const int t = threadIdx.x & 3;
+    for (int blk = 0; blk < blocks; ++blk, bp += 64, vp += 64) {
+        uint4 b[4];
+        if (blk * 32 + 32 <= rank) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = lds_v4(bp + i * b_step);
+        } else {
+            const int left = rank - blk * 32 - 8 * t;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                b[i] = left > 0 ? keep_first(lds_v4(bp + i * b_step), left) : zero4();
+        }
+#pragma unroll
+        for (int q = 0; q < terms<BF>(); ++q) {
+            uint4 c[NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) c[i] = lds_v4(vp + q * q_step + i * i_step);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                mma16816<BF>(acc[0][i], b[0].x, b[1].x, b[0].y, b[1].y, c[i].x, c[i].y);
+                mma16816<BF>(acc[1][i], b[2].x, b[3].x, b[2].y, b[3].y, c[i].x, c[i].y);
+            }
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                mma16816<BF>(acc[0][i], b[0].z, b[1].z, b[0].w, b[1].w, c[i].z, c[i].w);
+                mma16816<BF>(acc[1][i], b[2].z, b[3].z, b[2].w, b[3].w, c[i].z, c[i].w);
+            }
+        }
+    }
+}
+
+// y' = y + f acc of NI groups of tokens, y from shared memory (sy: this lane's
+// first), y' to global memory.  f, row: scale and start of y' of the lane's
+// first token; n: its first output; left: tokens from the first group on.
+template <int YT, int NI, int kYPitch, bool kWhole>
+__device__ __forceinline__ void ring_store(const pq2h::LoraParams& p, const float (&acc)[2][NI][4],
+                                           uint32_t sy, const float* f, const long long* row, int n,
+                                           int left, bool vec) {
+    const int t = threadIdx.x & 3;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (!kWhole && i * 8 + 2 * t + h >= left) continue;
+            const uint32_t a = sy + (i * 8 + h) * kYPitch;
+            float4 o;
+            if constexpr (YT == PQ2_F32) {
+                const uint4 u = lds_v4(a);
+                o = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                                __uint_as_float(u.w));
+            } else {
+                uint2 u;
+                asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(u.x), "=r"(u.y) : "r"(a));
+                o = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                                __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+            }
+            const float s = f[i * 8 + h];
+            o.x = fmaf(s, acc[0][i][h], o.x);
+            o.y = fmaf(s, acc[0][i][2 + h], o.y);
+            o.z = fmaf(s, acc[1][i][h], o.z);
+            o.w = fmaf(s, acc[1][i][2 + h], o.w);
+            y_store<YT>(p, row[i * 8 + h] + n, kWhole ? 4 : p.N - n, kWhole || vec, o);
+        }
+}
+
 template <bool BF, int YT, int kNB, int kPiece>
 __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
-    lora_expand_ring(pq2h::LoraParams p, Plan pl, int stages, int stage_bytes, int term_bytes) {
+    lora_expand_ring(pq2h::LoraParams p, Plan pl, int groups, int stages, int stage_bytes,
+                     int term_bytes) {
     constexpr int kUnit = YT == PQ2_F32 ? 4 : 2;
     constexpr int kYPitch = kNB * kUnit + 16;
-    constexpr int kNWarps = kNB / 32;                    // warps side by side along n
-    constexpr int kNI = kTile / 8 / (kRingWarps / kNWarps);
+    constexpr int kGroupWarps = kNB / 32;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t full[kRingMaxStages], empty[kRingMaxStages];
-    __shared__ int tok[kTile];
+    __shared__ long long row[kTile];   // start of each token's y'
     __shared__ float f[kTile];
     __shared__ int abort_word;
     volatile int* abort_flag = &abort_word;
@@ -1028,7 +1105,7 @@ __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
     if (tid == 0) {
         for (int s = 0; s < stages; ++s) {
             mbar_init(&full[s], kRingLoaders * 32 + 1);
-            mbar_init(&empty[s], kRingWarps);
+            mbar_init(&empty[s], kGroupWarps);
         }
         abort_word = 0;
         fence_mbar_init();
@@ -1080,7 +1157,7 @@ __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
             const int n0 = nb * kNB, n = min(kNB, p.N - n0);
             if (++nb == nblocks) nb = 0, ++index;
             if (rank == 0 && in_place) continue;   // nothing to read or write
-            if (turn > 0 && !mbar_wait_warp(&empty[s], (turn - 1) & 1, p.ctl, abort_flag)) break;
+            if (turn > 0 && !mbar_ready_warp(&empty[s], (turn - 1) & 1, p.ctl, abort_flag)) break;
             if (issued != p.ctl.debug_skip_stage) {  // else withheld (timeout test)
                 uint8_t* st = ring + static_cast<size_t>(s) * stage_bytes;
                 if (pt == 0) {
@@ -1120,22 +1197,23 @@ __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
         // the last copies land before the CTA ends, whatever the consumers do
         for (int k = max(0, issued - stages); k < issued; ++k)
             if (k != p.ctl.debug_skip_stage)
-                mbar_wait_warp(&full[k % stages], static_cast<uint32_t>(k / stages) & 1, p.ctl);
+                mbar_ready_warp(&full[k % stages], static_cast<uint32_t>(k / stages) & 1, p.ctl);
         cp_async_wait<0>();
         pdl_wait();
         return;
     }
 
     const int g = lane >> 2, t = lane & 3;
-    const int wn = (warp % kNWarps) * 32 + 4 * g;   // this lane's outputs within the item
-    const int j0 = (warp / kNWarps) * kNI * 8;      // this warp's first token
+    const int group = warp / kGroupWarps;
+    const int wn = (warp % kGroupWarps) * 32 + 4 * g;   // this lane's outputs within the item
     int cached = -1, rank = 0, count = 0, blocks = 0;
     const int pitch = term_pitch(pl.rp / 32), term_size = kTile * pitch;
-    const uint32_t b_step = p.R * 2;
-    uint32_t v_base = 0, i_step = 0, q_step = 0;
-    size_t out[kNI][2];
-    float fs[kNI][2];
-    int s = 0;
+    const uint32_t b_step = p.R * 2, i_step = 8 * pitch * 2, q_step = term_size * 2;
+    const uint32_t ring_base = smem_u32(ring);
+    const uint32_t b_off = kTile * kYPitch + (wn * p.R + 8 * t) * 2;
+    const uint32_t y_off = 2 * t * kYPitch + wn * kUnit;
+    const uint32_t v_base = smem_u32(sv + g * pitch + 8 * t);
+    int s = 0, turn_of = 0;      // stage, and the group whose turn it is
     uint32_t turn = 0;
     bool ok = true;
     // the tile's record a tile ahead
@@ -1164,105 +1242,55 @@ __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
                         load16_cg(pl.terms + (static_cast<size_t>(q) * p.M + tile.y + j) * pl.rp + lane * 8);
             }
             blocks = (rank + 31) / 32;
-            if (tid < count) {
-                tok[tid] = tv;
+            if (tid < kTile) {
+                row[tid] = tv * p.ld_out;
                 f[tid] = rank > 0 ? fv : 0.0f;
             }
             named_bar_sync(2, kRingWarps * 32);
-#pragma unroll
-            for (int i = 0; i < kNI; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int j = j0 + i * 8 + 2 * t + h;
-                    out[i][h] = j < count ? static_cast<size_t>(tok[j]) * p.ld_out : 0;
-                    fs[i][h] = j < count ? f[j] : 0.0f;
-                }
-            // shared-memory addresses of this lane's terms
-            v_base = smem_u32(sv + (j0 + g) * pitch + 8 * t);
-            i_step = 8 * pitch * 2, q_step = term_size * 2;
         }
         const int n = nb * kNB + wn;
         if (++nb == nblocks) nb = 0, ++index;
         if (rank == 0 && in_place) continue;
-        if (ok) ok = mbar_wait_warp(&full[s], turn & 1, p.ctl, abort_flag);
+        const int stage = s;
+        const uint32_t parity = turn & 1;
+        const bool mine = turn_of == group;
+        if (++s == stages) s = 0, ++turn;
+        if (++turn_of == groups) turn_of = 0;
+        if (!mine) continue;
+        if (ok) ok = mbar_ready_warp(&full[stage], parity, p.ctl, abort_flag);
         if (!ok) {
             *abort_flag = 1;
             continue;   // to the next tile's barrier
         }
-        const uint8_t* st = ring + static_cast<size_t>(s) * stage_bytes;
-        const uint8_t* sy = st;
-        const uint16_t* sb = reinterpret_cast<const uint16_t*>(st + kTile * kYPitch);
-        float acc[2][kNI][4];
+        const uint32_t st = ring_base + stage * stage_bytes;
+        // tokens by 32, or by one group of 8
+        auto part = [&](auto groups, int j) {
+            constexpr int NI = decltype(groups)::value;
+            float acc[2][NI][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < kNI; ++i)
+                for (int i = 0; i < NI; ++i)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) acc[h][i][c] = 0.0f;
-        if (j0 < count) {
-            // every group of tokens, also one past the tile's last (its
-            // columns are not stored): no branch between the instructions
-            uint32_t bp = smem_u32(sb + wn * p.R + 8 * t);
-            uint32_t vp = v_base;
-            for (int blk = 0; blk < blocks; ++blk, bp += 64, vp += 64) {
-                uint4 b[4], c[terms<BF>()][kNI];
-                const bool in = blk * 32 + 8 * t < rank;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) b[i] = in ? lds_v4(bp + i * b_step) : zero4();
-#pragma unroll
-                for (int q = 0; q < terms<BF>(); ++q)
-#pragma unroll
-                    for (int i = 0; i < kNI; ++i) c[q][i] = lds_v4(vp + q * q_step + i * i_step);
-                if (blk * 32 + 32 > rank) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) b[i] = keep_first(b[i], rank - blk * 32 - 8 * t);
-                }
-#pragma unroll
-                for (int q = 0; q < terms<BF>(); ++q) {
-#pragma unroll
-                    for (int i = 0; i < kNI; ++i) {
-                        mma16816<BF>(acc[0][i], b[0].x, b[1].x, b[0].y, b[1].y, c[q][i].x, c[q][i].y);
-                        mma16816<BF>(acc[1][i], b[2].x, b[3].x, b[2].y, b[3].y, c[q][i].x, c[q][i].y);
-                    }
-#pragma unroll
-                    for (int i = 0; i < kNI; ++i) {
-                        mma16816<BF>(acc[0][i], b[0].z, b[1].z, b[0].w, b[1].w, c[q][i].z, c[q][i].w);
-                        mma16816<BF>(acc[1][i], b[2].z, b[3].z, b[2].w, b[3].w, c[q][i].z, c[q][i].w);
-                    }
-                }
-            }
+                    for (int c = 0; c < 4; ++c) acc[h][i][c] = 0.0f;
+            ring_product<BF, NI>(acc, st + b_off, b_step, v_base + (j / 8) * i_step, i_step, q_step,
+                                 blocks, rank);
+            const uint32_t sy = st + y_off + j * kYPitch;
+            const float* fj = f + j + 2 * t;
+            const long long* rj = row + j + 2 * t;
+            if (kPiece == 16 && count - j >= NI * 8 && n - wn + kNB <= p.N)
+                ring_store<YT, NI, kYPitch, true>(p, acc, sy, fj, rj, n, count - j, true);
+            else if (n < p.N)
+                ring_store<YT, NI, kYPitch, false>(p, acc, sy, fj, rj, n, count - j, kPiece == 16);
+        };
+        for (int j = 0; j < count; j += 32) {
+            if (count - j > 8)
+                part(std::integral_constant<int, 4>{}, j);
+            else
+                part(std::integral_constant<int, 1>{}, j);
         }
-        float4 y[kNI][2];
-#pragma unroll
-        for (int i = 0; i < kNI; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint8_t* a = sy + (j0 + i * 8 + 2 * t + h) * kYPitch + wn * kUnit;
-                if constexpr (YT == PQ2_F32) {
-                    y[i][h] = *reinterpret_cast<const float4*>(a);
-                } else {
-                    const uint2 u = *reinterpret_cast<const uint2*>(a);
-                    y[i][h] = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                                          __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-                }
-            }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);   // the stage is in registers
-        if (++s == stages) s = 0, ++turn;
-        if (n < p.N) {
-#pragma unroll
-            for (int i = 0; i < kNI; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (j0 + i * 8 + 2 * t + h >= count) continue;
-                    float4 o = y[i][h];
-                    o.x = fmaf(fs[i][h], acc[0][i][h], o.x);
-                    o.y = fmaf(fs[i][h], acc[0][i][2 + h], o.y);
-                    o.z = fmaf(fs[i][h], acc[1][i][h], o.z);
-                    o.w = fmaf(fs[i][h], acc[1][i][2 + h], o.w);
-                    y_store<YT>(p, out[i][h] + n, p.N - n, kPiece == 16, o);
-                }
-        }
+        if (lane == 0) mbar_arrive(&empty[stage]);
     }
 }
 
@@ -1408,12 +1436,15 @@ template <bool BF, int YT, int kNB, int kPiece>
 cudaError_t run_ring(const LoraParams& p, const pq2::Plan& pl, int stages, int stage_bytes,
                      int term_bytes, cudaStream_t st, const DeviceInfo& dev) {
     auto kern = pq2::lora_expand_ring<BF, YT, kNB, kPiece>;
+    // whole turns of the groups (see the kernel)
+    const int groups = std::min(pq2::kRingWarps / (kNB / 32), stages);
+    stages -= stages % groups;
     static SmemLimit lim;
     const size_t smem = static_cast<size_t>(term_bytes) + static_cast<size_t>(stages) * stage_bytes;
     const cudaError_t e = ensure_smem(lim, kern, smem);
     if (e != cudaSuccess) return e;
     return launch(kern, dim3(dev.num_sms), dim3((pq2::kRingWarps + pq2::kRingLoaders) * 32), smem, st,
-                  true, p, pl, stages, stage_bytes, term_bytes);
+                  true, p, pl, groups, stages, stage_bytes, term_bytes);
 }
 
 // 128 outputs an item where three stages fit beside v's terms (they take two
