@@ -315,6 +315,15 @@ def _row(t, shape, name):
     return t.data_ptr(), ty, ld
 
 
+def _vec(t, n, dt, name):
+    """Pointer of a contiguous CUDA vector of n elements."""
+    if t.dtype is not dt or t.shape != (n,):
+        raise ValueError(f"{name}: expected {dt} of shape ({n},), got {t.dtype} {tuple(t.shape)}")
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
 def _weight(w, H, name):
     """(pointer, element type) of a contiguous CUDA vector [H]."""
     ty = _TYPE.get(w.dtype)
@@ -383,30 +392,25 @@ def pq2_lora_add(x, A, B, ids, y_in, y_out, workspace, ranks=None, scales=None, 
     """y_out[m] = y_in[m] + scales[l] * B[l] (A[l] x[m]) with l = ids[m]
     (l < 0: y_in[m]).  x [M, K], A [L, R, K], B [L, N, R] fp16 or bf16; ids
     int32 [M]; ranks int32 [L], scales fp32 [L] or None; y fp32 or bf16 [M, N]."""
-    M, K = x.shape
+    shape = x.shape
+    M, K = shape
     L, N, R = B.shape
-    if A.shape != (L, R, K) or ids.shape != (M,):
-        raise ValueError(f"shapes: x {tuple(x.shape)}, A {tuple(A.shape)}, B {tuple(B.shape)}, "
-                         f"ids {tuple(ids.shape)}")
-    xp, xt, xl = _row(x, x.shape, "x")
-    if A.dtype != x.dtype or B.dtype != x.dtype:
+    if A.shape != (L, R, K):
+        raise ValueError(f"shapes: x {tuple(shape)}, A {tuple(A.shape)}, B {tuple(B.shape)}")
+    xp, xt, xl = _row(x, shape, "x")
+    if A.dtype is not x.dtype or B.dtype is not x.dtype:
         raise ValueError("A and B: expected x's type")
-    _dtype(ids, torch.int32, "ids")
-    if ranks is not None:
-        _dtype(ranks, torch.int32, "ranks")
-        if ranks.shape != (L,):
-            raise ValueError("ranks: one value per adapter")
-    if scales is not None:
-        _dtype(scales, torch.float32, "scales")
-        if scales.shape != (L,):
-            raise ValueError("scales: one value per adapter")
-    ip, it, il = _row(y_in, (M, N), "y_in")
-    op, ot, ol = _row(y_out, (M, N), "y_out")
+    yshape = (M, N)
+    ip, it, il = _row(y_in, yshape, "y_in")
+    op, ot, ol = (ip, it, il) if y_out is y_in else _row(y_out, yshape, "y_out")
     if it != ot:
         raise ValueError("y_out: expected y_in's type")
     wp, wb = _ws(workspace)
-    _check(_lib.pq2_lora_add(xp, xl, _ptr(A), _ptr(B), xt, _ptr(ids), _ptr(ranks), _ptr(scales), ip,
-                             il, op, ol, it, M, N, K, L, R, wp, wb, _stream(stream)), "pq2_lora_add")
+    _check(_lib.pq2_lora_add(xp, xl, _ptr(A), _ptr(B), xt, _vec(ids, M, torch.int32, "ids"),
+                             None if ranks is None else _vec(ranks, L, torch.int32, "ranks"),
+                             None if scales is None else _vec(scales, L, torch.float32, "scales"),
+                             ip, il, op, ol, it, M, N, K, L, R, wp, wb, _stream(stream)),
+           "pq2_lora_add")
 
 
 def pq2_verify_workspace_bytes(B, rows, V) -> int:
@@ -432,17 +436,15 @@ def pq2_verify_drafts(logits, row_start, drafts, q, u, e, temperature, accepted,
     qp, qt, ql = (None, PQ2_F32, 0) if q is None else _row(q, logits.shape, "q")
     if lt or et or qt:
         raise ValueError("logits, q and e: expected torch.float32")
-    for t, n, dt, name in ((row_start, nb + 1, torch.int32, "row_start"),
-                           (drafts, rows, torch.int32, "drafts"), (u, rows, torch.float32, "u"),
-                           (temperature, nb, torch.float32, "temperature"),
-                           (accepted, nb, torch.int32, "accepted"),
-                           (tokens, rows, torch.int32, "tokens")):
-        if t.dtype != dt or t.shape != (n,):
-            raise ValueError(f"{name}: expected {dt} of shape ({n},), got {t.dtype} {tuple(t.shape)}")
+    i32, f32 = torch.int32, torch.float32
     wp, wb = _ws(workspace)
-    _check(_lib.pq2_verify_drafts(lp, ll, _ptr(row_start), _ptr(drafts), qp, ql, _ptr(u), ep, el,
-                                  _ptr(temperature), _ptr(accepted), _ptr(tokens), nb, rows, V, wp,
-                                  wb, _stream(stream)), "pq2_verify_drafts")
+    _check(_lib.pq2_verify_drafts(lp, ll, _vec(row_start, nb + 1, i32, "row_start"),
+                                  _vec(drafts, rows, i32, "drafts"), qp, ql,
+                                  _vec(u, rows, f32, "u"), ep, el,
+                                  _vec(temperature, nb, f32, "temperature"),
+                                  _vec(accepted, nb, i32, "accepted"),
+                                  _vec(tokens, rows, i32, "tokens"), nb, rows, V, wp, wb,
+                                  _stream(stream)), "pq2_verify_drafts")
 
 
 def pq2_group_dots(op, qp, T, codes, dots, workspace=None, stream=None):

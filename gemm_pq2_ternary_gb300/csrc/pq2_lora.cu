@@ -1436,8 +1436,11 @@ template <bool BF, int YT, int kNB, int kPiece>
 cudaError_t run_ring(const LoraParams& p, const pq2::Plan& pl, int stages, int stage_bytes,
                      int term_bytes, cudaStream_t st, const DeviceInfo& dev) {
     auto kern = pq2::lora_expand_ring<BF, YT, kNB, kPiece>;
-    // whole turns of the groups (see the kernel)
-    const int groups = std::min(pq2::kRingWarps / (kNB / 32), stages);
+    // whole turns of the groups (see the kernel).  128 outputs: two stages a
+    // group where they are few (4096 tokens of rank 64: two groups on four
+    // stages 149 us, three on three 158); 64 outputs, for ranks above 64 or so:
+    // as many groups as stages (rank 128: 167 us against 189 with two)
+    const int groups = kNB == 128 ? std::min(3, stages / 2) : std::min(6, stages);
     stages -= stages % groups;
     static SmemLimit lim;
     const size_t smem = static_cast<size_t>(term_bytes) + static_cast<size_t>(stages) * stage_bytes;

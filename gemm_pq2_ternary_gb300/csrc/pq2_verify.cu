@@ -17,10 +17,10 @@
 //   verify_stats_kernel  splits every row into pieces of kPiece values; a
 //       thread holds its values in registers, so maximum and sum of
 //       exponentials take one read and no rescaling within a piece.
-//   verify_pick_kernel   the same pieces of each sequence's chosen row; every
-//       CTA joins the pieces' statistics of the sequence's rows, finds the
-//       first refusal (the same arithmetic in each CTA) and reduces its piece
-//       to one 64-bit key (score bits, then lowest index first).  atomicMax
+//   verify_pick_kernel   spans of each sequence's chosen row; every CTA joins
+//       the pieces' statistics of the sequence's rows, finds the first refusal
+//       (the same arithmetic in each CTA) and reduces its span to one 64-bit
+//       key (score bits, then lowest index first).  atomicMax
 //       joins the keys: the maximum does not depend on the order.  The last
 //       CTA of a sequence writes the result.
 #include <algorithm>
@@ -34,8 +34,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kVecs = 4;                        // 16-byte vectors per thread
-constexpr int kPiece = kThreads * kVecs * 4;    // values of a row per CTA
+constexpr int kVecs = 4;                            // 16-byte vectors per thread at once
+constexpr int kStatVecs = 8;                        // of stats (4: 5 us more for 256 rows)
+constexpr int kPiece = kThreads * kStatVecs * 4;    // values of a row per CTA of stats
+constexpr int kPickPiece = kThreads * kVecs * 4;    // and per round of a CTA of pick
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
@@ -92,9 +94,9 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(pq2h::VerifyPara
     pdl_launch_dependents();
     const float* l = p.logits + row * p.ld_logits;
     const int e0 = chunk * kPiece - lead(l);
-    float v[kVecs][4];
+    float v[kStatVecs][4];
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
+    for (int i = 0; i < kStatVecs; ++i) {
         const float4 f = load4(l, e0 + (i * kThreads + tid) * 4, p.V, true, neg_inf());
         v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
     }
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(pq2h::VerifyPara
     float m = neg_inf();
     int at = INT_MAX;
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i)
+    for (int i = 0; i < kStatVecs; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (v[i][j] > m) {
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(pq2h::VerifyPara
     float s = 0.0f;
     if (m > neg_inf()) {
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i)
+        for (int i = 0; i < kStatVecs; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) s += ex2((v[i][j] - m) * c);
     }
@@ -157,51 +159,66 @@ __device__ __forceinline__ unsigned long long key_of(float score, int at) {
                         : 0ull;
 }
 
-__global__ void __launch_bounds__(kThreads) verify_pick_kernel(pq2h::VerifyParams p) {
+// What a warp needs to decide one row's draft; none of it comes from
+// verify_stats_kernel.
+struct RowTest {
+    bool last;          // no draft to test: the sequence ends here
+    int d;
+    float l, q, u;      // its logit, the drafter's probability, the uniform
+};
+__device__ __forceinline__ RowTest row_test(const pq2h::VerifyParams& p, int row, int r1,
+                                            bool greedy) {
+    RowTest r = {true, 0, 0.0f, 1.0f, 0.0f};
+    if (row >= r1) return r;
+    r.d = __ldcg(p.drafts + row);
+    r.last = row == r1 - 1 || r.d < 0 || r.d >= p.V;
+    if (!r.last && !greedy) {
+        r.l = __ldcg(p.logits + row * p.ld_logits + r.d);
+        r.u = __ldcg(p.u + row);
+        if (p.q) r.q = __ldcg(p.q + row * p.ld_q + r.d);
+    }
+    return r;
+}
+
+// CTA (span of pieces, sequence).  What does not come from
+// verify_stats_kernel is read before the dependency wait: that kernel lets
+// this one start only after its own wait, so everything before it is done.
+__global__ void __launch_bounds__(kThreads) verify_pick_kernel(pq2h::VerifyParams p, int spans,
+                                                               int pieces) {
     __shared__ int s_stop;
     __shared__ float s_max, s_inv;
-    __shared__ int s_best, s_refused;
+    __shared__ int s_best, s_refused, s_draft;
     __shared__ unsigned long long sk[2][kWarps];
     __shared__ bool s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long b = blockIdx.x / p.chunks;
-    const int chunk = static_cast<int>(blockIdx.x - b * p.chunks);
+    const int b = blockIdx.x / spans, span = blockIdx.x - b * spans;
     if (tid == 0) s_stop = INT_MAX;
-    pdl_wait();
-    pdl_launch_dependents();
-    __syncthreads();
-    const int r0 = p.row_start[b], r1 = p.row_start[b + 1];
-    if (r0 < 0 || r1 < r0 || r1 > p.rows) {  // uniform over the CTA
-        if (tid == 0 && chunk == 0) {
-            atomicOr(p.ctl.err, DEVERR_BAD_INDEX);
-            p.accepted[b] = 0;
+    const int r0 = __ldcg(p.row_start + b), r1 = __ldcg(p.row_start + b + 1);
+    const float c = scale_of(__ldcg(p.temperature + b));
+    const bool greedy = c == 0.0f;
+    const bool bad = r0 < 0 || r1 < r0 || r1 > p.rows;
+    if (bad || r0 == r1) {  // uniform over the CTA
+        pdl_wait();
+        if (tid == 0 && span == 0) {
+            if (bad) atomicOr(p.ctl.err, DEVERR_BAD_INDEX);
+            if (store_ok(p.ctl, b, 1, p.B)) p.accepted[b] = 0;
         }
         return;
     }
-    if (r0 == r1) {
-        if (tid == 0 && chunk == 0) p.accepted[b] = 0;
-        return;
-    }
-    const float c = scale_of(p.temperature[b]);
-    const bool greedy = c == 0.0f;
+    RowTest test = row_test(p, r0 + warp, r1, greedy);
+    const float* e = p.e + b * p.ld_e;
+    pdl_wait();
+    pdl_launch_dependents();
+    __syncthreads();
     // A warp per row, a round of kWarps rows at a time: join the row's pieces
     // and decide its draft.  The first row that stops ends the search.
     for (int base = r0; base < r1; base += kWarps) {
         const int row = base + warp;
+        if (base > r0) test = row_test(p, row, r1, greedy);
         float m = neg_inf(), s = 0.0f;
         int at = INT_MAX;
         bool stops = false, refused = false;
         if (row < r1) {
-            const int d = p.drafts[row];
-            const bool last = row == r1 - 1 || d < 0 || d >= p.V;
-            float ld = 0.0f, qd = 1.0f, u = 0.0f;
-            if (!last) {
-                ld = p.logits[row * p.ld_logits + d];
-                if (!greedy) {
-                    u = p.u[row];
-                    if (p.q) qd = p.q[row * p.ld_q + d];
-                }
-            }
             const long long o = static_cast<long long>(row) * p.chunks;
             for (int k = lane; k < p.chunks; k += 32) {
                 const float2 f = p.stats[o + k];
@@ -222,14 +239,14 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(pq2h::VerifyParam
                     join(m, s, m2, s2, c);
             }
             bool take = false;
-            if (!last) {
+            if (!test.last) {
                 if (greedy)
-                    take = d == at;
+                    take = test.d == at;
                 else if (s > 0.0f)
-                    take = u * qd < ex2((ld - m) * c) / s;
+                    take = test.u * test.q < ex2((test.l - m) * c) / s;
             }
             stops = !take;
-            refused = stops && !last;
+            refused = stops && !test.last;
             if (stops && lane == 0) atomicMin(&s_stop, row);
         }
         __syncthreads();
@@ -241,6 +258,7 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(pq2h::VerifyParam
                 s_inv = s > 0.0f ? 1.0f / s : 0.0f;
                 s_best = at;
                 s_refused = refused;
+                s_draft = test.d;
             }
             break;
         }
@@ -249,26 +267,26 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(pq2h::VerifyParam
     const int stop = s_stop;
     const bool refused = s_refused != 0;
     if (greedy) {
-        if (chunk != 0) return;
+        if (span != 0) return;
     } else {
         const float m = s_max, inv = s_inv;
-        const int d = p.drafts[stop];
+        const int d = s_draft;
         const float* l = p.logits + stop * p.ld_logits;
-        const float* e = p.e + b * p.ld_e;
         const float* q = refused && p.q ? p.q + stop * p.ld_q : nullptr;
         const int off = lead(l);
         const bool ve = lead(e) == off, vq = q && lead(q) == off;
         unsigned long long k0 = 0, k1 = 0;
-        const int e0 = chunk * kPiece - off;
-        float4 lv[kVecs], ev[kVecs], qv[kVecs];
+        for (int piece = 0; piece < pieces && m > neg_inf(); ++piece) {
+            const int e0 = (span * pieces + piece) * kPickPiece - off;
+            if (e0 >= p.V) break;
+            float4 lv[kVecs], ev[kVecs], qv[kVecs];
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int v0 = e0 + (i * kThreads + tid) * 4;
-            lv[i] = load4(l, v0, p.V, true, neg_inf());
-            ev[i] = load4(e, v0, p.V, ve, 1.0f);
-            qv[i] = q ? load4(q, v0, p.V, vq, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-        if (m > neg_inf()) {
+            for (int i = 0; i < kVecs; ++i) {
+                const int v0 = e0 + (i * kThreads + tid) * 4;
+                lv[i] = load4(l, v0, p.V, true, neg_inf());
+                ev[i] = load4(e, v0, p.V, ve, 1.0f);
+                qv[i] = q ? load4(q, v0, p.V, vq, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
                 const int v0 = e0 + (i * kThreads + tid) * 4;
@@ -303,9 +321,12 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(pq2h::VerifyParam
                 k0 = sk[0][w] > k0 ? sk[0][w] : k0;
                 k1 = sk[1][w] > k1 ? sk[1][w] : k1;
             }
-            if (k0) atomicMax(&p.keys[2 * b], k0);
-            if (k1) atomicMax(&p.keys[2 * b + 1], k1);
-            s_last = atom_add_acq_rel_gpu(&p.done[b], 1u) + 1u == static_cast<unsigned>(p.chunks);
+            // k1 counts only where no span has a k0
+            if (k0)
+                atomicMax(&p.keys[2 * b], k0);
+            else if (k1)
+                atomicMax(&p.keys[2 * b + 1], k1);
+            s_last = atom_add_acq_rel_gpu(&p.done[b], 1u) + 1u == static_cast<unsigned>(spans);
         }
         __syncthreads();
         if (!s_last) return;
@@ -332,6 +353,8 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(pq2h::VerifyParam
 namespace pq2h {
 
 namespace {
+
+constexpr int64_t kPickCtas = 1216;
 
 int verify_chunks(int64_t V) {
     // up to three values before the first 16-byte boundary of a row
@@ -365,8 +388,14 @@ cudaError_t launch_verify(VerifyParams p, void* workspace, cudaStream_t st) {
                                      dim3(pq2::kThreads), 0, st, true, p);
         if (e != cudaSuccess) return e;
     }
-    return launch(pq2::verify_pick_kernel, dim3(static_cast<unsigned>(p.B * p.chunks)),
-                  dim3(pq2::kThreads), 0, st, true, p);
+    // a CTA's start (the row's statistics, the decision) costs several trips to
+    // L2: about 1200 CTAs in all (two residencies), each over a span of pieces
+    const int all = static_cast<int>((p.V + 3 + pq2::kPickPiece - 1) / pq2::kPickPiece);
+    const int64_t most = std::max<int64_t>(1, kPickCtas / p.B);
+    const int rounds = static_cast<int>((all + most - 1) / most);
+    const int spans = (all + rounds - 1) / rounds;
+    return launch(pq2::verify_pick_kernel, dim3(static_cast<unsigned>(p.B * spans)),
+                  dim3(pq2::kThreads), 0, st, true, p, spans, rounds);
 }
 
 }  // namespace pq2h
