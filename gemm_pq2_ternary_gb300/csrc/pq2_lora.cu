@@ -454,7 +454,7 @@ __device__ __forceinline__ void y_fetch(const pq2h::LoraParams& p, float4 (&y)[N
 // kernel start only after its own wait, so everything before it is done.
 template <bool BF, int YT>
 __global__ void __launch_bounds__(kExpandMaxWarps * 32)
-    lora_expand_few(pq2h::LoraParams p, const float* part, int splits, int vec) {
+    lora_expand_few(pq2h::LoraParams p, const float* part, int splits, int rounds, int vec) {
     extern __shared__ __align__(16) uint16_t sv[];
     __shared__ FewTile tile;
     __shared__ float f[kFewTile];
@@ -468,7 +468,9 @@ __global__ void __launch_bounds__(kExpandMaxWarps * 32)
     }
     const int rank = l >= 0 ? rank_of(p, l) : 0;
     const int blocks = (rank + 31) / 32;
-    const int n = (blockIdx.x * nwarps + warp) * 32 + 4 * (lane >> 2);
+    // this warp's outputs: 32 a round, the rounds a CTA's width apart
+    const int step = nwarps * 32;
+    int n = blockIdx.x * rounds * step + warp * 32 + 4 * (lane >> 2);
     constexpr int kAhead = 2;  // blocks of B loaded before the wait
     BRows b[kAhead];
 #pragma unroll
@@ -517,22 +519,31 @@ __global__ void __launch_bounds__(kExpandMaxWarps * 32)
         if (threadIdx.x < kFewTile) f[threadIdx.x] = 0.0f;
     }
     __syncthreads();
-    float acc[2][1][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[h][0][c] = 0.0f;
-    for (int blk = 0; blk < blocks; blk += kAhead) {
-        if (blk > 0) {
+    for (int round = 0; round < rounds; ++round, n += step) {
+        if (round > 0) {
+            if (n - 4 * (lane >> 2) >= p.N) return;   // the whole warp is past the row
 #pragma unroll
             for (int i = 0; i < kAhead; ++i)
-                if (blk + i < blocks) b[i] = b_load(p, l, rank, n, blk + i);
+                if (i < blocks) b[i] = b_load(p, l, rank, n, i);
+            y_fetch<YT, 1>(p, y, tok, count, n, vec != 0);
         }
+        float acc[2][1][4];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (blk + i < blocks) expand_block<BF, 1>(acc, b[i], sv, pitch, term_size, blk + i, count);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[h][0][c] = 0.0f;
+        for (int blk = 0; blk < blocks; blk += kAhead) {
+            if (blk > 0) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    if (blk + i < blocks) b[i] = b_load(p, l, rank, n, blk + i);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (blk + i < blocks) expand_block<BF, 1>(acc, b[i], sv, pitch, term_size, blk + i, count);
+        }
+        expand_store<YT, 1>(p, acc, y, tok, f, count, n, vec != 0);
     }
-    expand_store<YT, 1>(p, acc, y, tok, f, count, n, vec != 0);
 }
 
 // ----------------------------------------------------------------------------
@@ -553,11 +564,11 @@ struct Plan {
 // last), cut into tiles of at most kTile.  Every warp counts and places a
 // contiguous range of tokens in its own histogram, so the order is fixed.
 __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Plan pl, int warps) {
-    extern __shared__ int hist[];  // [warps][bins], then offsets [bins], tiles [bins]
+    extern __shared__ int hist[];  // [warps][bins], then offsets [bins + 1], tiles [bins]
     __shared__ int ws[2][32];
     const int bins = p.L + 1;
     int* off = hist + warps * bins;
-    int* tfirst = off + bins;
+    int* tfirst = off + bins + 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nthreads = blockDim.x;
     for (int i = threadIdx.x; i < warps * bins; i += nthreads) hist[i] = 0;
     pdl_wait();
@@ -589,27 +600,33 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
         }
     }
     __syncthreads();
-    // per bin: the warps' counts to offsets; then a scan over the bins, each
-    // thread owning a contiguous span
+    // a warp per bin: its counts by warp to offsets within the bin
+    const int nwarps = nthreads >> 5;
+    for (int b = warp; b < bins; b += nwarps) {
+        const int c = lane < warps ? hist[lane * bins + b] : 0;
+        int sum = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        if (lane < warps) hist[lane * bins + b] = sum - c;
+        if (lane == 31) off[b] = sum;
+    }
+    __syncthreads();
+    // a scan over the bins, each thread owning a contiguous span
     const int span = (bins + nthreads - 1) / nthreads;
     const int b0 = min(static_cast<int>(threadIdx.x) * span, bins), b1 = min(b0 + span, bins);
     int n_tok = 0, n_tile = 0;
     for (int b = b0; b < b1; ++b) {
-        int total = 0;
-        for (int w = 0; w < warps; ++w) {
-            const int c = hist[w * bins + b];
-            hist[w * bins + b] = total;
-            total += c;
-        }
-        off[b] = total;
-        n_tok += total;
-        n_tile += (total + kTile - 1) / kTile;
+        n_tok += off[b];
+        n_tile += (off[b] + kTile - 1) / kTile;
     }
     int s_tok = n_tok, s_tile = n_tile;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, s_tok, o), c = __shfl_up_sync(0xffffffffu, s_tile, o);
-        if (lane >= o) s_tok += a, s_tile += c;
+        const int v = __shfl_up_sync(0xffffffffu, s_tok, o), c = __shfl_up_sync(0xffffffffu, s_tile, o);
+        if (lane >= o) s_tok += v, s_tile += c;
     }
     if (lane == 31) ws[0][warp] = s_tok, ws[1][warp] = s_tile;
     __syncthreads();
@@ -619,12 +636,20 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
         const int total = off[b];
         off[b] = at_tok;
         tfirst[b] = at_tile;
-        for (int k = 0; k < total; k += kTile)
-            pl.tiles[at_tile++] = make_int4(b < p.L ? b : -1, at_tok + k, min(kTile, total - k), 0);
         at_tok += total;
+        at_tile += (total + kTile - 1) / kTile;
     }
-    if (threadIdx.x == nthreads - 1) *pl.num_tiles = at_tile;
+    if (threadIdx.x == nthreads - 1) {
+        *pl.num_tiles = at_tile;
+        off[bins] = p.M;
+    }
     __syncthreads();
+    // tiles: a warp per bin again
+    for (int b = warp; b < bins; b += nwarps) {
+        const int first = off[b], total = off[b + 1] - first;
+        for (int k = lane * kTile; k < total; k += 32 * kTile)
+            pl.tiles[tfirst[b] + k / kTile] = make_int4(b < p.L ? b : -1, first + k, min(kTile, total - k), 0);
+    }
     for (int base = m0; base < m1; base += 32 * kBatch) {
         if (per > 32 * kBatch) load_keys(base, false);   // else still there
 #pragma unroll
@@ -1371,12 +1396,18 @@ cudaError_t run_few(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec
                         pq2::term_pitch((p.R + 31) / 32) * 2;
     e = ensure_smem(lim, pq2::lora_expand_few<BF, YT>, smem);
     if (e != cudaSuccess) return e;
-    // 128 outputs a CTA while the GPU has SMs to spare, 256 beyond
+    // 128 outputs a CTA while the GPU has SMs to spare; else 256, and as many
+    // rounds of them as keep the CTAs to one residency (two per SM): a CTA's
+    // start (its tile, v) costs several trips to L2
     const int64_t all = pq2::few_tiles(p.M, std::min(p.M, p.L + 1));
-    const int warps = (p.N + 127) / 128 * all <= 2 * kSms ? pq2::kExpandWarps : pq2::kExpandMaxWarps;
+    const bool spare = (p.N + 127) / 128 * all <= 2 * kSms;
+    const int cols = (spare ? pq2::kExpandWarps : pq2::kExpandMaxWarps) * 32;
+    const int64_t blocks = (p.N + cols - 1) / cols;
+    const int64_t per_tile = std::max<int64_t>(1, 2 * kSms / all);
+    const int rounds = spare ? 1 : static_cast<int>((blocks + per_tile - 1) / per_tile);
     return launch(pq2::lora_expand_few<BF, YT>,
-                  dim3((p.N + warps * 32 - 1) / (warps * 32), static_cast<unsigned>(all)),
-                  dim3(warps * 32), smem, st, true, p, part, lay.splits, vec);
+                  dim3(static_cast<unsigned>((blocks + rounds - 1) / rounds), static_cast<unsigned>(all)),
+                  dim3(cols), smem, st, true, p, part, lay.splits, rounds, vec);
 }
 
 template <typename Kern>
@@ -1480,7 +1511,7 @@ cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cu
     int warps = 32;
     while (warps > 1 && (warps / 2 * 32 >= p.M || static_cast<size_t>(warps + 2) * bins * 4 > 200 * 1024))
         warps /= 2;
-    const size_t plan_smem = static_cast<size_t>(warps + 2) * bins * 4;
+    const size_t plan_smem = (static_cast<size_t>(warps + 2) * bins + 1) * 4;
     cudaError_t e = ensure_smem(g_plan_smem, pq2::lora_plan_kernel, plan_smem);
     if (e != cudaSuccess) return e;
     e = launch(pq2::lora_plan_kernel, dim3(1), dim3(warps * 32), plan_smem, st, true, p, pl, warps);
