@@ -55,7 +55,7 @@ constexpr int kTile = 64;        // tokens per tile of the planned form
 constexpr int kShrinkWarps = 8;
 constexpr int kExpandWarps = 4;   // 32 outputs each
 constexpr int kExpandMaxWarps = 8;
-constexpr int kMaxSplits = 32;
+constexpr int kMaxSplits = 64;
 constexpr int kFlush = 8;        // k32 blocks (16 MMAs) per accumulator chain
 
 // d += a . b (16 x 8 x 16), fp32 accumulators.
@@ -282,11 +282,21 @@ __global__ void __launch_bounds__(kShrinkWarps * 32)
                 fb[u] = k < k1 && rb < rank ? load16(a1 + k) : zero4();
                 fx[u] = k < k1 && x ? load16(x + k) : zero4();
             }
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            // four accumulators: a dependent instruction waits some 150 cycles
+            float acc[4][4];
 #pragma unroll
-            for (int u = 0; u < U; ++u) mma_block<BF>(acc, fa[u], fb[u], fx[u]);
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sum[c] += acc[c];
+                for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float(&lo)[4] = acc[u % 2 * 2];
+                float(&hi)[4] = acc[u % 2 * 2 + 1];
+                mma16816<BF>(lo, fa[u].x, fb[u].x, fa[u].y, fb[u].y, fx[u].x, fx[u].y);
+                mma16816<BF>(hi, fa[u].z, fb[u].z, fa[u].w, fb[u].w, fx[u].z, fx[u].w);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sum[c] += (acc[0][c] + acc[1][c]) + (acc[2][c] + acc[3][c]);
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -384,7 +394,12 @@ __device__ __forceinline__ BRows b_load(const pq2h::LoraParams& p, int l, int ra
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         b.r[i] = left > 0 && n + i < p.N ? load16_cg(src + static_cast<size_t>(i) * p.R) : zero4();
-        if (left < 8) b.r[i] = keep_first(b.r[i], left);
+    }
+    // only a rank that is no multiple of 8 leaves a piece half used (asking
+    // about a value just loaded would wait for it)
+    if (rank % 8 != 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b.r[i] = keep_first(b.r[i], left);
     }
     return b;
 }
@@ -452,7 +467,11 @@ __device__ __forceinline__ void y_fetch(const pq2h::LoraParams& p, float4 (&y)[N
 // Few tokens: CTA (32 outputs a warp, tile).  The operands that do not come
 // from shrink (B, y) are loaded before the dependency wait: shrink lets this
 // kernel start only after its own wait, so everything before it is done.
-template <bool BF, int YT>
+// kOne: the adapters' rows of B are one block of 32 ranks, and the next
+// round's operands are loaded during this one (64 requests with adapters of
+// rank 16, 17408 outputs: 33 us against 44).  Else two blocks of this round
+// are.
+template <bool BF, int YT, bool kOne>
 __global__ void __launch_bounds__(kExpandMaxWarps * 32)
     lora_expand_few(pq2h::LoraParams p, const float* part, int splits, int rounds, int vec) {
     extern __shared__ __align__(16) uint16_t sv[];
@@ -471,26 +490,27 @@ __global__ void __launch_bounds__(kExpandMaxWarps * 32)
     // this warp's outputs: 32 a round, the rounds a CTA's width apart
     const int step = nwarps * 32;
     int n = blockIdx.x * rounds * step + warp * 32 + 4 * (lane >> 2);
-    constexpr int kAhead = 2;  // blocks of B loaded before the wait
+    constexpr int kAhead = 2;  // blocks of B in registers
     BRows b[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-        if (i < blocks) b[i] = b_load(p, l, rank, n, i);
-    float4 y[1][2];
-    y_fetch<YT, 1>(p, y, tok, count, n, vec != 0);
+    float4 y[kOne ? 2 : 1][1][2];
+    const auto load_b = [&](int slot, int blk, int at) {
+        if (blk < blocks) b[slot] = b_load(p, l, rank, at, blk);
+    };
+    load_b(0, 0, n);
+    if (!kOne) load_b(1, 1, n);
+    y_fetch<YT, 1>(p, y[0], tok, count, n, vec != 0);
     const float scale = l >= 0 && p.scales ? __ldcg(p.scales + l) : 1.0f;
 
     pdl_wait();
     pdl_launch_dependents();
-    // v: the K-split partials in order; then the 16-bit terms
+    // v: the K-split partials in order, a warp per token and 32 ranks; then the
+    // token's 16-bit terms
     const int pitch = term_pitch((p.R + 31) / 32), term_size = kFewTile * pitch;
-    for (int j = warp; j < count && blocks > 0; j += nwarps) {
-        float v[8], top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = i * 32 + lane;
-            v[i] = 0.0f;
-            if (i >= blocks || r >= rank) continue;
+    float* sf = reinterpret_cast<float*>(sv + terms<BF>() * term_size);   // [token][blocks][32]
+    for (int i = warp; i < count * blocks; i += nwarps) {
+        const int j = i / blocks, r = i % blocks * 32 + lane;
+        float v = 0.0f;
+        if (r < rank) {
             const float* src = part + static_cast<size_t>(tok[j]) * p.R + r;
             const size_t step = static_cast<size_t>(p.M) * p.R;
             for (int s0 = 0; s0 < splits; s0 += 16) {
@@ -498,16 +518,19 @@ __global__ void __launch_bounds__(kExpandMaxWarps * 32)
 #pragma unroll
                 for (int s = 0; s < 16; ++s) w[s] = s0 + s < splits ? src[(s0 + s) * step] : 0.0f;
 #pragma unroll
-                for (int s = 0; s < 16; ++s) v[i] += w[s];
+                for (int s = 0; s < 16; ++s) v += w[s];
             }
-            top = fmaxf(top, fabsf(v[i]));
         }
+        sf[i * 32 + lane] = v;
+    }
+    __syncthreads();
+    for (int j = warp; j < count && blocks > 0; j += nwarps) {
+        float top = 0.0f;
+        for (int i = 0; i < blocks; ++i) top = fmaxf(top, fabsf(sf[(j * blocks + i) * 32 + lane]));
         const float up = pow2_below<BF>(warp_max(top)), down = 1.0f / up;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (i >= blocks) break;
+        for (int i = 0; i < blocks; ++i) {
             uint16_t w[3];
-            split_terms<BF>(v[i] * down, w);
+            split_terms<BF>(sf[(j * blocks + i) * 32 + lane] * down, w);
 #pragma unroll
             for (int q = 0; q < terms<BF>(); ++q)
                 sv[q * term_size + j * pitch + i * 32 + lane] = w[q];
@@ -519,30 +542,68 @@ __global__ void __launch_bounds__(kExpandMaxWarps * 32)
         if (threadIdx.x < kFewTile) f[threadIdx.x] = 0.0f;
     }
     __syncthreads();
-    for (int round = 0; round < rounds; ++round, n += step) {
-        if (round > 0) {
-            if (n - 4 * (lane >> 2) >= p.N) return;   // the whole warp is past the row
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (i < blocks) b[i] = b_load(p, l, rank, n, i);
-            y_fetch<YT, 1>(p, y, tok, count, n, vec != 0);
-        }
-        float acc[2][1][4];
+    // an accumulator for either half of a block: a dependent instruction waits
+    // some 150 cycles
+    float acc[2][1][4], half[2][4];
+    const auto clear = [&] {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[h][0][c] = 0.0f;
-        for (int blk = 0; blk < blocks; blk += kAhead) {
-            if (blk > 0) {
+            for (int c = 0; c < 4; ++c) acc[h][0][c] = half[h][c] = 0.0f;
+    };
+    const auto product = [&](const BRows& rows, int blk) {
+        const uint16_t* src = sv + (lane >> 2) * pitch + blk * 32 + 8 * (lane & 3);
+        const uint4* r = rows.r;
+#pragma unroll
+        for (int q = 0; q < terms<BF>(); ++q) {
+            const uint4 c = *reinterpret_cast<const uint4*>(src + q * term_size);
+            mma16816<BF>(acc[0][0], r[0].x, r[1].x, r[0].y, r[1].y, c.x, c.y);
+            mma16816<BF>(acc[1][0], r[2].x, r[3].x, r[2].y, r[3].y, c.x, c.y);
+            mma16816<BF>(half[0], r[0].z, r[1].z, r[0].w, r[1].w, c.z, c.w);
+            mma16816<BF>(half[1], r[2].z, r[3].z, r[2].w, r[3].w, c.z, c.w);
+        }
+    };
+    const auto store = [&](const float4(&yv)[1][2]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[h][0][c] += half[h][c];
+        expand_store<YT, 1>(p, acc, yv, tok, f, count, n, vec != 0);
+    };
+    for (int round = 0; round < rounds; round += kOne ? 2 : 1) {
+        // a warp past the end of the row loads and stores nothing
+        if constexpr (kOne) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (round + s >= rounds) return;
+                if (round + s + 1 < rounds) {
+                    load_b(1 - s, 0, n + step);
+                    y_fetch<YT, 1>(p, y[1 - s], tok, count, n + step, vec != 0);
+                }
+                clear();
+                if (blocks > 0) product(b[s], 0);
+                store(y[s]);
+                n += step;
+            }
+        } else {
+            if (round > 0) {
+                load_b(0, 0, n);
+                load_b(1, 1, n);
+                y_fetch<YT, 1>(p, y[0], tok, count, n, vec != 0);
+            }
+            clear();
+            for (int blk = 0; blk < blocks; blk += kAhead) {
+                if (blk > 0) {
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) load_b(i, blk + i, n);
+                }
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i)
-                    if (blk + i < blocks) b[i] = b_load(p, l, rank, n, blk + i);
+                    if (blk + i < blocks) product(b[i], blk + i);
             }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (blk + i < blocks) expand_block<BF, 1>(acc, b[i], sv, pitch, term_size, blk + i, count);
+            store(y[0]);
+            n += step;
         }
-        expand_store<YT, 1>(p, acc, y, tok, f, count, n, vec != 0);
     }
 }
 
@@ -729,11 +790,22 @@ constexpr int shrink_stages() {
     return RPW * WN <= 2 ? 8 : RPW * WN == 4 ? 5 : 3;
 }
 
+// Accumulators of a consumer warp: where it has one or two fragments, a set per
+// half of a block of 32 columns (and per block) -- a dependent instruction
+// waits some 150 cycles, and a stage brings four in a row.  With four fragments
+// a second set costs the second CTA of an SM (4096 tokens of rank 64: 159 us
+// against 148).
+template <int RPW, int WN>
+constexpr int shrink_sets() {
+    return RPW * WN == 1 ? 4 : RPW * WN == 2 ? 2 : 1;
+}
+
 // A warp's share of one pipeline stage.  x0, a0: this lane's first rows of x
 // and A (shared-memory addresses); at[blk]: its chunk in either block of 32.
 template <bool BF, int RPW, int NI, int WN>
-__device__ __forceinline__ void shrink_stage(float (&acc)[RPW][WN][4], uint32_t x0, uint32_t a0,
-                                             const uint32_t (&at)[2]) {
+__device__ __forceinline__ void shrink_stage(float (&acc)[shrink_sets<RPW, WN>()][RPW][WN][4],
+                                             uint32_t x0, uint32_t a0, const uint32_t (&at)[2]) {
+    constexpr int kSets = shrink_sets<RPW, WN>();
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk) {
         uint4 a[RPW][2], c[NI];
@@ -747,12 +819,14 @@ __device__ __forceinline__ void shrink_stage(float (&acc)[RPW][WN][4], uint32_t 
         for (int r = 0; r < RPW; ++r)
 #pragma unroll
             for (int i = 0; i < NI; ++i)
-                mma16816<BF>(acc[r][i], a[r][0].x, a[r][1].x, a[r][0].y, a[r][1].y, c[i].x, c[i].y);
+                mma16816<BF>(acc[(2 * blk) % kSets][r][i], a[r][0].x, a[r][1].x, a[r][0].y, a[r][1].y,
+                             c[i].x, c[i].y);
 #pragma unroll
         for (int r = 0; r < RPW; ++r)
 #pragma unroll
             for (int i = 0; i < NI; ++i)
-                mma16816<BF>(acc[r][i], a[r][0].z, a[r][1].z, a[r][0].w, a[r][1].w, c[i].z, c[i].w);
+                mma16816<BF>(acc[(2 * blk + 1) % kSets][r][i], a[r][0].z, a[r][1].z, a[r][0].w,
+                             a[r][1].w, c[i].z, c[i].w);
     }
 }
 
@@ -868,13 +942,16 @@ __global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
     } else if (works) {
         const uint32_t at[2] = {static_cast<uint32_t>((t ^ ((g & 1) * 4)) * 16),
                                 static_cast<uint32_t>(((4 + t) ^ ((g & 1) * 4)) * 16)};
-        float acc[RPW][WN][4];
+        constexpr int kSets = shrink_sets<RPW, WN>();
+        float acc[kSets][RPW][WN][4];
 #pragma unroll
-        for (int r = 0; r < RPW; ++r)
+        for (int q = 0; q < kSets; ++q)
 #pragma unroll
-            for (int i = 0; i < WN; ++i)
+            for (int r = 0; r < RPW; ++r)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) acc[r][i][c] = 0.0f;
+                for (int i = 0; i < WN; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[q][r][i][c] = 0.0f;
         int s = 0;
         uint32_t turn = 0;
         for (int step = 0; step < steps; ++step) {
@@ -895,14 +972,16 @@ __global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
             if (++s == kStages) s = 0, ++turn;
             if ((step + 1) % (kFlush / 2) == 0 || step + 1 == steps) {
 #pragma unroll
-                for (int r = 0; r < RPW; ++r)
+                for (int q = 0; q < kSets; ++q)
 #pragma unroll
-                    for (int i = 0; i < WN; ++i)
+                    for (int r = 0; r < RPW; ++r)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            sum[r][i][c] += acc[r][i][c];
-                            acc[r][i][c] = 0.0f;
-                        }
+                        for (int i = 0; i < WN; ++i)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                sum[r][i][c] += acc[q][r][i][c];
+                                acc[q][r][i][c] = 0.0f;
+                            }
             }
         }
     }
@@ -1056,7 +1135,11 @@ __device__ __forceinline__ void ring_product(float (&acc)[2][NI][4], uint32_t bp
             const int left = rank - blk * 32 - 8 * t;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                b[i] = left > 0 ? keep_first(lds_v4(bp + i * b_step), left) : zero4();
+                b[i] = left > 0 ? lds_v4(bp + i * b_step) : zero4();
+            if (rank % 8 != 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) b[i] = keep_first(b[i], left);
+            }
         }
 #pragma unroll
         for (int q = 0; q < terms<BF>(); ++q) {
@@ -1391,10 +1474,12 @@ cudaError_t run_few(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec
     cudaError_t e = launch(pq2::lora_shrink_few<BF>, dim3(lay.splits, static_cast<unsigned>(with)),
                            dim3(pq2::kShrinkWarps * 32), 0, st, true, p, part, lay.k_split);
     if (e != cudaSuccess) return e;
-    static SmemLimit lim;
-    const size_t smem = static_cast<size_t>(pq2::terms<BF>()) * pq2::kFewTile *
-                        pq2::term_pitch((p.R + 31) / 32) * 2;
-    e = ensure_smem(lim, pq2::lora_expand_few<BF, YT>, smem);
+    static SmemLimit lim[2];
+    const int rb = (p.R + 31) / 32;
+    auto kern = rb == 1 ? pq2::lora_expand_few<BF, YT, true> : pq2::lora_expand_few<BF, YT, false>;
+    const size_t smem = static_cast<size_t>(pq2::terms<BF>()) * pq2::kFewTile * pq2::term_pitch(rb) * 2 +
+                        static_cast<size_t>(pq2::kFewTile) * rb * 32 * 4;
+    e = ensure_smem(lim[rb == 1], kern, smem);
     if (e != cudaSuccess) return e;
     // 128 outputs a CTA while the GPU has SMs to spare; else 256, and as many
     // rounds of them as keep the CTAs to one residency (two per SM): a CTA's
@@ -1405,7 +1490,7 @@ cudaError_t run_few(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec
     const int64_t blocks = (p.N + cols - 1) / cols;
     const int64_t per_tile = std::max<int64_t>(1, 2 * kSms / all);
     const int rounds = spare ? 1 : static_cast<int>((blocks + per_tile - 1) / per_tile);
-    return launch(pq2::lora_expand_few<BF, YT>,
+    return launch(kern,
                   dim3(static_cast<unsigned>((blocks + rounds - 1) / rounds), static_cast<unsigned>(all)),
                   dim3(cols), smem, st, true, p, part, lay.splits, rounds, vec);
 }
