@@ -7,6 +7,7 @@
 
 #include "../../include/pq2.h"
 #include "pq2_internal.h"
+#include "pq2_step.cuh"
 
 // Device error word: bit flags of pq2::DEVERR_*, one per device context.
 __device__ unsigned g_pq2_error_word = 0;

@@ -22,7 +22,6 @@ enum : unsigned {
     DEVERR_TIMEOUT = 1u,      // a bounded wait ran out
     DEVERR_BAD_TERNARY = 2u,  // pack met a value outside {-1,0,1}
     DEVERR_BOUNDS = 4u,       // bounds-checked build: a store outside its buffer (skipped)
-    DEVERR_BAD_INDEX = 8u,    // an index array held a value outside its range
 };
 
 // Passed by value to every kernel.
@@ -191,15 +190,6 @@ __device__ __forceinline__ bool mbar_suspend_bounded(uint64_t* bar, uint32_t par
             return false;
         }
     }
-}
-
-// The same, for phases that are mostly complete when asked for: all lanes try
-// at once and agree by a vote, and only if that fails lane 0 polls (its branch
-// and the shuffle after it take about 300 cycles in a short loop).
-__device__ __forceinline__ bool mbar_ready_warp(uint64_t* bar, uint32_t parity, const DevCtl& ctl,
-                                                volatile int* abort_flag = nullptr) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    return mbar_wait_warp(bar, parity, ctl, abort_flag);
 }
 
 // Warp-wide suspending wait (lane 0 waits in try_wait, the warp then

@@ -45,6 +45,7 @@
 
 #include "pq2_common.cuh"
 #include "pq2_internal.h"
+#include "pq2_step.cuh"
 
 namespace pq2 {
 namespace {
@@ -258,7 +259,12 @@ __global__ void __launch_bounds__(kShrinkWarps * 32)
     if (count == 0) return;  // uniform over the CTA
     const int rank = rank_of(p, l);
     const int k0 = blockIdx.x * k_split, k1 = min(k0 + k_split, p.K);
-    float* dst = part + static_cast<size_t>(blockIdx.x) * p.M * p.R;
+    const long long out0 = static_cast<long long>(blockIdx.x) * p.M * p.R;
+    const long long part_elems = static_cast<long long>(gridDim.x) * p.M * p.R;
+    const auto put = [&](int j, int r, float v) {
+        const long long o = out0 + static_cast<long long>(tile.tok[j]) * p.R + r;
+        if (store_ok(p.ctl, o, 1, part_elems)) part[o] = v;
+    };
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int rank_tiles = (rank + 15) / 16;
@@ -304,7 +310,7 @@ __global__ void __launch_bounds__(kShrinkWarps * 32)
             if (kw > 1)
                 red[(warp * 16 + r) * kFewTile + j] = sum[c];
             else if (j < count && rt * 16 + r < rank)
-                dst[static_cast<size_t>(tile.tok[j]) * p.R + rt * 16 + r] = sum[c];
+                put(j, rt * 16 + r, sum[c]);
         }
     }
     if (kw > 1) {
@@ -315,7 +321,7 @@ __global__ void __launch_bounds__(kShrinkWarps * 32)
             const float* src = red + ((r / 16) * kw * 16 + r % 16) * kFewTile + j;
             float v = 0.0f;
             for (int w = 0; w < kw; ++w) v += src[w * 16 * kFewTile];
-            dst[static_cast<size_t>(tile.tok[j]) * p.R + r] = v;
+            put(j, r, v);
         }
     }
 }
@@ -1033,15 +1039,17 @@ __global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
             top = fmaxf(top, fabsf(v[i]));
         }
         const float up = pow2_below<BF>(warp_max(top)), down = 1.0f / up;
-        if (lane == 0) pl.f[first + j] = scale * up;
+        if (lane == 0 && store_ok(p.ctl, first + j, 1, p.M)) pl.f[first + j] = scale * up;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (i >= blocks) break;
             uint16_t w[3];
             split_terms<BF>(v[i] * down, w);
 #pragma unroll
-            for (int q = 0; q < terms<BF>(); ++q)
-                pl.terms[q * term_size + static_cast<size_t>(first + j) * pl.rp + i * 32 + lane] = w[q];
+            for (int q = 0; q < terms<BF>(); ++q) {
+                const size_t o = q * term_size + static_cast<size_t>(first + j) * pl.rp + i * 32 + lane;
+                if (store_ok(p.ctl, o, 1, terms<BF>() * term_size)) pl.terms[o] = w[q];
+            }
         }
     }
 }

@@ -22,6 +22,7 @@
 #include "pq2_common.cuh"
 #include "pq2_elem.cuh"
 #include "pq2_internal.h"
+#include "pq2_step.cuh"
 
 namespace pq2 {
 namespace {

@@ -28,6 +28,7 @@
 
 #include "pq2_common.cuh"
 #include "pq2_internal.h"
+#include "pq2_step.cuh"
 
 namespace pq2 {
 namespace {
@@ -146,8 +147,10 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(pq2h::VerifyPara
         s = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) s += ss[w];
-        p.stats[blockIdx.x] = make_float2(m, s);
-        p.best[blockIdx.x] = at;
+        if (store_ok(p.ctl, blockIdx.x, 1, p.rows * p.chunks)) {
+            p.stats[blockIdx.x] = make_float2(m, s);
+            p.best[blockIdx.x] = at;
+        }
     }
 }
 

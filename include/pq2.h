@@ -558,8 +558,9 @@ pq2_status pq2_debug_skip_stage(int stage);
 /*
  * pq2_bounds_checked -- 1 in the bounds-checked build of the library
  * (libpq2_debug.so, compiled with PQ2_DEBUG=1), 0 in the normal one.  In the
- * bounds-checked build every kernel store to y, to the integer-dot output and
- * to the split-K scratch first checks that it lies inside its buffer; a store
+ * bounds-checked build every kernel store to an output (y, the integer dots,
+ * residual, x, accepted, tokens) and to the split-K and statistics scratch
+ * first checks that it lies inside its buffer; a store
  * that does not is skipped and pq2_last_device_error reports PQ2_ERR_BOUNDS.
  * Results are otherwise bit-identical to the normal build's.  It stands in
  * for a memory checker on GPUs where none can be run.
