@@ -8,6 +8,7 @@ importing this module fails if the library has not been built.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -78,6 +79,12 @@ class NormResidualArgs(ctypes.Structure):
                 [("eps", _F), ("alpha", _F), ("flags", _U32)])
 
 
+# The same as bytes (packing them takes a third of the time of the Structure's
+# fields); ctypes passes their address.
+_norm_residual_args = struct.Struct("=7Q5q5i2fI")
+assert _norm_residual_args.size == ctypes.sizeof(NormResidualArgs)
+
+
 SIGNATURES = {
     "pq2_status_string": ([_I], ctypes.c_char_p),
     "pq2_version": ([], ctypes.c_char_p),
@@ -93,7 +100,7 @@ SIGNATURES = {
     "pq2_gemm_bf16_splitk": ([_P, _P, _P, _I64, _I64, _I64, _U32, _P], _I),
     "pq2_mlp_down_swiglu": ([_P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P], _I),
     "pq2_rmsnorm": ([_P, _I, _I64, _P, _I, _P, _I, _I64, _I64, _I64, _F, _U32, _P], _I),
-    "pq2_norm_residual": ([ctypes.POINTER(NormResidualArgs), _I64, _I64, _P], _I),
+    "pq2_norm_residual": ([ctypes.c_void_p, _I64, _I64, _P], _I),
     "pq2_lora_workspace_bytes": ([_I64] * 5, _SZ),
     "pq2_lora_add": ([_P, _I64, _P, _P, _I, _P, _P, _P, _P, _I64, _P, _I64, _I] + [_I64] * 5 +
                      [_P, _SZ, _P], _I),
@@ -355,13 +362,13 @@ def pq2_norm_residual(y, r, r_out, w_post=None, gate=None, w_next=None, x=None, 
     if ot != rt:
         raise ValueError("r_out: expected r's type")
     H = shape[1]
-    pp = np_ = gp = xp = None
+    pp = np_ = gp = xp = 0
     wt = gt = gl = xt = xl = 0
     if w_post is not None:
         pp, wt = _weight(w_post, H, "w_post")
     if w_next is not None:
         np_, nt = _weight(w_next, H, "w_next")
-        if pp is not None and nt != wt:
+        if pp and nt != wt:
             raise ValueError("w_post and w_next: expected one type")
         wt = nt
     if gate is not None:
@@ -371,10 +378,9 @@ def pq2_norm_residual(y, r, r_out, w_post=None, gate=None, w_next=None, x=None, 
             gp, gt, gl = _row(gate, shape, "gate")
     if x is not None:
         xp, xt, xl = _row(x, shape, "x")
-    args = NormResidualArgs(yp, rp, op, pp, gp, np_, xp, yl, rl, ol, gl, xl, yt, rt, wt, gt, xt, eps,
-                            alpha, flags)
-    _check(_lib.pq2_norm_residual(ctypes.byref(args), shape[0], shape[1], _stream(stream)),
-           "pq2_norm_residual")
+    args = _norm_residual_args.pack(yp, rp, op, pp, gp, np_, xp, yl, rl, ol, gl, xl, yt, rt, wt, gt, xt,
+                                    eps, alpha, flags)
+    _check(_lib.pq2_norm_residual(args, shape[0], H, _stream(stream)), "pq2_norm_residual")
 
 
 def pq2_lora_workspace_bytes(M, N, K, L, R) -> int:
@@ -405,7 +411,7 @@ def pq2_lora_add(x, A, B, ids, y_in, y_out, workspace, ranks=None, scales=None, 
     op, ot, ol = (ip, it, il) if y_out is y_in else _row(y_out, yshape, "y_out")
     if it != ot:
         raise ValueError("y_out: expected y_in's type")
-    wp, wb = _ws(workspace)
+    wp, wb = (None, 0) if workspace is None else (_ptr(workspace), workspace.nbytes)
     _check(_lib.pq2_lora_add(xp, xl, _ptr(A), _ptr(B), xt, _vec(ids, M, torch.int32, "ids"),
                              None if ranks is None else _vec(ranks, L, torch.int32, "ranks"),
                              None if scales is None else _vec(scales, L, torch.float32, "scales"),
@@ -437,7 +443,7 @@ def pq2_verify_drafts(logits, row_start, drafts, q, u, e, temperature, accepted,
     if lt or et or qt:
         raise ValueError("logits, q and e: expected torch.float32")
     i32, f32 = torch.int32, torch.float32
-    wp, wb = _ws(workspace)
+    wp, wb = (None, 0) if workspace is None else (_ptr(workspace), workspace.nbytes)
     _check(_lib.pq2_verify_drafts(lp, ll, _vec(row_start, nb + 1, i32, "row_start"),
                                   _vec(drafts, rows, i32, "drafts"), qp, ql,
                                   _vec(u, rows, f32, "u"), ep, el,
