@@ -1410,6 +1410,456 @@ __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
     }
 }
 
+// ----------------------------------------------------------------------------
+// expand on the 5th-generation tensor cores
+// ----------------------------------------------------------------------------
+
+// The ring's expand for fp32 y: the same items, with the product on tcgen05
+// (kind::f16).  128 outputs are the rows of A (B's rows, K-major, 128-byte
+// swizzle, by TMA), the tile's 64 tokens the rows of B (v's terms, a pass of
+// the product each), and the sum arrives in tensor memory, 64 columns an item,
+// four items in flight.  One thread issues; the warps only add, store and hand
+// back: 200 instructions a warp and item where the mma.sync form takes 800 and
+// waits for its own results.  A lane is an output: y is read and written 128
+// bytes a warp, one value a lane, so its rows need no alignment for that.
+// Two more warps look at each item between its copies and its product: where
+// the rank is no multiple of 16, they put zeros over the ranks past it that
+// the product would read (they may hold anything, and v's zero times a NaN is
+// a NaN).
+constexpr int kTcEpilogue = 8;      // warps, two per quarter of the lanes
+constexpr int kTcIssuer = kTcEpilogue;
+constexpr int kTcProducer = kTcIssuer + 1;
+constexpr int kTcFixer0 = kTcProducer + 1, kTcFixers = 2;
+constexpr int kTcLoader0 = kTcFixer0 + kTcFixers, kTcLoaders = 4;   // where y does not come by TMA
+template <bool kTma>
+constexpr int tc_threads() {
+    return (kTcLoader0 + (kTma ? 0 : kTcLoaders)) * 32;
+}
+constexpr int kTcNB = 128;
+constexpr int kTcMaxStages = 4;
+constexpr int kTcDBufs = 4;
+constexpr uint32_t kTcTmemCols = kTcDBufs * kTile;
+constexpr int kTcABlock = kTcNB * 128;    // bytes of 64 ranks of an item's rows of B
+constexpr int kTcVBlock = kTile * 128;    // and of a tile's terms
+constexpr int kTcYBytes = kTile * kTcNB * 4;
+
+// Matrix descriptor: K-major, 128-byte swizzle, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(1) << 16;             // leading offset (unused here)
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;     // stride offset
+    d |= static_cast<uint64_t>(1) << 46;             // descriptor version
+    d |= static_cast<uint64_t>(2) << 61;             // 128-byte swizzle
+    return d;
+}
+
+// D[128 x 64] (+)= A[128 x 16] . B[64 x 16]^T; both operands fp16, or both bf16.
+template <bool BF>
+__device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t a, uint64_t b, bool add) {
+    constexpr uint32_t idesc = (1u << 4) | ((BF ? 1u : 0u) << 7) | ((BF ? 1u : 0u) << 10) |
+                               (static_cast<uint32_t>(kTile >> 3) << 17) |
+                               (static_cast<uint32_t>(kTcNB >> 4) << 24);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u));
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Tensor maps: y_in fp32 [M][N], box 128 x 1 (gathered by four rows); B 16-bit
+// [L * N][R], box 64 x 128, 128-byte swizzle, zeros past R.
+struct TcMaps {
+    CUtensorMap y, b;
+};
+
+// Rows r0 .. r3 of columns x .. x + 127 (x a multiple of 4) to four rows of
+// 512 bytes in shared memory; a row past the tensor's last gives zeros.
+__device__ __forceinline__ void tma_gather4(void* dst, const void* map, int x, int r0, int r1, int r2,
+                                            int r3, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+
+// kTma: y's rows start on 16-byte boundaries and come by TMA, four tokens an
+// instruction; else value by value, by warps of their own.
+template <bool BF, bool kTma>
+__global__ void __launch_bounds__(tc_threads<kTma>(), 1)
+    lora_expand_tc(pq2h::LoraParams p, Plan pl, const __grid_constant__ TcMaps maps, int stages,
+                   int stage_bytes, int term_bytes) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t full[kTcMaxStages];    // an item's y and B are there
+    __shared__ __align__(8) uint64_t ready[kTcMaxStages];   // B as the product may read it
+    __shared__ __align__(8) uint64_t empty[kTcMaxStages];   // looked at, read by the epilogue
+    __shared__ __align__(8) uint64_t dfull[kTcDBufs];       // an item's product is there
+    __shared__ __align__(8) uint64_t dempty[kTcDBufs];      // read by the epilogue's warps
+    __shared__ __align__(8) uint64_t vfull;                 // a tile's terms are there (ranks > 0)
+    __shared__ __align__(16) int row[kTile];                // start of each token's y'
+    __shared__ __align__(16) float f[kTile];
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_word;
+    volatile int* abort_flag = &abort_word;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint8_t* sv = smem + ((1024 - (smem_u32(smem) & 1023)) & 1023);
+    uint8_t* ring = sv + term_bytes;
+    if (tid == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&full[s], kTma ? 1 : kTcLoaders * 32 + 1);
+            mbar_init(&ready[s], kTcFixers);
+            mbar_init(&empty[s], kTcEpilogue + kTcFixers + 1);
+        }
+        for (int i = 0; i < kTcDBufs; ++i) {
+            mbar_init(&dfull[i], 1);
+            mbar_init(&dempty[i], kTcEpilogue);
+        }
+        mbar_init(&vfull, 1);
+        abort_word = 0;
+        fence_mbar_init();
+    }
+    if (warp == kTcIssuer) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&tmem_base)),
+                     "r"(kTcTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    const int nblocks = (p.N + kTcNB - 1) / kTcNB;
+    const bool in_place = p.y_in == p.y_out && p.ld_in == p.ld_out;
+    // the plan is complete before shrink lets this kernel start, as are y and
+    // B; v's terms are not
+    const long long total = static_cast<long long>(__ldcg(pl.num_tiles)) * nblocks;
+    const long long it0 = total * blockIdx.x / gridDim.x, it1 = total * (blockIdx.x + 1) / gridDim.x;
+    int index = static_cast<int>(it0 / nblocks), nb = static_cast<int>(it0 - static_cast<long long>(index) * nblocks);
+    int left = static_cast<int>(it1 - it0);
+    const int vblocks = (p.R + 63) / 64;
+
+    if (warp == kTcProducer) {
+        // ------------------------------ producer ------------------------------
+        int tk[4] = {0, 0, 0, 0};   // tokens 4 lane .. + 3 of the tile
+        int cached = -1, l = -1, used = 0, fours = 0, issued = 0, s = 0;
+        uint32_t turn = 0;
+        for (; left > 0; --left) {
+            if (index != cached) {
+                const int4 tile = __ldcg(pl.tiles + index);
+                cached = index, l = tile.x;
+                used = l >= 0 ? (rank_of(p, l) + 63) / 64 : 0;
+                fours = (tile.z + 3) / 4;
+                if constexpr (kTma) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tk[i] = 4 * lane + i < tile.z ? __ldcg(pl.perm + tile.y + 4 * lane + i) : p.M;
+                }
+            }
+            const int n0 = nb * kTcNB;
+            if (++nb == nblocks) nb = 0, ++index;
+            if (used == 0 && in_place) continue;   // nothing to read or write
+            if (turn > 0 && !mbar_ready_warp(&empty[s], (turn - 1) & 1, p.ctl, abort_flag)) break;
+            if (issued != p.ctl.debug_skip_stage) {  // else withheld (timeout test)
+                uint8_t* stage = ring + static_cast<size_t>(s) * stage_bytes;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&full[s],
+                                          (kTma ? fours * 4 * kTcNB * 4 : 0) + used * kTcABlock);
+                __syncwarp();
+                if (lane < used)
+                    tma_load_2d(stage + lane * kTcABlock, &maps.b, lane * 64, l * p.N + n0, &full[s]);
+                if (kTma && lane < fours)
+                    tma_gather4(stage + vblocks * kTcABlock + lane * 4 * kTcNB * 4, &maps.y, n0, tk[0], tk[1],
+                                tk[2], tk[3], &full[s]);
+            }
+            ++issued;
+            if (++s == stages) s = 0, ++turn;
+        }
+        // the last copies land before the CTA ends, whatever the others do
+        for (int k = max(0, issued - stages); k < issued; ++k)
+            if (k != p.ctl.debug_skip_stage)
+                mbar_ready_warp(&full[k % stages], static_cast<uint32_t>(k / stages) & 1, p.ctl);
+        pdl_wait();
+    } else if (warp >= kTcFixer0 && warp < kTcLoader0) {
+        // ------------------------------ fixers ------------------------------
+        const int ft = tid - kTcFixer0 * 32;
+        int cached = -1, rank = 0, s = 0;
+        uint32_t turn = 0;
+        for (; left > 0; --left) {
+            if (index != cached) {
+                const int l = __ldcg(&pl.tiles[index].x);
+                cached = index;
+                rank = l >= 0 ? rank_of(p, l) : 0;
+            }
+            if (++nb == nblocks) nb = 0, ++index;
+            if (rank == 0 && in_place) continue;
+            if (!mbar_ready_warp(&full[s], turn & 1, p.ctl, abort_flag)) {
+                *abort_flag = 1;
+                break;
+            }
+            if (rank % 16 != 0) {
+                const uint32_t st = smem_u32(ring) + s * stage_bytes;
+                for (int r = ft; r < kTcNB; r += kTcFixers * 32)
+                    for (int c = rank / 8; c < (rank + 15) / 16 * 2; ++c) {
+                        const uint32_t at = st + c / 8 * kTcABlock + r * 128 + (((c % 8) ^ (r & 7)) * 16);
+                        const uint4 v = c * 8 < rank ? keep_first(lds_v4(at), rank - c * 8) : zero4();
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x),
+                                     "r"(v.y), "r"(v.z), "r"(v.w)
+                                     : "memory");
+                    }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&ready[s]);
+                mbar_arrive(&empty[s]);
+            }
+            if (++s == stages) s = 0, ++turn;
+        }
+        pdl_wait();
+    } else if (!kTma && warp >= kTcLoader0) {
+        // ------------------------------ loaders of y ------------------------------
+        const int pt = tid - kTcLoader0 * 32;
+        const uint8_t* yb = reinterpret_cast<const uint8_t*>(p.y_in) + pt * 4;
+        const long long ld = p.ld_in * 4;
+        int tk[2] = {0, 0};   // tokens lane, lane + 32 of the tile
+        int cached = -1, count = 0, rank = 0, issued = 0, s = 0;
+        uint32_t turn = 0;
+        for (; left > 0; --left) {
+            if (index != cached) {
+                const int4 tile = __ldcg(pl.tiles + index);
+                cached = index, count = tile.z;
+                rank = tile.x >= 0 ? rank_of(p, tile.x) : 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (lane + 32 * h < count) tk[h] = __ldcg(pl.perm + tile.y + lane + 32 * h);
+            }
+            const int n0 = nb * kTcNB, n = min(kTcNB, p.N - n0);
+            if (++nb == nblocks) nb = 0, ++index;
+            if (rank == 0 && in_place) continue;
+            if (turn > 0 && !mbar_ready_warp(&empty[s], (turn - 1) & 1, p.ctl, abort_flag)) break;
+            if (issued != p.ctl.debug_skip_stage) {
+                const uint32_t ys = smem_u32(ring) + s * stage_bytes + vblocks * kTcABlock + pt * 4;
+                const uint8_t* src = yb + static_cast<size_t>(n0) * 4;
+#pragma unroll 8
+                for (int j = 0; j < count; ++j) {
+                    const int lo = __shfl_sync(0xffffffffu, tk[0], j & 31);
+                    const int hi = __shfl_sync(0xffffffffu, tk[1], j & 31);
+                    if (pt < n) cp_async<4>(ys + j * kTcNB * 4, src + (j & 32 ? hi : lo) * ld);
+                }
+                cp_async_arrive(&full[s]);
+            }
+            ++issued;
+            if (++s == stages) s = 0, ++turn;
+        }
+        cp_async_wait<0>();
+        pdl_wait();
+    } else if (warp == kTcIssuer) {
+        // ------------------------------ issuer ------------------------------
+        pdl_wait();
+        if (lane == 0) {
+            const uint32_t v0 = smem_u32(sv);
+            int cached = -1, rank = 0, steps = 0, s = 0, d = 0;
+            uint32_t turn = 0, dturn = 0, vturn = 0;
+            long long committed = 0;
+            for (; left > 0; --left) {
+                if (index != cached) {
+                    const int l = __ldcg(&pl.tiles[index].x);
+                    cached = index;
+                    rank = l >= 0 ? rank_of(p, l) : 0;
+                    steps = (rank + 15) / 16;
+                    if (rank > 0 && !mbar_spin_bounded(&vfull, vturn++ & 1, p.ctl, abort_flag)) {
+                        *abort_flag = 1;
+                        break;
+                    }
+                }
+                if (++nb == nblocks) nb = 0, ++index;
+                if (rank == 0 && in_place) continue;
+                if (!mbar_spin_bounded(&ready[s], turn & 1, p.ctl, abort_flag) ||
+                    (rank > 0 && dturn > 0 &&
+                     !mbar_spin_bounded(&dempty[d], (dturn - 1) & 1, p.ctl, abort_flag))) {
+                    *abort_flag = 1;
+                    break;
+                }
+                if (rank > 0) {
+                    tc_fence_after();
+                    const uint32_t a0 = smem_u32(ring) + s * stage_bytes;
+                    bool add = false;
+                    for (int q = 0; q < terms<BF>(); ++q)
+                        for (int k = 0; k < steps; ++k) {
+                            const uint32_t off = (k & 3) * 32;
+                            tc_mma<BF>(tmem + d * kTile, sw128_desc(a0 + (k >> 2) * kTcABlock + off),
+                                       sw128_desc(v0 + (q * vblocks + (k >> 2)) * kTcVBlock + off), add);
+                            add = true;
+                        }
+                    tc_commit(&dfull[d]);
+                    ++committed;
+                    if (++d == kTcDBufs) d = 0, ++dturn;
+                }
+                // everyone who waits for a stage hands it back: a parity tells
+                // the phase meant only from the one before
+                mbar_arrive(&empty[s]);
+                if (++s == stages) s = 0, ++turn;
+            }
+            // no product may still be running when tensor memory is released
+            if (committed > 0) {
+                const long long last = committed - 1;
+                mbar_spin_bounded(&dfull[last % kTcDBufs], static_cast<uint32_t>(last / kTcDBufs) & 1, p.ctl);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------ epilogue ------------------------------
+        const int quarter = warp & 3, half = warp >> 2;   // 32 outputs, 32 tokens
+        const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+        float* yout = static_cast<float*>(p.y_out);
+        const long long out_elems = static_cast<long long>(p.M - 1) * p.ld_out + p.N;
+        int cached = -1, rank = 0, count = 0, s = 0, d = 0;
+        uint32_t turn = 0, dturn = 0;
+        bool ok = true;
+        int4 next = __ldcg(pl.tiles + min(index, pl.max_tiles - 1));   // a tile ahead
+        pdl_wait();
+        pdl_launch_dependents();
+        for (; left > 0; --left) {
+            if (index != cached) {
+                // every warp is done with the old tile, and so is its product;
+                // a failed wait reaches all
+                if (named_bar_any(1, kTcEpilogue * 32, !ok)) break;
+                const int4 tile = next;
+                cached = index, count = tile.z;
+                next = __ldcg(pl.tiles + min(index + 1, pl.max_tiles - 1));
+                float fv = 0.0f;
+                int tv = 0;
+                if (tid < count) {
+                    tv = __ldcg(pl.perm + tile.y + tid);
+                    fv = __ldcg(pl.f + tile.y + tid);
+                }
+                rank = tile.x >= 0 ? rank_of(p, tile.x) : 0;
+                const int pieces = pl.rp / 8;   // of 8 ranks, at most 32
+                for (int i = warp; i < terms<BF>() * count && tile.x >= 0; i += kTcEpilogue) {
+                    const int q = i % terms<BF>(), j = i / terms<BF>();
+                    if (lane < pieces) {
+                        const uint4 v = load16_cg(pl.terms + (static_cast<size_t>(q) * p.M + tile.y + j) * pl.rp + lane * 8);
+                        *reinterpret_cast<uint4*>(sv + (q * vblocks + lane / 8) * kTcVBlock + j * 128 +
+                                                  (((lane % 8) ^ (j & 7)) * 16)) = v;
+                    }
+                }
+                if (tid < kTile) {
+                    row[tid] = static_cast<int>(tv * p.ld_out);
+                    f[tid] = rank > 0 ? fv : 0.0f;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                named_bar_sync(2, kTcEpilogue * 32);
+                if (tid == 0 && rank > 0) mbar_arrive(&vfull);
+            }
+            const int n = nb * kTcNB + quarter * 32 + lane;
+            if (++nb == nblocks) nb = 0, ++index;
+            if (rank == 0 && in_place) continue;
+            const int stage = s, buf = d;
+            const uint32_t parity = turn & 1, dparity = dturn & 1;
+            if (++s == stages) s = 0, ++turn;
+            if (rank > 0 && ++d == kTcDBufs) d = 0, ++dturn;
+            if (ok)
+                ok = mbar_ready_warp(&full[stage], parity, p.ctl, abort_flag) &&
+                     (rank == 0 || mbar_ready_warp(&dfull[buf], dparity, p.ctl, abort_flag));
+            if (!ok) {
+                *abort_flag = 1;
+                continue;   // to the next tile's barrier
+            }
+            tc_fence_after();
+            const int j0 = half * 32;
+            const float* sy = reinterpret_cast<const float*>(ring + static_cast<size_t>(stage) * stage_bytes +
+                                                             vblocks * kTcABlock) +
+                              j0 * kTcNB + quarter * 32 + lane;
+            // the first 8 tokens of this half, or all 32
+            const auto part = [&](auto tokens) {
+                constexpr int T = decltype(tokens)::value;
+                float acc[T], y[T];
+                if (rank > 0) {
+                    tc_ld(tmem + buf * kTile + j0 + lane_off, acc);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < T; ++j) acc[j] = 0.0f;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (rank > 0 && lane == 0) mbar_arrive(&dempty[buf]);
+#pragma unroll
+                for (int j = 0; j < T; ++j) y[j] = sy[j * kTcNB];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[stage]);   // the stage is in registers
+#pragma unroll
+                for (int j = 0; j < T; j += 4) {
+                    const int4 rj = *reinterpret_cast<const int4*>(row + j0 + j);
+                    const float4 fj = *reinterpret_cast<const float4*>(f + j0 + j);
+                    const int o[4] = {rj.x + n, rj.y + n, rj.z + n, rj.w + n};
+                    const float g[4] = {fj.x, fj.y, fj.z, fj.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (n < p.N && j0 + j + i < count && store_ok(p.ctl, o[i], 1, out_elems))
+                            yout[o[i]] = fmaf(g[i], acc[j + i], y[j + i]);
+                }
+            };
+            if (count - j0 > 8) {
+                part(std::integral_constant<int, 32>{});
+            } else if (count - j0 > 0) {
+                part(std::integral_constant<int, 8>{});
+            } else {
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank > 0) mbar_arrive(&dempty[buf]);
+                    mbar_arrive(&empty[stage]);
+                }
+            }
+            __syncwarp();
+        }
+    }
+    // every role is done with tensor memory
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kTcIssuer)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kTcTmemCols));
+}
+
 }  // namespace
 }  // namespace pq2
 
@@ -1585,6 +2035,34 @@ cudaError_t run_ring(const LoraParams& p, const pq2::Plan& pl, cudaStream_t st, 
     return run_ring<BF, YT, 64, kPiece>(p, pl, stages, sb, tb, st, dev);
 }
 
+// fp32 y on the tensor-memory form, where two stages fit and y's offsets and
+// B's rows count in 31 bits.
+template <bool BF, bool kTma>
+cudaError_t run_tc(const LoraParams& p, const pq2::Plan& pl, cudaStream_t st, const DeviceInfo& dev,
+                   bool* taken) {
+    const int vblocks = (p.R + 63) / 64;
+    const int term_bytes = pq2::terms<BF>() * vblocks * pq2::kTcVBlock;
+    const int stage_bytes = vblocks * pq2::kTcABlock + pq2::kTcYBytes;
+    const int stages = std::min(pq2::kTcMaxStages, (dev.max_smem_optin - 2048 - 1024 - term_bytes) / stage_bytes);
+    *taken = stages >= 2 && (static_cast<int64_t>(p.M) - 1) * p.ld_out + p.N < (int64_t(1) << 31) &&
+             static_cast<int64_t>(p.L) * p.N + pq2::kTcNB < (int64_t(1) << 31);
+    if (!*taken) return cudaSuccess;
+    pq2::TcMaps maps = {};
+    if ((kTma && !encode_tmap_2d(&maps.y, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.y_in, p.N, p.M,
+                                 static_cast<uint64_t>(p.ld_in) * 4, pq2::kTcNB, 1, false)) ||
+        !encode_tmap_2d(&maps.b, BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        p.B, p.R, static_cast<uint64_t>(p.L) * p.N, static_cast<uint64_t>(p.R) * 2, 64,
+                        pq2::kTcNB, true))
+        return cudaErrorUnknown;
+    auto kern = pq2::lora_expand_tc<BF, kTma>;
+    static SmemLimit lim;
+    const size_t smem = 1024 + static_cast<size_t>(term_bytes) + static_cast<size_t>(stages) * stage_bytes;
+    const cudaError_t e = ensure_smem(lim, kern, smem);
+    if (e != cudaSuccess) return e;
+    return launch(kern, dim3(dev.num_sms), dim3(pq2::tc_threads<kTma>()), smem, st, true, p, pl, maps, stages,
+                  stage_bytes, term_bytes);
+}
+
 SmemLimit g_plan_smem;  // one for the kernel: run() has several instantiations
 
 template <bool BF, int YT>
@@ -1620,9 +2098,14 @@ cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cu
     // the ring, by 16-byte pieces of y where its rows allow, else (fp32) by
     // values; bf16 rows off their 16 bytes go by plain loads
     constexpr int kPer16 = YT == PQ2_F32 ? 4 : 8;
-    if (p.N % kPer16 == 0 && p.ld_in % kPer16 == 0 && p.ld_out % 4 == 0 && vec &&
-        reinterpret_cast<uintptr_t>(p.y_in) % 16 == 0)
-        return run_ring<BF, YT, 16>(p, pl, st, dev);
+    const bool by16 = p.N % kPer16 == 0 && p.ld_in % kPer16 == 0 &&
+                      reinterpret_cast<uintptr_t>(p.y_in) % 16 == 0;
+    if constexpr (YT == PQ2_F32) {
+        bool taken = false;
+        e = by16 ? run_tc<BF, true>(p, pl, st, dev, &taken) : run_tc<BF, false>(p, pl, st, dev, &taken);
+        if (taken || e != cudaSuccess) return e;
+    }
+    if (by16 && p.ld_out % 4 == 0 && vec) return run_ring<BF, YT, 16>(p, pl, st, dev);
     if constexpr (YT == PQ2_F32) {
         return run_ring<BF, YT, 4>(p, pl, st, dev);
     } else {
