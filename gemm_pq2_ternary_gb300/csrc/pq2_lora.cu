@@ -807,10 +807,11 @@ constexpr int shrink_sets() {
 }
 
 // A warp's share of one pipeline stage.  x0, a0: this lane's first rows of x
-// and A (shared-memory addresses); at[blk]: its chunk in either block of 32.
+// and A (shared-memory addresses); xat, aat: its chunk in either block of 32.
 template <bool BF, int RPW, int NI, int WN>
 __device__ __forceinline__ void shrink_stage(float (&acc)[shrink_sets<RPW, WN>()][RPW][WN][4],
-                                             uint32_t x0, uint32_t a0, const uint32_t (&at)[2]) {
+                                             uint32_t x0, uint32_t a0, const uint32_t (&xat)[2],
+                                             const uint32_t (&aat)[2]) {
     constexpr int kSets = shrink_sets<RPW, WN>();
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk) {
@@ -818,9 +819,9 @@ __device__ __forceinline__ void shrink_stage(float (&acc)[shrink_sets<RPW, WN>()
 #pragma unroll
         for (int r = 0; r < RPW; ++r)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) a[r][h] = lds_v4(a0 + (r * 16 + h * 8) * 128 + at[blk]);
+            for (int h = 0; h < 2; ++h) a[r][h] = lds_v4(a0 + (r * 16 + h * 8) * 128 + aat[blk]);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) c[i] = lds_v4(x0 + i * 8 * 128 + at[blk]);
+        for (int i = 0; i < NI; ++i) c[i] = lds_v4(x0 + i * 8 * 128 + xat[blk]);
 #pragma unroll
         for (int r = 0; r < RPW; ++r)
 #pragma unroll
@@ -837,10 +838,13 @@ __device__ __forceinline__ void shrink_stage(float (&acc)[shrink_sets<RPW, WN>()
 }
 
 // A cluster of CTAs computes one tile: v[64 tokens][R] over its share of K
-// each.  Loader warps bring x and A through a ring of asynchronous copies; a
-// row is 8 chunks of 16 bytes, the halves swapped in odd rows, so that the 8
-// lanes of a 16-byte read (two rows, four chunks) touch all banks once.  A
-// consumer warp owns RPW rank tiles of 16 and WN groups of 8 tokens, and
+// each, through a ring: A by TMA, 16 ranks x 64 columns a box, x by the loader
+// warps' asynchronous copies (its rows are gathered; these copies reach some
+// 17 bytes a cycle and SM, so A does not go the same way).  A row is 8 chunks
+// of 16 bytes; in x's odd rows the halves are swapped, in A's rows the chunks
+// are permuted by the 128-byte swizzle, and a lane takes the rank whose row
+// puts the 8 lanes of a 16-byte read (two rows, four chunks) into different
+// banks.  A consumer warp owns RPW rank tiles of 16 and WN groups of 8 tokens, and
 // waits for nothing but its stage.  Every CTA stores its partials of token j
 // into the shared memory of CTA j % splits of the cluster, which adds them up,
 // CTA by CTA in order, and writes the token's 16-bit terms: one cluster
@@ -849,9 +853,11 @@ constexpr int kShrinkLoaders = 4;
 
 template <bool BF, int RPW, int WN>
 __global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
-    lora_shrink_tiles(pq2h::LoraParams p, Plan pl, int splits, int k_split) {
+    lora_shrink_tiles(pq2h::LoraParams p, Plan pl, const __grid_constant__ CUtensorMap map_a,
+                      int splits, int k_split) {
     constexpr int kStages = shrink_stages<RPW, WN>();
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);   // swizzled rows
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
     __shared__ int abort_word;
     volatile int* abort_flag = &abort_word;
@@ -870,7 +876,7 @@ __global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
     const int busy = ((rank + 16 * RPW - 1) / (16 * RPW)) * ((count + 8 * WN - 1) / (8 * WN));
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], kShrinkLoaders * 32);
+            mbar_init(&full[s], kShrinkLoaders * 32 + 1);
             mbar_init(&empty[s], busy);
         }
         abort_word = 0;
@@ -886,6 +892,9 @@ __global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
     const int stage_bytes = (kTile + r16) * 128;
     const uint32_t base = smem_u32(smem);
     const int rt0 = warp / kTokenWarps * RPW, n0 = warp % kTokenWarps * WN;
+    // the rank (of 8) that this lane's row of a fragment stands for: lanes g
+    // and g + 1 of a read take rows 4 apart, whose chunks lie 4 apart
+    const int gr = (g >> 1) | ((g & 1) << 2);
     const bool works = warp < kShrinkWarps && rt0 * 16 < rank && n0 * 8 < count;
     float sum[RPW][WN][4];
 #pragma unroll
@@ -897,45 +906,43 @@ __global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
 
     if (warp >= kShrinkWarps) {
         // thread -> chunk pt % 8 of rows pt / 8 + 16 i.  Rows past the rank or
-        // the tile are left as they are in shared memory: a row of A only
-        // reaches its own rank's sums, a row of x its own token's, and those
-        // are not stored.  Columns past K enter every sum: zeros.
+        // the tile hold anything: a row of A only reaches its own rank's sums,
+        // a row of x its own token's, and those are not stored.  Columns past
+        // K enter every sum: zeros, in x here and in A past the map's end (a
+        // share of K ends on a multiple of 64 otherwise).
         const int pt = tid - kShrinkWarps * 32;
         const int chunk = pt & 7, row0 = pt >> 3;
         constexpr int kRows = kShrinkLoaders * 4;   // rows per round
-        constexpr int kXRounds = kTile / kRows, kARounds = kShrinkWarps / kTokenWarps * RPW * 16 / kRows;
+        constexpr int kXRounds = kTile / kRows;
         const uint32_t dst0 = base + row0 * 128 + ((chunk ^ ((row0 & 1) * 4)) * 16);
-        const uint16_t *xs[kXRounds], *as[kARounds];
+        const uint16_t* xs[kXRounds];
 #pragma unroll
         for (int i = 0; i < kXRounds; ++i) {
             const int j = row0 + kRows * i;
             xs[i] = j < count ? p.x + static_cast<size_t>(pl.perm[first + j]) * p.ld_x + k0 + chunk * 8
                               : nullptr;
         }
-#pragma unroll
-        for (int i = 0; i < kARounds; ++i) {
-            const int r = row0 + kRows * i;
-            as[i] = r < rank ? p.A + (static_cast<size_t>(l) * p.R + r) * p.K + k0 + chunk * 8 : nullptr;
-        }
-        int s = 0;
+        const int boxes = (rank + 15) / 16;
+        int s = 0, issued = 0;
         uint32_t turn = 0;
-        for (int step = 0; step < steps; ++step) {
+        for (; issued < steps; ++issued) {
             if (turn > 0 && !mbar_ready_warp(&empty[s], (turn - 1) & 1, p.ctl, abort_flag)) break;
-            if (step != p.ctl.debug_skip_stage) {  // else withheld (timeout test)
+            if (issued != p.ctl.debug_skip_stage) {  // else withheld (timeout test)
                 const uint32_t st = dst0 + s * stage_bytes;
-                const int k = step * kStageK;
+                const int k = issued * kStageK;
+                if (warp == kShrinkWarps) {
+                    if (lane == 0) mbar_arrive_expect_tx(&full[s], boxes * 16 * 128);
+                    __syncwarp();
+                    if (lane < boxes)
+                        tma_load_2d(smem + s * stage_bytes + (kTile + lane * 16) * 128, &map_a, k0 + k,
+                                    l * p.R + lane * 16, &full[s]);
+                }
                 if (k0 + k + kStageK <= k1) {
-#pragma unroll
-                    for (int i = 0; i < kARounds; ++i)
-                        if (as[i]) cp_async<16>(st + (kTile + i * kRows) * 128, as[i] + k);
 #pragma unroll
                     for (int i = 0; i < kXRounds; ++i)
                         if (xs[i]) cp_async<16>(st + i * kRows * 128, xs[i] + k);
                 } else {
                     const bool in = k0 + k + chunk * 8 < k1;
-#pragma unroll
-                    for (int i = 0; i < kARounds; ++i)
-                        if (as[i]) cp_async16(st + (kTile + i * kRows) * 128, in ? as[i] + k : p.A, in ? 16 : 0);
 #pragma unroll
                     for (int i = 0; i < kXRounds; ++i)
                         if (xs[i]) cp_async16(st + i * kRows * 128, in ? xs[i] + k : p.x, in ? 16 : 0);
@@ -944,10 +951,16 @@ __global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
             }
             if (++s == kStages) s = 0, ++turn;
         }
+        // the last copies land before the CTA ends, whatever the consumers do
+        for (int k = max(0, issued - kStages); k < issued; ++k)
+            if (k != p.ctl.debug_skip_stage)
+                mbar_ready_warp(&full[k % kStages], static_cast<uint32_t>(k / kStages) & 1, p.ctl);
         cp_async_wait<0>();
     } else if (works) {
-        const uint32_t at[2] = {static_cast<uint32_t>((t ^ ((g & 1) * 4)) * 16),
-                                static_cast<uint32_t>(((4 + t) ^ ((g & 1) * 4)) * 16)};
+        const uint32_t xat[2] = {static_cast<uint32_t>((t ^ ((g & 1) * 4)) * 16),
+                                 static_cast<uint32_t>(((4 + t) ^ ((g & 1) * 4)) * 16)};
+        const uint32_t aat[2] = {static_cast<uint32_t>((t ^ gr) * 16),
+                                 static_cast<uint32_t>(((4 + t) ^ gr) * 16)};
         constexpr int kSets = shrink_sets<RPW, WN>();
         float acc[kSets][RPW][WN][4];
 #pragma unroll
@@ -966,13 +979,13 @@ __global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
                 break;
             }
             const uint32_t st = base + s * stage_bytes;
-            const uint32_t x0 = st + (n0 * 8 + g) * 128, a0 = st + (kTile + rt0 * 16 + g) * 128;
+            const uint32_t x0 = st + (n0 * 8 + g) * 128, a0 = st + (kTile + rt0 * 16 + gr) * 128;
             // one group of tokens, or all of this warp's (columns past the
             // tile's last token hold anything and are not stored)
             if (count - n0 * 8 > 8)
-                shrink_stage<BF, RPW, WN, WN>(acc, x0, a0, at);
+                shrink_stage<BF, RPW, WN, WN>(acc, x0, a0, xat, aat);
             else
-                shrink_stage<BF, RPW, 1, WN>(acc, x0, a0, at);
+                shrink_stage<BF, RPW, 1, WN>(acc, x0, a0, xat, aat);
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
             if (++s == kStages) s = 0, ++turn;
@@ -1010,7 +1023,7 @@ __global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
                 for (int r = 0; r < RPW; ++r)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const int rr = (rt0 + r) * 16 + c * 8 + g;
+                        const int rr = (rt0 + r) * 16 + c * 8 + gr;
                         if (rr >= rank) continue;
                         if (splits > 1)
                             st_cluster_f32(to + rr * 4, sum[r][i][c * 2 + h]);
@@ -1969,7 +1982,12 @@ cudaError_t run_shrink(const LoraParams& p, const pq2::Plan& pl, const Layout& l
     static SmemLimit lim;
     const size_t r16 = static_cast<size_t>((p.R + 16 * RPW - 1) / (16 * RPW) * (16 * RPW));
     const size_t inbox = static_cast<size_t>(lay.splits) * ((kTile + lay.splits - 1) / lay.splits) * r16 * 4;
-    const size_t smem = (kTile + r16) * 128 * pq2::shrink_stages<RPW, WN>() + inbox;
+    const size_t smem = 1024 + (kTile + r16) * 128 * pq2::shrink_stages<RPW, WN>() + inbox;
+    CUtensorMap map_a;
+    if (!encode_tmap_2d(&map_a, BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        p.A, p.K, static_cast<uint64_t>(p.L) * p.R, static_cast<uint64_t>(p.K) * 2,
+                        pq2::kStageK, 16, true))
+        return cudaErrorUnknown;
     cudaError_t e = ensure_smem(lim, kern, smem);
     if (e != cudaSuccess) return e;
     if (lay.splits > 8) {
@@ -1992,7 +2010,7 @@ cudaError_t run_shrink(const LoraParams& p, const pq2::Plan& pl, const Layout& l
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = lay.splits > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, p, pl, lay.splits, lay.k_split);
+    return cudaLaunchKernelEx(&cfg, kern, p, pl, map_a, lay.splits, lay.k_split);
 }
 
 // The ring's shared memory: v's terms, then as many stages as fit (0: fewer

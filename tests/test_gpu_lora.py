@@ -116,6 +116,8 @@ SHAPES = [
     (128, 128, 40, 8, 128, "f16", "f32", {}),
     (100, 1664, 260, 40, 2, "bf16", "f32", dict(ids="runs")),
     (129, 640, 300, 16, 3, "f16", "f32", {}),
+    (150, 8, 40, 16, 3, "f16", "f32", {}),
+    (150, 24, 260, 40, 3, "bf16", "f32", {}),
     (4097, 64, 36, 8, 3, "f16", "f32", {}),
     (9000, 64, 36, 8, 1000, "f16", "f32", {}),
     # whole 16-byte rows of y and more than 128 tokens: the copy ring
