@@ -620,7 +620,8 @@ __global__ void __launch_bounds__(kExpandMaxWarps * 32)
 struct Plan {
     int* perm;           // [M] tokens, sorted by adapter
     int4* tiles;         // adapter (-1: none), first position, tokens
-    int* num_tiles;
+    int* num_tiles;      // [0] tiles, [1] those with an adapter
+    unsigned* taken;     // times that expand took items from the counter
     uint16_t* terms;     // [terms][M][rp], by position
     float* f;            // [M] scale and power of two, by position
     int max_tiles;
@@ -707,7 +708,9 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
         at_tile += (total + kTile - 1) / kTile;
     }
     if (threadIdx.x == nthreads - 1) {
-        *pl.num_tiles = at_tile;
+        pl.num_tiles[0] = at_tile;
+        pl.num_tiles[1] = tfirst[p.L];   // tokens without an adapter come last
+        *pl.taken = 0u;
         off[bins] = p.M;
     }
     __syncthreads();
@@ -1435,19 +1438,28 @@ __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
 // back: 200 instructions a warp and item where the mma.sync form takes 800 and
 // waits for its own results.  A lane is an output: y is read and written 128
 // bytes a warp, one value a lane, so its rows need no alignment for that.
-// Two more warps look at each item between its copies and its product: where
-// the rank is no multiple of 16, they put zeros over the ranks past it that
-// the product would read (they may hold anything, and v's zero times a NaN is
-// a NaN).
+// A CTA takes a contiguous share of the items; where there are many, the
+// shares stop at three quarters and the rest is taken from a counter, a few
+// items at a time (with shares alone the median CTA of 4096 tokens was done at
+// 116 us and the last at 134).  The items of one tile that a CTA takes in a
+// row are a unit.  The scheduler warp fixes the units ahead and publishes them
+// to the others; one warp loads a unit's terms while the unit before is under
+// way (a tile change took 3 us otherwise); one looks at each item between its copies and its product: where the rank is no
+// multiple of 16, it puts zeros over the ranks past it that the product would
+// read (they may hold anything, and v's zero times a NaN is a NaN).
+// Everyone who waits on a barrier sees each of its phases: a parity tells the
+// phase meant only from the one before.
 constexpr int kTcEpilogue = 8;      // warps, two per quarter of the lanes
-constexpr int kTcIssuer = kTcEpilogue;
-constexpr int kTcProducer = kTcIssuer + 1;
-constexpr int kTcFixer0 = kTcProducer + 1, kTcFixers = 2;
-constexpr int kTcLoader0 = kTcFixer0 + kTcFixers, kTcLoaders = 4;   // where y does not come by TMA
+constexpr int kTcIssuer = 8, kTcProducer = 9, kTcFixer = 10, kTcTerms = 11, kTcScheduler = 12;
+constexpr int kTcLoader0 = 13, kTcLoaders = 4;   // where y does not come by TMA
 template <bool kTma>
 constexpr int tc_threads() {
     return (kTcLoader0 + (kTma ? 0 : kTcLoaders)) * 32;
 }
+constexpr int kTcUnit = 8;          // items of a unit, at most
+constexpr int kTcTail = 2;          // items taken at a time from the counter
+constexpr int kTcShares = 16;       // items a CTA from which there is a counter
+constexpr int kTcUnits = 2;         // units known at a time
 constexpr int kTcNB = 128;
 constexpr int kTcMaxStages = 4;
 constexpr int kTcDBufs = 4;
@@ -1517,9 +1529,10 @@ __device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[8]) {
 }
 
 // Tensor maps: y_in fp32 [M][N], box 128 x 1 (gathered by four rows); B 16-bit
-// [L * N][R], box 64 x 128, 128-byte swizzle, zeros past R.
+// [L * N][R], box 64 x 128, 128-byte swizzle, zeros past R; v's terms 16-bit
+// [terms * M][rp], box 64 x 64, the same.
 struct TcMaps {
-    CUtensorMap y, b;
+    CUtensorMap y, b, terms;
 };
 
 // Rows r0 .. r3 of columns x .. x + 127 (x a multiple of 4) to four rows of
@@ -1536,332 +1549,400 @@ __device__ __forceinline__ void tma_gather4(void* dst, const void* map, int x, i
 
 // kTma: y's rows start on 16-byte boundaries and come by TMA, four tokens an
 // instruction; else value by value, by warps of their own.
+struct TcUnit {
+    int adapter, first, count, rank;   // count 0: no more units
+    int nb0, nb1;
+    int slot;
+};
+struct TcShared {
+    uint64_t full[kTcMaxStages];    // an item's y and B are there
+    uint64_t ready[kTcMaxStages];   // B as the product may read it
+    uint64_t empty[kTcMaxStages];   // everyone is done with the stage
+    uint64_t dfull[kTcDBufs];       // an item's product is there
+    uint64_t dempty[kTcDBufs];      // read by the epilogue's warps
+    uint64_t vfull[2];              // a unit's terms, rows and scales are there
+    uint64_t vempty[2];             // everyone is done with them
+    uint64_t ufull[kTcUnits];       // a unit is published
+    uint64_t uempty[kTcUnits];      // everyone has taken it
+    // read as 16-byte vectors
+    alignas(16) int row[2][kTile];  // start of each token's y'
+    alignas(16) float f[2][kTile];
+    alignas(16) int token[kTcUnits][kTile];   // a unit's tokens (M past its count)
+    TcUnit unit[kTcUnits];
+    uint32_t tmem_base;
+    int abort_word;
+};
+
+// The k-th unit, for every warp but the scheduler's; false: no more, or a wait
+// ran out.  A warp is done with its place (u.slot) when it calls release_unit.
+__device__ __forceinline__ bool take_unit(TcShared& sh, int k, TcUnit& u, const DevCtl& ctl) {
+    volatile int* abort_flag = &sh.abort_word;
+    const int slot = k % kTcUnits;
+    if (!mbar_ready_warp(&sh.ufull[slot], static_cast<uint32_t>(k / kTcUnits) & 1, ctl, abort_flag)) {
+        *abort_flag = 1;
+        return false;
+    }
+    u = sh.unit[slot];
+    return u.count > 0;
+}
+__device__ __forceinline__ void release_unit(TcShared& sh, const TcUnit& u) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.uempty[u.slot]);
+}
+
 template <bool BF, bool kTma>
 __global__ void __launch_bounds__(tc_threads<kTma>(), 1)
     lora_expand_tc(pq2h::LoraParams p, Plan pl, const __grid_constant__ TcMaps maps, int stages,
                    int stage_bytes, int term_bytes) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full[kTcMaxStages];    // an item's y and B are there
-    __shared__ __align__(8) uint64_t ready[kTcMaxStages];   // B as the product may read it
-    __shared__ __align__(8) uint64_t empty[kTcMaxStages];   // looked at, read by the epilogue
-    __shared__ __align__(8) uint64_t dfull[kTcDBufs];       // an item's product is there
-    __shared__ __align__(8) uint64_t dempty[kTcDBufs];      // read by the epilogue's warps
-    __shared__ __align__(8) uint64_t vfull;                 // a tile's terms are there (ranks > 0)
-    __shared__ __align__(16) int row[kTile];                // start of each token's y'
-    __shared__ __align__(16) float f[kTile];
-    __shared__ uint32_t tmem_base;
-    __shared__ int abort_word;
-    volatile int* abort_flag = &abort_word;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    __shared__ __align__(16) TcShared sh;
+    volatile int* abort_flag = &sh.abort_word;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint8_t* sv = smem + ((1024 - (smem_u32(smem) & 1023)) & 1023);
-    uint8_t* ring = sv + term_bytes;
+    // terms of two units, then the stages; swizzled rows from 1024 on
+    uint8_t* sv = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t* ring = sv + 2 * term_bytes;
     if (tid == 0) {
         for (int s = 0; s < stages; ++s) {
-            mbar_init(&full[s], kTma ? 1 : kTcLoaders * 32 + 1);
-            mbar_init(&ready[s], kTcFixers);
-            mbar_init(&empty[s], kTcEpilogue + kTcFixers + 1);
+            mbar_init(&sh.full[s], kTma ? 1 : kTcLoaders * 32 + 1);
+            mbar_init(&sh.ready[s], 1);
+            mbar_init(&sh.empty[s], kTcEpilogue + 2);
         }
         for (int i = 0; i < kTcDBufs; ++i) {
-            mbar_init(&dfull[i], 1);
-            mbar_init(&dempty[i], kTcEpilogue);
+            mbar_init(&sh.dfull[i], 1);
+            mbar_init(&sh.dempty[i], kTcEpilogue);
         }
-        mbar_init(&vfull, 1);
-        abort_word = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.vfull[i], 2);
+            mbar_init(&sh.vempty[i], kTcEpilogue + 1);
+        }
+        for (int i = 0; i < kTcUnits; ++i) {
+            mbar_init(&sh.ufull[i], 1);
+            mbar_init(&sh.uempty[i], kTcEpilogue + 4 + (kTma ? 0 : kTcLoaders));
+        }
+        sh.abort_word = 0;
         fence_mbar_init();
     }
     if (warp == kTcIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_u32(&tmem_base)),
+                         smem_u32(&sh.tmem_base)),
                      "r"(kTcTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_base;
-    const int nblocks = (p.N + kTcNB - 1) / kTcNB;
-    const bool in_place = p.y_in == p.y_out && p.ld_in == p.ld_out;
-    // the plan is complete before shrink lets this kernel start, as are y and
-    // B; v's terms are not
-    const long long total = static_cast<long long>(__ldcg(pl.num_tiles)) * nblocks;
-    const long long it0 = total * blockIdx.x / gridDim.x, it1 = total * (blockIdx.x + 1) / gridDim.x;
-    int index = static_cast<int>(it0 / nblocks), nb = static_cast<int>(it0 - static_cast<long long>(index) * nblocks);
-    int left = static_cast<int>(it1 - it0);
+    const uint32_t tmem = sh.tmem_base;
     const int vblocks = (p.R + 63) / 64;
+    TcUnit u;
 
-    if (warp == kTcProducer) {
-        // ------------------------------ producer ------------------------------
-        int tk[4] = {0, 0, 0, 0};   // tokens 4 lane .. + 3 of the tile
-        int cached = -1, l = -1, used = 0, fours = 0, issued = 0, s = 0;
-        uint32_t turn = 0;
-        for (; left > 0; --left) {
-            if (index != cached) {
-                const int4 tile = __ldcg(pl.tiles + index);
-                cached = index, l = tile.x;
-                used = l >= 0 ? (rank_of(p, l) + 63) / 64 : 0;
-                fours = (tile.z + 3) / 4;
-                if constexpr (kTma) {
+    if (warp == kTcScheduler) {
+        // ------------------------------ scheduler ------------------------------
+        // the plan is complete before shrink lets this kernel start
+        const bool in_place = p.y_in == p.y_out && p.ld_in == p.ld_out;
+        const int nblocks = (p.N + kTcNB - 1) / kTcNB;
+        const long long total = static_cast<long long>(__ldcg(pl.num_tiles + (in_place ? 1 : 0))) * nblocks;
+        const long long grid = gridDim.x, shared = total >= kTcShares * grid ? total / 4 * 3 : total;
+        long long pos = shared * blockIdx.x / grid, end = shared * (blockIdx.x + 1) / grid;
+        for (int k = 0;;) {
+            if (pos >= end && shared < total) {
+                int got = 0;
+                if (lane == 0) got = static_cast<int>(atomicAdd(pl.taken, 1u));
+                pos = shared + static_cast<long long>(__shfl_sync(0xffffffffu, got, 0)) * kTcTail;
+                end = min(pos + kTcTail, total);
+            }
+            const int slot = k % kTcUnits;
+            TcUnit r = {-1, 0, 0, 0, 0, 0, slot};
+            int tok[2] = {p.M, p.M};
+            if (pos < end) {
+                const int4 tile = __ldcg(pl.tiles + pos / nblocks);
+                const int nb0 = static_cast<int>(pos % nblocks);
+                const int n = static_cast<int>(min(static_cast<long long>(min(kTcUnit, nblocks - nb0)), end - pos));
+                const int rank = tile.x >= 0 ? rank_of(p, tile.x) : 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        tk[i] = 4 * lane + i < tile.z ? __ldcg(pl.perm + tile.y + 4 * lane + i) : p.M;
+                for (int h = 0; h < 2; ++h)
+                    if (lane + 32 * h < tile.z) tok[h] = __ldcg(pl.perm + tile.y + lane + 32 * h);
+                pos += n;
+                if (rank == 0 && in_place) continue;
+                r = {tile.x, tile.y, tile.z, rank, nb0, nb0 + n, slot};
+            }
+            if (k >= kTcUnits &&
+                !mbar_ready_warp(&sh.uempty[slot], static_cast<uint32_t>(k / kTcUnits - 1) & 1, p.ctl,
+                                 abort_flag)) {
+                *abort_flag = 1;
+                break;
+            }
+            sh.token[slot][lane] = tok[0];
+            sh.token[slot][lane + 32] = tok[1];
+            if (lane == 0) sh.unit[slot] = r;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.ufull[slot]);
+            if (r.count == 0) break;
+            ++k;
+        }
+        pdl_wait();
+    } else if (warp == kTcProducer) {
+        // ------------------------------ producer ------------------------------
+        // y and B are older than the kernel before; v's terms are not
+        int issued = 0, s = 0;
+        uint32_t turn = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            if (!take_unit(sh, k, u, p.ctl)) break;
+            const int used = (u.rank + 63) / 64, fours = (u.count + 3) / 4;
+            const int4 tk = *reinterpret_cast<const int4*>(&sh.token[u.slot][(lane & 15) * 4]);
+            release_unit(sh, u);
+            for (int nb = u.nb0; nb < u.nb1; ++nb) {
+                if (turn > 0 && !mbar_ready_warp(&sh.empty[s], (turn - 1) & 1, p.ctl, abort_flag)) {
+                    ok = false;
+                    break;
                 }
+                if (issued != p.ctl.debug_skip_stage) {  // else withheld (timeout test)
+                    uint8_t* stage = ring + static_cast<size_t>(s) * stage_bytes;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&sh.full[s],
+                                              (kTma ? fours * 4 * kTcNB * 4 : 0) + used * kTcABlock);
+                    __syncwarp();
+                    if (lane < used)
+                        tma_load_2d(stage + lane * kTcABlock, &maps.b, lane * 64,
+                                    u.adapter * p.N + nb * kTcNB, &sh.full[s]);
+                    if (kTma && lane < fours)
+                        tma_gather4(stage + vblocks * kTcABlock + lane * 4 * kTcNB * 4, &maps.y, nb * kTcNB,
+                                    tk.x, tk.y, tk.z, tk.w, &sh.full[s]);
+                }
+                ++issued;
+                if (++s == stages) s = 0, ++turn;
             }
-            const int n0 = nb * kTcNB;
-            if (++nb == nblocks) nb = 0, ++index;
-            if (used == 0 && in_place) continue;   // nothing to read or write
-            if (turn > 0 && !mbar_ready_warp(&empty[s], (turn - 1) & 1, p.ctl, abort_flag)) break;
-            if (issued != p.ctl.debug_skip_stage) {  // else withheld (timeout test)
-                uint8_t* stage = ring + static_cast<size_t>(s) * stage_bytes;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&full[s],
-                                          (kTma ? fours * 4 * kTcNB * 4 : 0) + used * kTcABlock);
-                __syncwarp();
-                if (lane < used)
-                    tma_load_2d(stage + lane * kTcABlock, &maps.b, lane * 64, l * p.N + n0, &full[s]);
-                if (kTma && lane < fours)
-                    tma_gather4(stage + vblocks * kTcABlock + lane * 4 * kTcNB * 4, &maps.y, n0, tk[0], tk[1],
-                                tk[2], tk[3], &full[s]);
-            }
-            ++issued;
-            if (++s == stages) s = 0, ++turn;
         }
         // the last copies land before the CTA ends, whatever the others do
         for (int k = max(0, issued - stages); k < issued; ++k)
             if (k != p.ctl.debug_skip_stage)
-                mbar_ready_warp(&full[k % stages], static_cast<uint32_t>(k / stages) & 1, p.ctl);
+                mbar_ready_warp(&sh.full[k % stages], static_cast<uint32_t>(k / stages) & 1, p.ctl);
         pdl_wait();
-    } else if (warp >= kTcFixer0 && warp < kTcLoader0) {
-        // ------------------------------ fixers ------------------------------
-        const int ft = tid - kTcFixer0 * 32;
-        int cached = -1, rank = 0, s = 0;
+    } else if (warp == kTcFixer) {
+        // ------------------------------ fixer ------------------------------
+        int s = 0;
         uint32_t turn = 0;
-        for (; left > 0; --left) {
-            if (index != cached) {
-                const int l = __ldcg(&pl.tiles[index].x);
-                cached = index;
-                rank = l >= 0 ? rank_of(p, l) : 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            if (!take_unit(sh, k, u, p.ctl)) break;
+            release_unit(sh, u);
+            for (int nb = u.nb0; nb < u.nb1; ++nb) {
+                ok = mbar_ready_warp(&sh.full[s], turn & 1, p.ctl, abort_flag);
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+                if (u.rank % 16 != 0) {
+                    const uint32_t st = smem_u32(ring) + s * stage_bytes;
+                    for (int r = lane; r < kTcNB; r += 32)
+                        for (int c = u.rank / 8; c < (u.rank + 15) / 16 * 2; ++c) {
+                            const uint32_t at = st + c / 8 * kTcABlock + r * 128 + (((c % 8) ^ (r & 7)) * 16);
+                            const uint4 v = c * 8 < u.rank ? keep_first(lds_v4(at), u.rank - c * 8) : zero4();
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x),
+                                         "r"(v.y), "r"(v.z), "r"(v.w)
+                                         : "memory");
+                        }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh.ready[s]);
+                    mbar_arrive(&sh.empty[s]);
+                }
+                if (++s == stages) s = 0, ++turn;
             }
-            if (++nb == nblocks) nb = 0, ++index;
-            if (rank == 0 && in_place) continue;
-            if (!mbar_ready_warp(&full[s], turn & 1, p.ctl, abort_flag)) {
+        }
+        pdl_wait();
+    } else if (warp == kTcTerms) {
+        // ------------------------------ terms ------------------------------
+        pdl_wait();
+        int k = 0;
+        for (;; ++k) {
+            if (!take_unit(sh, k, u, p.ctl)) break;
+            const int b = k & 1;
+            const int tok[2] = {sh.token[u.slot][lane], sh.token[u.slot][lane + 32]};
+            release_unit(sh, u);
+            if (k >= 2 && !mbar_ready_warp(&sh.vempty[b], static_cast<uint32_t>(k / 2 - 1) & 1, p.ctl, abort_flag)) {
                 *abort_flag = 1;
                 break;
             }
-            if (rank % 16 != 0) {
-                const uint32_t st = smem_u32(ring) + s * stage_bytes;
-                for (int r = ft; r < kTcNB; r += kTcFixers * 32)
-                    for (int c = rank / 8; c < (rank + 15) / 16 * 2; ++c) {
-                        const uint32_t at = st + c / 8 * kTcABlock + r * 128 + (((c % 8) ^ (r & 7)) * 16);
-                        const uint4 v = c * 8 < rank ? keep_first(lds_v4(at), rank - c * 8) : zero4();
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x),
-                                     "r"(v.y), "r"(v.z), "r"(v.w)
-                                     : "memory");
-                    }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            }
+            const int used = (u.rank + 63) / 64, boxes = terms<BF>() * used;
+            if (lane == 0) mbar_arrive_expect_tx(&sh.vfull[b], boxes * kTcVBlock);
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&ready[s]);
-                mbar_arrive(&empty[s]);
+            // rows past the tile's are its neighbours' and give columns that
+            // are not stored
+            if (lane < boxes) {
+                const int q = lane / used, c = lane % used;
+                tma_load_2d(sv + b * term_bytes + (q * vblocks + c) * kTcVBlock, &maps.terms, c * 64,
+                            q * p.M + u.first, &sh.vfull[b]);
             }
-            if (++s == stages) s = 0, ++turn;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (lane + 32 * h < u.count) {
+                    sh.row[b][lane + 32 * h] = static_cast<int>(tok[h] * p.ld_out);
+                    sh.f[b][lane + 32 * h] = u.rank > 0 ? __ldcg(pl.f + u.first + lane + 32 * h) : 0.0f;
+                }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.vfull[b]);
         }
-        pdl_wait();
+        // the last copies land before the CTA ends, whatever the others do
+        for (int i = max(0, k - 2); i < k; ++i)
+            mbar_ready_warp(&sh.vfull[i & 1], static_cast<uint32_t>(i / 2) & 1, p.ctl);
     } else if (!kTma && warp >= kTcLoader0) {
         // ------------------------------ loaders of y ------------------------------
         const int pt = tid - kTcLoader0 * 32;
         const uint8_t* yb = reinterpret_cast<const uint8_t*>(p.y_in) + pt * 4;
         const long long ld = p.ld_in * 4;
-        int tk[2] = {0, 0};   // tokens lane, lane + 32 of the tile
-        int cached = -1, count = 0, rank = 0, issued = 0, s = 0;
+        int issued = 0, s = 0;
         uint32_t turn = 0;
-        for (; left > 0; --left) {
-            if (index != cached) {
-                const int4 tile = __ldcg(pl.tiles + index);
-                cached = index, count = tile.z;
-                rank = tile.x >= 0 ? rank_of(p, tile.x) : 0;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (lane + 32 * h < count) tk[h] = __ldcg(pl.perm + tile.y + lane + 32 * h);
-            }
-            const int n0 = nb * kTcNB, n = min(kTcNB, p.N - n0);
-            if (++nb == nblocks) nb = 0, ++index;
-            if (rank == 0 && in_place) continue;
-            if (turn > 0 && !mbar_ready_warp(&empty[s], (turn - 1) & 1, p.ctl, abort_flag)) break;
-            if (issued != p.ctl.debug_skip_stage) {
-                const uint32_t ys = smem_u32(ring) + s * stage_bytes + vblocks * kTcABlock + pt * 4;
-                const uint8_t* src = yb + static_cast<size_t>(n0) * 4;
-#pragma unroll 8
-                for (int j = 0; j < count; ++j) {
-                    const int lo = __shfl_sync(0xffffffffu, tk[0], j & 31);
-                    const int hi = __shfl_sync(0xffffffffu, tk[1], j & 31);
-                    if (pt < n) cp_async<4>(ys + j * kTcNB * 4, src + (j & 32 ? hi : lo) * ld);
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            if (!take_unit(sh, k, u, p.ctl)) break;
+            const int tk[2] = {sh.token[u.slot][lane], sh.token[u.slot][lane + 32]};
+            release_unit(sh, u);
+            for (int nb = u.nb0; nb < u.nb1; ++nb) {
+                const int n0 = nb * kTcNB, n = min(kTcNB, p.N - n0);
+                if (turn > 0 && !mbar_ready_warp(&sh.empty[s], (turn - 1) & 1, p.ctl, abort_flag)) {
+                    ok = false;
+                    break;
                 }
-                cp_async_arrive(&full[s]);
+                if (issued != p.ctl.debug_skip_stage) {
+                    const uint32_t ys = smem_u32(ring) + s * stage_bytes + vblocks * kTcABlock + pt * 4;
+                    const uint8_t* src = yb + static_cast<size_t>(n0) * 4;
+#pragma unroll 8
+                    for (int j = 0; j < u.count; ++j) {
+                        const int lo = __shfl_sync(0xffffffffu, tk[0], j & 31);
+                        const int hi = __shfl_sync(0xffffffffu, tk[1], j & 31);
+                        if (pt < n) cp_async<4>(ys + j * kTcNB * 4, src + (j & 32 ? hi : lo) * ld);
+                    }
+                    cp_async_arrive(&sh.full[s]);
+                }
+                ++issued;
+                if (++s == stages) s = 0, ++turn;
             }
-            ++issued;
-            if (++s == stages) s = 0, ++turn;
         }
         cp_async_wait<0>();
         pdl_wait();
     } else if (warp == kTcIssuer) {
         // ------------------------------ issuer ------------------------------
-        pdl_wait();
-        if (lane == 0) {
-            const uint32_t v0 = smem_u32(sv);
-            int cached = -1, rank = 0, steps = 0, s = 0, d = 0;
-            uint32_t turn = 0, dturn = 0, vturn = 0;
-            long long committed = 0;
-            for (; left > 0; --left) {
-                if (index != cached) {
-                    const int l = __ldcg(&pl.tiles[index].x);
-                    cached = index;
-                    rank = l >= 0 ? rank_of(p, l) : 0;
-                    steps = (rank + 15) / 16;
-                    if (rank > 0 && !mbar_spin_bounded(&vfull, vturn++ & 1, p.ctl, abort_flag)) {
-                        *abort_flag = 1;
-                        break;
+        int s = 0, d = 0;
+        uint32_t turn = 0, dturn = 0;
+        long long committed = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            if (!take_unit(sh, k, u, p.ctl)) break;
+            release_unit(sh, u);
+            if (lane == 0) {
+                const int steps = (u.rank + 15) / 16;
+                const uint32_t v0 = smem_u32(sv) + (k & 1) * term_bytes;
+                ok = mbar_spin_bounded(&sh.vfull[k & 1], static_cast<uint32_t>(k / 2) & 1, p.ctl, abort_flag);
+                for (int nb = u.nb0; nb < u.nb1 && ok; ++nb) {
+                    ok = mbar_spin_bounded(&sh.ready[s], turn & 1, p.ctl, abort_flag) &&
+                         (steps == 0 || dturn == 0 ||
+                          mbar_spin_bounded(&sh.dempty[d], (dturn - 1) & 1, p.ctl, abort_flag));
+                    if (!ok) break;
+                    if (steps > 0) {
+                        tc_fence_after();
+                        const uint32_t a0 = smem_u32(ring) + s * stage_bytes;
+                        bool add = false;
+                        for (int q = 0; q < terms<BF>(); ++q)
+                            for (int i = 0; i < steps; ++i) {
+                                const uint32_t off = (i & 3) * 32;
+                                tc_mma<BF>(tmem + d * kTile, sw128_desc(a0 + (i >> 2) * kTcABlock + off),
+                                           sw128_desc(v0 + (q * vblocks + (i >> 2)) * kTcVBlock + off), add);
+                                add = true;
+                            }
+                        tc_commit(&sh.dfull[d]);
+                        ++committed;
+                        if (++d == kTcDBufs) d = 0, ++dturn;
                     }
+                    mbar_arrive(&sh.empty[s]);
+                    if (++s == stages) s = 0, ++turn;
                 }
-                if (++nb == nblocks) nb = 0, ++index;
-                if (rank == 0 && in_place) continue;
-                if (!mbar_spin_bounded(&ready[s], turn & 1, p.ctl, abort_flag) ||
-                    (rank > 0 && dturn > 0 &&
-                     !mbar_spin_bounded(&dempty[d], (dturn - 1) & 1, p.ctl, abort_flag))) {
-                    *abort_flag = 1;
-                    break;
-                }
-                if (rank > 0) {
-                    tc_fence_after();
-                    const uint32_t a0 = smem_u32(ring) + s * stage_bytes;
-                    bool add = false;
-                    for (int q = 0; q < terms<BF>(); ++q)
-                        for (int k = 0; k < steps; ++k) {
-                            const uint32_t off = (k & 3) * 32;
-                            tc_mma<BF>(tmem + d * kTile, sw128_desc(a0 + (k >> 2) * kTcABlock + off),
-                                       sw128_desc(v0 + (q * vblocks + (k >> 2)) * kTcVBlock + off), add);
-                            add = true;
-                        }
-                    tc_commit(&dfull[d]);
-                    ++committed;
-                    if (++d == kTcDBufs) d = 0, ++dturn;
-                }
-                // everyone who waits for a stage hands it back: a parity tells
-                // the phase meant only from the one before
-                mbar_arrive(&empty[s]);
-                if (++s == stages) s = 0, ++turn;
+                if (ok) mbar_arrive(&sh.vempty[k & 1]);
+                else *abort_flag = 1;
             }
-            // no product may still be running when tensor memory is released
-            if (committed > 0) {
-                const long long last = committed - 1;
-                mbar_spin_bounded(&dfull[last % kTcDBufs], static_cast<uint32_t>(last / kTcDBufs) & 1, p.ctl);
-            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        }
+        // no product may still be running when tensor memory is released
+        if (lane == 0 && committed > 0) {
+            const long long last = committed - 1;
+            mbar_spin_bounded(&sh.dfull[last % kTcDBufs], static_cast<uint32_t>(last / kTcDBufs) & 1, p.ctl);
         }
         __syncwarp();
+        pdl_wait();
     } else {
         // ------------------------------ epilogue ------------------------------
         const int quarter = warp & 3, half = warp >> 2;   // 32 outputs, 32 tokens
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
         float* yout = static_cast<float*>(p.y_out);
         const long long out_elems = static_cast<long long>(p.M - 1) * p.ld_out + p.N;
-        int cached = -1, rank = 0, count = 0, s = 0, d = 0;
+        int s = 0, d = 0;
         uint32_t turn = 0, dturn = 0;
-        bool ok = true;
-        int4 next = __ldcg(pl.tiles + min(index, pl.max_tiles - 1));   // a tile ahead
         pdl_wait();
         pdl_launch_dependents();
-        for (; left > 0; --left) {
-            if (index != cached) {
-                // every warp is done with the old tile, and so is its product;
-                // a failed wait reaches all
-                if (named_bar_any(1, kTcEpilogue * 32, !ok)) break;
-                const int4 tile = next;
-                cached = index, count = tile.z;
-                next = __ldcg(pl.tiles + min(index + 1, pl.max_tiles - 1));
-                float fv = 0.0f;
-                int tv = 0;
-                if (tid < count) {
-                    tv = __ldcg(pl.perm + tile.y + tid);
-                    fv = __ldcg(pl.f + tile.y + tid);
-                }
-                rank = tile.x >= 0 ? rank_of(p, tile.x) : 0;
-                const int pieces = pl.rp / 8;   // of 8 ranks, at most 32
-                for (int i = warp; i < terms<BF>() * count && tile.x >= 0; i += kTcEpilogue) {
-                    const int q = i % terms<BF>(), j = i / terms<BF>();
-                    if (lane < pieces) {
-                        const uint4 v = load16_cg(pl.terms + (static_cast<size_t>(q) * p.M + tile.y + j) * pl.rp + lane * 8);
-                        *reinterpret_cast<uint4*>(sv + (q * vblocks + lane / 8) * kTcVBlock + j * 128 +
-                                                  (((lane % 8) ^ (j & 7)) * 16)) = v;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            if (!take_unit(sh, k, u, p.ctl)) break;
+            release_unit(sh, u);
+            const int vb = k & 1, j0 = half * 32;
+            ok = mbar_ready_warp(&sh.vfull[vb], static_cast<uint32_t>(k / 2) & 1, p.ctl, abort_flag);
+            for (int nb = u.nb0; nb < u.nb1 && ok; ++nb) {
+                const int n = nb * kTcNB + quarter * 32 + lane;
+                ok = mbar_ready_warp(&sh.full[s], turn & 1, p.ctl, abort_flag) &&
+                     (u.rank == 0 || mbar_ready_warp(&sh.dfull[d], dturn & 1, p.ctl, abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+                const float* sy = reinterpret_cast<const float*>(ring + static_cast<size_t>(s) * stage_bytes +
+                                                                 vblocks * kTcABlock) +
+                                  j0 * kTcNB + quarter * 32 + lane;
+                // the first 8 tokens of this half, or all 32
+                const auto part = [&](auto tokens) {
+                    constexpr int T = decltype(tokens)::value;
+                    float acc[T], y[T];
+                    if (u.rank > 0) {
+                        tc_ld(tmem + d * kTile + j0 + lane_off, acc);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < T; ++j) acc[j] = 0.0f;
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (u.rank > 0 && lane == 0) mbar_arrive(&sh.dempty[d]);
+#pragma unroll
+                    for (int j = 0; j < T; ++j) y[j] = sy[j * kTcNB];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.empty[s]);   // the stage is in registers
+#pragma unroll
+                    for (int j = 0; j < T; j += 4) {
+                        const int4 rj = *reinterpret_cast<const int4*>(&sh.row[vb][j0 + j]);
+                        const float4 fj = *reinterpret_cast<const float4*>(&sh.f[vb][j0 + j]);
+                        const int o[4] = {rj.x + n, rj.y + n, rj.z + n, rj.w + n};
+                        const float g[4] = {fj.x, fj.y, fj.z, fj.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (n < p.N && j0 + j + i < u.count && store_ok(p.ctl, o[i], 1, out_elems))
+                                yout[o[i]] = fmaf(g[i], acc[j + i], y[j + i]);
+                    }
+                };
+                if (u.count - j0 > 8) {
+                    part(std::integral_constant<int, 32>{});
+                } else if (u.count - j0 > 0) {
+                    part(std::integral_constant<int, 8>{});
+                } else {
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (u.rank > 0) mbar_arrive(&sh.dempty[d]);
+                        mbar_arrive(&sh.empty[s]);
                     }
                 }
-                if (tid < kTile) {
-                    row[tid] = static_cast<int>(tv * p.ld_out);
-                    f[tid] = rank > 0 ? fv : 0.0f;
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                named_bar_sync(2, kTcEpilogue * 32);
-                if (tid == 0 && rank > 0) mbar_arrive(&vfull);
-            }
-            const int n = nb * kTcNB + quarter * 32 + lane;
-            if (++nb == nblocks) nb = 0, ++index;
-            if (rank == 0 && in_place) continue;
-            const int stage = s, buf = d;
-            const uint32_t parity = turn & 1, dparity = dturn & 1;
-            if (++s == stages) s = 0, ++turn;
-            if (rank > 0 && ++d == kTcDBufs) d = 0, ++dturn;
-            if (ok)
-                ok = mbar_ready_warp(&full[stage], parity, p.ctl, abort_flag) &&
-                     (rank == 0 || mbar_ready_warp(&dfull[buf], dparity, p.ctl, abort_flag));
-            if (!ok) {
-                *abort_flag = 1;
-                continue;   // to the next tile's barrier
-            }
-            tc_fence_after();
-            const int j0 = half * 32;
-            const float* sy = reinterpret_cast<const float*>(ring + static_cast<size_t>(stage) * stage_bytes +
-                                                             vblocks * kTcABlock) +
-                              j0 * kTcNB + quarter * 32 + lane;
-            // the first 8 tokens of this half, or all 32
-            const auto part = [&](auto tokens) {
-                constexpr int T = decltype(tokens)::value;
-                float acc[T], y[T];
-                if (rank > 0) {
-                    tc_ld(tmem + buf * kTile + j0 + lane_off, acc);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < T; ++j) acc[j] = 0.0f;
-                }
-                tc_fence_before();
                 __syncwarp();
-                if (rank > 0 && lane == 0) mbar_arrive(&dempty[buf]);
-#pragma unroll
-                for (int j = 0; j < T; ++j) y[j] = sy[j * kTcNB];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[stage]);   // the stage is in registers
-#pragma unroll
-                for (int j = 0; j < T; j += 4) {
-                    const int4 rj = *reinterpret_cast<const int4*>(row + j0 + j);
-                    const float4 fj = *reinterpret_cast<const float4*>(f + j0 + j);
-                    const int o[4] = {rj.x + n, rj.y + n, rj.z + n, rj.w + n};
-                    const float g[4] = {fj.x, fj.y, fj.z, fj.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (n < p.N && j0 + j + i < count && store_ok(p.ctl, o[i], 1, out_elems))
-                            yout[o[i]] = fmaf(g[i], acc[j + i], y[j + i]);
-                }
-            };
-            if (count - j0 > 8) {
-                part(std::integral_constant<int, 32>{});
-            } else if (count - j0 > 0) {
-                part(std::integral_constant<int, 8>{});
-            } else {
-                __syncwarp();
-                if (lane == 0) {
-                    if (rank > 0) mbar_arrive(&dempty[buf]);
-                    mbar_arrive(&empty[stage]);
-                }
+                if (u.rank > 0 && ++d == kTcDBufs) d = 0, ++dturn;
+                if (++s == stages) s = 0, ++turn;
             }
             __syncwarp();
+            if (!ok) *abort_flag = 1;
+            else if (lane == 0) mbar_arrive(&sh.vempty[vb]);
         }
     }
     // every role is done with tensor memory
@@ -2061,7 +2142,9 @@ cudaError_t run_tc(const LoraParams& p, const pq2::Plan& pl, cudaStream_t st, co
     const int vblocks = (p.R + 63) / 64;
     const int term_bytes = pq2::terms<BF>() * vblocks * pq2::kTcVBlock;
     const int stage_bytes = vblocks * pq2::kTcABlock + pq2::kTcYBytes;
-    const int stages = std::min(pq2::kTcMaxStages, (dev.max_smem_optin - 2048 - 1024 - term_bytes) / stage_bytes);
+    const int stages =
+        std::min(pq2::kTcMaxStages, (dev.max_smem_optin - static_cast<int>(sizeof(pq2::TcShared)) - 1024 -
+                                     2 * term_bytes) / stage_bytes);
     *taken = stages >= 2 && (static_cast<int64_t>(p.M) - 1) * p.ld_out + p.N < (int64_t(1) << 31) &&
              static_cast<int64_t>(p.L) * p.N + pq2::kTcNB < (int64_t(1) << 31);
     if (!*taken) return cudaSuccess;
@@ -2070,11 +2153,14 @@ cudaError_t run_tc(const LoraParams& p, const pq2::Plan& pl, cudaStream_t st, co
                                  static_cast<uint64_t>(p.ld_in) * 4, pq2::kTcNB, 1, false)) ||
         !encode_tmap_2d(&maps.b, BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                         p.B, p.R, static_cast<uint64_t>(p.L) * p.N, static_cast<uint64_t>(p.R) * 2, 64,
-                        pq2::kTcNB, true))
+                        pq2::kTcNB, true) ||
+        !encode_tmap_2d(&maps.terms, BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        pl.terms, pl.rp, static_cast<uint64_t>(pq2::terms<BF>()) * p.M,
+                        static_cast<uint64_t>(pl.rp) * 2, 64, kTile, true))
         return cudaErrorUnknown;
     auto kern = pq2::lora_expand_tc<BF, kTma>;
     static SmemLimit lim;
-    const size_t smem = 1024 + static_cast<size_t>(term_bytes) + static_cast<size_t>(stages) * stage_bytes;
+    const size_t smem = 1024 + 2 * static_cast<size_t>(term_bytes) + static_cast<size_t>(stages) * stage_bytes;
     const cudaError_t e = ensure_smem(lim, kern, smem);
     if (e != cudaSuccess) return e;
     return launch(kern, dim3(dev.num_sms), dim3(pq2::tc_threads<kTma>()), smem, st, true, p, pl, maps, stages,
@@ -2093,6 +2179,7 @@ cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cu
     pl.perm = reinterpret_cast<int*>(ws + lay.perm);
     pl.tiles = reinterpret_cast<int4*>(ws + lay.tiles);
     pl.num_tiles = reinterpret_cast<int*>(ws + lay.num_tiles);
+    pl.taken = reinterpret_cast<unsigned*>(ws + lay.num_tiles + 128);
     pl.max_tiles = lay.max_tiles;
     pl.rp = lay.rp;
     // as many warps as have tokens and fit their histograms in 200 KB
