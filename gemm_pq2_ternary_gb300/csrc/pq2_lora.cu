@@ -53,6 +53,7 @@ namespace {
 constexpr int kFewTokens = 128;
 constexpr int kFewTile = 8;       // tokens per tile of the few-token form
 constexpr int kTile = 64;        // tokens per tile of the planned form
+constexpr int kSmallTile = 16;   // where adapters have few tokens each
 constexpr int kShrinkWarps = 8;
 constexpr int kExpandWarps = 4;   // 32 outputs each
 constexpr int kExpandMaxWarps = 8;
@@ -621,6 +622,7 @@ struct Plan {
     int* perm;           // [M] tokens, sorted by adapter
     int4* tiles;         // adapter (-1: none), first position, tokens
     int* num_tiles;      // [0] tiles, [1] those with an adapter
+    int tile;            // tokens of a tile, at most: kTile or kSmallTile
     unsigned* taken;     // times that expand took items from the counter
     uint16_t* terms;     // [terms][M][rp], by position
     float* f;            // [M] scale and power of two, by position
@@ -629,7 +631,7 @@ struct Plan {
 };
 
 // One CTA: stable counting sort of the tokens by adapter (tokens without one
-// last), cut into tiles of at most kTile.  Every warp counts and places a
+// last), cut into tiles of at most pl.tile.  Every warp counts and places a
 // contiguous range of tokens in its own histogram, so the order is fixed.
 __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Plan pl, int warps) {
     extern __shared__ int hist[];  // [warps][bins], then offsets [bins + 1], tiles [bins]
@@ -688,7 +690,7 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
     int n_tok = 0, n_tile = 0;
     for (int b = b0; b < b1; ++b) {
         n_tok += off[b];
-        n_tile += (off[b] + kTile - 1) / kTile;
+        n_tile += (off[b] + pl.tile - 1) / pl.tile;
     }
     int s_tok = n_tok, s_tile = n_tile;
 #pragma unroll
@@ -705,7 +707,7 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
         off[b] = at_tok;
         tfirst[b] = at_tile;
         at_tok += total;
-        at_tile += (total + kTile - 1) / kTile;
+        at_tile += (total + pl.tile - 1) / pl.tile;
     }
     if (threadIdx.x == nthreads - 1) {
         pl.num_tiles[0] = at_tile;
@@ -717,8 +719,9 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
     // tiles: a warp per bin again
     for (int b = warp; b < bins; b += nwarps) {
         const int first = off[b], total = off[b + 1] - first;
-        for (int k = lane * kTile; k < total; k += 32 * kTile)
-            pl.tiles[tfirst[b] + k / kTile] = make_int4(b < p.L ? b : -1, first + k, min(kTile, total - k), 0);
+        for (int k = lane * pl.tile; k < total; k += 32 * pl.tile)
+            pl.tiles[tfirst[b] + k / pl.tile] =
+                make_int4(b < p.L ? b : -1, first + k, min(pl.tile, total - k), 0);
     }
     for (int base = m0; base < m1; base += 32 * kBatch) {
         if (per > 32 * kBatch) load_keys(base, false);   // else still there
@@ -1451,22 +1454,37 @@ __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
 // phase meant only from the one before.
 constexpr int kTcEpilogue = 8;      // warps, two per quarter of the lanes
 constexpr int kTcIssuer = 8, kTcProducer = 9, kTcFixer = 10, kTcTerms = 11, kTcScheduler = 12;
-constexpr int kTcLoader0 = 13, kTcLoaders = 4;   // where y does not come by TMA
-template <bool kTma>
+constexpr int kTcIssuer2 = 13;      // where there are two groups
+constexpr int kTcLoaders = 4;       // the last, where y does not come by TMA
+template <int T>
+constexpr int tc_loader0() {
+    return T == kTile ? kTcIssuer2 : kTcIssuer2 + 1;
+}
+template <bool kTma, int T>
 constexpr int tc_threads() {
-    return (kTcLoader0 + (kTma ? 0 : kTcLoaders)) * 32;
+    return (tc_loader0<T>() + (kTma ? 0 : kTcLoaders)) * 32;
 }
 constexpr int kTcUnit = 8;          // items of a unit, at most
 constexpr int kTcTail = 2;          // items taken at a time from the counter
 constexpr int kTcShares = 16;       // items a CTA from which there is a counter
 constexpr int kTcUnits = 2;         // units known at a time
 constexpr int kTcNB = 128;
-constexpr int kTcMaxStages = 4;
-constexpr int kTcDBufs = 4;
-constexpr uint32_t kTcTmemCols = kTcDBufs * kTile;
+constexpr int kTcMaxStages = 8;
 constexpr int kTcABlock = kTcNB * 128;    // bytes of 64 ranks of an item's rows of B
-constexpr int kTcVBlock = kTile * 128;    // and of a tile's terms
-constexpr int kTcYBytes = kTile * kTcNB * 4;
+// For tiles of at most T tokens:
+template <int T>
+struct Tc {
+    // the epilogue's warps as groups that take the items in turn (an item of
+    // few tokens is mostly waits); else they share each item's tokens
+    static constexpr int kGroups = T == kTile ? 1 : 2;
+    static constexpr int kItemWarps = kTcEpilogue / kGroups;
+    static constexpr int kWarpTokens = T * 4 / kItemWarps;
+    static constexpr int kDBufs = T == kTile ? 4 : 8;   // products in tensor memory
+    static constexpr uint32_t kTmemCols = kDBufs * T;
+    static constexpr int kVBlock = T * 128;             // bytes of 64 ranks of the terms
+    static constexpr int kYBytes = T * kTcNB * 4;
+};
+constexpr int kTcMaxDBufs = 8;
 
 // Matrix descriptor: K-major, 128-byte swizzle, 8-row groups 1024 bytes apart.
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
@@ -1479,16 +1497,21 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
     return d;
 }
 
-// D[128 x 64] (+)= A[128 x 16] . B[64 x 16]^T; both operands fp16, or both bf16.
-template <bool BF>
+// D[128 x T] (+)= A[128 x 16] . B[T x 16]^T; both operands fp16, or both bf16.
+template <bool BF, int T>
 __device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t a, uint64_t b, bool add) {
     constexpr uint32_t idesc = (1u << 4) | ((BF ? 1u : 0u) << 7) | ((BF ? 1u : 0u) << 10) |
-                               (static_cast<uint32_t>(kTile >> 3) << 17) |
+                               (static_cast<uint32_t>(T >> 3) << 17) |
                                (static_cast<uint32_t>(kTcNB >> 4) << 24);
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u));
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
 }
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile(
@@ -1516,6 +1539,19 @@ __device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[8]) {
     uint32_t r[8];
@@ -1558,8 +1594,8 @@ struct TcShared {
     uint64_t full[kTcMaxStages];    // an item's y and B are there
     uint64_t ready[kTcMaxStages];   // B as the product may read it
     uint64_t empty[kTcMaxStages];   // everyone is done with the stage
-    uint64_t dfull[kTcDBufs];       // an item's product is there
-    uint64_t dempty[kTcDBufs];      // read by the epilogue's warps
+    uint64_t dfull[kTcMaxDBufs];     // an item's product is there
+    uint64_t dempty[kTcMaxDBufs];     // read by the epilogue's warps
     uint64_t vfull[2];              // a unit's terms, rows and scales are there
     uint64_t vempty[2];             // everyone is done with them
     uint64_t ufull[kTcUnits];       // a unit is published
@@ -1590,8 +1626,8 @@ __device__ __forceinline__ void release_unit(TcShared& sh, const TcUnit& u) {
     if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.uempty[u.slot]);
 }
 
-template <bool BF, bool kTma>
-__global__ void __launch_bounds__(tc_threads<kTma>(), 1)
+template <bool BF, bool kTma, int T>
+__global__ void __launch_bounds__(tc_threads<kTma, T>(), 1)
     lora_expand_tc(pq2h::LoraParams p, Plan pl, const __grid_constant__ TcMaps maps, int stages,
                    int stage_bytes, int term_bytes) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -1605,19 +1641,19 @@ __global__ void __launch_bounds__(tc_threads<kTma>(), 1)
         for (int s = 0; s < stages; ++s) {
             mbar_init(&sh.full[s], kTma ? 1 : kTcLoaders * 32 + 1);
             mbar_init(&sh.ready[s], 1);
-            mbar_init(&sh.empty[s], kTcEpilogue + 2);
+            mbar_init(&sh.empty[s], Tc<T>::kItemWarps + 1);
         }
-        for (int i = 0; i < kTcDBufs; ++i) {
+        for (int i = 0; i < Tc<T>::kDBufs; ++i) {
             mbar_init(&sh.dfull[i], 1);
-            mbar_init(&sh.dempty[i], kTcEpilogue);
+            mbar_init(&sh.dempty[i], Tc<T>::kItemWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.vfull[i], 2);
-            mbar_init(&sh.vempty[i], kTcEpilogue + 1);
+            mbar_init(&sh.vempty[i], kTcEpilogue);
         }
         for (int i = 0; i < kTcUnits; ++i) {
             mbar_init(&sh.ufull[i], 1);
-            mbar_init(&sh.uempty[i], kTcEpilogue + 4 + (kTma ? 0 : kTcLoaders));
+            mbar_init(&sh.uempty[i], kTcEpilogue + 3 + Tc<T>::kGroups + (kTma ? 0 : kTcLoaders));
         }
         sh.abort_word = 0;
         fence_mbar_init();
@@ -1625,7 +1661,7 @@ __global__ void __launch_bounds__(tc_threads<kTma>(), 1)
     if (warp == kTcIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&sh.tmem_base)),
-                     "r"(kTcTmemCols));
+                     "r"(Tc<T>::kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     tc_fence_before();
@@ -1767,13 +1803,13 @@ __global__ void __launch_bounds__(tc_threads<kTma>(), 1)
                 break;
             }
             const int used = (u.rank + 63) / 64, boxes = terms<BF>() * used;
-            if (lane == 0) mbar_arrive_expect_tx(&sh.vfull[b], boxes * kTcVBlock);
+            if (lane == 0) mbar_arrive_expect_tx(&sh.vfull[b], boxes * Tc<T>::kVBlock);
             __syncwarp();
             // rows past the tile's are its neighbours' and give columns that
             // are not stored
             if (lane < boxes) {
                 const int q = lane / used, c = lane % used;
-                tma_load_2d(sv + b * term_bytes + (q * vblocks + c) * kTcVBlock, &maps.terms, c * 64,
+                tma_load_2d(sv + b * term_bytes + (q * vblocks + c) * Tc<T>::kVBlock, &maps.terms, c * 64,
                             q * p.M + u.first, &sh.vfull[b]);
             }
 #pragma unroll
@@ -1788,9 +1824,9 @@ __global__ void __launch_bounds__(tc_threads<kTma>(), 1)
         // the last copies land before the CTA ends, whatever the others do
         for (int i = max(0, k - 2); i < k; ++i)
             mbar_ready_warp(&sh.vfull[i & 1], static_cast<uint32_t>(i / 2) & 1, p.ctl);
-    } else if (!kTma && warp >= kTcLoader0) {
+    } else if (!kTma && warp >= tc_loader0<T>()) {
         // ------------------------------ loaders of y ------------------------------
-        const int pt = tid - kTcLoader0 * 32;
+        const int pt = tid - tc_loader0<T>() * 32;
         const uint8_t* yb = reinterpret_cast<const uint8_t*>(p.y_in) + pt * 4;
         const long long ld = p.ld_in * 4;
         int issued = 0, s = 0;
@@ -1823,57 +1859,60 @@ __global__ void __launch_bounds__(tc_threads<kTma>(), 1)
         }
         cp_async_wait<0>();
         pdl_wait();
-    } else if (warp == kTcIssuer) {
+    } else if (warp == kTcIssuer || (Tc<T>::kGroups > 1 && warp == kTcIssuer2)) {
         // ------------------------------ issuer ------------------------------
-        int s = 0, d = 0;
+        // one for each group of the epilogue.  The warp stays together up to
+        // the products themselves: under a branch of one lane their operands
+        // took several hundred cycles an item to reach the uniform registers
+        const int group = warp == kTcIssuer ? 0 : 1;
+        int s = 0, d = 0, next = 0;
         uint32_t turn = 0, dturn = 0;
-        long long committed = 0;
+        int last_d = -1;              // of the last product issued, and its phase
+        uint32_t last_phase = 0;
         bool ok = true;
         for (int k = 0; ok; ++k) {
             if (!take_unit(sh, k, u, p.ctl)) break;
             release_unit(sh, u);
-            if (lane == 0) {
-                const int steps = (u.rank + 15) / 16;
-                const uint32_t v0 = smem_u32(sv) + (k & 1) * term_bytes;
-                ok = mbar_spin_bounded(&sh.vfull[k & 1], static_cast<uint32_t>(k / 2) & 1, p.ctl, abort_flag);
-                for (int nb = u.nb0; nb < u.nb1 && ok; ++nb) {
-                    ok = mbar_spin_bounded(&sh.ready[s], turn & 1, p.ctl, abort_flag) &&
-                         (steps == 0 || dturn == 0 ||
-                          mbar_spin_bounded(&sh.dempty[d], (dturn - 1) & 1, p.ctl, abort_flag));
+            const int steps = (u.rank + 15) / 16;
+            const uint32_t v0 = smem_u32(sv) + (k & 1) * term_bytes;
+            ok = mbar_ready_warp(&sh.vfull[k & 1], static_cast<uint32_t>(k / 2) & 1, p.ctl, abort_flag);
+            for (int nb = u.nb0; nb < u.nb1 && ok; ++nb) {
+                if (next == group) {
+                    ok = mbar_ready_warp(&sh.ready[s], turn & 1, p.ctl, abort_flag) &&
+                         (dturn == 0 || mbar_ready_warp(&sh.dempty[d], (dturn - 1) & 1, p.ctl, abort_flag));
                     if (!ok) break;
-                    if (steps > 0) {
-                        tc_fence_after();
-                        const uint32_t a0 = smem_u32(ring) + s * stage_bytes;
-                        bool add = false;
+                    tc_fence_after();
+                    const uint32_t a0 = smem_u32(ring) + s * stage_bytes;
+                    if (elect_one()) {
+#pragma unroll
                         for (int q = 0; q < terms<BF>(); ++q)
                             for (int i = 0; i < steps; ++i) {
                                 const uint32_t off = (i & 3) * 32;
-                                tc_mma<BF>(tmem + d * kTile, sw128_desc(a0 + (i >> 2) * kTcABlock + off),
-                                           sw128_desc(v0 + (q * vblocks + (i >> 2)) * kTcVBlock + off), add);
-                                add = true;
+                                tc_mma<BF, T>(tmem + d * T, sw128_desc(a0 + (i >> 2) * kTcABlock + off),
+                                              sw128_desc(v0 + (q * vblocks + (i >> 2)) * Tc<T>::kVBlock + off),
+                                              q + i > 0);
                             }
-                        tc_commit(&sh.dfull[d]);
-                        ++committed;
-                        if (++d == kTcDBufs) d = 0, ++dturn;
+                        tc_commit(&sh.dfull[d]);   // at once where the rank is 0
                     }
-                    mbar_arrive(&sh.empty[s]);
-                    if (++s == stages) s = 0, ++turn;
+                    __syncwarp();
+                    last_d = d;
+                    last_phase = dturn & 1;
                 }
-                if (ok) mbar_arrive(&sh.vempty[k & 1]);
-                else *abort_flag = 1;
+                if (++next == Tc<T>::kGroups) next = 0;
+                if (++d == Tc<T>::kDBufs) d = 0, ++dturn;
+                if (++s == stages) s = 0, ++turn;
             }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
+        if (!ok) *abort_flag = 1;
         // no product may still be running when tensor memory is released
-        if (lane == 0 && committed > 0) {
-            const long long last = committed - 1;
-            mbar_spin_bounded(&sh.dfull[last % kTcDBufs], static_cast<uint32_t>(last / kTcDBufs) & 1, p.ctl);
-        }
-        __syncwarp();
+        if (last_d >= 0) mbar_ready_warp(&sh.dfull[last_d], last_phase, p.ctl);
         pdl_wait();
     } else {
         // ------------------------------ epilogue ------------------------------
-        const int quarter = warp & 3, half = warp >> 2;   // 32 outputs, 32 tokens
+        const int quarter = warp & 3, part_of = warp >> 2;   // 32 outputs; a group or a part of the tokens
+        const int group = Tc<T>::kGroups > 1 ? part_of : 0;
+        const int j0 = Tc<T>::kGroups > 1 ? 0 : part_of * Tc<T>::kWarpTokens;
+        int next = 0;    // the group whose item it is
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
         float* yout = static_cast<float*>(p.y_out);
         const long long out_elems = static_cast<long long>(p.M - 1) * p.ld_out + p.N;
@@ -1885,59 +1924,63 @@ __global__ void __launch_bounds__(tc_threads<kTma>(), 1)
         for (int k = 0; ok; ++k) {
             if (!take_unit(sh, k, u, p.ctl)) break;
             release_unit(sh, u);
-            const int vb = k & 1, j0 = half * 32;
+            const int vb = k & 1;
             ok = mbar_ready_warp(&sh.vfull[vb], static_cast<uint32_t>(k / 2) & 1, p.ctl, abort_flag);
             for (int nb = u.nb0; nb < u.nb1 && ok; ++nb) {
                 const int n = nb * kTcNB + quarter * 32 + lane;
-                ok = mbar_ready_warp(&sh.full[s], turn & 1, p.ctl, abort_flag) &&
-                     (u.rank == 0 || mbar_ready_warp(&sh.dfull[d], dturn & 1, p.ctl, abort_flag));
-                if (!ok) break;
-                tc_fence_after();
-                const float* sy = reinterpret_cast<const float*>(ring + static_cast<size_t>(s) * stage_bytes +
-                                                                 vblocks * kTcABlock) +
-                                  j0 * kTcNB + quarter * 32 + lane;
-                // the first 8 tokens of this half, or all 32
-                const auto part = [&](auto tokens) {
-                    constexpr int T = decltype(tokens)::value;
-                    float acc[T], y[T];
-                    if (u.rank > 0) {
-                        tc_ld(tmem + d * kTile + j0 + lane_off, acc);
+                const bool mine = next == group;
+                if (++next == Tc<T>::kGroups) next = 0;
+                if (mine) {
+                    ok = mbar_ready_warp(&sh.full[s], turn & 1, p.ctl, abort_flag) &&
+                         mbar_ready_warp(&sh.dfull[d], dturn & 1, p.ctl, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float* sy = reinterpret_cast<const float*>(ring + static_cast<size_t>(s) * stage_bytes +
+                                                                     vblocks * kTcABlock) +
+                                      j0 * kTcNB + quarter * 32 + lane;
+                    // the first 8 tokens of this half, or all of them
+                    const auto part = [&](auto tokens) {
+                        constexpr int W = decltype(tokens)::value;
+                        float acc[W], y[W];
+                        if (u.rank > 0) {
+                            tc_ld(tmem + d * T + j0 + lane_off, acc);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < W; ++j) acc[j] = 0.0f;
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.dempty[d]);
+#pragma unroll
+                        for (int j = 0; j < W; ++j) y[j] = sy[j * kTcNB];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.empty[s]);   // the stage is in registers
+#pragma unroll
+                        for (int j = 0; j < W; j += 4) {
+                            const int4 rj = *reinterpret_cast<const int4*>(&sh.row[vb][j0 + j]);
+                            const float4 fj = *reinterpret_cast<const float4*>(&sh.f[vb][j0 + j]);
+                            const int o[4] = {rj.x + n, rj.y + n, rj.z + n, rj.w + n};
+                            const float g[4] = {fj.x, fj.y, fj.z, fj.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (n < p.N && j0 + j + i < u.count && store_ok(p.ctl, o[i], 1, out_elems))
+                                    yout[o[i]] = fmaf(g[i], acc[j + i], y[j + i]);
+                        }
+                    };
+                    if (u.count - j0 > 8) {
+                        part(std::integral_constant<int, Tc<T>::kWarpTokens>{});
+                    } else if (u.count - j0 > 0) {
+                        part(std::integral_constant<int, 8>{});
                     } else {
-#pragma unroll
-                        for (int j = 0; j < T; ++j) acc[j] = 0.0f;
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&sh.dempty[d]);
+                            mbar_arrive(&sh.empty[s]);
+                        }
                     }
-                    tc_fence_before();
                     __syncwarp();
-                    if (u.rank > 0 && lane == 0) mbar_arrive(&sh.dempty[d]);
-#pragma unroll
-                    for (int j = 0; j < T; ++j) y[j] = sy[j * kTcNB];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.empty[s]);   // the stage is in registers
-#pragma unroll
-                    for (int j = 0; j < T; j += 4) {
-                        const int4 rj = *reinterpret_cast<const int4*>(&sh.row[vb][j0 + j]);
-                        const float4 fj = *reinterpret_cast<const float4*>(&sh.f[vb][j0 + j]);
-                        const int o[4] = {rj.x + n, rj.y + n, rj.z + n, rj.w + n};
-                        const float g[4] = {fj.x, fj.y, fj.z, fj.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (n < p.N && j0 + j + i < u.count && store_ok(p.ctl, o[i], 1, out_elems))
-                                yout[o[i]] = fmaf(g[i], acc[j + i], y[j + i]);
-                    }
-                };
-                if (u.count - j0 > 8) {
-                    part(std::integral_constant<int, 32>{});
-                } else if (u.count - j0 > 0) {
-                    part(std::integral_constant<int, 8>{});
-                } else {
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (u.rank > 0) mbar_arrive(&sh.dempty[d]);
-                        mbar_arrive(&sh.empty[s]);
-                    }
                 }
-                __syncwarp();
-                if (u.rank > 0 && ++d == kTcDBufs) d = 0, ++dturn;
+                if (++d == Tc<T>::kDBufs) d = 0, ++dturn;
                 if (++s == stages) s = 0, ++turn;
             }
             __syncwarp();
@@ -1951,7 +1994,7 @@ __global__ void __launch_bounds__(tc_threads<kTma>(), 1)
     tc_fence_after();
     if (warp == kTcIssuer)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"(kTcTmemCols));
+                     "r"(Tc<T>::kTmemCols));
 }
 
 }  // namespace
@@ -1963,6 +2006,7 @@ namespace {
 
 using pq2::kFewTokens;
 using pq2::kMaxSplits;
+using pq2::kSmallTile;
 using pq2::kTile;
 
 // The GPU's SMs: the K splits are sized for it on the host, before a device
@@ -1972,7 +2016,7 @@ constexpr int64_t kSms = 152;
 size_t pad(size_t b) { return (b + 255) & ~size_t(255); }
 
 struct Layout {
-    int splits, k_split, max_tiles, rp;
+    int splits, k_split, tile, max_tiles, rp;
     size_t part, terms, f, perm, tiles, num_tiles, bytes;
 };
 
@@ -1991,7 +2035,8 @@ Layout layout(int64_t M, int64_t K, int64_t L, int64_t R) {
         // a cluster per tile: one and a half CTAs per SM over the tiles that
         // are likely, at least 256 columns each; more than 8 CTAs (the portable
         // cluster size) from 512 columns each
-        const int64_t tiles = (M + kTile - 1) / kTile + std::min(L, M / 2);
+        y.tile = M <= 8 * L ? kSmallTile : kTile;
+        const int64_t tiles = (M + y.tile - 1) / y.tile + std::min(L, M / 2);
         s = 1;
         while (s < 16 && s * tiles * 2 < 3 * kSms && K / (2 * s) >= (s < 8 ? 256 : 512)) s *= 2;
     }
@@ -2003,7 +2048,7 @@ Layout layout(int64_t M, int64_t K, int64_t L, int64_t R) {
         y.part = o;
         o += pad(static_cast<size_t>(y.splits) * M * R * 4);
     } else {
-        y.max_tiles = static_cast<int>((M + kTile - 1) / kTile + std::min(L + 1, M));
+        y.max_tiles = static_cast<int>((M + y.tile - 1) / y.tile + std::min(L + 1, M));
         y.terms = o;
         o += pad(static_cast<size_t>(3) * M * y.rp * 2);
         y.f = o;
@@ -2136,15 +2181,16 @@ cudaError_t run_ring(const LoraParams& p, const pq2::Plan& pl, cudaStream_t st, 
 
 // fp32 y on the tensor-memory form, where two stages fit and y's offsets and
 // B's rows count in 31 bits.
-template <bool BF, bool kTma>
+template <bool BF, bool kTma, int T>
 cudaError_t run_tc(const LoraParams& p, const pq2::Plan& pl, cudaStream_t st, const DeviceInfo& dev,
                    bool* taken) {
     const int vblocks = (p.R + 63) / 64;
-    const int term_bytes = pq2::terms<BF>() * vblocks * pq2::kTcVBlock;
-    const int stage_bytes = vblocks * pq2::kTcABlock + pq2::kTcYBytes;
-    const int stages =
+    const int term_bytes = pq2::terms<BF>() * vblocks * pq2::Tc<T>::kVBlock;
+    const int stage_bytes = vblocks * pq2::kTcABlock + pq2::Tc<T>::kYBytes;
+    int stages =
         std::min(pq2::kTcMaxStages, (dev.max_smem_optin - static_cast<int>(sizeof(pq2::TcShared)) - 1024 -
                                      2 * term_bytes) / stage_bytes);
+    stages -= stages % pq2::Tc<T>::kGroups;   // a stage is always the same group's
     *taken = stages >= 2 && (static_cast<int64_t>(p.M) - 1) * p.ld_out + p.N < (int64_t(1) << 31) &&
              static_cast<int64_t>(p.L) * p.N + pq2::kTcNB < (int64_t(1) << 31);
     if (!*taken) return cudaSuccess;
@@ -2156,14 +2202,14 @@ cudaError_t run_tc(const LoraParams& p, const pq2::Plan& pl, cudaStream_t st, co
                         pq2::kTcNB, true) ||
         !encode_tmap_2d(&maps.terms, BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                         pl.terms, pl.rp, static_cast<uint64_t>(pq2::terms<BF>()) * p.M,
-                        static_cast<uint64_t>(pl.rp) * 2, 64, kTile, true))
+                        static_cast<uint64_t>(pl.rp) * 2, 64, T, true))
         return cudaErrorUnknown;
-    auto kern = pq2::lora_expand_tc<BF, kTma>;
+    auto kern = pq2::lora_expand_tc<BF, kTma, T>;
     static SmemLimit lim;
     const size_t smem = 1024 + 2 * static_cast<size_t>(term_bytes) + static_cast<size_t>(stages) * stage_bytes;
     const cudaError_t e = ensure_smem(lim, kern, smem);
     if (e != cudaSuccess) return e;
-    return launch(kern, dim3(dev.num_sms), dim3(pq2::tc_threads<kTma>()), smem, st, true, p, pl, maps, stages,
+    return launch(kern, dim3(dev.num_sms), dim3(pq2::tc_threads<kTma, T>()), smem, st, true, p, pl, maps, stages,
                   stage_bytes, term_bytes);
 }
 
@@ -2181,6 +2227,7 @@ cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cu
     pl.num_tiles = reinterpret_cast<int*>(ws + lay.num_tiles);
     pl.taken = reinterpret_cast<unsigned*>(ws + lay.num_tiles + 128);
     pl.max_tiles = lay.max_tiles;
+    pl.tile = lay.tile;
     pl.rp = lay.rp;
     // as many warps as have tokens and fit their histograms in 200 KB
     const int bins = p.L + 1;
@@ -2207,7 +2254,12 @@ cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cu
                       reinterpret_cast<uintptr_t>(p.y_in) % 16 == 0;
     if constexpr (YT == PQ2_F32) {
         bool taken = false;
-        e = by16 ? run_tc<BF, true>(p, pl, st, dev, &taken) : run_tc<BF, false>(p, pl, st, dev, &taken);
+        if (lay.tile == kTile)
+            e = by16 ? run_tc<BF, true, kTile>(p, pl, st, dev, &taken)
+                     : run_tc<BF, false, kTile>(p, pl, st, dev, &taken);
+        else
+            e = by16 ? run_tc<BF, true, kSmallTile>(p, pl, st, dev, &taken)
+                     : run_tc<BF, false, kSmallTile>(p, pl, st, dev, &taken);
         if (taken || e != cudaSuccess) return e;
     }
     if (by16 && p.ld_out % 4 == 0 && vec) return run_ring<BF, YT, 16>(p, pl, st, dev);

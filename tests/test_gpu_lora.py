@@ -130,6 +130,12 @@ SHAPES = [
     (1025, 1000, 1028, 48, 2, "bf16", "f32", dict(ranks=False, ids="runs")),
     (129, 6144, 700, 64, 1, "f16", "f32", dict(scales=False)),
     (4000, 256, 264, 128, 64, "f16", "bf16", {}),
+    # few tokens an adapter
+    (300, 512, 1028, 128, 40, "f16", "f32", {}),
+    (300, 256, 1025, 24, 60, "bf16", "f32", dict(ld_y=1027)),
+    (500, 256, 2052, 192, 100, "f16", "f32", {}),
+    (640, 256, 1032, 64, 80, "bf16", "bf16", dict(ids="runs")),
+    (600, 256, 2600, 40, 90, "bf16", "f32", dict(ids="runs")),
 ]
 
 
