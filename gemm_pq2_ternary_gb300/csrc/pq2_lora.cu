@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kExpandMaxWarps * 32)
 
 struct Plan {
     int* perm;           // [M] tokens, sorted by adapter
-    int4* tiles;         // adapter (-1: none), first position, tokens
+    int4* tiles;         // adapter (-1: none), first position, tokens, rank
     int* num_tiles;      // [0] tiles, [1] those with an adapter
     int tile;            // tokens of a tile, at most: kTile or kSmallTile
     unsigned* taken;     // times that expand took items from the counter
@@ -634,11 +634,12 @@ struct Plan {
 // last), cut into tiles of at most pl.tile.  Every warp counts and places a
 // contiguous range of tokens in its own histogram, so the order is fixed.
 __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Plan pl, int warps) {
-    extern __shared__ int hist[];  // [warps][bins], then offsets [bins + 1], tiles [bins]
+    extern __shared__ int hist[];  // [warps][bins], then offsets [bins + 1], tiles and ranks [bins]
     __shared__ int ws[2][32];
     const int bins = p.L + 1;
     int* off = hist + warps * bins;
     int* tfirst = off + bins + 1;
+    int* rank = tfirst + bins;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nthreads = blockDim.x;
     for (int i = threadIdx.x; i < warps * bins; i += nthreads) hist[i] = 0;
     pdl_wait();
@@ -647,9 +648,14 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
     const int per = ((p.M + warps - 1) / warps + 31) / 32 * 32;
     const int m0 = warp * per, m1 = min(m0 + per, p.M);
     int* mine = hist + warp * bins;
+    // each thread's bins: their ranks are on the way meanwhile
+    const int span = (bins + nthreads - 1) / nthreads;
+    const int b0 = min(static_cast<int>(threadIdx.x) * span, bins), b1 = min(b0 + span, bins);
+    const int first_rank = b0 < b1 && b0 < p.L ? rank_of(p, b0) : 0;
     // the tokens four at a time a lane, loaded together
     constexpr int kBatch = 4;
     int keys[kBatch];
+    unsigned same[kBatch];   // lanes with the same key
     auto load_keys = [&](int base, bool report) {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
@@ -657,15 +663,17 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
             keys[i] = m < m1 ? adapter_of(p, m, report) : -2;
         }
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) keys[i] = keys[i] == -1 ? p.L : keys[i];
+        for (int i = 0; i < kBatch; ++i) {
+            keys[i] = keys[i] == -1 ? p.L : keys[i];
+            same[i] = __match_any_sync(0xffffffffu, keys[i]);
+        }
     };
     for (int base = m0; base < m1; base += 32 * kBatch) {
         load_keys(base, true);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             if (base + i * 32 >= m1) break;
-            const unsigned same = __match_any_sync(0xffffffffu, keys[i]);
-            if (keys[i] >= 0 && __ffs(same) - 1 == lane) mine[keys[i]] += __popc(same);
+            if (keys[i] >= 0 && __ffs(same[i]) - 1 == lane) mine[keys[i]] += __popc(same[i]);
             __syncwarp();
         }
     }
@@ -685,10 +693,9 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
     }
     __syncthreads();
     // a scan over the bins, each thread owning a contiguous span
-    const int span = (bins + nthreads - 1) / nthreads;
-    const int b0 = min(static_cast<int>(threadIdx.x) * span, bins), b1 = min(b0 + span, bins);
     int n_tok = 0, n_tile = 0;
     for (int b = b0; b < b1; ++b) {
+        rank[b] = b == b0 ? first_rank : b < p.L ? rank_of(p, b) : 0;
         n_tok += off[b];
         n_tile += (off[b] + pl.tile - 1) / pl.tile;
     }
@@ -721,24 +728,22 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
         const int first = off[b], total = off[b + 1] - first;
         for (int k = lane * pl.tile; k < total; k += 32 * pl.tile)
             pl.tiles[tfirst[b] + k / pl.tile] =
-                make_int4(b < p.L ? b : -1, first + k, min(pl.tile, total - k), 0);
+                make_int4(b < p.L ? b : -1, first + k, min(pl.tile, total - k), rank[b]);
     }
     for (int base = m0; base < m1; base += 32 * kBatch) {
         if (per > 32 * kBatch) load_keys(base, false);   // else still there
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             if (base + i * 32 >= m1) break;
-            const int key = keys[i];
-            const unsigned same = __match_any_sync(0xffffffffu, key);
-            const int leader = __ffs(same) - 1;
+            const int key = keys[i], leader = __ffs(same[i]) - 1;
             int at = 0;
             if (key >= 0 && leader == lane) {
                 at = mine[key];
-                mine[key] = at + __popc(same);
+                mine[key] = at + __popc(same[i]);
             }
             at = __shfl_sync(0xffffffffu, at, leader);
             if (key >= 0)
-                pl.perm[off[key] + at + __popc(same & ((1u << lane) - 1u))] = base + i * 32 + lane;
+                pl.perm[off[key] + at + __popc(same[i] & ((1u << lane) - 1u))] = base + i * 32 + lane;
             __syncwarp();
         }
     }
@@ -875,7 +880,7 @@ __global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
     const int4 tile = pl.tiles[index];    // there for every index; a tile if below num_tiles
     if (index >= *pl.num_tiles) return;   // the whole cluster
     const int l = tile.x, first = tile.y, count = tile.z;
-    const int rank = l >= 0 ? rank_of(p, l) : 0;
+    const int rank = tile.w;
     if (rank == 0) return;
     // warps that have ranks and tokens
     constexpr int kTokenWarps = kTile / 8 / WN;
@@ -1087,7 +1092,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32, 3)
     const bool here = static_cast<int>(blockIdx.y) < __ldcg(pl.num_tiles);
     const int4 tile = here ? __ldcg(pl.tiles + blockIdx.y) : make_int4(-1, 0, 0, 0);
     const int l = tile.x, first = tile.y, count = tile.z;
-    const int rank = l >= 0 ? rank_of(p, l) : 0;
+    const int rank = tile.w;
     const int blocks = (rank + 31) / 32;
     const bool in_place = p.y_in == p.y_out && p.ld_in == p.ld_out;
     if (!here || (rank == 0 && in_place)) {  // uniform over the CTA
@@ -1276,7 +1281,7 @@ __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
             if (index != cached) {
                 const int4 tile = __ldcg(pl.tiles + index);
                 cached = index, l = tile.x, count = tile.z;
-                rank = l >= 0 ? rank_of(p, l) : 0;
+                rank = tile.w;
                 if constexpr (kByAddress) {
 #pragma unroll
                     for (int i = 0; i < kRounds; ++i) {
@@ -1369,7 +1374,7 @@ __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
                 tv = __ldcg(pl.perm + tile.y + tid);
                 fv = __ldcg(pl.f + tile.y + tid);
             }
-            rank = tile.x >= 0 ? rank_of(p, tile.x) : 0;
+            rank = tile.w;
             for (int i = warp; i < terms<BF>() * count && tile.x >= 0; i += kRingWarps) {
                 const int q = i % terms<BF>(), j = i / terms<BF>();
                 if (lane < pieces)
@@ -1693,7 +1698,7 @@ __global__ void __launch_bounds__(tc_threads<kTma, T>(), 1)
                 const int4 tile = __ldcg(pl.tiles + pos / nblocks);
                 const int nb0 = static_cast<int>(pos % nblocks);
                 const int n = static_cast<int>(min(static_cast<long long>(min(kTcUnit, nblocks - nb0)), end - pos));
-                const int rank = tile.x >= 0 ? rank_of(p, tile.x) : 0;
+                const int rank = tile.w;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     if (lane + 32 * h < tile.z) tok[h] = __ldcg(pl.perm + tile.y + lane + 32 * h);
@@ -2232,9 +2237,9 @@ cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cu
     // as many warps as have tokens and fit their histograms in 200 KB
     const int bins = p.L + 1;
     int warps = 32;
-    while (warps > 1 && (warps / 2 * 32 >= p.M || static_cast<size_t>(warps + 2) * bins * 4 > 200 * 1024))
+    while (warps > 1 && (warps / 2 * 32 >= p.M || static_cast<size_t>(warps + 3) * bins * 4 > 200 * 1024))
         warps /= 2;
-    const size_t plan_smem = (static_cast<size_t>(warps + 2) * bins + 1) * 4;
+    const size_t plan_smem = (static_cast<size_t>(warps + 3) * bins + 1) * 4;
     cudaError_t e = ensure_smem(g_plan_smem, pq2::lora_plan_kernel, plan_smem);
     if (e != cudaSuccess) return e;
     e = launch(pq2::lora_plan_kernel, dim3(1), dim3(warps * 32), plan_smem, st, true, p, pl, warps);
