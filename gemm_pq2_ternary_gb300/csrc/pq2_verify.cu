@@ -357,7 +357,7 @@ namespace pq2h {
 
 namespace {
 
-constexpr int64_t kPickCtas = 1216;
+constexpr int64_t kPickCtas = 456;
 
 int verify_chunks(int64_t V) {
     // up to three values before the first 16-byte boundary of a row
@@ -392,7 +392,9 @@ cudaError_t launch_verify(VerifyParams p, void* workspace, cudaStream_t st) {
         if (e != cudaSuccess) return e;
     }
     // a CTA's start (the row's statistics, the decision) costs several trips to
-    // L2: about 1200 CTAs in all (two residencies), each over a span of pieces
+    // L2: one residency in all (three CTAs per SM), each over a span of pieces.
+    // 64 sequences of 248320: 75.4 us, with twice as many 78.9; 16 sequences of
+    // 128000: 18.8 and 19.9; 16 sequences of 248320: 37.4 and 36.2
     const int all = static_cast<int>((p.V + 3 + pq2::kPickPiece - 1) / pq2::kPickPiece);
     const int64_t most = std::max<int64_t>(1, kPickCtas / p.B);
     const int rounds = static_cast<int>((all + most - 1) / most);

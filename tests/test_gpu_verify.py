@@ -205,6 +205,14 @@ def test_repeated_calls_and_streams_agree():
         assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("V", [1, 3, 5, 2045, 2046, 2047, 2048, 2049, 4094, 4095, 4099])
+@pytest.mark.parametrize("ld", [None, 4101, 4102])
+def test_row_edges(V, ld):
+    # rows that start and end at each offset from 16 bytes
+    p = _problem([3, 1, 0, 5], V, seed=V, masked=(3,), temps=[0.7, 0.0, 1.0, 1.3], ld=ld)
+    _check(p)
+
+
 def test_binding_refuses():
     from gemm_pq2_ternary_gb300 import binding as pq2
     p = _problem([2, 2], 64, seed=13)
