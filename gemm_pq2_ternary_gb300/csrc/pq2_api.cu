@@ -594,11 +594,6 @@ pq2_status pq2_lora_add(const void* x, int64_t ld_x, const void* A, const void* 
         !aligned_to(ids, 4) || !aligned_to(ranks, 4) || !aligned_to(scales, 4) ||
         !aligned_to(y_in, type_bytes(y_type)) || !aligned_to(y_out, type_bytes(y_type)))
         return PQ2_ERR_MISALIGNED;
-    if (!workspace || workspace_bytes < pq2h::lora_workspace_bytes(M, N, K, L, R))
-        return PQ2_ERR_WORKSPACE;
-    Ctx c;
-    s = get_ctx(&c);
-    if (s != PQ2_OK) return s;
     pq2h::LoraParams p = {};
     p.x = static_cast<const uint16_t*>(x);
     p.A = static_cast<const uint16_t*>(A);
@@ -610,6 +605,10 @@ pq2_status pq2_lora_add(const void* x, int64_t ld_x, const void* A, const void* 
     p.L = static_cast<int>(L), p.R = static_cast<int>(R);
     p.bf16 = type == PQ2_BF16;
     p.y_type = y_type;
+    if (!workspace || workspace_bytes < pq2h::lora_workspace_needed(p)) return PQ2_ERR_WORKSPACE;
+    Ctx c;
+    s = get_ctx(&c);
+    if (s != PQ2_OK) return s;
     p.ctl = c.ctl;
     return cuda_status(pq2h::launch_lora(p, workspace, static_cast<cudaStream_t>(stream), c.dev));
 }

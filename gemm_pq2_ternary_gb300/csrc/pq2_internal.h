@@ -221,6 +221,7 @@ struct LoraParams {
     pq2::DevCtl ctl;
 };
 size_t lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
+size_t lora_workspace_needed(const LoraParams& p);  // for this call
 cudaError_t launch_lora(const LoraParams& p, void* workspace, cudaStream_t st,
                         const DeviceInfo& dev);
 

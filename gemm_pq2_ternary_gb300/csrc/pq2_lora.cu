@@ -2021,15 +2021,25 @@ constexpr int64_t kSms = 152;
 size_t pad(size_t b) { return (b + 255) & ~size_t(255); }
 
 struct Layout {
+    bool few;
     int splits, k_split, tile, max_tiles, rp;
     size_t part, terms, f, perm, tiles, num_tiles, bytes;
 };
 
-Layout layout(int64_t M, int64_t K, int64_t L, int64_t R) {
+// The few-token form up to kFewTokens tokens; the planned one already above 64
+// where their adapters' B is large, since its copies run further ahead (128
+// tokens, 17408 outputs: 64 adapters of rank 64 69.5 us few, 51.6 planned; 30 of
+// rank 128 64.4 and 47.7; but 64 of rank 128 at 5120 outputs 56.3 and 59.9, 64 of
+// rank 16 at 17408 both 49; 64 tokens over 64 adapters of rank 64 52.6 and 55.3).
+bool few_tokens(int64_t M, int64_t N, int64_t L, int64_t R) {
+    return M <= 64 || (M <= kFewTokens && std::min(M, L) * N * R * 2 <= 96000000);
+}
+
+Layout layout(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
     Layout y = {};
-    const bool few = M <= kFewTokens;
+    y.few = few_tokens(M, N, L, R);
     int64_t s;
-    if (few) {
+    if (y.few) {
         // K splits: two CTAs per SM over the tiles that may appear, at
         // least 16 KB of A each
         const int64_t tiles = pq2::few_tiles(M, std::min(M, L));
@@ -2046,10 +2056,10 @@ Layout layout(int64_t M, int64_t K, int64_t L, int64_t R) {
         while (s < 16 && s * tiles * 2 < 3 * kSms && K / (2 * s) >= (s < 8 ? 256 : 512)) s *= 2;
     }
     y.k_split = static_cast<int>(((K + s - 1) / s + 127) / 128 * 128);
-    y.splits = few ? static_cast<int>((K + y.k_split - 1) / y.k_split) : static_cast<int>(s);
+    y.splits = y.few ? static_cast<int>((K + y.k_split - 1) / y.k_split) : static_cast<int>(s);
     y.rp = static_cast<int>((R + 31) / 32 * 32);
     size_t o = 0;
-    if (few) {
+    if (y.few) {
         y.part = o;
         o += pad(static_cast<size_t>(y.splits) * M * R * 4);
     } else {
@@ -2060,8 +2070,8 @@ Layout layout(int64_t M, int64_t K, int64_t L, int64_t R) {
         o += pad(static_cast<size_t>(M) * 4);
         y.perm = o;
         o += pad(static_cast<size_t>(M) * 4);
-        y.tiles = o;
-        o += pad(static_cast<size_t>(y.max_tiles) * 16);
+        y.tiles = o;   // with room for as many as any M up to this one has
+        o += pad(static_cast<size_t>((M + kSmallTile - 1) / kSmallTile + std::min(L + 1, M)) * 16);
         y.num_tiles = o;
         o += 256;
     }
@@ -2223,7 +2233,7 @@ SmemLimit g_plan_smem;  // one for the kernel: run() has several instantiations
 template <bool BF, int YT>
 cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cudaStream_t st,
                 const DeviceInfo& dev) {
-    if (p.M <= kFewTokens) return run_few<BF, YT>(p, lay, ws, vec, st);
+    if (lay.few) return run_few<BF, YT>(p, lay, ws, vec, st);
     pq2::Plan pl = {};
     pl.terms = reinterpret_cast<uint16_t*>(ws + lay.terms);
     pl.f = reinterpret_cast<float*>(ws + lay.f);
@@ -2286,13 +2296,19 @@ cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cu
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
-    (void)N;
-    return layout(M, K, L, R).bytes;
+    // enough for any smaller M: few tokens may take more than many (their
+    // partial sums over K are in memory)
+    size_t most = layout(M, N, K, L, R).bytes;
+    for (int64_t m = 1; m < std::min<int64_t>(M, kFewTokens + 1); ++m)
+        most = std::max(most, layout(m, N, K, L, R).bytes);
+    return most;
 }
+
+size_t lora_workspace_needed(const LoraParams& p) { return layout(p.M, p.N, p.K, p.L, p.R).bytes; }
 
 cudaError_t launch_lora(const LoraParams& p, void* workspace, cudaStream_t st,
                         const DeviceInfo& dev) {
-    const Layout lay = layout(p.M, p.K, p.L, p.R);
+    const Layout lay = layout(p.M, p.N, p.K, p.L, p.R);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     // 4-wide accesses to y: every row starts on their boundary
     const size_t unit = p.y_type == PQ2_F32 ? 16 : 8;

@@ -369,7 +369,8 @@ pq2_status pq2_norm_residual(const pq2_norm_residual_args* args, int64_t M, int6
  *   scales  in   fp32 [L] or NULL (1)
  *   y_in, y_out  [M, N] (y_type: PQ2_F32 or PQ2_BF16; row strides ld_in,
  *                ld_out >= N); the same array, or arrays that do not overlap
- *   workspace    pq2_lora_workspace_bytes(M, N, K, L, R) bytes
+ *   workspace    pq2_lora_workspace_bytes(M, N, K, L, R) bytes; enough for any
+ *                smaller M too
  * M >= 0 and N >= 0 (either 0 enqueues nothing), 8 <= K <= PQ2_MAX_K with
  * K % 8 == 0, 8 <= R <= PQ2_LORA_MAX_R with R % 8 == 0,
  * 1 <= L <= PQ2_LORA_MAX_L, M <= PQ2_LORA_MAX_M.  x, A, B and workspace

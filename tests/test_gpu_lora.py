@@ -131,6 +131,8 @@ SHAPES = [
     (129, 6144, 700, 64, 1, "f16", "f32", dict(scales=False)),
     (4000, 256, 264, 128, 64, "f16", "bf16", {}),
     # few tokens an adapter
+    (70, 64, 5120, 256, 40, "f16", "f32", {}),
+    (90, 64, 5124, 256, 37, "bf16", "bf16", {}),
     (300, 512, 1028, 128, 40, "f16", "f32", {}),
     (300, 256, 1025, 24, 60, "bf16", "f32", dict(ld_y=1027)),
     (500, 256, 2052, 192, 100, "f16", "f32", {}),
@@ -264,6 +266,17 @@ def test_the_copy_ring_reports_a_stage_that_never_comes():
         pq2.pq2_debug_set_wait_limit_ns(2_000_000_000)
     _call(pq2, p)
     _check(pq2, p, p["out"])
+
+
+def test_a_workspace_for_many_tokens_serves_fewer():
+    from gemm_pq2_ternary_gb300 import binding as pq2
+    K, N, R, L = 5120, 640, 32, 3
+    ws = pq2.alloc_lora_workspace(500, N, K, L, R)
+    for M in (500, 129, 128, 17, 1):
+        p = _problem(M, K, N, R, L, "f16", "f32", seed=M)
+        pq2.pq2_lora_add(p["x"], p["A"], p["B"], p["ids"], p["y"], p["out"], ws,
+                         ranks=p["ranks"], scales=p["scales"])
+        _check(pq2, p, p["out"])
 
 
 def test_offsets_past_32_bits():

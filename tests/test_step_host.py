@@ -93,6 +93,11 @@ def test_lora_checks_arguments(lib):  # noqa: F811
     assert b.pq2_lora_workspace_bytes(4, 32, 60, 2, 8) == b.SIZE_MAX
     assert b.pq2_lora_workspace_bytes(0, 32, 64, 2, 8) == 0
     assert 0 < b.pq2_lora_workspace_bytes(4096, 17408, 5120, 16384, 256) < 1 << 30
+    # a workspace for many tokens serves fewer
+    for N, K, L, R in ((5120, 17408, 64, 64), (17408, 5120, 64, 128), (40, 8, 1, 8), (64, 640, 300, 16)):
+        sizes = [b.pq2_lora_workspace_bytes(M, N, K, L, R)
+                 for M in (*range(1, 140), 512, 513, 2400, 2401, 5000)]
+        assert sizes == sorted(sizes)
 
 
 def _verify(lib, b, **kw):  # noqa: F811
