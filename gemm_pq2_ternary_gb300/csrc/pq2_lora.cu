@@ -799,259 +799,161 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-constexpr int kStageK = 64;       // columns of K per pipeline stage: rows of 128 bytes
-// Pipeline stages: with the partials about 100 KB a CTA, two CTAs per SM (ranks
-// above 128: 184 KB).
-template <int RPW, int WN>
-constexpr int shrink_stages() {
-    return RPW * WN <= 2 ? 8 : RPW * WN == 4 ? 5 : 3;
+constexpr int kTcNB = 128;          // rows of a product's first operand
+
+// Matrix descriptor: K-major, 128-byte swizzle, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(1) << 16;             // leading offset (unused here)
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;     // stride offset
+    d |= static_cast<uint64_t>(1) << 46;             // descriptor version
+    d |= static_cast<uint64_t>(2) << 61;             // 128-byte swizzle
+    return d;
 }
 
-// Accumulators of a consumer warp: where it has one or two fragments, a set per
-// half of a block of 32 columns (and per block) -- a dependent instruction
-// waits some 150 cycles, and a stage brings four in a row.  With four fragments
-// a second set costs the second CTA of an SM (4096 tokens of rank 64: 159 us
-// against 148).
-template <int RPW, int WN>
-constexpr int shrink_sets() {
-    return RPW * WN == 1 ? 4 : RPW * WN == 2 ? 2 : 1;
+// D[128 x T] (+)= A[128 x 16] . B[T x 16]^T; both operands fp16, or both bf16.
+template <bool BF, int T>
+__device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t a, uint64_t b, bool add) {
+    constexpr uint32_t idesc = (1u << 4) | ((BF ? 1u : 0u) << 7) | ((BF ? 1u : 0u) << 10) |
+                               (static_cast<uint32_t>(T >> 3) << 17) |
+                               (static_cast<uint32_t>(kTcNB >> 4) << 24);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u));
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// A warp's share of one pipeline stage.  x0, a0: this lane's first rows of x
-// and A (shared-memory addresses); xat, aat: its chunk in either block of 32.
-template <bool BF, int RPW, int NI, int WN>
-__device__ __forceinline__ void shrink_stage(float (&acc)[shrink_sets<RPW, WN>()][RPW][WN][4],
-                                             uint32_t x0, uint32_t a0, const uint32_t (&xat)[2],
-                                             const uint32_t (&aat)[2]) {
-    constexpr int kSets = shrink_sets<RPW, WN>();
-#pragma unroll
-    for (int blk = 0; blk < 2; ++blk) {
-        uint4 a[RPW][2], c[NI];
-#pragma unroll
-        for (int r = 0; r < RPW; ++r)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) a[r][h] = lds_v4(a0 + (r * 16 + h * 8) * 128 + aat[blk]);
-#pragma unroll
-        for (int i = 0; i < NI; ++i) c[i] = lds_v4(x0 + i * 8 * 128 + xat[blk]);
-#pragma unroll
-        for (int r = 0; r < RPW; ++r)
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                mma16816<BF>(acc[(2 * blk) % kSets][r][i], a[r][0].x, a[r][1].x, a[r][0].y, a[r][1].y,
-                             c[i].x, c[i].y);
-#pragma unroll
-        for (int r = 0; r < RPW; ++r)
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                mma16816<BF>(acc[(2 * blk + 1) % kSets][r][i], a[r][0].z, a[r][1].z, a[r][0].w,
-                             a[r][1].w, c[i].z, c[i].w);
-    }
-}
-
-// A cluster of CTAs computes one tile: v[64 tokens][R] over its share of K
-// each, through a ring: A by TMA, 16 ranks x 64 columns a box, x by the loader
-// warps' asynchronous copies (its rows are gathered; these copies reach some
-// 17 bytes a cycle and SM, so A does not go the same way).  A row is 8 chunks
-// of 16 bytes; in x's odd rows the halves are swapped, in A's rows the chunks
-// are permuted by the 128-byte swizzle, and a lane takes the rank whose row
-// puts the 8 lanes of a 16-byte read (two rows, four chunks) into different
-// banks.  A consumer warp owns RPW rank tiles of 16 and WN groups of 8 tokens, and
-// waits for nothing but its stage.  Every CTA stores its partials of token j
-// into the shared memory of CTA j % splits of the cluster, which adds them up,
-// CTA by CTA in order, and writes the token's 16-bit terms: one cluster
-// barrier, and nobody has to stay for the others.
+constexpr int kStageK = 64;         // columns of K per pipeline stage: rows of 128 bytes
+constexpr int kFlushStages = kFlush * 32 / kStageK;
+constexpr int kShrinkMaxStages = 8;
 constexpr int kShrinkLoaders = 4;
 
-template <bool BF, int RPW, int WN>
-__global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
-    lora_shrink_tiles(pq2h::LoraParams p, Plan pl, const __grid_constant__ CUtensorMap map_a,
-                      int splits, int k_split) {
-    constexpr int kStages = shrink_stages<RPW, WN>();
-    extern __shared__ __align__(128) uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);   // swizzled rows
-    __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
-    __shared__ int abort_word;
-    volatile int* abort_flag = &abort_word;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, t = lane & 3;
-    pdl_wait();
-    pdl_launch_dependents();
-    const int index = blockIdx.x / splits;
-    const int4 tile = pl.tiles[index];    // there for every index; a tile if below num_tiles
-    if (index >= *pl.num_tiles) return;   // the whole cluster
-    const int l = tile.x, first = tile.y, count = tile.z;
-    const int rank = tile.w;
-    if (rank == 0) return;
-    // warps that have ranks and tokens
-    constexpr int kTokenWarps = kTile / 8 / WN;
-    const int busy = ((rank + 16 * RPW - 1) / (16 * RPW)) * ((count + 8 * WN - 1) / (8 * WN));
-    if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], kShrinkLoaders * 32 + 1);
-            mbar_init(&empty[s], busy);
-        }
-        abort_word = 0;
-        fence_mbar_init();
+// The loader warps' share (pt: thread of them): stages of 64 columns from k0 to
+// k1.  Thread -> chunk `chunk` of rows row0 + 16 i, the first of them to dst0.
+__device__ __forceinline__ void shrink_load(const pq2h::LoraParams& p, const Plan& pl,
+                                            const CUtensorMap* map_a, uint8_t* smem, uint64_t* full,
+                                            uint64_t* empty, int stages, int stage_bytes, int steps,
+                                            int k0, int k1, int l, int rank, int first, int count,
+                                            int pt, int chunk, int row0, uint32_t dst0,
+                                            volatile int* abort_flag) {
+    const int lane = pt & 31;
+    // Rows past the rank or the tile hold anything: a row of A only reaches its
+    // own rank's sums, a row of x its own token's, and those are not stored.
+    // Columns past K enter every sum: zeros, in x here and in A past the map's
+    // end (a share of K ends on a multiple of 64 otherwise).
+    constexpr int kRows = kShrinkLoaders * 4;   // rows per round
+    constexpr int kXRounds = kTile / kRows;
+    const uint16_t* xs[kXRounds];
+#pragma unroll
+    for (int i = 0; i < kXRounds; ++i) {
+        const int j = row0 + kRows * i;
+        xs[i] = j < count ? p.x + static_cast<size_t>(pl.perm[first + j]) * p.ld_x + k0 + chunk * 8
+                          : nullptr;
     }
-    if (splits > 1) cluster_arrive_relaxed();
-    __syncthreads();
-    const int part = splits > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const int k0 = part * k_split, k1 = min(k0 + k_split, p.K);
-    const int steps = (max(k1 - k0, 0) + kStageK - 1) / kStageK;
-    // rows of A per stage: whole shares of a warp (16 RPW)
-    const int r16 = (p.R + 16 * RPW - 1) / (16 * RPW) * (16 * RPW);
-    const int stage_bytes = (kTile + r16) * 128;
-    const uint32_t base = smem_u32(smem);
-    const int rt0 = warp / kTokenWarps * RPW, n0 = warp % kTokenWarps * WN;
-    // the rank (of 8) that this lane's row of a fragment stands for: lanes g
-    // and g + 1 of a read take rows 4 apart, whose chunks lie 4 apart
-    const int gr = (g >> 1) | ((g & 1) << 2);
-    const bool works = warp < kShrinkWarps && rt0 * 16 < rank && n0 * 8 < count;
-    float sum[RPW][WN][4];
+    const int boxes = (rank + 15) / 16;
+    int s = 0, issued = 0;
+    uint32_t turn = 0;
+    for (; issued < steps; ++issued) {
+        if (turn > 0 && !mbar_ready_warp(&empty[s], (turn - 1) & 1, p.ctl, abort_flag)) break;
+        if (issued != p.ctl.debug_skip_stage) {  // else withheld (timeout test)
+            const uint32_t st = dst0 + s * stage_bytes;
+            const int k = issued * kStageK;
+            if (pt < 32) {
+                if (lane == 0) mbar_arrive_expect_tx(&full[s], boxes * 16 * 128);
+                __syncwarp();
+                if (lane < boxes)
+                    tma_load_2d(smem + s * stage_bytes + (kTile + lane * 16) * 128, map_a, k0 + k,
+                                l * p.R + lane * 16, &full[s]);
+            }
+            if (k0 + k + kStageK <= k1) {
 #pragma unroll
-    for (int r = 0; r < RPW; ++r)
+                for (int i = 0; i < kXRounds; ++i)
+                    if (xs[i]) cp_async<16>(st + i * kRows * 128, xs[i] + k);
+            } else {
+                const bool in = k0 + k + chunk * 8 < k1;
 #pragma unroll
-        for (int i = 0; i < WN; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) sum[r][i][c] = 0.0f;
+                for (int i = 0; i < kXRounds; ++i)
+                    if (xs[i]) cp_async16(st + i * kRows * 128, in ? xs[i] + k : p.x, in ? 16 : 0);
+            }
+            cp_async_arrive(&full[s]);
+        }
+        if (++s == stages) s = 0, ++turn;
+    }
+    // the last copies land before the CTA ends, whatever the others do
+    for (int k = max(0, issued - stages); k < issued; ++k)
+        if (k != p.ctl.debug_skip_stage)
+            mbar_ready_warp(&full[k % stages], static_cast<uint32_t>(k / stages) & 1, p.ctl);
+    cp_async_wait<0>();
+}
 
-    if (warp >= kShrinkWarps) {
-        // thread -> chunk pt % 8 of rows pt / 8 + 16 i.  Rows past the rank or
-        // the tile hold anything: a row of A only reaches its own rank's sums,
-        // a row of x its own token's, and those are not stored.  Columns past
-        // K enter every sum: zeros, in x here and in A past the map's end (a
-        // share of K ends on a multiple of 64 otherwise).
-        const int pt = tid - kShrinkWarps * 32;
-        const int chunk = pt & 7, row0 = pt >> 3;
-        constexpr int kRows = kShrinkLoaders * 4;   // rows per round
-        constexpr int kXRounds = kTile / kRows;
-        const uint32_t dst0 = base + row0 * 128 + ((chunk ^ ((row0 & 1) * 4)) * 16);
-        const uint16_t* xs[kXRounds];
-#pragma unroll
-        for (int i = 0; i < kXRounds; ++i) {
-            const int j = row0 + kRows * i;
-            xs[i] = j < count ? p.x + static_cast<size_t>(pl.perm[first + j]) * p.ld_x + k0 + chunk * 8
-                              : nullptr;
-        }
-        const int boxes = (rank + 15) / 16;
-        int s = 0, issued = 0;
-        uint32_t turn = 0;
-        for (; issued < steps; ++issued) {
-            if (turn > 0 && !mbar_ready_warp(&empty[s], (turn - 1) & 1, p.ctl, abort_flag)) break;
-            if (issued != p.ctl.debug_skip_stage) {  // else withheld (timeout test)
-                const uint32_t st = dst0 + s * stage_bytes;
-                const int k = issued * kStageK;
-                if (warp == kShrinkWarps) {
-                    if (lane == 0) mbar_arrive_expect_tx(&full[s], boxes * 16 * 128);
-                    __syncwarp();
-                    if (lane < boxes)
-                        tma_load_2d(smem + s * stage_bytes + (kTile + lane * 16) * 128, &map_a, k0 + k,
-                                    l * p.R + lane * 16, &full[s]);
-                }
-                if (k0 + k + kStageK <= k1) {
-#pragma unroll
-                    for (int i = 0; i < kXRounds; ++i)
-                        if (xs[i]) cp_async<16>(st + i * kRows * 128, xs[i] + k);
-                } else {
-                    const bool in = k0 + k + chunk * 8 < k1;
-#pragma unroll
-                    for (int i = 0; i < kXRounds; ++i)
-                        if (xs[i]) cp_async16(st + i * kRows * 128, in ? xs[i] + k : p.x, in ? 16 : 0);
-                }
-                cp_async_arrive(&full[s]);
-            }
-            if (++s == kStages) s = 0, ++turn;
-        }
-        // the last copies land before the CTA ends, whatever the consumers do
-        for (int k = max(0, issued - kStages); k < issued; ++k)
-            if (k != p.ctl.debug_skip_stage)
-                mbar_ready_warp(&full[k % kStages], static_cast<uint32_t>(k / kStages) & 1, p.ctl);
-        cp_async_wait<0>();
-    } else if (works) {
-        const uint32_t xat[2] = {static_cast<uint32_t>((t ^ ((g & 1) * 4)) * 16),
-                                 static_cast<uint32_t>(((4 + t) ^ ((g & 1) * 4)) * 16)};
-        const uint32_t aat[2] = {static_cast<uint32_t>((t ^ gr) * 16),
-                                 static_cast<uint32_t>(((4 + t) ^ gr) * 16)};
-        constexpr int kSets = shrink_sets<RPW, WN>();
-        float acc[kSets][RPW][WN][4];
-#pragma unroll
-        for (int q = 0; q < kSets; ++q)
-#pragma unroll
-            for (int r = 0; r < RPW; ++r)
-#pragma unroll
-                for (int i = 0; i < WN; ++i)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[q][r][i][c] = 0.0f;
-        int s = 0;
-        uint32_t turn = 0;
-        for (int step = 0; step < steps; ++step) {
-            if (!mbar_ready_warp(&full[s], turn & 1, p.ctl, abort_flag)) {
-                *abort_flag = 1;   // the host reads the error; v is not used
-                break;
-            }
-            const uint32_t st = base + s * stage_bytes;
-            const uint32_t x0 = st + (n0 * 8 + g) * 128, a0 = st + (kTile + rt0 * 16 + gr) * 128;
-            // one group of tokens, or all of this warp's (columns past the
-            // tile's last token hold anything and are not stored)
-            if (count - n0 * 8 > 8)
-                shrink_stage<BF, RPW, WN, WN>(acc, x0, a0, xat, aat);
-            else
-                shrink_stage<BF, RPW, 1, WN>(acc, x0, a0, xat, aat);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
-            if (++s == kStages) s = 0, ++turn;
-            if ((step + 1) % (kFlush / 2) == 0 || step + 1 == steps) {
-#pragma unroll
-                for (int q = 0; q < kSets; ++q)
-#pragma unroll
-                    for (int r = 0; r < RPW; ++r)
-#pragma unroll
-                        for (int i = 0; i < WN; ++i)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                sum[r][i][c] += acc[q][r][i][c];
-                                acc[q][r][i][c] = 0.0f;
-                            }
-            }
-        }
-    }
-    // partials [from CTA][token / splits][r16], in the owner's shared memory
-    float* inbox = reinterpret_cast<float*>(smem + kStages * stage_bytes);
-    const int per_cta = (kTile + splits - 1) / splits;
-    __syncwarp();
-    if (splits > 1) cluster_wait();   // all of the cluster have started
-    if (works) {
-        const uint32_t mine = smem_u32(inbox) + part * per_cta * r16 * 4;
-#pragma unroll
-        for (int i = 0; i < WN; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int j = (n0 + i) * 8 + 2 * t + h;
-                if (j >= count) continue;
-                uint32_t to = mine + (j / splits) * r16 * 4;
-                if (splits > 1) to = map_to_rank(to, j % splits);
-#pragma unroll
-                for (int r = 0; r < RPW; ++r)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int rr = (rt0 + r) * 16 + c * 8 + gr;
-                        if (rr >= rank) continue;
-                        if (splits > 1)
-                            st_cluster_f32(to + rr * 4, sum[r][i][c * 2 + h]);
-                        else
-                            sts_f32(to + rr * 4, sum[r][i][c * 2 + h]);
-                    }
-            }
-    }
-    __syncwarp();
-    if (splits > 1)
-        cluster_sync();
-    else
-        __syncthreads();
+// The cluster's partials of this CTA's tokens (in its inbox, [from CTA][token /
+// splits][r16]) added up in order, scaled and split into 16-bit terms, a warp
+// per token.
+template <bool BF>
+__device__ __forceinline__ void shrink_finish(const pq2h::LoraParams& p, const Plan& pl, const float* inbox,
+                                              int part, int splits, int per_cta, int r16, int l,
+                                              int rank, int first, int count, int warps) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float scale = p.scales ? p.scales[l] : 1.0f;
     const size_t term_size = static_cast<size_t>(p.M) * pl.rp;
     const int blocks = (rank + 31) / 32;
-    for (int j = part + splits * warp; j < count; j += splits * (kShrinkWarps + kShrinkLoaders)) {
+    for (int j = part + splits * warp; j < count; j += splits * warps) {
         float v[8], top = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -1076,6 +978,332 @@ __global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
             }
         }
     }
+}
+
+// Up to 32 ranks.  A cluster of CTAs computes one tile: v[64 tokens][R] over
+// its share of K each, through a ring: A by TMA, 16 ranks x 64 columns a box, x
+// by the loader warps' asynchronous copies (its rows are gathered; these copies
+// reach some 17 bytes a cycle and SM, so A does not go the same way).  A row is
+// 8 chunks of 16 bytes; in x's odd rows the halves are swapped, in A's rows the
+// chunks are permuted by the 128-byte swizzle, and a lane takes the rank whose
+// row puts the 8 lanes of a 16-byte read (two rows, four chunks) into different
+// banks.  A consumer warp owns one rank tile of 16 and WN groups of 8 tokens,
+// and waits for nothing but its stage.  Every CTA stores its partials of token j
+// into the shared memory of CTA j % splits of the cluster, which adds them up,
+// CTA by CTA in order, and writes the token's 16-bit terms: one cluster
+// barrier, and nobody has to stay for the others.
+// An accumulator set per half of a block of 32 columns (WN 1: and per block):
+// a dependent mma.sync waits some 150 cycles, and a stage brings four in a row.
+template <bool BF, int WN>
+__global__ void __launch_bounds__((kShrinkWarps + kShrinkLoaders) * 32)
+    lora_shrink_small(pq2h::LoraParams p, Plan pl, const __grid_constant__ CUtensorMap map_a,
+                      int splits, int k_split, int stages) {
+    constexpr int kSets = 4 / WN;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);   // swizzled rows
+    __shared__ __align__(8) uint64_t full[kShrinkMaxStages], empty[kShrinkMaxStages];
+    __shared__ int abort_word;
+    volatile int* abort_flag = &abort_word;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int index = blockIdx.x / splits;
+    const int4 tile = pl.tiles[index];    // there for every index; a tile if below num_tiles
+    const int l = tile.x, first = tile.y, count = tile.z, rank = tile.w;
+    if (index >= *pl.num_tiles || rank == 0) return;   // the whole cluster
+    // warps that have ranks and tokens
+    constexpr int kTokenWarps = kTile / 8 / WN;
+    const int busy = ((rank + 15) / 16) * ((count + 8 * WN - 1) / (8 * WN));
+    if (tid == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&full[s], kShrinkLoaders * 32 + 1);
+            mbar_init(&empty[s], busy);
+        }
+        abort_word = 0;
+        fence_mbar_init();
+    }
+    if (splits > 1) cluster_arrive_relaxed();
+    __syncthreads();
+    const int part = splits > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int k0 = part * k_split, k1 = min(k0 + k_split, p.K);
+    const int steps = (max(k1 - k0, 0) + kStageK - 1) / kStageK;
+    const int r16 = (p.R + 15) / 16 * 16;   // rows of A per stage
+    const int stage_bytes = (kTile + r16) * 128;
+    const uint32_t base = smem_u32(smem);
+    const int r0 = warp / kTokenWarps * 16, n0 = warp % kTokenWarps * WN;
+    // the rank (of 8) that this lane's row of a fragment stands for: lanes g
+    // and g + 1 of a read take rows 4 apart, whose chunks lie 4 apart
+    const int gr = (g >> 1) | ((g & 1) << 2);
+    const bool works = warp < kShrinkWarps && r0 < rank && n0 * 8 < count;
+    float sum[WN][4];
+#pragma unroll
+    for (int i = 0; i < WN; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sum[i][c] = 0.0f;
+
+    if (warp >= kShrinkWarps) {
+        const int pt = tid - kShrinkWarps * 32, chunk = pt & 7, row0 = pt >> 3;
+        shrink_load(p, pl, &map_a, smem, full, empty, stages, stage_bytes, steps, k0, k1, l, rank, first,
+                    count, pt, chunk, row0, base + row0 * 128 + ((chunk ^ ((row0 & 1) * 4)) * 16), abort_flag);
+    } else if (works) {
+        const uint32_t xat[2] = {static_cast<uint32_t>((t ^ ((g & 1) * 4)) * 16),
+                                 static_cast<uint32_t>(((4 + t) ^ ((g & 1) * 4)) * 16)};
+        const uint32_t aat[2] = {static_cast<uint32_t>((t ^ gr) * 16),
+                                 static_cast<uint32_t>(((4 + t) ^ gr) * 16)};
+        float acc[kSets][WN][4];
+#pragma unroll
+        for (int q = 0; q < kSets; ++q)
+#pragma unroll
+            for (int i = 0; i < WN; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[q][i][c] = 0.0f;
+        int s = 0;
+        uint32_t turn = 0;
+        for (int step = 0; step < steps; ++step) {
+            if (!mbar_ready_warp(&full[s], turn & 1, p.ctl, abort_flag)) {
+                *abort_flag = 1;   // the host reads the error; v is not used
+                break;
+            }
+            const uint32_t st = base + s * stage_bytes;
+            const uint32_t x0 = st + (n0 * 8 + g) * 128, a0 = st + (kTile + r0 + gr) * 128;
+#pragma unroll
+            for (int blk = 0; blk < 2; ++blk) {
+                const uint4 a = lds_v4(a0 + aat[blk]), b = lds_v4(a0 + 8 * 128 + aat[blk]);
+                uint4 c[WN];   // columns past the tile's last token hold anything and are not stored
+#pragma unroll
+                for (int i = 0; i < WN; ++i) c[i] = lds_v4(x0 + i * 8 * 128 + xat[blk]);
+#pragma unroll
+                for (int i = 0; i < WN; ++i)
+                    mma16816<BF>(acc[(2 * blk) % kSets][i], a.x, b.x, a.y, b.y, c[i].x, c[i].y);
+#pragma unroll
+                for (int i = 0; i < WN; ++i)
+                    mma16816<BF>(acc[(2 * blk + 1) % kSets][i], a.z, b.z, a.w, b.w, c[i].z, c[i].w);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);
+            if (++s == stages) s = 0, ++turn;
+            if ((step + 1) % kFlushStages == 0 || step + 1 == steps) {
+#pragma unroll
+                for (int q = 0; q < kSets; ++q)
+#pragma unroll
+                    for (int i = 0; i < WN; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            sum[i][c] += acc[q][i][c];
+                            acc[q][i][c] = 0.0f;
+                        }
+            }
+        }
+    }
+    // partials [from CTA][token / splits][r16], in the owner's shared memory
+    float* inbox = reinterpret_cast<float*>(smem + stages * stage_bytes);
+    const int per_cta = (kTile + splits - 1) / splits;
+    __syncwarp();
+    if (splits > 1) cluster_wait();   // all of the cluster have started
+    if (works) {
+        const uint32_t mine = smem_u32(inbox) + part * per_cta * r16 * 4;
+#pragma unroll
+        for (int i = 0; i < WN; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int j = (n0 + i) * 8 + 2 * t + h;
+                if (j >= count) continue;
+                uint32_t to = mine + (j / splits) * r16 * 4;
+                if (splits > 1) to = map_to_rank(to, j % splits);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int r = r0 + c * 8 + gr;
+                    if (r >= rank) continue;
+                    if (splits > 1)
+                        st_cluster_f32(to + r * 4, sum[i][c * 2 + h]);
+                    else
+                        sts_f32(to + r * 4, sum[i][c * 2 + h]);
+                }
+            }
+    }
+    __syncwarp();
+    if (splits > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    shrink_finish<BF>(p, pl, inbox, part, splits, per_cta, r16, l, rank, first, count,
+                      kShrinkWarps + kShrinkLoaders);
+}
+
+// More ranks, on the fifth-generation tensor cores: the same ring, x's rows too
+// with the 128-byte swizzle, so that both lie as the product's operands.  One
+// warp issues the products, A's ranks as the 128 rows of an accumulator (rows
+// past the rank hold anything and reach only their own sums), the tokens as its
+// 64 columns.  256 columns of K are summed in tensor memory and then added to
+// the epilogue warps' registers in fp32, a lane per rank, while the next 256 go
+// to the other accumulator.  With mma.sync a stage took 950 cycles (rank 64: 32
+// instructions a scheduler), against 480 for its copies.  The longer way from
+// the copies to the sums costs up to 2 us: 333 tokens of 17408 columns, rank
+// 64, 26.5 us against 28.8 with mma.sync; 400 of rank 128 30.4 and 48.3; 4096
+// of 5120 columns, rank 64, 113.9 and 115.6; but 1000 tokens of rank 32 27.3
+// and 26.1, 4000 of rank 8 58.9 and 56.6.  MB: accumulators of 128 ranks.
+template <int MB>
+constexpr int shrink_threads() {
+    return (8 * MB + kShrinkLoaders + 1) * 32;
+}
+
+template <bool BF, int MB>
+__global__ void __launch_bounds__(shrink_threads<MB>(), MB == 1 ? 2 : 1)
+    lora_shrink_tiles(pq2h::LoraParams p, Plan pl, const __grid_constant__ CUtensorMap map_a,
+                      int splits, int k_split, int stages) {
+    constexpr int kEpilogue = 8 * MB, kIssuer = kEpilogue + kShrinkLoaders;
+    constexpr int kHalf = kTile / 2;             // tokens of an epilogue warp
+    constexpr uint32_t kCols = 2 * MB * kTile;   // tensor memory
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);   // swizzled rows
+    __shared__ __align__(8) uint64_t full[kShrinkMaxStages], empty[kShrinkMaxStages], dfull[2], dempty[2];
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_word;
+    volatile int* abort_flag = &abort_word;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&full[s], kShrinkLoaders * 32 + 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&dfull[i], 1);
+            mbar_init(&dempty[i], kEpilogue);
+        }
+        abort_word = 0;
+        fence_mbar_init();
+    }
+    if (warp == kIssuer) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&tmem_base)),
+                     "r"(kCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    const auto release = [&] {
+        if (warp == kIssuer)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+    };
+    pdl_wait();
+    pdl_launch_dependents();
+    const int index = blockIdx.x / splits;
+    const int4 tile = pl.tiles[index];    // there for every index; a tile if below num_tiles
+    const int l = tile.x, first = tile.y, count = tile.z;
+    const int rank = tile.w;
+    if (index >= *pl.num_tiles || rank == 0) {   // the whole cluster
+        release();
+        return;
+    }
+    if (splits > 1) cluster_arrive_relaxed();
+    const int part = splits > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int k0 = part * k_split, k1 = min(k0 + k_split, p.K);
+    const int steps = (max(k1 - k0, 0) + kStageK - 1) / kStageK;
+    const int r16 = (p.R + 15) / 16 * 16;   // rows of A per stage
+    const int stage_bytes = (kTile + r16) * 128;
+    const uint32_t base = smem_u32(smem);
+    // an epilogue warp's ranks and tokens
+    const int r0 = (warp / 8 * 4 + warp % 4) * 32, j0 = warp / 4 % 2 * kHalf;
+    const bool works = warp < kEpilogue && r0 < rank && j0 < count;
+    float sum[kHalf];
+
+    if (warp >= kEpilogue && warp < kIssuer) {
+        const int pt = tid - kEpilogue * 32, chunk = pt & 7, row0 = pt >> 3;
+        shrink_load(p, pl, &map_a, smem, full, empty, stages, stage_bytes, steps, k0, k1, l, rank, first,
+                    count, pt, chunk, row0, base + row0 * 128 + ((chunk ^ (row0 & 7)) * 16), abort_flag);
+    } else if (warp == kIssuer) {
+        int s = 0, last_s = -1;
+        uint32_t turn = 0, last_phase = 0;
+        for (int step = 0; step < steps; ++step) {
+            const int g = step / kFlushStages, d = g & 1;
+            const bool opens = step % kFlushStages == 0;
+            if (!mbar_ready_warp(&full[s], turn & 1, p.ctl, abort_flag) ||
+                (opens && g >= 2 &&
+                 !mbar_ready_warp(&dempty[d], static_cast<uint32_t>(g / 2 - 1) & 1, p.ctl, abort_flag))) {
+                *abort_flag = 1;   // the host reads the error; v is not used
+                break;
+            }
+            // x was written through the generic proxy
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            tc_fence_after();
+            const uint32_t x0 = base + s * stage_bytes, a0 = x0 + kTile * 128;
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < kStageK / 16; ++i)
+#pragma unroll
+                    for (int m = 0; m < MB; ++m)
+                        tc_mma<BF, kTile>(tmem + (d * MB + m) * kTile, sw128_desc(a0 + m * 128 * 128 + i * 32),
+                                          sw128_desc(x0 + i * 32), !opens || i > 0);
+                tc_commit(&empty[s]);
+                if ((step + 1) % kFlushStages == 0 || step + 1 == steps) tc_commit(&dfull[d]);
+            }
+            __syncwarp();
+            last_s = s;
+            last_phase = turn & 1;
+            if (++s == stages) s = 0, ++turn;
+        }
+        // no product may still be running when tensor memory is released
+        if (last_s >= 0) mbar_ready_warp(&empty[last_s], last_phase, p.ctl);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) sum[j] = 0.0f;
+        const uint32_t from = tmem + warp / 8 * kTile + j0 + (static_cast<uint32_t>(warp % 4 * 32) << 16);
+        const int groups = (steps + kFlushStages - 1) / kFlushStages;
+        for (int g = 0; g < groups; ++g) {
+            const int d = g & 1;
+            if (!mbar_ready_warp(&dfull[d], static_cast<uint32_t>(g / 2) & 1, p.ctl, abort_flag)) {
+                *abort_flag = 1;
+                break;
+            }
+            if (works) {
+                tc_fence_after();
+                const auto add = [&](auto at) {   // 16 tokens from there on
+                    constexpr int A = decltype(at)::value;
+                    float v[16];
+                    tc_ld(from + d * MB * kTile + A, v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) sum[A + j] += v[j];
+                };
+                add(std::integral_constant<int, 0>{});
+                if (count - j0 > 16) add(std::integral_constant<int, 16>{});
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&dempty[d]);
+        }
+    }
+    // partials [from CTA][token / splits][r16], in the owner's shared memory
+    float* inbox = reinterpret_cast<float*>(smem + stages * stage_bytes);
+    const int per_cta = (kTile + splits - 1) / splits;
+    __syncwarp();
+    if (splits > 1) cluster_wait();   // all of the cluster have started
+    if (works) {
+        const int r = r0 + lane, shift = 31 - __clz(splits);
+        const uint32_t mine = smem_u32(inbox) + (part * per_cta * r16 + r) * 4;
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) {
+            const int j = j0 + i;
+            if (j >= count || r >= rank) continue;
+            const uint32_t to = mine + (j >> shift) * r16 * 4;
+            if (splits > 1)
+                st_cluster_f32(map_to_rank(to, j & (splits - 1)), sum[i]);
+            else
+                sts_f32(to, sum[i]);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    if (splits > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after();
+    release();
+    shrink_finish<BF>(p, pl, inbox, part, splits, per_cta, r16, l, rank, first, count,
+                      shrink_threads<MB>() / 32);
 }
 
 // CTA (rounds x 128 outputs, tile): v's terms in shared memory, then per 32
@@ -1473,7 +1701,6 @@ constexpr int kTcUnit = 8;          // items of a unit, at most
 constexpr int kTcTail = 2;          // items taken at a time from the counter
 constexpr int kTcShares = 16;       // items a CTA from which there is a counter
 constexpr int kTcUnits = 2;         // units known at a time
-constexpr int kTcNB = 128;
 constexpr int kTcMaxStages = 8;
 constexpr int kTcABlock = kTcNB * 128;    // bytes of 64 ranks of an item's rows of B
 // For tiles of at most T tokens:
@@ -1490,84 +1717,6 @@ struct Tc {
     static constexpr int kYBytes = T * kTcNB * 4;
 };
 constexpr int kTcMaxDBufs = 8;
-
-// Matrix descriptor: K-major, 128-byte swizzle, 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>(1) << 16;             // leading offset (unused here)
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;     // stride offset
-    d |= static_cast<uint64_t>(1) << 46;             // descriptor version
-    d |= static_cast<uint64_t>(2) << 61;             // 128-byte swizzle
-    return d;
-}
-
-// D[128 x T] (+)= A[128 x 16] . B[T x 16]^T; both operands fp16, or both bf16.
-template <bool BF, int T>
-__device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t a, uint64_t b, bool add) {
-    constexpr uint32_t idesc = (1u << 4) | ((BF ? 1u : 0u) << 7) | ((BF ? 1u : 0u) << 10) |
-                               (static_cast<uint32_t>(T >> 3) << 17) |
-                               (static_cast<uint32_t>(kTcNB >> 4) << 24);
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u));
-}
-__device__ __forceinline__ bool elect_one() {
-    uint32_t one;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-    return one != 0;
-}
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[8]) {
-    uint32_t r[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                   "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
 
 // Tensor maps: y_in fp32 [M][N], box 128 x 1 (gathered by four rows); B 16-bit
 // [L * N][R], box 64 x 128, 128-byte swizzle, zeros past R; v's terms 16-bit
@@ -2117,13 +2266,26 @@ cudaError_t ensure_wide_cluster(SmemLimit& done, Kern kern) {
     return e;
 }
 
-template <bool BF, int RPW, int WN>
-cudaError_t run_shrink(const LoraParams& p, const pq2::Plan& pl, const Layout& lay, cudaStream_t st) {
-    auto kern = pq2::lora_shrink_tiles<BF, RPW, WN>;
+// MB 0: lora_shrink_small, over p.R / 16 rank tiles.
+template <bool BF, int MB, int WN>
+cudaError_t run_shrink(const LoraParams& p, const pq2::Plan& pl, const Layout& lay, cudaStream_t st,
+                       const DeviceInfo& dev) {
+    const auto kern = [] {
+        if constexpr (MB == 0)
+            return pq2::lora_shrink_small<BF, WN>;
+        else
+            return pq2::lora_shrink_tiles<BF, MB>;
+    }();
     static SmemLimit lim;
-    const size_t r16 = static_cast<size_t>((p.R + 16 * RPW - 1) / (16 * RPW) * (16 * RPW));
-    const size_t inbox = static_cast<size_t>(lay.splits) * ((kTile + lay.splits - 1) / lay.splits) * r16 * 4;
-    const size_t smem = 1024 + (kTile + r16) * 128 * pq2::shrink_stages<RPW, WN>() + inbox;
+    const int r16 = (p.R + 15) / 16 * 16, stage = (kTile + r16) * 128;
+    const int inbox = lay.splits * ((kTile + lay.splits - 1) / lay.splits) * r16 * 4;
+    // two CTAs per SM (1 KB each is the system's), above 128 ranks one
+    const int room = (MB < 2 ? (dev.max_smem_optin + 1024) / 2 - 1024 : dev.max_smem_optin) - 2048;
+    const int stages = std::min(pq2::kShrinkMaxStages, (room - inbox) / stage);
+    // a product reads MB * 128 rows of A, whatever follows the last stage's
+    const size_t smem = 1024 + std::max<size_t>(static_cast<size_t>(stages) * stage + inbox,
+                                                static_cast<size_t>(stages - 1) * stage +
+                                                    (kTile + MB * 128) * 128);
     CUtensorMap map_a;
     if (!encode_tmap_2d(&map_a, BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                         p.A, p.K, static_cast<uint64_t>(p.L) * p.R, static_cast<uint64_t>(p.K) * 2,
@@ -2139,7 +2301,7 @@ cudaError_t run_shrink(const LoraParams& p, const pq2::Plan& pl, const Layout& l
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(lay.splits * lay.max_tiles));
-    cfg.blockDim = dim3((pq2::kShrinkWarps + pq2::kShrinkLoaders) * 32);
+    cfg.blockDim = dim3(MB == 0 ? (pq2::kShrinkWarps + pq2::kShrinkLoaders) * 32 : pq2::shrink_threads<MB>());
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -2151,7 +2313,7 @@ cudaError_t run_shrink(const LoraParams& p, const pq2::Plan& pl, const Layout& l
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = lay.splits > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, p, pl, map_a, lay.splits, lay.k_split);
+    return cudaLaunchKernelEx(&cfg, kern, p, pl, map_a, lay.splits, lay.k_split, stages);
 }
 
 // The ring's shared memory: v's terms, then as many stages as fit (0: fewer
@@ -2254,13 +2416,10 @@ cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cu
     if (e != cudaSuccess) return e;
     e = launch(pq2::lora_plan_kernel, dim3(1), dim3(warps * 32), plan_smem, st, true, p, pl, warps);
     if (e != cudaSuccess) return e;
-    // 8 warps over the rank tiles, the rest over the token groups
-    const int rt = (p.R + 15) / 16;
-    e = rt == 1 ? run_shrink<BF, 1, 1>(p, pl, lay, st)
-        : rt == 2 ? run_shrink<BF, 1, 2>(p, pl, lay, st)
-        : rt <= 4 ? run_shrink<BF, 1, 4>(p, pl, lay, st)
-        : rt <= 8 ? run_shrink<BF, 1, 8>(p, pl, lay, st)
-                  : run_shrink<BF, 2, 8>(p, pl, lay, st);
+    e = p.R <= 16    ? run_shrink<BF, 0, 1>(p, pl, lay, st, dev)
+        : p.R <= 32  ? run_shrink<BF, 0, 2>(p, pl, lay, st, dev)
+        : p.R <= 128 ? run_shrink<BF, 1, 0>(p, pl, lay, st, dev)
+                     : run_shrink<BF, 2, 0>(p, pl, lay, st, dev);
     if (e != cudaSuccess) return e;
     // the ring, by 16-byte pieces of y where its rows allow, else (fp32) by
     // values; bf16 rows off their 16 bytes go by plain loads
