@@ -36,6 +36,7 @@ PQ2_WEIGHTS_STATIC = 1
 PQ2_F32 = 0
 PQ2_F16 = 1
 PQ2_BF16 = 2
+_I32, _F32 = torch.int32, torch.float32
 _TYPE = {torch.float32: PQ2_F32, torch.float16: PQ2_F16, torch.bfloat16: PQ2_BF16}
 
 # flags of the norms
@@ -84,6 +85,10 @@ class NormResidualArgs(ctypes.Structure):
 _norm_residual_args = struct.Struct("=7Q5q5i2fI")
 assert _norm_residual_args.size == ctypes.sizeof(NormResidualArgs)
 
+# pq2_lora_add_args and pq2_verify_drafts_args, likewise
+_lora_add_args = struct.Struct("=9Q8qQ2i")
+_verify_drafts_args = struct.Struct("=10Q6qQ")
+
 
 SIGNATURES = {
     "pq2_status_string": ([_I], ctypes.c_char_p),
@@ -104,9 +109,11 @@ SIGNATURES = {
     "pq2_lora_workspace_bytes": ([_I64] * 5, _SZ),
     "pq2_lora_add": ([_P, _I64, _P, _P, _I, _P, _P, _P, _P, _I64, _P, _I64, _I] + [_I64] * 5 +
                      [_P, _SZ, _P], _I),
+    "pq2_lora_add_packed": ([_P, _P], _I),
     "pq2_verify_workspace_bytes": ([_I64] * 3, _SZ),
     "pq2_verify_drafts": ([_P, _I64, _P, _P, _P, _I64, _P, _P, _I64, _P, _P, _P] + [_I64] * 3 +
                           [_P, _SZ, _P], _I),
+    "pq2_verify_drafts_packed": ([_P, _P], _I),
     "pq2_workspace_bytes": ([_I, _I64, _I64, _I64], _SZ),
     "pq2_group_dots": ([_I, _P, _P, _P, _I64, _I64, _I64, _P, _P, _SZ, _P], _I),
     "pq2_last_device_error": ([_P], _I),
@@ -322,13 +329,13 @@ def _row(t, shape, name):
     return t.data_ptr(), ty, ld
 
 
-def _vec(t, n, dt, name):
-    """Pointer of a contiguous CUDA vector of n elements."""
-    if t.dtype is not dt or t.shape != (n,):
-        raise ValueError(f"{name}: expected {dt} of shape ({n},), got {t.dtype} {tuple(t.shape)}")
-    if not (t.is_cuda and t.is_contiguous()):
-        raise ValueError(f"{name}: expected a contiguous CUDA tensor")
-    return t.data_ptr()
+def _vec(t, shape, dt, name):
+    """Pointer of a contiguous CUDA vector of that shape (n,)."""
+    if t.dtype is dt and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dt or t.shape != shape:
+        raise ValueError(f"{name}: expected {dt} of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    raise ValueError(f"{name}: expected a contiguous CUDA tensor")
 
 
 def _weight(w, H, name):
@@ -358,9 +365,11 @@ def pq2_norm_residual(y, r, r_out, w_post=None, gate=None, w_next=None, x=None, 
     shape = r.shape
     yp, yt, yl = _row(y, shape, "y")
     rp, rt, rl = _row(r, shape, "r")
-    op, ot, ol = _row(r_out, shape, "r_out")
-    if ot != rt:
-        raise ValueError("r_out: expected r's type")
+    op, ol = rp, rl
+    if r_out is not r:
+        op, ot, ol = _row(r_out, shape, "r_out")
+        if ot != rt:
+            raise ValueError("r_out: expected r's type")
     H = shape[1]
     pp = np_ = gp = xp = 0
     wt = gt = gl = xt = xl = 0
@@ -398,25 +407,31 @@ def pq2_lora_add(x, A, B, ids, y_in, y_out, workspace, ranks=None, scales=None, 
     """y_out[m] = y_in[m] + scales[l] * B[l] (A[l] x[m]) with l = ids[m]
     (l < 0: y_in[m]).  x [M, K], A [L, R, K], B [L, N, R] fp16 or bf16; ids
     int32 [M]; ranks int32 [L], scales fp32 [L] or None; y fp32 or bf16 [M, N]."""
-    shape = x.shape
-    M, K = shape
+    M, K = x.shape
     L, N, R = B.shape
     if A.shape != (L, R, K):
-        raise ValueError(f"shapes: x {tuple(shape)}, A {tuple(A.shape)}, B {tuple(B.shape)}")
-    xp, xt, xl = _row(x, shape, "x")
-    if A.dtype is not x.dtype or B.dtype is not x.dtype:
+        raise ValueError(f"shapes: x {tuple(x.shape)}, A {tuple(A.shape)}, B {tuple(B.shape)}")
+    xp, xt, xl = _row(x, (M, K), "x")
+    dt = x.dtype
+    if A.dtype is not dt or B.dtype is not dt:
         raise ValueError("A and B: expected x's type")
-    yshape = (M, N)
-    ip, it, il = _row(y_in, yshape, "y_in")
-    op, ot, ol = (ip, it, il) if y_out is y_in else _row(y_out, yshape, "y_out")
-    if it != ot:
-        raise ValueError("y_out: expected y_in's type")
-    wp, wb = (None, 0) if workspace is None else (_ptr(workspace), workspace.nbytes)
-    _check(_lib.pq2_lora_add(xp, xl, _ptr(A), _ptr(B), xt, _vec(ids, M, torch.int32, "ids"),
-                             None if ranks is None else _vec(ranks, L, torch.int32, "ranks"),
-                             None if scales is None else _vec(scales, L, torch.float32, "scales"),
-                             ip, il, op, ol, it, M, N, K, L, R, wp, wb, _stream(stream)),
-           "pq2_lora_add")
+    if not (A.is_contiguous() and B.is_contiguous() and A.is_cuda and B.is_cuda):
+        raise ValueError("expected a contiguous CUDA tensor")
+    ip, it, il = _row(y_in, (M, N), "y_in")
+    op, ol = ip, il
+    if y_out is not y_in:
+        op, ot, ol = _row(y_out, (M, N), "y_out")
+        if it != ot:
+            raise ValueError("y_out: expected y_in's type")
+    wp, wb = (0, 0) if workspace is None else (_ptr(workspace), workspace.nbytes)
+    args = _lora_add_args.pack(
+        xp, A.data_ptr(), B.data_ptr(), _vec(ids, (M,), _I32, "ids"),
+        0 if ranks is None else _vec(ranks, (L,), _I32, "ranks"),
+        0 if scales is None else _vec(scales, (L,), _F32, "scales"),
+        ip, op, wp, xl, il, ol, M, N, K, L, R, wb, xt, it)
+    status = _lib.pq2_lora_add_packed(args, _stream(stream))
+    if status:
+        raise PQ2Error(status, "pq2_lora_add")
 
 
 def pq2_verify_workspace_bytes(B, rows, V) -> int:
@@ -435,22 +450,24 @@ def pq2_verify_drafts(logits, row_start, drafts, q, u, e, temperature, accepted,
     """Kept drafts of each sequence and the token after them: logits, q (or
     None) fp32 [rows, V]; row_start int32 [B + 1]; drafts, tokens int32
     [rows]; u fp32 [rows]; e fp32 [B, V]; temperature fp32, accepted int32 [B]."""
-    rows, V = logits.shape
+    shape = logits.shape
+    rows, V = shape
     nb = temperature.shape[0]
-    lp, lt, ll = _row(logits, logits.shape, "logits")
+    lp, lt, ll = _row(logits, shape, "logits")
     ep, et, el = _row(e, (nb, V), "e")
-    qp, qt, ql = (None, PQ2_F32, 0) if q is None else _row(q, logits.shape, "q")
+    qp, qt, ql = (0, PQ2_F32, 0) if q is None else _row(q, shape, "q")
     if lt or et or qt:
         raise ValueError("logits, q and e: expected torch.float32")
-    i32, f32 = torch.int32, torch.float32
-    wp, wb = (None, 0) if workspace is None else (_ptr(workspace), workspace.nbytes)
-    _check(_lib.pq2_verify_drafts(lp, ll, _vec(row_start, nb + 1, i32, "row_start"),
-                                  _vec(drafts, rows, i32, "drafts"), qp, ql,
-                                  _vec(u, rows, f32, "u"), ep, el,
-                                  _vec(temperature, nb, f32, "temperature"),
-                                  _vec(accepted, nb, i32, "accepted"),
-                                  _vec(tokens, rows, i32, "tokens"), nb, rows, V, wp, wb,
-                                  _stream(stream)), "pq2_verify_drafts")
+    wp, wb = (0, 0) if workspace is None else (_ptr(workspace), workspace.nbytes)
+    n, m = (rows,), (nb,)
+    args = _verify_drafts_args.pack(
+        lp, _vec(row_start, (nb + 1,), _I32, "row_start"), _vec(drafts, n, _I32, "drafts"), qp,
+        _vec(u, n, _F32, "u"), ep, _vec(temperature, m, _F32, "temperature"),
+        _vec(accepted, m, _I32, "accepted"), _vec(tokens, n, _I32, "tokens"), wp,
+        ll, ql, el, nb, rows, V, wb)
+    status = _lib.pq2_verify_drafts_packed(args, _stream(stream))
+    if status:
+        raise PQ2Error(status, "pq2_verify_drafts")
 
 
 def pq2_group_dots(op, qp, T, codes, dots, workspace=None, stream=None):

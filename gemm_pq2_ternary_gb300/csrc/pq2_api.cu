@@ -613,6 +613,16 @@ pq2_status pq2_lora_add(const void* x, int64_t ld_x, const void* A, const void* 
     return cuda_status(pq2h::launch_lora(p, workspace, static_cast<cudaStream_t>(stream), c.dev));
 }
 
+// (bindings build these structs byte by byte)
+static_assert(sizeof(pq2_lora_add_args) == 152 && sizeof(pq2_verify_drafts_args) == 136, "no padding");
+
+pq2_status pq2_lora_add_packed(const pq2_lora_add_args* a, void* stream) {
+    if (!a) return PQ2_ERR_INVALID_ARG;
+    return pq2_lora_add(a->x, a->ld_x, a->A, a->B, a->type, a->ids, a->ranks, a->scales, a->y_in,
+                        a->ld_in, a->y_out, a->ld_out, a->y_type, a->M, a->N, a->K, a->L, a->R,
+                        a->workspace, a->workspace_bytes, stream);
+}
+
 static pq2_status check_verify(int64_t B, int64_t rows, int64_t V) {
     if (B < 0 || rows < 0 || V < 1) return PQ2_ERR_INVALID_ARG;
     // pieces of rows, and of sequences, are counted in 31 bits
@@ -655,6 +665,13 @@ pq2_status pq2_verify_drafts(const float* logits, int64_t ld_logits, const int32
     p.B = B, p.rows = rows, p.V = static_cast<int>(V);
     p.ctl = c.ctl;
     return cuda_status(pq2h::launch_verify(p, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+pq2_status pq2_verify_drafts_packed(const pq2_verify_drafts_args* a, void* stream) {
+    if (!a) return PQ2_ERR_INVALID_ARG;
+    return pq2_verify_drafts(a->logits, a->ld_logits, a->row_start, a->drafts, a->q, a->ld_q, a->u,
+                             a->e, a->ld_e, a->temperature, a->accepted, a->tokens, a->B, a->rows,
+                             a->V, a->workspace, a->workspace_bytes, stream);
 }
 
 pq2_status pq2_group_dots(int op, const int8_t* qp, const int32_t* T, const uint8_t* codes,

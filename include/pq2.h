@@ -386,6 +386,19 @@ pq2_status pq2_lora_add(const void* x, int64_t ld_x, const void* A, const void* 
                         const void* y_in, int64_t ld_in, void* y_out, int64_t ld_out, int y_type,
                         int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, void* workspace,
                         size_t workspace_bytes, void* stream);
+/* The same with the arguments in one struct, for bindings that convert them
+ * one by one. */
+typedef struct {
+    const void *x, *A, *B;
+    const int32_t *ids, *ranks;
+    const float* scales;
+    const void* y_in;
+    void *y_out, *workspace;
+    int64_t ld_x, ld_in, ld_out, M, N, K, L, R;
+    size_t workspace_bytes;
+    int32_t type, y_type;
+} pq2_lora_add_args;
+pq2_status pq2_lora_add_packed(const pq2_lora_add_args* args, void* stream);
 
 /*
  * pq2_verify_drafts -- which drafted tokens the target model keeps, and the
@@ -424,6 +437,18 @@ pq2_status pq2_verify_drafts(const float* logits, int64_t ld_logits, const int32
                              const float* e, int64_t ld_e, const float* temperature,
                              int32_t* accepted, int32_t* tokens, int64_t B, int64_t rows, int64_t V,
                              void* workspace, size_t workspace_bytes, void* stream);
+/* The same with the arguments in one struct, for bindings that convert them
+ * one by one. */
+typedef struct {
+    const float* logits;
+    const int32_t *row_start, *drafts;
+    const float *q, *u, *e, *temperature;
+    int32_t *accepted, *tokens;
+    void* workspace;
+    int64_t ld_logits, ld_q, ld_e, B, rows, V;
+    size_t workspace_bytes;
+} pq2_verify_drafts_args;
+pq2_status pq2_verify_drafts_packed(const pq2_verify_drafts_args* args, void* stream);
 
 /*
  * pq2_workspace_bytes -- scratch bytes `op` needs for this shape (0 if none,

@@ -144,3 +144,38 @@ def test_bindings_refuse_host_tensors(lib):  # noqa: F811
         b.pq2_lora_add(h, torch.zeros((1, 8, 8), dtype=torch.float16),
                        torch.zeros((1, 4, 8), dtype=torch.float16),
                        torch.zeros(2, dtype=torch.int32), r, r, None)
+
+
+def test_packed_arguments_meet_the_same_checks(lib):  # noqa: F811
+    from gemm_pq2_ternary_gb300 import binding as b
+    assert lib.pq2_lora_add_packed(None, None) == b.PQ2_ERR_INVALID_ARG
+    assert lib.pq2_verify_drafts_packed(None, None) == b.PQ2_ERR_INVALID_ARG
+    # each field in its place: only the one that is wrong decides
+    ok = dict(x=FAKE, A=FAKE, B=FAKE, ids=FAKE, ranks=0, scales=0, y_in=FAKE, y_out=FAKE, workspace=FAKE,
+              ld_x=64, ld_in=32, ld_out=32, M=4, N=32, K=64, L=2, R=8, workspace_bytes=0, type=b.PQ2_F16,
+              y_type=b.PQ2_F32)
+
+    def lora(**kw):
+        return lib.pq2_lora_add_packed(b._lora_add_args.pack(*{**ok, **kw}.values()), None)
+    assert lora() == b.PQ2_ERR_WORKSPACE
+    assert lora(M=0) == b.PQ2_OK
+    assert lora(K=60) == lora(R=9) == b.PQ2_ERR_UNSUPPORTED_SHAPE
+    for kw in (dict(x=0), dict(B=0), dict(ids=0), dict(y_in=0), dict(y_out=0), dict(ld_x=56),
+               dict(ld_in=31), dict(ld_out=31), dict(type=b.PQ2_F32), dict(y_type=b.PQ2_F16),
+               dict(L=0), dict(M=-1), dict(N=-1)):
+        assert lora(**kw) == b.PQ2_ERR_INVALID_ARG, kw
+    for kw in (dict(A=ODD), dict(workspace=ODD), dict(ranks=FAKE + 2), dict(scales=FAKE + 2)):
+        assert lora(**kw) == b.PQ2_ERR_MISALIGNED, kw
+    ok2 = dict(logits=FAKE, row_start=FAKE, drafts=FAKE, q=FAKE, u=FAKE, e=FAKE, temperature=FAKE,
+               accepted=FAKE, tokens=FAKE, workspace=FAKE, ld_logits=50, ld_q=50, ld_e=50, B=2, rows=4,
+               V=50, workspace_bytes=0)
+
+    def verify(**kw):
+        return lib.pq2_verify_drafts_packed(b._verify_drafts_args.pack(*{**ok2, **kw}.values()), None)
+    assert verify() == b.PQ2_ERR_WORKSPACE
+    assert verify(B=0) == b.PQ2_OK
+    for kw in (dict(ld_logits=49), dict(ld_q=49), dict(ld_e=49), dict(V=0), dict(rows=-1), dict(logits=0),
+               dict(row_start=0), dict(temperature=0), dict(accepted=0)):
+        assert verify(**kw) == b.PQ2_ERR_INVALID_ARG, kw
+    for kw in (dict(q=FAKE + 2), dict(e=FAKE + 2), dict(workspace=ODD)):
+        assert verify(**kw) == b.PQ2_ERR_MISALIGNED, kw
