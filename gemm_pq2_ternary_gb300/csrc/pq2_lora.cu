@@ -6,26 +6,8 @@
 // A is [L][R][K], B [L][N][R], fp16 or bf16 like x; y is the projection's
 // output.  Two kernels, "shrink" (x -> v) and "expand" (v -> y').
 //
-// Both products run on the warp-level tensor instructions
-// (mma.m16n8k16, fp32 accumulators) with the weights as the 16-row operand
-// and the tokens as the 8 columns: a decode step has one or a few tokens per
-// adapter, and 8 columns waste the least.  The sum index may be visited in
-// any order, so a lane feeds the instructions from 16-byte loads of 8
-// consecutive values (columns 8t .. 8t + 7 of a block of 32, t = lane % 4):
-// the first instruction takes their first four, the second the others, the
-// same for both operands.  Weights go from global memory straight to
-// registers, with no shared-memory stage: each is used once per tile of
-// tokens.
-//
-// Precision.  v stays fp32 and would lose 13 bits (16 for bf16) as an operand
-// of the expand product, so it enters as a sum of 16-bit terms: hi + lo for
-// fp16 (22 bits below the largest |v| of the token; each token is scaled by a
-// power of two, undone in fp32, so no term overflows), hi + mid + lo for
-// bf16 (24 bits).  Tensor accumulation may round towards zero: chains are cut
-// every 16 instructions and added up in fp32.
-//
 // Two forms:
-//   few tokens (M <= 128): every CTA finds its tile of at most 8 tokens of one
+//   few tokens (up to 128): every CTA finds its tile of at most 8 tokens of one
 //     adapter itself, and expand adds up the K-split partials of shrink in a
 //     fixed order.  Two launches.
 //   more tokens: a plan kernel sorts the tokens by adapter into tiles of at
@@ -35,8 +17,32 @@
 //     shared memory against v's 16-bit terms.  Three launches.
 // Results do not depend on which tokens share a tile: deterministic.
 //
+// The few-token form runs on the warp-level tensor instructions
+// (mma.m16n8k16, fp32 accumulators) with the weights as the 16-row operand
+// and the tokens as the 8 columns: a decode step has one or a few tokens per
+// adapter, and 8 columns waste the least.  The sum index may be visited in
+// any order, so a lane feeds the instructions from 16-byte loads of 8
+// consecutive values (columns 8t .. 8t + 7 of a block of 32, t = lane % 4):
+// the first instruction takes their first four, the second the others, the
+// same for both operands.  Weights go from global memory straight to
+// registers, with no shared-memory stage: each is used once per tile of
+// tokens.  The planned form runs on tcgen05 with accumulators in tensor memory
+// (shrink above 32 ranks; expand for fp32 y where two stages of its ring fit:
+// up to rank 128, for bf16 64), else on the same instructions from shared
+// memory.
+//
+// Precision.  v stays fp32 and would lose 13 bits (16 for bf16) as an operand
+// of the expand product, so it enters as a sum of 16-bit terms: hi + lo for
+// fp16 (22 bits below the largest |v| of the token; each token is scaled by a
+// power of two, undone in fp32, so no term overflows), hi + mid + lo for
+// bf16 (24 bits).  Tensor accumulation may round towards zero: chains are cut
+// every 16 instructions and added up in fp32.
+//
 // Bounds: bytes.  Decode: A and B of the adapters in use; prompts: y in and
-// out (8 N bytes per token against 2 K + 2 R (K + N) / tokens).
+// out (8 N bytes per token against 2 K + 2 R (K + N) / tokens).  Measured: one
+// token, rank 16, 5120 -> 17408: 4.6 us (the two launches); 48 tokens over 32
+// adapters of rank 32, 6144 -> 5120: 11.2 us (1.8 TB/s); 4096 tokens, rank 64,
+// 5120 -> 17408: 113.9 us (5.5 TB/s, 82% of the copy rate).
 #include <algorithm>
 #include <cstddef>
 #include <type_traits>
@@ -1680,8 +1686,8 @@ __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
 // 116 us and the last at 134).  The items of one tile that a CTA takes in a
 // row are a unit.  The scheduler warp fixes the units ahead and publishes them
 // to the others; one warp loads a unit's terms while the unit before is under
-// way (a tile change took 3 us otherwise); one looks at each item between its copies and its product: where the rank is no
-// multiple of 16, it puts zeros over the ranks past it that the product would
+// way (a tile change took 3 us otherwise); one looks at each item between its
+// copies and its product: where the rank is no multiple of 16, it puts zeros over the ranks past it that the product would
 // read (they may hold anything, and v's zero times a NaN is a NaN).
 // Everyone who waits on a barrier sees each of its phases: a parity tells the
 // phase meant only from the one before.
@@ -2199,7 +2205,12 @@ Layout layout(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
         // a cluster per tile: one and a half CTAs per SM over the tiles that
         // are likely, at least 256 columns each; more than 8 CTAs (the portable
         // cluster size) from 512 columns each
-        y.tile = M <= 8 * L ? kSmallTile : kTile;
+        // small tiles up to 32 tokens an adapter: expand's stages are smaller, so
+        // there are more, and more items.  129 tokens over 64 adapters of rank 64,
+        // 17408 outputs: 49.0 us against 60.7 with 64; 1000 over 64 of rank 16 38.9
+        // and 44.1; 250 over 10 of rank 64 26.7 and 29.4; but 600 over 10 of rank
+        // 32 30.9 and 23.7, 1000 over 30 of rank 24 84.6 and 42.0
+        y.tile = M <= 32 * L ? kSmallTile : kTile;
         const int64_t tiles = (M + y.tile - 1) / y.tile + std::min(L, M / 2);
         s = 1;
         while (s < 16 && s * tiles * 2 < 3 * kSms && K / (2 * s) >= (s < 8 ? 256 : 512)) s *= 2;
@@ -2357,7 +2368,10 @@ cudaError_t run_ring(const LoraParams& p, const pq2::Plan& pl, cudaStream_t st, 
 }
 
 // fp32 y on the tensor-memory form, where two stages fit and y's offsets and
-// B's rows count in 31 bits.
+// B's rows count in 31 bits (us with it, and on the ring of mma.sync: 4096
+// tokens, rank 64, 17408 outputs 114.0 and 147.0; 1000 47.8 and 57.6; 4000 of
+// rank 8, 5120 outputs 56.7 and 62.2; 300 of rank 128 22.6 and 23.5; 129 of rank
+// 16, 5120 outputs 16.1 and 15.8).
 template <bool BF, bool kTma, int T>
 cudaError_t run_tc(const LoraParams& p, const pq2::Plan& pl, cudaStream_t st, const DeviceInfo& dev,
                    bool* taken) {
