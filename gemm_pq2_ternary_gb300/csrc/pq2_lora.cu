@@ -7,7 +7,7 @@
 // output.  Two kernels, "shrink" (x -> v) and "expand" (v -> y').
 //
 // Two forms:
-//   few tokens (up to 128): every CTA finds its tile of at most 8 tokens of one
+//   few tokens (to 128 at most): every CTA finds its tile of at most 8 tokens of one
 //     adapter itself, and expand adds up the K-split partials of shrink in a
 //     fixed order.  Two launches.
 //   more tokens: a plan kernel sorts the tokens by adapter into tiles of at
@@ -639,6 +639,8 @@ struct Plan {
 // One CTA: stable counting sort of the tokens by adapter (tokens without one
 // last), cut into tiles of at most pl.tile.  Every warp counts and places a
 // contiguous range of tokens in its own histogram, so the order is fixed.
+// Bound by its chain of barriers and shared-memory trips: 3 us for 333 tokens,
+// 6 for 4096.
 __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Plan pl, int warps) {
     extern __shared__ int hist[];  // [warps][bins], then offsets [bins + 1], tiles and ranks [bins]
     __shared__ int ws[2][32];
@@ -1674,23 +1676,27 @@ __global__ void __launch_bounds__((kRingWarps + kRingLoaders) * 32, 1)
 
 // The ring's expand for fp32 y: the same items, with the product on tcgen05
 // (kind::f16).  128 outputs are the rows of A (B's rows, K-major, 128-byte
-// swizzle, by TMA), the tile's 64 tokens the rows of B (v's terms, a pass of
-// the product each), and the sum arrives in tensor memory, 64 columns an item,
-// four items in flight.  One thread issues; the warps only add, store and hand
+// swizzle, by TMA), the tile's tokens the rows of B (v's terms, a pass of the
+// product each), and the sum arrives in tensor memory, a column per token,
+// several items in flight.  The epilogue's warps only add, store and hand
 // back: 200 instructions a warp and item where the mma.sync form takes 800 and
 // waits for its own results.  A lane is an output: y is read and written 128
 // bytes a warp, one value a lane, so its rows need no alignment for that.
+//
 // A CTA takes a contiguous share of the items; where there are many, the
-// shares stop at three quarters and the rest is taken from a counter, a few
+// shares stop at three quarters and the rest is taken from a counter, two
 // items at a time (with shares alone the median CTA of 4096 tokens was done at
-// 116 us and the last at 134).  The items of one tile that a CTA takes in a
-// row are a unit.  The scheduler warp fixes the units ahead and publishes them
-// to the others; one warp loads a unit's terms while the unit before is under
-// way (a tile change took 3 us otherwise); one looks at each item between its
-// copies and its product: where the rank is no multiple of 16, it puts zeros over the ranks past it that the product would
-// read (they may hold anything, and v's zero times a NaN is a NaN).
+// 116 us and the last at 134: 130.4 us for the call against 117.1).  The items
+// of one tile that a CTA takes in a row, eight at most, are a unit.  The
+// scheduler warp fixes the units ahead and publishes them to the others; one
+// warp loads a unit's terms while the unit before is under way (a tile change
+// took 3 us otherwise); one looks at each item between its copies and its
+// product: where the rank is no multiple of 16, it puts zeros over the ranks
+// past it that the product would read (they may hold anything, and v's zero
+// times a NaN is a NaN).
 // Everyone who waits on a barrier sees each of its phases: a parity tells the
 // phase meant only from the one before.
+// Bound by HBM: 4096 tokens, rank 64, 17408 outputs 93 us alone, 5.8 TB/s.
 constexpr int kTcEpilogue = 8;      // warps, two per quarter of the lanes
 constexpr int kTcIssuer = 8, kTcProducer = 9, kTcFixer = 10, kTcTerms = 11, kTcScheduler = 12;
 constexpr int kTcIssuer2 = 13;      // where there are two groups

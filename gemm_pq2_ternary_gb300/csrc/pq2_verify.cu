@@ -23,6 +23,9 @@
 //       key (score bits, then lowest index first).  atomicMax
 //       joins the keys: the maximum does not depend on the order.  The last
 //       CTA of a sequence writes the result.
+// Measured: one sequence of 4 rows of 248320 7.2 us; 64 of them 75.4 us, 5.1
+// TB/s of the bytes that the call cannot do without (the first kernel alone 5.6
+// TB/s).
 #include <algorithm>
 #include <climits>
 

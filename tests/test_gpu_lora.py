@@ -130,6 +130,11 @@ SHAPES = [
     (1025, 1000, 1028, 48, 2, "bf16", "f32", dict(ranks=False, ids="runs")),
     (129, 6144, 700, 64, 1, "f16", "f32", dict(scales=False)),
     (4000, 256, 264, 128, 64, "f16", "bf16", {}),
+    # clusters of 16 with each count of ranks
+    (140, 17408, 130, 256, 2, "f16", "f32", {}),
+    (131, 17400, 260, 136, 3, "bf16", "f32", dict(ids="runs")),
+    (135, 17408, 132, 96, 2, "bf16", "f32", {}),
+    (200, 17408, 132, 24, 2, "f16", "f32", {}),
     # few tokens an adapter
     (70, 64, 5120, 256, 40, "f16", "f32", {}),
     (90, 64, 5124, 256, 37, "bf16", "bf16", {}),
