@@ -41,7 +41,7 @@
 // Bounds: bytes.  Decode: A and B of the adapters in use; prompts: y in and
 // out (8 N bytes per token against 2 K + 2 R (K + N) / tokens).  Measured: one
 // token, rank 16, 5120 -> 17408: 4.6 us (the two launches); 48 tokens over 32
-// adapters of rank 32, 6144 -> 5120: 11.2 us (1.8 TB/s); 4096 tokens, rank 64,
+// adapters of rank 32, 6144 -> 5120: 10.5 us (1.9 TB/s); 4096 tokens, rank 64,
 // 5120 -> 17408: 113.9 us (5.5 TB/s, 82% of the copy rate).
 #include <algorithm>
 #include <cstddef>
@@ -477,6 +477,17 @@ __device__ __forceinline__ void y_fetch(const pq2h::LoraParams& p, float4 (&y)[N
         }
 }
 
+// Rounds a CTA from which a round's lines are asked for as whole lines, before
+// its loads take them in pieces of 64 bytes (us with and without: 64 tokens over
+// 64 adapters of rank 64, 17408 outputs, 17 rounds, 50.0 and 52.2; 32 over 32 of
+// rank 128 41.0 and 42.7; at 4 rounds, 48 tokens over 32 adapters of rank 32,
+// 5120 outputs, 10.8 and 10.5).
+constexpr int kAskRounds = 8;
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // Few tokens: CTA (32 outputs a warp, tile).  The operands that do not come
 // from shrink (B, y) are loaded before the dependency wait: shrink lets this
 // kernel start only after its own wait, so everything before it is done.
@@ -512,6 +523,19 @@ __global__ void __launch_bounds__(kExpandMaxWarps * 32)
     load_b(0, 0, n);
     if (!kOne) load_b(1, 1, n);
     y_fetch<YT, 1>(p, y[0], tok, count, n, vec != 0);
+    // the lines of a round: B a row per lane, y a token per lane
+    const auto ask = [&](int first) {   // the warp's first output there
+        if (first + lane < p.N) {
+            const uint8_t* rows = reinterpret_cast<const uint8_t*>(
+                p.B + (static_cast<size_t>(max(l, 0)) * p.N + first + lane) * p.R);
+            for (int c = 0; c < rank * 2; c += 128) prefetch_l2(rows + c);
+        }
+        if (lane < count && first < p.N)
+            prefetch_l2(static_cast<const uint8_t*>(p.y_in) +
+                        (static_cast<size_t>(tok[lane]) * p.ld_in + first) * (YT == PQ2_F32 ? 4 : 2));
+    };
+    const int first = n - 4 * (lane >> 2);
+    const bool asks = rounds >= kAskRounds;
     const float scale = l >= 0 && p.scales ? __ldcg(p.scales + l) : 1.0f;
 
     pdl_wait();
@@ -590,6 +614,7 @@ __global__ void __launch_bounds__(kExpandMaxWarps * 32)
             for (int s = 0; s < 2; ++s) {
                 if (round + s >= rounds) return;
                 if (round + s + 1 < rounds) {
+                    if (asks) ask(first + (round + s + 1) * step);
                     load_b(1 - s, 0, n + step);
                     y_fetch<YT, 1>(p, y[1 - s], tok, count, n + step, vec != 0);
                 }
@@ -600,6 +625,7 @@ __global__ void __launch_bounds__(kExpandMaxWarps * 32)
             }
         } else {
             if (round > 0) {
+                if (asks) ask(first + round * step);
                 load_b(0, 0, n);
                 load_b(1, 1, n);
                 y_fetch<YT, 1>(p, y[0], tok, count, n, vec != 0);
