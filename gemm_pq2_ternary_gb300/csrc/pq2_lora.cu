@@ -41,7 +41,7 @@
 // Bounds: bytes.  Decode: A and B of the adapters in use; prompts: y in and
 // out (8 N bytes per token against 2 K + 2 R (K + N) / tokens).  Measured: one
 // token, rank 16, 5120 -> 17408: 4.6 us (the two launches); 48 tokens over 32
-// adapters of rank 32, 6144 -> 5120: 10.5 us (1.9 TB/s); 4096 tokens, rank 64,
+// adapters of rank 32, 6144 -> 5120: 11.4 us (1.7 TB/s); 4096 tokens, rank 64,
 // 5120 -> 17408: 113.9 us (5.5 TB/s, 82% of the copy rate).
 #include <algorithm>
 #include <cstddef>
