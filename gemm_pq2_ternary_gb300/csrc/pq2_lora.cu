@@ -2214,12 +2214,13 @@ struct Layout {
 };
 
 // The few-token form up to kFewTokens tokens; the planned one already above 64
-// where their adapters' B is large, since its copies run further ahead (128
-// tokens, 17408 outputs: 64 adapters of rank 64 69.5 us few, 51.6 planned; 30 of
-// rank 128 64.4 and 47.7; but 64 of rank 128 at 5120 outputs 56.3 and 59.9, 64 of
-// rank 16 at 17408 both 49; 64 tokens over 64 adapters of rank 64 52.6 and 55.3).
+// where tokens and their adapters' B are many, since its copies run further
+// ahead and read B once for 16 tokens (17408 outputs, us few and planned: 128
+// tokens over 64 adapters of rank 64 56.5 and 51.7, over 30 of rank 128 54.5 and
+// 38.4; 66 over 64 of rank 128 71.3 and 64.9; but 80 over 64 of rank 64 47.3 and
+// 53.0; 128 over 64 of rank 128 with 5120 outputs 50.2 and 59.9).
 bool few_tokens(int64_t M, int64_t N, int64_t L, int64_t R) {
-    return M <= 64 || (M <= kFewTokens && std::min(M, L) * N * R * 2 <= 96000000);
+    return M <= 64 || (M <= kFewTokens && M * std::min(M, L) * N * R * 2 <= 15000000000);
 }
 
 Layout layout(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
@@ -2286,13 +2287,15 @@ cudaError_t run_few(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec
     e = ensure_smem(lim[rb == 1], kern, smem);
     if (e != cudaSuccess) return e;
     // 128 outputs a CTA while the GPU has SMs to spare; else 256, and as many
-    // rounds of them as keep the CTAs to one residency (two per SM): a CTA's
-    // start (its tile, v) costs several trips to L2
+    // rounds of them as keep the CTAs to about one residency (two per SM): a
+    // CTA's start (its tile, v) costs several trips to L2.  Rounded up, since
+    // `all` is the most tiles that may appear (64 tokens over 64 adapters of rank
+    // 64, 17408 outputs: 45.3 us, rounded down 50.0, with 2.5 per SM 58.6)
     const int64_t all = pq2::few_tiles(p.M, std::min(p.M, p.L + 1));
     const bool spare = (p.N + 127) / 128 * all <= 2 * kSms;
     const int cols = (spare ? pq2::kExpandWarps : pq2::kExpandMaxWarps) * 32;
     const int64_t blocks = (p.N + cols - 1) / cols;
-    const int64_t per_tile = std::max<int64_t>(1, 2 * kSms / all);
+    const int64_t per_tile = (2 * kSms + all - 1) / all;
     const int rounds = spare ? 1 : static_cast<int>((blocks + per_tile - 1) / per_tile);
     return launch(kern,
                   dim3(static_cast<unsigned>((blocks + rounds - 1) / rounds), static_cast<unsigned>(all)),

@@ -137,6 +137,7 @@ SHAPES = [
     (200, 17408, 132, 24, 2, "f16", "f32", {}),
     # few tokens an adapter
     (70, 64, 5120, 256, 40, "f16", "f32", {}),
+    (127, 64, 5120, 256, 50, "f16", "f32", {}),
     (90, 64, 5124, 256, 37, "bf16", "bf16", {}),
     (300, 512, 1028, 128, 40, "f16", "f32", {}),
     (300, 256, 1025, 24, 60, "bf16", "f32", dict(ld_y=1027)),
