@@ -23,7 +23,7 @@
 //       key (score bits, then lowest index first).  atomicMax
 //       joins the keys: the maximum does not depend on the order.  The last
 //       CTA of a sequence writes the result.
-// Measured: one sequence of 4 rows of 248320 7.2 us; 64 of them 75.4 us, 5.1
+// Measured: one sequence of 4 rows of 248320 6.9 us; 64 of them 76 us, 5.0
 // TB/s of the bytes that the call cannot do without (the first kernel alone 5.6
 // TB/s).
 #include <algorithm>
@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kVecs = 4;                            // 16-byte vectors per thread at once
+constexpr int kVecs = 2;                            // 16-byte vectors per thread and array at once
 constexpr int kStatVecs = 8;                        // of stats (4: 5 us more for 256 rows)
 constexpr int kPiece = kThreads * kStatVecs * 4;    // values of a row per CTA of stats
 constexpr int kPickPiece = kThreads * kVecs * 4;    // and per round of a CTA of pick
@@ -282,23 +282,27 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(pq2h::VerifyParam
         const int off = lead(l);
         const bool ve = lead(e) == off, vq = q && lead(q) == off;
         unsigned long long k0 = 0, k1 = 0;
-        for (int piece = 0; piece < pieces && m > neg_inf(); ++piece) {
+        // two pieces in turn: one is on its way while the other is reduced
+        float4 lv[2][kVecs], ev[2][kVecs], qv[2][kVecs];
+        const auto fetch = [&](int slot, int piece) {
             const int e0 = (span * pieces + piece) * kPickPiece - off;
-            if (e0 >= p.V) break;
-            float4 lv[kVecs], ev[kVecs], qv[kVecs];
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
                 const int v0 = e0 + (i * kThreads + tid) * 4;
-                lv[i] = load4(l, v0, p.V, true, neg_inf());
-                ev[i] = load4(e, v0, p.V, ve, 1.0f);
-                qv[i] = q ? load4(q, v0, p.V, vq, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                lv[slot][i] = load4(l, v0, p.V, true, neg_inf());
+                ev[slot][i] = load4(e, v0, p.V, ve, 1.0f);
+                qv[slot][i] = q ? load4(q, v0, p.V, vq, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
+        };
+        const auto reduce = [&](int slot, int piece) {
+            const int e0 = (span * pieces + piece) * kPickPiece - off;
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
                 const int v0 = e0 + (i * kThreads + tid) * 4;
-                const float lj[4] = {lv[i].x, lv[i].y, lv[i].z, lv[i].w};
-                const float ej[4] = {ev[i].x, ev[i].y, ev[i].z, ev[i].w};
-                const float qj[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+                const float4 lf = lv[slot][i], ef = ev[slot][i], qf = qv[slot][i];
+                const float lj[4] = {lf.x, lf.y, lf.z, lf.w};
+                const float ej[4] = {ef.x, ef.y, ef.z, ef.w};
+                const float qj[4] = {qf.x, qf.y, qf.z, qf.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float pv = ex2((lj[j] - m) * c) * inv;
@@ -311,6 +315,16 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(pq2h::VerifyParam
                         k1 = t > k1 ? t : k1;
                     }
                 }
+            }
+        };
+        if (m > neg_inf()) {
+            fetch(0, 0);
+            for (int piece = 0; piece < pieces; piece += 2) {
+                if (piece + 1 < pieces) fetch(1, piece + 1);
+                reduce(0, piece);
+                if (piece + 1 == pieces) break;
+                if (piece + 2 < pieces) fetch(0, piece + 2);
+                reduce(1, piece + 1);
             }
         }
 #pragma unroll
@@ -396,8 +410,8 @@ cudaError_t launch_verify(VerifyParams p, void* workspace, cudaStream_t st) {
     }
     // a CTA's start (the row's statistics, the decision) costs several trips to
     // L2: one residency in all (three CTAs per SM), each over a span of pieces.
-    // 64 sequences of 248320: 75.4 us, with twice as many 78.9; 16 sequences of
-    // 128000: 18.8 and 19.9; 16 sequences of 248320: 37.4 and 36.2
+    // 64 sequences of 248320: 76.2 us, with a third more 87.3; 16 sequences of
+    // 128000: 17.5 and 20.1
     const int all = static_cast<int>((p.V + 3 + pq2::kPickPiece - 1) / pq2::kPickPiece);
     const int64_t most = std::max<int64_t>(1, kPickCtas / p.B);
     const int rounds = static_cast<int>((all + most - 1) / most);
