@@ -747,12 +747,14 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
         const int total = off[b];
         off[b] = at_tok;
         tfirst[b] = at_tile;
+        // tokens without an adapter come last: the tiles before theirs.  By this
+        // bin's own thread; the last thread's count of all tiles needs no other's
+        if (b == p.L) pl.num_tiles[1] = at_tile;
         at_tok += total;
         at_tile += (total + pl.tile - 1) / pl.tile;
     }
     if (threadIdx.x == nthreads - 1) {
         pl.num_tiles[0] = at_tile;
-        pl.num_tiles[1] = tfirst[p.L];   // tokens without an adapter come last
         *pl.taken = 0u;
         off[bins] = p.M;
     }

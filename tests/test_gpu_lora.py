@@ -168,6 +168,22 @@ def test_in_place_equals_out_of_place(M, N):
     assert torch.equal(y, p["out"])
 
 
+@pytest.mark.parametrize("L", [1, 31, 33, 200, 1023, 1100, 3000])
+def test_in_place_with_any_number_of_adapters(L):
+    # in place, expand's items end where the tokens without an adapter begin:
+    # a count that the plan takes from that bin's own thread, in another warp
+    # than the last one's for some of these L
+    from gemm_pq2_ternary_gb300 import binding as pq2
+    for M in (400, 2000):
+        ids = [-1 if m % 7 == 3 else m * 5 % L for m in range(M)]
+        p = _problem(M, 64, 260, 8, L, "f16", "f32", seed=M + L, ids=ids)
+        _call(pq2, p)
+        y = p["y"].clone()
+        _call(pq2, p, out=y, y=y)
+        _check(pq2, p, y)
+        assert torch.equal(y, p["out"])
+
+
 @pytest.mark.parametrize("N", [77, 160])
 @pytest.mark.parametrize("M", [1, 31, 32, 33, 128, 129, 300])
 def test_a_batch_without_adapters_is_a_copy(M, N):
