@@ -566,7 +566,8 @@ cudaError_t route(const NormParams& p, cudaStream_t st, const DeviceInfo& dev) {
     // and 5.2, of 255 values one by one 6.7 and 6.7; 64 of 255 3.3 and 3.5
     if (vec && H <= 512) return go<8, 2, kAfter, true>(p, 256, 8, sms * 4, st);
     if (vec && H <= 8192) {
-        const int threads = (H / 16 + 31) / 32 * 32;
+        // two vectors of 8 a thread: H may end half way through the last one's
+        const int threads = ((H + 15) / 16 + 31) / 32 * 32;
         return go<8, 2, kAfter, false>(p, threads, 1, sms * std::max(1, 1280 / threads), st);
     }
     if (H <= 256) return go<1, 8, kAfter, true>(p, 256, 8, sms * 4, st);

@@ -234,3 +234,16 @@ def test_binding_refuses():
         pq2.pq2_norm_residual(r, r, x)
     with pytest.raises(pq2.PQ2Error):
         pq2.pq2_rmsnorm(r, None, x, flags=1 << 20)
+
+
+# widths a few columns past what whole warps of 16 values a thread hold
+@pytest.mark.parametrize("H", [520, 1032, 2056, 5128, 7688])
+@pytest.mark.parametrize("M", [1, 6, 70])
+def test_widths_just_past_whole_warps(M, H):
+    test_norm_residual((M, H, "f32", "bf16", "f32", "bf16", "f16", "sigmoid", True, True, 0, 0), False)
+    test_norm_residual((M, H, "f32", "f32", "f32", None, "f16", None, False, True, 8, 0), False)
+    test_rmsnorm(M, H, "f32", "f16", "f32", 0, 0)
+
+
+def test_a_width_just_past_whole_warps_that_is_too_wide_for_the_ring():
+    test_norm_residual((700, 7688, "f32", "f32", "f32", "f32", "f16", "silu", True, True, 0, 0), False)
