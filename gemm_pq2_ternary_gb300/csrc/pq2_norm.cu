@@ -397,12 +397,16 @@ __global__ void __launch_bounds__((kRingMaxWarps + 1) * 32, 1)
     }
     if (!p.weights_static) pdl_wait();
     // eight weights a thread, every load before the first conversion: one
-    // trip to L2 (value by value this took 9 us)
+    // trip to L2 (value by value this took 9 us).  A gate vector is no weight:
+    // the kernel before may be writing it, whatever the flag says
     for (int e = tid * 8; e < p.H; e += consumers * 8) {
         RawVec<8> rp = raw_zero<8>(), rg = rp, rn = rp;
         if (kAfter && p.w_post) rp = raw_load<8>(p.w_post, p.w_type, e);
-        if (gate_vec) rg = raw_load<8>(p.gate, p.gate_type, e);
         if (p.w_next) rn = raw_load<8>(p.w_next, p.w_type, e);
+        if (gate_vec) {
+            pdl_wait();   // at once where it has been waited for
+            rg = raw_load<8>(p.gate, p.gate_type, e);
+        }
         float v[8], g[8], n[8];
         raw_to_f32<8>(rp, p.w_type, v);
         raw_to_f32<8>(rg, p.gate_type, g);

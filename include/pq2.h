@@ -292,7 +292,7 @@ pq2_status pq2_gemm_bf16_splitk(const uint16_t* x, const uint16_t* w, uint16_t* 
 #define PQ2_BF16 2
 
 /* Flags of pq2_rmsnorm and pq2_norm_residual (PQ2_WEIGHTS_STATIC, the norm
- * weights, may be added). */
+ * weights w, w_post and w_next and never the gate, may be added). */
 #define PQ2_NORM_UNIT_OFFSET 2u /* weights are stored as w - 1                  */
 #define PQ2_NORM_NO_POST 4u     /* the block's output is not normed             */
 #define PQ2_GATE_SIGMOID 8u     /* the gate enters as sigmoid(gate)             */

@@ -247,3 +247,33 @@ def test_widths_just_past_whole_warps(M, H):
 
 def test_a_width_just_past_whole_warps_that_is_too_wide_for_the_ring():
     test_norm_residual((700, 7688, "f32", "f32", "f32", "f32", "f16", "silu", True, True, 0, 0), False)
+
+
+@pytest.mark.parametrize("M,H", [(5, 1024), (700, 1024), (700, 5120)])
+def test_static_weights_do_not_cover_the_gate(M, H):
+    # a gate vector that a projection writes directly before, a new one each
+    # call: the flag lets the norm weights be read early, the gate not
+    from gemm_pq2_ternary_gb300 import binding as pq2
+    gen = torch.Generator(device=DEV).manual_seed(H)
+    y = torch.randn((M, H), generator=gen, device=DEV)
+    r = torch.randn((M, H), generator=gen, device=DEV)
+    w = 1 + 0.2 * torch.randn(H, generator=gen, device=DEV)
+    wg = (torch.randn((H, 4096), generator=gen, device=DEV) / 64).bfloat16()
+    xg = torch.randn((20, 1, 4096), generator=gen, device=DEV).bfloat16()
+    gate = torch.full((1, H), 50.0, dtype=torch.bfloat16, device=DEV)
+    outs = [torch.empty_like(r) for _ in range(20)]
+    big = torch.zeros(1 << 26, device=DEV)
+    torch.cuda.synchronize()
+    for x, out in zip(xg, outs):
+        big.add_(1)              # both calls are queued before the first starts
+        pq2.pq2_gemm_bf16_splitk(x, wg, gate)
+        pq2.pq2_norm_residual(y, r, out, w_post=w, gate=gate[0], flags=pq2.PQ2_WEIGHTS_STATIC)
+    torch.cuda.synchronize()
+    for x, out in zip(xg, outs):
+        pq2.pq2_gemm_bf16_splitk(x, wg, gate)
+        torch.cuda.synchronize()
+        want = torch.empty_like(r)
+        pq2.pq2_norm_residual(y, r, want, w_post=w, gate=gate[0])
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert pq2.pq2_last_device_error() == pq2.PQ2_OK
