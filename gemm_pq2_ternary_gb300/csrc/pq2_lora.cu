@@ -667,8 +667,12 @@ struct Plan {
 // contiguous range of tokens in its own histogram, so the order is fixed.
 // Bound by its chain of barriers and shared-memory trips: 3 us for 333 tokens,
 // 6 for 4096.
-__global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Plan pl, int warps) {
-    extern __shared__ int hist[];  // [warps][bins], then offsets [bins + 1], tiles and ranks [bins]
+// ranks_here: there is room for the bins' ranks too (else they are asked for
+// again, a trip to L2 a bin).
+__global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Plan pl, int warps,
+                                                         int ranks_here) {
+    // [warps][bins], then offsets [bins + 1], tiles [bins] and ranks [bins]
+    extern __shared__ int hist[];
     __shared__ int ws[2][32];
     const int bins = p.L + 1;
     int* off = hist + warps * bins;
@@ -729,7 +733,7 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
     // a scan over the bins, each thread owning a contiguous span
     int n_tok = 0, n_tile = 0;
     for (int b = b0; b < b1; ++b) {
-        rank[b] = b == b0 ? first_rank : b < p.L ? rank_of(p, b) : 0;
+        if (ranks_here) rank[b] = b == b0 ? first_rank : b < p.L ? rank_of(p, b) : 0;
         n_tok += off[b];
         n_tile += (off[b] + pl.tile - 1) / pl.tile;
     }
@@ -762,9 +766,11 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(pq2h::LoraParams p, Pla
     // tiles: a warp per bin again
     for (int b = warp; b < bins; b += nwarps) {
         const int first = off[b], total = off[b + 1] - first;
+        if (total == 0) continue;
+        const int r = ranks_here ? rank[b] : b < p.L ? rank_of(p, b) : 0;
         for (int k = lane * pl.tile; k < total; k += 32 * pl.tile)
             pl.tiles[tfirst[b] + k / pl.tile] =
-                make_int4(b < p.L ? b : -1, first + k, min(pl.tile, total - k), rank[b]);
+                make_int4(b < p.L ? b : -1, first + k, min(pl.tile, total - k), r);
     }
     for (int base = m0; base < m1; base += 32 * kBatch) {
         if (per > 32 * kBatch) load_keys(base, false);   // else still there
@@ -2457,15 +2463,21 @@ cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cu
     pl.max_tiles = lay.max_tiles;
     pl.tile = lay.tile;
     pl.rp = lay.rp;
-    // as many warps as have tokens and fit their histograms in 200 KB
+    // as many warps as have tokens and fit their histograms in 200 KB; one
+    // warp's and the ranks fit up to some 14500 adapters, without the ranks the
+    // most there can be do
     const int bins = p.L + 1;
     int warps = 32;
     while (warps > 1 && (warps / 2 * 32 >= p.M || static_cast<size_t>(warps + 3) * bins * 4 > 200 * 1024))
         warps /= 2;
-    const size_t plan_smem = (static_cast<size_t>(warps + 3) * bins + 1) * 4;
+    const auto plan_bytes = [&](int arrays) { return (static_cast<size_t>(arrays) * bins + 1) * 4; };
+    static_assert((3 * (PQ2_LORA_MAX_L + 1) + 1) * 4 <= 200 * 1024, "one warp's plan fits");
+    const int ranks_here = plan_bytes(warps + 3) + 512 <= static_cast<size_t>(dev.max_smem_optin);
+    const size_t plan_smem = plan_bytes(warps + 2 + ranks_here);
     cudaError_t e = ensure_smem(g_plan_smem, pq2::lora_plan_kernel, plan_smem);
     if (e != cudaSuccess) return e;
-    e = launch(pq2::lora_plan_kernel, dim3(1), dim3(warps * 32), plan_smem, st, true, p, pl, warps);
+    e = launch(pq2::lora_plan_kernel, dim3(1), dim3(warps * 32), plan_smem, st, true, p, pl, warps,
+               ranks_here);
     if (e != cudaSuccess) return e;
     e = p.R <= 16    ? run_shrink<BF, 0, 1>(p, pl, lay, st, dev)
         : p.R <= 32  ? run_shrink<BF, 0, 2>(p, pl, lay, st, dev)

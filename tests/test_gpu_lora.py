@@ -340,3 +340,19 @@ def test_binding_refuses():
     bad(6, None, "workspace")
     with pytest.raises(pq2.PQ2Error, match="shape"):
         pq2.alloc_lora_workspace(4, 32, 64, 2, 12)
+
+
+@pytest.mark.parametrize("L", [12000, 14512, 16384])
+@pytest.mark.parametrize("M", [200, 3000])
+def test_as_many_adapters_as_are_allowed(M, L):
+    from gemm_pq2_ternary_gb300 import binding as pq2
+    assert L <= pq2.PQ2_LORA_MAX_L
+    ids = [-1 if m % 11 == 5 else (m * 977 + L - 1) % L for m in range(M)]
+    p = _problem(M, 64, 36, 8, L, "f16", "f32", seed=L, ids=ids, ranks=False)
+    p["ranks"] = (torch.arange(L, device=DEV) * 5 % 9).to(torch.int32)
+    _call(pq2, p)
+    _check(pq2, p, p["out"])
+    y = p["y"].clone()
+    _call(pq2, p, out=y, y=y)
+    torch.cuda.synchronize()
+    assert torch.equal(y, p["out"])
