@@ -27,6 +27,7 @@
 // TB/s of the bytes that the call cannot do without (the first kernel alone 5.6
 // TB/s).
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 
 #include "pq2_common.cuh"
@@ -67,9 +68,12 @@ __device__ __forceinline__ int lead(const float* p) {
     return static_cast<int>((reinterpret_cast<uintptr_t>(p) >> 2) & 3u);
 }
 
-// 1 / temperature in units of log2(e); 0 selects the greedy rule.
+// 1 / temperature in units of log2(e); 0 selects the greedy rule.  A
+// temperature is never taken for greedy because it is large (infinite: every
+// allowed value alike), and 0 times a tiny one's scale stays 0: the scale is
+// kept between the smallest and the largest finite number.
 __device__ __forceinline__ float scale_of(float temperature) {
-    return temperature > 0.0f ? kLog2e / temperature : 0.0f;
+    return temperature > 0.0f ? fminf(fmaxf(kLog2e / temperature, FLT_TRUE_MIN), FLT_MAX) : 0.0f;
 }
 
 // The later of two (maximum, lowest index) pairs.

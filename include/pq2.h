@@ -413,6 +413,7 @@ pq2_status pq2_lora_add_packed(const pq2_lora_add_args* args, void* stream);
  * With e drawn from Exp(1) and u from U[0, 1), kept drafts and token follow
  * the target's distribution.  temperature[b] <= 0: greedy -- a draft is kept
  * while it is the row's argmax, and token is the argmax of the row after.
+ * temperature[b] may be infinite (every value that is not masked alike).
  * Ties go to the lowest index.  Values of -inf are masked (never drawn); a
  * row with nothing else keeps no draft and gives token -1.  A draft outside
  * [0, V) ends the sequence's drafts (padding): its row is the row after.

@@ -236,3 +236,24 @@ def test_binding_refuses():
         call(e=d["e"][:1])
     with pytest.raises(pq2.PQ2Error, match="workspace"):
         call(workspace=ws[:16])
+
+
+@pytest.mark.parametrize("q", [True, False])
+def test_temperatures_at_the_ends_of_their_range(q):
+    # infinite: every allowed value alike; tiny, subnormal ones included: the
+    # maximum alone
+    big, tiny = np.float32(3e38), np.float32(1e-45)
+    temps = [np.inf, 1e-40, tiny, big, np.inf, 1e-30]
+    for seed in range(5):
+        _check(_problem([4] * 6, 3001, seed=40 + seed, temps=temps, q=q))
+
+
+def test_infinite_temperature_draws_no_masked_value():
+    from gemm_pq2_ternary_gb300 import binding as pq2
+    p = _problem([3, 2, 4], 2500, seed=50, temps=[np.inf] * 3)
+    p["logits"][:, np.random.default_rng(51).random(2500) < 0.5] = -np.inf
+    flat = np.where(np.isfinite(p["logits"]), 0.0, -np.inf)   # the same distribution at 1
+    acc, tok, margin = step.verify(flat, p["row_start"], p["drafts"], p["q"], p["u"], p["e"], [1.0] * 3)
+    assert margin > MARGIN, "choose another seed"
+    a, t = _run(pq2, p)
+    assert np.array_equal(a, acc) and np.array_equal(t, tok)
