@@ -406,7 +406,9 @@ cudaError_t launch_verify(VerifyParams p, void* workspace, cudaStream_t st) {
     p.keys = reinterpret_cast<unsigned long long*>(w);
     w += pad(static_cast<size_t>(p.B) * 16);
     p.done = reinterpret_cast<unsigned*>(w);
-    // without rows every sequence is empty: nothing to prepare for pick
+    // without rows every sequence is empty: nothing to prepare for pick, which
+    // then starts after all before it (it reads ahead of its dependency wait
+    // because the statistics kernel has waited by then)
     if (pieces > 0) {
         const cudaError_t e = launch(pq2::verify_stats_kernel, dim3(static_cast<unsigned>(pieces)),
                                      dim3(pq2::kThreads), 0, st, true, p);
@@ -421,7 +423,7 @@ cudaError_t launch_verify(VerifyParams p, void* workspace, cudaStream_t st) {
     const int rounds = static_cast<int>((all + most - 1) / most);
     const int spans = (all + rounds - 1) / rounds;
     return launch(pq2::verify_pick_kernel, dim3(static_cast<unsigned>(p.B * spans)),
-                  dim3(pq2::kThreads), 0, st, true, p, spans, rounds);
+                  dim3(pq2::kThreads), 0, st, pieces > 0, p, spans, rounds);
 }
 
 }  // namespace pq2h

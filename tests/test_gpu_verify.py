@@ -257,3 +257,28 @@ def test_infinite_temperature_draws_no_masked_value():
     assert margin > MARGIN, "choose another seed"
     a, t = _run(pq2, p)
     assert np.array_equal(a, acc) and np.array_equal(t, tok)
+
+
+def test_no_rows_behind_the_kernel_that_writes_the_ranges():
+    # the ranges (all zero) come from a call directly before; what the buffer
+    # held until then breaks every rule
+    from gemm_pq2_ternary_gb300 import binding as pq2
+    n = 40000
+    zeros = torch.zeros((1, n), device=DEV)
+    ranges = torch.empty((1, n), device=DEV)
+    start = ranges.view(torch.int32)[0]
+    a = torch.empty(n - 1, dtype=torch.int32, device=DEV)
+    i = torch.zeros(0, dtype=torch.int32, device=DEV)
+    f = torch.zeros(0, device=DEV)
+    e, temp, z = torch.ones((n - 1, 1), device=DEV), torch.ones(n - 1, device=DEV), torch.zeros((0, 1), device=DEV)
+    ws = pq2.alloc_verify_workspace(n - 1, 0, 1)
+    big = torch.zeros(1 << 28, device=DEV)
+    for _ in range(5):
+        start.fill_(7)
+        a.fill_(5)
+        torch.cuda.synchronize()
+        big.add_(1)              # both calls are queued before the first starts
+        pq2.pq2_rmsnorm(zeros, None, ranges)
+        pq2.pq2_verify_drafts(z, start, i, None, f, e, temp, a, i, ws)
+        assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+        assert int(torch.count_nonzero(a)) == 0
