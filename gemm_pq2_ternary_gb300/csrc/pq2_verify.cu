@@ -95,6 +95,7 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2, flo
 __global__ void __launch_bounds__(kThreads) verify_stats_kernel(pq2h::VerifyParams p) {
     __shared__ float sm[kWarps], ss[kWarps];
     __shared__ int si[kWarps];
+    __shared__ int s_seq;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row = blockIdx.x / p.chunks;
     const int chunk = static_cast<int>(blockIdx.x - row * p.chunks);
@@ -114,13 +115,17 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(pq2h::VerifyPara
             p.done[b] = 0u;
         }
     }
-    // the row's sequence: the number of sequences that end at or before it
-    int seq = 0;
-    for (long long b0 = 0; b0 < p.B; b0 += kThreads) {
-        const long long b = b0 + tid;
-        seq += __syncthreads_count(b < p.B && p.row_start[b + 1] <= row);
+    // the row's sequence: the one whose range is sound and has the row (a
+    // broken range elsewhere says nothing about this row)
+    bool found = false;
+    for (long long b = tid; b < p.B; b += kThreads) {
+        const int r0 = p.row_start[b], r1 = p.row_start[b + 1];
+        if (r0 >= 0 && r0 <= row && row < r1 && r1 <= p.rows) {
+            s_seq = static_cast<int>(b);
+            found = true;
+        }
     }
-    const float c = seq < p.B ? scale_of(p.temperature[seq]) : 0.0f;
+    const float c = __syncthreads_or(found) ? scale_of(p.temperature[s_seq]) : 0.0f;
 
     float m = neg_inf();
     int at = INT_MAX;

@@ -420,7 +420,9 @@ pq2_status pq2_lora_add_packed(const pq2_lora_add_args* args, void* stream);
  *   logits      in   fp32 [rows, V], row stride ld_logits >= V (no NaN, no +inf)
  *   row_start   in   int32 [B + 1], 0 <= row_start[b] <= row_start[b+1] <= rows;
  *                    a sequence that breaks this keeps 0 and sets the device
- *                    error word.  A sequence without rows keeps 0.
+ *                    error word; the others are not affected (two that share
+ *                    rows, possible only around a broken one, are undefined).
+ *                    A sequence without rows keeps 0.
  *   drafts      in   int32 [rows] (a sequence's last one is not read as a draft)
  *   q           in   fp32 [rows, V], row stride ld_q >= V, or NULL
  *   u           in   fp32 [rows]

@@ -282,3 +282,20 @@ def test_no_rows_behind_the_kernel_that_writes_the_ranges():
         pq2.pq2_verify_drafts(z, start, i, None, f, e, temp, a, i, ws)
         assert pq2.pq2_last_device_error() == pq2.PQ2_OK
         assert int(torch.count_nonzero(a)) == 0
+
+
+def test_a_broken_range_leaves_the_sequences_after_it_alone():
+    from gemm_pq2_ternary_gb300 import binding as pq2
+    for seed in range(6):
+        p = _problem([4, 4], 300, seed=60 + seed)
+        p["temperature"] = np.array([3.0, 7.0, 0.5], dtype=np.float32)
+        p["e"] = np.random.default_rng(seed).exponential(size=(3, 300)).astype(np.float32)
+        p["u"] *= 0.5                        # some drafts are kept
+        p["row_start"] = np.array([0, 100, 4, 8], dtype=np.int32)
+        want_a, want_t, margin = step.verify(p["logits"], [4, 8], p["drafts"], p["q"], p["u"], p["e"][2:],
+                                             p["temperature"][2:])
+        assert margin > MARGIN, "choose another seed"
+        a, t = _run(pq2, p)
+        assert pq2.pq2_last_device_error() == pq2.PQ2_ERR_INVALID_ARG
+        assert list(a) == [0, 0, want_a[0]] and np.array_equal(t[4:], want_t[4:])
+        assert np.all(t[:4] == SENTINEL)
