@@ -522,6 +522,10 @@ static pq2_status norm(const pq2_norm_residual_args& a, int64_t M, int64_t H, vo
         !aligned_to(a.w_post, type_bytes(a.w_type)) || !aligned_to(a.w_next, type_bytes(a.w_type)) ||
         !aligned_to(a.x, type_bytes(a.x_type)))
         return PQ2_ERR_MISALIGNED;
+    // in place only row on row: rows are taken in any order, and read ahead
+    if (a.r_out == a.r && M > 1 && a.ld_r_out != a.ld_r) return PQ2_ERR_INVALID_ARG;
+    if (!a.y && a.x == a.r && (a.x_type != a.r_type || (M > 1 && a.ld_x != a.ld_r)))
+        return PQ2_ERR_INVALID_ARG;
     Ctx c;
     const pq2_status s = get_ctx(&c);
     if (s != PQ2_OK) return s;

@@ -309,7 +309,7 @@ pq2_status pq2_gemm_bf16_splitk(const uint16_t* x, const uint16_t* w, uint16_t* 
  * pq2_gemm_bf16_splitk takes.
  *   r in [M, H] (r_type, row stride ld_r >= H elements), w in [H] (w_type) or
  *   NULL (1), x out [M, H] (x_type, ld_x >= H).  x may be r where their types
- *   and strides are the same.
+ *   and strides are the same (PQ2_ERR_INVALID_ARG otherwise).
  * M >= 0 (M == 0 enqueues nothing), 1 <= H <= PQ2_NORM_MAX_H, eps >= 0.
  * Pointers need their element's alignment only (PQ2_ERR_MISALIGNED
  * otherwise); rows on 16-byte boundaries with H % 8 == 0 take the vector path.
@@ -328,7 +328,7 @@ pq2_status pq2_rmsnorm(const void* r, int r_type, int64_t ld_r, const void* w, i
  * optional parts; every pointer is a device pointer.
  *   y       in   [M, H] the block's output (fp32 from pq2_matmul)
  *   r       in   [M, H] residual stream
- *   r_out   out  [M, H] of r's type; may be r
+ *   r_out   out  [M, H] of r's type; may be r, with the same row stride
  *   w_post  in   [H] or NULL (1)
  *   gate    in   [M, H] with row stride ld_gate >= H, or one vector [H] for
  *                all rows (ld_gate == 0), or NULL

@@ -179,3 +179,21 @@ def test_packed_arguments_meet_the_same_checks(lib):  # noqa: F811
         assert verify(**kw) == b.PQ2_ERR_INVALID_ARG, kw
     for kw in (dict(q=FAKE + 2), dict(e=FAKE + 2), dict(workspace=ODD)):
         assert verify(**kw) == b.PQ2_ERR_MISALIGNED, kw
+
+
+def test_norms_in_place_need_one_row_stride(lib):  # noqa: F811
+    # rows are worked on in any order: with another stride (or type) a row
+    # would be written over one that is still to be read
+    from gemm_pq2_ternary_gb300 import binding as b
+    f = lib.pq2_norm_residual
+    wide = dict(x=None, ld_y=64)
+    assert f(_norm_args(b, ld_r_out=72, **wide), 2, 64, None) == b.PQ2_ERR_INVALID_ARG
+    assert f(_norm_args(b, ld_r=72, **wide), 3, 64, None) == b.PQ2_ERR_INVALID_ARG
+    g, P = lib.pq2_rmsnorm, _p(FAKE)
+
+    def before(rt, ld_r, xt, ld_x, M):
+        return g(P, rt, ld_r, P, b.PQ2_F32, P, xt, ld_x, M, 64, 1e-6, 0, None)
+    assert before(b.PQ2_BF16, 64, b.PQ2_BF16, 72, 2) == b.PQ2_ERR_INVALID_ARG
+    assert before(b.PQ2_F16, 72, b.PQ2_F16, 64, 2) == b.PQ2_ERR_INVALID_ARG
+    assert before(b.PQ2_F32, 64, b.PQ2_F16, 64, 2) == b.PQ2_ERR_INVALID_ARG
+    assert before(b.PQ2_F32, 64, b.PQ2_F16, 64, 1) == b.PQ2_ERR_INVALID_ARG
