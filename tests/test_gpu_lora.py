@@ -356,3 +356,41 @@ def test_as_many_adapters_as_are_allowed(M, L):
     _call(pq2, p, out=y, y=y)
     torch.cuda.synchronize()
     assert torch.equal(y, p["out"])
+
+
+# (M, K, N, R, L, y type, kernel whose stage is withheld: the other has none
+# of that number)
+STAGES = [
+    (200, 640, 64, 32, 3, "f32", "shrink, mma.sync"),
+    (200, 1280, 64, 64, 3, "f32", "shrink, tcgen05"),
+    (200, 1280, 64, 200, 3, "f32", "shrink, tcgen05, two accumulators"),
+    (200, 64, 10240, 64, 3, "f32", "expand, tcgen05"),
+    (200, 64, 10241, 64, 3, "f32", "expand, tcgen05, y by values"),
+    (200, 64, 5120, 16, 20, "f32", "expand, tcgen05, tiles of 16"),
+    (200, 64, 5121, 16, 20, "f32", "expand, tcgen05, tiles of 16, y by values"),
+    (200, 64, 10240, 64, 3, "bf16", "expand, mma.sync, bf16 y"),
+    (200, 64, 5120, 256, 3, "f32", "expand, mma.sync"),
+    (200, 64, 5121, 256, 3, "f32", "expand, mma.sync, y by values"),
+]
+
+
+@pytest.mark.parametrize("case", STAGES, ids=lambda c: c[-1])
+def test_every_ring_reports_a_stage_that_never_comes(case):
+    from gemm_pq2_ternary_gb300 import binding as pq2
+    M, K, N, R, L, y_type, _ = case
+    p = _problem(M, K, N, R, L, "f16", y_type, seed=R, ranks=False)
+    _call(pq2, p)
+    _check(pq2, p, p["out"])
+    want = p["out"].clone()
+    for stage in (1, 2):
+        try:
+            pq2.pq2_debug_set_wait_limit_ns(20_000_000)
+            pq2.pq2_debug_skip_stage(stage)
+            _call(pq2, p)
+            assert pq2.pq2_last_device_error() == pq2.PQ2_ERR_TIMEOUT
+        finally:
+            pq2.pq2_debug_skip_stage(-1)
+            pq2.pq2_debug_set_wait_limit_ns(2_000_000_000)
+        _call(pq2, p)
+        assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+        assert torch.equal(p["out"], want)
