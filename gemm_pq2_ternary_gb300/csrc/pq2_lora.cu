@@ -28,8 +28,8 @@
 // registers, with no shared-memory stage: each is used once per tile of
 // tokens.  The planned form runs on tcgen05 with accumulators in tensor memory
 // (shrink above 32 ranks; expand for fp32 y where two stages of its ring fit:
-// up to rank 128, for bf16 64), else on the same instructions from shared
-// memory.
+// up to rank 128, in tiles of 16 tokens any rank), else on the same
+// instructions from shared memory.
 //
 // Precision.  v stays fp32 and would lose 13 bits (16 for bf16) as an operand
 // of the expand product, so it enters as a sum of 16-bit terms: hi + lo for
@@ -1809,6 +1809,10 @@ struct TcShared {
     int abort_word;
 };
 
+// Two stages of rank 128 and bf16 terms take 230400 bytes beside it, of 232448
+// a CTA may have: a larger struct would send them to the other ring.
+static_assert(sizeof(TcShared) <= 2048, "two stages fit up to rank 128");
+
 // The k-th unit, for every warp but the scheduler's; false: no more, or a wait
 // ran out.  A warp is done with its place (u.slot) when it calls release_unit.
 __device__ __forceinline__ bool take_unit(TcShared& sh, int k, TcUnit& u, const DevCtl& ctl) {
@@ -2250,7 +2254,10 @@ Layout layout(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
         // there are more, and more items.  129 tokens over 64 adapters of rank 64,
         // 17408 outputs: 49.0 us against 60.7 with 64; 1000 over 64 of rank 16 38.9
         // and 44.1; 250 over 10 of rank 64 26.7 and 29.4; but 600 over 10 of rank
-        // 32 30.9 and 23.7, 1000 over 30 of rank 24 84.6 and 42.0
+        // 32 30.9 and 23.7, 1000 over 30 of rank 24 84.6 and 42.0.  The rule goes by
+        // the stack's adapters, which may be more than have tokens, and not by N or
+        // the rank: a rank that is no multiple of 16, whose items all pass the
+        // fixing warp, is better off with 64 well below 32 tokens an adapter
         y.tile = M <= 32 * L ? kSmallTile : kTile;
         const int64_t tiles = (M + y.tile - 1) / y.tile + std::min(L, M / 2);
         s = 1;

@@ -321,7 +321,7 @@ pq2_status pq2_rmsnorm(const void* r, int r_type, int64_t ld_r, const void* w, i
 /*
  * pq2_norm_residual -- the end of a block, and the norm before the next one,
  * in one pass:
- *   n    = y / sqrt(mean(y^2) + eps) * w_post      (n = y with NO_POST)
+ *   n    = y / sqrt(mean(y^2) + eps) * w_post      (n = y * w_post with NO_POST)
  *   r'   = r + alpha * act(gate) * n               (gate absent: 1)
  *   x    = r' / sqrt(mean(r'^2) + eps) * w_next    (from r' before rounding)
  * per row, in fp32; r' and x are rounded once.  A struct, for its many
