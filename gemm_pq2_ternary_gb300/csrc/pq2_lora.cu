@@ -2299,7 +2299,7 @@ cudaError_t run_few(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec
     auto kern = rb == 1 ? pq2::lora_expand_few<BF, YT, true> : pq2::lora_expand_few<BF, YT, false>;
     const size_t smem = static_cast<size_t>(pq2::terms<BF>()) * pq2::kFewTile * pq2::term_pitch(rb) * 2 +
                         static_cast<size_t>(pq2::kFewTile) * rb * 32 * 4;
-    e = ensure_smem(lim[rb == 1], kern, smem);
+    e = raise_smem(lim[rb == 1], kern, smem);
     if (e != cudaSuccess) return e;
     // 128 outputs a CTA while the GPU has SMs to spare; else 256, and as many
     // rounds of them as keep the CTAs to about one residency (two per SM): a
@@ -2352,7 +2352,7 @@ cudaError_t run_shrink(const LoraParams& p, const pq2::Plan& pl, const Layout& l
                         p.A, p.K, static_cast<uint64_t>(p.L) * p.R, static_cast<uint64_t>(p.K) * 2,
                         pq2::kStageK, 16, true))
         return cudaErrorUnknown;
-    cudaError_t e = ensure_smem(lim, kern, smem);
+    cudaError_t e = raise_smem(lim, kern, smem);
     if (e != cudaSuccess) return e;
     if (lay.splits > 8) {
         // clusters past the portable size are asked for once per kernel
@@ -2400,7 +2400,7 @@ cudaError_t run_ring(const LoraParams& p, const pq2::Plan& pl, int stages, int s
     stages -= stages % groups;
     static SmemLimit lim;
     const size_t smem = static_cast<size_t>(term_bytes) + static_cast<size_t>(stages) * stage_bytes;
-    const cudaError_t e = ensure_smem(lim, kern, smem);
+    const cudaError_t e = raise_smem(lim, kern, smem);
     if (e != cudaSuccess) return e;
     return launch(kern, dim3(dev.num_sms), dim3((pq2::kRingWarps + pq2::kRingLoaders) * 32), smem, st,
                   true, p, pl, groups, stages, stage_bytes, term_bytes);
@@ -2448,7 +2448,7 @@ cudaError_t run_tc(const LoraParams& p, const pq2::Plan& pl, cudaStream_t st, co
     auto kern = pq2::lora_expand_tc<BF, kTma, T>;
     static SmemLimit lim;
     const size_t smem = 1024 + 2 * static_cast<size_t>(term_bytes) + static_cast<size_t>(stages) * stage_bytes;
-    const cudaError_t e = ensure_smem(lim, kern, smem);
+    const cudaError_t e = raise_smem(lim, kern, smem);
     if (e != cudaSuccess) return e;
     return launch(kern, dim3(dev.num_sms), dim3(pq2::tc_threads<kTma, T>()), smem, st, true, p, pl, maps, stages,
                   stage_bytes, term_bytes);
@@ -2481,7 +2481,7 @@ cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cu
     static_assert((3 * (PQ2_LORA_MAX_L + 1) + 1) * 4 <= 200 * 1024, "one warp's plan fits");
     const int ranks_here = plan_bytes(warps + 3) + 512 <= static_cast<size_t>(dev.max_smem_optin);
     const size_t plan_smem = plan_bytes(warps + 2 + ranks_here);
-    cudaError_t e = ensure_smem(g_plan_smem, pq2::lora_plan_kernel, plan_smem);
+    cudaError_t e = raise_smem(g_plan_smem, pq2::lora_plan_kernel, plan_smem);
     if (e != cudaSuccess) return e;
     e = launch(pq2::lora_plan_kernel, dim3(1), dim3(warps * 32), plan_smem, st, true, p, pl, warps,
                ranks_here);
@@ -2513,7 +2513,7 @@ cudaError_t run(const LoraParams& p, const Layout& lay, uint8_t* ws, int vec, cu
         static SmemLimit lim;
         const size_t smem = static_cast<size_t>(pq2::terms<BF>()) * kTile *
                             pq2::term_pitch((p.R + 31) / 32) * 2;
-        e = ensure_smem(lim, pq2::lora_expand_tiles<BF, YT>, smem);
+        e = raise_smem(lim, pq2::lora_expand_tiles<BF, YT>, smem);
         if (e != cudaSuccess) return e;
         const int rounds = p.M <= 512 ? 1 : 4;
         const int cols = pq2::kExpandWarps * 32 * rounds;

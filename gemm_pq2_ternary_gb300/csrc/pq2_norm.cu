@@ -562,7 +562,7 @@ cudaError_t route(const NormParams& p, cudaStream_t st, const DeviceInfo& dev) {
             auto kern = full ? pq2::norm_ring_kernel<kAfter, true> : pq2::norm_ring_kernel<kAfter, false>;
             static SmemLimit lim[2];
             const size_t smem = static_cast<size_t>(stages) * stage + 8 * static_cast<size_t>(H);
-            const cudaError_t e = ensure_smem(lim[full], kern, smem);
+            const cudaError_t e = raise_smem(lim[full], kern, smem);
             if (e != cudaSuccess) return e;
             return launch(kern, dim3(static_cast<unsigned>(sms)), dim3(threads * groups + 32), smem, st,
                           true, p, threads, groups, stages, stage);
@@ -583,7 +583,7 @@ cudaError_t route(const NormParams& p, cudaStream_t st, const DeviceInfo& dev) {
     }
     static SmemLimit lim;
     const size_t smem = static_cast<size_t>(H) * 4;
-    cudaError_t e = ensure_smem(lim, pq2::norm_wide_kernel<kAfter>, smem);
+    cudaError_t e = raise_smem(lim, pq2::norm_wide_kernel<kAfter>, smem);
     if (e != cudaSuccess) return e;
     return launch(pq2::norm_wide_kernel<kAfter>,
                   dim3(static_cast<unsigned>(std::min<int64_t>(p.M, sms * 2))), dim3(1024), smem, st,

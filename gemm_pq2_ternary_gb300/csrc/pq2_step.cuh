@@ -2,6 +2,8 @@
 // share beyond pq2_common.cuh.
 #pragma once
 
+#include <mutex>
+
 #include "pq2_common.cuh"
 
 namespace pq2 {
@@ -20,3 +22,21 @@ __device__ __forceinline__ bool mbar_ready_warp(uint64_t* bar, uint32_t parity, 
 }
 
 }  // namespace pq2
+
+namespace pq2h {
+
+// ensure_smem for kernels whose size changes from call to call, from any number
+// of host threads: of two that raise one kernel's limit at once, the smaller
+// could set it last, below what is noted down (later launches would then fail).
+template <typename Kern>
+cudaError_t raise_smem(SmemLimit& lim, Kern kern, size_t smem) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kSmemLimitDevices &&
+        lim.bytes[dev].load(std::memory_order_acquire) >= static_cast<int>(smem))
+        return cudaSuccess;
+    static std::mutex one_at_a_time;
+    std::lock_guard<std::mutex> hold(one_at_a_time);
+    return ensure_smem(lim, kern, smem);   // asks again
+}
+
+}  // namespace pq2h
