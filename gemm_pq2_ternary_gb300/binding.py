@@ -45,6 +45,17 @@ PQ2_NORM_NO_POST = 4
 PQ2_GATE_SIGMOID = 8
 PQ2_GATE_SILU = 16
 
+# frequencies of rotary positions, flags of pq2_rope and pq2_cache4_append
+PQ2_ROPE_PLAIN = 0
+PQ2_ROPE_LINEAR = 1
+PQ2_ROPE_BASE = 2
+PQ2_ROPE_RAMP = 3
+PQ2_ROPE_BANDS = 4
+PQ2_ROPE_NEIGHBOURS = 1
+PQ2_ROPE_INVERSE = 2
+PQ2_ROPE_MAX_DIM = 512
+PQ2_CACHE4_MAX_HEADS = 1024
+
 PQ2_NORM_MAX_H = 49152
 PQ2_LORA_MAX_R = 256
 PQ2_LORA_MAX_L = 16384
@@ -89,6 +100,17 @@ assert _norm_residual_args.size == ctypes.sizeof(NormResidualArgs)
 _lora_add_args = struct.Struct("=9Q8qQ2i")
 _verify_drafts_args = struct.Struct("=10Q6qQ")
 
+# pq2_rope_scaling; pq2_cache4 and the arguments of the calls on it and on its
+# pages, likewise
+_rope_scaling = struct.Struct("=if4d")
+_rope_args = struct.Struct("=6Q10q6iIi")
+_CACHE4 = "4Q5q4i"
+_cache4_append_args = struct.Struct("=" + _CACHE4 + "6Q10q4iIi")
+_cache4_read_args = struct.Struct("=" + _CACHE4 + "2Q5q2i")
+_cache4_attend_args = struct.Struct("=" + _CACHE4 + "3Q7qQf3i")
+_pages_update_args = struct.Struct("=11Q6qQ")
+_pages_compact_args = struct.Struct("=8Q6qQ")
+
 
 SIGNATURES = {
     "pq2_status_string": ([_I], ctypes.c_char_p),
@@ -114,6 +136,17 @@ SIGNATURES = {
     "pq2_verify_drafts": ([_P, _I64, _P, _P, _P, _I64, _P, _P, _I64, _P, _P, _P] + [_I64] * 3 +
                           [_P, _SZ, _P], _I),
     "pq2_verify_drafts_packed": ([_P, _P], _I),
+    "pq2_rope_table": ([_P, _I64, _I64, _I64, ctypes.c_double, _P, _P], _I),
+    "pq2_rope": ([_P, _P], _I),
+    "pq2_cache4_page_bytes": ([_I64] * 3, _SZ),
+    "pq2_cache4_append": ([_P, _P], _I),
+    "pq2_cache4_read": ([_P, _P], _I),
+    "pq2_cache4_attend_workspace_bytes": ([_I64] * 4, _SZ),
+    "pq2_cache4_attend": ([_P, _P], _I),
+    "pq2_pages_workspace_bytes": ([_I64] * 2, _SZ),
+    "pq2_pages_update": ([_P, _P], _I),
+    "pq2_pages_compact": ([_P, _P], _I),
+    "pq2_pages_copy": ([_P, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P], _I),
     "pq2_workspace_bytes": ([_I, _I64, _I64, _I64], _SZ),
     "pq2_group_dots": ([_I, _P, _P, _P, _I64, _I64, _I64, _P, _P, _SZ, _P], _I),
     "pq2_last_device_error": ([_P], _I),
@@ -468,6 +501,265 @@ def pq2_verify_drafts(logits, row_start, drafts, q, u, e, temperature, accepted,
     status = _lib.pq2_verify_drafts_packed(args, _stream(stream))
     if status:
         raise PQ2Error(status, "pq2_verify_drafts")
+
+
+def _heads(t, shape, name):
+    """(pointer, element type, token stride, head stride) of a CUDA tensor
+    [tokens, heads, values] whose heads are contiguous."""
+    ty = _TYPE.get(t.dtype)
+    if ty is None or not t.is_cuda or t.shape != shape:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: expected a CUDA tensor")
+        if ty is None:
+            raise ValueError(f"{name}: expected float32, float16 or bfloat16, got {t.dtype}")
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    ld, hs, unit = t.stride()
+    M, H, D = shape
+    if unit != 1 and D > 1:
+        raise ValueError(f"{name}: a head's values must be contiguous")
+    # a single head's, or token's, stride says nothing
+    if H <= 1:
+        hs = D
+    if M <= 1:
+        ld = H * hs
+    return t.data_ptr(), ty, ld, hs
+
+
+def pq2_rope_table(table, base, first=0, kind=PQ2_ROPE_PLAIN, factor=1.0, old_len=0.0, low=0.0, high=0.0,
+                   magnitude=0.0, stream=None):
+    """table fp32 [count, rot / 2, 2]: cosines and sines of positions first ..
+    first + count - 1; kind and the rest: how the frequencies are scaled."""
+    _dtype(table, _F32, "table")
+    if table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError(f"table: expected shape [count, rot / 2, 2], got {tuple(table.shape)}")
+    _check(_lib.pq2_rope_table(_ptr(table), first, table.shape[0], 2 * table.shape[1], base,
+                               _rope_scaling.pack(kind, magnitude, factor, old_len, low, high), _stream(stream)),
+           "pq2_rope_table")
+
+
+def _rot(table):
+    """(pointer, rows, rot) of a table fp32 [rows, rot / 2, 2]."""
+    if table is None:
+        return 0, 0, 0
+    rows, half, two = table.shape
+    if table.dtype is not _F32 or two != 2:
+        raise ValueError(f"table: expected {_F32} [rows, rot / 2, 2], got {table.dtype} {tuple(table.shape)}")
+    return _ptr(table), rows, 2 * half
+
+
+def pq2_rope(x, table, positions, out, x2=None, out2=None, flags=0, stream=None):
+    """out = x with the first rot values of every head turned by their token's
+    angles; x, out [M, heads, dim], x2, out2 [M, heads2, dim] likewise or None;
+    table fp32 [rows, rot / 2, 2]; positions int32 [M], its rows.  out may be x."""
+    shape = x.shape
+    M, H, D = shape
+    xp, xt, xl, xh = _heads(x, shape, "x")
+    op, ot, ol, oh = (xp, xt, xl, xh) if out is x else _heads(out, shape, "out")
+    x2p = o2p = H2 = x2l = x2h = o2l = o2h = 0
+    if x2 is not None:
+        shape2 = x2.shape
+        H2 = shape2[1]
+        if shape2 != (M, H2, D) or out2 is None:
+            raise ValueError("x2: expected x's tokens and head size, and out2 with it")
+        x2p, t2, x2l, x2h = _heads(x2, shape2, "x2")
+        o2p, t3, o2l, o2h = (x2p, t2, x2l, x2h) if out2 is x2 else _heads(out2, shape2, "out2")
+        if t2 != xt or t3 != ot:
+            raise ValueError("x2 and out2: expected the types of x and out")
+    tp, rows, rot = _rot(table)
+    status = _lib.pq2_rope(_rope_args.pack(
+        xp, x2p, op, o2p, tp, _vec(positions, (M,), _I32, "positions"), xl, xh, x2l, x2h, ol, oh, o2l, o2h, M, rows,
+        H, H2, D, rot, xt, ot, flags, 0), _stream(stream))
+    if status:
+        raise PQ2Error(status, "pq2_rope")
+
+
+def pq2_cache4_page_bytes(heads, dim, page_tokens) -> int:
+    return int(_lib.pq2_cache4_page_bytes(heads, dim, page_tokens))
+
+
+def alloc_cache4(pages, heads, dim, page_tokens, device="cuda"):
+    """A pool of pages: uint8 [pages, heads, page_tokens * (dim + 8)], zeros."""
+    if pq2_cache4_page_bytes(heads, dim, page_tokens) == 0:
+        raise PQ2Error(PQ2_ERR_UNSUPPORTED_SHAPE, "pq2_cache4_page_bytes")
+    return torch.zeros((pages, heads, page_tokens * (dim + 8)), dtype=torch.uint8, device=device)
+
+
+def _cache4(pool, pages, row_start, lens, dim):
+    """The fields of pq2_cache4: pool uint8 [pages, heads, T * (dim + 8)] (any
+    page stride), pages int32 [B, W] (any row stride)."""
+    P, heads, nbytes = pool.shape
+    B, W = pages.shape
+    T, rest = divmod(nbytes, dim + 8)
+    if rest or pool.dtype is not torch.uint8 or not pool.is_cuda:
+        raise ValueError(f"pool: expected a uint8 CUDA tensor [pages, heads, T * {dim + 8}], got {pool.dtype} "
+                         f"{tuple(pool.shape)}")
+    ps, hs, unit = pool.stride()
+    if unit != 1 or (heads > 1 and hs != nbytes):
+        raise ValueError("pool: a page must be contiguous")
+    if P <= 1:
+        ps = heads * nbytes
+    if pages.dtype is not _I32 or not pages.is_cuda or (W > 1 and pages.stride(1) != 1):
+        raise ValueError("pages: expected an int32 CUDA tensor with contiguous rows")
+    return (pool.data_ptr(), pages.data_ptr(), _vec(row_start, (B + 1,), _I32, "row_start"),
+            _vec(lens, (B,), _I32, "lens"), ps, P, pages.stride(0) if B > 1 else W, B, W, heads, dim, T, 0)
+
+
+def pq2_cache4_append(k, v, pool, pages, row_start, lens, q=None, q_out=None, table=None, positions=None,
+                      flags=0, stream=None):
+    """New tokens into the cache: k (turned) and v [M, heads, dim], quantised;
+    with q [M, q_heads, dim], q_out = q turned.  pool uint8 [pages, heads,
+    T * (dim + 8)], pages int32 [B, W], row_start int32 [B + 1], lens int32 [B]
+    (with the new tokens); table fp32 [rows, rot / 2, 2] or None; positions
+    int32 [M] or None (the tokens' places)."""
+    shape = k.shape
+    M, H, D = shape
+    kp, kt, kl, kh = _heads(k, shape, "k")
+    vp, vt, vl, vh = _heads(v, shape, "v")
+    if pool.shape[1] != H:
+        raise ValueError(f"pool: expected {H} heads, got {pool.shape[1]}")
+    qp = op = Hq = ql = qh = ol = oh = ot = 0
+    qt = kt
+    if q is not None:
+        qshape = q.shape
+        Hq = qshape[1]
+        if qshape != (M, Hq, D) or q_out is None:
+            raise ValueError("q: expected k's tokens and head size, and q_out with it")
+        qp, qt, ql, qh = _heads(q, qshape, "q")
+        op, ot, ol, oh = (qp, qt, ql, qh) if q_out is q else _heads(q_out, qshape, "q_out")
+    if vt != kt or qt != kt:
+        raise ValueError("k, v and q: expected one type")
+    tp, rows, rot = _rot(table)
+    status = _lib.pq2_cache4_append(_cache4_append_args.pack(
+        *_cache4(pool, pages, row_start, lens, D), kp, vp, qp, op, tp,
+        0 if positions is None else _vec(positions, (M,), _I32, "positions"), kl, kh, vl, vh, ql, qh, ol, oh, M, rows,
+        Hq, rot, kt, ot, flags, 0), _stream(stream))
+    if status:
+        raise PQ2Error(status, "pq2_cache4_append")
+
+
+def pq2_cache4_read(pool, pages, row_start, lens, k_out, v_out, stream=None):
+    """The cache's keys and values of the call's token rows: k_out, v_out
+    [M, heads, dim], either may be None."""
+    a = k_out if k_out is not None else v_out
+    shape = a.shape
+    if pool.shape[1] != shape[1]:
+        raise ValueError(f"pool: expected {shape[1]} heads, got {pool.shape[1]}")
+    kp, kt, kl, kh = (0, 0, 0, 0) if k_out is None else _heads(k_out, shape, "k_out")
+    vp, vt, vl, vh = (0, kt, 0, 0) if v_out is None else _heads(v_out, shape, "v_out")
+    if k_out is not None and vt != kt:
+        raise ValueError("v_out: expected k_out's type")
+    status = _lib.pq2_cache4_read(_cache4_read_args.pack(
+        *_cache4(pool, pages, row_start, lens, shape[2]), kp, vp, kl, kh, vl, vh, shape[0], vt, 0), _stream(stream))
+    if status:
+        raise PQ2Error(status, "pq2_cache4_read")
+
+
+def pq2_cache4_attend_workspace_bytes(M, q_heads, heads, dim) -> int:
+    return int(_lib.pq2_cache4_attend_workspace_bytes(M, q_heads, heads, dim))
+
+
+def alloc_attend_workspace(M, q_heads, heads, dim, device="cuda"):
+    n = pq2_cache4_attend_workspace_bytes(M, q_heads, heads, dim)
+    if n == SIZE_MAX:
+        raise PQ2Error(PQ2_ERR_UNSUPPORTED_SHAPE, "pq2_cache4_attend_workspace_bytes")
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def pq2_cache4_attend(q, pool, pages, row_start, lens, out, workspace, scale=None, window=0, max_rows=0, stream=None):
+    """out = attention of the token rows q [M, q_heads, dim] (fp16 or bf16)
+    over the cache, each over its sequence's positions up to its own (the last
+    `window` of them); out of q's type.  scale: 1 / sqrt(dim) by default.
+    max_rows: an upper bound of the sequences' rows (1 in a decode step)."""
+    shape = q.shape
+    M, Hq, D = shape
+    qp, qt, ql, qh = _heads(q, shape, "q")
+    op, ot, ol, oh = _heads(out, shape, "out")
+    if ot != qt or qt == PQ2_F32:
+        raise ValueError("q and out: expected float16 or bfloat16, both the same")
+    wp, wb = (0, 0) if workspace is None else (_ptr(workspace), workspace.nbytes)
+    status = _lib.pq2_cache4_attend(_cache4_attend_args.pack(
+        *_cache4(pool, pages, row_start, lens, D), qp, op, wp, ql, qh, ol, oh, M, max_rows, window, wb,
+        D ** -0.5 if scale is None else scale, Hq, qt, 0), _stream(stream))
+    if status:
+        raise PQ2Error(status, "pq2_cache4_attend")
+
+
+def pq2_pages_workspace_bytes(B, P) -> int:
+    return int(_lib.pq2_pages_workspace_bytes(B, P))
+
+
+def alloc_pages_workspace(B, P, device="cuda"):
+    n = pq2_pages_workspace_bytes(B, P)
+    if n == SIZE_MAX:
+        raise PQ2Error(PQ2_ERR_UNSUPPORTED_SHAPE, "pq2_pages_workspace_bytes")
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def _pages(t, shape, name):
+    """(pointer, row stride) of an int32 CUDA tensor [B, W] with contiguous rows."""
+    if t.dtype is not _I32 or t.shape != shape or not t.is_cuda or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected an int32 CUDA tensor of shape {tuple(shape)} with contiguous rows")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def pq2_pages_update(pages, refs, lens, source, keep, new_lens, page_tokens, pages_out, refs_out, copies, info,
+                     workspace, stream=None):
+    """Slot b goes on from slot source[b] (itself, another, or < 0: none) with
+    its first keep[b] tokens, and gets pages for new_lens[b]: pages, pages_out
+    int32 [B, W]; refs, refs_out int32 [P] (may be one); lens, source, keep,
+    new_lens int32 [B]; copies int32 [B, 2] (for pq2_pages_copy); info int32 [2]."""
+    shape = pages.shape
+    B, W = shape
+    P = refs.shape[0]
+    pp, pl = _pages(pages, shape, "pages")
+    op, ol = _pages(pages_out, shape, "pages_out")
+    n = (B,)
+    wp, wb = (0, 0) if workspace is None else (_ptr(workspace), workspace.nbytes)
+    status = _lib.pq2_pages_update(_pages_update_args.pack(
+        pp, _vec(lens, n, _I32, "lens"), _vec(refs, (P,), _I32, "refs"), _vec(source, n, _I32, "source"),
+        _vec(keep, n, _I32, "keep"), _vec(new_lens, n, _I32, "new_lens"), op, _vec(refs_out, (P,), _I32, "refs_out"),
+        _vec(copies, (B, 2), _I32, "copies"), _vec(info, (2,), _I32, "info"), wp, pl, ol, B, W, P, page_tokens, wb),
+        _stream(stream))
+    if status:
+        raise PQ2Error(status, "pq2_pages_update")
+
+
+def pq2_pages_compact(pages, refs, lens, page_tokens, pages_out, refs_out, copies, info, workspace, stream=None):
+    """The moves after which the pages in use (refs > 0) are the first ones:
+    copies int32 [P // 2, 2] (for pq2_pages_copy), and pages and refs after them."""
+    shape = pages.shape
+    B, W = shape
+    P = refs.shape[0]
+    pp, pl = _pages(pages, shape, "pages")
+    op, ol = _pages(pages_out, shape, "pages_out")
+    wp, wb = (0, 0) if workspace is None else (_ptr(workspace), workspace.nbytes)
+    status = _lib.pq2_pages_compact(_pages_compact_args.pack(
+        pp, _vec(lens, (B,), _I32, "lens"), _vec(refs, (P,), _I32, "refs"), op, _vec(refs_out, (P,), _I32, "refs_out"),
+        _vec(copies, (P // 2, 2), _I32, "copies"), _vec(info, (2,), _I32, "info"), wp, pl, ol, B, W, P, page_tokens,
+        wb), _stream(stream))
+    if status:
+        raise PQ2Error(status, "pq2_pages_compact")
+
+
+def pq2_pages_copy(pool, copies, layers=False, stream=None):
+    """Copies pages within a pool: copies int32 [n, 2], pairs (old, new), those
+    with a negative page skipped.  pool [pages, ...] of any type, a page
+    contiguous; with layers, [layers, pages, ...], the same pairs in each."""
+    if not pool.is_cuda:
+        raise ValueError("pool: expected a CUDA tensor")
+    at = 1 if layers else 0
+    if pool.dim() <= at or (pool.numel() and not pool[(0,) * (at + 1)].is_contiguous()):
+        raise ValueError("pool: a page must be contiguous")
+    size = pool.element_size()
+    P = pool.shape[at]
+    nbytes = size
+    for n in pool.shape[at + 1:]:
+        nbytes *= n
+    page_stride = pool.stride(at) * size if P > 1 else nbytes
+    n = copies.shape[0]
+    _check(_lib.pq2_pages_copy(pool.data_ptr(), nbytes, page_stride, P, pool.shape[0] if layers else 1,
+                               pool.stride(0) * size if layers else 0, _vec(copies, (n, 2), _I32, "copies"), n,
+                               _stream(stream)), "pq2_pages_copy")
 
 
 def pq2_group_dots(op, qp, T, codes, dots, workspace=None, stream=None):

@@ -2,6 +2,7 @@
 // routing to the kernels, and the device error word.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -676,6 +677,361 @@ pq2_status pq2_verify_drafts_packed(const pq2_verify_drafts_args* a, void* strea
     return pq2_verify_drafts(a->logits, a->ld_logits, a->row_start, a->drafts, a->q, a->ld_q, a->u,
                              a->e, a->ld_e, a->temperature, a->accepted, a->tokens, a->B, a->rows,
                              a->V, a->workspace, a->workspace_bytes, stream);
+}
+
+// --- rotary positions, the cache in 4 bits, its pages -----------------------
+
+static_assert(sizeof(pq2_cache4) == 88 && sizeof(pq2_rope_args) == 160 &&
+                  sizeof(pq2_cache4_append_args) == 240 && sizeof(pq2_cache4_read_args) == 152 &&
+                  sizeof(pq2_cache4_attend_args) == 192 && sizeof(pq2_pages_update_args) == 144 &&
+                  sizeof(pq2_pages_compact_args) == 120,
+              "no padding");
+
+// The last element (and one more) of an array [M, heads, dim].
+static int64_t extent(int64_t M, int64_t ld, int64_t heads, int64_t hs, int64_t dim) {
+    return M > 0 && heads > 0 ? (M - 1) * ld + (heads - 1) * hs + dim : 0;
+}
+
+// One array of heads: present, strides that keep heads and tokens apart.
+static pq2_status check_heads(const void* x, int type, int64_t ld, int64_t hs, int64_t heads, int64_t dim) {
+    if (heads == 0) return PQ2_OK;
+    if (!x || (heads > 1 && hs < dim) || ld < dim || hs < 0) return PQ2_ERR_INVALID_ARG;
+    return aligned_to(x, type_bytes(type)) ? PQ2_OK : PQ2_ERR_MISALIGNED;
+}
+
+pq2_status pq2_rope_table(float* table, int64_t first, int64_t count, int64_t rot, double base,
+                          const pq2_rope_scaling* scaling, void* stream) {
+    if (first < 0 || count < 0 || rot < 2 || rot % 2 != 0 || !(base > 1.0) || !std::isfinite(base))
+        return PQ2_ERR_INVALID_ARG;
+    pq2_rope_scaling s = {};
+    if (scaling) s = *scaling;
+    if (s.kind < PQ2_ROPE_PLAIN || s.kind > PQ2_ROPE_BANDS || !std::isfinite(s.magnitude)) return PQ2_ERR_INVALID_ARG;
+    if (s.kind != PQ2_ROPE_PLAIN && (!(s.factor >= 1.0) || !std::isfinite(s.factor))) return PQ2_ERR_INVALID_ARG;
+    if (s.kind == PQ2_ROPE_BASE && rot == 2) return PQ2_ERR_INVALID_ARG;
+    if ((s.kind == PQ2_ROPE_RAMP || s.kind == PQ2_ROPE_BANDS) &&
+        (!(s.old_len > 0.0) || !(s.low > 0.0) || !(s.high > s.low) || !std::isfinite(s.old_len) ||
+         !std::isfinite(s.high)))
+        return PQ2_ERR_INVALID_ARG;
+    if (rot > PQ2_ROPE_MAX_DIM || first + count > (int64_t(1) << 31)) return PQ2_ERR_UNSUPPORTED_SHAPE;
+    if (count == 0) return PQ2_OK;
+    if (!table) return PQ2_ERR_INVALID_ARG;
+    if (!aligned16(table)) return PQ2_ERR_MISALIGNED;
+    pq2h::RopeTableParams p = {};
+    p.table = table;
+    p.first = first, p.count = count;
+    p.rot = static_cast<int>(rot);
+    p.kind = s.kind;
+    p.factor = s.kind == PQ2_ROPE_PLAIN ? 1.0 : s.factor;
+    p.magnitude = s.magnitude == 0.0f ? 1.0 : s.magnitude;
+    p.old_len = s.old_len, p.low = s.low, p.high = s.high;
+    p.log_base = std::log(base);
+    const double r = static_cast<double>(rot);
+    if (s.kind == PQ2_ROPE_BASE) p.log_base += std::log(s.factor) * r / (r - 2.0);
+    if (s.kind == PQ2_ROPE_RAMP) {
+        // the index whose pair turns n times over old_len positions
+        const auto index = [&](double n) { return r / 2.0 * std::log(s.old_len / (6.283185307179586476925 * n)) / p.log_base; };
+        p.low = std::max(std::floor(index(s.high)), 0.0);
+        p.high = std::min(std::ceil(index(s.low)), r - 1.0);
+        if (p.high - p.low < 0.001) p.high = p.low + 0.001;
+    }
+    Ctx c;
+    const pq2_status st = get_ctx(&c);
+    if (st != PQ2_OK) return st;
+    p.ctl = c.ctl;
+    return cuda_status(pq2h::launch_rope_table(p, static_cast<cudaStream_t>(stream)));
+}
+
+pq2_status pq2_rope(const pq2_rope_args* args, void* stream) {
+    if (!args) return PQ2_ERR_INVALID_ARG;
+    const pq2_rope_args& a = *args;
+    if (a.M < 0 || a.heads < 0 || a.heads2 < 0 || a.dim < 1 || a.rot < 0 || a.rot > a.dim || a.rot % 2 != 0 ||
+        a.table_rows < 0 || a.reserved != 0 || (a.flags & ~(PQ2_ROPE_NEIGHBOURS | PQ2_ROPE_INVERSE)) ||
+        !type_ok(a.x_type) || !type_ok(a.out_type))
+        return PQ2_ERR_INVALID_ARG;
+    if (a.dim > PQ2_ROPE_MAX_DIM || int64_t(a.heads) + a.heads2 > 65536 || a.M > (int64_t(1) << 24))
+        return PQ2_ERR_UNSUPPORTED_SHAPE;
+    if (a.M == 0 || a.heads + a.heads2 == 0) return PQ2_OK;
+    pq2_status s = check_heads(a.x, a.x_type, a.ld_x, a.hs_x, a.heads, a.dim);
+    if (s == PQ2_OK) s = check_heads(a.x2, a.x_type, a.ld_x2, a.hs_x2, a.heads2, a.dim);
+    if (s == PQ2_OK) s = check_heads(a.out, a.out_type, a.ld_out, a.hs_out, a.heads, a.dim);
+    if (s == PQ2_OK) s = check_heads(a.out2, a.out_type, a.ld_out2, a.hs_out2, a.heads2, a.dim);
+    if (s != PQ2_OK) return s;
+    if (a.rot > 0 && (!a.table || !a.positions)) return PQ2_ERR_INVALID_ARG;
+    if (!aligned16(a.table) || !aligned_to(a.positions, 4)) return PQ2_ERR_MISALIGNED;
+    if ((a.heads > 0 && a.out == a.x && (a.out_type != a.x_type || a.ld_out != a.ld_x || a.hs_out != a.hs_x)) ||
+        (a.heads2 > 0 && a.out2 == a.x2 && (a.out_type != a.x_type || a.ld_out2 != a.ld_x2 || a.hs_out2 != a.hs_x2)))
+        return PQ2_ERR_INVALID_ARG;
+    Ctx c;
+    s = get_ctx(&c);
+    if (s != PQ2_OK) return s;
+    pq2h::RopeParams p = {};
+    p.x[0] = a.x, p.x[1] = a.x2, p.out[0] = a.out, p.out[1] = a.out2;
+    p.ld[0] = a.ld_x, p.hs[0] = a.hs_x, p.ld[1] = a.ld_x2, p.hs[1] = a.hs_x2;
+    p.ldo[0] = a.ld_out, p.hso[0] = a.hs_out, p.ldo[1] = a.ld_out2, p.hso[1] = a.hs_out2;
+    p.out_elems[0] = extent(a.M, a.ld_out, a.heads, a.hs_out, a.dim);
+    p.out_elems[1] = extent(a.M, a.ld_out2, a.heads2, a.hs_out2, a.dim);
+    p.table = a.table, p.positions = a.positions;
+    p.M = a.M, p.table_rows = a.table_rows;
+    p.heads[0] = a.heads, p.heads[1] = a.heads2;
+    p.dim = a.dim, p.rot = a.rot, p.x_type = a.x_type, p.out_type = a.out_type;
+    p.flags = a.flags;
+    p.ctl = c.ctl;
+    return cuda_status(pq2h::launch_rope(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t pq2_cache4_page_bytes(int64_t heads, int64_t dim, int64_t page_tokens) {
+    if (heads < 1 || heads > PQ2_CACHE4_MAX_HEADS || (dim != 64 && dim != 128 && dim != 256) || page_tokens < 16 ||
+        page_tokens % 16 != 0 || page_tokens > 1024)
+        return 0;
+    return static_cast<size_t>(heads * page_tokens * (dim + 8));
+}
+
+// Sizes first (they decide what is supported), then, where there is work to
+// do, pointers.
+static pq2_status check_cache(const pq2_cache4& a) {
+    if (a.B < 0 || a.W < 0 || a.num_pages < 0 || a.heads < 1 || a.reserved != 0) return PQ2_ERR_INVALID_ARG;
+    const size_t page = pq2_cache4_page_bytes(a.heads, a.dim, a.page_tokens);
+    if (page == 0 || a.B > (int64_t(1) << 20) || a.num_pages > (int64_t(1) << 30) || a.page_stride % 16 != 0 ||
+        a.W * a.page_tokens > (int64_t(1) << 30) || a.W > (int64_t(1) << 30))
+        return PQ2_ERR_UNSUPPORTED_SHAPE;
+    if (a.page_stride < static_cast<int64_t>(page) || a.ld_pages < a.W) return PQ2_ERR_INVALID_ARG;
+    return PQ2_OK;
+}
+static pq2_status check_cache_pointers(const pq2_cache4& a) {
+    if (!a.row_start || !a.lens || (a.W > 0 && !a.pages) || (a.num_pages > 0 && !a.pool)) return PQ2_ERR_INVALID_ARG;
+    if (!aligned16(a.pool) || !aligned_to(a.pages, 4) || !aligned_to(a.row_start, 4) || !aligned_to(a.lens, 4))
+        return PQ2_ERR_MISALIGNED;
+    return PQ2_OK;
+}
+static pq2h::CacheParams cache_params(const pq2_cache4& a) {
+    pq2h::CacheParams p = {};
+    p.pool = static_cast<uint8_t*>(a.pool);
+    p.pages = a.pages, p.row_start = a.row_start, p.lens = a.lens;
+    p.page_stride = a.page_stride, p.num_pages = a.num_pages, p.ld_pages = a.ld_pages;
+    p.pool_bytes = a.num_pages > 0 ? (a.num_pages - 1) * a.page_stride +
+                                         static_cast<int64_t>(pq2_cache4_page_bytes(a.heads, a.dim, a.page_tokens))
+                                   : 0;
+    p.B = static_cast<int>(a.B), p.W = static_cast<int>(a.W), p.heads = a.heads, p.T = a.page_tokens;
+    return p;
+}
+
+pq2_status pq2_cache4_append(const pq2_cache4_append_args* args, void* stream) {
+    if (!args) return PQ2_ERR_INVALID_ARG;
+    const pq2_cache4_append_args& a = *args;
+    pq2_status s = check_cache(a.cache);
+    if (s != PQ2_OK) return s;
+    const int dim = a.cache.dim;
+    if (a.M < 0 || a.q_heads < 0 || a.rot < 0 || a.rot > dim || a.rot % 2 != 0 || a.table_rows < 0 || a.reserved != 0 ||
+        (a.flags & ~PQ2_ROPE_NEIGHBOURS) || !type_ok(a.x_type) || (a.q_heads > 0 && !type_ok(a.out_type)))
+        return PQ2_ERR_INVALID_ARG;
+    if (a.M > (int64_t(1) << 24) || a.q_heads > 65536) return PQ2_ERR_UNSUPPORTED_SHAPE;
+    if (a.M == 0 || a.cache.B == 0) return PQ2_OK;
+    s = check_cache_pointers(a.cache);
+    if (s == PQ2_OK) s = check_heads(a.k, a.x_type, a.ld_k, a.hs_k, a.cache.heads, dim);
+    if (s == PQ2_OK) s = check_heads(a.v, a.x_type, a.ld_v, a.hs_v, a.cache.heads, dim);
+    if (s == PQ2_OK) s = check_heads(a.q, a.x_type, a.ld_q, a.hs_q, a.q_heads, dim);
+    if (s == PQ2_OK && a.q_heads > 0) s = check_heads(a.q_out, a.out_type, a.ld_q_out, a.hs_q_out, a.q_heads, dim);
+    if (s != PQ2_OK) return s;
+    if (a.rot > 0 && !a.table) return PQ2_ERR_INVALID_ARG;
+    if (!aligned16(a.table) || !aligned_to(a.positions, 4)) return PQ2_ERR_MISALIGNED;
+    if (a.q_heads > 0 && a.q_out == a.q && (a.out_type != a.x_type || a.ld_q_out != a.ld_q || a.hs_q_out != a.hs_q))
+        return PQ2_ERR_INVALID_ARG;
+    Ctx c;
+    s = get_ctx(&c);
+    if (s != PQ2_OK) return s;
+    pq2h::RopeParams p = {};
+    p.x[0] = a.q, p.x[1] = a.k, p.x[2] = a.v, p.out[0] = a.q_out;
+    p.ld[0] = a.ld_q, p.hs[0] = a.hs_q, p.ld[1] = a.ld_k, p.hs[1] = a.hs_k, p.ld[2] = a.ld_v, p.hs[2] = a.hs_v;
+    p.ldo[0] = a.ld_q_out, p.hso[0] = a.hs_q_out;
+    p.out_elems[0] = extent(a.M, a.ld_q_out, a.q_heads, a.hs_q_out, dim);
+    p.table = a.table, p.positions = a.positions;
+    p.M = a.M, p.table_rows = a.table_rows;
+    p.heads[0] = a.q_heads, p.heads[1] = p.heads[2] = a.cache.heads;
+    p.dim = dim, p.rot = a.rot, p.x_type = a.x_type, p.out_type = a.out_type;
+    p.flags = a.flags;
+    p.cache = cache_params(a.cache);
+    p.ctl = c.ctl;
+    return cuda_status(pq2h::launch_cache_append(p, static_cast<cudaStream_t>(stream)));
+}
+
+pq2_status pq2_cache4_read(const pq2_cache4_read_args* args, void* stream) {
+    if (!args) return PQ2_ERR_INVALID_ARG;
+    const pq2_cache4_read_args& a = *args;
+    pq2_status s = check_cache(a.cache);
+    if (s != PQ2_OK) return s;
+    const int dim = a.cache.dim, heads = a.cache.heads;
+    if (a.M < 0 || a.reserved != 0 || !type_ok(a.out_type)) return PQ2_ERR_INVALID_ARG;
+    if (a.M > (int64_t(1) << 24)) return PQ2_ERR_UNSUPPORTED_SHAPE;
+    if (a.M == 0 || a.cache.B == 0 || (!a.k_out && !a.v_out)) return PQ2_OK;
+    s = check_cache_pointers(a.cache);
+    if (s == PQ2_OK && a.k_out) s = check_heads(a.k_out, a.out_type, a.ld_k, a.hs_k, heads, dim);
+    if (s == PQ2_OK && a.v_out) s = check_heads(a.v_out, a.out_type, a.ld_v, a.hs_v, heads, dim);
+    if (s != PQ2_OK) return s;
+    Ctx c;
+    s = get_ctx(&c);
+    if (s != PQ2_OK) return s;
+    pq2h::RopeParams p = {};
+    int n = 0;
+    for (int value = 0; value < 2; ++value) {
+        if (!(value ? a.v_out : a.k_out)) continue;
+        p.out[n] = value ? a.v_out : a.k_out;
+        p.ldo[n] = value ? a.ld_v : a.ld_k;
+        p.hso[n] = value ? a.hs_v : a.hs_k;
+        p.out_elems[n] = extent(a.M, p.ldo[n], heads, p.hso[n], dim);
+        p.heads[n] = heads;
+        p.read_kind[n++] = value;
+    }
+    p.M = a.M;
+    p.dim = dim, p.out_type = a.out_type;
+    p.cache = cache_params(a.cache);
+    p.ctl = c.ctl;
+    return cuda_status(pq2h::launch_cache_read(p, static_cast<cudaStream_t>(stream)));
+}
+
+static pq2_status check_attend(int64_t M, int64_t q_heads, int64_t heads, int64_t dim) {
+    if (M < 0 || q_heads < 1 || heads < 1 || q_heads % heads != 0) return PQ2_ERR_INVALID_ARG;
+    if (M > (int64_t(1) << 20) || heads > PQ2_CACHE4_MAX_HEADS || q_heads / heads > 64 ||
+        M * q_heads > (int64_t(1) << 30) || (dim != 64 && dim != 128 && dim != 256))
+        return PQ2_ERR_UNSUPPORTED_SHAPE;
+    return PQ2_OK;
+}
+
+size_t pq2_cache4_attend_workspace_bytes(int64_t M, int64_t q_heads, int64_t heads, int64_t dim) {
+    if (check_attend(M, q_heads, heads, dim) != PQ2_OK) return SIZE_MAX;
+    return M == 0 ? 0 : pq2h::attend_workspace_bytes(M, q_heads, heads, dim);
+}
+
+pq2_status pq2_cache4_attend(const pq2_cache4_attend_args* args, void* stream) {
+    if (!args) return PQ2_ERR_INVALID_ARG;
+    const pq2_cache4_attend_args& a = *args;
+    pq2_status s = check_cache(a.cache);
+    if (s == PQ2_OK) s = check_attend(a.M, a.q_heads, a.cache.heads, a.cache.dim);
+    if (s != PQ2_OK) return s;
+    const int dim = a.cache.dim;
+    if ((a.type != PQ2_F16 && a.type != PQ2_BF16) || a.max_rows < 0 || a.window < 0 || !std::isfinite(a.scale) ||
+        a.reserved != 0)
+        return PQ2_ERR_INVALID_ARG;
+    if (a.M == 0 || a.cache.B == 0) return PQ2_OK;
+    s = check_cache_pointers(a.cache);
+    if (s == PQ2_OK) s = check_heads(a.q, a.type, a.ld_q, a.hs_q, a.q_heads, dim);
+    if (s == PQ2_OK) s = check_heads(a.out, a.type, a.ld_out, a.hs_out, a.q_heads, dim);
+    if (s != PQ2_OK) return s;
+    if (!aligned16(a.q) || !aligned16(a.out) || !aligned16(a.workspace) || a.ld_q % 8 != 0 || a.hs_q % 8 != 0 ||
+        a.ld_out % 8 != 0 || a.hs_out % 8 != 0)
+        return PQ2_ERR_MISALIGNED;
+    if (!a.workspace || a.workspace_bytes < pq2h::attend_workspace_bytes(a.M, a.q_heads, a.cache.heads, dim))
+        return PQ2_ERR_WORKSPACE;
+    Ctx c;
+    s = get_ctx(&c);
+    if (s != PQ2_OK) return s;
+    pq2h::AttendParams p = {};
+    p.cache = cache_params(a.cache);
+    p.q = static_cast<const uint16_t*>(a.q);
+    p.out = static_cast<uint16_t*>(a.out);
+    p.ld_q = a.ld_q, p.hs_q = a.hs_q, p.ld_out = a.ld_out, p.hs_out = a.hs_out;
+    p.out_elems = extent(a.M, a.ld_out, a.q_heads, a.hs_out, dim);
+    p.M = static_cast<int>(a.M);
+    p.max_rows = static_cast<int>(a.max_rows > 0 ? std::min(a.max_rows, a.M) : a.M);
+    p.window = static_cast<int>(std::min<int64_t>(a.window, (int64_t(1) << 30) + 1));
+    p.q_heads = a.q_heads, p.dim = dim, p.bf16 = a.type == PQ2_BF16;
+    p.scale = a.scale;
+    p.ctl = c.ctl;
+    return cuda_status(pq2h::launch_attend(p, a.workspace, static_cast<cudaStream_t>(stream), c.dev));
+}
+
+static pq2_status check_pages(int64_t B, int64_t W, int64_t P, int64_t T, int64_t ld_pages, int64_t ld_out) {
+    if (B < 0 || W < 1 || P < 0 || T < 1) return PQ2_ERR_INVALID_ARG;
+    if (B > (int64_t(1) << 20) || W > (int64_t(1) << 20) || B * W > (int64_t(1) << 30) || P > (int64_t(1) << 28) ||
+        T > (int64_t(1) << 20) || W * T > (int64_t(1) << 30))
+        return PQ2_ERR_UNSUPPORTED_SHAPE;
+    return ld_pages >= W && ld_out >= W ? PQ2_OK : PQ2_ERR_INVALID_ARG;
+}
+
+size_t pq2_pages_workspace_bytes(int64_t B, int64_t P) {
+    if (check_pages(B, 1, P, 1, 1, 1) != PQ2_OK) return SIZE_MAX;
+    return pq2h::pages_workspace_bytes(B, P);
+}
+
+pq2_status pq2_pages_update(const pq2_pages_update_args* args, void* stream) {
+    if (!args) return PQ2_ERR_INVALID_ARG;
+    const pq2_pages_update_args& a = *args;
+    pq2_status s = check_pages(a.B, a.W, a.P, a.T, a.ld_pages, a.ld_out);
+    if (s != PQ2_OK) return s;
+    if (!a.info || (a.P > 0 && (!a.refs || !a.refs_out)) ||
+        (a.B > 0 && (!a.pages || !a.lens || !a.source || !a.keep || !a.new_lens || !a.pages_out || !a.copies)))
+        return PQ2_ERR_INVALID_ARG;
+    for (const void* x : {static_cast<const void*>(a.pages), static_cast<const void*>(a.lens),
+                          static_cast<const void*>(a.refs), static_cast<const void*>(a.source),
+                          static_cast<const void*>(a.keep), static_cast<const void*>(a.new_lens),
+                          static_cast<const void*>(a.pages_out), static_cast<const void*>(a.refs_out),
+                          static_cast<const void*>(a.copies), static_cast<const void*>(a.info)})
+        if (!aligned_to(x, 4)) return PQ2_ERR_MISALIGNED;
+    if (a.B > 0 && a.pages_out == a.pages) return PQ2_ERR_INVALID_ARG;
+    if (!aligned16(a.workspace)) return PQ2_ERR_MISALIGNED;
+    if (!a.workspace || a.workspace_bytes < pq2h::pages_workspace_bytes(a.B, a.P)) return PQ2_ERR_WORKSPACE;
+    Ctx c;
+    s = get_ctx(&c);
+    if (s != PQ2_OK) return s;
+    pq2h::PagesParams p = {};
+    p.pages = a.pages, p.lens = a.lens, p.refs = a.refs, p.source = a.source, p.keep = a.keep;
+    p.new_lens = a.new_lens, p.pages_out = a.pages_out, p.refs_out = a.refs_out, p.copies = a.copies;
+    p.info = a.info;
+    p.ld_pages = a.ld_pages, p.ld_out = a.ld_out;
+    p.B = static_cast<int>(a.B), p.W = static_cast<int>(a.W), p.P = static_cast<int>(a.P);
+    p.T = static_cast<int>(a.T);
+    p.ctl = c.ctl;
+    return cuda_status(pq2h::launch_pages_update(p, a.workspace, static_cast<cudaStream_t>(stream)));
+}
+
+pq2_status pq2_pages_compact(const pq2_pages_compact_args* args, void* stream) {
+    if (!args) return PQ2_ERR_INVALID_ARG;
+    const pq2_pages_compact_args& a = *args;
+    pq2_status s = check_pages(a.B, a.W, a.P, a.T, a.ld_pages, a.ld_out);
+    if (s != PQ2_OK) return s;
+    if (!a.info || (a.P > 0 && (!a.refs || !a.refs_out)) || (a.P > 1 && !a.copies) ||
+        (a.B > 0 && (!a.pages || !a.lens || !a.pages_out)))
+        return PQ2_ERR_INVALID_ARG;
+    for (const void* x : {static_cast<const void*>(a.pages), static_cast<const void*>(a.lens),
+                          static_cast<const void*>(a.refs), static_cast<const void*>(a.pages_out),
+                          static_cast<const void*>(a.refs_out), static_cast<const void*>(a.copies),
+                          static_cast<const void*>(a.info)})
+        if (!aligned_to(x, 4)) return PQ2_ERR_MISALIGNED;
+    if (a.B > 0 && a.pages_out == a.pages && a.ld_out != a.ld_pages) return PQ2_ERR_INVALID_ARG;
+    if (!aligned16(a.workspace)) return PQ2_ERR_MISALIGNED;
+    if (!a.workspace || a.workspace_bytes < pq2h::pages_workspace_bytes(a.B, a.P)) return PQ2_ERR_WORKSPACE;
+    Ctx c;
+    s = get_ctx(&c);
+    if (s != PQ2_OK) return s;
+    pq2h::PagesParams p = {};
+    p.pages = a.pages, p.lens = a.lens, p.refs = a.refs;
+    p.pages_out = a.pages_out, p.refs_out = a.refs_out, p.copies = a.copies, p.info = a.info;
+    p.ld_pages = a.ld_pages, p.ld_out = a.ld_out;
+    p.B = static_cast<int>(a.B), p.W = static_cast<int>(a.W), p.P = static_cast<int>(a.P);
+    p.T = static_cast<int>(a.T);
+    p.ctl = c.ctl;
+    return cuda_status(pq2h::launch_pages_compact(p, a.workspace, static_cast<cudaStream_t>(stream)));
+}
+
+pq2_status pq2_pages_copy(void* pool, int64_t page_bytes, int64_t page_stride, int64_t P, int64_t layers,
+                          int64_t layer_stride, const int32_t* pairs, int64_t n, void* stream) {
+    if (page_bytes < 0 || page_stride < page_bytes || P < 0 || layers < 0 || layer_stride < 0 || n < 0)
+        return PQ2_ERR_INVALID_ARG;
+    if (page_bytes % 16 != 0 || page_stride % 16 != 0 || layer_stride % 16 != 0 || layers > 65536 ||
+        n > (int64_t(1) << 28) || P > (int64_t(1) << 31) || page_bytes > (int64_t(1) << 32))
+        return PQ2_ERR_UNSUPPORTED_SHAPE;
+    if (n == 0 || layers == 0 || P == 0 || page_bytes == 0) return PQ2_OK;
+    if (!pool || !pairs) return PQ2_ERR_INVALID_ARG;
+    if (!aligned16(pool) || !aligned_to(pairs, 8)) return PQ2_ERR_MISALIGNED;
+    Ctx c;
+    const pq2_status s = get_ctx(&c);
+    if (s != PQ2_OK) return s;
+    pq2h::PagesCopyParams p = {};
+    p.pool = static_cast<uint8_t*>(pool);
+    p.pairs = pairs;
+    p.page_bytes = page_bytes, p.page_stride = page_stride, p.P = P, p.layer_stride = layer_stride, p.n = n;
+    p.layers = static_cast<int>(layers);
+    p.ctl = c.ctl;
+    return cuda_status(pq2h::launch_pages_copy(p, static_cast<cudaStream_t>(stream), c.dev));
 }
 
 pq2_status pq2_group_dots(int op, const int8_t* qp, const int32_t* T, const uint8_t* codes,

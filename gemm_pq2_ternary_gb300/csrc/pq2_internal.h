@@ -225,4 +225,86 @@ size_t lora_workspace_needed(const LoraParams& p);  // for this call
 cudaError_t launch_lora(const LoraParams& p, void* workspace, cudaStream_t st,
                         const DeviceInfo& dev);
 
+// Keys and values held in 4 bits, in pages (pq2_cache.cuh).
+struct CacheParams {
+    uint8_t* pool;
+    const int32_t* pages;      // [B, W], row stride ld_pages
+    const int32_t* row_start;  // [B + 1]
+    const int32_t* lens;       // [B]
+    long long page_stride, num_pages, ld_pages;
+    long long pool_bytes;      // for the bounds-checked build
+    int B, W, heads, T;
+};
+
+// Rotary positions, appending to the cache and reading it back (pq2_rope.cu).
+// Arrays 0 (queries) and 1 (keys) are turned, array 2 (values) is not; strides
+// from token to token and from head to head in elements.
+struct RopeParams {
+    const void* x[3];
+    void* out[2];
+    long long ld[3], hs[3], ldo[2], hso[2];
+    long long out_elems[2];    // for the bounds-checked build
+    const float* table;        // [table_rows, rot / 2, 2]
+    const int32_t* positions;  // [M] or null: those in the cache
+    long long M, table_rows;
+    int heads[3];
+    int dim, rot, x_type, out_type;
+    int read_kind[2];          // launch_cache_read: array k is of keys (0) or values (1)
+    uint32_t flags;
+    CacheParams cache;
+    pq2::DevCtl ctl;
+};
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t st);
+cudaError_t launch_cache_append(const RopeParams& p, cudaStream_t st);
+cudaError_t launch_cache_read(const RopeParams& p, cudaStream_t st);
+
+struct RopeTableParams {
+    float* table;
+    long long first, count;
+    int rot, kind;
+    double log_base, factor, old_len;
+    double low, high;          // PQ2_ROPE_RAMP: the indexes; PQ2_ROPE_BANDS: the turns
+    double magnitude;
+    pq2::DevCtl ctl;
+};
+cudaError_t launch_rope_table(const RopeTableParams& p, cudaStream_t st);
+
+// Attention over the cache (pq2_attend.cu).
+struct AttendParams {
+    CacheParams cache;
+    const uint16_t* q;         // [M, q_heads, dim]
+    uint16_t* out;
+    long long ld_q, hs_q, ld_out, hs_out;
+    long long out_elems;
+    int M, max_rows, window;   // window 0: none
+    int q_heads, dim, bf16;
+    float scale;
+    pq2::DevCtl ctl;
+};
+size_t attend_workspace_bytes(int64_t M, int64_t q_heads, int64_t heads, int64_t dim);
+cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t st, const DeviceInfo& dev);
+
+// The pages of a cache between two steps (pq2_pages.cu).
+struct PagesParams {
+    const int32_t *pages, *lens, *refs, *source, *keep, *new_lens;
+    int32_t *pages_out, *refs_out, *copies, *info;
+    int32_t *w0, *w1, *w2, *w3;  // workspace: [P] each
+    int32_t *s0, *s1, *s2;       // workspace: [B] each
+    int32_t* sums;               // workspace: [2][kPagesSums]
+    long long ld_pages, ld_out;
+    int B, W, P, T;
+    pq2::DevCtl ctl;
+};
+size_t pages_workspace_bytes(int64_t B, int64_t P);
+cudaError_t launch_pages_update(PagesParams p, void* workspace, cudaStream_t st);
+cudaError_t launch_pages_compact(PagesParams p, void* workspace, cudaStream_t st);
+struct PagesCopyParams {
+    uint8_t* pool;
+    const int32_t* pairs;      // [n, 2]
+    long long page_bytes, page_stride, P, layer_stride, n;
+    int layers;
+    pq2::DevCtl ctl;
+};
+cudaError_t launch_pages_copy(const PagesCopyParams& p, cudaStream_t st, const DeviceInfo& dev);
+
 }  // namespace pq2h

@@ -454,6 +454,283 @@ typedef struct {
 pq2_status pq2_verify_drafts_packed(const pq2_verify_drafts_args* args, void* stream);
 
 /*
+ * Rotary positions.  A table holds, for positions first .. first + count - 1,
+ * the cosine and sine of each pair's angle: fp32 [count, rot / 2, 2].
+ */
+
+/* How a table's frequencies f_i = base^(-2 i / rot), i = 0 .. rot/2 - 1, are
+ * scaled for contexts longer than the trained one. */
+#define PQ2_ROPE_PLAIN 0  /* as they are                                        */
+#define PQ2_ROPE_LINEAR 1 /* f_i / factor                                       */
+#define PQ2_ROPE_BASE 2   /* base * factor^(rot / (rot - 2)) for base (rot > 2) */
+#define PQ2_ROPE_RAMP 3   /* by the index: f_i where it turns at least `high`
+                             times over `old_len` positions, f_i / factor where
+                             at most `low` times, and linear in i between the
+                             two indexes (rounded outwards, at least 0.001 apart) */
+#define PQ2_ROPE_BANDS 4  /* by the wavelength w = 2 pi / f_i: f_i where
+                             w < old_len / high, f_i / factor where w > old_len / low,
+                             between them (1 - t) f_i / factor + t f_i with
+                             t = (old_len / w - low) / (high - low)             */
+typedef struct pq2_rope_scaling {
+    int32_t kind;
+    float magnitude;  /* cosines and sines are multiplied by this (0: 1)        */
+    double factor;    /* >= 1 (kinds 1 to 4)                                    */
+    double old_len;   /* > 0 (kinds 3 and 4)                                    */
+    double low, high; /* 0 < low < high (kinds 3 and 4)                         */
+} pq2_rope_scaling;
+
+/* Largest rotated part, and largest head, of the entry points below. */
+#define PQ2_ROPE_MAX_DIM 512
+
+/*
+ * pq2_rope_table -- table out: fp32 [count, rot / 2, 2].  Frequencies and
+ * angles in 64 bits, cosines and sines rounded once to fp32.
+ *   scaling: NULL (PQ2_ROPE_PLAIN) or a host struct, read before the call returns.
+ * 2 <= rot <= PQ2_ROPE_MAX_DIM, rot % 2 == 0; base > 1; first >= 0, count >= 0 (0
+ * enqueues nothing), first + count <= 2^31.  table 16-byte aligned.
+ */
+pq2_status pq2_rope_table(float* table, int64_t first, int64_t count, int64_t rot, double base,
+                          const pq2_rope_scaling* scaling, void* stream);
+
+/* Flags of pq2_rope and pq2_cache4_append. */
+#define PQ2_ROPE_NEIGHBOURS 1u /* pairs (2i, 2i + 1); without it (i, i + rot/2) */
+#define PQ2_ROPE_INVERSE 2u    /* by the negative angle (pq2_rope only)         */
+
+/*
+ * pq2_rope -- turns the first `rot` values of every head by its token's angles:
+ *   a' = a cos - b sin,  b' = b cos + a sin
+ * for every pair (a, b), each product and sum one fp32 operation, rounded once
+ * to the output's type; the values behind `rot` are copied.
+ * One call takes up to two arrays (queries and keys) of the same tokens.
+ *   x, x2         in   [M, heads, dim] and [M, heads2, dim] (x_type; x2 and out2
+ *                      may be NULL with heads2 == 0)
+ *   out, out2     out  the same shapes (out_type); out may be x and out2 may be x2
+ *                      where types and strides are the same; else nothing overlaps
+ *   table         in   fp32 [table_rows, rot / 2, 2] (pq2_rope_table, or one's own)
+ *   positions     in   int32 [M], rows of the table; a token with one outside
+ *                      [0, table_rows) is left as it was in the outputs and sets the device
+ *                      error word (PQ2_ERR_INVALID_ARG from pq2_last_device_error)
+ * ld_*: strides from token to token, hs_*: from head to head (both >= dim), in
+ * elements.  A head's values are adjacent.  The gradient of x is the same call with
+ * PQ2_ROPE_INVERSE on the gradient of out.
+ * M >= 0 (0 enqueues nothing), 1 <= dim <= PQ2_ROPE_MAX_DIM, 0 <= rot <= dim,
+ * rot % 2 == 0, heads + heads2 <= 65536, M <= 2^24.  Pointers aligned to their elements, the table to
+ * 16 bytes.  The vector path takes dims of 64, 128 and 256 whose pairs fall on
+ * 16-byte boundaries (rot / 2, or rot with NEIGHBOURS, a multiple of dim / 32).
+ */
+typedef struct pq2_rope_args {
+    const void *x, *x2;
+    void *out, *out2;
+    const float* table;
+    const int32_t* positions;
+    int64_t ld_x, hs_x, ld_x2, hs_x2, ld_out, hs_out, ld_out2, hs_out2;
+    int64_t M, table_rows;
+    int32_t heads, heads2, dim, rot, x_type, out_type;
+    uint32_t flags;
+    int32_t reserved; /* 0 */
+} pq2_rope_args;
+pq2_status pq2_rope(const pq2_rope_args* args, void* stream);
+
+/*
+ * A cache of keys and values in 4 bits, in pages of T tokens (T % 16 == 0).
+ * A page of one key/value head is T / 16 tiles of 16 tokens, each
+ *     16 rows of D/2 bytes   key codes (value 2i in the low half of byte i)
+ *     16 rows of D/2 bytes   value codes
+ *     16 pairs of fp16       scale and offset of each key row
+ *     16 pairs of fp16       scale and offset of each value row
+ * (16 (D + 8) bytes), the heads of a page one behind the other.  Every row of
+ * D values has one scale and one offset; a code c stands for c * scale + offset.
+ * From values x of a row, in fp32, each step rounded to nearest even:
+ *     scale  = fp16(min((max - min) * (1/15), 65504)),  offset = fp16(min clamped to +-65504)
+ *     c      = rint((x - offset) * (1 / scale)) clamped to 0 .. 15     (0 where scale is 0)
+ * with 1/15 the nearest fp32.  NaN or Inf in a row: its contents are undefined.
+ *
+ * The sequences of a call:
+ *   row_start  int32 [B + 1]  token rows row_start[b] .. row_start[b+1] - 1 are
+ *                             sequence b's newest; rows from row_start[B] on
+ *                             belong to none (padding): outputs there are left as they were
+ *   lens       int32 [B]      tokens of the sequence with the new ones: row i of
+ *                             its n rows has position lens[b] - n + i
+ *   pages      int32 [B, W]   page of positions T j .. T j + T - 1 (row stride ld_pages >= W);
+ *                             entries behind the last token's are not read
+ */
+#define PQ2_CACHE4_MAX_HEADS 1024
+
+/* The arguments that the calls on such a cache share. */
+typedef struct pq2_cache4 {
+    void* pool;             /* 16-byte aligned                                   */
+    const int32_t* pages;
+    const int32_t* row_start;
+    const int32_t* lens;
+    int64_t page_stride;    /* bytes from page to page (>= pq2_cache4_page_bytes, % 16 == 0) */
+    int64_t num_pages;      /* in the pool                                       */
+    int64_t ld_pages;
+    int64_t B, W;
+    int32_t heads, dim;     /* key/value heads; 64, 128 or 256 values            */
+    int32_t page_tokens;    /* T: a multiple of 16, at most 1024                 */
+    int32_t reserved;       /* 0                                                 */
+} pq2_cache4;
+
+/* Bytes of a page (all its heads); 0 for sizes that are not supported. */
+size_t pq2_cache4_page_bytes(int64_t heads, int64_t dim, int64_t page_tokens);
+
+/*
+ * pq2_cache4_append -- new tokens into the cache: keys turned by their
+ * positions (pq2_rope's arithmetic), keys and values quantised and stored; with q, the
+ * queries turned in the same launch.
+ *   k, v       in   [M, heads, dim] (x_type), token and head strides in elements
+ *   q, q_out   q in [M, q_heads, dim] (x_type), q_out out (out_type), or both NULL with
+ *                   q_heads == 0.  q_out may be q where type and strides are the same.
+ *   table      in   fp32 [table_rows, rot / 2, 2], or NULL with rot == 0 (nothing is turned)
+ *   positions  in   int32 [M] rows of the table, or NULL: the tokens' positions
+ * A token whose position, page or row of the table lies outside its range is
+ * skipped and sets the device error word (PQ2_ERR_INVALID_ARG from
+ * pq2_last_device_error); a page past the pool leaves q alone to be written.
+ * Two tokens of one call must not have the same place in the cache.
+ * flags: 0 or PQ2_ROPE_NEIGHBOURS.  M: rows of the arrays, 0 <= M <= 2^24.
+ */
+typedef struct pq2_cache4_append_args {
+    pq2_cache4 cache;
+    const void *k, *v, *q;
+    void* q_out;
+    const float* table;
+    const int32_t* positions;
+    int64_t ld_k, hs_k, ld_v, hs_v, ld_q, hs_q, ld_q_out, hs_q_out;
+    int64_t M, table_rows;
+    int32_t q_heads, rot, x_type, out_type;
+    uint32_t flags;
+    int32_t reserved; /* 0 */
+} pq2_cache4_append_args;
+pq2_status pq2_cache4_append(const pq2_cache4_append_args* args, void* stream);
+
+/*
+ * pq2_cache4_read -- the values that the cache holds for the call's token rows
+ * (code * scale + offset in fp32, rounded once): k_out, v_out [M, heads, dim]
+ * (out_type; either may be NULL).  Rows without a place in the cache are
+ * skipped as in pq2_cache4_append.
+ */
+typedef struct pq2_cache4_read_args {
+    pq2_cache4 cache;
+    void *k_out, *v_out;
+    int64_t ld_k, hs_k, ld_v, hs_v;
+    int64_t M;
+    int32_t out_type, reserved; /* 0 */
+} pq2_cache4_read_args;
+pq2_status pq2_cache4_read(const pq2_cache4_read_args* args, void* stream);
+
+/*
+ * pq2_cache4_attend -- attention of the call's token rows over the cache:
+ *   out[m, h] = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q[m, h] . k_j)
+ * over the positions j <= p(m) of its sequence, p(m) - window < j where window > 0; k and
+ * v of key/value head h / (q_heads / heads).  The new tokens' keys and values
+ * have to be in the cache (pq2_cache4_append).  A row that sees nothing (its position
+ * below 0) gives zeros.  Scores, maxima, sums and accumulated outputs are
+ * fp32; q enters the products with the 11 bits of its type or the fp16 rounding of its
+ * row scaled by a power of two (bf16: no rounding within 2^28 of the row's
+ * largest), the weights w times the values' scales as fp16, scaled by powers
+ * of two likewise.
+ *   q, out     [M, q_heads, dim] (type: PQ2_F16 or PQ2_BF16), token and head
+ *              strides in elements, a head's values adjacent
+ *   max_rows   an upper bound of the sequences' rows that the host knows
+ *              (1 in a decode step), or 0 (M); it chooses the kernels and is
+ *              part of the contract: a sequence with more rows gets none of
+ *              them (and sets the device error word)
+ *   workspace  pq2_cache4_attend_workspace_bytes(M, q_heads, heads, dim) bytes, 16-byte aligned;
+ *              enough for fewer rows too
+ * Pages outside the pool among those that a sequence needs: its rows are
+ * undefined and the device error word is set; lens past W T likewise (nothing behind the
+ * table is read).  NaN or Inf in q: that row and head undefined.
+ * Results do not depend on other sequences' contents, but the order in which a
+ * row's partial sums are joined depends on the sequences' lengths.
+ * M >= 0, B >= 0 (0 enqueues nothing), q_heads % heads == 0, q_heads / heads <= 64,
+ * window >= 0, scale finite; M <= 2^20, M * q_heads <= 2^30.  q and out 16-byte aligned with strides
+ * % 8 == 0.
+ */
+typedef struct pq2_cache4_attend_args {
+    pq2_cache4 cache;
+    const void* q;
+    void *out, *workspace;
+    int64_t ld_q, hs_q, ld_out, hs_out;
+    int64_t M, max_rows, window;
+    size_t workspace_bytes;
+    float scale;
+    int32_t q_heads, type, reserved; /* 0 */
+} pq2_cache4_attend_args;
+size_t pq2_cache4_attend_workspace_bytes(int64_t M, int64_t q_heads, int64_t heads, int64_t dim);
+pq2_status pq2_cache4_attend(const pq2_cache4_attend_args* args, void* stream);
+
+/*
+ * The pages of a cache between two steps.  refs [P] counts each page's
+ * holders: the sequences of the table, and whoever else keeps it (a stored prefix).
+ *
+ * pq2_pages_update -- slot b goes on from slot source[b] (itself, another:
+ * a fork, or < 0: none, the slot is emptied) with the first keep[b] of that
+ * slot's lens[source[b]] tokens, and gets pages for new_lens[b] tokens in all.
+ * With k = min(keep, lens[source], new_lens) (0 without a source), the k / T whole pages are
+ * shared.  A page of which only the first k % T tokens are kept goes on to
+ * the lowest slot that keeps such a part if nobody else holds it (whole, or
+ * from outside the table); every other such slot gets a page and a pair
+ * (old, new) in copies, to be copied before the slot's next append.  Pages
+ * that are wanted are taken in the order of slots and positions, lowest free page first.
+ *   pages       in   int32 [B, W] (row stride ld_pages); lens int32 [B]
+ *   refs        in   int32 [P]
+ *   source, keep, new_lens  in int32 [B]; new_lens <= W T
+ *   pages_out   out  int32 [B, W] (row stride ld_out), -1 behind the last page; not `pages`
+ *   refs_out    out  int32 [P]; may be refs
+ *   copies      out  int32 [B, 2]: slot b's pair, or (-1, -1)
+ *   info        out  int32 [2]: free pages left, pages that were wanted and not there
+ *                    (their entries are -1)
+ * Values out of range (source >= B, keep or lens or new_lens outside [0, W T],
+ * a page outside [0, P) in use) count as the nearest in range (a source past B as none, such a page as
+ * -1, held by nobody) and set the device error word.
+ *   workspace   pq2_pages_workspace_bytes(B, P) bytes, 16-byte aligned
+ * 0 <= B <= 2^20, 1 <= W <= 2^20, B W <= 2^30, 0 <= P <= 2^28, 1 <= T <= 2^20,
+ * W T <= 2^30 (PQ2_ERR_UNSUPPORTED_SHAPE otherwise).
+ */
+typedef struct pq2_pages_update_args {
+    const int32_t *pages, *lens, *refs, *source, *keep, *new_lens;
+    int32_t *pages_out, *refs_out, *copies, *info;
+    void* workspace;
+    int64_t ld_pages, ld_out, B, W, P, T;
+    size_t workspace_bytes;
+} pq2_pages_update_args;
+size_t pq2_pages_workspace_bytes(int64_t B, int64_t P);
+pq2_status pq2_pages_update(const pq2_pages_update_args* args, void* stream);
+
+/*
+ * pq2_pages_compact -- which pages to move so that the n in use (refs > 0) are
+ * pages 0 .. n - 1: the i-th page in use from n on goes to the i-th free one
+ * below n.
+ *   pages, lens, refs  in   as above
+ *   pages_out          out  [B, W]: the same places, moved; -1 behind the last page
+ *   refs_out           out  [P]; may be refs
+ *   copies             out  int32 [P / 2, 2]: the moves (old, new), then (-1, -1)
+ *   info               out  int32 [2]: pages in use, moves
+ * Sizes, workspace and out-of-range values as pq2_pages_update.
+ */
+typedef struct pq2_pages_compact_args {
+    const int32_t *pages, *lens, *refs;
+    int32_t *pages_out, *refs_out, *copies, *info;
+    void* workspace;
+    int64_t ld_pages, ld_out, B, W, P, T;
+    size_t workspace_bytes;
+} pq2_pages_compact_args;
+pq2_status pq2_pages_compact(const pq2_pages_compact_args* args, void* stream);
+
+/*
+ * pq2_pages_copy -- copies pages of a pool within it: for each of the n pairs
+ * (old, new) whose two pages are in [0, P), in each of `layers` pools that lie
+ * layer_stride bytes apart.  Pairs with a negative page are skipped; a page >= P is
+ * skipped too and sets the device error word.  No new page may be another pair's old or new one.
+ *   pool  16-byte aligned; page_bytes, page_stride (>= page_bytes), layer_stride % 16 == 0
+ *   pairs int32 [n, 2], 8-byte aligned
+ * n >= 0 (0 enqueues nothing), n <= 2^28, 0 <= layers <= 65536, P >= 0.
+ */
+pq2_status pq2_pages_copy(void* pool, int64_t page_bytes, int64_t page_stride, int64_t P,
+                          int64_t layers, int64_t layer_stride, const int32_t* pairs, int64_t n,
+                          void* stream);
+
+/*
  * pq2_workspace_bytes -- scratch bytes `op` needs for this shape (0 if none,
  * SIZE_MAX if the shape is not supported).
  */
