@@ -36,6 +36,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 8;            // query rows of a pass
+constexpr int kFewRows = 32;        // rows of a sequence and head that this kernel takes, at most
+constexpr int kExtra = 16;          // what an item takes besides its tiles, in tiles
 constexpr float kEmpty = -1e30f;    // maximum of a row that has seen nothing
 constexpr float kSlack = 2.0f;      // how far (as a power of two) a score may exceed the maximum
 constexpr float kWeight = 4096.0f;  // weights enter the product times this
@@ -411,38 +413,44 @@ __device__ __forceinline__ void segment(const pq2h::AttendParams& p, const Atten
     if (lane == 0 && store_ok(p.ctl, slot * kRows + row, 1, wk.ml_elems)) wk.ml[slot * kRows + row] = make_float2(m, l);
 }
 
-// The list's tiles, dealt out; or (row_tiles > 0) a CTA per sequence, tile of
-// rows and head.
+// The list's tiles, dealt out.
 template <int D>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
     attend_kernel(const __grid_constant__ pq2h::AttendParams p, const __grid_constant__ AttendWork wk, int row_tiles) {
     extern __shared__ __align__(16) float smem[];
     pdl_wait();
     pdl_launch_dependents();
-    const int H = p.cache.heads;
-    if (row_tiles > 0) {
-        const long long items = static_cast<long long>(p.cache.B) * row_tiles * H;
-        for (long long i = blockIdx.x; i < items; i += gridDim.x) {
-            const int h = static_cast<int>(i % H), rt = static_cast<int>(i / H % row_tiles);
-            const int b = static_cast<int>(i / H / row_tiles);
-            const AttendItem it = attend_item<kRows>(p, b, rt, h);
-            if (it.n > 0) segment<D>(p, wk, it, it.tile0, it.tile1, true, 0, smem);
+    // (the walk through the list is thread 0's: in registers of all threads it
+    // would be in the way of the tiles')
+    __shared__ AttendSpan walk;
+    __shared__ AttendStep step;
+    long long u, u1;
+    {
+        AttendSpan span;
+        if (row_tiles == 1)
+            attend_span<kRows>(p, 1, kExtra, 2 * kWarps, span);
+        else
+            attend_span_block<kRows, kWarps>(p, row_tiles, 1, kExtra, 2 * kWarps, span);
+        if (threadIdx.x == 0) {
+            walk = span;
+            wk.join[blockIdx.x] = {0, 0, 0, 0, 0};
         }
-        return;
+        u = span.u0, u1 = span.u1;
     }
-    AttendSpan span;
-    attend_span<kRows>(p, 1, 2 * kWarps, span);
-    AttendJoin join = {0, 0, 0, 0, 0};
-    for (long long u = span.u0; u < span.u1;) {
-        const AttendStep s = attend_step<kRows>(p, 1, span, u);
-        const AttendItem it = attend_item<kRows>(p, s.b, 0, s.head);
-        const int t0 = it.tile0 + s.first, slot = 2 * blockIdx.x + (u == span.u0 ? 0 : 1);
+    for (int n = 0; u < u1; ++n) {
+        __syncthreads();
+        if (threadIdx.x == 0) step = attend_step<kRows>(p, row_tiles, 1, kExtra, walk, u);
+        __syncthreads();
+        const AttendStep s = step;
+        u += s.units;
+        if (s.count == 0) continue;
+        const AttendItem it = attend_item<kRows>(p, s.b, s.row_tile, s.head);
+        const int t0 = it.tile0 + s.first, slot = 2 * blockIdx.x + (n > 0);
+        if (threadIdx.x == 0 && s.first == 0 && s.count < s.of)
+            wk.join[blockIdx.x] = {s.b, s.row_tile, s.head,
+                                   attend_cta_of(walk, s.end - 1) - static_cast<int>(blockIdx.x) + 1, slot};
         segment<D>(p, wk, it, t0, min(t0 + s.count, it.tile1), s.count == s.of, slot, smem);
-        if (s.first == 0 && s.count < s.of)
-            join = {s.b, 0, s.head, attend_cta_of(span, u + s.of - 1) - static_cast<int>(blockIdx.x) + 1, slot};
-        u += s.count;
     }
-    if (threadIdx.x == 0) wk.join[blockIdx.x] = join;
 }
 
 // CTA (c, row): row `row` of the item whose first part is CTA c's.  Each of
@@ -514,15 +522,9 @@ cudaError_t launch_few(const AttendParams& p, const pq2::AttendWork& wk, cudaStr
     const size_t smem = pq2::smem_bytes<D>();
     cudaError_t e = raise_smem(lim, pq2::attend_kernel<D>, smem);
     if (e != cudaSuccess) return e;
-    const int G = p.q_heads / p.cache.heads;
-    const int64_t row_tiles = (static_cast<int64_t>(p.max_rows) * G + pq2::kRows - 1) / pq2::kRows;
+    const int G = p.q_heads / p.cache.heads, row_tiles = (p.max_rows * G + pq2::kRows - 1) / pq2::kRows;
     const int64_t ctas = std::min<int64_t>(dev.num_sms * (D == 256 ? 1 : 2), pq2::kAttendCtas);
-    if (row_tiles > 1) {
-        const int64_t items = std::min<int64_t>(static_cast<int64_t>(p.cache.B) * row_tiles * p.cache.heads, 1 << 24);
-        return launch(pq2::attend_kernel<D>, dim3(static_cast<unsigned>(items)), dim3(pq2::kThreads), smem, st, true, p,
-                      wk, static_cast<int>(row_tiles));
-    }
-    e = launch(pq2::attend_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(pq2::kThreads), smem, st, true, p, wk, 0);
+    e = launch(pq2::attend_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(pq2::kThreads), smem, st, true, p, wk, row_tiles);
     if (e != cudaSuccess) return e;
     return launch(pq2::attend_join_kernel<D>, dim3(static_cast<unsigned>(ctas), pq2::kRows),
                   dim3(32 * pq2::kJoinWarps), 0, st, true, p, wk);
@@ -531,13 +533,16 @@ cudaError_t launch_few(const AttendParams& p, const pq2::AttendWork& wk, cudaStr
 }  // namespace
 
 size_t attend_workspace_bytes(int64_t M, int64_t q_heads, int64_t heads, int64_t dim) {
-    (void)M, (void)q_heads, (void)heads;
     const size_t rows = 2ull * pq2::kAttendCtas * pq2::kRows;
-    return pad(rows * dim * 4) + pad(rows * 8) + pad(pq2::kAttendCtas * sizeof(pq2::AttendJoin));
+    const size_t few = pad(rows * dim * 4) + pad(rows * 8) + pad(pq2::kAttendCtas * sizeof(pq2::AttendJoin));
+    return M * (q_heads / heads) > pq2::kFewRows ? std::max(few, attend_many_workspace_bytes(M, q_heads, heads, dim)) : few;
 }
 
 cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t st, const DeviceInfo& dev) {
-    pq2::AttendWork wk;
+    const int64_t G = p.q_heads / p.cache.heads;
+    if (p.max_rows * G > pq2::kFewRows) return launch_attend_many(p, workspace, st, dev);
+    pq2::AttendWork wk = {};
+    wk.rows = pq2::kRows;
     uint8_t* w = static_cast<uint8_t*>(workspace);
     const size_t rows = 2ull * pq2::kAttendCtas * pq2::kRows;
     wk.o = reinterpret_cast<float*>(w);

@@ -29,6 +29,7 @@ struct AttendWork {
     float* o;          // [2 CTAs][rows][dim] outputs, not yet divided
     float2* ml;        // [2 CTAs][rows] maximum, sum of weights
     AttendJoin* join;  // [CTAs]
+    int rows;          // of a partial result
     long long o_elems, ml_elems;  // for the bounds-checked build
 };
 
@@ -71,45 +72,58 @@ __device__ __forceinline__ AttendItem attend_item(const pq2h::AttendParams& p, i
 }
 
 // Units of an item: its tiles of `per` times 16 tokens, at least one (an item without
-// any still has outputs to write).
-__device__ __forceinline__ int attend_units(const AttendItem& it, int per) {
+// any still has outputs to write), and before them `extra` for its rows.
+__device__ __forceinline__ int attend_units(const AttendItem& it, int per, int extra) {
     if (it.n == 0) return 0;
     const int n = (it.tile1 + per - 1) / per - it.tile0 / per;
-    return it.tile1 > it.tile0 ? n : 1;
+    return (it.tile1 > it.tile0 ? n : 1) + extra;
 }
 
-// A CTA's part of the list of units (sequence by sequence, head by head), and
-// where a walk through it is.
+// A CTA's part of the list of units, and where a walk through it is.  The
+// list's entries are (sequence, tile of rows), `row_tiles` for every sequence (those
+// that it does not have are empty); an entry's heads follow one another.
 struct AttendSpan {
     long long u0, u1, total;
     int ctas;
-    int b, units;       // a sequence, its units per head
+    int entry, units;   // an entry, its units per head
     long long before;   // units before it
 };
 
-// All threads of the CTA call it (every warp finds the same).  One tile of rows per
-// sequence; at least `least` units go to a CTA.
 template <int ROWS>
-__device__ __forceinline__ void attend_span(const pq2h::AttendParams& p, int per, int least, AttendSpan& s) {
-    const int lane = threadIdx.x & 31, B = p.cache.B, H = p.cache.heads;
-    long long total = 0;
-    for (int b0 = 0; b0 < B; b0 += 32) {
-        int c = 0;
-        if (b0 + lane < B) c = attend_units(attend_item<ROWS>(p, b0 + lane, 0, 0), per);
-        total += __reduce_add_sync(0xffffffffu, c);
-    }
-    total *= H;
+__device__ __forceinline__ int attend_entry_units(const pq2h::AttendParams& p, long long entry, int row_tiles, int per,
+                                                  int extra) {
+    const int b = static_cast<int>(entry / row_tiles);
+    return attend_units(attend_item<ROWS>(p, b, static_cast<int>(entry - static_cast<long long>(b) * row_tiles), 0), per,
+                        extra);
+}
+
+// The CTA's share of `total` units, at least `least` to a CTA (unless there are fewer).
+__device__ __forceinline__ void attend_share(AttendSpan& s, long long total, int least) {
     s.total = total;
-    s.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + least - 1) / least));
+    s.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total / least, 1ll)));
     s.u0 = s.u1 = 0;
-    s.b = 0, s.units = 0, s.before = 0;
+    s.entry = 0, s.units = 0, s.before = 0;
     const int cta = blockIdx.x;
     if (cta >= s.ctas) return;
     s.u0 = cta * total / s.ctas;
     s.u1 = (cta + 1) * total / s.ctas;
+}
+
+// All threads of the CTA call it (every warp finds the same).
+template <int ROWS>
+__device__ __forceinline__ void attend_span(const pq2h::AttendParams& p, int per, int extra, int least, AttendSpan& s) {
+    const int lane = threadIdx.x & 31, B = p.cache.B, H = p.cache.heads;
+    long long total = 0;
     for (int b0 = 0; b0 < B; b0 += 32) {
         int c = 0;
-        if (b0 + lane < B) c = attend_units(attend_item<ROWS>(p, b0 + lane, 0, 0), per);
+        if (b0 + lane < B) c = attend_entry_units<ROWS>(p, b0 + lane, 1, per, extra);
+        total += __reduce_add_sync(0xffffffffu, c);
+    }
+    attend_share(s, total * H, least);
+    if (s.u0 >= s.u1) return;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        int c = 0;
+        if (b0 + lane < B) c = attend_entry_units<ROWS>(p, b0 + lane, 1, per, extra);
         int inc = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -119,7 +133,7 @@ __device__ __forceinline__ void attend_span(const pq2h::AttendParams& p, int per
         const unsigned past = __ballot_sync(0xffffffffu, s.before + static_cast<long long>(inc) * H > s.u0);
         if (past) {
             const int at = __ffs(past) - 1;
-            s.b = b0 + at;
+            s.entry = b0 + at;
             s.units = __shfl_sync(0xffffffffu, c, at);
             s.before += static_cast<long long>(__shfl_sync(0xffffffffu, inc - c, at)) * H;
             return;
@@ -128,26 +142,83 @@ __device__ __forceinline__ void attend_span(const pq2h::AttendParams& p, int per
     }
 }
 
-// The piece of work that begins at unit u: `count` of the `of` units of an
-// item, from its unit `first` on.
+// The same with the work on many entries split over the CTA's warps.
+template <int ROWS, int WARPS>
+__device__ __forceinline__ void attend_span_block(const pq2h::AttendParams& p, int row_tiles, int per, int extra, int least,
+                                                  AttendSpan& s) {
+    __shared__ long long sums[WARPS];
+    __shared__ long long found_before;
+    __shared__ int found_entry, found_units;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, H = p.cache.heads;
+    const long long entries = static_cast<long long>(p.cache.B) * row_tiles;
+    const long long share = (entries + WARPS - 1) / WARPS;
+    const long long e0 = min(warp * share, entries), e1 = min(e0 + share, entries);
+    long long mine = 0;
+    for (long long e = e0; e < e1; e += 32)
+        mine += __reduce_add_sync(0xffffffffu, e + lane < e1 ? attend_entry_units<ROWS>(p, e + lane, row_tiles, per, extra) : 0);
+    if (lane == 0) sums[warp] = mine * H;
+    __syncthreads();
+    long long total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        if (w == warp) before = total;
+        total += sums[w];
+    }
+    attend_share(s, total, least);
+    if (s.u0 >= s.u1) return;  // (all threads alike)
+    if (before <= s.u0 && s.u0 < before + mine * H) {
+        for (long long e = e0; e < e1; e += 32) {
+            const int c = e + lane < e1 ? attend_entry_units<ROWS>(p, e + lane, row_tiles, per, extra) : 0;
+            int inc = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += u;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, before + static_cast<long long>(inc) * H > s.u0);
+            if (past) {
+                if (lane == __ffs(past) - 1) {
+                    found_entry = static_cast<int>(e + lane);
+                    found_units = c;
+                    found_before = before + static_cast<long long>(inc - c) * H;
+                }
+                break;
+            }
+            before += static_cast<long long>(__shfl_sync(0xffffffffu, inc, 31)) * H;
+        }
+    }
+    __syncthreads();
+    s.entry = found_entry;
+    s.units = found_units;
+    s.before = found_before;
+}
+
+// The piece of work that begins at unit u: `units` units of an item, in them
+// `count` of its `of` tiles, from its tile `first` on; `end`: unit behind the item.
 struct AttendStep {
-    int b, head, first, count, of;
+    int b, row_tile, head, first, count, of, units;
+    long long end;
 };
 template <int ROWS>
-__device__ __forceinline__ AttendStep attend_step(const pq2h::AttendParams& p, int per, AttendSpan& s, long long u) {
+__device__ __forceinline__ AttendStep attend_step(const pq2h::AttendParams& p, int row_tiles, int per, int extra,
+                                                  AttendSpan& s, long long u) {
     const int H = p.cache.heads;
     while (u >= s.before + static_cast<long long>(s.units) * H) {
         s.before += static_cast<long long>(s.units) * H;
-        ++s.b;
-        s.units = attend_units(attend_item<ROWS>(p, s.b, 0, 0), per);
+        ++s.entry;
+        s.units = attend_entry_units<ROWS>(p, s.entry, row_tiles, per, extra);
     }
     const long long in = u - s.before;
     AttendStep st;
-    st.b = s.b;
+    st.b = s.entry / row_tiles;
+    st.row_tile = s.entry - st.b * row_tiles;
     st.head = static_cast<int>(in / s.units);
-    st.first = static_cast<int>(in - static_cast<long long>(st.head) * s.units);
-    st.of = s.units;
-    st.count = static_cast<int>(min(static_cast<long long>(s.units - st.first), s.u1 - u));
+    const int at = static_cast<int>(in - static_cast<long long>(st.head) * s.units);
+    st.units = static_cast<int>(min(static_cast<long long>(s.units - at), s.u1 - u));
+    st.first = max(at - extra, 0);
+    st.count = max(at + st.units - extra, 0) - st.first;
+    st.of = s.units - extra;
+    st.end = u - at + s.units;
     return st;
 }
 

@@ -283,6 +283,9 @@ struct AttendParams {
 };
 size_t attend_workspace_bytes(int64_t M, int64_t q_heads, int64_t heads, int64_t dim);
 cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t st, const DeviceInfo& dev);
+// The same for more than 8 query rows per key/value head (pq2_attend_many.cu).
+size_t attend_many_workspace_bytes(int64_t M, int64_t q_heads, int64_t heads, int64_t dim);
+cudaError_t launch_attend_many(const AttendParams& p, void* workspace, cudaStream_t st, const DeviceInfo& dev);
 
 // The pages of a cache between two steps (pq2_pages.cu).
 struct PagesParams {
