@@ -58,7 +58,7 @@ struct Slot {
     float scale[4 * kQuarter];    // of the scores
     float value[4 * kQuarter];    // values' scales
     float offset[4 * kQuarter];   // values' z'
-    long long base[kKeys];        // byte offset of the key's row of key codes in the pool, -1: none
+    long long base[kPer];         // byte offset in the pool of the tiles of 16 keys, -1: none
     float ref;                    // power of two with values' scales below twice it
     int last, two;                // 1: the tile is its segment's last, 2: and the CTA's; more than 128 rows
     int key0;                     // the tile's first key where some row does not see all of it, else -1
@@ -232,9 +232,10 @@ struct Ctl {
             if (__any_sync(0xffffffffu, *stop || i == kPolls)) return false;
         return true;
     }
-    __device__ __forceinline__ bool timed_wait(uint64_t* bar, uint32_t parity) const {
+    // every lane (that `need`s to) its own barrier
+    __device__ __forceinline__ bool timed_wait(uint64_t* bar, uint32_t parity, bool need) const {
         unsigned long long t0 = 0;
-        for (uint32_t i = 0; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++i) {
+        for (uint32_t i = 0; !__all_sync(0xffffffffu, !need || mbar_try_wait(bar, parity)); ++i) {
             if (i % 64 != 63) continue;
             if (t0 == 0) t0 = globaltimer_ns();
             if (__any_sync(0xffffffffu, *stop || globaltimer_ns() - t0 > p.ctl.wait_limit_ns)) {
@@ -312,7 +313,7 @@ __device__ __forceinline__ void factors(const Ctl& k, const AttendWork& wk, int 
                 const int in = key % p.cache.T;
                 const long long tile = page * p.cache.page_stride + head_at +
                                        static_cast<long long>(in / kTileTokens) * tile_bytes(D);
-                base[i] = tile + (in % kTileTokens) * (D / 2);
+                base[i] = tile;
                 const uint8_t* at = p.cache.pool + tile + (in % kTileTokens) * 4;
                 kp[i] = __ldg(reinterpret_cast<const uint32_t*>(at + tile_pairs(D, 0)));
                 vp[i] = __ldg(reinterpret_cast<const uint32_t*>(at + tile_pairs(D, 1)));
@@ -341,7 +342,7 @@ __device__ __forceinline__ void factors(const Ctl& k, const AttendWork& wk, int 
                 slot.scale[at] = s * to_score;
                 slot.value[at] = vs;
                 slot.offset[at] = fmaf(8.0f, vs, __half2float(__ushort_as_half(vp[i] >> 16)));
-                slot.base[key] = base[i];
+                if (lane % kTileTokens == 0) slot.base[key / kTileTokens] = base[i];
             }
             if (lane == 0) {
                 slot.ref = __uint_as_float(__float_as_uint(top) & 0x7f800000u);
@@ -384,23 +385,23 @@ __device__ __forceinline__ uint32_t plain(uint32_t w) {
     return HIGH ? w & 0x00f000f0u : w & 0x000f000fu;
 }
 
-// Four warps expand keys and four values.  They take whole tiles in turn with the
-// products of others, or (256 dims, where there is no room for two tiles) halves: of
-// keys 128 dims, of values 64 keys.  A lane takes 16 bytes (32 codes) at a
-// time and stores four pieces of 16; of the eight lanes of a load's or a store's
-// phase two have the same row and four have neighbouring ones.  So loads take whole
-// sectors of 32 bytes, and stores, swizzled, meet every bank once without a different
-// order for each lane.  The next codes are asked for as soon as these are used.
+// Four warps expand keys and four values, in pieces: whole tiles, or (256 dims, where there is
+// no room for two) halves: of keys 128 dims, of values 64 keys.  A lane takes 16
+// bytes (32 codes) at a time and stores four pieces of 16; of the eight lanes of a
+// load's or a store's phase two have the same row and four have neighbouring ones.  So
+// loads take whole sectors of 32 bytes, and stores, swizzled, meet every bank once
+// without a different order for each lane.  The next codes are asked for as soon as
+// these are used.
 template <int D, bool VALUES>
 __device__ __forceinline__ void expand(const Ctl& k, const Slot* slots, uint8_t* smem, int warp) {
     using C = Cfg<D>;
-    constexpr int kDims = VALUES ? D : D / C::kHalves;          // of a row of a piece
-    constexpr int kRows = VALUES ? kKeys / C::kHalves : kKeys;  // rows of a piece
-    constexpr int kRowsAtOnce = 1024 / kDims, kLoads = kRows / 4 / kRowsAtOnce;
+    constexpr int kDims = VALUES ? D : D / C::kHalves;              // of a row of a piece
+    constexpr int kRows = (VALUES ? kKeys / C::kHalves : kKeys) / 4;  // of a piece for the warp
+    constexpr int kRowsAtOnce = 1024 / kDims, kLoads = kRows / kRowsAtOnce;
     const int lane = threadIdx.x & 31, phase = lane >> 3;
     const int j = (lane & 1) + 2 * (kDims == 256 ? phase : kDims == 128 ? phase & 1 : 0);
-    const int row0 = kRows / 4 * warp + ((lane >> 1) & 3) + 4 * (kDims == 256 ? 0 : kDims == 128 ? phase >> 1 : phase);
-    const uint8_t* pool = k.p.cache.pool + (VALUES ? tile_codes(D, 1) : 0) + 16 * j;
+    const int in16 = ((lane >> 1) & 3) + 4 * (kDims == 256 ? 0 : kDims == 128 ? phase >> 1 : phase);
+    const int row0 = kRows * warp + in16;
     const int skip = VALUES ? -1 : k.p.ctl.debug_skip_stage;
     // where the lane's rows are in a piece (its 64 dims are block j / 2), and its
     // 16 bytes in a row: with 4 rows at a time every other row has the other half's
@@ -409,34 +410,48 @@ __device__ __forceinline__ void expand(const Ctl& k, const Slot* slots, uint8_t*
         VALUES ? (row0 / C::kPartKeys) * kChunk + (j >> 1) * (C::kPartKeys * 128) + (row0 % C::kPartKeys) * 128
                : (j >> 1) * kChunk + row0 * 128;
     const uint32_t at = (((j & 1) * 4) ^ (row0 & 7)) << 4;
+    // piece e: half e % kHalves of tile e / kHalves; the warp's rows lie in kGroups tiles
+    // of 16 (what is behind the last token is read too: any codes will do)
+    constexpr int kGroups = kRows / kTileTokens;
+    const uint8_t* pool = k.p.cache.pool + (VALUES ? tile_codes(D, 1) : 0) + 16 * j + in16 * (D / 2);
     uint4 raw[kLoads];
-    // piece e: half e % kHalves of tile e / kHalves
-    const auto load = [&](uint32_t e, int i) {
+    long long base[kGroups];
+    bool ends = false;  // whether the piece is the CTA's last
+    const auto places = [&](uint32_t e) {
         const uint32_t half = e % C::kHalves;
-        const long long base = slots[e / C::kHalves % kSlots].base[(VALUES ? half * kRows : 0) + row0 + kRowsAtOnce * i];
-        raw[i] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // codes 8
-        if (base >= 0) raw[i] = __ldg(reinterpret_cast<const uint4*>(pool + (VALUES ? 0 : half * (kDims / 2)) + base));
+        const int group = kGroups * warp + (VALUES ? half * (4 * kGroups) : 0);
+#pragma unroll
+        for (int x = 0; x < kGroups; ++x) {
+            base[x] = slots[e / C::kHalves % kSlots].base[group + x];
+            if (!VALUES && C::kHalves == 2 && base[x] >= 0) base[x] += half * (kDims / 2);
+        }
+        ends = half == C::kHalves - 1 && slots[e / C::kHalves % kSlots].last == 2;
     };
-    // once a piece's codes have been asked for; true: the CTA's last piece
-    const auto loaded = [&](uint32_t e) {
-        if (e % C::kHalves != C::kHalves - 1) return false;
-        const uint32_t n = e / C::kHalves;
-        const bool ends = slots[n % kSlots].last == 2;
+    const auto load = [&](int i) {
+        const long long from = base[kRowsAtOnce * i / kTileTokens];
+        raw[i] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // codes 8
+        if (from >= 0) raw[i] = __ldg(reinterpret_cast<const uint4*>(pool + from + kRowsAtOnce * i % kTileTokens * (D / 2)));
+    };
+    // once a piece's codes have been asked for
+    const auto give_back = [&](uint32_t e) {
+        if (e % C::kHalves != C::kHalves - 1) return;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&k.bars.slot_empty[n % kSlots]);
-        return ends;
+        if (lane == 0) mbar_arrive(&k.bars.slot_empty[e / C::kHalves % kSlots]);
     };
     if (!k.warp_wait(&k.bars.slot_full[0], 0)) return;
+    places(0);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) load(0, i);
-    bool ends = loaded(0);
+    for (int i = 0; i < kLoads; ++i) load(i);
+    give_back(0);
 #pragma unroll 1
     for (uint32_t e = 0;; ++e) {
         const uint32_t buf = e & 1, next = (e + 1) / C::kHalves;  // (the next piece's tile)
         const bool more = !ends;
-        if (e >= 2 && !k.warp_wait(&k.bars.empty[VALUES][buf], (e / 2 - 1) & 1)) return;
-        // (the next tile's factors may have to wait for this tile's products)
+        // a lane looks whether the next tile's factors are there (they may have to wait for this
+        // tile's products), the others wait for the buffer
         const bool early = more && __all_sync(0xffffffffu, mbar_test_wait(&k.bars.slot_full[next % kSlots], (next / kSlots) & 1));
+        if (early) places(e + 1);
+        if (e >= 2 && !k.warp_wait(&k.bars.empty[VALUES][buf], (e / 2 - 1) & 1)) return;
         uint8_t* to = smem + (VALUES ? C::kValuesAt : C::kKeysAt) + buf * C::kPieceBytes + row_at;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
@@ -450,7 +465,7 @@ __device__ __forceinline__ void expand(const Ctl& k, const Slot* slots, uint8_t*
                     VALUES ? make_uint4(centred<0>(w[x]), centred<1>(w[x]), centred<0>(w8), centred<1>(w8))
                            : make_uint4(plain<0>(w[x]), plain<1>(w[x]), plain<0>(w8), plain<1>(w8));
             }
-            if (early) load(e + 1, i);
+            if (early) load(i);
         }
         fence_async();
         __syncwarp();
@@ -458,125 +473,128 @@ __device__ __forceinline__ void expand(const Ctl& k, const Slot* slots, uint8_t*
         if (!more) return;
         if (!early) {
             if (!k.warp_wait(&k.bars.slot_full[next % kSlots], (next / kSlots) & 1)) return;
+            places(e + 1);
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) load(e + 1, i);
+            for (int i = 0; i < kLoads; ++i) load(i);
         }
-        ends = loaded(e + 1);
+        give_back(e + 1);
     }
 }
 
 // ---------------------------------------------------------------------------
 // Warp 12: the products (one thread)
 // ---------------------------------------------------------------------------
+// A wait of a barrier that is ready takes some 300 cycles while the expanding warps keep
+// shared memory busy, and the tensor cores run dry meanwhile: all that a step
+// needs is waited for at once, a barrier a lane.
 template <int D>
 struct Issue {
     using C = Cfg<D>;
     const Ctl& k;
     const Slot* slots;
     uint32_t smem;
-    uint32_t weights;     // parity of the weights' next phase, bit 2 * warpgroup + buffer
+    uint32_t weights;  // parity of the weights' next phase, bit 2 * warpgroup + buffer
 
-    // Scores of accumulator t with tile n's keys.  The first accumulator waits
-    // for the keys, the last one gives them back.
-    __device__ __forceinline__ bool keys(int t, uint32_t n, bool last, bool alone) {
-        const int buf = alone ? n & 1 : t;
+    // Waits for what is asked for: keys of tile m, values of tile n, weights of
+    // the warpgroups in `from` in buffer buf, the queries of segment seg.
+    __device__ __forceinline__ bool wait(bool keys, uint32_t m, bool values, uint32_t n, uint32_t from, uint32_t buf,
+                                         bool queries, uint32_t seg) {
+        const uint32_t lane = threadIdx.x & 31, i = lane & 1;
+        const uint32_t e = (lane < 2 ? m : n) * C::kHalves + i;  // a piece of keys (lanes 0, 1) or values (2, 3)
+        uint64_t* bar = &k.bars.full[lane >> 1 & 1][e & 1];
+        uint32_t parity = e >> 1 & 1;
+        bool need = lane < 2 ? keys && i < C::kHalves : lane < 4 && values && i < C::kHalves;
+        if (lane == 4 || lane == 5) {
+            bar = &k.bars.p_full[i][buf];
+            parity = weights >> (2 * i + buf) & 1;
+            need = from >> i & 1;
+        }
+        if (lane == 6) bar = &k.bars.q_full, parity = seg & 1, need = queries;
+        weights ^= (from & 1) << buf | (from >> 1) << (2 + buf);
+        if (!k.timed_wait(bar, parity, need)) return false;
+        tc_after();
+        return true;
+    }
+    // Scores of accumulator t with tile n's keys; `last`: the last use of these.
+    __device__ __forceinline__ void keys(int t, uint32_t n, uint32_t buf, bool last) {
         const uint32_t zeros = smem + static_cast<uint32_t>(C::kZeroAt);
         const uint32_t aug_q = smem + static_cast<uint32_t>(C::kAugAt) + t * 2048;
         const uint32_t aug_k = smem + static_cast<uint32_t>(C::kSlotAt + (n % kSlots) * sizeof(Slot));
+        // (halves: of every tile the first is in the first buffer)
+        const uint32_t in = C::kHalves == 2 ? 0 : n & 1;
         const uint32_t d = uniform(256 + buf * 128);
+        const uint32_t a = uniform(desc_lo(smem + t * C::kParts * kChunk, 16));
+        const uint32_t b = uniform(desc_lo(smem + static_cast<uint32_t>(C::kKeysAt + in * C::kPieceBytes), 16));
         const uint32_t qa = uniform(desc_lo(aug_q, zeros - aug_q)), ka = uniform(desc_lo(aug_k, zeros - aug_k));
-#pragma unroll 1
-        for (int half = 0; half < C::kHalves; ++half) {
-            const uint32_t e = n * C::kHalves + half, in = e & 1;
-            if (t == 0) {
-                if (!k.timed_wait(&k.bars.full[0][in], (e >> 1) & 1)) return false;
-                tc_after();
-            }
-            const uint32_t a = uniform(desc_lo(smem + (t * C::kParts + half * C::kPieceParts) * kChunk, 16));
-            const uint32_t b = uniform(desc_lo(smem + static_cast<uint32_t>(C::kKeysAt + in * C::kPieceBytes), 16));
-            const uint32_t add = uniform(half);
-            if (elect_one()) {
+        if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < C::kPieceParts; ++i)
+            for (int i = 0; i < C::kParts; ++i) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        mma_ss<128, false, kRowsHi>(d, a + (i * kChunk / 16 + 2 * x), b + (i * kChunk / 16 + 2 * x),
-                                                    i > 0 || x > 0 ? 1u : add);
-                if (half == C::kHalves - 1) mma_ss<128, false, kAugHi>(d, qa, ka, 1);
-                if (last) tc_commit(&k.bars.empty[0][in]);
-                if (half == C::kHalves - 1) tc_commit(&k.bars.s_full[buf]);
+                for (int x = 0; x < 4; ++x)
+                    mma_ss<128, false, kRowsHi>(d, a + (i * kChunk / 16 + 2 * x), b + (i * kChunk / 16 + 2 * x),
+                                                i > 0 || x > 0 ? 1u : 0u);
+                if (C::kHalves == 2 && i == C::kPieceParts - 1 && last) tc_commit(&k.bars.empty[0][0]);
             }
+            mma_ss<128, false, kAugHi>(d, qa, ka, 1);
+            if (last) tc_commit(&k.bars.empty[0][C::kHalves == 2 ? 1 : in]);
+            tc_commit(&k.bars.s_full[buf]);
         }
-        return true;
     }
-    // Outputs of accumulator t with tile n's values.
-    __device__ __forceinline__ bool values(int t, uint32_t n, bool first, bool last, bool alone, bool ends) {
-        const int buf = alone ? n & 1 : t;
-        // alone: each warpgroup has written half of the rows
-        for (int wg = alone ? 0 : t; wg < (alone ? 2 : t + 1); ++wg) {
-            if (!k.timed_wait(&k.bars.p_full[wg][buf], (weights >> (2 * wg + buf)) & 1)) return false;
-            weights ^= 1u << (2 * wg + buf);
-        }
-        const uint32_t d = uniform(t * D);
-#pragma unroll 1
-        for (int half = 0; half < C::kHalves; ++half) {
-            const uint32_t e = n * C::kHalves + half, in = e & 1;
-            if (t == 0 && !k.timed_wait(&k.bars.full[1][in], (e >> 1) & 1)) return false;
-            tc_after();
-            const uint32_t a = uniform(256 + buf * 128 + half * (kKeys / 4)), add = uniform(first && half == 0 ? 0u : 1u);
-            const uint32_t b = uniform(desc_lo(smem + static_cast<uint32_t>(C::kValuesAt + in * C::kPieceBytes), C::kPartKeys * 128));
-            if (elect_one()) {
+    // Outputs of accumulator t with tile n's values and the weights in buffer buf.
+    __device__ __forceinline__ void values(int t, uint32_t n, uint32_t buf, bool first, bool last, bool ends) {
+        const uint32_t in = C::kHalves == 2 ? 0 : n & 1;
+        const uint32_t d = uniform(t * D), a = uniform(256 + buf * 128), add = uniform(first ? 0u : 1u);
+        const uint32_t b = uniform(desc_lo(smem + static_cast<uint32_t>(C::kValuesAt + in * C::kPieceBytes), C::kPartKeys * 128));
+        if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < C::kPieceParts; ++i)
+            for (int i = 0; i < C::kParts; ++i) {
 #pragma unroll
-                    for (int x = 0; x < C::kPartKeys / 16; ++x)
-                        mma_ts<D, true, kRowsHi>(d, a + (i * C::kPartKeys + 16 * x) / 2, b + (i * kChunk / 16 + 128 * x),
-                                                 i > 0 || x > 0 ? 1u : add);
-                if (last) tc_commit(&k.bars.empty[1][in]);
-                if (half == C::kHalves - 1) {
-                    tc_commit(&k.bars.pv_done[t]);
-                    if (ends) tc_commit(&k.bars.out_full[t]);
-                }
+                for (int x = 0; x < C::kPartKeys / 16; ++x)
+                    mma_ts<D, true, kRowsHi>(d, a + (i * C::kPartKeys + 16 * x) / 2, b + (i * kChunk / 16 + 128 * x),
+                                             i > 0 || x > 0 ? 1u : add);
+                if (C::kHalves == 2 && i == C::kPieceParts - 1 && last) tc_commit(&k.bars.empty[1][0]);
             }
+            if (last) tc_commit(&k.bars.empty[1][C::kHalves == 2 ? 1 : in]);
+            tc_commit(&k.bars.pv_done[t]);
+            if (ends) tc_commit(&k.bars.out_full[t]);
         }
-        return true;
-    }
-    __device__ __forceinline__ bool slot(uint32_t n) const {
-        return k.timed_wait(&k.bars.slot_full[n % kSlots], (n / kSlots) & 1);
     }
     __device__ __forceinline__ void run() {
         uint32_t seg = 0, n = 0;
 #pragma unroll 1
         for (int last = 0; last != 2; ++seg) {
             // a segment: from tile n to the one that says it is the last
-            if (!slot(n)) return;
+            if (!k.timed_wait(&k.bars.slot_full[n % kSlots], (n / kSlots) & 1, true)) return;
             const int acc = C::kTiles == 2 && slots[n % kSlots].two ? 2 : 1;
             const bool alone = acc == 1;
-            if (!k.timed_wait(&k.bars.q_full, seg & 1)) return;
-            tc_after();
             bool first = true;
             int next_last = 0;
             last = slots[n % kSlots].last;
-            // one pass more than tiles: scores of tile n + 1 behind outputs of tile n
+            // one pass more than tiles: scores of tile m = n + 1 behind outputs of tile n
             // (before them with one accumulator, which has both buffers of scores)
             bool primed = false;
 #pragma unroll 1
             for (;;) {
                 const bool more = !primed || !last;
                 const uint32_t m = primed ? n + 1 : n;
-                if (primed && more) {
-                    // (the last tile's slot may be another's by the time of its values)
-                    if (!slot(m)) return;
-                    next_last = slots[m % kSlots].last;
-                }
-                // (alone: keys before values)
 #pragma unroll 1
                 for (int o = 0; o < 2 * acc; ++o) {
                     const int t = alone ? 0 : o >> 1;
-                    if (alone ? o == 0 : o & 1) {
-                        if (more && !keys(t, m, t == acc - 1, alone)) return;
-                    } else if (primed && !values(t, n, first, t == acc - 1, alone, last)) {
-                        return;
+                    const bool is_keys = alone ? o == 0 : o & 1;
+                    const uint32_t buf = alone ? (is_keys ? m : n) & 1 : t;
+                    // alone: a wait for each product (a warpgroup has written half of the
+                    // weights); else one for both
+                    const bool k_here = more && (alone ? is_keys : o == 0), v_here = primed && (alone ? !is_keys : o == 0);
+                    const uint32_t from = !primed || is_keys ? 0 : alone ? 3 : 1u << t;
+                    if (k_here || from != 0) {
+                        if (!wait(k_here, m, v_here, n, from, buf, k_here && !primed, seg)) return;
+                        // (the last tile's slot may be another's by the time of its values)
+                        if (k_here && primed) next_last = slots[m % kSlots].last;
+                    }
+                    if (is_keys) {
+                        if (more) keys(t, m, buf, t == acc - 1);
+                    } else if (primed) {
+                        values(t, n, buf, first, t == acc - 1, last);
                     }
                 }
                 if (primed) {
