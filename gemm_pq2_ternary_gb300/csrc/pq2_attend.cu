@@ -102,14 +102,20 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t* p) {
 }
 
 template <int D>
-__device__ __forceinline__ void load_tile(Tile<D>& x, const uint8_t* tile, int g, int t) {
-    const int kg = key_of(g);
+__device__ __forceinline__ void load_keys(Tile<D>& x, const uint8_t* tile, int g, int t) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) load_words(x.k[r], tile + (key_of(g) + 8 * r) * (D / 2) + t * (D / 8));
+}
+template <int D>
+__device__ __forceinline__ void load_pairs(Tile<D>& x, const uint8_t* tile, int g) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        load_words(x.k[r], tile + (kg + 8 * r) * (D / 2) + t * (D / 8));
-        x.kp[r] = __ldg(reinterpret_cast<const uint32_t*>(tile + tile_pairs(D, 0)) + kg + 8 * r);
-        x.vp[r] = __ldg(reinterpret_cast<const uint32_t*>(tile + tile_pairs(D, 1)) + kg + 8 * r);
+        x.kp[r] = __ldg(reinterpret_cast<const uint32_t*>(tile + tile_pairs(D, 0)) + key_of(g) + 8 * r);
+        x.vp[r] = __ldg(reinterpret_cast<const uint32_t*>(tile + tile_pairs(D, 1)) + key_of(g) + 8 * r);
     }
+}
+template <int D>
+__device__ __forceinline__ void load_values(Tile<D>& x, const uint8_t* tile, int g, int t) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) load_words(x.v[r], tile + tile_codes(D, 1) + (t + 4 * r) * (D / 2) + g * (D / 16));
 }
@@ -121,7 +127,6 @@ __device__ __forceinline__ float pair_offset(uint32_t p) { return __half2float(_
 // queries: a lane has rows 2t and 2t + 1 of maxima, sums and outputs.
 template <int D>
 struct Rows {
-    uint32_t q[D / 32][4];  // as products' operands
     float fq[2], sq[2];     // factor of the products, sum of the row (both in powers of two: times log2 e)
     int first[2], last[2];  // positions that the row sees
     float m[2], l[2], z[2]; // maximum, sum of weights, sum of weights times offsets
@@ -140,9 +145,11 @@ __device__ __forceinline__ void clear(Rows<D>& r) {
         for (int i = 0; i < 4; ++i) r.o[j][i] = 0.0f;
 }
 
-// The query rows of item `it`: lane (g, t) loads quarter t of row g.
+// The query rows of item `it`: lane (g, t) loads quarter t of row g.  `q`: the
+// lane's place for the products' operands (in shared memory: in registers they would be spilled).
 template <int D>
-__device__ __forceinline__ void load_rows(Rows<D>& r, const pq2h::AttendParams& p, const AttendItem& it, int g, int t) {
+__device__ __forceinline__ void load_rows(Rows<D>& r, uint4* q, const pq2h::AttendParams& p, const AttendItem& it, int g,
+                                          int t) {
     const int G = p.q_heads / p.cache.heads;
     const int i = it.row_tile * kRows + g, token = i / G;
     const bool there = token < it.n;
@@ -182,10 +189,8 @@ __device__ __forceinline__ void load_rows(Rows<D>& r, const pq2h::AttendParams& 
     for (int w = 0; w < D / 32; ++w) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[w][k] *= up;
-        r.q[w][0] = half2_bits(v[w][0], v[w][4]);
-        r.q[w][1] = half2_bits(v[w][1] * 0.0625f, v[w][5] * 0.0625f);
-        r.q[w][2] = half2_bits(v[w][2], v[w][6]);
-        r.q[w][3] = half2_bits(v[w][3] * 0.0625f, v[w][7] * 0.0625f);
+        q[32 * w] = make_uint4(half2_bits(v[w][0], v[w][4]), half2_bits(v[w][1] * 0.0625f, v[w][5] * 0.0625f),
+                               half2_bits(v[w][2], v[w][6]), half2_bits(v[w][3] * 0.0625f, v[w][7] * 0.0625f));
     }
     const float k = p.scale * 1.4426950408889634f;
     const float f = k * 0x1p24f / up, s = k * sum;
@@ -229,17 +234,21 @@ __device__ __forceinline__ void raise(Rows<D>& r, const float (&x)[2][2], const 
     }
 }
 
-// Tokens key0 .. key0 + 15 into the warp's rows.
+// Tokens key0 .. key0 + 15 into the warp's rows; what of the tile has been used makes
+// room for tile `next` (null: there is none).
 template <int D>
-__device__ __forceinline__ void take_tile(Rows<D>& r, const Tile<D>& x, int key0, bool inside, int g) {
+__device__ __forceinline__ void take_tile(Rows<D>& r, const uint4* q, Tile<D>& x, int key0, bool inside,
+                                          const uint8_t* next, int g, int t) {
     float a[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
         const uint32_t k0 = x.k[0][w], k1 = x.k[1][w];
-        mma16816(a[0], k0 & 0x000f000fu, k1 & 0x000f000fu, k0 & 0x00f000f0u, k1 & 0x00f000f0u, r.q[w][0], r.q[w][1]);
+        const uint4 b = q[32 * w];
+        mma16816(a[0], k0 & 0x000f000fu, k1 & 0x000f000fu, k0 & 0x00f000f0u, k1 & 0x00f000f0u, b.x, b.y);
         const uint32_t h0 = k0 >> 8, h1 = k1 >> 8;
-        mma16816(a[1], h0 & 0x000f000fu, h1 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x00f000f0u, r.q[w][2], r.q[w][3]);
+        mma16816(a[1], h0 & 0x000f000fu, h1 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x00f000f0u, b.z, b.w);
     }
+    if (next) load_keys<D>(x, next, g, t);
     float y[2][2], s[2], z[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -250,6 +259,7 @@ __device__ __forceinline__ void take_tile(Rows<D>& r, const Tile<D>& x, int key0
         for (int c = 0; c < 2; ++c)
             y[i][c] = fmaf(a[0][2 * i + c] + a[1][2 * i + c], ks * r.fq[c], kz * r.sq[c]);
     }
+    if (next) load_pairs<D>(x, next, g);
     if (!inside) {
         // tokens that a row does not see; what lies behind a sequence's last
         // token may be anything, a NaN included
@@ -295,15 +305,21 @@ __device__ __forceinline__ void take_tile(Rows<D>& r, const Tile<D>& x, int key0
                      b[1]);
         }
     }
+    if (next) load_values<D>(x, next, g, t);
 }
 
 template <int D>
 constexpr int so_row() {
     return D + 4;
 }
+// Floats before the warps' queries.
+template <int D>
+constexpr int q_at() {
+    return kWarps * kRows * (so_row<D>() + 2);
+}
 template <int D>
 constexpr size_t smem_bytes() {
-    return static_cast<size_t>(kWarps) * kRows * (so_row<D>() + 2) * 4;
+    return static_cast<size_t>(q_at<D>()) * 4 + static_cast<size_t>(kWarps) * D * 16;
 }
 
 // The segment of item `it` in tiles [t0, t1): every warp its own tiles, then
@@ -314,7 +330,8 @@ __device__ __forceinline__ void segment(const pq2h::AttendParams& p, const Atten
                                         int t1, bool whole, int slot, float* smem) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     Rows<D> r;
-    load_rows<D>(r, p, it, g, t);
+    uint4* q = reinterpret_cast<uint4*>(smem + q_at<D>()) + warp * D + lane;
+    load_rows<D>(r, q, p, it, g, t);
     clear<D>(r);
     const int per_page = p.cache.T / kTileTokens;
     const long long head_at = static_cast<long long>(it.head) * per_page * tile_bytes(D);
@@ -341,26 +358,33 @@ __device__ __forceinline__ void segment(const pq2h::AttendParams& p, const Atten
         return p.cache.pool + page * p.cache.page_stride + head_at +
                static_cast<long long>(tile % per_page) * tile_bytes(D);
     };
-    Tile<D> x[2];
-    const uint8_t* from[2] = {nullptr, nullptr};
-    const auto fetch = [&](int b, int i) {
-        if (i >= mine) return;
-        if ((i & 31) == 0) look_up(i);
-        from[b] = place(i);
-        if (from[b]) load_tile<D>(x[b], from[b], g, t);
-    };
-    const auto take = [&](int b, int i) {
-        if (i >= mine || !from[b]) return;
-        const int key0 = (t0 + warp + kWarps * i) * kTileTokens;
-        take_tile<D>(r, x[b], key0, key0 >= in0 && key0 + kTileTokens - 1 <= in1, g);
-    };
-    fetch(0, 0);
-    fetch(1, 1);
-    for (int i = 0; i < mine; i += 2) {
-        take(0, i);
-        fetch(0, i + 2);
-        take(1, i + 1);
-        fetch(1, i + 3);
+    Tile<D> x;
+    const uint8_t* from = nullptr;
+    if (mine > 0) {
+        look_up(0);
+        from = place(0);
+    }
+    if (from) {
+        load_keys<D>(x, from, g, t);
+        load_pairs<D>(x, from, g);
+        load_values<D>(x, from, g, t);
+    }
+#pragma unroll 1
+    for (int i = 0; i < mine; ++i) {
+        const uint8_t* next = nullptr;
+        if (i + 1 < mine) {
+            if (((i + 1) & 31) == 0) look_up(i + 1);
+            next = place(i + 1);
+        }
+        if (from) {
+            const int key0 = (t0 + warp + kWarps * i) * kTileTokens;
+            take_tile<D>(r, q, x, key0, key0 >= in0 && key0 + kTileTokens - 1 <= in1, next, g, t);
+        } else if (next) {
+            load_keys<D>(x, next, g, t);
+            load_pairs<D>(x, next, g);
+            load_values<D>(x, next, g, t);
+        }
+        from = next;
     }
     // the warps' results: [warp][row][D] with maxima and sums behind them
     float* so = smem;
