@@ -19,7 +19,7 @@
 // A warp takes tiles of 16 tokens straight from memory into registers,
 // two tiles ahead, with a maximum, sums and outputs of its own.  Maxima are
 // raised only when a score exceeds the present one by 2^kSlack (a vote, not a
-// reduction per tile): weights stay below 4, and times the values' scales (over a
+// reduction per tile): weights stay below 32, and times the values' scales (over a
 // power of two, raised likewise, below 2) times kWeight below 2^15, with 2^-26
 // of the largest still at fp16's full precision.
 //
@@ -33,14 +33,17 @@
 namespace pq2 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+// Warps of a CTA and CTAs of an SM: as many as registers allow.
+template <int D>
+constexpr int kWarps = D == 256 ? 12 : 8;
+template <int D>
+constexpr int kBlocks = D == 256 ? 1 : 2;
 constexpr int kRows = 8;            // query rows of a pass
 constexpr int kFewRows = 32;        // rows of a sequence and head that this kernel takes, at most
 constexpr int kExtra = 16;          // what an item takes besides its tiles, in tiles
 constexpr float kEmpty = -1e30f;    // maximum of a row that has seen nothing
-constexpr float kSlack = 2.0f;      // how far (as a power of two) a score may exceed the maximum
-constexpr float kWeight = 4096.0f;  // weights enter the product times this
+constexpr float kSlack = 5.0f;      // how far (as a power of two) a score may exceed the maximum
+constexpr float kWeight = 512.0f;  // weights enter the product times this
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -72,52 +75,27 @@ __device__ __forceinline__ uint32_t centred(uint32_t w) {
     return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-// One tile as a lane (g, t) = (lane / 4, lane % 4) holds it.  The token in
-// place r of the products' 16 is key_of(r), so that each load of a warp covers whole lines: keys of
-// places g and g + 8 (a quarter t of each row), values of places 2t, 2t + 1,
-// 2t + 8, 2t + 9 (an eighth g of each).
-__device__ __forceinline__ int key_of(int place) { return (place & 8) + ((place & 7) >> 1) + 4 * (place & 1); }
-
-template <int D>
-struct Tile {
-    uint32_t k[2][D / 32];
-    uint32_t v[4][D / 64];
-    uint32_t kp[2], vp[2];  // (scale, offset) of places g and g + 8
-};
+// One tile as a lane (g, t) = (lane / 4, lane % 4) takes it from shared memory: keys
+// of places g and g + 8 of the products' 16 (a quarter t of each row), values of
+// places 2t, 2t + 1, 2t + 8, 2t + 9 (an eighth g of each).  The token in a place:
+// of two neighbouring places one is odd, of four values taken at once two are, so that
+// with rows of 64 bytes keys meet every bank once and values twice.
+__device__ __forceinline__ int key_of(int place) { return place ^ ((place >> 1) & 1); }
 
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t* p) {
     if constexpr (N == 1) {
-        w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
     } else if constexpr (N == 2) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
         w[0] = u.x, w[1] = u.y;
     } else {
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+            const uint4 u = *(reinterpret_cast<const uint4*>(p) + i);
             w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
         }
     }
-}
-
-template <int D>
-__device__ __forceinline__ void load_keys(Tile<D>& x, const uint8_t* tile, int g, int t) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) load_words(x.k[r], tile + (key_of(g) + 8 * r) * (D / 2) + t * (D / 8));
-}
-template <int D>
-__device__ __forceinline__ void load_pairs(Tile<D>& x, const uint8_t* tile, int g) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        x.kp[r] = __ldg(reinterpret_cast<const uint32_t*>(tile + tile_pairs(D, 0)) + key_of(g) + 8 * r);
-        x.vp[r] = __ldg(reinterpret_cast<const uint32_t*>(tile + tile_pairs(D, 1)) + key_of(g) + 8 * r);
-    }
-}
-template <int D>
-__device__ __forceinline__ void load_values(Tile<D>& x, const uint8_t* tile, int g, int t) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) load_words(x.v[r], tile + tile_codes(D, 1) + (t + 4 * r) * (D / 2) + g * (D / 16));
 }
 
 __device__ __forceinline__ float pair_scale(uint32_t p) { return __half2float(__ushort_as_half(p & 0xffffu)); }
@@ -127,11 +105,18 @@ __device__ __forceinline__ float pair_offset(uint32_t p) { return __half2float(_
 // queries: a lane has rows 2t and 2t + 1 of maxima, sums and outputs.
 template <int D>
 struct Rows {
+    uint4 q[D <= 128 ? D / 32 : 1];  // as products' operands; of 256 dims they stay in shared memory
     float fq[2], sq[2];     // factor of the products, sum of the row (both in powers of two: times log2 e)
     int first[2], last[2];  // positions that the row sees
     float m[2], l[2], z[2]; // maximum, sum of weights, sum of weights times offsets
     float ref;              // values' scales over this (a power of two) are below 2
     float o[D / 16][4];     // outputs: dims 2j and 2j + 1 (times 16) of the lane's eighth
+    __device__ __forceinline__ uint4 query(const uint4* shared, int w) const {
+        if constexpr (D <= 128)
+            return q[w];
+        else
+            return shared[32 * w];
+    }
 };
 
 template <int D>
@@ -146,7 +131,7 @@ __device__ __forceinline__ void clear(Rows<D>& r) {
 }
 
 // The query rows of item `it`: lane (g, t) loads quarter t of row g.  `q`: the
-// lane's place for the products' operands (in shared memory: in registers they would be spilled).
+// lane's place for those of 256 dims.
 template <int D>
 __device__ __forceinline__ void load_rows(Rows<D>& r, uint4* q, const pq2h::AttendParams& p, const AttendItem& it, int g,
                                           int t) {
@@ -189,8 +174,12 @@ __device__ __forceinline__ void load_rows(Rows<D>& r, uint4* q, const pq2h::Atte
     for (int w = 0; w < D / 32; ++w) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[w][k] *= up;
-        q[32 * w] = make_uint4(half2_bits(v[w][0], v[w][4]), half2_bits(v[w][1] * 0.0625f, v[w][5] * 0.0625f),
-                               half2_bits(v[w][2], v[w][6]), half2_bits(v[w][3] * 0.0625f, v[w][7] * 0.0625f));
+        const uint4 b = make_uint4(half2_bits(v[w][0], v[w][4]), half2_bits(v[w][1] * 0.0625f, v[w][5] * 0.0625f),
+                                   half2_bits(v[w][2], v[w][6]), half2_bits(v[w][3] * 0.0625f, v[w][7] * 0.0625f));
+        if constexpr (D <= 128)
+            r.q[w] = b;
+        else if (threadIdx.x < 32)  // (all warps have the same)
+            q[32 * w] = b;
     }
     const float k = p.scale * 1.4426950408889634f;
     const float f = k * 0x1p24f / up, s = k * sum;
@@ -204,6 +193,9 @@ __device__ __forceinline__ void load_rows(Rows<D>& r, uint4* q, const pq2h::Atte
         r.first[c] = p.window > 0 ? r.last[c] - p.window + 1 : 0;
     }
 }
+
+// 1 / x of a power of two.
+__device__ __forceinline__ float inverse(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 
 // Raises maxima and the values' reference where this tile needs it.
 template <int D>
@@ -224,7 +216,7 @@ __device__ __forceinline__ void raise(Rows<D>& r, const float (&x)[2][2], const 
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
     ref = __uint_as_float(__float_as_uint(ref) & 0x7f800000u);
-    const float down = r.ref / ref;
+    const float down = r.ref * inverse(ref);
     r.ref = ref;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -234,32 +226,44 @@ __device__ __forceinline__ void raise(Rows<D>& r, const float (&x)[2][2], const 
     }
 }
 
-// Tokens key0 .. key0 + 15 into the warp's rows; what of the tile has been used makes
-// room for tile `next` (null: there is none).
+// Tokens key0 .. key0 + 15, in shared memory, into the warp's rows.
 template <int D>
-__device__ __forceinline__ void take_tile(Rows<D>& r, const uint4* q, Tile<D>& x, int key0, bool inside,
-                                          const uint8_t* next, int g, int t) {
+__device__ __forceinline__ void take_tile(Rows<D>& r, const uint4* q, const uint8_t* tile, int key0, bool inside, int g,
+                                          int t) {
+    uint32_t k[2][D / 32], kp[2], vp[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int key = key_of(g) + 8 * i;
+        load_words(k[i], tile + key * (D / 2) + t * (D / 8));
+        kp[i] = reinterpret_cast<const uint32_t*>(tile + tile_pairs(D, 0))[key];
+        vp[i] = reinterpret_cast<const uint32_t*>(tile + tile_pairs(D, 1))[key];
+    }
     float a[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
-        const uint32_t k0 = x.k[0][w], k1 = x.k[1][w];
-        const uint4 b = q[32 * w];
+        const uint32_t k0 = k[0][w], k1 = k[1][w];
+        const uint4 b = r.query(q, w);
         mma16816(a[0], k0 & 0x000f000fu, k1 & 0x000f000fu, k0 & 0x00f000f0u, k1 & 0x00f000f0u, b.x, b.y);
         const uint32_t h0 = k0 >> 8, h1 = k1 >> 8;
         mma16816(a[1], h0 & 0x000f000fu, h1 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x00f000f0u, b.z, b.w);
     }
-    if (next) load_keys<D>(x, next, g, t);
+    // (in flight meanwhile)
+    uint32_t v[4][D / 64];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int key = key_of(2 * t + (i & 1) + 8 * (i >> 1));
+        load_words(v[i], tile + tile_codes(D, 1) + key * (D / 2) + g * (D / 16));
+    }
     float y[2][2], s[2], z[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        s[i] = pair_scale(x.vp[i]);
-        z[i] = pair_offset(x.vp[i]);
-        const float ks = pair_scale(x.kp[i]), kz = pair_offset(x.kp[i]);
+        s[i] = pair_scale(vp[i]);
+        z[i] = pair_offset(vp[i]);
+        const float ks = pair_scale(kp[i]), kz = pair_offset(kp[i]);
 #pragma unroll
         for (int c = 0; c < 2; ++c)
             y[i][c] = fmaf(a[0][2 * i + c] + a[1][2 * i + c], ks * r.fq[c], kz * r.sq[c]);
     }
-    if (next) load_pairs<D>(x, next, g);
     if (!inside) {
         // tokens that a row does not see; what lies behind a sequence's last
         // token may be anything, a NaN included
@@ -279,7 +283,7 @@ __device__ __forceinline__ void take_tile(Rows<D>& r, const uint4* q, Tile<D>& x
     const bool more = y[0][0] > r.m[0] + kSlack || y[1][0] > r.m[0] + kSlack || y[0][1] > r.m[1] + kSlack ||
                       y[1][1] > r.m[1] + kSlack || s[0] >= 2.0f * r.ref || s[1] >= 2.0f * r.ref;
     if (__any_sync(0xffffffffu, more)) raise<D>(r, y, s);
-    const float f = kWeight / r.ref;
+    const float f = kWeight * inverse(r.ref);
     uint32_t b[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -297,50 +301,63 @@ __device__ __forceinline__ void take_tile(Rows<D>& r, const uint4* q, Tile<D>& x
     for (int w = 0; w < D / 64; ++w) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t lo = __byte_perm(x.v[0][w], x.v[1][w], h ? 0x7632 : 0x5410);
-            const uint32_t hi = __byte_perm(x.v[2][w], x.v[3][w], h ? 0x7632 : 0x5410);
+            const uint32_t lo = __byte_perm(v[0][w], v[1][w], h ? 0x7632 : 0x5410);
+            const uint32_t hi = __byte_perm(v[2][w], v[3][w], h ? 0x7632 : 0x5410);
             mma16816(r.o[w * 4 + 2 * h], centred<0>(lo), centred<1>(lo), centred<0>(hi), centred<1>(hi), b[0], b[1]);
             const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
             mma16816(r.o[w * 4 + 2 * h + 1], centred<0>(lo8), centred<1>(lo8), centred<0>(hi8), centred<1>(hi8), b[0],
                      b[1]);
         }
     }
-    if (next) load_values<D>(x, next, g, t);
 }
 
 template <int D>
 constexpr int so_row() {
     return D + 4;
 }
-// Floats before the warps' queries.
+// Shared memory: every warp's ring of tiles, in whose place the warps' results
+// are joined, and the queries of 256 dims.
+constexpr int kStages = 4;
 template <int D>
-constexpr int q_at() {
-    return kWarps * kRows * (so_row<D>() + 2);
+constexpr size_t ring_bytes() {
+    return static_cast<size_t>(kStages) * tile_bytes(D);
+}
+template <int D>
+constexpr size_t q_at() {
+    const size_t rings = kWarps<D> * ring_bytes<D>(), join = static_cast<size_t>(kWarps<D>) * kRows * (so_row<D>() + 2) * 4;
+    return (rings > join ? rings : join) + 15 & ~size_t(15);
 }
 template <int D>
 constexpr size_t smem_bytes() {
-    return static_cast<size_t>(q_at<D>()) * 4 + static_cast<size_t>(kWarps) * D * 16;
+    return q_at<D>() + (D == 256 ? D * 16 : 0);
 }
+
+// A warp's tiles of a segment on their way through its ring: contiguous in memory, so
+// that one lane's bulk copy brings one, three ahead of the one that is worked on.
+// (Loads into registers, one tile ahead, left too few bytes on their way.)
+struct Ring {
+    uint8_t* at;
+    uint64_t* bars;
+    uint32_t count;  // tiles so far
+    uint32_t bad;    // stages whose tile has no page
+    bool stuck;      // a copy did not come: no further ones
+};
 
 // The segment of item `it` in tiles [t0, t1): every warp its own tiles, then
 // joined.  `whole`: all of the item (the outputs are final), else its partial
 // result goes to `slot`.
 template <int D>
 __device__ __forceinline__ void segment(const pq2h::AttendParams& p, const AttendWork& wk, const AttendItem& it, int t0,
-                                        int t1, bool whole, int slot, float* smem) {
+                                        int t1, bool whole, int slot, uint8_t* shared, Ring& ring) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    Rows<D> r;
-    uint4* q = reinterpret_cast<uint4*>(smem + q_at<D>()) + warp * D + lane;
-    load_rows<D>(r, q, p, it, g, t);
-    clear<D>(r);
     const int per_page = p.cache.T / kTileTokens;
     const long long head_at = static_cast<long long>(it.head) * per_page * tile_bytes(D);
-    const int mine = t1 - t0 > warp ? (t1 - t0 - warp + kWarps - 1) / kWarps : 0;
+    const int mine = t1 - t0 > warp ? (t1 - t0 - warp + kWarps<D> - 1) / kWarps<D> : 0;
     // tiles that every row sees all of
     const int in0 = it.first_hi, in1 = it.last_lo;
     int page_lane = 0;
     const auto look_up = [&](int i) {  // pages of the warp's tiles i .. i + 31, one a lane
-        const int tile = t0 + warp + kWarps * (i + lane);
+        const int tile = t0 + warp + kWarps<D> * (i + lane);
         int page = -1;
         if (tile < t1) {
             page = __ldg(p.cache.pages + it.b * p.cache.ld_pages + tile / per_page);
@@ -351,46 +368,70 @@ __device__ __forceinline__ void segment(const pq2h::AttendParams& p, const Atten
         }
         page_lane = page;
     };
-    const auto place = [&](int i) -> const uint8_t* {  // tile i's bytes, null outside the pool
-        const int page = __shfl_sync(0xffffffffu, page_lane, i & 31);
-        if (page < 0) return nullptr;
-        const int tile = t0 + warp + kWarps * i;
-        return p.cache.pool + page * p.cache.page_stride + head_at +
-               static_cast<long long>(tile % per_page) * tile_bytes(D);
+    // tiles are asked for in order: the next one's place in its page
+    const int step = kWarps<D> % per_page;
+    int in_page = (t0 + warp) % per_page;
+    const auto fetch = [&](int i) {
+        if ((i & 31) == 0) look_up(i);
+        const int page = __shfl_sync(0xffffffffu, page_lane, i & 31), in = in_page;
+        in_page += step;
+        if (in_page >= per_page) in_page -= per_page;
+        const uint32_t stage = (ring.count + i) % kStages;
+        ring.bad = page < 0 ? ring.bad | (1u << stage) : ring.bad & ~(1u << stage);
+        if (lane != 0) return;
+        if (page < 0) {
+            mbar_arrive(&ring.bars[stage]);
+            return;
+        }
+        const uint8_t* from = p.cache.pool + page * p.cache.page_stride + head_at +
+                              in * tile_bytes(D);
+        mbar_arrive_expect_tx(&ring.bars[stage], tile_bytes(D));
+        bulk_g2s(ring.at + stage * tile_bytes(D), from, tile_bytes(D), &ring.bars[stage]);
     };
-    Tile<D> x;
-    const uint8_t* from = nullptr;
-    if (mine > 0) {
-        look_up(0);
-        from = place(0);
-    }
-    if (from) {
-        load_keys<D>(x, from, g, t);
-        load_pairs<D>(x, from, g);
-        load_values<D>(x, from, g, t);
-    }
+    const auto wait = [&](uint32_t n) {
+        unsigned long long since = 0;
+        for (uint32_t i = 0; !__all_sync(0xffffffffu, mbar_try_wait(&ring.bars[n % kStages], (n / kStages) & 1)); ++i) {
+            if (i % 64 != 63) continue;
+            if (since == 0) since = globaltimer_ns();
+            if (__any_sync(0xffffffffu, globaltimer_ns() - since > p.ctl.wait_limit_ns)) {
+                if (lane == 0) atomicOr(p.ctl.err, DEVERR_TIMEOUT);
+                return false;
+            }
+        }
+        return true;
+    };
+    // the segment before's results, in the rings' place, have been read
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    if (!ring.stuck)
+        for (int i = 0; i < min(kStages - 1, mine); ++i) fetch(i);
+    Rows<D> r;
+    uint4* q = reinterpret_cast<uint4*>(shared + q_at<D>()) + lane;
+    load_rows<D>(r, q, p, it, g, t);
+    clear<D>(r);
+    if constexpr (D == 256) __syncthreads();
 #pragma unroll 1
-    for (int i = 0; i < mine; ++i) {
-        const uint8_t* next = nullptr;
-        if (i + 1 < mine) {
-            if (((i + 1) & 31) == 0) look_up(i + 1);
-            next = place(i + 1);
+    for (int i = 0; i < mine && !ring.stuck; ++i) {
+        if (i + kStages - 1 < mine) fetch(i + kStages - 1);
+        const uint32_t n = ring.count + i, stage = n % kStages;
+        if (!wait(n)) {
+            // (not before the others are here, or have not come either)
+            for (int k = 1; k < kStages && i + k < mine; ++k) wait(n + k);
+            ring.stuck = true;
+            break;
         }
-        if (from) {
-            const int key0 = (t0 + warp + kWarps * i) * kTileTokens;
-            take_tile<D>(r, q, x, key0, key0 >= in0 && key0 + kTileTokens - 1 <= in1, next, g, t);
-        } else if (next) {
-            load_keys<D>(x, next, g, t);
-            load_pairs<D>(x, next, g);
-            load_values<D>(x, next, g, t);
-        }
-        from = next;
+        const int key0 = (t0 + warp + kWarps<D> * i) * kTileTokens;
+        if (!(ring.bad >> stage & 1))
+            take_tile<D>(r, q, ring.at + stage * tile_bytes(D), key0, key0 >= in0 && key0 + kTileTokens - 1 <= in1, g, t);
+        __syncwarp();
     }
+    ring.count += mine;
+    float* smem = reinterpret_cast<float*>(shared);
     // the warps' results: [warp][row][D] with maxima and sums behind them
     float* so = smem;
-    float* sm = smem + kWarps * kRows * so_row<D>();
-    float* sl = sm + kWarps * kRows;
-    __syncthreads();  // (the segment before may still be read)
+    float* sm = smem + kWarps<D> * kRows * so_row<D>();
+    float* sl = sm + kWarps<D> * kRows;
+    __syncthreads();  // (other warps' tiles)
     const float f = r.ref / kWeight;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -410,14 +451,15 @@ __device__ __forceinline__ void segment(const pq2h::AttendParams& p, const Atten
     __syncthreads();
     // warp w joins row w, a lane D / 32 dims of it
     const int row = warp;
+    if (row >= kRows) return;
     float m = kEmpty;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm[w * kRows + row]);
+    for (int w = 0; w < kWarps<D>; ++w) m = fmaxf(m, sm[w * kRows + row]);
     float l = 0.0f, o[D / 32];
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) o[j] = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kWarps<D>; ++w) {
         const float a = ex2(sm[w * kRows + row] - m);
         l = fmaf(a, sl[w * kRows + row], l);
         const float* from_w = so + (w * kRows + row) * so_row<D>() + lane * (D / 32);
@@ -439,22 +481,28 @@ __device__ __forceinline__ void segment(const pq2h::AttendParams& p, const Atten
 
 // The list's tiles, dealt out.
 template <int D>
-__global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
+__global__ void __launch_bounds__(32 * kWarps<D>, kBlocks<D>)
     attend_kernel(const __grid_constant__ pq2h::AttendParams p, const __grid_constant__ AttendWork wk, int row_tiles) {
-    extern __shared__ __align__(16) float smem[];
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ uint64_t bars[kWarps<D>][kStages];
     pdl_wait();
     pdl_launch_dependents();
     // (the walk through the list is thread 0's: in registers of all threads it
     // would be in the way of the tiles')
     __shared__ AttendSpan walk;
     __shared__ AttendStep step;
+    const int warp = threadIdx.x >> 5;
+    Ring ring = {smem + warp * ring_bytes<D>(), bars[warp], 0, 0, false};
+    if (threadIdx.x % 32 < kStages) mbar_init(&bars[warp][threadIdx.x % 32], 1);
+    fence_mbar_init();
+    __syncwarp();
     long long u, u1;
     {
         AttendSpan span;
         if (row_tiles == 1)
-            attend_span<kRows>(p, 1, kExtra, 2 * kWarps, span);
+            attend_span<kRows>(p, 1, kExtra, kWarps<D>, span);
         else
-            attend_span_block<kRows, kWarps>(p, row_tiles, 1, kExtra, 2 * kWarps, span);
+            attend_span_block<kRows, kWarps<D>>(p, row_tiles, 1, kExtra, kWarps<D>, span);
         if (threadIdx.x == 0) {
             walk = span;
             wk.join[blockIdx.x] = {0, 0, 0, 0, 0};
@@ -473,60 +521,66 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
         if (threadIdx.x == 0 && s.first == 0 && s.count < s.of)
             wk.join[blockIdx.x] = {s.b, s.row_tile, s.head,
                                    attend_cta_of(walk, s.end - 1) - static_cast<int>(blockIdx.x) + 1, slot};
-        segment<D>(p, wk, it, t0, min(t0 + s.count, it.tile1), s.count == s.of, slot, smem);
+        segment<D>(p, wk, it, t0, min(t0 + s.count, it.tile1), s.count == s.of, slot, smem, ring);
     }
 }
 
-// CTA (c, row): row `row` of the item whose first part is CTA c's.  Each of
-// the warps takes every kJoinWarps-th part, a lane D / 32 dims.
-constexpr int kJoinWarps = 4;
+// CTA (c, row): row `row` of the item whose first part is CTA c's.  Every warp
+// finds the weights of all parts, one a lane, and adds up every kJoinWarps-th part's
+// outputs, a lane D / 32 dims.
+constexpr int kJoinWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     attend_join_kernel(const __grid_constant__ pq2h::AttendParams p, const __grid_constant__ AttendWork wk) {
+    constexpr int kN = D / 32;
     __shared__ float so[kJoinWarps][D];
-    __shared__ float sm[kJoinWarps], sl[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y;
     pdl_wait();
     pdl_launch_dependents();
     const AttendJoin j = wk.join[blockIdx.x];
     if (j.parts == 0) return;
-    const auto slot_of = [&](int i) { return i == 0 ? j.first_slot : 2 * (static_cast<int>(blockIdx.x) + i); };
-    float m = kEmpty, l = 0.0f, o[D / 32];
+    const auto place = [&](int i) {
+        return static_cast<long long>(i == 0 ? j.first_slot : 2 * (static_cast<int>(blockIdx.x) + i)) * kRows + row;
+    };
+    float m = kEmpty;
+    for (int i = lane; i < j.parts; i += 32) m = fmaxf(m, wk.ml[place(i)].x);
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) o[k] = 0.0f;
-    for (int i = warp; i < j.parts; i += kJoinWarps) m = fmaxf(m, wk.ml[slot_of(i) * kRows + row].x);
-    for (int i = warp; i < j.parts; i += kJoinWarps) {
-        const long long at = static_cast<long long>(slot_of(i)) * kRows + row;
-        const float2 ml = wk.ml[at];
-        const float a = ex2(ml.x - m);
-        l = fmaf(a, ml.y, l);
-        const float2* f = reinterpret_cast<const float2*>(wk.o + at * D + lane * (D / 32));
+    for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    float l = 0.0f, o[kN];
 #pragma unroll
-        for (int k = 0; k < D / 64; ++k) {
-            const float2 v = f[k];
-            o[2 * k] = fmaf(a, v.x, o[2 * k]);
-            o[2 * k + 1] = fmaf(a, v.y, o[2 * k + 1]);
+    for (int k = 0; k < kN; ++k) o[k] = 0.0f;
+    for (int i0 = 0; i0 < j.parts; i0 += 32) {
+        float a = 0.0f;
+        if (i0 + lane < j.parts) {
+            const float2 ml = wk.ml[place(i0 + lane)];
+            a = ex2(ml.x - m);
+            l = fmaf(a, ml.y, l);
+        }
+#pragma unroll
+        for (int k = 0; k < 32 / kJoinWarps; ++k) {
+            const int i = warp + kJoinWarps * k;
+            const float ai = __shfl_sync(0xffffffffu, a, i);
+            if (i0 + i >= j.parts) continue;
+            const float2* from = reinterpret_cast<const float2*>(wk.o + place(i0 + i) * D + lane * kN);
+#pragma unroll
+            for (int x = 0; x < kN / 2; ++x) {
+                const float2 v = from[x];
+                o[2 * x] = fmaf(ai, v.x, o[2 * x]);
+                o[2 * x + 1] = fmaf(ai, v.y, o[2 * x + 1]);
+            }
         }
     }
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) so[warp][lane * (D / 32) + k] = o[k];
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
+    for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) so[warp][lane * kN + k] = o[k];
     __syncthreads();
     if (warp != 0) return;
-    float top = kEmpty;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, sm[w]);
-    l = 0.0f;
+    for (int w = 1; w < kJoinWarps; ++w)
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) o[k] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-        const float a = ex2(sm[w] - top);
-        l = fmaf(a, sl[w], l);
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) o[k] = fmaf(a, so[w][lane * (D / 32) + k], o[k]);
-    }
+        for (int k = 0; k < kN; ++k) o[k] += so[w][lane * kN + k];
     const AttendItem it = attend_item<kRows>(p, j.b, j.row_tile, j.head);
     write_row<D / 32>(p, it, kRows, row, lane * (D / 32), l, o);
 }
@@ -547,8 +601,8 @@ cudaError_t launch_few(const AttendParams& p, const pq2::AttendWork& wk, cudaStr
     cudaError_t e = raise_smem(lim, pq2::attend_kernel<D>, smem);
     if (e != cudaSuccess) return e;
     const int G = p.q_heads / p.cache.heads, row_tiles = (p.max_rows * G + pq2::kRows - 1) / pq2::kRows;
-    const int64_t ctas = std::min<int64_t>(dev.num_sms * (D == 256 ? 1 : 2), pq2::kAttendCtas);
-    e = launch(pq2::attend_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(pq2::kThreads), smem, st, true, p, wk, row_tiles);
+    const int64_t ctas = std::min<int64_t>(dev.num_sms * pq2::kBlocks<D>, pq2::kAttendCtas);
+    e = launch(pq2::attend_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(32 * pq2::kWarps<D>), smem, st, true, p, wk, row_tiles);
     if (e != cudaSuccess) return e;
     return launch(pq2::attend_join_kernel<D>, dim3(static_cast<unsigned>(ctas), pq2::kRows),
                   dim3(32 * pq2::kJoinWarps), 0, st, true, p, wk);
