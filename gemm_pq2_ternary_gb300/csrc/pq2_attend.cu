@@ -40,7 +40,8 @@ template <int D>
 constexpr int kBlocks = D == 256 ? 1 : 2;
 constexpr int kRows = 8;            // query rows of a pass
 constexpr int kFewRows = 32;        // rows of a sequence and head that this kernel takes, at most
-constexpr int kExtra = 16;          // what an item takes besides its tiles, in tiles
+constexpr int kExtra = 32;          // what an item takes besides its tiles, in tiles (8: 111 us for 64 sequences, 16: 107,
+                                    // 32: 95, 64: 96, 96: 99)
 constexpr float kEmpty = -1e30f;    // maximum of a row that has seen nothing
 constexpr float kSlack = 5.0f;      // how far (as a power of two) a score may exceed the maximum
 constexpr float kWeight = 512.0f;  // weights enter the product times this

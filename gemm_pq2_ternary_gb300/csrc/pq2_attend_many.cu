@@ -39,7 +39,8 @@ constexpr int kKeys = 128;                // keys of a tile
 constexpr int kPer = kKeys / kTileTokens;
 constexpr int kChunk = 16384;             // bytes
 constexpr int kSlots = 4;                 // tiles whose factors are held
-constexpr int kExtra = 2;                 // what a segment's queries and outputs take, in tiles
+constexpr int kExtra = 6;                 // what an item's queries and outputs take, in tiles (2: 390 us for
+                                          // chunks behind 6000 tokens, 3: 333, 4: 324, 6: 316)
 constexpr float kEmpty = -1e30f;
 constexpr float kSlack = 5.0f;
 constexpr float kWeight = 512.0f;
