@@ -250,6 +250,7 @@ struct RopeParams {
     int heads[3];
     int dim, rot, x_type, out_type;
     int read_kind[2];          // launch_cache_read: array k is of keys (0) or values (1)
+    int parts;                 // warps of a token (set at the launch)
     uint32_t flags;
     CacheParams cache;
     pq2::DevCtl ctl;

@@ -7,12 +7,17 @@
 // (rope_table_kernel, in 64 bits: at position 262144 a 32-bit angle would be off by
 // up to 0.016): a row of it serves all heads of a token.
 //
-// Bound by memory: each value is read once and written once (2 or 4 bytes, or
-// half a byte), with a few operations between.  head_kernel gives a warp a
-// head's row of D values, D/32 neighbours a lane, and kSlots of them at once so that
-// their loads are in flight together; a pair's other half is loaded by both
-// lanes that need it (the second time from L1).  A row's least and largest
-// value, which its scale and offset come from, are one reduction over the warp each.
+// Each value is read once and written once (2 or 4 bytes, or half a byte), with a few
+// operations between.  head_kernel gives a warp a head's row of D values, D/32
+// neighbours a lane, and two heads at once so that their loads are in flight together;
+// in long calls it goes on to the token's other heads, so that place and angles
+// are found once.  A pair's other half is loaded by both lanes that need it (the second
+// time from L1).  A row's least and largest value, which its scale and offset come
+// from, are one reduction over the warp each.  With inputs' type and pairing known when it
+// is compiled it needs 64 registers (80 with the cache), and 32 (24) warps of an SM
+// keep memory busy: 4096 tokens of 28 heads of 256 (fp32 in, bf16 out) 30 us, 5.9 TB/s
+// (two heads a warp and no more, both types in one kernel: 53 us).  Into the cache the
+// issue of instructions is the limit: 5105 tokens of 64 heads of 128 in 75 us.
 #include <algorithm>
 #include <cmath>
 
@@ -164,50 +169,33 @@ __device__ __forceinline__ Place place_of(const pq2h::CacheParams& c, int row, c
     return at;
 }
 
-// A warp takes kSlots heads of one token.  Slots of a token: heads[0] of
-// array 0, heads[1] of array 1 (both turned), heads[2] of array 2 (values as
-// they are); where CACHE, arrays 1 and 2 go to the cache.
-template <int E, bool VEC, bool CACHE>
-__global__ void __launch_bounds__(kThreads) head_kernel(const __grid_constant__ pq2h::RopeParams p) {
-    constexpr int D = 32 * E;
+// A warp takes a part of one token's heads (all of them in long calls), kSlots at a
+// time.  Slots of a token: heads[0] of array 0, heads[1] of array 1 (both
+// turned), heads[2] of array 2 (values as they are); where CACHE, arrays 1 and 2 go
+// to the cache.
+// MODE: kAny, or of values on boundaries of a lane's size kF32 (inputs are fp32) + kNear
+// (neighbours make pairs): with both known a warp needs half of the registers.
+constexpr int kAny = -1, kF32 = 1, kNear = 2;
+
+template <int E, int MODE, bool CACHE>
+__global__ void __launch_bounds__(kThreads, MODE == kAny ? 2 : CACHE ? 3 : 4) head_kernel(const __grid_constant__ pq2h::RopeParams p) {
+    constexpr bool VEC = MODE != kAny;
+    constexpr int D = 32 * E, kN = kSlots;
+    const int x_type = VEC && (MODE & kF32) ? PQ2_F32 : p.x_type;
+    if (VEC && !(MODE & kF32)) __builtin_assume(x_type != PQ2_F32);
     const int lane = threadIdx.x & 31;
     const int slots = p.heads[0] + p.heads[1] + p.heads[2];
-    const int groups = (slots + kSlots - 1) / kSlots;
-    const long long total = p.M * groups;
+    const int per_part = ((slots + kN - 1) / kN + p.parts - 1) / p.parts * kN;
+    const long long total = p.M * p.parts;
     const int d = lane * E, half = p.rot >> 1;
-    const bool near = p.flags & PQ2_ROPE_NEIGHBOURS;
+    const bool near = VEC ? (MODE & kNear) != 0 : (p.flags & PQ2_ROPE_NEIGHBOURS) != 0;
     pdl_wait();
     pdl_launch_dependents();
     for (long long w = blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5); w < total;
          w += static_cast<long long>(gridDim.x) * kWarps) {
-        const long long row = w / groups;
-        const int slot0 = static_cast<int>(w - row * groups) * kSlots;
-        float x[kSlots][E], o[kSlots][E];
-        int kind[kSlots], head[kSlots];
-#pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
-            int h = slot0 + i, k = 0;
-            if (h >= p.heads[0]) h -= p.heads[0], k = 1;
-            if (k == 1 && h >= p.heads[1]) h -= p.heads[1], k = 2;
-            if (slot0 + i >= slots) k = -1, h = 0;
-            kind[i] = k, head[i] = h;
-            if (k < 0) continue;
-            const long long at = row * p.ld[k] + h * p.hs[k];
-            load_elems<E, VEC>(p.x[k], p.x_type, at + d, x[i]);
-            if (k == 2 || near) continue;
-            if constexpr (VEC) {
-                // (rot / 2 is a multiple of E: a lane is on one side)
-                if (d < p.rot) load_elems<E, true>(p.x[k], p.x_type, at + (d < half ? d + half : d - half), o[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    const int e = d + j;
-                    float one[1] = {0.0f};
-                    if (e < p.rot) load_elems<1, false>(p.x[k], p.x_type, at + (e < half ? e + half : e - half), one);
-                    o[i][j] = one[0];
-                }
-            }
-        }
+        const long long row = p.parts == 1 ? w : w / p.parts;
+        const int first = static_cast<int>(w - row * p.parts) * per_part, end = min(first + per_part, slots);
+        if (first >= end) continue;
         Place place = {0, 0};
         if constexpr (CACHE) {
             bool mine;
@@ -254,49 +242,89 @@ __global__ void __launch_bounds__(kThreads) head_kernel(const __grid_constant__ 
                 for (int j = 0; j < E; ++j) s[j] = -s[j];
             }
         }
-        // in place: everything that the warp reads is read before it writes
-        __syncwarp();
+        // (an array at a time: what depends on it alone is found once)
+        int off = 0;
+#pragma unroll 1
+        for (int k = 0; k < 3; off += p.heads[k], ++k) {
+            const int h1 = min(end - off, p.heads[k]);
+            int h = max(first - off, 0);
+            if (h >= h1) continue;
+            const bool cached = CACHE && k > 0, turn = k < 2 && p.rot > 0;
+            if (cached && place.page < 0) continue;
+            const long long hs = p.hs[k];
+            long long in = row * p.ld[k] + h * hs + d, out = 0, out_hs = 0;
+            int pair_at = 0;
+            if (cached) {
+                const int T = p.cache.T, t = static_cast<int>(place.pos % T);
+                out_hs = static_cast<long long>(T / kTileTokens) * tile_bytes(D);
+                out = place.page * p.cache.page_stride + h * out_hs + t / kTileTokens * tile_bytes(D);
+                pair_at = tile_pairs(D, k - 1) + (t % kTileTokens) * 4;
+                out += tile_codes(D, k - 1) + (t % kTileTokens) * (D / 2) + lane * (E / 2);
+                pair_at -= tile_codes(D, k - 1) + (t % kTileTokens) * (D / 2);
+            } else {
+                out_hs = p.hso[k];
+                out = row * p.ldo[k] + h * out_hs + d;
+            }
+            const long long other = d < half ? half : -half;
+#pragma unroll 1
+            for (; h < h1; h += kN, in += kN * hs, out += kN * out_hs) {
+                float x[kN][E], o[kN][E];
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
-            if (kind[i] < 0) continue;
-            if (kind[i] < 2 && p.rot > 0) {
-                float y[E];
+                for (int i = 0; i < kN; ++i) {
+                    if (h + i >= h1) continue;
+                    const long long at = in + i * hs;
+                    load_elems<E, VEC>(p.x[k], x_type, at, x[i]);
+                    if (!turn || near) continue;
+                    if constexpr (VEC) {
+                        // (rot / 2 is a multiple of E: a lane is on one side)
+                        if (d < p.rot) load_elems<E, true>(p.x[k], x_type, at + other, o[i]);
+                    } else {
 #pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    const int e = d + j;
-                    y[j] = x[i][j];
-                    if (e < p.rot)
-                        y[j] = near ? turned(x[i][j], x[i][j ^ 1], c[j], s[j], e & 1)
-                                    : turned(x[i][j], o[i][j], c[j], s[j], e >= half);
+                        for (int j = 0; j < E; ++j) {
+                            const int e = d + j;
+                            float one[1] = {0.0f};
+                            if (e < p.rot) load_elems<1, false>(p.x[k], x_type, at + j + (e < half ? half : -half), one);
+                            o[i][j] = one[0];
+                        }
+                    }
                 }
+                // in place: everything that the warp reads of these heads is read before it writes
+                __syncwarp();
 #pragma unroll
-                for (int j = 0; j < E; ++j) x[i][j] = y[j];
+                for (int i = 0; i < kN; ++i) {
+                    if (h + i >= h1) continue;
+                    if (turn) {
+                        float y[E];
+#pragma unroll
+                        for (int j = 0; j < E; ++j) {
+                            const int e = d + j;
+                            y[j] = x[i][j];
+                            if (e < p.rot)
+                                y[j] = near ? turned(x[i][j], x[i][j ^ 1], c[j], s[j], e & 1)
+                                            : turned(x[i][j], o[i][j], c[j], s[j], e >= half);
+                        }
+#pragma unroll
+                        for (int j = 0; j < E; ++j) x[i][j] = y[j];
+                    }
+                    const long long at = out + i * out_hs;
+                    if (!cached) {
+                        if (store_ok(p.ctl, at, E, p.out_elems[k])) store_elems<E, VEC>(p.out[k], p.out_type, at, x[i]);
+                        continue;
+                    }
+                    uint32_t pair;
+                    const uint32_t codes = quantise_row<E>(x[i], pair);
+                    if (store_ok(p.ctl, at, E / 2, p.cache.pool_bytes)) {
+                        if constexpr (E == 8)
+                            *reinterpret_cast<uint32_t*>(p.cache.pool + at) = codes;
+                        else if constexpr (E == 4)
+                            *reinterpret_cast<uint16_t*>(p.cache.pool + at) = static_cast<uint16_t>(codes);
+                        else
+                            p.cache.pool[at] = static_cast<uint8_t>(codes);
+                    }
+                    if (lane == 0 && store_ok(p.ctl, at + pair_at, 4, p.cache.pool_bytes))
+                        *reinterpret_cast<uint32_t*>(p.cache.pool + at + pair_at) = pair;
+                }
             }
-            if (!CACHE || kind[i] == 0) {
-                const int k = kind[i];
-                const long long at = row * p.ldo[k] + head[i] * p.hso[k] + d;
-                if (store_ok(p.ctl, at, E, p.out_elems[k])) store_elems<E, VEC>(p.out[k], p.out_type, at, x[i]);
-                continue;
-            }
-            if (place.page < 0) continue;
-            uint32_t pair;
-            const uint32_t codes = quantise_row<E>(x[i], pair);
-            const int value = kind[i] - 1, T = p.cache.T;
-            const int t = static_cast<int>(place.pos % T);
-            const long long tile = place.page * p.cache.page_stride +
-                                   (head[i] * static_cast<long long>(T / kTileTokens) + t / kTileTokens) * tile_bytes(D);
-            const long long at = tile + tile_codes(D, value) + (t % kTileTokens) * (D / 2) + lane * (E / 2);
-            if (store_ok(p.ctl, at, E / 2, p.cache.pool_bytes)) {
-                if constexpr (E == 8)
-                    *reinterpret_cast<uint32_t*>(p.cache.pool + at) = codes;
-                else if constexpr (E == 4)
-                    *reinterpret_cast<uint16_t*>(p.cache.pool + at) = static_cast<uint16_t>(codes);
-                else
-                    p.cache.pool[at] = static_cast<uint8_t>(codes);
-            }
-            const long long pa = tile + tile_pairs(D, value) + (t % kTileTokens) * 4;
-            if (lane == 0 && store_ok(p.ctl, pa, 4, p.cache.pool_bytes))
-                *reinterpret_cast<uint32_t*>(p.cache.pool + pa) = pair;
         }
     }
 }
@@ -449,13 +477,23 @@ bool vector_path(const RopeParams& p, int E, bool cache) {
     return true;
 }
 
+constexpr long long kEnoughWarps = 152 * 48;  // (four times as many: 88 us for 5105 tokens of 64 heads, not 75)
+
 template <int E, bool CACHE>
-cudaError_t launch_heads(const RopeParams& p, cudaStream_t st) {
+cudaError_t launch_heads(const RopeParams& args, cudaStream_t st) {
+    RopeParams p = args;
     const int slots = p.heads[0] + p.heads[1] + p.heads[2];
-    const unsigned grid = grid_for(p.M * ((slots + pq2::kSlots - 1) / pq2::kSlots));
-    if (vector_path(p, E, CACHE))
-        return launch(pq2::head_kernel<E, true, CACHE>, dim3(grid), dim3(pq2::kThreads), 0, st, true, p);
-    return launch(pq2::head_kernel<E, false, CACHE>, dim3(grid), dim3(pq2::kThreads), 0, st, true, p);
+    // a token's place and angles are found once for all its heads where there are
+    // tokens enough to keep all SMs busy
+    p.parts = static_cast<int>(std::min<long long>((slots + pq2::kSlots - 1) / pq2::kSlots,
+                                                   std::max<long long>(kEnoughWarps / std::max<long long>(p.M, 1), 1)));
+    p.parts = std::max(p.parts, 1);
+    const unsigned grid = grid_for(p.M * p.parts);
+    const auto go = [&](auto kernel) { return launch(kernel, dim3(grid), dim3(pq2::kThreads), 0, st, true, p); };
+    if (!vector_path(p, E, CACHE)) return go(pq2::head_kernel<E, pq2::kAny, CACHE>);
+    const bool f32 = p.x_type == PQ2_F32, near = p.flags & PQ2_ROPE_NEIGHBOURS;
+    if (near) return f32 ? go(pq2::head_kernel<E, pq2::kF32 + pq2::kNear, CACHE>) : go(pq2::head_kernel<E, pq2::kNear, CACHE>);
+    return f32 ? go(pq2::head_kernel<E, pq2::kF32, CACHE>) : go(pq2::head_kernel<E, 0, CACHE>);
 }
 
 template <int E>
