@@ -217,6 +217,16 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 // ---------------------------------------------------------------------------
 // What every role knows
 // ---------------------------------------------------------------------------
+// r (of a key) and sum(q) are two fp16 each, hi + lo; three of their products are
+// summed: hi hi + (hi kAugLo) (lo / kAugLo) + (lo kAugHi2) (hi / kAugHi2).  With those powers of
+// two no factor falls so far below fp16's normal numbers that the scores notice (sum(q)'s
+// lo as it is would be off by 2^-14 of sum(q)).
+constexpr float kAugLo = 0x1p-6f, kAugHi2 = 0x1p3f;
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // All waits are by whole warps, none of whose lanes goes apart from the others
 // (a branch for one lane and the shuffle after it take some 300 cycles), and
 // short in code.  The issuing warp, without which nothing goes on, also watches
@@ -335,10 +345,10 @@ __device__ __forceinline__ void factors(const Ctl& k, const AttendWork& wk, int 
                 // the offset counts as that)
                 s = fmaxf(s, fmaxf(fabsf(z) * 0x1p-25f, 0x1p-24f));
                 const float r = 0x1p-10f * z / s;
-                const __half hi = __float2half_rn(r), lo = __float2half_rn(r - __half2float(hi));
-                const uint32_t h = __half_as_ushort(hi), l = __half_as_ushort(lo);
+                const __half hi = __float2half_rn(r);
+                const float hf = __half2float(hi);
                 *reinterpret_cast<uint4*>(slot.aug + key * 16) =
-                    make_uint4(h | (h << 16), l, 0u, 0u);
+                    make_uint4(half2_bits(hf, hf * kAugLo), half2_bits((r - hf) * kAugHi2, 0.0f), 0u, 0u);
                 const float vs = __half2float(__ushort_as_half(vp[i] & 0xffffu));
                 slot.scale[at] = s * to_score;
                 slot.value[at] = vs;
@@ -613,11 +623,6 @@ struct Issue {
 // ---------------------------------------------------------------------------
 // Warps 0-7
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 __device__ __forceinline__ float4 lds4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 // What a softmax warp counts over all segments.
@@ -1022,9 +1027,9 @@ __device__ __forceinline__ void softmax(const Ctl& k, const AttendWork& wk, uint
                 for (int o = D / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 if (col == 0) {
                     sum *= 0x1p-14f;
-                    const __half hi = __float2half_rn(sum), lo = __float2half_rn(sum - __half2float(hi));
-                    const uint32_t a = __half_as_ushort(hi), b = __half_as_ushort(lo);
-                    *reinterpret_cast<uint4*>(smem + C::kAugAt + at * 2048 + r * 16) = make_uint4(a | (b << 16), a, 0u, 0u);
+                    const float hi = __half2float(__float2half_rn(sum));
+                    *reinterpret_cast<uint4*>(smem + C::kAugAt + at * 2048 + r * 16) =
+                        make_uint4(half2_bits(hi, (sum - hi) / kAugLo), half2_bits(hi / kAugHi2, 0.0f), 0u, 0u);
                 }
             }
             fence_async();
