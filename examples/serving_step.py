@@ -4,6 +4,11 @@ A block of a ternary model with adapters and drafted tokens: the rows of a
 step are a few drafted tokens each of several requests, and every request may
 have a low-rank adapter of its own.
 
+    pages for the step's tokens, refused drafts' given back   pq2_pages_update, pq2_pages_copy
+    q, k, v = projection of rms(r)                     pq2_rmsnorm, pq2_matmul
+    q turned, k turned and v into the 4-bit cache      pq2_cache4_append
+    a      = attention over the cache                  pq2_cache4_attend
+    r     += output projection of a                    pq2_matmul, pq2_norm_residual
     x      = rms(r) * w1                               pq2_rmsnorm
     gu     = gate/up projection of x                   pq2_matmul
     gu    += adapter on gate/up                        pq2_lora_add (in place)
@@ -93,6 +98,66 @@ class Block:
         return self.accepted, self.tokens
 
 
+class Attention:
+    """Weights, cache and buffers of the attention before a Block: `q_heads` query
+    heads share `heads` key/value heads of `dim`."""
+
+    def __init__(self, block, q_heads, heads, dim, length, page=32, seed=1, device="cuda"):
+        gen = torch.Generator(device=device).manual_seed(seed)
+        self.block, self.q_heads, self.heads, self.dim, self.page = block, q_heads, heads, dim, page
+        rows, B = block.rows, block.requests
+        wide = q_heads + 2 * heads
+
+        def projection(N, K):
+            tern = inputs.draw_ternary_torch(N, K, "p343", gen, device)
+            return pq2.pack(tern, inputs.draw_ws_torch(N, K, gen, device))
+
+        def empty(*shape, dtype=torch.float32):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+        self.qkv = projection(wide * dim, block.hidden)
+        self.out = projection(block.hidden, q_heads * dim)
+        self.ws_qkv = pq2.alloc_workspace(pq2.PQ2_OP_MATMUL, rows, wide * dim, block.hidden, device)
+        self.ws_out = pq2.alloc_workspace(pq2.PQ2_OP_MATMUL, rows, block.hidden, q_heads * dim, device)
+        W = -(-length // page)
+        self.pool = pq2.alloc_cache4(B * (W + 1), heads, dim, page, device=device)
+        self.pages = torch.full((2, B, W), -1, dtype=torch.int32, device=device)
+        self.refs = torch.zeros((2, B * (W + 1)), dtype=torch.int32, device=device)
+        self.turn = 0                                   # which of the two is in use
+        self.lens = torch.zeros(B, dtype=torch.int32, device=device)
+        self.source = torch.arange(B, dtype=torch.int32, device=device)
+        self.copies = empty(B, 2, dtype=torch.int32)
+        self.info = empty(2, dtype=torch.int32)
+        self.ws_pages = pq2.alloc_pages_workspace(B, B * (W + 1), device)
+        self.ws_attend = pq2.alloc_attend_workspace(rows, q_heads, heads, dim, device)
+        self.angles = empty(W * page, dim // 2, 2)
+        pq2.pq2_rope_table(self.angles, 1e6)
+        self.x = empty(rows, block.hidden, dtype=torch.float16)
+        self.rows = empty(rows, wide, dim)
+        self.q, self.a = (empty(rows, q_heads, dim, dtype=torch.float16) for _ in range(2))
+        self.y, self.r_out = (empty(rows, block.hidden) for _ in range(2))
+
+    def step(self, r, row_start, keep):
+        """r fp32 [rows, hidden] with row_start int32 [requests + 1]; keep int32
+        [requests]: tokens of the cache that still hold (refused drafts do not)."""
+        b, now = self.block, self.turn
+        after = keep + (row_start[1:] - row_start[:-1])
+        pq2.pq2_pages_update(self.pages[now], self.refs[now], self.lens, self.source, keep, after, self.page,
+                             self.pages[1 - now], self.refs[1 - now], self.copies, self.info, self.ws_pages)
+        pq2.pq2_pages_copy(self.pool, self.copies)
+        self.turn, self.lens = 1 - now, after
+        pages = self.pages[self.turn]
+        pq2.pq2_rmsnorm(r, b.w1, self.x, EPS)
+        pq2.pq2_matmul(self.x, *self.qkv, self.rows.view(b.rows, -1), self.ws_qkv)
+        h = self.q_heads
+        pq2.pq2_cache4_append(self.rows[:, h:h + self.heads], self.rows[:, h + self.heads:], self.pool, pages, row_start,
+                              after, q=self.rows[:, :h], q_out=self.q, table=self.angles)
+        pq2.pq2_cache4_attend(self.q, self.pool, pages, row_start, after, self.a, self.ws_attend)
+        pq2.pq2_matmul(self.a.view(b.rows, -1), *self.out, self.y, self.ws_out)
+        pq2.pq2_norm_residual(self.y, r, self.r_out, w_post=b.w2, eps=EPS, alpha=ALPHA)
+        return self.r_out
+
+
 def random_step(block, drafts, adapters, seed=0, device="cuda"):
     """Arguments of Block.step for requests with `drafts` drafts each."""
     gen = torch.Generator(device=device).manual_seed(seed)
@@ -119,15 +184,28 @@ def main():
     ap.add_argument("--vocab", type=int, default=248320)
     ap.add_argument("--adapters", type=int, default=3)
     ap.add_argument("--rank", type=int, default=16)
+    ap.add_argument("--query-heads", type=int, default=24)
+    ap.add_argument("--heads", type=int, default=4)
+    ap.add_argument("--head-dim", type=int, default=256)
     a = ap.parse_args()
     block = Block(a.requests * (a.drafts + 1), a.hidden, a.inner, a.vocab, a.adapters, a.rank, a.requests)
     args = random_step(block, a.drafts, a.adapters)
+    attention = Attention(block, a.query_heads, a.heads, a.head_dim, 32 * (a.drafts + 1))
+    keep = torch.zeros(a.requests, dtype=torch.int32, device="cuda")
+
+    def step():
+        nonlocal keep
+        r = attention.step(args["r"], args["row_start"], keep)
+        accepted, tokens = block.step(**{**args, "r": r})
+        keep = keep + accepted + 1      # the drafts kept and the token before them
+        return accepted, tokens
+
     for _ in range(3):
-        accepted, tokens = block.step(**args)
+        accepted, tokens = step()
     start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
     start.record()
     for _ in range(20):
-        block.step(**args)
+        step()
     end.record()
     torch.cuda.synchronize()
     assert pq2.pq2_last_device_error() == pq2.PQ2_OK

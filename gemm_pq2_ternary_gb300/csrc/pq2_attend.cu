@@ -379,7 +379,7 @@ __device__ __forceinline__ void segment(const pq2h::AttendParams& p, const Atten
         if (in_page >= per_page) in_page -= per_page;
         const uint32_t stage = (ring.count + i) % kStages;
         ring.bad = page < 0 ? ring.bad | (1u << stage) : ring.bad & ~(1u << stage);
-        if (lane != 0) return;
+        if (lane != 0 || static_cast<int>(ring.count + i) == p.ctl.debug_skip_stage) return;
         if (page < 0) {
             mbar_arrive(&ring.bars[stage]);
             return;
