@@ -39,7 +39,12 @@ constexpr int kWarps = D == 256 ? 12 : 8;
 template <int D>
 constexpr int kBlocks = D == 256 ? 1 : 2;
 constexpr int kRows = 8;            // query rows of a pass
-constexpr int kFewRows = 32;        // rows of a sequence and head that this kernel takes, at most
+// Rows of a sequence and head that this kernel takes, at most; more go to
+// pq2_attend_many.cu.  Both, in us (this one first), for heads of 128: 24 sequences of 5003 tokens,
+// 25 rows 184 and 178, 40 rows 219 and 176; one of 30000, 25 rows 49 and 68, 65 rows 90 and
+// 70; two of 700, 25 rows 19 and 31, 200 rows 33 and 43.  For heads of 256 and 24
+// sequences 18 rows 141 and 106, for one 65 rows 78 and 89.
+constexpr int kFewRows = 32;
 constexpr int kExtra = 32;          // what an item takes besides its tiles, in tiles (8: 111 us for 64 sequences, 16: 107,
                                     // 32: 95, 64: 96, 96: 99)
 constexpr float kEmpty = -1e30f;    // maximum of a row that has seen nothing

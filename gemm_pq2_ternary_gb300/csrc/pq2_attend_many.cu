@@ -1,11 +1,11 @@
 // Attention over a cache held in 4 bits, many query rows for each key/value
-// head (prompts, drafts to verify), on tcgen05 with accumulators in tensor memory.
+// head (prompts, chunks of them), on tcgen05 with accumulators in tensor memory.
 //
 // With c' = code - 8, z' = offset + 8 scale:
-//   q . k_j = s_j (q . c'_j + r_j sum(q)),  r_j = z'_j / s_j
+//   q . k_j = s_j (q . c_j + r_j sum(q)),  r_j = offset_j / s_j
 //   sum_j w_j v_j = sum_j (w_j s_j) c'_j + sum_j w_j z'_j
-// Both products run on c' (exact in fp16), the first with one more step of 16
-// for r_j sum(q) (each as two fp16, three of their products).  What is left for the
+// Both products run on codes (exact in fp16; keys' as subnormals c 2^-24, as in
+// pq2_attend.cu), the first with one more step of 16 for r_j sum(q).  What is left for the
 // softmax is one factor per key for the scores (s_j with the softmax scale), and
 // two for the weights (s_j of values, z'_j): keys and values enter as exactly
 // as the cache holds them, only the weights are rounded (to fp16, as in
@@ -14,19 +14,29 @@
 // A CTA works on 256 rows (128 of 256 dims), two accumulators of 128 rows that take
 // turns: the tensor cores multiply for one while the other's weights are computed.
 // Rows are (token, head of the group) pairs, so that a group shares the expanded keys.
-// 16 warps:
-//   0-7   softmax: scores from tensor memory as 16x256b fragments (a lane has
-//         a quarter of the keys of four rows: with a row a lane, every factor would be loaded by every
-//         lane, and shared memory cannot give that), weights back to it as the second
-//         product's first operand; at the end the outputs
-//   8-11  expand codes into a ring of 16 KB chunks: keys K-major (64 dims of 128
-//         keys), values MN-major (as they are: a row of dims per key); both are
-//         128 rows of 128 bytes with the 128-byte swizzle.  A chunk a warp: the waits
-//         and fences of a chunk take as long as its arithmetic for a quarter of it
-//   12    issues the products
-//   13-15 look up pages and compute the keys' factors, a tile of 128 keys each in turn
+// 20 warps:
+//   0-7    softmax: scores from tensor memory as 16x256b fragments (a lane has
+//          a quarter of the keys of four rows: with a row a lane, every factor would be
+//          loaded by every lane, and shared memory cannot give that), weights back to it as
+//          the second product's first operand; at the end the outputs
+//   8-11   expand codes of keys (K-major: 64 dims of 128 keys to 16 KB), and
+//   12-15  of values (MN-major, as they are: a row of dims per key); both are rows of
+//          128 bytes with the 128-byte swizzle, in two buffers each
+//   16     issues the products
+//   17-19  look up pages and compute the keys' factors, a tile of 128 keys each in turn
 // Work is dealt out in tiles of 128 keys as in pq2_attend.cu; a CTA that has
 // only a part of an item's keys writes a partial result, and attend_many_join_kernel joins them.
+//
+// Bound by what happens between the products: with the issuing and expanding warps' waits
+// out of the way a tile takes 5500 cycles of 2100 that its products need (256 dims;
+// 128 dims 6500 of 2200), most of it the softmax of its 128 (256) rows in 8 warps, some
+// 4000 cycles for 1400 instructions a warp.  What held it up before: local memory (arrays
+// indexed at run time, too few registers for a role), operands' descriptors in
+// registers that had to be moved to uniform ones (100 cycles a product), waits one
+// by one, an address read from shared memory before every load of codes, and items that
+// counted for their tiles alone.  On GB300: 4096 tokens behind 4096, 24 heads of 256 on 4:
+// 790 us, 784 TFLOP/s; 3 chunks of up to 1000 tokens behind up to 5000, 40 heads of 128 on 8:
+// 315 us (mma.sync, 8 rows at a time: 4528 and 1250 us).
 #include <algorithm>
 
 #include "pq2_attend.cuh"
@@ -282,7 +292,7 @@ __device__ __forceinline__ Segment segment_at(const pq2h::AttendParams& p, int r
 }
 
 // ---------------------------------------------------------------------------
-// Warps 13-15: pages and factors
+// Warps 17-19: pages and factors
 // ---------------------------------------------------------------------------
 template <int D>
 __device__ __forceinline__ void factors(const Ctl& k, const AttendWork& wk, int row_tiles, AttendSpan span, Slot* slots,
@@ -379,7 +389,7 @@ __device__ __forceinline__ void factors(const Ctl& k, const AttendWork& wk, int 
 }
 
 // ---------------------------------------------------------------------------
-// Warps 8-11: codes to operands
+// Warps 8-15: codes to operands
 // ---------------------------------------------------------------------------
 // Two codes less 8 of four bytes (HIGH: the high halves, times 16).
 template <int HIGH>
@@ -493,7 +503,7 @@ __device__ __forceinline__ void expand(const Ctl& k, const Slot* slots, uint8_t*
 }
 
 // ---------------------------------------------------------------------------
-// Warp 12: the products (one thread)
+// Warp 16: the products (one thread)
 // ---------------------------------------------------------------------------
 // A wait of a barrier that is ready takes some 300 cycles while the expanding warps keep
 // shared memory busy, and the tensor cores run dry meanwhile: all that a step
@@ -987,7 +997,8 @@ __device__ __forceinline__ void softmax(const Ctl& k, const AttendWork& wk, uint
                     float v[8];
                     values(raw[i], v);
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) top = fmaxf(top, fabsf(v[x]));
+                    for (int x = 0; x < 8; ++x)  // (a row with an infinity or a NaN is not the others' concern)
+                        if (fabsf(v[x]) < __uint_as_float(0x7f800000u)) top = fmaxf(top, fabsf(v[x]));
                 }
             }
 #pragma unroll
@@ -1003,7 +1014,7 @@ __device__ __forceinline__ void softmax(const Ctl& k, const AttendWork& wk, uint
             top = __int_as_float(*reinterpret_cast<volatile int*>(&k.bars.top[seg & 1]));
             // all rows times one power of two, the largest value in [1, 2); its
             // inverse goes to the scores' factors
-            const int ex = top > 0.0f ? 127 - static_cast<int>(__float_as_uint(fmaxf(top, 0x1p-100f)) >> 23) : 0;
+            const int ex = top > 0.0f ? max(127 - static_cast<int>(__float_as_uint(fmaxf(top, 0x1p-100f)) >> 23), -126) : 0;
             const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
             if (tid == 0) k.bars.back = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
 #pragma unroll 2

@@ -627,8 +627,10 @@ pq2_status pq2_cache4_read(const pq2_cache4_read_args* args, void* stream);
  * below 0) gives zeros.  Scores, maxima, sums and accumulated outputs are
  * fp32; q enters the products with the 11 bits of its type or the fp16 rounding of its
  * row scaled by a power of two (bf16: no rounding within 2^28 of the row's
- * largest), the weights w times the values' scales as fp16, scaled by powers
- * of two likewise.
+ * largest; where max_rows * q_heads / heads > 32, up to 256 rows of a sequence
+ * are scaled alike, and a value is off by up to 2^-22 of the largest of them),
+ * the weights w times the values' scales as fp16, scaled by powers of two
+ * likewise.
  *   q, out     [M, q_heads, dim] (type: PQ2_F16 or PQ2_BF16), token and head
  *              strides in elements, a head's values adjacent
  *   max_rows   an upper bound of the sequences' rows that the host knows
@@ -753,8 +755,8 @@ pq2_status pq2_group_dots(int op, const int8_t* qp, const int32_t* T, const uint
  * current device's error word: PQ2_ERR_TIMEOUT if a kernel's bounded wait ran
  * out, PQ2_ERR_BOUNDS (bounds-checked build only) if a kernel skipped a store
  * outside its buffer, PQ2_ERR_INVALID_ARG if pq2_pack_weights met a
- * non-ternary value or an index array of pq2_lora_add or pq2_verify_drafts a
- * value outside its range,
+ * non-ternary value or an index array of pq2_lora_add, pq2_verify_drafts, the
+ * rotary positions, the cache or its pages a value outside its range,
  * PQ2_OK otherwise (PQ2_ERR_CUDA if the synchronisation itself failed).
  */
 pq2_status pq2_last_device_error(void* stream);

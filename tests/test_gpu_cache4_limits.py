@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from oracle import attention as ref
+from oracle.step import TINY, UNIT
 from test_gpu_cache4 import Cache, _attend, _check, _dev, _np, _q, _starts
 
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
@@ -118,6 +119,47 @@ class _Part:
 
     def __init__(self, c, b):
         self.T, self.D, self.H, self.pages = c.T, c.D, c.H, c.pages[b:b + 1]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D,n", [(64, 70), (128, 5), (128, 70), (256, 40)])
+def test_rows_with_infinities_stay_among_themselves(pq2, D, n, dtype):
+    ln, G = 200, 2
+    c = Cache(pq2, 1, 13, 1, D, 16)
+    pool = c.fill([ln])
+    q = _q(n, G, D, dtype)
+    bad = q.clone()
+    bad[1, 0, 3] = float("inf")
+    bad[2, 1, D - 1] = float("nan")
+    bad[n - 1, 0, 0] = float("-inf")
+    got = _attend(pq2, c, bad, [n], [ln])
+    assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+    for i, h in ((1, 0), (2, 1), (n - 1, 0)):
+        got[i, h] = 0.0
+    want, tol = ref.attend(_np(q), pool, c.pages, _starts([n]), [ln], 16, D ** -0.5, 0)
+    for i, h in ((1, 0), (2, 1), (n - 1, 0)):
+        want[i, h] = 0.0
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert np.all(err <= tol + np.abs(want) * UNIT[dtype] + TINY[dtype])
+
+
+@pytest.mark.parametrize("D,n", [(64, 70), (128, 70), (256, 40)])
+def test_rows_of_very_different_size(pq2, D, n):
+    # bf16 rows from 2^-60 to 2^60: small ones count as what they are next to the largest
+    ln = 100
+    c = Cache(pq2, 1, 7, 1, D, 16)
+    pool = c.fill([ln], spread=1e-3)
+    q = _q(n, 2, D, "bf16")
+    q = (q.float() * torch.exp2(torch.arange(n, device=DEV).float()[:, None, None] * (120.0 / n) - 60.0)).bfloat16()
+    got = _attend(pq2, c, q, [n], [ln], scale=2.0 ** -58)
+    assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+    want, tol = ref.attend(_np(q), pool, c.pages, _starts([n]), [ln], 16, 2.0 ** -58, 0)
+    # a value of q is off by up to 2^-22 of the largest, so a score by D k 2^-22 times the scale
+    kmax = max(np.abs(ref.read_rows(pool, c.pages[0], ln, 0, 16, D)[1].astype(np.float64)).max() * 16, 1e-30)
+    off = 2.0 ** -22 * float(q.float().abs().max()) * 2.0 ** -58 * D * kmax
+    vmax = np.abs(want).max() + 1e-2
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert np.all(err <= tol + np.abs(want) * UNIT["bf16"] + TINY["bf16"] + 2 * off * vmax)
 
 
 # --- the bounds-checked build ---------------------------------------------
