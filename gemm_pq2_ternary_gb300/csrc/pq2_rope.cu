@@ -373,43 +373,64 @@ __global__ void __launch_bounds__(kThreads) any_head_kernel(const __grid_constan
     }
 }
 
-// The cache's values of a call's token rows: a warp per row of D values.
+// The cache's values of a call's token rows: a warp takes a part of a token's
+// rows of D values (all of them in long calls), kReads at a time.
+constexpr int kReads = 4;
+
 template <int E, bool VEC>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ pq2h::RopeParams p) {
     constexpr int D = 32 * E;
     const int lane = threadIdx.x & 31;
     const int slots = p.heads[0] + p.heads[1];
-    const long long total = p.M * slots;
+    const int per_part = ((slots + kReads - 1) / kReads + p.parts - 1) / p.parts * kReads;
+    const long long total = p.M * p.parts;
     pdl_wait();
     pdl_launch_dependents();
     for (long long w = blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5); w < total;
          w += static_cast<long long>(gridDim.x) * kWarps) {
-        const long long row = w / slots;
-        int h = static_cast<int>(w - row * slots), k = 0;
-        if (h >= p.heads[0]) h -= p.heads[0], k = 1;
+        const long long row = p.parts == 1 ? w : w / p.parts;
+        const int first = static_cast<int>(w - row * p.parts) * per_part, end = min(first + per_part, slots);
+        if (first >= end) continue;
         bool mine;
         const Place place = place_of(p.cache, static_cast<int>(row), p.ctl, mine);
         if (!mine || place.page < 0) continue;
         const int T = p.cache.T, t = static_cast<int>(place.pos % T);
-        const int value = p.read_kind[k];
-        const uint8_t* tile = p.cache.pool + place.page * p.cache.page_stride +
-                              (h * static_cast<long long>(T / kTileTokens) + t / kTileTokens) * tile_bytes(D);
-        const uint8_t* at = tile + tile_codes(D, value) + (t % kTileTokens) * (D / 2) + lane * (E / 2);
-        uint32_t codes;
-        if constexpr (E == 8)
-            codes = *reinterpret_cast<const uint32_t*>(at);
-        else if constexpr (E == 4)
-            codes = *reinterpret_cast<const uint16_t*>(at);
-        else
-            codes = *at;
-        const uint32_t pair = *reinterpret_cast<const uint32_t*>(tile + tile_pairs(D, value) + (t % kTileTokens) * 4);
-        const float s = elem_to_f32(pair & 0xffffu, PQ2_F16), z = elem_to_f32(pair >> 16, PQ2_F16);
-        float v[E];
+        const long long head_bytes = static_cast<long long>(T / kTileTokens) * tile_bytes(D);
+        const uint8_t* tile = p.cache.pool + place.page * p.cache.page_stride + t / kTileTokens * tile_bytes(D);
+        int off = 0;
+#pragma unroll 1
+        for (int k = 0; k < 2; off += p.heads[k], ++k) {
+            const int h1 = min(end - off, p.heads[k]), value = p.read_kind[k];
+            const int code_at = tile_codes(D, value) + (t % kTileTokens) * (D / 2) + lane * (E / 2);
+            const int pair_at = tile_pairs(D, value) + (t % kTileTokens) * 4;
+#pragma unroll 1
+            for (int h = max(first - off, 0); h < h1; h += kReads) {
+                uint32_t codes[kReads], pair[kReads];
 #pragma unroll
-        for (int j = 0; j < E; ++j)  // (code * scale is exact: 4 + 11 bits)
-            v[j] = __fadd_rn(__fmul_rn(static_cast<float>((codes >> (4 * j)) & 15u), s), z);
-        const long long out = row * p.ldo[k] + h * p.hso[k] + lane * E;
-        if (store_ok(p.ctl, out, E, p.out_elems[k])) store_elems<E, VEC>(p.out[k], p.out_type, out, v);
+                for (int i = 0; i < kReads; ++i) {
+                    if (h + i >= h1) continue;
+                    const uint8_t* at = tile + (h + i) * head_bytes;
+                    if constexpr (E == 8)
+                        codes[i] = *reinterpret_cast<const uint32_t*>(at + code_at);
+                    else if constexpr (E == 4)
+                        codes[i] = *reinterpret_cast<const uint16_t*>(at + code_at);
+                    else
+                        codes[i] = at[code_at];
+                    pair[i] = *reinterpret_cast<const uint32_t*>(at + pair_at);
+                }
+#pragma unroll
+                for (int i = 0; i < kReads; ++i) {
+                    if (h + i >= h1) continue;
+                    const float s = elem_to_f32(pair[i] & 0xffffu, PQ2_F16), z = elem_to_f32(pair[i] >> 16, PQ2_F16);
+                    float v[E];
+#pragma unroll
+                    for (int j = 0; j < E; ++j)  // (code * scale is exact: 4 + 11 bits)
+                        v[j] = __fadd_rn(__fmul_rn(static_cast<float>((codes[i] >> (4 * j)) & 15u), s), z);
+                    const long long out = row * p.ldo[k] + (h + i) * p.hso[k] + lane * E;
+                    if (store_ok(p.ctl, out, E, p.out_elems[k])) store_elems<E, VEC>(p.out[k], p.out_type, out, v);
+                }
+            }
+        }
     }
 }
 
@@ -479,15 +500,18 @@ bool vector_path(const RopeParams& p, int E, bool cache) {
 
 constexpr long long kEnoughWarps = 152 * 48;  // (four times as many: 88 us for 5105 tokens of 64 heads, not 75)
 
+// Warps for each of M tokens: a token's place and angles are found once for all
+// its heads where there are tokens enough to keep all SMs busy.
+int parts_for(long long M, int slots, int at_once) {
+    const long long most = std::max((slots + at_once - 1) / at_once, 1);
+    return static_cast<int>(std::min(most, std::max(kEnoughWarps / std::max(M, 1ll), 1ll)));
+}
+
 template <int E, bool CACHE>
 cudaError_t launch_heads(const RopeParams& args, cudaStream_t st) {
     RopeParams p = args;
     const int slots = p.heads[0] + p.heads[1] + p.heads[2];
-    // a token's place and angles are found once for all its heads where there are
-    // tokens enough to keep all SMs busy
-    p.parts = static_cast<int>(std::min<long long>((slots + pq2::kSlots - 1) / pq2::kSlots,
-                                                   std::max<long long>(kEnoughWarps / std::max<long long>(p.M, 1), 1)));
-    p.parts = std::max(p.parts, 1);
+    p.parts = parts_for(p.M, slots, pq2::kSlots);
     const unsigned grid = grid_for(p.M * p.parts);
     const auto go = [&](auto kernel) { return launch(kernel, dim3(grid), dim3(pq2::kThreads), 0, st, true, p); };
     if (!vector_path(p, E, CACHE)) return go(pq2::head_kernel<E, pq2::kAny, CACHE>);
@@ -497,8 +521,10 @@ cudaError_t launch_heads(const RopeParams& args, cudaStream_t st) {
 }
 
 template <int E>
-cudaError_t launch_read(const RopeParams& p, cudaStream_t st) {
-    const unsigned grid = grid_for(p.M * (p.heads[0] + p.heads[1]));
+cudaError_t launch_read(const RopeParams& args, cudaStream_t st) {
+    RopeParams p = args;
+    p.parts = parts_for(p.M, p.heads[0] + p.heads[1], pq2::kReads);
+    const unsigned grid = grid_for(p.M * p.parts);
     bool vec = true;
     for (int k = 0; k < 2; ++k)
         if (p.heads[k]) vec = vec && fits(p.out[k], p.ldo[k], p.hso[k], E, size_of(p.out_type));
