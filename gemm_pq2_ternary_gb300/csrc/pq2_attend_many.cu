@@ -52,8 +52,10 @@ constexpr int kSlots = 4;                 // tiles whose factors are held
 constexpr int kExtra = 6;                 // what an item's queries and outputs take, in tiles (2: 390 us for
                                           // chunks behind 6000 tokens, 3: 333, 4: 324, 6: 316)
 constexpr float kEmpty = -1e30f;
-constexpr float kSlack = 5.0f;
-constexpr float kWeight = 512.0f;
+// (Larger and smaller than pq2_attend.cu's 5 and 512: a raise touches all outputs in
+// tensor memory.  A prompt took 862, 776 and 731 us with 2, 5 and 8, chunks 356, 315 and 296.)
+constexpr float kSlack = 8.0f;
+constexpr float kWeight = 64.0f;
 constexpr int kExpandWarps = 8;
 constexpr int kFactorWarps = 3;
 constexpr int kIssuer = 16;

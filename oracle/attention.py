@@ -116,9 +116,9 @@ def attend(q, pool, pages, row_start, lens, T, scale, window=0):
     rounding).  The bound: weights rounded to 11 bits (2^-11 of their share),
     scores off by fp32 sums of D products, exponentials by 2^-21, sums of
     tiles cut off at 24 bits.  Below fp16's normal numbers a weight is off by up
-    to half a step of 2^-24 instead: weights stand for w s / ref 512 there, where ref <= the
+    to half a step of 2^-24 instead: weights stand for w s / ref 64 there, where ref <= the
     largest scale s and the largest w >= 1/2, codes are at most 8 off the middle, so
-    that each key adds up to 2^-25 / 512 s 8 / (1/2) = s 2^-30."""
+    that each key adds up to 2^-25 / 64 s 8 / (1/2) = s 2^-27."""
     q = np.asarray(q, np.float64)
     M, Hq, D = q.shape
     H = pool.shape[1]
@@ -154,7 +154,7 @@ def attend(q, pool, pages, row_start, lens, T, scale, window=0):
                     tol[r0 + i, h * (Hq // H) + g] = (
                         w @ mid[at] * (2.0 ** -11 + tiles * 2.0 ** -23 + 2 * off) +
                         w @ rest[at] * (tiles * 2.0 ** -23 + 2 * off) + np.abs(o) * (2 * off + tiles * 2.0 ** -24)) + (
-                        (pos + 1 - lo) * s[1][at].max() * 2.0 ** -30)
+                        (pos + 1 - lo) * s[1][at].max() * 2.0 ** -27)
     return out, tol
 
 
