@@ -13,40 +13,53 @@
 // would leave sums many times the result, and the tensor cores cut off sums' low bits (over
 // 131071 tokens 7e-4 of the result was lost, with codes around 0 nothing).
 //
-// Bound by HBM: (D + 8) bytes a token and head, each read once.  Scores are computed as
-// K q^T (m16n8k16: 16 keys by 8 query rows), outputs as V^T w^T (16 dims by 8
-// rows), so that up to 8 rows (a group of query heads) share one pass over the codes.
-// A warp takes tiles of 16 tokens straight from memory into registers,
-// two tiles ahead, with a maximum, sums and outputs of its own.  Maxima are
-// raised only when a score exceeds the present one by 2^kSlack (a vote, not a
-// reduction per tile): weights stay below 32, and times the values' scales (over a
-// power of two, raised likewise, below 2) times kWeight below 2^15, with 2^-26
-// of the largest still at fp16's full precision.
+// Has to read (D + 8) bytes a token and head once.  Scores are computed as K q^T
+// (m16n8k16: 16 keys by 8 query rows), outputs as V^T w^T (16 dims by 8 rows), so
+// that up to 8 rows (a group of query heads), or 16 in two products, share one pass over
+// the codes.  A warp takes tiles of 16 tokens from a ring of its own in shared memory, which
+// bulk copies fill three tiles ahead, with a maximum, sums and outputs of its own.
+// Maxima are raised only when a score exceeds the present one by 2^kSlack (a vote,
+// not a reduction per tile): weights stay below 32, and times the values' scales (over
+// a power of two, raised likewise, below 2) times kWeight below 2^15, with weights down to
+// 2^-23 at fp16's full precision.
 //
-// The tiles of all sequences and heads form one list, dealt out evenly to the CTAs.
-// A CTA joins its warps' results in shared memory; a head whose tiles lie
-// in several CTAs is joined by a second kernel, in the CTAs' order.
+// The tiles of all sequences and heads form one list, dealt out evenly to the CTAs;
+// an item (a sequence's tile of rows and head) counts for kExtra tiles more.  A CTA joins its warps'
+// results in shared memory; a head whose tiles lie in several CTAs is joined by a second
+// kernel, in the CTAs' order.
+//
+// Bound by instructions and their latency: some 340 a tile of 16 tokens and head, most of
+// them on the integer pipe (operands from codes), issued at 52% of the rate.  On GB300: 131071
+// tokens, 24 heads of 256 on 4: 44 us, 3.1 TB/s (58 with loads into registers, 8 warps an
+// SM and a join of one warp's loads at a time); 64 sequences of up to 8192, 48 heads of 128 on
+// 8: 94 us, 3.0 TB/s (107 to 147 while the list counted tiles alone and registers were
+// spilled); 24 sequences of up to 5003 with 5 tokens each, 40 heads of 128 on 8: 57 us (62
+// with 8 rows a pass).
 #include <algorithm>
+#include <type_traits>
 
 #include "pq2_attend.cuh"
 
 namespace pq2 {
 namespace {
 
+// A pass takes RG groups of 8 query rows: two of them share a tile's operands.
 // Warps of a CTA and CTAs of an SM: as many as registers allow.
-template <int D>
-constexpr int kWarps = D == 256 ? 12 : 8;
+template <int D, int RG>
+constexpr int kWarps = D == 256 && RG == 1 ? 12 : 8;
 template <int D>
 constexpr int kBlocks = D == 256 ? 1 : 2;
-constexpr int kRows = 8;            // query rows of a pass
 // Rows of a sequence and head that this kernel takes, at most; more go to
-// pq2_attend_many.cu.  Both, in us (this one first), for heads of 128: 24 sequences of 5003 tokens,
-// 25 rows 184 and 178, 40 rows 219 and 176; one of 30000, 25 rows 49 and 68, 65 rows 90 and
-// 70; two of 700, 25 rows 19 and 31, 200 rows 33 and 43.  For heads of 256 and 24
-// sequences 18 rows 141 and 106, for one 65 rows 78 and 89.
-constexpr int kFewRows = 32;
-constexpr int kExtra = 32;          // what an item takes besides its tiles, in tiles (8: 111 us for 64 sequences, 16: 107,
-                                    // 32: 95, 64: 96, 96: 99)
+// pq2_attend_many.cu.  Both, in us (this one first).  24 sequences of 5003 tokens: heads of
+// 128, 25 rows 120 and 166, 40 rows 161 and 164, 65 rows 246 and 166; of 256, 18 rows 111 and
+// 106, 30 rows 111 and 108, 48 rows 151 and 109; of 64, 48 rows 112 and 125, 64 rows 141 and
+// 130.  One sequence of 30000: heads of 128, 50 rows 62 and 65; of 256, 78 rows 70 and 90.
+constexpr int few_rows(int64_t dim) { return dim == 256 ? 32 : 48; }
+constexpr int kMostRows = 16;       // of a pass
+// What an item takes besides its tiles, in tiles (64 sequences, 8 rows: 8 111 us, 16 107, 32 95,
+// 64 96, 96 99; drafts, 25 rows: 16 69 us, 32 59, 48 57).
+template <int RG>
+constexpr int kExtra = RG == 1 ? 32 : 48;
 constexpr float kEmpty = -1e30f;    // maximum of a row that has seen nothing
 constexpr float kSlack = 5.0f;      // how far (as a power of two) a score may exceed the maximum
 constexpr float kWeight = 512.0f;  // weights enter the product times this
@@ -109,40 +122,44 @@ __device__ __forceinline__ float pair_offset(uint32_t p) { return __half2float(_
 
 // What a warp holds of 8 query rows.  Columns of the products are rows of
 // queries: a lane has rows 2t and 2t + 1 of maxima, sums and outputs.
-template <int D>
+template <int D, int RG>
 struct Rows {
-    uint4 q[D <= 128 ? D / 32 : 1];  // as products' operands; of 256 dims they stay in shared memory
-    float fq[2], sq[2];     // factor of the products, sum of the row (both in powers of two: times log2 e)
-    int first[2], last[2];  // positions that the row sees
-    float m[2], l[2], z[2]; // maximum, sum of weights, sum of weights times offsets
-    float ref;              // values' scales over this (a power of two) are below 2
-    float o[D / 16][4];     // outputs: dims 2j and 2j + 1 (times 16) of the lane's eighth
-    __device__ __forceinline__ uint4 query(const uint4* shared, int w) const {
-        if constexpr (D <= 128)
-            return q[w];
+    static constexpr bool kShared = D == 256 || RG == 2;  // products' operands stay in shared memory
+    uint4 q[kShared ? 1 : D / 32];
+    float fq[RG][2], sq[RG][2];      // factor of the products, sum of the row (both in powers of two: times log2 e)
+    int first[RG][2], last[RG][2];   // positions that the row sees
+    float m[RG][2], l[RG][2], z[RG][2];  // maximum, sum of weights, sum of weights times offsets
+    float ref;                       // values' scales over this (a power of two) are below 2
+    float o[RG][D / 16][4];          // outputs: dims 2j and 2j + 1 (times 16) of the lane's eighth
+    __device__ __forceinline__ uint4 query(const uint4* shared, int u, int w) const {
+        if constexpr (kShared)
+            return shared[32 * (u * (D / 32) + w)];
         else
-            return shared[32 * w];
+            return q[w];
     }
 };
 
-template <int D>
-__device__ __forceinline__ void clear(Rows<D>& r) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) r.m[c] = kEmpty, r.l[c] = 0.0f, r.z[c] = 0.0f;
+template <int D, int RG>
+__device__ __forceinline__ void clear(Rows<D, RG>& r) {
     r.ref = 0x1p-24f;
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j)
+    for (int u = 0; u < RG; ++u) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r.o[j][i] = 0.0f;
+        for (int c = 0; c < 2; ++c) r.m[u][c] = kEmpty, r.l[u][c] = 0.0f, r.z[u][c] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r.o[u][j][i] = 0.0f;
+    }
 }
 
 // The query rows of item `it`: lane (g, t) loads quarter t of row g.  `q`: the
 // lane's place for those of 256 dims.
-template <int D>
-__device__ __forceinline__ void load_rows(Rows<D>& r, uint4* q, const pq2h::AttendParams& p, const AttendItem& it, int g,
-                                          int t) {
+template <int D, int RG>
+__device__ __forceinline__ void load_rows(Rows<D, RG>& r, uint4* q, const pq2h::AttendParams& p, const AttendItem& it, int u,
+                                          int g, int t) {
     const int G = p.q_heads / p.cache.heads;
-    const int i = it.row_tile * kRows + g, token = i / G;
+    const int i = it.row_tile * 8 * RG + 8 * u + g, token = i / G;
     const bool there = token < it.n;
     float v[D / 32][8];
     float top = 0.0f, sum = 0.0f;
@@ -182,21 +199,21 @@ __device__ __forceinline__ void load_rows(Rows<D>& r, uint4* q, const pq2h::Atte
         for (int k = 0; k < 8; ++k) v[w][k] *= up;
         const uint4 b = make_uint4(half2_bits(v[w][0], v[w][4]), half2_bits(v[w][1] * 0.0625f, v[w][5] * 0.0625f),
                                    half2_bits(v[w][2], v[w][6]), half2_bits(v[w][3] * 0.0625f, v[w][7] * 0.0625f));
-        if constexpr (D <= 128)
+        if constexpr (!Rows<D, RG>::kShared)
             r.q[w] = b;
         else if (threadIdx.x < 32)  // (all warps have the same)
-            q[32 * w] = b;
+            q[32 * (u * (D / 32) + w)] = b;
     }
     const float k = p.scale * 1.4426950408889634f;
     const float f = k * 0x1p24f / up, s = k * sum;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         // row 2t + c is held by lanes (2t + c, *)
-        r.fq[c] = __shfl_sync(0xffffffffu, f, (2 * t + c) * 4);
-        r.sq[c] = __shfl_sync(0xffffffffu, s, (2 * t + c) * 4);
-        const int token_c = (it.row_tile * kRows + 2 * t + c) / G;
-        r.last[c] = token_c < it.n ? it.pos0 + token_c : it.pos0 + it.n - 1;
-        r.first[c] = p.window > 0 ? r.last[c] - p.window + 1 : 0;
+        r.fq[u][c] = __shfl_sync(0xffffffffu, f, (2 * t + c) * 4);
+        r.sq[u][c] = __shfl_sync(0xffffffffu, s, (2 * t + c) * 4);
+        const int token_c = (it.row_tile * 8 * RG + 8 * u + 2 * t + c) / G;
+        r.last[u][c] = token_c < it.n ? it.pos0 + token_c : it.pos0 + it.n - 1;
+        r.first[u][c] = p.window > 0 ? r.last[u][c] - p.window + 1 : 0;
     }
 }
 
@@ -204,20 +221,8 @@ __device__ __forceinline__ void load_rows(Rows<D>& r, uint4* q, const pq2h::Atte
 __device__ __forceinline__ float inverse(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 
 // Raises maxima and the values' reference where this tile needs it.
-template <int D>
-__device__ __forceinline__ void raise(Rows<D>& r, const float (&x)[2][2], const float (&s)[2]) {
-    float alpha[2];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        float top = fmaxf(x[0][c], x[1][c]);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        top = fmaxf(top, r.m[c]);
-        alpha[c] = ex2(r.m[c] - top);
-        r.m[c] = top;
-        r.l[c] *= alpha[c];
-        r.z[c] *= alpha[c];
-    }
+template <int D, int RG>
+__device__ __forceinline__ void raise(Rows<D, RG>& r, const float (&x)[RG][2][2], const float (&s)[2]) {
     float ref = fmaxf(fmaxf(s[0], s[1]), r.ref);
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
@@ -225,16 +230,31 @@ __device__ __forceinline__ void raise(Rows<D>& r, const float (&x)[2][2], const 
     const float down = r.ref * inverse(ref);
     r.ref = ref;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float a = alpha[i & 1] * down;
+    for (int u = 0; u < RG; ++u) {
+        float alpha[2];
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) r.o[j][i] *= a;
+        for (int c = 0; c < 2; ++c) {
+            float top = fmaxf(x[u][0][c], x[u][1][c]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            top = fmaxf(top, r.m[u][c]);
+            alpha[c] = ex2(r.m[u][c] - top);
+            r.m[u][c] = top;
+            r.l[u][c] *= alpha[c];
+            r.z[u][c] *= alpha[c];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = alpha[i & 1] * down;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) r.o[u][j][i] *= a;
+        }
     }
 }
 
 // Tokens key0 .. key0 + 15, in shared memory, into the warp's rows.
-template <int D>
-__device__ __forceinline__ void take_tile(Rows<D>& r, const uint4* q, const uint8_t* tile, int key0, bool inside, int g,
+template <int D, int RG>
+__device__ __forceinline__ void take_tile(Rows<D, RG>& r, const uint4* q, const uint8_t* tile, int key0, bool inside, int g,
                                           int t) {
     uint32_t k[2][D / 32], kp[2], vp[2];
 #pragma unroll
@@ -244,14 +264,20 @@ __device__ __forceinline__ void take_tile(Rows<D>& r, const uint4* q, const uint
         kp[i] = reinterpret_cast<const uint32_t*>(tile + tile_pairs(D, 0))[key];
         vp[i] = reinterpret_cast<const uint32_t*>(tile + tile_pairs(D, 1))[key];
     }
-    float a[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+    float a[RG][2][4];
+#pragma unroll
+    for (int u = 0; u < RG; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[u][i >> 2][i & 3] = 0.0f;
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
-        const uint32_t k0 = k[0][w], k1 = k[1][w];
-        const uint4 b = r.query(q, w);
-        mma16816(a[0], k0 & 0x000f000fu, k1 & 0x000f000fu, k0 & 0x00f000f0u, k1 & 0x00f000f0u, b.x, b.y);
-        const uint32_t h0 = k0 >> 8, h1 = k1 >> 8;
-        mma16816(a[1], h0 & 0x000f000fu, h1 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x00f000f0u, b.z, b.w);
+        const uint32_t k0 = k[0][w], k1 = k[1][w], h0 = k0 >> 8, h1 = k1 >> 8;
+#pragma unroll
+        for (int u = 0; u < RG; ++u) {
+            const uint4 b = r.query(q, u, w);
+            mma16816(a[u][0], k0 & 0x000f000fu, k1 & 0x000f000fu, k0 & 0x00f000f0u, k1 & 0x00f000f0u, b.x, b.y);
+            mma16816(a[u][1], h0 & 0x000f000fu, h1 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x00f000f0u, b.z, b.w);
+        }
     }
     // (in flight meanwhile)
     uint32_t v[4][D / 64];
@@ -260,15 +286,17 @@ __device__ __forceinline__ void take_tile(Rows<D>& r, const uint4* q, const uint
         const int key = key_of(2 * t + (i & 1) + 8 * (i >> 1));
         load_words(v[i], tile + tile_codes(D, 1) + key * (D / 2) + g * (D / 16));
     }
-    float y[2][2], s[2], z[2];
+    float y[RG][2][2], s[2], z[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         s[i] = pair_scale(vp[i]);
         z[i] = pair_offset(vp[i]);
         const float ks = pair_scale(kp[i]), kz = pair_offset(kp[i]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-            y[i][c] = fmaf(a[0][2 * i + c] + a[1][2 * i + c], ks * r.fq[c], kz * r.sq[c]);
+        for (int u = 0; u < RG; ++u)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                y[u][i][c] = fmaf(a[u][0][2 * i + c] + a[u][1][2 * i + c], ks * r.fq[u][c], kz * r.sq[u][c]);
     }
     if (!inside) {
         // tokens that a row does not see; what lies behind a sequence's last
@@ -278,30 +306,38 @@ __device__ __forceinline__ void take_tile(Rows<D>& r, const uint4* q, const uint
             const int key = key0 + key_of(g) + 8 * i;
             bool seen = false;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const bool in = key >= r.first[c] && key <= r.last[c];
-                if (!in) y[i][c] = __uint_as_float(0xff800000u);
-                seen |= in;
-            }
+            for (int u = 0; u < RG; ++u)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const bool in = key >= r.first[u][c] && key <= r.last[u][c];
+                    if (!in) y[u][i][c] = __uint_as_float(0xff800000u);
+                    seen |= in;
+                }
             if (!seen) s[i] = 0.0f, z[i] = 0.0f;
         }
     }
-    const bool more = y[0][0] > r.m[0] + kSlack || y[1][0] > r.m[0] + kSlack || y[0][1] > r.m[1] + kSlack ||
-                      y[1][1] > r.m[1] + kSlack || s[0] >= 2.0f * r.ref || s[1] >= 2.0f * r.ref;
-    if (__any_sync(0xffffffffu, more)) raise<D>(r, y, s);
+    bool more = s[0] >= 2.0f * r.ref || s[1] >= 2.0f * r.ref;
+#pragma unroll
+    for (int u = 0; u < RG; ++u)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) more |= fmaxf(y[u][0][c], y[u][1][c]) > r.m[u][c] + kSlack;
+    if (__any_sync(0xffffffffu, more)) raise<D, RG>(r, y, s);
     const float f = kWeight * inverse(r.ref);
-    uint32_t b[2];
+    uint32_t b[RG][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        float w[2];
+        const float sf = s[i] * f, zf = fmaf(8.0f, s[i], z[i]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            w[c] = ex2(y[i][c] - r.m[c]);
-            r.l[c] += w[c];
-            r.z[c] = fmaf(w[c], fmaf(8.0f, s[i], z[i]), r.z[c]);
+        for (int u = 0; u < RG; ++u) {
+            float w[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                w[c] = ex2(y[u][i][c] - r.m[u][c]);
+                r.l[u][c] += w[c];
+                r.z[u][c] = fmaf(w[c], zf, r.z[u][c]);
+            }
+            b[u][i] = transpose8x8(half2_bits(w[0] * sf, w[1] * sf));
         }
-        const float sf = s[i] * f;
-        b[i] = transpose8x8(half2_bits(w[0] * sf, w[1] * sf));
     }
 #pragma unroll
     for (int w = 0; w < D / 64; ++w) {
@@ -309,10 +345,13 @@ __device__ __forceinline__ void take_tile(Rows<D>& r, const uint4* q, const uint
         for (int h = 0; h < 2; ++h) {
             const uint32_t lo = __byte_perm(v[0][w], v[1][w], h ? 0x7632 : 0x5410);
             const uint32_t hi = __byte_perm(v[2][w], v[3][w], h ? 0x7632 : 0x5410);
-            mma16816(r.o[w * 4 + 2 * h], centred<0>(lo), centred<1>(lo), centred<0>(hi), centred<1>(hi), b[0], b[1]);
+            const uint32_t a0 = centred<0>(lo), a1 = centred<1>(lo), a2 = centred<0>(hi), a3 = centred<1>(hi);
+#pragma unroll
+            for (int u = 0; u < RG; ++u) mma16816(r.o[u][w * 4 + 2 * h], a0, a1, a2, a3, b[u][0], b[u][1]);
             const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
-            mma16816(r.o[w * 4 + 2 * h + 1], centred<0>(lo8), centred<1>(lo8), centred<0>(hi8), centred<1>(hi8), b[0],
-                     b[1]);
+            const uint32_t c0 = centred<0>(lo8), c1 = centred<1>(lo8), c2 = centred<0>(hi8), c3 = centred<1>(hi8);
+#pragma unroll
+            for (int u = 0; u < RG; ++u) mma16816(r.o[u][w * 4 + 2 * h + 1], c0, c1, c2, c3, b[u][0], b[u][1]);
         }
     }
 }
@@ -328,14 +367,15 @@ template <int D>
 constexpr size_t ring_bytes() {
     return static_cast<size_t>(kStages) * tile_bytes(D);
 }
-template <int D>
+template <int D, int RG>
 constexpr size_t q_at() {
-    const size_t rings = kWarps<D> * ring_bytes<D>(), join = static_cast<size_t>(kWarps<D>) * kRows * (so_row<D>() + 2) * 4;
+    const size_t rings = kWarps<D, RG> * ring_bytes<D>();
+    const size_t join = static_cast<size_t>(kWarps<D, RG>) * 8 * RG * (so_row<D>() + 2) * 4;
     return (rings > join ? rings : join) + 15 & ~size_t(15);
 }
-template <int D>
+template <int D, int RG>
 constexpr size_t smem_bytes() {
-    return q_at<D>() + (D == 256 ? D * 16 : 0);
+    return q_at<D, RG>() + (Rows<D, RG>::kShared ? RG * D * 16 : 0);
 }
 
 // A warp's tiles of a segment on their way through its ring: contiguous in memory, so
@@ -352,18 +392,19 @@ struct Ring {
 // The segment of item `it` in tiles [t0, t1): every warp its own tiles, then
 // joined.  `whole`: all of the item (the outputs are final), else its partial
 // result goes to `slot`.
-template <int D>
+template <int D, int RG>
 __device__ __forceinline__ void segment(const pq2h::AttendParams& p, const AttendWork& wk, const AttendItem& it, int t0,
                                         int t1, bool whole, int slot, uint8_t* shared, Ring& ring) {
+    constexpr int kW = kWarps<D, RG>, kR = 8 * RG;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int per_page = p.cache.T / kTileTokens;
     const long long head_at = static_cast<long long>(it.head) * per_page * tile_bytes(D);
-    const int mine = t1 - t0 > warp ? (t1 - t0 - warp + kWarps<D> - 1) / kWarps<D> : 0;
+    const int mine = t1 - t0 > warp ? (t1 - t0 - warp + kW - 1) / kW : 0;
     // tiles that every row sees all of
     const int in0 = it.first_hi, in1 = it.last_lo;
     int page_lane = 0;
     const auto look_up = [&](int i) {  // pages of the warp's tiles i .. i + 31, one a lane
-        const int tile = t0 + warp + kWarps<D> * (i + lane);
+        const int tile = t0 + warp + kW * (i + lane);
         int page = -1;
         if (tile < t1) {
             page = __ldg(p.cache.pages + it.b * p.cache.ld_pages + tile / per_page);
@@ -375,7 +416,7 @@ __device__ __forceinline__ void segment(const pq2h::AttendParams& p, const Atten
         page_lane = page;
     };
     // tiles are asked for in order: the next one's place in its page
-    const int step = kWarps<D> % per_page;
+    const int step = kW % per_page;
     int in_page = (t0 + warp) % per_page;
     const auto fetch = [&](int i) {
         if ((i & 31) == 0) look_up(i);
@@ -411,11 +452,12 @@ __device__ __forceinline__ void segment(const pq2h::AttendParams& p, const Atten
     __syncthreads();
     if (!ring.stuck)
         for (int i = 0; i < min(kStages - 1, mine); ++i) fetch(i);
-    Rows<D> r;
-    uint4* q = reinterpret_cast<uint4*>(shared + q_at<D>()) + lane;
-    load_rows<D>(r, q, p, it, g, t);
-    clear<D>(r);
-    if constexpr (D == 256) __syncthreads();
+    Rows<D, RG> r;
+    uint4* q = reinterpret_cast<uint4*>(shared + q_at<D, RG>()) + lane;
+#pragma unroll
+    for (int u = 0; u < RG; ++u) load_rows<D, RG>(r, q, p, it, u, g, t);
+    clear<D, RG>(r);
+    if constexpr (Rows<D, RG>::kShared) __syncthreads();
 #pragma unroll 1
     for (int i = 0; i < mine && !ring.stuck; ++i) {
         if (i + kStages - 1 < mine) fetch(i + kStages - 1);
@@ -426,71 +468,75 @@ __device__ __forceinline__ void segment(const pq2h::AttendParams& p, const Atten
             ring.stuck = true;
             break;
         }
-        const int key0 = (t0 + warp + kWarps<D> * i) * kTileTokens;
+        const int key0 = (t0 + warp + kW * i) * kTileTokens;
         if (!(ring.bad >> stage & 1))
-            take_tile<D>(r, q, ring.at + stage * tile_bytes(D), key0, key0 >= in0 && key0 + kTileTokens - 1 <= in1, g, t);
+            take_tile<D, RG>(r, q, ring.at + stage * tile_bytes(D), key0, key0 >= in0 && key0 + kTileTokens - 1 <= in1, g, t);
         __syncwarp();
     }
     ring.count += mine;
     float* smem = reinterpret_cast<float*>(shared);
     // the warps' results: [warp][row][D] with maxima and sums behind them
     float* so = smem;
-    float* sm = smem + kWarps<D> * kRows * so_row<D>();
-    float* sl = sm + kWarps<D> * kRows;
+    float* sm = smem + kW * kR * so_row<D>();
+    float* sl = sm + kW * kR;
     __syncthreads();  // (other warps' tiles)
     const float f = r.ref / kWeight;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int u = 0; u < RG; ++u)
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-            r.l[c] += __shfl_xor_sync(0xffffffffu, r.l[c], o);
-            r.z[c] += __shfl_xor_sync(0xffffffffu, r.z[c], o);
+        for (int c = 0; c < 2; ++c) {
+            float l = r.l[u][c], z = r.z[u][c];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                l += __shfl_xor_sync(0xffffffffu, l, o);
+                z += __shfl_xor_sync(0xffffffffu, z, o);
+            }
+            const int row = warp * kR + 8 * u + 2 * t + c;
+            if (g == 0) sm[row] = r.m[u][c], sl[row] = l;
+            float* to = so + row * so_row<D>() + g * (D / 8);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+                *reinterpret_cast<float2*>(to + 2 * j) =
+                    make_float2(fmaf(r.o[u][j][c], f, z), fmaf(r.o[u][j][2 + c], f * 0.0625f, z));
         }
-        const int row = warp * kRows + 2 * t + c;
-        if (g == 0) sm[row] = r.m[c], sl[row] = r.l[c];
-        float* to = so + row * so_row<D>() + g * (D / 8);
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j)
-            *reinterpret_cast<float2*>(to + 2 * j) =
-                make_float2(fmaf(r.o[j][c], f, r.z[c]), fmaf(r.o[j][2 + c], f * 0.0625f, r.z[c]));
-    }
     __syncthreads();
     // warp w joins row w, a lane D / 32 dims of it
-    const int row = warp;
-    if (row >= kRows) return;
+    for (int row = warp; row < kR; row += kW) {
     float m = kEmpty;
 #pragma unroll
-    for (int w = 0; w < kWarps<D>; ++w) m = fmaxf(m, sm[w * kRows + row]);
+    for (int w = 0; w < kW; ++w) m = fmaxf(m, sm[w * kR + row]);
     float l = 0.0f, o[D / 32];
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) o[j] = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps<D>; ++w) {
-        const float a = ex2(sm[w * kRows + row] - m);
-        l = fmaf(a, sl[w * kRows + row], l);
-        const float* from_w = so + (w * kRows + row) * so_row<D>() + lane * (D / 32);
+    for (int w = 0; w < kW; ++w) {
+        const float a = ex2(sm[w * kR + row] - m);
+        l = fmaf(a, sl[w * kR + row], l);
+        const float* from_w = so + (w * kR + row) * so_row<D>() + lane * (D / 32);
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) o[j] = fmaf(a, from_w[j], o[j]);
     }
     const int d = lane * (D / 32);
     if (whole) {
-        write_row<D / 32>(p, it, kRows, row, d, l, o);
-        return;
+        write_row<D / 32>(p, it, kR, row, d, l, o);
+        continue;
     }
-    const long long at = (static_cast<long long>(slot) * kRows + row) * D + d;
+    const long long at = (static_cast<long long>(slot) * kR + row) * D + d;
     if (store_ok(p.ctl, at, D / 32, wk.o_elems)) {
 #pragma unroll
         for (int j = 0; j < D / 32; j += 2) *reinterpret_cast<float2*>(wk.o + at + j) = make_float2(o[j], o[j + 1]);
     }
-    if (lane == 0 && store_ok(p.ctl, slot * kRows + row, 1, wk.ml_elems)) wk.ml[slot * kRows + row] = make_float2(m, l);
+    if (lane == 0 && store_ok(p.ctl, slot * kR + row, 1, wk.ml_elems)) wk.ml[slot * kR + row] = make_float2(m, l);
+    }
 }
 
 // The list's tiles, dealt out.
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps<D>, kBlocks<D>)
+template <int D, int RG>
+__global__ void __launch_bounds__(32 * kWarps<D, RG>, kBlocks<D>)
     attend_kernel(const __grid_constant__ pq2h::AttendParams p, const __grid_constant__ AttendWork wk, int row_tiles) {
+    constexpr int kR = 8 * RG;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ uint64_t bars[kWarps<D>][kStages];
+    __shared__ uint64_t bars[kWarps<D, RG>][kStages];
     pdl_wait();
     pdl_launch_dependents();
     // (the walk through the list is thread 0's: in registers of all threads it
@@ -506,9 +552,9 @@ __global__ void __launch_bounds__(32 * kWarps<D>, kBlocks<D>)
     {
         AttendSpan span;
         if (row_tiles == 1)
-            attend_span<kRows>(p, 1, kExtra, kWarps<D>, span);
+            attend_span<kR>(p, 1, kExtra<RG>, kWarps<D, RG>, span);
         else
-            attend_span_block<kRows, kWarps<D>>(p, row_tiles, 1, kExtra, kWarps<D>, span);
+            attend_span_block<kR, kWarps<D, RG>>(p, row_tiles, 1, kExtra<RG>, kWarps<D, RG>, span);
         if (threadIdx.x == 0) {
             walk = span;
             wk.join[blockIdx.x] = {0, 0, 0, 0, 0};
@@ -517,17 +563,17 @@ __global__ void __launch_bounds__(32 * kWarps<D>, kBlocks<D>)
     }
     for (int n = 0; u < u1; ++n) {
         __syncthreads();
-        if (threadIdx.x == 0) step = attend_step<kRows>(p, row_tiles, 1, kExtra, walk, u);
+        if (threadIdx.x == 0) step = attend_step<kR>(p, row_tiles, 1, kExtra<RG>, walk, u);
         __syncthreads();
         const AttendStep s = step;
         u += s.units;
         if (s.count == 0) continue;
-        const AttendItem it = attend_item<kRows>(p, s.b, s.row_tile, s.head);
+        const AttendItem it = attend_item<kR>(p, s.b, s.row_tile, s.head);
         const int t0 = it.tile0 + s.first, slot = 2 * blockIdx.x + (n > 0);
         if (threadIdx.x == 0 && s.first == 0 && s.count < s.of)
             wk.join[blockIdx.x] = {s.b, s.row_tile, s.head,
                                    attend_cta_of(walk, s.end - 1) - static_cast<int>(blockIdx.x) + 1, slot};
-        segment<D>(p, wk, it, t0, min(t0 + s.count, it.tile1), s.count == s.of, slot, smem, ring);
+        segment<D, RG>(p, wk, it, t0, min(t0 + s.count, it.tile1), s.count == s.of, slot, smem, ring);
     }
 }
 
@@ -536,10 +582,10 @@ __global__ void __launch_bounds__(32 * kWarps<D>, kBlocks<D>)
 // outputs, a lane D / 32 dims.
 constexpr int kJoinWarps = 8;
 
-template <int D>
+template <int D, int RG>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     attend_join_kernel(const __grid_constant__ pq2h::AttendParams p, const __grid_constant__ AttendWork wk) {
-    constexpr int kN = D / 32;
+    constexpr int kN = D / 32, kR = 8 * RG;
     __shared__ float so[kJoinWarps][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y;
     pdl_wait();
@@ -547,7 +593,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     const AttendJoin j = wk.join[blockIdx.x];
     if (j.parts == 0) return;
     const auto place = [&](int i) {
-        return static_cast<long long>(i == 0 ? j.first_slot : 2 * (static_cast<int>(blockIdx.x) + i)) * kRows + row;
+        return static_cast<long long>(i == 0 ? j.first_slot : 2 * (static_cast<int>(blockIdx.x) + i)) * kR + row;
     };
     float m = kEmpty;
     for (int i = lane; i < j.parts; i += 32) m = fmaxf(m, wk.ml[place(i)].x);
@@ -587,8 +633,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     for (int w = 1; w < kJoinWarps; ++w)
 #pragma unroll
         for (int k = 0; k < kN; ++k) o[k] += so[w][lane * kN + k];
-    const AttendItem it = attend_item<kRows>(p, j.b, j.row_tile, j.head);
-    write_row<D / 32>(p, it, kRows, row, lane * (D / 32), l, o);
+    const AttendItem it = attend_item<kR>(p, j.b, j.row_tile, j.head);
+    write_row<D / 32>(p, it, kR, row, lane * (D / 32), l, o);
 }
 
 }  // namespace
@@ -600,35 +646,35 @@ namespace {
 
 size_t pad(size_t b) { return (b + 255) & ~size_t(255); }
 
-template <int D>
+template <int D, int RG>
 cudaError_t launch_few(const AttendParams& p, const pq2::AttendWork& wk, cudaStream_t st, const DeviceInfo& dev) {
     static SmemLimit lim;
-    const size_t smem = pq2::smem_bytes<D>();
-    cudaError_t e = raise_smem(lim, pq2::attend_kernel<D>, smem);
+    const size_t smem = pq2::smem_bytes<D, RG>();
+    cudaError_t e = raise_smem(lim, pq2::attend_kernel<D, RG>, smem);
     if (e != cudaSuccess) return e;
-    const int G = p.q_heads / p.cache.heads, row_tiles = (p.max_rows * G + pq2::kRows - 1) / pq2::kRows;
+    const int G = p.q_heads / p.cache.heads, row_tiles = (p.max_rows * G + 8 * RG - 1) / (8 * RG);
     const int64_t ctas = std::min<int64_t>(dev.num_sms * pq2::kBlocks<D>, pq2::kAttendCtas);
-    e = launch(pq2::attend_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(32 * pq2::kWarps<D>), smem, st, true, p, wk, row_tiles);
+    e = launch(pq2::attend_kernel<D, RG>, dim3(static_cast<unsigned>(ctas)), dim3(32 * pq2::kWarps<D, RG>), smem, st, true, p, wk, row_tiles);
     if (e != cudaSuccess) return e;
-    return launch(pq2::attend_join_kernel<D>, dim3(static_cast<unsigned>(ctas), pq2::kRows),
+    return launch(pq2::attend_join_kernel<D, RG>, dim3(static_cast<unsigned>(ctas), 8 * RG),
                   dim3(32 * pq2::kJoinWarps), 0, st, true, p, wk);
 }
 
 }  // namespace
 
 size_t attend_workspace_bytes(int64_t M, int64_t q_heads, int64_t heads, int64_t dim) {
-    const size_t rows = 2ull * pq2::kAttendCtas * pq2::kRows;
+    const size_t rows = 2ull * pq2::kAttendCtas * pq2::kMostRows;
     const size_t few = pad(rows * dim * 4) + pad(rows * 8) + pad(pq2::kAttendCtas * sizeof(pq2::AttendJoin));
-    return M * (q_heads / heads) > pq2::kFewRows ? std::max(few, attend_many_workspace_bytes(M, q_heads, heads, dim)) : few;
+    return M * (q_heads / heads) > pq2::few_rows(dim) ? std::max(few, attend_many_workspace_bytes(M, q_heads, heads, dim)) : few;
 }
 
 cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t st, const DeviceInfo& dev) {
     const int64_t G = p.q_heads / p.cache.heads;
-    if (p.max_rows * G > pq2::kFewRows) return launch_attend_many(p, workspace, st, dev);
+    if (p.max_rows * G > pq2::few_rows(p.dim)) return launch_attend_many(p, workspace, st, dev);
     pq2::AttendWork wk = {};
-    wk.rows = pq2::kRows;
+    wk.rows = pq2::kMostRows;
     uint8_t* w = static_cast<uint8_t*>(workspace);
-    const size_t rows = 2ull * pq2::kAttendCtas * pq2::kRows;
+    const size_t rows = 2ull * pq2::kAttendCtas * pq2::kMostRows;
     wk.o = reinterpret_cast<float*>(w);
     wk.o_elems = rows * p.dim;
     w += pad(rows * p.dim * 4);
@@ -636,11 +682,15 @@ cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t s
     wk.ml_elems = rows;
     w += pad(rows * 8);
     wk.join = reinterpret_cast<pq2::AttendJoin*>(w);
-    switch (p.dim) {
-        case 64: return launch_few<64>(p, wk, st, dev);
-        case 128: return launch_few<128>(p, wk, st, dev);
-    }
-    return launch_few<256>(p, wk, st, dev);
+    const auto run = [&](auto rows) {
+        constexpr int RG = decltype(rows)::value;
+        switch (p.dim) {
+            case 64: return launch_few<64, RG>(p, wk, st, dev);
+            case 128: return launch_few<128, RG>(p, wk, st, dev);
+        }
+        return launch_few<256, RG>(p, wk, st, dev);
+    };
+    return p.max_rows * G > 8 ? run(std::integral_constant<int, 2>()) : run(std::integral_constant<int, 1>());
 }
 
 }  // namespace pq2h
