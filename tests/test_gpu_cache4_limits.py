@@ -162,6 +162,20 @@ def test_rows_of_very_different_size(pq2, D, n):
     assert np.all(err <= tol + np.abs(want) * UNIT["bf16"] + TINY["bf16"] + 2 * off * vmax)
 
 
+@pytest.mark.parametrize("D,T,n", [(128, 16, 1), (128, 16, 9), (64, 16, 70), (128, 32, 60), (256, 64, 40)])
+def test_pages_before_a_window_may_be_gone(pq2, D, T, n):
+    ln, window = 700, 50
+    c = Cache(pq2, 1, -(-ln // T), 1, D, T)
+    pool = c.fill([ln])
+    q = _q(n, 2, D, "f16")
+    want = _attend(pq2, c, q, [n], [ln], window=window)
+    _check(want, q, pool, c, [n], [ln], window=window)
+    c.dev[0, :(ln - n - window + 1) // T] = -1
+    got = _attend(pq2, c, q, [n], [ln], window=window)
+    assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+    assert torch.equal(got, want)
+
+
 # --- the bounds-checked build ---------------------------------------------
 @pytest.fixture(scope="module")
 def libs():
