@@ -35,8 +35,8 @@
 // registers that had to be moved to uniform ones (100 cycles a product), waits one
 // by one, an address read from shared memory before every load of codes, and items that
 // counted for their tiles alone.  On GB300: 4096 tokens behind 4096, 24 heads of 256 on 4:
-// 790 us, 784 TFLOP/s; 3 chunks of up to 1000 tokens behind up to 5000, 40 heads of 128 on 8:
-// 315 us (mma.sync, 8 rows at a time: 4528 and 1250 us).
+// 701 us, 882 TFLOP/s; 3 chunks of up to 1000 tokens behind up to 5000, 40 heads of 128 on 8:
+// 292 us (mma.sync, 8 rows at a time: 4528 and 1250 us).
 #include <algorithm>
 
 #include "pq2_attend.cuh"
@@ -158,7 +158,7 @@ __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sy
 // Operand lists of the loads and stores below.
 #define PQ2_R8(x, i) x(i), x(i + 1), x(i + 2), x(i + 3), x(i + 4), x(i + 5), x(i + 6), x(i + 7)
 #define PQ2_R16(x, i) PQ2_R8(x, i), PQ2_R8(x, i + 8)
-// 16 rows by 32 (64) columns; lane (g, t): v[4 n], v[4 n + 1] row g, columns
+// 16 rows by 32 columns; lane (g, t): v[4 n], v[4 n + 1] row g, columns
 // 8 n + 2 t and the next, v[4 n + 2], v[4 n + 3] row g + 8.  Load and wait are one
 // statement: a copy of a register between the two would copy what was in it before.
 #define PQ2_OUT(i) "=f"(v[i])
@@ -167,15 +167,6 @@ __device__ __forceinline__ void tc_load(uint32_t addr, float (&v)[16]) {
         "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : PQ2_R16(PQ2_OUT, 0)
-        : "r"(addr)
-        : "memory");
-}
-__device__ __forceinline__ void tc_load(uint32_t addr, float (&v)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
-        "%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : PQ2_R16(PQ2_OUT, 0), PQ2_R16(PQ2_OUT, 16)
         : "r"(addr)
         : "memory");
 }
@@ -201,15 +192,10 @@ __device__ __forceinline__ void tc_store(uint32_t addr, const float (&v)[16]) {
                  : "memory");
 }
 #undef PQ2_IN
-// 16 rows by 16 (32) columns of two fp16; lane (g, t): w[2 n] row g, column 4 n + t, w[2 n + 1] row g + 8.
+// 16 rows by 16 columns of two fp16; lane (g, t): w[2 n] row g, column 4 n + t, w[2 n + 1] row g + 8.
 #define PQ2_IN(i) "r"(w[i])
 __device__ __forceinline__ void tc_store_weights(uint32_t addr, const uint32_t (&w)[8]) {
     asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), PQ2_R8(PQ2_IN, 0)
-                 : "memory");
-}
-__device__ __forceinline__ void tc_store_weights(uint32_t addr, const uint32_t (&w)[16]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-                 PQ2_R16(PQ2_IN, 0)
                  : "memory");
 }
 #undef PQ2_IN
@@ -314,7 +300,8 @@ __device__ __forceinline__ void factors(const Ctl& k, const AttendWork& wk, int 
         u += g.units;
         // (an item has at least one tile behind its kExtra units)
         const int last = span.u1 - u > kExtra ? 1 : 2;
-        const int len = g.it.pos0 + g.it.n;
+        // keys that some row sees (what is before a window may have lost its page)
+        const int key_lo = g.it.tile0 * kTileTokens, key_hi = min(g.it.tile1 * kTileTokens, g.it.pos0 + g.it.n);
         const long long head_at = static_cast<long long>(g.it.head) * per_page * tile_bytes(D);
         for (int j = 0; j < g.count; ++j, ++n) {
             if (n != next) continue;
@@ -327,7 +314,7 @@ __device__ __forceinline__ void factors(const Ctl& k, const AttendWork& wk, int 
                 const int key = (g.tile + j) * kKeys + lane + 32 * i;
                 base[i] = -1;
                 kp[i] = vp[i] = 0;
-                if (key >= len) continue;
+                if (key < key_lo || key >= key_hi) continue;
                 const int page = __ldg(p.cache.pages + g.it.b * p.cache.ld_pages + key / p.cache.T);
                 if (page < 0 || page >= p.cache.num_pages) {
                     atomicOr(p.ctl.err, DEVERR_BAD_INDEX);
@@ -705,9 +692,10 @@ __device__ __forceinline__ bool rows_of_segment(const Ctl& k, const AttendWork& 
             if (j == 0) back = *reinterpret_cast<volatile float*>(&k.bars.back);
             const int key0 = slot.key0;  // (-1: all rows see the whole tile)
             const uint32_t at_s = lanes + 256 + buf * 128;
-            // 32 or 64 keys at a time, in a loop: with a tile's code unrolled, the
-            // roles' instructions do not fit the instruction caches
-            constexpr int kStep = 64 / NS, kGroups = kStep / 8;
+            // 32 keys at a time, in a loop: with a tile's code unrolled, the roles'
+            // instructions do not fit the instruction caches (64 at a time with one
+            // group of rows: 750 us for a prompt, not 701)
+            constexpr int kStep = 32, kGroups = kStep / 8;
 #pragma unroll 1
             for (int q = 0; q < kKeys; q += kStep) {
                 float x[NS][kStep / 2];

@@ -627,8 +627,8 @@ pq2_status pq2_cache4_read(const pq2_cache4_read_args* args, void* stream);
  * below 0) gives zeros.  Scores, maxima, sums and accumulated outputs are
  * fp32; q enters the products with the 11 bits of its type or the fp16 rounding of its
  * row scaled by a power of two (bf16: no rounding within 2^28 of the row's
- * largest; where max_rows * q_heads / heads > 32, up to 256 rows of a sequence
- * are scaled alike, and a value is off by up to 2^-22 of the largest of them),
+ * largest; where max_rows * q_heads / heads > 48, or 32 with dim 256, up to 256
+ * rows of a sequence are scaled alike, and a value is off by up to 2^-22 of the largest of them),
  * the weights w times the values' scales as fp16, scaled by powers of two
  * likewise.
  *   q, out     [M, q_heads, dim] (type: PQ2_F16 or PQ2_BF16), token and head
