@@ -57,6 +57,7 @@ __device__ __forceinline__ AttendItem attend_item(const pq2h::AttendParams& p, i
         if (r0 < 0 || r1 < r0 || r1 > p.M || n > p.max_rows) return it;
     }
     if (static_cast<long long>(row_tile) * ROWS >= static_cast<long long>(n) * G) return it;
+    if (n * G <= p.over || n * G > p.upto) return it;  // (another kernel's)
     const int first = row_tile * ROWS / G, last = min(n - 1, (row_tile * ROWS + ROWS - 1) / G);
     it.n = n;
     it.row0 = r0;

@@ -279,12 +279,13 @@ struct AttendParams {
     long long out_elems;
     int M, max_rows, window;   // window 0: none
     int q_heads, dim, bf16;
+    int over, upto;            // sequences with more and with at most so many rows per key/value head
     float scale;
     pq2::DevCtl ctl;
 };
 size_t attend_workspace_bytes(int64_t M, int64_t q_heads, int64_t heads, int64_t dim);
 cudaError_t launch_attend(const AttendParams& p, void* workspace, cudaStream_t st, const DeviceInfo& dev);
-// The same for more than 8 query rows per key/value head (pq2_attend_many.cu).
+// The same for many query rows per key/value head (pq2_attend_many.cu).
 size_t attend_many_workspace_bytes(int64_t M, int64_t q_heads, int64_t heads, int64_t dim);
 cudaError_t launch_attend_many(const AttendParams& p, void* workspace, cudaStream_t st, const DeviceInfo& dev);
 
