@@ -31,9 +31,9 @@ def pq2():
                                       (2, 2, 64, 70), (6, 1, 128, 9), (6, 1, 128, 60), (6, 1, 256, 30)])
 @pytest.mark.parametrize("stage", [0, 1])
 def test_a_tile_that_never_comes(pq2, Hq, H, D, n, stage):
-    # (tile or half of a tile `stage` of every ring is withheld; with few rows
-    # a warp may have one tile of the 1500 tokens and no second one)
-    reaches = stage == 0 or n * Hq // H > 32
+    # (tile or half of a tile `stage` of every ring is withheld; of 1500 tokens a
+    # warp, or a CTA, may have one tile and no second one)
+    reaches = stage == 0
     ln = 1500
     c = Cache(pq2, 1, -(-ln // 64), H, D, 64)
     pool = c.fill([ln])
@@ -53,19 +53,20 @@ def test_a_tile_that_never_comes(pq2, Hq, H, D, n, stage):
     assert pq2.pq2_last_device_error() == pq2.PQ2_OK
 
 
+@pytest.mark.parametrize("n", [1, 20])
 @pytest.mark.parametrize("stage", [1, 2])
-def test_a_later_tile_that_never_comes(pq2, stage):
-    # 24 tiles and more for each warp
+def test_a_later_tile_that_never_comes(pq2, stage, n):
+    # 24 tiles and more for each warp, or CTA
     ln, W = 60000, 200
     pool = torch.zeros((2, 1, 16 * 136 * 20), dtype=torch.uint8, device=DEV)
     pages = _dev(np.arange(64 * W).reshape(64, W) % 2)
-    q = _q(64, 6, 128, "f16")
+    q = _q(64 * n, 6, 128, "f16")
     out = torch.empty_like(q)
-    ws = pq2.alloc_attend_workspace(64, 6, 1, 128)
-    start, lens = _dev(np.arange(65)), _dev(np.full(64, ln))
+    ws = pq2.alloc_attend_workspace(64 * n, 6, 1, 128)
+    start, lens = _dev(n * np.arange(65)), _dev(np.full(64, ln))
 
     def run():
-        pq2.pq2_cache4_attend(q, pool, pages, start, lens, out, ws, max_rows=1)
+        pq2.pq2_cache4_attend(q, pool, pages, start, lens, out, ws, max_rows=n)
         return pq2.pq2_last_device_error()
 
     assert run() == pq2.PQ2_OK and torch.all(out == 0)
