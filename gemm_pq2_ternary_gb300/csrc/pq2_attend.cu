@@ -534,13 +534,13 @@ __device__ __forceinline__ void segment(const pq2h::AttendParams& p, const Atten
 // The list's tiles, dealt out.
 template <int D, int RG>
 __global__ void __launch_bounds__(32 * kWarps<D, RG>, kBlocks<D>)
-    attend_kernel(const __grid_constant__ pq2h::AttendParams p, const __grid_constant__ AttendWork wk, int row_tiles) {
+    attend_kernel(const __grid_constant__ pq2h::AttendParams p, const __grid_constant__ AttendWork wk) {
     constexpr int kR = 8 * RG;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ uint64_t bars[kWarps<D, RG>][kStages];
     pdl_wait();
     pdl_launch_dependents();
-    // (the walk through the list is thread 0's: in registers of all threads it
+    // (the walk through the list is warp 0's: in registers of all threads it
     // would be in the way of the tiles')
     __shared__ AttendSpan walk;
     __shared__ AttendStep step;
@@ -552,10 +552,7 @@ __global__ void __launch_bounds__(32 * kWarps<D, RG>, kBlocks<D>)
     long long u, u1;
     {
         AttendSpan span;
-        if (row_tiles == 1)
-            attend_span<kR>(p, 1, kExtra<RG>, kWarps<D, RG>, span);
-        else
-            attend_span_block<kR, kWarps<D, RG>>(p, row_tiles, 1, kExtra<RG>, kWarps<D, RG>, span);
+        attend_span<kR, kWarps<D, RG>>(p, 1, kExtra<RG>, kWarps<D, RG>, span);
         if (threadIdx.x == 0) {
             walk = span;
             wk.join[blockIdx.x] = {0, 0, 0, 0, 0};
@@ -564,7 +561,12 @@ __global__ void __launch_bounds__(32 * kWarps<D, RG>, kBlocks<D>)
     }
     for (int n = 0; u < u1; ++n) {
         __syncthreads();
-        if (threadIdx.x == 0) step = attend_step<kR>(p, row_tiles, 1, kExtra<RG>, walk, u);
+        if (warp == 0) {
+            AttendSpan span = walk;
+            const AttendStep next = attend_step<kR>(p, 1, kExtra<RG>, span, u);
+            __syncwarp();
+            if (threadIdx.x == 0) step = next, walk = span;
+        }
         __syncthreads();
         const AttendStep s = step;
         u += s.units;
@@ -653,9 +655,8 @@ cudaError_t launch_few(const AttendParams& p, const pq2::AttendWork& wk, cudaStr
     const size_t smem = pq2::smem_bytes<D, RG>();
     cudaError_t e = raise_smem(lim, pq2::attend_kernel<D, RG>, smem);
     if (e != cudaSuccess) return e;
-    const int G = p.q_heads / p.cache.heads, row_tiles = (std::min(p.max_rows * G, p.upto) + 8 * RG - 1) / (8 * RG);
     const int64_t ctas = std::min<int64_t>(dev.num_sms * pq2::kBlocks<D>, pq2::kAttendCtas);
-    e = launch(pq2::attend_kernel<D, RG>, dim3(static_cast<unsigned>(ctas)), dim3(32 * pq2::kWarps<D, RG>), smem, st, true, p, wk, row_tiles);
+    e = launch(pq2::attend_kernel<D, RG>, dim3(static_cast<unsigned>(ctas)), dim3(32 * pq2::kWarps<D, RG>), smem, st, true, p, wk);
     if (e != cudaSuccess) return e;
     return launch(pq2::attend_join_kernel<D, RG>, dim3(static_cast<unsigned>(ctas), 8 * RG),
                   dim3(32 * pq2::kJoinWarps), 0, st, true, p, wk);

@@ -3,6 +3,8 @@
 // written and joined.
 #pragma once
 
+#include <climits>
+
 #include "pq2_cache.cuh"
 #include "pq2_elem.cuh"
 
@@ -43,25 +45,34 @@ struct AttendItem {
     int first_hi, last_lo;  // positions that all rows see all of: first_hi .. last_lo
 };
 
-template <int ROWS>
-__device__ __forceinline__ AttendItem attend_item(const pq2h::AttendParams& p, int b, int row_tile, int head) {
-    AttendItem it = {b, row_tile, head, 0, 0, 0, 0, 0, 0, -1};
-    const int G = p.q_heads / p.cache.heads;
+// What of a sequence its items are made from.
+struct AttendSequence {
+    int n, row0, pos0;  // n == 0: nothing for this kernel
+};
+
+__device__ __forceinline__ AttendSequence attend_sequence(const pq2h::AttendParams& p, int b) {
     const int r0 = __ldcg(p.cache.row_start + b), r1 = __ldcg(p.cache.row_start + b + 1);
     const int len = __ldcg(p.cache.lens + b);
     const int most = p.cache.W * p.cache.T;
     const int n = r1 - r0;
-    if (r0 < 0 || r1 < r0 || r1 > p.M || n > p.max_rows || len < 0 || len > most) {
-        atomicOr(p.ctl.err, DEVERR_BAD_INDEX);
-        if (!(len < 0 || len > most)) return it;
-        if (r0 < 0 || r1 < r0 || r1 > p.M || n > p.max_rows) return it;
-    }
-    if (static_cast<long long>(row_tile) * ROWS >= static_cast<long long>(n) * G) return it;
-    if (n * G <= p.over || n * G > p.upto) return it;  // (another kernel's)
-    const int first = row_tile * ROWS / G, last = min(n - 1, (row_tile * ROWS + ROWS - 1) / G);
-    it.n = n;
-    it.row0 = r0;
-    it.pos0 = min(max(len, 0), most) - n;
+    const bool bad = r0 < 0 || r1 < r0 || r1 > p.M || n > p.max_rows;
+    if (bad || len < 0 || len > most) atomicOr(p.ctl.err, DEVERR_BAD_INDEX);
+    if (bad || n == 0) return {0, 0, 0};
+    const int rows = n * (p.q_heads / p.cache.heads);
+    if (rows <= p.over || rows > p.upto) return {0, 0, 0};  // (another kernel's)
+    return {n, r0, min(max(len, 0), most) - n};
+}
+
+template <int ROWS>
+__device__ __forceinline__ AttendItem attend_item(const pq2h::AttendParams& p, const AttendSequence& q, int b, int row_tile,
+                                                  int head) {
+    AttendItem it = {b, row_tile, head, 0, 0, 0, 0, 0, 0, -1};
+    const int G = p.q_heads / p.cache.heads;
+    if (static_cast<long long>(row_tile) * ROWS >= static_cast<long long>(q.n) * G) return it;
+    const int first = row_tile * ROWS / G, last = min(q.n - 1, (row_tile * ROWS + ROWS - 1) / G);
+    it.n = q.n;
+    it.row0 = q.row0;
+    it.pos0 = q.pos0;
     const int lo = it.pos0 + first, hi = it.pos0 + last;
     if (hi >= 0) {
         it.tile1 = hi / kTileTokens + 1;
@@ -70,6 +81,11 @@ __device__ __forceinline__ AttendItem attend_item(const pq2h::AttendParams& p, i
     it.first_hi = p.window > 0 ? max(hi - p.window + 1, 0) : 0;
     it.last_lo = lo;
     return it;
+}
+
+template <int ROWS>
+__device__ __forceinline__ AttendItem attend_item(const pq2h::AttendParams& p, int b, int row_tile, int head) {
+    return attend_item<ROWS>(p, attend_sequence(p, b), b, row_tile, head);
 }
 
 // Units of an item: its tiles of `per` times 16 tokens, at least one (an item without
@@ -81,21 +97,65 @@ __device__ __forceinline__ int attend_units(const AttendItem& it, int per, int e
 }
 
 // A CTA's part of the list of units, and where a walk through it is.  The
-// list's entries are (sequence, tile of rows), `row_tiles` for every sequence (those
-// that it does not have are empty); an entry's heads follow one another.
+// list's entries are the sequences' tiles of rows; an entry's heads follow one another.
 struct AttendSpan {
     long long u0, u1, total;
     int ctas;
-    int entry, units;   // an entry, its units per head
-    long long before;   // units before it
+    int b, row_tile, tiles;  // an entry; its sequence's tiles of rows
+    AttendSequence sequence;
+    int units;               // the entry's, per head
+    long long before;        // units before it
 };
 
+// A sequence's tiles of rows.
 template <int ROWS>
-__device__ __forceinline__ int attend_entry_units(const pq2h::AttendParams& p, long long entry, int row_tiles, int per,
+__device__ __forceinline__ int attend_row_tiles(const pq2h::AttendParams& p, const AttendSequence& q) {
+    return static_cast<int>((static_cast<long long>(q.n) * (p.q_heads / p.cache.heads) + ROWS - 1) / ROWS);
+}
+
+template <int ROWS>
+__device__ __forceinline__ int attend_entry_units(const pq2h::AttendParams& p, const AttendSequence& q, int row_tile, int per,
                                                   int extra) {
-    const int b = static_cast<int>(entry / row_tiles);
-    return attend_units(attend_item<ROWS>(p, b, static_cast<int>(entry - static_cast<long long>(b) * row_tiles), 0), per,
-                        extra);
+    return attend_units(attend_item<ROWS>(p, q, 0, row_tile, 0), per, extra);
+}
+
+// That of a lane, for all.
+__device__ __forceinline__ AttendSequence attend_sequence_of(const AttendSequence& q, int lane) {
+    return {__shfl_sync(0xffffffffu, q.n, lane), __shfl_sync(0xffffffffu, q.row0, lane), __shfl_sync(0xffffffffu, q.pos0, lane)};
+}
+
+// The sum over a warp's lanes, and up to a lane.
+__device__ __forceinline__ long long warp_scan(long long v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+// Units per head of a lane's sequence.  A few tiles of rows are its lane's
+// work, more are all lanes'.
+template <int ROWS>
+__device__ __forceinline__ long long attend_sequence_units(const pq2h::AttendParams& p, const AttendSequence& q, int per,
+                                                           int extra) {
+    constexpr int kFew = 4;
+    const int lane = threadIdx.x & 31, tiles = attend_row_tiles<ROWS>(p, q);
+    long long units = 0;
+#pragma unroll 1
+    for (int r = 0; r < (tiles > kFew ? 0 : tiles); ++r) units += attend_entry_units<ROWS>(p, q, r, per, extra);
+    __syncwarp();
+#pragma unroll 1
+    for (unsigned longer = __ballot_sync(0xffffffffu, tiles > kFew); longer; longer &= longer - 1) {
+        const int from = __ffs(longer) - 1, n = __shfl_sync(0xffffffffu, tiles, from);
+        const AttendSequence other = attend_sequence_of(q, from);
+        long long sum = 0;
+        for (int r = lane; r < n; r += 32) sum += attend_entry_units<ROWS>(p, other, r, per, extra);
+        sum = __shfl_sync(0xffffffffu, warp_scan(sum), 31);
+        if (lane == from) units = sum;
+    }
+    return units;
 }
 
 // The CTA's share of `total` units, at least `least` to a CTA (unless there are fewer).
@@ -103,60 +163,28 @@ __device__ __forceinline__ void attend_share(AttendSpan& s, long long total, int
     s.total = total;
     s.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total / least, 1ll)));
     s.u0 = s.u1 = 0;
-    s.entry = 0, s.units = 0, s.before = 0;
+    s.b = 0, s.row_tile = 0, s.tiles = 0, s.units = 0, s.before = 0;
+    s.sequence = {0, 0, 0};
     const int cta = blockIdx.x;
     if (cta >= s.ctas) return;
     s.u0 = cta * total / s.ctas;
     s.u1 = (cta + 1) * total / s.ctas;
 }
 
-// All threads of the CTA call it (every warp finds the same).
-template <int ROWS>
-__device__ __forceinline__ void attend_span(const pq2h::AttendParams& p, int per, int extra, int least, AttendSpan& s) {
-    const int lane = threadIdx.x & 31, B = p.cache.B, H = p.cache.heads;
-    long long total = 0;
-    for (int b0 = 0; b0 < B; b0 += 32) {
-        int c = 0;
-        if (b0 + lane < B) c = attend_entry_units<ROWS>(p, b0 + lane, 1, per, extra);
-        total += __reduce_add_sync(0xffffffffu, c);
-    }
-    attend_share(s, total * H, least);
-    if (s.u0 >= s.u1) return;
-    for (int b0 = 0; b0 < B; b0 += 32) {
-        int c = 0;
-        if (b0 + lane < B) c = attend_entry_units<ROWS>(p, b0 + lane, 1, per, extra);
-        int inc = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += u;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, s.before + static_cast<long long>(inc) * H > s.u0);
-        if (past) {
-            const int at = __ffs(past) - 1;
-            s.entry = b0 + at;
-            s.units = __shfl_sync(0xffffffffu, c, at);
-            s.before += static_cast<long long>(__shfl_sync(0xffffffffu, inc - c, at)) * H;
-            return;
-        }
-        s.before += static_cast<long long>(__shfl_sync(0xffffffffu, inc, 31)) * H;
-    }
-}
-
-// The same with the work on many entries split over the CTA's warps.
+// All threads of the CTA call it; the sequences are split over its warps.
 template <int ROWS, int WARPS>
-__device__ __forceinline__ void attend_span_block(const pq2h::AttendParams& p, int row_tiles, int per, int extra, int least,
-                                                  AttendSpan& s) {
+__device__ __forceinline__ void attend_span(const pq2h::AttendParams& p, int per, int extra, int least, AttendSpan& s) {
     __shared__ long long sums[WARPS];
     __shared__ long long found_before;
-    __shared__ int found_entry, found_units;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, H = p.cache.heads;
-    const long long entries = static_cast<long long>(p.cache.B) * row_tiles;
-    const long long share = (entries + WARPS - 1) / WARPS;
-    const long long e0 = min(warp * share, entries), e1 = min(e0 + share, entries);
+    __shared__ int found[4];  // b, row_tile, tiles, units
+    __shared__ AttendSequence found_sequence;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, B = p.cache.B, H = p.cache.heads;
+    const int share = (B + WARPS - 1) / WARPS;
+    const int b0 = min(warp * share, B), b1 = min(b0 + share, B);
     long long mine = 0;
-    for (long long e = e0; e < e1; e += 32)
-        mine += __reduce_add_sync(0xffffffffu, e + lane < e1 ? attend_entry_units<ROWS>(p, e + lane, row_tiles, per, extra) : 0);
+    const auto sequence_at = [&](int b) { return b < b1 ? attend_sequence(p, b) : AttendSequence{0, 0, 0}; };
+    for (int b = b0; b < b1; b += 32)
+        mine += __shfl_sync(0xffffffffu, warp_scan(attend_sequence_units<ROWS>(p, sequence_at(b + lane), per, extra)), 31);
     if (lane == 0) sums[warp] = mine * H;
     __syncthreads();
     long long total = 0, before = 0;
@@ -168,30 +196,39 @@ __device__ __forceinline__ void attend_span_block(const pq2h::AttendParams& p, i
     attend_share(s, total, least);
     if (s.u0 >= s.u1) return;  // (all threads alike)
     if (before <= s.u0 && s.u0 < before + mine * H) {
-        for (long long e = e0; e < e1; e += 32) {
-            const int c = e + lane < e1 ? attend_entry_units<ROWS>(p, e + lane, row_tiles, per, extra) : 0;
-            int inc = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += u;
-            }
-            const unsigned past = __ballot_sync(0xffffffffu, before + static_cast<long long>(inc) * H > s.u0);
+        for (int b = b0; b < b1; b += 32) {
+            const AttendSequence mine_q = sequence_at(b + lane);
+            const long long c = attend_sequence_units<ROWS>(p, mine_q, per, extra), inc = warp_scan(c);
+            const unsigned past = __ballot_sync(0xffffffffu, before + inc * H > s.u0);
             if (past) {
-                if (lane == __ffs(past) - 1) {
-                    found_entry = static_cast<int>(e + lane);
-                    found_units = c;
-                    found_before = before + static_cast<long long>(inc - c) * H;
+                // the sequence; then its tile of rows
+                const int at = __ffs(past) - 1;
+                before += __shfl_sync(0xffffffffu, inc - c, at) * H;
+                const AttendSequence q = attend_sequence_of(mine_q, at);
+                const int tiles = attend_row_tiles<ROWS>(p, q);
+                for (int r = 0; r < tiles; r += 32) {
+                    const int units = r + lane < tiles ? attend_entry_units<ROWS>(p, q, r + lane, per, extra) : 0;
+                    const long long upto = warp_scan(units);
+                    const unsigned here = __ballot_sync(0xffffffffu, before + upto * H > s.u0);
+                    if (here) {
+                        if (lane == __ffs(here) - 1) {
+                            found[0] = b + at, found[1] = r + lane, found[2] = tiles, found[3] = units;
+                            found_before = before + (upto - units) * H;
+                            found_sequence = q;
+                        }
+                        break;
+                    }
+                    before += __shfl_sync(0xffffffffu, upto, 31) * H;
                 }
                 break;
             }
-            before += static_cast<long long>(__shfl_sync(0xffffffffu, inc, 31)) * H;
+            before += __shfl_sync(0xffffffffu, inc, 31) * H;
         }
     }
     __syncthreads();
-    s.entry = found_entry;
-    s.units = found_units;
+    s.b = found[0], s.row_tile = found[1], s.tiles = found[2], s.units = found[3];
     s.before = found_before;
+    s.sequence = found_sequence;
 }
 
 // The piece of work that begins at unit u: `units` units of an item, in them
@@ -200,19 +237,37 @@ struct AttendStep {
     int b, row_tile, head, first, count, of, units;
     long long end;
 };
+// (by whole warps: sequences without work are passed over 32 at a time)
 template <int ROWS>
-__device__ __forceinline__ AttendStep attend_step(const pq2h::AttendParams& p, int row_tiles, int per, int extra,
-                                                  AttendSpan& s, long long u) {
-    const int H = p.cache.heads;
+__device__ __forceinline__ AttendStep attend_step(const pq2h::AttendParams& p, int per, int extra, AttendSpan& s,
+                                                  long long u) {
+    const int H = p.cache.heads, lane = threadIdx.x & 31;
     while (u >= s.before + static_cast<long long>(s.units) * H) {
         s.before += static_cast<long long>(s.units) * H;
-        ++s.entry;
-        s.units = attend_entry_units<ROWS>(p, s.entry, row_tiles, per, extra);
+        if (++s.row_tile >= s.tiles) {
+            s.row_tile = 0;
+            unsigned some = 0;
+            int b = s.b + 1;
+            for (; some == 0 && b < p.cache.B; b += 32) {
+                const AttendSequence q = b + lane < p.cache.B ? attend_sequence(p, b + lane) : AttendSequence{0, 0, 0};
+                const int tiles = attend_row_tiles<ROWS>(p, q);
+                some = __ballot_sync(0xffffffffu, tiles > 0);
+                if (some == 0) continue;
+                s.b = b + __ffs(some) - 1;
+                s.tiles = __shfl_sync(0xffffffffu, tiles, __ffs(some) - 1);
+                s.sequence = attend_sequence_of(q, __ffs(some) - 1);
+            }
+            if (some == 0) {  // (only where the inputs have changed under way)
+                s.units = INT_MAX;
+                break;
+            }
+        }
+        s.units = attend_entry_units<ROWS>(p, s.sequence, s.row_tile, per, extra);
     }
     const long long in = u - s.before;
     AttendStep st;
-    st.b = s.entry / row_tiles;
-    st.row_tile = s.entry - st.b * row_tiles;
+    st.b = s.b;
+    st.row_tile = s.row_tile;
     st.head = static_cast<int>(in / s.units);
     const int at = static_cast<int>(in - static_cast<long long>(st.head) * s.units);
     st.units = static_cast<int>(min(static_cast<long long>(s.units - at), s.u1 - u));

@@ -266,8 +266,8 @@ struct Segment {
 };
 
 template <int D>
-__device__ __forceinline__ Segment segment_at(const pq2h::AttendParams& p, int row_tiles, AttendSpan& span, long long u) {
-    const AttendStep s = attend_step<Cfg<D>::kRows>(p, row_tiles, kPer, kExtra, span, u);
+__device__ __forceinline__ Segment segment_at(const pq2h::AttendParams& p, AttendSpan& span, long long u) {
+    const AttendStep s = attend_step<Cfg<D>::kRows>(p, kPer, kExtra, span, u);
     Segment g;
     g.it = attend_item<Cfg<D>::kRows>(p, s.b, s.row_tile, s.head);
     g.units = s.units;
@@ -283,7 +283,7 @@ __device__ __forceinline__ Segment segment_at(const pq2h::AttendParams& p, int r
 // Warps 17-19: pages and factors
 // ---------------------------------------------------------------------------
 template <int D>
-__device__ __forceinline__ void factors(const Ctl& k, const AttendWork& wk, int row_tiles, AttendSpan span, Slot* slots,
+__device__ __forceinline__ void factors(const Ctl& k, const AttendWork& wk, AttendSpan span, Slot* slots,
                                         uint32_t w) {
     const pq2h::AttendParams& p = k.p;
     const int G = p.q_heads / p.cache.heads;
@@ -292,7 +292,7 @@ __device__ __forceinline__ void factors(const Ctl& k, const AttendWork& wk, int 
     uint32_t n = 0, next = w;  // tiles so far; this warp's next
     const float to_score = p.scale * 1.4426950408889634f * 0x1p24f;
     for (long long u = span.u0; u < span.u1;) {
-        const Segment g = segment_at<D>(p, row_tiles, span, u);
+        const Segment g = segment_at<D>(p, span, u);
         const int part = 2 * blockIdx.x + (u == span.u0 ? 0 : 1);
         if (g.count > 0 && n == next && g.starts && !g.whole && lane == 0)
             wk.join[blockIdx.x] = {g.it.b, g.it.row_tile, g.it.head,
@@ -1050,7 +1050,7 @@ __device__ __forceinline__ void softmax(const Ctl& k, const AttendWork& wk, uint
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    attend_many_kernel(const __grid_constant__ pq2h::AttendParams p, const __grid_constant__ AttendWork wk, int row_tiles) {
+    attend_many_kernel(const __grid_constant__ pq2h::AttendParams p, const __grid_constant__ AttendWork wk) {
     using C = Cfg<D>;
     extern __shared__ uint8_t dynamic_smem[];
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -1061,7 +1061,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     AttendSpan span;
     // (at least one tile behind an item's kExtra units)
-    attend_span_block<C::kRows, kThreads / 32>(p, row_tiles, kPer, kExtra, kExtra + 1, span);
+    attend_span<C::kRows, kThreads / 32>(p, kPer, kExtra, kExtra + 1, span);
     if (span.u0 >= span.u1) {  // (all threads alike)
         if (tid == 0) wk.join[blockIdx.x] = {0, 0, 0, 0, 0};
         return;
@@ -1106,7 +1106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (warp > kIssuer)
-            factors<D>(k, wk, row_tiles, span, slots, warp - kIssuer - 1);
+            factors<D>(k, wk, span, slots, warp - kIssuer - 1);
         else
             Issue<D>{k, slots, smem_u32(smem), 0}.run();
         __syncwarp();
@@ -1177,10 +1177,8 @@ cudaError_t launch_many(const pq2h::AttendParams& p, const AttendWork& wk, cudaS
         return cudaFuncGetAttributes(&fa, attend_many_kernel<D>) == cudaSuccess && fa.numRegs * kThreads >= kRegsNeeded;
     }();
     if (!fits) return cudaErrorLaunchOutOfResources;
-    const int G = p.q_heads / p.cache.heads;
-    const int row_tiles = static_cast<int>((static_cast<int64_t>(p.max_rows) * G + Cfg<D>::kRows - 1) / Cfg<D>::kRows);
     const int ctas = std::min(dev.num_sms, kMostCtas);
-    e = pq2h::launch(attend_many_kernel<D>, dim3(ctas), dim3(kThreads), Cfg<D>::kSmem, st, true, p, wk, row_tiles);
+    e = pq2h::launch(attend_many_kernel<D>, dim3(ctas), dim3(kThreads), Cfg<D>::kSmem, st, true, p, wk);
     if (e != cudaSuccess) return e;
     return pq2h::launch(attend_many_join_kernel<D>, dim3(ctas, (wk.rows + 31) / 32), dim3(256), 0, st, true, p, wk);
 }

@@ -177,6 +177,21 @@ def test_pages_before_a_window_may_be_gone(pq2, D, T, n):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("Hq,H,D", [(6, 2, 64), (5, 1, 128), (4, 1, 256)])
+@pytest.mark.parametrize("window", [0, 30])
+def test_prompts_around_many_decoding_sequences(pq2, Hq, H, D, window):
+    # more sequences than a walk looks at at once, empty ones among them, in both kernels' shares
+    n = [90] + [1, 0, 1, 2] * 20 + [300] + [1] * 5 + [0] * 40 + [33]
+    lens = [95] + [17, 0, 33, 5] * 20 + [310] + [64] * 5 + [9] * 40 + [40]
+    c = Cache(pq2, len(n), -(-max(lens) // 16), H, D, 16, seed=5)
+    pool = c.fill(lens)
+    q = _q(sum(n) + 1, Hq, D, "f16")
+    got = _attend(pq2, c, q, n, lens, window=window)
+    assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+    _check(got, q, pool, c, n, lens, window=window)
+    assert torch.all(got[sum(n):] == 7.0)
+
+
 # --- the bounds-checked build ---------------------------------------------
 @pytest.fixture(scope="module")
 def libs():
