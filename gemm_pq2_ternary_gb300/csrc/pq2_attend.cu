@@ -30,10 +30,10 @@
 //
 // Bound by instructions and their latency: some 340 a tile of 16 tokens and head, most of
 // them on the integer pipe (operands from codes), issued at 52% of the rate.  On GB300: 131071
-// tokens, 24 heads of 256 on 4: 44 us, 3.1 TB/s (58 with loads into registers, 8 warps an
+// tokens, 24 heads of 256 on 4: 45 us, 3.0 TB/s (58 with loads into registers, 8 warps an
 // SM and a join of one warp's loads at a time); 64 sequences of up to 8192, 48 heads of 128 on
 // 8: 94 us, 3.0 TB/s (107 to 147 while the list counted tiles alone and registers were
-// spilled); 24 sequences of up to 5003 with 5 tokens each, 40 heads of 128 on 8: 57 us (62
+// spilled); 24 sequences of up to 5003 with 5 tokens each, 40 heads of 128 on 8: 59 us (62
 // with 8 rows a pass).
 #include <algorithm>
 #include <climits>

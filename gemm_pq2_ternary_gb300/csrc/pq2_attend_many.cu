@@ -35,8 +35,8 @@
 // registers that had to be moved to uniform ones (100 cycles a product), waits one
 // by one, an address read from shared memory before every load of codes, and items that
 // counted for their tiles alone.  On GB300: 4096 tokens behind 4096, 24 heads of 256 on 4:
-// 701 us, 882 TFLOP/s; 3 chunks of up to 1000 tokens behind up to 5000, 40 heads of 128 on 8:
-// 292 us (mma.sync, 8 rows at a time: 4528 and 1250 us).
+// 714 us, 866 TFLOP/s; 3 chunks of up to 1000 tokens behind up to 5000, 40 heads of 128 on 8:
+// 295 us (mma.sync, 8 rows at a time: 4528 and 1250 us).
 #include <algorithm>
 
 #include "pq2_attend.cuh"
