@@ -706,18 +706,14 @@ __device__ __forceinline__ bool rows_of_segment(const Ctl& k, const AttendWork& 
                 const int at_f = t * kQuarter + q / 4;
                 // (plain fp32 operations: pairs of them in one instruction cost more
                 // in moves than they save)
-                float neg[kR];
-#pragma unroll
-                for (int r = 0; r < kR; ++r) neg[r] = m[r] == kEmpty ? 0.0f : -m[r];
 #pragma unroll
                 for (int c = 0; c < kGroups; c += 2) {
                     const float4 f4 = lds4(slot.scale + at_f + 2 * c);
-                    const float f[4] = {f4.x * back, f4.y * back, f4.z * back, f4.w * back};
+                    const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
                     for (int i = 0; i < NS; ++i)
 #pragma unroll
-                        for (int h = 0; h < 8; ++h)
-                            x[i][4 * c + h] = fmaf(x[i][4 * c + h], f[2 * (h >> 2) + (h & 1)], neg[2 * i + ((h >> 1) & 1)]);
+                        for (int h = 0; h < 8; ++h) x[i][4 * c + h] *= f[2 * (h >> 2) + (h & 1)];
                 }
                 if (__builtin_expect(key0 >= 0, 0)) {
                     const int key1 = key0 + q + 2 * t;
@@ -739,12 +735,14 @@ __device__ __forceinline__ bool rows_of_segment(const Ctl& k, const AttendWork& 
                     top[r] = fmaxf(v[0], v[1]);
 #pragma unroll
                     for (int c = 1; c < kGroups; ++c) top[r] = fmaxf(fmaxf(top[r], v[4 * c]), v[4 * c + 1]);
-                    more |= top[r] > (m[r] == kEmpty ? kEmpty : kSlack);
+                    top[r] *= back;
+                    more |= top[r] > m[r] + kSlack;
                 }
                 if (__builtin_expect(__any_sync(0xffffffffu, more), 0)) {
-                    // raise maxima (by whole numbers: what was rounded is scaled exactly)
-                    // and the values' reference: the rows' sums and outputs are
-                    // scaled down (a row's lanes are four neighbours)
+                    // raise the values' reference, and maxima where a row needs it, to whole
+                    // numbers (what was rounded is scaled exactly; from 2^23 on every fp32 number is
+                    // one, and the maximum is the score): sums and outputs are scaled down
+                    // (a row's lanes are four neighbours)
                     float alpha[kR];
                     const float down = ref / fmaxf(ref, slot.ref);
                     ref = fmaxf(ref, slot.ref);
@@ -752,21 +750,12 @@ __device__ __forceinline__ bool rows_of_segment(const Ctl& k, const AttendWork& 
                     for (int r = 0; r < kR; ++r) {
                         top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
                         top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-                        float by = 0.0f;
-                        alpha[r] = 1.0f;
-                        if (m[r] == kEmpty) {  // (nothing there yet)
-                            if (top[r] > kEmpty) m[r] = by = top[r];
-                        } else {
-                            by = fminf(ceilf(fmaxf(top[r], 0.0f)), 0x1p30f);
-                            m[r] += by;
-                            alpha[r] = by < 126.0f ? __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(by)) << 23) : 0.0f;
-                        }
+                        const float to = top[r] > m[r] + kSlack ? ceilf(top[r]) : m[r], by = to - m[r];
+                        m[r] = to;
+                        alpha[r] = by < 126.0f ? __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(by)) << 23) : 0.0f;
                         l[r] *= alpha[r];
                         z[r] *= alpha[r];
                         alpha[r] *= down;
-                        float* v = x[r >> 1] + 2 * (r & 1);
-#pragma unroll
-                        for (int c = 0; c < kGroups; ++c) v[4 * c] -= by, v[4 * c + 1] -= by;
                     }
                     // the tile's weights so far
                     tc_wait_st();
@@ -816,7 +805,7 @@ __device__ __forceinline__ bool rows_of_segment(const Ctl& k, const AttendWork& 
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
                             const int at = 4 * c + 2 * h, r = 2 * i + (h & 1), key = 2 * (h >> 1);
-                            const float w0 = ex2(x[i][at]), w1 = ex2(x[i][at + 1]);
+                            const float w0 = ex2(fmaf(x[i][at], back, -m[r])), w1 = ex2(fmaf(x[i][at + 1], back, -m[r]));
                             l[r] += w0 + w1;
                             z[r] = fmaf(w1, zs[key + 1], fmaf(w0, zs[key], z[r]));
                             w[i][2 * c + h] = half2_bits(w0 * f[key], w1 * f[key + 1]);

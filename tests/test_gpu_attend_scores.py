@@ -1,0 +1,79 @@
+"""Attention over the 4-bit cache where scores, or the sizes of queries, lie far
+apart: finite inputs of any size have their definition's result."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as ref
+from oracle.step import TINY, UNIT
+from test_gpu_cache4 import TYPES, Cache, _attend, _dev, _np
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+G, T = 2, 16
+# few rows, and many: heads of D values, rows of one sequence
+SIZES = [(64, 1), (128, 5), (256, 3), (64, 70), (128, 60), (128, 300), (256, 40)]
+
+
+@pytest.fixture(scope="module")
+def pq2():
+    from gemm_pq2_ternary_gb300 import binding
+    return binding
+
+
+def _cache(pq2, k, v):
+    """One sequence of keys and values [tokens, D] (one head)."""
+    ln, D = k.shape
+    c = Cache(pq2, 1, -(-ln // T), 1, D, T)
+    k, v = (torch.as_tensor(a, dtype=torch.float32, device=DEV)[:, None].contiguous() for a in (k, v))
+    pq2.pq2_cache4_append(k, v, c.pool, c.dev, _dev([0, ln]), _dev([ln]))
+    return c
+
+
+def _held(c, ln):
+    """The values as the cache holds them, their parts around code 8, and the rest."""
+    code, pair = ref.read_rows(c.pool.cpu().numpy(), c.pages[0], ln, 0, T, c.D)
+    s, z = pair[1, :, :1].astype(np.float64), pair[1, :, 1:].astype(np.float64)
+    return code[1] * s + z, np.abs((code[1] - 8.0) * s), np.abs(z + 8 * s)
+
+
+def _close(got, want, mid, rest, keys, dtype):
+    # weights to fp16's 11 bits (of the share around code 8), sums of `keys` keys by tiles of
+    # 16 cut off at 24 bits, exponentials and quotients by 2^-21, the output's rounding
+    tiles = keys / 16 + 16
+    bound = mid * 2.0 ** -11 + (mid + rest) * (tiles * 2.0 ** -23 + 2.0 ** -20) + np.abs(want) * UNIT[dtype] + TINY[dtype]
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert np.all(err <= bound), float((err / bound).max())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("at", [3, 64, 300])
+@pytest.mark.parametrize("D,n", SIZES)
+def test_a_key_far_above_the_others(pq2, D, n, at, dtype):
+    # a score past 2^30 behind scores of 0: that key's value, exactly weighed
+    ln = at + n + 6
+    rng = np.random.default_rng(D + n)
+    k = np.zeros((ln, D))
+    k[at] = 60000.0
+    c = _cache(pq2, k, rng.standard_normal((ln, D)))
+    q = torch.full((n, G, D), 60000.0, dtype=TYPES[dtype], device=DEV)
+    got = _attend(pq2, c, q, [n], [ln])
+    assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+    v, mid, rest = _held(c, ln)
+    _close(got, np.broadcast_to(v[at], got.shape), mid[at], rest[at], ln, dtype)
+
+
+@pytest.mark.parametrize("size", [30.0, 3e3, 4e4])
+@pytest.mark.parametrize("D,n", SIZES)
+def test_equal_keys_weigh_the_same(pq2, D, n, size):
+    # the same large score for all keys: the mean of the values, whatever 32 bits keep of the score
+    ln = n + 290
+    rng = np.random.default_rng(D + n)
+    c = _cache(pq2, np.broadcast_to(1e3 * rng.standard_normal(D), (ln, D)), rng.standard_normal((ln, D)))
+    q = torch.from_numpy(np.clip(size * rng.standard_normal((n, G, D)), -6e4, 6e4)).half().to(DEV)
+    got = _attend(pq2, c, q, [n], [ln])
+    assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+    seen = np.arange(ln - n, ln) + 1
+    v, mid, rest = (np.cumsum(a, 0)[seen - 1] / seen[:, None] for a in _held(c, ln))
+    _close(got, np.repeat(v[:, None], G, 1), mid[:, None], rest[:, None], ln, "f16")
