@@ -190,8 +190,8 @@ __device__ __forceinline__ void load_rows(Rows<D, RG>& r, uint4* q, const pq2h::
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
-    // the row times a power of two, its largest value in [2^7, 2^8): an eighth
-    // of the steps below fp16's smallest normal number is 2^-32 of it
+    // the row times a power of two, its largest value in [2^7, 2^8): half a step of a
+    // sixteenth below fp16's smallest normal number is 2^-28 of it
     const int e = top > 0.0f ? 134 - static_cast<int>(__float_as_uint(fmaxf(top, 0x1p-100f)) >> 23) : 0;
     const float up = __uint_as_float(static_cast<uint32_t>(127 + min(e, 126)) << 23);
 #pragma unroll

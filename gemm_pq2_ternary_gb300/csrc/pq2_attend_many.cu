@@ -84,13 +84,12 @@ static_assert(sizeof(Slot) % 16 == 0, "");
 struct Bars {
     uint64_t full[2][2], empty[2][2];  // of keys and of values, by buffer
     uint64_t slot_full[kSlots], slot_empty[kSlots];
-    uint64_t q_max, q_full;
+    uint64_t q_full;
     uint64_t s_full[2], p_full[2][2], pv_done[2];  // p_full: of each warpgroup
     uint64_t out_full[2];  // all products of an accumulator's segment
-    int top[2];  // largest |q|, as bits, of this and the next segment
-    float back;  // inverse of the power of two that the queries are multiplied by
     int abort_word;
     uint32_t tmem;
+    float back[256];  // inverses of the powers of two that the rows of queries are multiplied by
 };
 
 template <int D>
@@ -666,7 +665,7 @@ __device__ __forceinline__ bool rows_of_segment(const Ctl& k, const AttendWork& 
     const int G = p.q_heads / p.cache.heads;
     const bool there = tile * 128 + row0 < s.rows;  // the warp has rows
     const bool whole = s.part < 0;
-    float m[kR], ref = 0x1p-24f, back = 1.0f;
+    float m[kR], ref = 0x1p-24f, back[kR];
     float l[kR], z[kR];
     int last[kR];
     const int back_to = p.window > 0 ? p.window - 1 : s.pos0 + s.n;  // positions that a row sees before its own
@@ -674,8 +673,9 @@ __device__ __forceinline__ bool rows_of_segment(const Ctl& k, const AttendWork& 
     for (int r = 0; r < kR; ++r) {
         m[r] = kEmpty;
         l[r] = z[r] = 0.0f;
-        const int row = s.row_tile * C::kRows + tile * 128 + row0 + (r >> 1) * 16 + (r & 1) * 8 + g;
-        last[r] = s.pos0 + min(row / G, s.n - 1);
+        const int row = tile * 128 + row0 + (r >> 1) * 16 + (r & 1) * 8 + g;
+        last[r] = s.pos0 + min((s.row_tile * C::kRows + row) / G, s.n - 1);
+        back[r] = k.bars.back[row];
     }
     bool more_tiles = true;
 #pragma unroll 1
@@ -689,7 +689,6 @@ __device__ __forceinline__ bool rows_of_segment(const Ctl& k, const AttendWork& 
         more_tiles = slot.last == 0;
         count.ends = slot.last == 2;
         if (there) {
-            if (j == 0) back = *reinterpret_cast<volatile float*>(&k.bars.back);
             const int key0 = slot.key0;  // (-1: all rows see the whole tile)
             const uint32_t at_s = lanes + 256 + buf * 128;
             // 32 keys at a time, in a loop: with a tile's code unrolled, the roles'
@@ -735,7 +734,7 @@ __device__ __forceinline__ bool rows_of_segment(const Ctl& k, const AttendWork& 
                     top[r] = fmaxf(v[0], v[1]);
 #pragma unroll
                     for (int c = 1; c < kGroups; ++c) top[r] = fmaxf(fmaxf(top[r], v[4 * c]), v[4 * c + 1]);
-                    top[r] *= back;
+                    top[r] *= back[r];
                     more |= top[r] > m[r] + kSlack;
                 }
                 if (__builtin_expect(__any_sync(0xffffffffu, more), 0)) {
@@ -805,7 +804,7 @@ __device__ __forceinline__ bool rows_of_segment(const Ctl& k, const AttendWork& 
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
                             const int at = 4 * c + 2 * h, r = 2 * i + (h & 1), key = 2 * (h >> 1);
-                            const float w0 = ex2(fmaf(x[i][at], back, -m[r])), w1 = ex2(fmaf(x[i][at + 1], back, -m[r]));
+                            const float w0 = ex2(fmaf(x[i][at], back[r], -m[r])), w1 = ex2(fmaf(x[i][at + 1], back[r], -m[r]));
                             l[r] += w0 + w1;
                             z[r] = fmaf(w1, zs[key + 1], fmaf(w0, zs[key], z[r]));
                             w[i][2 * c + h] = half2_bits(w0 * f[key], w1 * f[key + 1]);
@@ -928,7 +927,9 @@ __device__ __forceinline__ void softmax(const Ctl& k, const AttendWork& wk, uint
         const bool two = its.two;
         // --- the queries ---------------------------------------------------
         {
-            // pieces of 8 values: as they are to their places, then the operands.  (Kept in
+            // pieces of 8 values: as they are to their places, then the operands, every row
+            // with a power of two of its own, so that it does not depend on the rows beside it
+            // (one for all rows was no faster: a prompt 715 us, not 714).  (Kept in
             // registers between the two, their code would be 16 times as long, and code
             // that is run once a segment comes from L2.)
             constexpr int kPieces = C::kRows * (D / 8) / 256;  // a thread
@@ -953,7 +954,6 @@ __device__ __forceinline__ void softmax(const Ctl& k, const AttendWork& wk, uint
             const auto values = [&](const uint4& q, float (&v)[8]) {
                 value(q.x, v[0], v[1]), value(q.y, v[2], v[3]), value(q.z, v[4], v[5]), value(q.w, v[6], v[7]);
             };
-            float top = 0.0f;
             const int r0 = s.row_tile * C::kRows + row0;
             int token = r0 / G, head = r0 - token * G;
             const int tokens = kStride / G, heads = kStride - tokens * G;
@@ -971,36 +971,21 @@ __device__ __forceinline__ void softmax(const Ctl& k, const AttendWork& wk, uint
                     if (head >= G) head -= G, ++token;
                 }
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    *place(i0 + i) = raw[i];
-                    float v[8];
-                    values(raw[i], v);
-#pragma unroll
-                    for (int x = 0; x < 8; ++x)  // (a row with an infinity or a NaN is not the others' concern)
-                        if (fabsf(v[x]) < __uint_as_float(0x7f800000u)) top = fmaxf(top, fabsf(v[x]));
-                }
+                for (int i = 0; i < kBatch; ++i) *place(i0 + i) = raw[i];
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            // (the segment before's maximum has been read by all: this warp's, or
-            // its own segment's end, came after q_full)
-            if (tid == 0) *reinterpret_cast<volatile int*>(&k.bars.top[(seg + 1) & 1]) = 0;
-            if (lane == 0) {
-                atomicMax(&k.bars.top[seg & 1], __float_as_int(top));
-                mbar_arrive(&k.bars.q_max);
-            }
-            if (!k.warp_wait(&k.bars.q_max, seg & 1)) return;
-            top = __int_as_float(*reinterpret_cast<volatile int*>(&k.bars.top[seg & 1]));
-            // all rows times one power of two, the largest value in [1, 2); its
-            // inverse goes to the scores' factors
-            const int ex = top > 0.0f ? max(127 - static_cast<int>(__float_as_uint(fmaxf(top, 0x1p-100f)) >> 23), -126) : 0;
-            const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-            if (tid == 0) k.bars.back = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
 #pragma unroll 2
             for (int i = 0; i < kPieces; ++i) {
                 const int row = row0 + i * kStride;
-                float v[8], sum = 0.0f;
+                float v[8], sum = 0.0f, top = 0.0f;
                 values(*place(i), v);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) top = fmaxf(top, fabsf(v[x]));
+#pragma unroll
+                for (int o = D / 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                // every row times a power of two of its own, its largest value in [2^14, 2^15): half
+                // a step of a sixteenth below fp16's smallest normal number is 2^-35 of it
+                const int e = top > 0.0f ? 141 - static_cast<int>(__float_as_uint(fmaxf(top, 0x1p-100f)) >> 23) : 0;
+                const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
                 uint32_t h[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
@@ -1016,6 +1001,7 @@ __device__ __forceinline__ void softmax(const Ctl& k, const AttendWork& wk, uint
 #pragma unroll
                 for (int o = D / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 if (col == 0) {
+                    k.bars.back[row] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
                     sum *= 0x1p-14f;
                     const float hi = __half2float(__float2half_rn(sum));
                     *reinterpret_cast<uint4*>(smem + C::kAugAt + at * 2048 + r * 16) =
@@ -1025,6 +1011,8 @@ __device__ __forceinline__ void softmax(const Ctl& k, const AttendWork& wk, uint
             fence_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&k.bars.q_full);
+            // (a warp's rows of scores may be others' of queries)
+            if (!k.warp_wait(&k.bars.q_full, seg & 1)) return;
         }
         // --- the tiles and the outputs ---------------------------------------
         if constexpr (C::kTiles == 2) {
@@ -1058,7 +1046,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         wk.join[blockIdx.x] = {0, 0, 0, 0, 0};
         for (int i = 0; i < kSlots; ++i) mbar_init(&bars.slot_full[i], 1), mbar_init(&bars.slot_empty[i], 8 + kExpandWarps);
-        mbar_init(&bars.q_max, 8);
         mbar_init(&bars.q_full, 8);
         for (int i = 0; i < 2; ++i) {
             for (int b = 0; b < 2; ++b) mbar_init(&bars.full[i][b], kExpandWarps / 2), mbar_init(&bars.empty[i][b], 1);
@@ -1066,7 +1053,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars.p_full[i][0], 4), mbar_init(&bars.p_full[i][1], 4);
             mbar_init(&bars.pv_done[i], 1);
             mbar_init(&bars.out_full[i], 1);
-            bars.top[i] = 0;
         }
         bars.abort_word = 0;
         fence_mbar_init();

@@ -625,12 +625,17 @@ pq2_status pq2_cache4_read(const pq2_cache4_read_args* args, void* stream);
  * v of key/value head h / (q_heads / heads).  The new tokens' keys and values
  * have to be in the cache (pq2_cache4_append).  A row that sees nothing (its position
  * below 0) gives zeros.  Scores, maxima, sums and accumulated outputs are
- * fp32; q enters the products with the 11 bits of its type or the fp16 rounding of its
- * row scaled by a power of two (bf16: no rounding within 2^28 of the row's
- * largest; where max_rows * q_heads / heads > 48, or 32 with dim 256, up to 256
- * rows of a sequence are scaled alike, and a value is off by up to 2^-22 of the largest of them),
- * the weights w times the values' scales as fp16, scaled by powers of two
- * likewise.
+ * fp32.  What enters the products with fewer bits, for a sequence with up to 48 rows per
+ * key/value head (n q_heads / heads; 32 with dim 256) and, in brackets, with more:
+ *   q           times a power of two of its row's own, as fp16: a value is off by at most 2^-28
+ *               [2^-35] of the row's largest, and those within 2^17 [2^24] of that
+ *               (bf16: 2^20 [2^27]) are exact.  [The row's sum is kept to 2^-22 of itself or 2^-31
+ *               of the row's largest, a key's offset to 2^-21 of itself or 2^-17 of its scale, and a
+ *               scale below 2^-25 of its offset counts as that.]
+ *   weights w   times the values' scales over a power of two, as fp16: 11 bits of itself,
+ *               or a key's part of an output to 2^-27 of the largest values' scale
+ *               that the rows worked on together see (up to 256 of a sequence)
+ * (B == 1: max_rows, or M, stands for the sequence's rows.)
  *   q, out     [M, q_heads, dim] (type: PQ2_F16 or PQ2_BF16), token and head
  *              strides in elements, a head's values adjacent
  *   max_rows   an upper bound of the sequences' rows that the host knows

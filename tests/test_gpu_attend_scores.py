@@ -77,3 +77,58 @@ def test_equal_keys_weigh_the_same(pq2, D, n, size):
     seen = np.arange(ln - n, ln) + 1
     v, mid, rest = (np.cumsum(a, 0)[seen - 1] / seen[:, None] for a in _held(c, ln))
     _close(got, np.repeat(v[:, None], G, 1), mid[:, None], rest[:, None], ln, "f16")
+
+
+def _unlike(D, n, dtype):
+    """Queries of which every third row is small next to its neighbours, keys
+    so large that the small rows' scores spread over several units."""
+    rng = np.random.default_rng(D + n)
+    low, high, scale = (2.0 ** -10, 2.0 ** 13, D ** -0.5) if dtype == "f16" else (2.0 ** -20, 2.0 ** 20, 2.0 ** 10 * D ** -0.5)
+    size = np.array([low, 1.0, high])[(np.arange(n * G) * 2 % 3)].reshape(n, G, 1)
+    q = torch.from_numpy(rng.standard_normal((n, G, D)) * size).to(TYPES[dtype])
+    ln = n + 60
+    k = rng.standard_normal((ln, D)) * (2.0 / (low * scale * D ** 0.5))
+    return q, k, rng.standard_normal((ln, D)), scale, (size == low)[..., 0]
+
+
+def _bound(q, pool, pages, n, ln, scale, dtype):
+    want, tol = ref.attend(_np(q), pool, pages, [0, n], [ln], T, scale)
+    return want, tol + np.abs(want) * UNIT[dtype] + TINY[dtype]
+
+
+def _rounded(q, step):
+    """q with all values of all rows to whole steps of `step` times the largest."""
+    step = step * float(q.float().abs().max())
+    return torch.round(q.double() / step) * step
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D,n", SIZES)
+def test_rows_keep_what_they_have_next_to_larger_ones(pq2, D, n, dtype):
+    q, k, v, scale, small = _unlike(D, n, dtype)
+    c = _cache(pq2, k, v)
+    ln = len(k)
+    got = _attend(pq2, c, q.to(DEV), [n], [ln], scale=scale).double().cpu().numpy()
+    assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+    pool = c.pool.cpu().numpy()
+    want, bound = _bound(q, pool, c.pages, n, ln, scale, dtype)
+    assert np.all(np.abs(got - want) <= bound), float((np.abs(got - want) / bound)[small].max())
+    # what one step for all rows would do is far outside the bound of the small ones
+    if n > 1:
+        coarse, _ = ref.attend(_rounded(q, 2.0 ** -18).numpy(), pool, c.pages, [0, n], [ln], T, scale)
+        assert np.any((np.abs(coarse - want) > 4 * bound)[small])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D,n", [(64, 60), (128, 60), (256, 40)])
+def test_a_row_does_not_depend_on_the_rows_after_it(pq2, D, n, dtype):
+    # the first rows' queries stay, the others' grow: the same bits for the first
+    rng = np.random.default_rng(D)
+    ln = n + 70
+    c = _cache(pq2, rng.standard_normal((ln, D)), rng.standard_normal((ln, D)))
+    q = torch.from_numpy(rng.standard_normal((n, G, D))).to(TYPES[dtype]).to(DEV)
+    grown = q.clone()
+    grown[n // 3:] *= 2.0 ** 12
+    one, two = (_attend(pq2, c, x, [n], [ln]) for x in (q, grown))
+    assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+    assert torch.equal(one[:n // 3], two[:n // 3])
