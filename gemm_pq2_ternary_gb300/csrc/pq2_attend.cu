@@ -36,6 +36,7 @@
 // spilled); 24 sequences of up to 5003 with 5 tokens each, 40 heads of 128 on 8: 59 us (62
 // with 8 rows a pass).
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <type_traits>
 
@@ -61,7 +62,7 @@ constexpr int kMostRows = 16;       // of a pass
 // 64 96, 96 99; drafts, 25 rows: 16 69 us, 32 59, 48 57).
 template <int RG>
 constexpr int kExtra = RG == 1 ? 32 : 48;
-constexpr float kEmpty = -1e30f;    // maximum of a row that has seen nothing
+constexpr float kEmpty = -FLT_MAX;  // maximum of a row that has seen nothing: below any score
 constexpr float kSlack = 5.0f;      // how far (as a power of two) a score may exceed the maximum
 constexpr float kWeight = 512.0f;  // weights enter the product times this
 

@@ -38,6 +38,7 @@
 // 714 us, 866 TFLOP/s; 3 chunks of up to 1000 tokens behind up to 5000, 40 heads of 128 on 8:
 // 295 us (mma.sync, 8 rows at a time: 4528 and 1250 us).
 #include <algorithm>
+#include <cfloat>
 
 #include "pq2_attend.cuh"
 
@@ -51,7 +52,7 @@ constexpr int kChunk = 16384;             // bytes
 constexpr int kSlots = 4;                 // tiles whose factors are held
 constexpr int kExtra = 6;                 // what an item's queries and outputs take, in tiles (2: 390 us for
                                           // chunks behind 6000 tokens, 3: 333, 4: 324, 6: 316)
-constexpr float kEmpty = -1e30f;
+constexpr float kEmpty = -FLT_MAX;
 // (Larger and smaller than pq2_attend.cu's 5 and 512: a raise touches all outputs in
 // tensor memory.  A prompt took 862, 776 and 731 us with 2, 5 and 8, chunks 356, 315 and 296.)
 constexpr float kSlack = 8.0f;
@@ -216,8 +217,7 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 // ---------------------------------------------------------------------------
 // r (of a key) and sum(q) are two fp16 each, hi + lo; three of their products are
 // summed: hi hi + (hi kAugLo) (lo / kAugLo) + (lo kAugHi2) (hi / kAugHi2).  With those powers of
-// two no factor falls so far below fp16's normal numbers that the scores notice (sum(q)'s
-// lo as it is would be off by 2^-14 of sum(q)).
+// two no factor falls so far below fp16's normal numbers that the scores notice.
 constexpr float kAugLo = 0x1p-6f, kAugHi2 = 0x1p3f;
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);

@@ -646,7 +646,9 @@ pq2_status pq2_cache4_read(const pq2_cache4_read_args* args, void* stream);
  *              enough for fewer rows too
  * Pages outside the pool among those that a sequence needs: its rows are
  * undefined and the device error word is set; lens past W T likewise (nothing behind the
- * table is read).  NaN or Inf in q: that row and head undefined.
+ * table is read).  NaN or Inf in q: that row and head undefined; the same where scale times a
+ * value, or that times a value or a scale of a key, is 2^108 or more in size, or scale
+ * itself 2^80.  out and q do not overlap.
  * Results do not depend on other sequences' contents, but the order in which a
  * row's partial sums are joined depends on the sequences' lengths.
  * M >= 0, B >= 0 (0 enqueues nothing), q_heads % heads == 0, q_heads / heads <= 64,

@@ -79,6 +79,21 @@ def test_equal_keys_weigh_the_same(pq2, D, n, size):
     _close(got, np.repeat(v[:, None], G, 1), mid[:, None], rest[:, None], ln, "f16")
 
 
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("D,n", SIZES)
+def test_scores_past_any_that_stands_for_nothing_seen(pq2, D, n, sign):
+    # scores of about +-2^107, all the same
+    ln = n + 40
+    rng = np.random.default_rng(D + n)
+    c = _cache(pq2, np.full((ln, D), -8.0), rng.standard_normal((ln, D)))
+    q = torch.full((n, G, D), sign * 2.0 ** 100, dtype=torch.bfloat16, device=DEV)
+    got = _attend(pq2, c, q, [n], [ln])
+    assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+    seen = np.arange(ln - n, ln) + 1
+    v, mid, rest = (np.cumsum(a, 0)[seen - 1] / seen[:, None] for a in _held(c, ln))
+    _close(got, np.repeat(v[:, None], G, 1), mid[:, None], rest[:, None], ln, "bf16")
+
+
 def _unlike(D, n, dtype):
     """Queries of which every third row is small next to its neighbours, keys
     so large that the small rows' scores spread over several units."""
