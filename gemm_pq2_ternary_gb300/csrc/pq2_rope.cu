@@ -147,7 +147,7 @@ __device__ __forceinline__ uint32_t quantise_row(const float (&x)[E], uint32_t& 
     return w;
 }
 
-// Where a token stands in the cache; page < 0: nowhere.
+// Where a token stands in the cache; page < 0: nowhere, pos < 0: its position is out of range too.
 struct Place {
     long long pos;
     long long page;
@@ -161,7 +161,9 @@ __device__ __forceinline__ Place place_of(const pq2h::CacheParams& c, int row, c
     if (!mine) return at;
     at.pos = static_cast<long long>(__ldcg(c.lens + seq)) - end + row;
     bool bad = at.pos < 0 || at.pos >= static_cast<long long>(c.W) * c.T;
-    if (!bad) {
+    if (bad) {
+        at.pos = -1;
+    } else {
         const int p = __ldcg(c.pages + seq * c.ld_pages + at.pos / c.T);
         bad = p < 0 || p >= c.num_pages;
         if (!bad) at.page = p;
