@@ -712,7 +712,7 @@ pq2_status pq2_rope_table(float* table, int64_t first, int64_t count, int64_t ro
         (!(s.old_len > 0.0) || !(s.low > 0.0) || !(s.high > s.low) || !std::isfinite(s.old_len) ||
          !std::isfinite(s.high)))
         return PQ2_ERR_INVALID_ARG;
-    if (rot > PQ2_ROPE_MAX_DIM || first + count > (int64_t(1) << 31)) return PQ2_ERR_UNSUPPORTED_SHAPE;
+    if (rot > PQ2_ROPE_MAX_DIM || first > (int64_t(1) << 31) || count > (int64_t(1) << 31) - first) return PQ2_ERR_UNSUPPORTED_SHAPE;
     if (count == 0) return PQ2_OK;
     if (!table) return PQ2_ERR_INVALID_ARG;
     if (!aligned16(table)) return PQ2_ERR_MISALIGNED;
@@ -792,7 +792,7 @@ static pq2_status check_cache(const pq2_cache4& a) {
     if (a.B < 0 || a.W < 0 || a.num_pages < 0 || a.heads < 1 || a.reserved != 0) return PQ2_ERR_INVALID_ARG;
     const size_t page = pq2_cache4_page_bytes(a.heads, a.dim, a.page_tokens);
     if (page == 0 || a.B > (int64_t(1) << 20) || a.num_pages > (int64_t(1) << 30) || a.page_stride % 16 != 0 ||
-        a.W * a.page_tokens > (int64_t(1) << 30) || a.W > (int64_t(1) << 30))
+        a.W > (int64_t(1) << 30) || a.W * a.page_tokens > (int64_t(1) << 30))
         return PQ2_ERR_UNSUPPORTED_SHAPE;
     if (a.page_stride < static_cast<int64_t>(page) || a.ld_pages < a.W) return PQ2_ERR_INVALID_ARG;
     return PQ2_OK;
