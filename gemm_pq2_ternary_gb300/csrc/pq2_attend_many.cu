@@ -60,6 +60,7 @@ constexpr float kWeight = 64.0f;
 constexpr int kExpandWarps = 8;
 constexpr int kFactorWarps = 3;
 constexpr int kIssuer = 16;
+constexpr int kSkipValues = 1 << 16;  // (timeout tests) from here on it is a piece of values that is withheld
 constexpr int kRegsSoftmax = 128, kRegsExpand = 72, kRegsOther = 80;
 constexpr int kRegsNeeded = 256 * kRegsSoftmax + 256 * kRegsExpand + 128 * kRegsOther;
 static_assert(kRegsNeeded <= kThreads * 96, "the launch's registers");
@@ -411,7 +412,7 @@ __device__ __forceinline__ void expand(const Ctl& k, const Slot* slots, uint8_t*
     const int j = (lane & 1) + 2 * (kDims == 256 ? phase : kDims == 128 ? phase & 1 : 0);
     const int in16 = ((lane >> 1) & 3) + 4 * (kDims == 256 ? 0 : kDims == 128 ? phase >> 1 : phase);
     const int row0 = kRows * warp + in16;
-    const int skip = VALUES ? -1 : k.p.ctl.debug_skip_stage;
+    const int skip = k.p.ctl.debug_skip_stage - (VALUES ? kSkipValues : 0);
     // where the lane's rows are in a piece (its 64 dims are block j / 2), and its
     // 16 bytes in a row: with 4 rows at a time every other row has the other half's
     // (a warp's rows are in one chunk of values: kPartKeys is a multiple of them)

@@ -866,7 +866,8 @@ pq2_status pq2_debug_set_wait_limit_ns(uint64_t ns);
  * pq2_debug_skip_stage -- test hook: from now on, the producer of every
  * bulk-copy pipeline withholds its stage number `stage` (never issues it), so
  * the consumers' bounded wait runs out and the call reports PQ2_ERR_TIMEOUT
- * through pq2_last_device_error.  -1 turns it off (the default).
+ * through pq2_last_device_error.  -1 turns it off (the default).  Attention with
+ * many rows withholds a piece of expanded keys, or piece stage - 65536 of values.
  */
 pq2_status pq2_debug_skip_stage(int stage);
 

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_cache4 import Cache, _dev
+from test_gpu_cache4 import Cache, _attend, _check, _dev, _q
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +43,71 @@ def test_queries_of_tokens_without_a_place(pq2, D, out, angles):
         assert pq2.pq2_last_device_error() == pq2.PQ2_ERR_INVALID_ARG
         written = (q_out != 9.0).any(-1).any(-1).tolist()
         assert written == there, (n, ln)
+
+
+@pytest.mark.parametrize("G", [25, 33, 48, 64])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 2, 7])
+def test_groups_of_many_heads(pq2, G, D, n):
+    lens = [n, 40, 131]
+    c = Cache(pq2, 3, 9, 1, D, 16, seed=G)
+    pool = c.fill(lens)
+    q = _q(3 * n, G, D, "f16")
+    got = _attend(pq2, c, q, [n] * 3, lens, max_rows=n)
+    assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+    _check(got, q, pool, c, [n] * 3, lens)
+
+
+@pytest.mark.parametrize("D,G,n", [(64, 1, [47, 48, 49, 50, 2]), (128, 3, [15, 16, 17, 1, 0]), (128, 1, [49, 48, 0, 49, 1]),
+                                   (256, 1, [31, 32, 33, 34, 1]), (256, 4, [9, 8, 7, 9, 0])])
+@pytest.mark.parametrize("window", [0, 37])
+def test_rows_on_both_sides_of_the_change_of_kernel(pq2, D, G, n, window):
+    # sequences with just as many rows as the one kernel takes, and with one more, in one call
+    lens = [max(k, 20 + 30 * i) for i, k in enumerate(n)]
+    c = Cache(pq2, len(n), -(-max(lens) // 16), 1, D, 16, seed=D)
+    pool = c.fill(lens)
+    q = _q(sum(n) + 1, G, D, "bf16")
+    for max_rows in (0, max(n)):
+        got = _attend(pq2, c, q, n, lens, window, max_rows=max_rows)
+        assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+        _check(got, q, pool, c, n, lens, window, dtype="bf16")
+        assert torch.all(got[sum(n):] == 7.0)
+    for n0 in sorted(set(n)):                  # and alone
+        if n0 == 0:
+            continue
+        b = n.index(n0)
+        r0 = sum(n[:b])
+        one = Cache.__new__(Cache)
+        one.T, one.D, one.H, one.pool, one.pages, one.dev = 16, D, 1, c.pool, c.pages[b:b + 1], c.dev[b:b + 1].contiguous()
+        alone = _attend(pq2, one, q[r0:r0 + n0].contiguous(), [n0], [lens[b]], window)
+        _check(alone, q[r0:r0 + n0], pool, one, [n0], [lens[b]], window, dtype="bf16")
+
+
+VALUES = 1 << 16   # withheld pieces of values, with many rows
+
+
+@pytest.mark.parametrize("D,n", [(64, 1), (128, 1), (256, 1), (64, 20), (128, 20), (256, 20)])
+@pytest.mark.parametrize("stage", [1, 2, 3, 4, VALUES, VALUES + 1, VALUES + 2, VALUES + 3])
+def test_a_piece_that_never_comes(pq2, D, n, stage):
+    # 24 tiles and more for each warp, or CTA; few rows have no pieces of values
+    ln, W, G = 60000, 200, 6
+    pool = torch.zeros((2, 1, 16 * (D + 8) * 20), dtype=torch.uint8, device=DEV)
+    pages = _dev(np.arange(64 * W).reshape(64, W) % 2)
+    q = _q(64 * n, G, D, "f16")
+    out = torch.empty_like(q)
+    ws = pq2.alloc_attend_workspace(64 * n, G, 1, D)
+    start, lens = _dev(n * np.arange(65)), _dev(np.full(64, ln))
+
+    def run():
+        pq2.pq2_cache4_attend(q, pool, pages, start, lens, out, ws, max_rows=n)
+        return pq2.pq2_last_device_error()
+
+    assert run() == pq2.PQ2_OK and torch.all(out == 0)
+    try:
+        pq2.pq2_debug_set_wait_limit_ns(20_000_000)
+        pq2.pq2_debug_skip_stage(stage)
+        assert run() == (pq2.PQ2_OK if n == 1 and stage >= VALUES else pq2.PQ2_ERR_TIMEOUT)
+    finally:
+        pq2.pq2_debug_skip_stage(-1)
+        pq2.pq2_debug_set_wait_limit_ns(2_000_000_000)
+    assert run() == pq2.PQ2_OK and torch.all(out == 0)
