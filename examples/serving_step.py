@@ -137,9 +137,10 @@ class Attention:
         self.q, self.a = (empty(rows, q_heads, dim, dtype=torch.float16) for _ in range(2))
         self.y, self.r_out = (empty(rows, block.hidden) for _ in range(2))
 
-    def step(self, r, row_start, keep):
+    def step(self, r, row_start, keep, max_rows=0):
         """r fp32 [rows, hidden] with row_start int32 [requests + 1]; keep int32
-        [requests]: tokens of the cache that still hold (refused drafts do not)."""
+        [requests]: tokens of the cache that still hold (refused drafts do not);
+        max_rows: rows of any request at most, where the host knows (0: all)."""
         b, now = self.block, self.turn
         after = keep + (row_start[1:] - row_start[:-1])
         pq2.pq2_pages_update(self.pages[now], self.refs[now], self.lens, self.source, keep, after, self.page,
@@ -152,7 +153,8 @@ class Attention:
         h = self.q_heads
         pq2.pq2_cache4_append(self.rows[:, h:h + self.heads], self.rows[:, h + self.heads:], self.pool, pages, row_start,
                               after, q=self.rows[:, :h], q_out=self.q, table=self.angles)
-        pq2.pq2_cache4_attend(self.q, self.pool, pages, row_start, after, self.a, self.ws_attend)
+        pq2.pq2_cache4_attend(self.q, self.pool, pages, row_start, after, self.a, self.ws_attend,
+                              max_rows=max_rows)
         pq2.pq2_matmul(self.a.view(b.rows, -1), *self.out, self.y, self.ws_out)
         pq2.pq2_norm_residual(self.y, r, self.r_out, w_post=b.w2, eps=EPS, alpha=ALPHA)
         return self.r_out
@@ -195,7 +197,7 @@ def main():
 
     def step():
         nonlocal keep
-        r = attention.step(args["r"], args["row_start"], keep)
+        r = attention.step(args["r"], args["row_start"], keep, a.drafts + 1)
         accepted, tokens = block.step(**{**args, "r": r})
         keep = keep + accepted + 1      # the drafts kept and the token before them
         return accepted, tokens

@@ -1,10 +1,16 @@
 """The 4-bit cache at the edges of what a call may hold: tokens without a place,
 groups of many heads, numbers of rows on both sides of a change of kernel."""
+import os
+import sys
+
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_cache4 import Cache, _attend, _check, _dev, _q
+from oracle import attention as ref
+from test_gpu_cache4 import Cache, _attend, _check, _dev, _np, _q
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +117,21 @@ def test_a_piece_that_never_comes(pq2, D, n, stage):
         pq2.pq2_debug_skip_stage(-1)
         pq2.pq2_debug_set_wait_limit_ns(2_000_000_000)
     assert run() == pq2.PQ2_OK and torch.all(out == 0)
+
+
+@pytest.mark.parametrize("drafts", [0, 7])
+def test_steps_of_the_serving_example_that_know_their_rows(pq2, drafts):
+    import serving_step
+    B, q_heads, heads, dim = 9, 4, 1, 128
+    block = serving_step.Block(B * (drafts + 1), 512, 640, 1000, 2, 16, B)
+    args = serving_step.random_step(block, drafts, 2)
+    at = serving_step.Attention(block, q_heads, heads, dim, 40 * (drafts + 1), page=16)
+    keep = torch.zeros(B, dtype=torch.int32, device=DEV)
+    for step in range(3):
+        at.step(args["r"] * (1 + step), args["row_start"], keep, max_rows=drafts + 1)
+        assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+        want, tol = ref.attend(_np(at.q), at.pool.cpu().numpy(), at.pages[at.turn].cpu().numpy(),
+                               args["row_start"].cpu().numpy(), at.lens.cpu().numpy(), 16, dim ** -0.5, 0)
+        err = np.abs(at.a.double().cpu().numpy() - want)
+        assert np.all(err <= tol + np.abs(want) * 2.0 ** -11 + 2.0 ** -24)
+        keep = keep + drafts + 1
