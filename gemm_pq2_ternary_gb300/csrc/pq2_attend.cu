@@ -28,13 +28,13 @@
 // results in shared memory; a head whose tiles lie in several CTAs is joined by a second
 // kernel, in the CTAs' order.
 //
-// Bound by instructions and their latency: some 340 a tile of 16 tokens and head, most of
-// them on the integer pipe (operands from codes), issued at 52% of the rate.  On GB300: 131071
-// tokens, 24 heads of 256 on 4: 45 us, 3.0 TB/s (58 with loads into registers, 8 warps an
-// SM and a join of one warp's loads at a time); 64 sequences of up to 8192, 48 heads of 128 on
-// 8: 94 us, 3.0 TB/s (107 to 147 while the list counted tiles alone and registers were
-// spilled); 24 sequences of up to 5003 with 5 tokens each, 40 heads of 128 on 8: 59 us (62
-// with 8 rows a pass).
+// Bound by instructions and their latency: 484 warp instructions a tile of 16 tokens and head of
+// 128 dims, 650 of 256, most of them on the integer pipe (operands from codes), issued at 53% and
+// 47% of the rate.  On GB300: 131071 tokens, 24 heads of 256 on 4: 46 us, 3.0 TB/s (58 with
+// loads into registers, 8 warps an SM and a join of one warp's loads at a time); 64 sequences of up
+// to 8192, 48 heads of 128 on 8: 94 us, 3.0 TB/s (107 to 147 while the list counted tiles alone
+// and registers were spilled); 75 tokens of 24 sequences of up to 5003, 40 heads of 128 on 8: 59 us
+// (62 with 8 rows a pass).  Two groups of rows of 128 dims spill 216 bytes.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -700,8 +700,12 @@ cudaError_t launch_attend(const AttendParams& args, void* workspace, cudaStream_
     };
     if (!many) return p.max_rows * G > 8 ? run(std::integral_constant<int, 2>()) : run(std::integral_constant<int, 1>());
     // Prompts and decoding sequences in one call: each to its kernel, one after the
-    // other, in the same workspace.  2000 tokens behind 500 with 256 sequences of
-    // one token behind 1000, 40 heads of 128 on 8: 302 us; all by the other kernel 795.
+    // other, in the same workspace.  2000 tokens behind 500, 40 heads of 128 on 8, with 256
+    // sequences of one token behind 1000: 275 us, all by the other kernel 800; with 64 of 3 behind
+    // 2000: 260 and 447; with 24 of 9 behind 3000: 304 and 320.  24 heads of 256 on 4 with
+    // 256 of one: 278 and 380; with 24 of 5 behind 3000: 254 and 193 (the worst case of this rule).
+    // 8 rows a pass: nothing bounds the rows of the short sequences, and most have one token.
+    // With 16 the five took 325, 246, 275, 313 and 237 us.
     const cudaError_t e = run(std::integral_constant<int, 1>());
     if (e != cudaSuccess) return e;
     p.over = p.upto, p.upto = INT_MAX;

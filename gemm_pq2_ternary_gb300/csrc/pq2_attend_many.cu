@@ -35,8 +35,10 @@
 // registers that had to be moved to uniform ones (100 cycles a product), waits one
 // by one, an address read from shared memory before every load of codes, and items that
 // counted for their tiles alone.  On GB300: 4096 tokens behind 4096, 24 heads of 256 on 4:
-// 714 us, 866 TFLOP/s; 3 chunks of up to 1000 tokens behind up to 5000, 40 heads of 128 on 8:
-// 295 us (mma.sync, 8 rows at a time: 4528 and 1250 us).
+// 717 us, 863 TFLOP/s, for the first calls after a pause, and 757 us, 817 TFLOP/s, in a row of a hundred
+// (in a graph as from the host; the SM clock reads its maximum throughout, at 900 W); chunks of 1000,
+// 948 and 895 tokens, the last of 6000, 948 and 1895, 40 heads of 128 on 8: 294 us (mma.sync, 8
+// rows at a time: 4528 and 1250 us).
 #include <algorithm>
 #include <cfloat>
 

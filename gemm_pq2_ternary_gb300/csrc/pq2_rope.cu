@@ -14,11 +14,14 @@
 // are found once.  A pair's other half is loaded by both lanes that need it (the second
 // time from L1).  A row's least and largest value, which its scale and offset come
 // from, are one reduction over the warp each.  With inputs' type and pairing known when it
-// is compiled it needs 64 registers (80 with the cache), and 32 (24) warps of an SM
-// keep memory busy: 4096 tokens of 28 heads of 256 (fp32 in, bf16 out) 30 us, 5.9 TB/s
-// (two heads a warp and no more, both types in one kernel: 53 us).  Into the cache the
-// issue of instructions is the limit: 5105 tokens of 64 heads of 128 in 48 us, and read
-// back in 13.
+// is compiled it is held to 64 registers (80 with the cache), so that 32 (24) warps of an SM
+// keep memory busy.  Neighbours fit (of 256 dims into the cache but for 12 bytes); halves of
+// 256 dims spill 112 to 156 bytes (into the cache 24 to 132, of 128 dims 20).  4096 tokens of 28
+// heads of 256 (fp32 in, bf16 out), floor 26.9 us: neighbours 30.6 us, halves 47.8; bf16
+// in, floor 18.2: 29.3 and 43.3.  Parts whose half is no multiple of a lane's values, loaded
+// one at a time: 52 and 75 us (fp32, 122 of 256).  Into the cache the issue of instructions
+// is the limit: 3369 tokens of 64 heads of 128 in 49 us (floor 24; bf16 in 60), and read
+// back in 10 (floor 3.2), where a lane's loads are small.
 #include <algorithm>
 #include <cmath>
 
@@ -501,7 +504,7 @@ bool vector_path(const RopeParams& p, int E, bool cache) {
     return true;
 }
 
-constexpr long long kEnoughWarps = 152 * 48;  // (four times as many: 88 us for 5105 tokens appended
+constexpr long long kEnoughWarps = 152 * 48;  // (four times as many: 88 us for 3369 tokens appended
                                                // and read back, when this took 75)
 
 // Warps for each of M tokens: a token's place and angles are found once for all

@@ -466,7 +466,8 @@ pq2_status pq2_verify_drafts_packed(const pq2_verify_drafts_args* args, void* st
 #define PQ2_ROPE_RAMP 3   /* by the index: f_i where it turns at least `high`
                              times over `old_len` positions, f_i / factor where
                              at most `low` times, and linear in i between the
-                             two indexes (rounded outwards, at least 0.001 apart) */
+                             two indexes (rounded outwards, kept within 0 .. rot - 1,
+                             at least 0.001 apart)                              */
 #define PQ2_ROPE_BANDS 4  /* by the wavelength w = 2 pi / f_i: f_i where
                              w < old_len / high, f_i / factor where w > old_len / low,
                              between them (1 - t) f_i / factor + t f_i with
@@ -509,7 +510,8 @@ pq2_status pq2_rope_table(float* table, int64_t first, int64_t count, int64_t ro
  *   table         in   fp32 [table_rows, rot / 2, 2] (pq2_rope_table, or one's own)
  *   positions     in   int32 [M], rows of the table; a token with one outside
  *                      [0, table_rows) is left as it was in the outputs and sets the device
- *                      error word (PQ2_ERR_INVALID_ARG from pq2_last_device_error)
+ *                      error word (PQ2_ERR_INVALID_ARG from pq2_last_device_error).  With
+ *                      rot == 0 neither it nor the table is read
  * ld_*: strides from token to token, hs_*: from head to head (both >= dim), in
  * elements.  A head's values are adjacent.  The gradient of x is the same call with
  * PQ2_ROPE_INVERSE on the gradient of out.
@@ -733,7 +735,8 @@ pq2_status pq2_pages_compact(const pq2_pages_compact_args* args, void* stream);
  * skipped too and sets the device error word.  No new page may be another pair's old or new one.
  *   pool  16-byte aligned; page_bytes, page_stride (>= page_bytes), layer_stride % 16 == 0
  *   pairs int32 [n, 2], 8-byte aligned
- * n >= 0 (0 enqueues nothing), n <= 2^28, 0 <= layers <= 65536, P >= 0.
+ * n >= 0 (0 enqueues nothing), n <= 2^28, 0 <= layers <= 65536, 0 <= P <= 2^31,
+ * page_bytes <= 2^32.
  */
 pq2_status pq2_pages_copy(void* pool, int64_t page_bytes, int64_t page_stride, int64_t P,
                           int64_t layers, int64_t layer_stride, const int32_t* pairs, int64_t n,

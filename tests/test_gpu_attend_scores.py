@@ -26,7 +26,7 @@ def _cache(pq2, k, v):
     """One sequence of keys and values [tokens, D] (one head)."""
     ln, D = k.shape
     c = Cache(pq2, 1, -(-ln // T), 1, D, T)
-    k, v = (torch.as_tensor(a, dtype=torch.float32, device=DEV)[:, None].contiguous() for a in (k, v))
+    k, v = (torch.from_numpy(np.array(a, np.float32)).to(DEV)[:, None].contiguous() for a in (k, v))
     pq2.pq2_cache4_append(k, v, c.pool, c.dev, _dev([0, ln]), _dev([ln]))
     return c
 
