@@ -132,6 +132,8 @@ struct Rows {
     int first[RG][2], last[RG][2];   // positions that the row sees
     float m[RG][2], l[RG][2], z[RG][2];  // maximum, sum of weights, sum of weights times offsets
     float ref;                       // values' scales over this (a power of two) are below 2
+    float slack;                     // kSlack less the largest b (pq2_attend.cuh)
+    uint32_t bs;
     float o[RG][D / 16][4];          // outputs: dims 2j and 2j + 1 (times 16) of the lane's eighth
     __device__ __forceinline__ uint4 query(const uint4* shared, int u, int w) const {
         if constexpr (kShared)
@@ -143,7 +145,7 @@ struct Rows {
 
 template <int D, int RG>
 __device__ __forceinline__ void clear(Rows<D, RG>& r) {
-    r.ref = 0x1p-24f;
+    r.ref = 0x1p-24f, r.slack = kSlack, r.bs = 0;
 #pragma unroll
     for (int u = 0; u < RG; ++u) {
 #pragma unroll
@@ -224,11 +226,55 @@ __device__ __forceinline__ float inverse(float x) { return __uint_as_float((254u
 
 // Raises maxima and the values' reference where this tile needs it.
 template <int D, int RG>
-__device__ __forceinline__ void raise(Rows<D, RG>& r, const float (&x)[RG][2][2], const float (&s)[2]) {
-    float ref = fmaxf(fmaxf(s[0], s[1]), r.ref);
+__device__ __forceinline__ void raise(Rows<D, RG>& r, const float (&x)[RG][2][2], const float (&s)[2], bool inside, int key) {
+    float ref, top[RG][2];
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
-    ref = __uint_as_float(__float_as_uint(ref) & 0x7f800000u);
+    for (int u = 0; u < RG; ++u)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            top[u][c] = fmaxf(x[u][0][c], x[u][1][c]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) top[u][c] = fmaxf(top[u][c], __shfl_xor_sync(0xffffffffu, top[u][c], o));
+        }
+    if (__all_sync(0xffffffffu, inside && r.bs == 0)) {  // all rows see the same
+        ref = scale_power(fmaxf(warp_max(fmaxf(s[0], s[1])), r.ref));
+#pragma unroll
+        for (int u = 0; u < RG; ++u)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) top[u][c] = fmaxf(top[u][c], r.m[u][c]);
+    } else {
+        Apart apart;
+        float own[RG][2];  // the largest scale of the values that the row sees
+#pragma unroll
+        for (int u = 0; u < RG; ++u)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float most = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (key + 8 * i >= r.first[u][c] && key + 8 * i <= r.last[u][c]) most = fmaxf(most, s[i]);
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                const float b = static_cast<float>(row_b(r.bs, 2 * u + c));
+                const bool empty = r.m[u][c] == kEmpty;
+                own[u][c] = fmaxf(scale_power(most), empty ? 0.0f : r.ref * power_of_two(b));
+                top[u][c] = fmaxf(top[u][c], empty ? kEmpty : r.m[u][c] - b);
+                apart.row(top[u][c], own[u][c], kEmpty);
+            }
+        ref = apart.reference(r.ref);
+        r.bs = 0;
+        float most = 0.0f;
+#pragma unroll
+        for (int u = 0; u < RG; ++u)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int b = top[u][c] == kEmpty ? 0 : max(power_between(ref, own[u][c]), 0);
+                r.bs |= static_cast<uint32_t>(b) << (8 * (2 * u + c));
+                top[u][c] += static_cast<float>(b);
+                most = fmaxf(most, static_cast<float>(b));
+            }
+        r.slack = kSlack - warp_max(most);
+    }
     const float down = r.ref * inverse(ref);
     r.ref = ref;
 #pragma unroll
@@ -236,12 +282,8 @@ __device__ __forceinline__ void raise(Rows<D, RG>& r, const float (&x)[RG][2][2]
         float alpha[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            float top = fmaxf(x[u][0][c], x[u][1][c]);
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            top = fmaxf(top, r.m[u][c]);
-            alpha[c] = ex2(r.m[u][c] - top);
-            r.m[u][c] = top;
+            alpha[c] = r.m[u][c] == kEmpty ? 0.0f : ex2(r.m[u][c] - top[u][c]);
+            r.m[u][c] = top[u][c];
             r.l[u][c] *= alpha[c];
             r.z[u][c] *= alpha[c];
         }
@@ -322,8 +364,8 @@ __device__ __forceinline__ void take_tile(Rows<D, RG>& r, const uint4* q, const 
 #pragma unroll
     for (int u = 0; u < RG; ++u)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) more |= fmaxf(y[u][0][c], y[u][1][c]) > r.m[u][c] + kSlack;
-    if (__any_sync(0xffffffffu, more)) raise<D, RG>(r, y, s);
+        for (int c = 0; c < 2; ++c) more |= fmaxf(y[u][0][c], y[u][1][c]) > r.m[u][c] + r.slack;
+    if (__any_sync(0xffffffffu, more)) raise<D, RG>(r, y, s, inside, key0 + key_of(g));
     const float f = kWeight * inverse(r.ref);
     uint32_t b[RG][2];
 #pragma unroll

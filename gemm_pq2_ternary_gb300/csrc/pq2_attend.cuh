@@ -16,6 +16,53 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Rows of a warp that do not see the same values.  The values' reference is a power of two; scales
+// over it are below 2.  With one that goes by all values a row's weights could sink below fp16's
+// numbers next to values that other rows alone see.  So it goes by the row that sees the smallest
+// ones, and a row that sees values larger by 2^kApart and more has its maximum raised by b, the
+// difference of the two, which takes its weights down as much.  (Rows whose maximum is so large
+// that this is not exact have no b.)
+constexpr int kApart = 4;
+constexpr float kHuge = 0x1p22f;
+
+// b of a lane's rows, 8 bits each.
+__device__ __forceinline__ int row_b(uint32_t bs, int r) { return bs >> (8 * r) & 255; }
+
+// A scale's power of two, fp16's smallest number at least; and such powers' quotient, as an exponent.
+__device__ __forceinline__ float scale_power(float x) {
+    return __uint_as_float(__float_as_uint(fmaxf(x, 0x1p-24f)) & 0x7f800000u);
+}
+__device__ __forceinline__ int power_between(float lo, float hi) {
+    return static_cast<int>(__float_as_uint(hi) >> 23) - static_cast<int>(__float_as_uint(lo) >> 23);
+}
+
+// 2^n for whole |n| < 127; 0 from -126 on.
+__device__ __forceinline__ float power_of_two(float n) {
+    return n > -126.0f ? __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(n)) << 23) : 0.0f;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// What the rows that have seen something need of the reference: `lo` and `hi` for the smallest and largest
+// of their values, `huge` for the largest of the rows without a b.
+struct Apart {
+    float lo = 0x1p30f, hi = 0.0f, huge = 0.0f;
+    __device__ __forceinline__ void row(float max, float own, float empty) {
+        if (max == empty) return;
+        lo = fminf(lo, own);
+        hi = fmaxf(hi, own);
+        if (fabsf(max) >= kHuge) huge = fmaxf(huge, own);
+    }
+    __device__ __forceinline__ float reference(float ref) const {
+        const float least = fmaxf(-warp_max(-lo), warp_max(huge)), most = warp_max(hi);
+        return most == 0.0f ? ref : most < least * (1 << kApart) ? most : least;
+    }
+};
+
 // A head whose tiles lie in more than one CTA: the CTA that has its first
 // ones writes down which partial results belong together.
 struct AttendJoin {

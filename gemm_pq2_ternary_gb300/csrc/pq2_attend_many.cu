@@ -357,7 +357,7 @@ __device__ __forceinline__ void factors(const Ctl& k, const AttendWork& wk, Atte
                 if (lane % kTileTokens == 0) slot.base[key / kTileTokens] = base[i];
             }
             if (lane == 0) {
-                slot.ref = __uint_as_float(__float_as_uint(top) & 0x7f800000u);
+                slot.ref = scale_power(top);
                 slot.last = j == g.count - 1 ? last : 0;
                 slot.rows = static_cast<int>(min(static_cast<long long>(g.it.n) * G -
                                                      static_cast<long long>(g.it.row_tile) * Cfg<D>::kRows,
@@ -669,6 +669,8 @@ __device__ __forceinline__ bool rows_of_segment(const Ctl& k, const AttendWork& 
     const bool there = tile * 128 + row0 < s.rows;  // the warp has rows
     const bool whole = s.part < 0;
     float m[kR], ref = 0x1p-24f, back[kR];
+    float slack = kSlack;  // (less the largest b)
+    uint32_t bs = 0;
     float l[kR], z[kR];
     int last[kR];
     const int back_to = p.window > 0 ? p.window - 1 : s.pos0 + s.n;  // positions that a row sees before its own
@@ -738,23 +740,68 @@ __device__ __forceinline__ bool rows_of_segment(const Ctl& k, const AttendWork& 
 #pragma unroll
                     for (int c = 1; c < kGroups; ++c) top[r] = fmaxf(fmaxf(top[r], v[4 * c]), v[4 * c + 1]);
                     top[r] *= back[r];
-                    more |= top[r] > m[r] + kSlack;
+                    more |= top[r] > m[r] + slack;
                 }
                 if (__builtin_expect(__any_sync(0xffffffffu, more), 0)) {
                     // raise the values' reference, and maxima where a row needs it, to whole
                     // numbers (what was rounded is scaled exactly; from 2^23 on every fp32 number is
                     // one, and the maximum is the score): sums and outputs are scaled down
                     // (a row's lanes are four neighbours)
-                    float alpha[kR];
-                    const float down = ref / fmaxf(ref, slot.ref);
-                    ref = fmaxf(ref, slot.ref);
+                    float alpha[kR], to_ref = fmaxf(ref, slot.ref);
 #pragma unroll
                     for (int r = 0; r < kR; ++r) {
                         top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
                         top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-                        const float to = top[r] > m[r] + kSlack ? ceilf(top[r]) : m[r], by = to - m[r];
-                        m[r] = to;
-                        alpha[r] = by < 126.0f ? __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(by)) << 23) : 0.0f;
+                    }
+                    if (__all_sync(0xffffffffu, key0 < 0 && bs == 0)) {  // all rows see the same
+#pragma unroll
+                        for (int r = 0; r < kR; ++r) {
+                            const float to = top[r] > m[r] + kSlack ? ceilf(top[r]) : m[r];
+                            alpha[r] = power_of_two(m[r] - to);
+                            m[r] = to;
+                        }
+                    } else {
+                        float own[kR];  // the largest scale of the values that the row sees
+#pragma unroll
+                        for (int r = 0; r < kR; ++r) own[r] = 0.0f;
+#pragma unroll 1
+                        for (int c = 0; c < kStep / 4; ++c) {
+                            const int key = key0 + q + 2 * t + 8 * (c >> 1) + (c & 1);
+                            const float v = slot.value[at_f + c];
+#pragma unroll
+                            for (int r = 0; r < kR; ++r)
+                                if (key0 < 0 || (key >= last[r] - back_to && key <= last[r])) own[r] = fmaxf(own[r], v);
+                        }
+                        float max[kR];
+                        Apart apart;
+#pragma unroll
+                        for (int r = 0; r < kR; ++r) {
+                            own[r] = fmaxf(own[r], __shfl_xor_sync(0xffffffffu, own[r], 1));
+                            own[r] = scale_power(fmaxf(own[r], __shfl_xor_sync(0xffffffffu, own[r], 2)));
+                            const float b = static_cast<float>(row_b(bs, r));
+                            max[r] = m[r] == kEmpty ? kEmpty : m[r] - b;
+                            if (m[r] != kEmpty) own[r] = fmaxf(own[r], ref * power_of_two(b));
+                            max[r] = top[r] > max[r] + kSlack ? ceilf(top[r]) : max[r];
+                            apart.row(max[r], own[r], kEmpty);
+                        }
+                        to_ref = apart.reference(ref);
+                        bs = 0;
+                        float most = 0.0f;
+#pragma unroll
+                        for (int r = 0; r < kR; ++r) {
+                            const int b = max[r] == kEmpty ? 0 : ::max(power_between(to_ref, own[r]), 0);
+                            bs |= static_cast<uint32_t>(b) << (8 * r);
+                            max[r] += static_cast<float>(b);
+                            most = fmaxf(most, static_cast<float>(b));
+                            alpha[r] = m[r] == kEmpty ? 0.0f : power_of_two(m[r] - max[r]);
+                            m[r] = max[r];
+                        }
+                        slack = kSlack - warp_max(most);
+                    }
+                    const float down = ref / to_ref;
+                    ref = to_ref;
+#pragma unroll
+                    for (int r = 0; r < kR; ++r) {
                         l[r] *= alpha[r];
                         z[r] *= alpha[r];
                         alpha[r] *= down;

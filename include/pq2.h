@@ -635,8 +635,8 @@ pq2_status pq2_cache4_read(const pq2_cache4_read_args* args, void* stream);
  *               of the row's largest, a key's offset to 2^-21 of itself or 2^-17 of its scale, and a
  *               scale below 2^-25 of its offset counts as that.]
  *   weights w   times the values' scales over a power of two, as fp16: 11 bits of itself,
- *               or a key's part of an output to 2^-27 of the largest values' scale
- *               that the rows worked on together see (up to 256 of a sequence)
+ *               or a key's part of an output to 2^-24 of the largest values' scale that the row
+ *               sees (beside rows of the sequence with scores past 2^22: that those see)
  * (B == 1: max_rows, or M, stands for the sequence's rows.)
  *   q, out     [M, q_heads, dim] (type: PQ2_F16 or PQ2_BF16), token and head
  *              strides in elements, a head's values adjacent

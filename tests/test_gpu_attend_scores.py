@@ -147,3 +147,43 @@ def test_a_row_does_not_depend_on_the_rows_after_it(pq2, D, n, dtype):
     one, two = (_attend(pq2, c, x, [n], [ln]) for x in (q, grown))
     assert pq2.pq2_last_device_error() == pq2.PQ2_OK
     assert torch.equal(one[:n // 3], two[:n // 3])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D,n", [(64, 4), (64, 23), (128, 5), (128, 24), (256, 3), (256, 16), (64, 70), (128, 60), (128, 300),
+                                 (256, 40)])
+@pytest.mark.parametrize("before", [0, 150])
+def test_rows_do_not_feel_values_that_they_do_not_see(pq2, D, n, before, dtype):
+    # small values, then huge ones from the middle of the rows on: earlier rows keep what they have
+    ln = before + n
+    cut = before + n // 2
+    rng = np.random.default_rng(D + n)
+    size = np.where(np.arange(ln) < cut, 2.0 ** -12, 3e5)[:, None]
+    c = _cache(pq2, rng.standard_normal((ln, D)), rng.standard_normal((ln, D)) * size)
+    q = torch.from_numpy(rng.standard_normal((n, G, D))).to(TYPES[dtype]).to(DEV)
+    got = _attend(pq2, c, q, [n], [ln]).double().cpu().numpy()
+    assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+    want, bound = _bound(q, c.pool.cpu().numpy(), c.pages, n, ln, D ** -0.5, dtype)
+    fits = np.abs(want) < (6e4 if dtype == "f16" else 1e30)     # (outputs that the type can hold)
+    assert fits[:n // 2].all()
+    worst = (np.abs(got - want) / bound)[fits]
+    assert np.all(worst <= 1), float(worst.max())
+
+
+@pytest.mark.parametrize("window", [0, 1, 13, 90])
+@pytest.mark.parametrize("size", [1.0, 300.0])
+@pytest.mark.parametrize("D,n", [(64, 4), (64, 23), (128, 5), (128, 24), (256, 3), (256, 16), (64, 70), (128, 60), (128, 300),
+                                 (256, 40)])
+def test_values_of_very_different_size(pq2, D, n, size, window):
+    # tokens' values from 2^-14 to 2^12 in any order, behind and among the rows, with windows that leave
+    # some of them to some of the rows
+    ln = n + 230
+    rng = np.random.default_rng(D + n)
+    c = _cache(pq2, rng.standard_normal((ln, D)), rng.standard_normal((ln, D)) * 2.0 ** rng.uniform(-14, 12, (ln, 1)))
+    q = torch.from_numpy(size * rng.standard_normal((n, G, D))).half().to(DEV)
+    got = _attend(pq2, c, q, [n], [ln], window).double().cpu().numpy()
+    assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+    want, tol = ref.attend(_np(q), c.pool.cpu().numpy(), c.pages, [0, n], [ln], T, D ** -0.5, window)
+    bound = tol + np.abs(want) * UNIT["f16"] + TINY["f16"]
+    worst = np.abs(got - want) / bound
+    assert np.all(worst <= 1), float(worst.max())
