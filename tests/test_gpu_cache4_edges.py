@@ -135,3 +135,94 @@ def test_steps_of_the_serving_example_that_know_their_rows(pq2, drafts):
         err = np.abs(at.a.double().cpu().numpy() - want)
         assert np.all(err <= tol + np.abs(want) * 2.0 ** -11 + 2.0 ** -24)
         keep = keep + drafts + 1
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 5, 60])
+def test_heads_before_tokens(pq2, D, n):
+    # all arrays laid out [heads, tokens, values], the first token of the call a sequence of none
+    Hq, H, T, ln = 4, 2, 16, 75
+    g = torch.Generator(device=DEV).manual_seed(D + n)
+    table = torch.empty((128, D // 2, 2), device=DEV)
+    pq2.pq2_rope_table(table, 1e4)
+
+    def across(heads, dtype=torch.float16):
+        return torch.randn((heads, n + 2, D), generator=g, device=DEV).to(dtype).transpose(0, 1)
+    c, plain = (Cache(pq2, 1, -(-ln // T), H, D, T, seed=D) for _ in range(2))
+    pool = c.fill([ln])
+    plain.pool.copy_(c.pool)
+    q, k, v = across(Hq), across(H), across(H)
+    outs = []
+    for cache, lay in ((c, lambda t: t), (plain, lambda t: t.contiguous())):
+        q_out, out, kr, vr = (torch.full((h, n + 2, D), 7.0, dtype=torch.float16, device=DEV).transpose(0, 1) for h in (Hq, Hq, H, H))
+        q_out, out, kr, vr = lay(q_out), lay(out), lay(kr), lay(vr)
+        args = (cache.pool, cache.dev, _dev([1, 1 + n]), _dev([ln]))
+        pq2.pq2_cache4_append(lay(k), lay(v), *args, q=lay(q), q_out=q_out, table=table)
+        pq2.pq2_cache4_read(*args, kr, vr)
+        pq2.pq2_cache4_attend(q_out, *args, out, pq2.alloc_attend_workspace(n + 2, Hq, H, D))
+        turned = lay(torch.full((Hq, n + 2, D), 7.0, dtype=torch.float16, device=DEV).transpose(0, 1))
+        pq2.pq2_rope(lay(q), table, _dev(np.arange(n + 2)), turned)
+        assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+        outs.append([t.clone() for t in (q_out, out, kr, vr, turned, cache.pool)])
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    for t in outs[0][:4]:                      # rows of no sequence are left as they were
+        assert torch.all(t[0] == 7.0) and torch.all(t[n + 1] == 7.0)
+    want, tol = ref.attend(_np(outs[0][0][1:1 + n]), c.pool.cpu().numpy(), c.pages, [0, n], [ln], T, D ** -0.5)
+    err = np.abs(outs[0][1][1:1 + n].double().cpu().numpy() - want)
+    assert np.all(err <= tol + np.abs(want) * 2.0 ** -11 + 2.0 ** -24)
+    assert pool is not None
+
+
+@pytest.mark.parametrize("H,D,n", [(1024, 64, 1), (1000, 128, 2), (300, 64, 60)])
+def test_many_key_value_heads(pq2, H, D, n):
+    ln, T = 70, 16
+    c = Cache(pq2, 2, 5, H, D, T, spare=0)
+    g = torch.Generator(device=DEV).manual_seed(H)
+    x = torch.randn((2, ln, 2 * H, D), generator=g, device=DEV).flatten(0, 1)
+    pq2.pq2_cache4_append(x[:, :H], x[:, H:], c.pool, c.dev, _dev([0, ln, 2 * ln]), _dev([ln, ln]))
+    q = _q(2 * n, H, D, "f16")
+    got = _attend(pq2, c, q, [n, n], [ln, ln], max_rows=n)
+    assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+    pool = c.pool.cpu().numpy()
+    for h in (0, 1, H // 2, H - 1):
+        want, tol = ref.attend(_np(q[:, h:h + 1]), pool[:, h:h + 1], c.pages, [0, n, 2 * n], [ln, ln], T, D ** -0.5)
+        err = np.abs(got[:, h:h + 1].double().cpu().numpy() - want)
+        assert np.all(err <= tol + np.abs(want) * 2.0 ** -11 + 2.0 ** -24)
+
+
+@pytest.mark.parametrize("D,T,n", [(64, 1024, 1), (128, 1008, 3), (256, 1024, 40), (128, 1024, 70)])
+def test_large_pages(pq2, D, T, n):
+    lens = [1100, 2017, 16]
+    rows = [n, n, min(n, 16)]
+    c = Cache(pq2, 3, 3, 1, D, T, spare=1)
+    pool = c.fill(lens)
+    q = _q(sum(rows), 2, D, "bf16")
+    got = _attend(pq2, c, q, rows, lens)
+    assert pq2.pq2_last_device_error() == pq2.PQ2_OK
+    _check(got, q, pool, c, rows, lens, dtype="bf16")
+
+
+@pytest.mark.parametrize("n", [1, 60])
+def test_a_captured_step_over_changing_lengths(pq2, n):
+    # one graph, replayed after the lengths, the pages and the queries have changed
+    Hq, H, D, T, B = 4, 2, 128, 16, 3
+    c = Cache(pq2, B, 20, H, D, T)
+    pool = c.fill([320] * B)
+    q, out = _q(B * n, Hq, D, "f16"), torch.empty((B * n, Hq, D), dtype=torch.float16, device=DEV)
+    start, lens = _dev(n * np.arange(B + 1)), _dev([n] * B)
+    ws = pq2.alloc_attend_workspace(B * n, Hq, H, D)
+    pq2.pq2_cache4_attend(q, c.pool, c.dev, start, lens, out, ws, max_rows=n)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pq2.pq2_cache4_attend(q, c.pool, c.dev, start, lens, out, ws, max_rows=n)
+    rng = np.random.default_rng(1)
+    for step in range(4):
+        now = rng.integers(n, 321, B)
+        c.pages = c.pages[rng.permutation(B)]
+        c.dev.copy_(_dev(c.pages))
+        lens.copy_(_dev(now))
+        q.copy_(_q(B * n, Hq, D, "f16", seed=step))
+        g.replay()
+        _check(out, q, pool, c, [n] * B, now)
+    assert pq2.pq2_last_device_error() == pq2.PQ2_OK
