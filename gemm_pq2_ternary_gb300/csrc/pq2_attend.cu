@@ -21,20 +21,20 @@
 // Maxima are raised only when a score exceeds the present one by 2^kSlack (a vote,
 // not a reduction per tile): weights stay below 32, and times the values' scales (over
 // a power of two, raised likewise, below 2) times kWeight below 2^15, with weights down to
-// 2^-23 at fp16's full precision.
+// 2^-23 at fp16's full precision (where all rows see values of like size; pq2_attend.cuh).
 //
 // The tiles of all sequences and heads form one list, dealt out evenly to the CTAs;
 // an item (a sequence's tile of rows and head) counts for kExtra tiles more.  A CTA joins its warps'
 // results in shared memory; a head whose tiles lie in several CTAs is joined by a second
 // kernel, in the CTAs' order.
 //
-// Bound by instructions and their latency: 484 warp instructions a tile of 16 tokens and head of
-// 128 dims, 650 of 256, most of them on the integer pipe (operands from codes), issued at 53% and
-// 47% of the rate.  On GB300: 131071 tokens, 24 heads of 256 on 4: 46 us, 3.0 TB/s (58 with
+// Bound by instructions and their latency: 497 warp instructions a tile of 16 tokens and head of
+// 128 dims, 632 of 256, most of them on the integer pipe (operands from codes), issued at 52% and
+// 45% of the rate.  On GB300: 131071 tokens, 24 heads of 256 on 4: 45 us, 3.1 TB/s (58 with
 // loads into registers, 8 warps an SM and a join of one warp's loads at a time); 64 sequences of up
 // to 8192, 48 heads of 128 on 8: 94 us, 3.0 TB/s (107 to 147 while the list counted tiles alone
-// and registers were spilled); 75 tokens of 24 sequences of up to 5003, 40 heads of 128 on 8: 59 us
-// (62 with 8 rows a pass).  Two groups of rows of 128 dims spill 216 bytes.
+// and registers were spilled); 75 tokens of 24 sequences of up to 5003, 40 heads of 128 on 8: 60 us
+// (62 with 8 rows a pass).  Two groups of rows of 128 dims spill 284 bytes.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -224,7 +224,8 @@ __device__ __forceinline__ void load_rows(Rows<D, RG>& r, uint4* q, const pq2h::
 // 1 / x of a power of two.
 __device__ __forceinline__ float inverse(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 
-// Raises maxima and the values' reference where this tile needs it.
+// Raises maxima and the values' reference where this tile (its keys from `key` on, and
+// key + 8) needs it.  With `inside` all rows see all of it.
 template <int D, int RG>
 __device__ __forceinline__ void raise(Rows<D, RG>& r, const float (&x)[RG][2][2], const float (&s)[2], bool inside, int key) {
     float ref, top[RG][2];
@@ -743,9 +744,9 @@ cudaError_t launch_attend(const AttendParams& args, void* workspace, cudaStream_
     if (!many) return p.max_rows * G > 8 ? run(std::integral_constant<int, 2>()) : run(std::integral_constant<int, 1>());
     // Prompts and decoding sequences in one call: each to its kernel, one after the
     // other, in the same workspace.  2000 tokens behind 500, 40 heads of 128 on 8, with 256
-    // sequences of one token behind 1000: 275 us, all by the other kernel 800; with 64 of 3 behind
-    // 2000: 260 and 447; with 24 of 9 behind 3000: 304 and 320.  24 heads of 256 on 4 with
-    // 256 of one: 278 and 380; with 24 of 5 behind 3000: 254 and 193 (the worst case of this rule).
+    // sequences of one token behind 1000: 278 us, all by the other kernel 800; with 64 of 3 behind
+    // 2000: 264 and 447; with 24 of 9 behind 3000: 309 and 320.  24 heads of 256 on 4 with
+    // 256 of one: 279 and 380; with 24 of 5 behind 3000: 253 and 193 (the worst case of this rule).
     // 8 rows a pass: nothing bounds the rows of the short sequences, and most have one token.
     // With 16 the five took 325, 246, 275, 313 and 237 us.
     const cudaError_t e = run(std::integral_constant<int, 1>());

@@ -37,8 +37,9 @@
 // counted for their tiles alone.  On GB300: 4096 tokens behind 4096, 24 heads of 256 on 4:
 // 717 us, 863 TFLOP/s, for the first calls after a pause, and 757 us, 817 TFLOP/s, in a row of a hundred
 // (in a graph as from the host; the SM clock reads its maximum throughout, at 900 W); chunks of 1000,
-// 948 and 895 tokens, the last of 6000, 948 and 1895, 40 heads of 128 on 8: 294 us (mma.sync, 8
-// rows at a time: 4528 and 1250 us).
+// 948 and 895 tokens, the last of 6000, 948 and 1895, 40 heads of 128 on 8: 304 us (mma.sync, 8
+// rows at a time: 4528 and 1250 us).  That rows do not share their values' reference
+// (pq2_attend.cuh) costs 9 of the 304, none of the 717.
 #include <algorithm>
 #include <cfloat>
 

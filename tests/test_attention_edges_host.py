@@ -1,6 +1,5 @@
 """Host-side argument checks of the attention side of a step, sizes whose sums
 and products do not fit 64 bits (no GPU: every call here is refused)."""
-import pytest  # noqa: F401
 
 from test_abi_host import FAKE, _p, lib  # noqa: F401  (lib is a fixture)
 from test_attention_host import CACHE, _caller
